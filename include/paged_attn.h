@@ -63,7 +63,8 @@ enum {
     PA_ERRBIT_PAGE_RANGE = 1u,   /* a block-table page id used by a sequence was outside [0, num_pages) */
     PA_ERRBIT_TIMEOUT = 2u,      /* a pipeline wait gave up after its time limit (results invalid) */
     PA_ERRBIT_SEQ_CLIPPED = 4u,  /* seq_lens[b] needed more pages than bt_stride holds; clipped to bt_stride pages */
-    PA_ERRBIT_QSTART = 8u        /* paged_attn_fwd_varlen: a q_start entry out of [0, total tokens] or decreasing */
+    PA_ERRBIT_QSTART = 8u,       /* a packed batch's q_start entry out of [0, total tokens] or decreasing */
+    PA_ERRBIT_REFUSED = 16u      /* paged_attn_step_tables: a request could not be served (see there) */
 };
 
 /* kernel variants (paged_attn_fwd_variant) */
@@ -336,6 +337,109 @@ int paged_attn_fwd_kvq_splitkv(const void *q, const void *k_cache, const void *v
                                int64_t workspace_bytes, int num_sms, int64_t device_bytes, void *stream);
 
 /*
+ * ------------------------------------------------------------------ serving step over selected pages
+ * The four calls below make one serving step over the paged cache: paged_attn_step_tables turns the
+ * requests' lengths into block tables and slots, paged_attn_append writes the new tokens' K and V
+ * rows (and the envelopes of the pages they land in), paged_attn_select_pages picks the pages each
+ * query token attends to, and paged_attn_fwd_sparse attends over them.  Each is one launch on
+ * `stream`, needs no workspace, synchronises nothing and can be captured into a CUDA graph (make the
+ * first call on a device outside a capture: it looks up the device error word).
+ * These calls are this library's own; the pages have no counterpart.
+ *
+ * Query layout of the last two: q_start NULL = q [batch, q_len, Hq, D]; q_start [batch + 1] (device) =
+ * q [T, Hq, D] packed as for paged_attn_fwd_varlen, with T = dims->q_len the rows of q.  Rows at or
+ * past q_start[batch] (padding) belong to no sequence: nothing of theirs is written.  A sequence whose
+ * q_start entries are out of [0, T] or decrease is skipped and sets PA_ERRBIT_QSTART.  `causal` and
+ * q_offset are paged_attn_fwd's; a query token's reach is the number of keys it may see.
+ */
+
+/*
+ * paged_attn_step_tables — block tables, slots and query ranges of one step from request lengths.
+ *   cached_lens [B]       tokens request b already has in the cache; the first ceil(cached / page_size)
+ *                         entries of its block-table row list their pages
+ *   new_lens [B]          tokens to append in this step (0: idle)
+ *   free_pages [free_cap] the free pages, a stack: entry free_count[0] - 1 is taken first
+ *   block_table [B, bt_stride]   updated in place: the new pages' entries are written, no other
+ *   seq_lens, q_offset [B], q_start [B + 1], free_left [1], slots [total_tokens]   written
+ * Request b needs ceil((cached + new) / page_size) - ceil(cached / page_size) pages.  It is usable if
+ * neither length is negative and its pages fit bt_stride, and it is served if it is usable, its pages
+ * on top of what the usable requests before it need (served or not) are at most free_count (or it
+ * needs none), and its tokens on top of theirs are at most total_tokens.  The served requests take
+ * pages from the stack in batch order and are packed in batch order:
+ *   seq_lens[b] = cached + new, or cached if not served;  q_offset[b] = cached
+ *   q_start[b]  = new tokens of the served requests before b
+ *   slots[t]    = page * page_size + row of packed token t; -1 at and past q_start[B], and where the
+ *                 page id is outside [0, num_pages) (sets PA_ERRBIT_PAGE_RANGE)
+ *   free_left   = free_count - pages taken
+ * A request that asks for tokens and is not served (or has a negative length), or a free_count outside
+ * [0, free_cap] (clamped), sets PA_ERRBIT_REFUSED.  seq_lens (or q_offset) may be cached_lens itself,
+ * and free_left may be free_count, so that a loop's state advances in place; no other arrays may
+ * overlap.
+ * Limits: batch <= PA_STEP_MAX_BATCH (PA_EUNSUPPORTED), page_size in {16, 32, 64},
+ * num_pages * page_size < 2^31.  batch = 0 returns PA_OK and writes nothing.
+ */
+#define PA_STEP_MAX_BATCH 16384
+int paged_attn_step_tables(const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages,
+                           int free_cap, const int32_t *free_count, int32_t *block_table, int32_t *seq_lens,
+                           int32_t *q_offset, int32_t *q_start, int32_t *slots, int32_t *free_left, int batch,
+                           int total_tokens, int page_size, int64_t num_pages, int bt_stride, void *stream);
+
+/*
+ * paged_attn_append — write new tokens' K and V rows into their slots and, on request, the envelopes
+ * of the pages they land in.
+ *   k_new, v_new [T, Hkv, D]  dims->dtype, T = dims->q_len; tokens k_stride / v_stride elements apart
+ *                             (0: dense), so that both may be slices of a fused projection
+ *   slots [T]                 page * page_size + row; -1: the token is not written; any other value
+ *                             outside the pool is skipped and sets PA_ERRBIT_PAGE_RANGE
+ *   k_env, k_env_scale        both NULL, or int8 [num_pages, Hkv, 2, D] and float32 [num_pages, Hkv]
+ * The envelope of a (page, kv head) bounds its keys: with lo_d / hi_d the smallest / largest of element
+ * d over the page's rows 0 .. r (r the last row written now) and a the largest |element| of them,
+ *   k_env_scale = a / 127,  k_env[0][d] = rint((lo_d / a) * 127),  k_env[1][d] = rint((hi_d / a) * 127)
+ * in float32, each operation rounded to nearest even (a = 0: all 0).  Keys with a non-finite element
+ * give k_env 0 and k_env_scale +inf.  Rows 0 .. r must all hold tokens by then, and the new tokens of
+ * one page must be consecutive and in order, as paged_attn_step_tables gives them.  A slot named twice
+ * holds either token's elements.
+ * dims->batch, num_q_heads, bt_stride and q_stride are not used (num_q_heads a multiple of
+ * num_kv_heads all the same).
+ */
+int paged_attn_append(const void *k_new, const void *v_new, const int32_t *slots, int64_t k_stride,
+                      int64_t v_stride, void *k_cache, void *v_cache, int8_t *k_env, float *k_env_scale,
+                      const pa_dims *dims, void *stream);
+
+/*
+ * paged_attn_select_pages — for every query token and kv head, the top_k pages to attend to.
+ * A token with reach r has np = ceil(r / page_size) candidate pages.  np <= top_k: all of them are
+ * selected.  Otherwise the first sink_pages and the last local_pages are (sink + local <= top_k), and
+ * the rest of top_k goes to the pages of highest score between them, the lower index first on a tie:
+ *   qi    = rint((q / a) * 127) over the G heads of the kv head, a their largest |element| (float32
+ *           steps as for the envelope; a = 0 or not finite: qi = 0)
+ *   s     = max over the G heads of  sum_d  qi_d > 0 ? qi_d * k_env[1][d] : qi_d * k_env[0][d]
+ *   score = float(s) * k_env_scale, rounded once; +inf where k_env_scale is +inf
+ * s bounds q.k over the page's keys up to the rounding to 8 bits; it is an exact integer below 2^24, so
+ * the selection does not depend on the order of any sum.
+ *   sel [tokens, Hkv, top_k] int32: the selected logical pages in ascending order, then -1.
+ * q has dims->dtype.  A page id outside [0, num_pages) counts as score 0 and sets PA_ERRBIT_PAGE_RANGE.
+ * Limit: bt_stride <= PA_SELECT_MAX_PAGES (PA_EUNSUPPORTED).
+ */
+#define PA_SELECT_MAX_PAGES 49152
+int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_env_scale,
+                            const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_start, int causal,
+                            const int32_t *q_offset, int sink_pages, int local_pages, int top_k, int32_t *sel,
+                            const pa_dims *dims, void *stream);
+
+/*
+ * paged_attn_fwd_sparse — paged_attn_fwd over listed pages only: query token t's heads of kv head h
+ * attend to the keys below the token's reach of the logical pages sel[t][h][0 .. top_k).  Entries below
+ * 0, or at or past ceil(reach / page_size), list nothing; the order is free and an index listed twice
+ * counts twice.  out [tokens, Hq, D] in dims->dtype (rounded once, to nearest even), lse [tokens, Hq]
+ * float32 or NULL; a row without a key gets 0 and -inf.  q may be a view (dims->q_stride).
+ */
+int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                          const int32_t *seq_lens, const int32_t *q_start, int causal, const int32_t *q_offset,
+                          const int32_t *sel, int top_k, float scale, void *out, float *lse, const pa_dims *dims,
+                          void *stream);
+
+/*
  * paged_attn_plan — the split plan as data: plan [batch, split_kv, 2] int32 =
  * {first page, one past the last page} of each run (see paged_attn_fwd).
  * seq_lens is a device pointer [batch]; negative lengths count as 0.
@@ -373,8 +477,8 @@ int paged_attn_debug_wait_timeout(uint32_t limit_us, void *stream);
  *                lay outside [0, num_pages); its tokens read as zero (the
  *                rocm-libraries PR #14349 kernel leaves this unchecked, "Not in
  *                this PR"), every other sequence's results are exact;
- *   PA_EINVAL    otherwise, PA_ERRBIT_QSTART is set (paged_attn_fwd_varlen);
- *   PA_OK        no bit other than PA_ERRBIT_SEQ_CLIPPED is set.
+ *   PA_EINVAL    otherwise, PA_ERRBIT_QSTART is set (a packed batch's q_start);
+ *   PA_OK        no bit other than PA_ERRBIT_SEQ_CLIPPED and PA_ERRBIT_REFUSED is set.
  * *flags holds the bits in every case but PA_ECUDA (the read failed) and
  * PA_EINVAL for a NULL flags.  The forward calls are asynchronous and cannot
  * return these themselves: a caller that must not consume invalid outputs

@@ -23,7 +23,9 @@ __all__ = [
     "paged_attn_strerror", "paged_attn_version", "attention", "paged_attn_auto_split",
     "paged_attn_workspace_bytes", "paged_attn_fwd_splitkv", "paged_attn_fwd_splitkv_noalloc", "paged_attn_fwd_kvq",
     "paged_attn_fwd_kvq_splitkv", "attention_kvq", "paged_attn_fwd_varlen", "attention_varlen",
-    "paged_attn_fwd_varlen_overlap", "paged_attn_varlen_hint", "paged_attn_varlen_overlap_share", "PaVarlenHint", "PA_F32", "PA_F16", "PA_BF16", "PA_FP8_E4M3",
+    "paged_attn_fwd_varlen_overlap", "paged_attn_varlen_hint", "paged_attn_varlen_overlap_share", "PaVarlenHint",
+    "paged_attn_step_tables", "paged_attn_append", "paged_attn_select_pages", "paged_attn_fwd_sparse",
+    "step_tables", "page_envelopes", "attention_sparse", "PA_F32", "PA_F16", "PA_BF16", "PA_FP8_E4M3",
     "PA_INT8",
     "VARIANT_AUTO", "VARIANT_SIMT", "VARIANT_MMA_DECODE", "VARIANT_MMA_PREFILL", "VARIANT_TC05_PREFILL",
     "VARIANT_MMA_T", "VARIANT_MMA_SPLIT_GROUP",
@@ -32,7 +34,7 @@ __all__ = [
 PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT8 = 0, 1, 2, 3, 4
 VARIANT_AUTO, VARIANT_SIMT, VARIANT_MMA_DECODE, VARIANT_MMA_PREFILL, VARIANT_TC05_PREFILL, VARIANT_MMA_T = 0, 1, 2, 3, 4, 5
 VARIANT_MMA_SPLIT_GROUP = 6
-ERRBIT_PAGE_RANGE, ERRBIT_TIMEOUT, ERRBIT_SEQ_CLIPPED, ERRBIT_QSTART = 1, 2, 4, 8
+ERRBIT_PAGE_RANGE, ERRBIT_TIMEOUT, ERRBIT_SEQ_CLIPPED, ERRBIT_QSTART, ERRBIT_REFUSED = 1, 2, 4, 8, 16
 PA_OK, PA_EINVAL, PA_EDTYPE, PA_EUNSUPPORTED, PA_ECUDA, PA_EBOUNDS, PA_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6
 
 
@@ -103,6 +105,14 @@ def load_library(build_if_missing: bool = False):
     lib.paged_attn_varlen_hint.restype = ctypes.c_int
     lib.paged_attn_varlen_overlap_share.argtypes = [D, ctypes.POINTER(PaVarlenHint), I32]
     lib.paged_attn_varlen_overlap_share.restype = ctypes.c_int
+    lib.paged_attn_step_tables.argtypes = [P, P, P, I32, P, P, P, P, P, P, P, I32, I32, I32, I64, I32, P]
+    lib.paged_attn_step_tables.restype = ctypes.c_int
+    lib.paged_attn_append.argtypes = [P, P, P, I64, I64, P, P, P, P, D, P]
+    lib.paged_attn_append.restype = ctypes.c_int
+    lib.paged_attn_select_pages.argtypes = [P, P, P, P, P, P, I32, P, I32, I32, I32, P, D, P]
+    lib.paged_attn_select_pages.restype = ctypes.c_int
+    lib.paged_attn_fwd_sparse.argtypes = [P, P, P, P, P, P, I32, P, P, I32, F, P, P, D, P]
+    lib.paged_attn_fwd_sparse.restype = ctypes.c_int
     lib.paged_attn_debug_gather.argtypes = [P, P, P, D, I32, P, P]
     lib.paged_attn_debug_wait_timeout.argtypes = [ctypes.c_uint32, P]
     lib.paged_attn_debug_wait_timeout.restype = ctypes.c_int
@@ -465,6 +475,173 @@ def paged_attn_fwd_varlen_overlap(q, k_cache, v_cache, block_table, seq_lens, q_
                           out, lse, stream, hint if hint is not None else PaVarlenHint())
 
 
+# ----------------------------------------------------------------------------- serving step over selected pages
+def _check_device(*named) -> None:
+    """The tensors of one call are all on the current CUDA device (the one its stream belongs to)."""
+    dev = _torch().cuda.current_device()
+    for t, name in named:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device {dev}")
+
+
+def _check_rows(t, name, dtype, heads, head_dim) -> int:
+    """t [T, heads, head_dim] may be a view whose tokens are further apart than its heads; returns the
+    elements between tokens (0: dense)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [T, {heads}, {head_dim}], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim) or t.stride(0) < heads * head_dim:
+        raise ValueError(f"{name}'s heads must be dense and its tokens apart ([T, H, D] rows)")
+    return int(t.stride(0)) if t.shape[0] > 1 else 0
+
+
+def paged_attn_step_tables(cached_lens, new_lens, free_pages, free_count, block_table, seq_lens, q_offset, q_start,
+                           slots, free_left, page_size: int, num_pages: int, stream=None) -> None:
+    """Block tables, slots and query ranges of one step from request lengths; see
+    ``paged_attn_step_tables`` in include/paged_attn.h.  Every tensor int32 on the device: cached_lens,
+    new_lens, seq_lens, q_offset [B], free_pages [F] (a stack), free_count, free_left [1], block_table
+    [B, W] (in place), q_start [B + 1], slots [T].  seq_lens may be cached_lens, free_left free_count."""
+    torch = _torch()
+    i32 = torch.int32
+    B, W = block_table.shape
+    for t, name, n in ((cached_lens, "cached_lens", B), (new_lens, "new_lens", B), (free_pages, "free_pages", None),
+                       (free_count, "free_count", 1), (seq_lens, "seq_lens", B), (q_offset, "q_offset", B),
+                       (q_start, "q_start", B + 1), (slots, "slots", None), (free_left, "free_left", 1)):
+        _check(t, name, i32, 1)
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    _check(block_table, "block_table", i32, 2)
+    _check_device((cached_lens, "cached_lens"), (new_lens, "new_lens"), (free_pages, "free_pages"),
+                  (free_count, "free_count"), (block_table, "block_table"), (seq_lens, "seq_lens"),
+                  (q_offset, "q_offset"), (q_start, "q_start"), (slots, "slots"), (free_left, "free_left"))
+    rc = load_library().paged_attn_step_tables(
+        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
+        free_count.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), q_offset.data_ptr(), q_start.data_ptr(),
+        slots.data_ptr(), free_left.data_ptr(), B, slots.shape[0], int(page_size), int(num_pages), W, _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_step_tables")
+
+
+def paged_attn_append(k_new, v_new, slots, k_cache, v_cache, k_env=None, k_env_scale=None, stream=None) -> None:
+    """Write the new tokens' K and V rows ([T, Hkv, D], possibly slices of a fused projection) into
+    their slots (int32 [T], page * page_size + row, -1 to skip) and, with k_env (int8
+    [num_pages, Hkv, 2, D]) and k_env_scale (float32 [num_pages, Hkv]), the envelopes of the pages they
+    land in; see ``paged_attn_append`` in include/paged_attn.h."""
+    torch = _torch()
+    _check(k_cache, "k_cache", None, 4)
+    _check(v_cache, "v_cache", k_cache.dtype, 4)
+    P, ps, Hkv, D = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    ks = _check_rows(k_new, "k_new", k_cache.dtype, Hkv, D)
+    vs = _check_rows(v_new, "v_new", k_cache.dtype, Hkv, D)
+    _check(slots, "slots", torch.int32, 1)
+    T = slots.shape[0]
+    if k_new.shape[0] != T or v_new.shape[0] != T:
+        raise ValueError("k_new, v_new and slots must have the same number of tokens")
+    if (k_env is None) != (k_env_scale is None):
+        raise ValueError("k_env and k_env_scale come together")
+    if k_env is not None:
+        _check_env(k_env, k_env_scale, P, Hkv, D)
+    _check_device((k_new, "k_new"), (v_new, "v_new"), (slots, "slots"), (k_cache, "k_cache"), (v_cache, "v_cache"),
+                  (k_env, "k_env"), (k_env_scale, "k_env_scale"))
+    dims = PaDims(1, T, Hkv, Hkv, D, ps, P, 0, _dtype_code(k_cache))
+    rc = load_library().paged_attn_append(_ptr(k_new), _ptr(v_new), _ptr(slots), ks, vs, _ptr(k_cache), _ptr(v_cache),
+                                          _ptr(k_env), _ptr(k_env_scale), ctypes.byref(dims), _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_append")
+
+
+def _check_env(k_env, k_env_scale, P, Hkv, D) -> None:
+    torch = _torch()
+    _check(k_env, "k_env", torch.int8, 4)
+    _check(k_env_scale, "k_env_scale", torch.float32, 2)
+    if tuple(k_env.shape) != (P, Hkv, 2, D) or tuple(k_env_scale.shape) != (P, Hkv):
+        raise ValueError(f"k_env must be {(P, Hkv, 2, D)} and k_env_scale {(P, Hkv)}, got {tuple(k_env.shape)} "
+                         f"and {tuple(k_env_scale.shape)}")
+
+
+def _sparse_dims(q, Hkv, D, ps, P, block_table, seq_lens, q_offset, q_start, sel, sel_name) -> PaDims:
+    """Shapes of a call over selected pages: q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start."""
+    torch = _torch()
+    _check_q(q, 4 if q_start is None else 3)
+    _check(block_table, "block_table", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    _check(q_offset, "q_offset", torch.int32, 1)
+    _check(q_start, "q_start", torch.int32, 1)
+    _check(sel, sel_name, torch.int32, q.dim())
+    B, W = block_table.shape
+    Hq = q.shape[-2]
+    if q.shape[-1] != D:
+        raise ValueError("q's head dim differs from the cache's")
+    if seq_lens.shape[0] != B or (q_offset is not None and q_offset.shape[0] != B):
+        raise ValueError("seq_lens and q_offset must have one entry per block_table row")
+    if q_start is None:
+        if q.shape[0] != B:
+            raise ValueError("q must have one batch entry per block_table row")
+    elif q_start.shape[0] != B + 1:
+        raise ValueError("q_start must have one entry more than block_table has rows")
+    if sel.shape[:-2] != q.shape[:-2] or sel.shape[-2] != Hkv:
+        raise ValueError(f"{sel_name} must be {tuple(q.shape[:-2])} + ({Hkv}, top_k), got {tuple(sel.shape)}")
+    stride = _q_token_stride(q)
+    if not stride and not q.is_contiguous() or stride and stride < Hq * D:
+        raise ValueError("q's tokens must be apart (no broadcast or overlapping view)")
+    return PaDims(B, q.shape[-3], Hq, Hkv, D, ps, P, W, _dtype_code(q), stride)
+
+
+def paged_attn_select_pages(q, k_env, k_env_scale, block_table, seq_lens, causal, q_offset, sink_pages: int,
+                            local_pages: int, sel, page_size: int, q_start=None, stream=None) -> None:
+    """The pages each query token and kv head attends to, into sel (int32 [..., Hkv, top_k], ascending
+    logical pages, then -1): the first sink_pages, the last local_pages and the best of the others by
+    the score of their key envelope; see ``paged_attn_select_pages`` in include/paged_attn.h.
+    q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start [B + 1]."""
+    if k_env.dim() != 4:
+        raise ValueError("k_env must be [num_pages, Hkv, 2, D]")
+    P, Hkv, _, D = k_env.shape
+    _check_env(k_env, k_env_scale, P, Hkv, D)
+    dims = _sparse_dims(q, Hkv, D, int(page_size), P, block_table, seq_lens, q_offset, q_start, sel, "sel")
+    _check_device((q, "q"), (k_env, "k_env"), (k_env_scale, "k_env_scale"), (block_table, "block_table"),
+                  (seq_lens, "seq_lens"), (q_offset, "q_offset"), (q_start, "q_start"), (sel, "sel"))
+    rc = load_library().paged_attn_select_pages(
+        _ptr(q), _ptr(k_env), _ptr(k_env_scale), _ptr(block_table), _ptr(seq_lens), _ptr(q_start), int(bool(causal)),
+        _ptr(q_offset), int(sink_pages), int(local_pages), sel.shape[-1], _ptr(sel), ctypes.byref(dims),
+        _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_select_pages")
+
+
+def paged_attn_fwd_sparse(q, k_cache, v_cache, block_table, seq_lens, causal, q_offset, sel, scale, out, lse,
+                          q_start=None, stream=None) -> None:
+    """Forward over the pages listed in sel (int32 [..., Hkv, top_k] logical pages, as
+    ``paged_attn_select_pages`` gives them); see ``paged_attn_fwd_sparse`` in include/paged_attn.h.
+    q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start [B + 1]; out as q (dense), lse without D or None."""
+    torch = _torch()
+    _check(k_cache, "k_cache", q.dtype, 4)
+    _check(v_cache, "v_cache", q.dtype, 4)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    P, ps, Hkv, D = k_cache.shape
+    dims = _sparse_dims(q, Hkv, D, ps, P, block_table, seq_lens, q_offset, q_start, sel, "sel")
+    _check(out, "out", q.dtype)
+    _check(lse, "lse", torch.float32)
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:-1]):
+        raise ValueError("out must be shaped as q, and lse as q without its last dim")
+    _check_device((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (block_table, "block_table"),
+                  (seq_lens, "seq_lens"), (q_offset, "q_offset"), (q_start, "q_start"), (sel, "sel"), (out, "out"),
+                  (lse, "lse"))
+    rc = load_library().paged_attn_fwd_sparse(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(q_start), int(bool(causal)),
+        _ptr(q_offset), _ptr(sel), sel.shape[-1], float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims),
+        _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_fwd_sparse")
+
+
 def paged_attn_combine(part_out, part_lse, out, lse=None, stream=None) -> None:
     """Merge split partials: part_out [S, ..., D] f32, part_lse [S, ...] f32 -> out [..., D], lse [...]."""
     torch = _torch()
@@ -618,3 +795,54 @@ def attention_varlen(q, k_cache, v_cache, block_table, seq_lens, q_start, *, cau
                               scale, po, pl, stream, hint)
         paged_attn_combine(po, pl, out, lse, stream)
     return (out, lse) if want_lse else out
+
+
+def step_tables(cached_lens, new_lens, free_pages, free_count, block_table, total_tokens: int, page_size: int,
+                num_pages: int, stream=None):
+    """``paged_attn_step_tables`` with its outputs allocated: updates block_table in place and returns
+    ``(seq_lens, q_offset, q_start, slots, free_left)``."""
+    torch = _torch()
+    B = block_table.shape[0]
+    def i32(n):
+        return torch.empty(n, dtype=torch.int32, device=block_table.device)
+    seq_lens, q_offset, q_start, slots, free_left = i32(B), i32(B), i32(B + 1), i32(total_tokens), i32(1)
+    if stream is not None:  # allocated on the current stream, used on another
+        for t in (seq_lens, q_offset, q_start, slots, free_left):
+            t.record_stream(stream)
+    paged_attn_step_tables(cached_lens, new_lens, free_pages, free_count, block_table, seq_lens, q_offset, q_start,
+                           slots, free_left, page_size, num_pages, stream)
+    return seq_lens, q_offset, q_start, slots, free_left
+
+
+def page_envelopes(k_cache):
+    """Zeroed ``(k_env, k_env_scale)`` for a pool: what ``paged_attn_append`` keeps and
+    ``paged_attn_select_pages`` reads."""
+    torch = _torch()
+    P, _, Hkv, D = k_cache.shape
+    return (torch.zeros((P, Hkv, 2, D), dtype=torch.int8, device=k_cache.device),
+            torch.zeros((P, Hkv), dtype=torch.float32, device=k_cache.device))
+
+
+def attention_sparse(q, k_cache, v_cache, k_env, k_env_scale, block_table, seq_lens, *, top_k: int,
+                     sink_pages: int = 1, local_pages: int = 2, causal: bool = True, q_offset=None, q_start=None,
+                     scale: Optional[float] = None, want_lse: bool = False, want_pages: bool = False, stream=None):
+    """Select top_k pages per query token and kv head by their key envelopes and attend over them: q
+    [B, Sq, Hq, D], or packed [T, Hq, D] with q_start [B + 1].  Rows of a packed q that belong to no
+    sequence are not written.  Returns ``out``, or a tuple with ``lse`` (want_lse) and the selected
+    pages (want_pages) after it."""
+    torch = _torch()
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    sel = torch.empty((*q.shape[:-2], k_cache.shape[2], int(top_k)), dtype=torch.int32, device=q.device)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
+    if stream is not None:  # allocated on the current stream, used on another
+        for t in (sel, out, lse):
+            if t is not None:
+                t.record_stream(stream)
+    paged_attn_select_pages(q, k_env, k_env_scale, block_table, seq_lens, causal, q_offset, sink_pages, local_pages,
+                            sel, k_cache.shape[1], q_start, stream)
+    paged_attn_fwd_sparse(q, k_cache, v_cache, block_table, seq_lens, causal, q_offset, sel, scale, out, lse, q_start,
+                          stream)
+    extra = ([lse] if want_lse else []) + ([sel] if want_pages else [])
+    return (out, *extra) if extra else out

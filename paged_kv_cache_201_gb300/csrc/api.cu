@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "kernels.h"
@@ -643,6 +644,151 @@ int paged_attn_varlen_hint(const int32_t *q_start, const int32_t *seq_lens, cons
     hint->long_pairs = long_pairs;
     hint->short_kv_tokens = short_kv;
     return PA_OK;
+}
+
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks of paged_attn_select_pages and paged_attn_fwd_sparse: shape, queries, tables and lists.
+// *n_tok: query tokens (rows of q).  PA_OK with *n_tok = 0 when there is nothing to do.
+int check_sparse(const pa_dims *d, const void *q, const int32_t *block_table, const int32_t *seq_lens,
+                 const int32_t *q_start, const int32_t *q_offset, const int32_t *sel, int top_k, int64_t *n_tok) {
+    int rc = check_dims(d);
+    if (rc != PA_OK) return rc;
+    if (top_k < 1) return PA_EINVAL;
+    *n_tok = d->batch == 0 ? 0 : q_start ? (int64_t)d->q_len : (int64_t)d->batch * d->q_len;
+    if (*n_tok == 0) return PA_OK;
+    if (!q || !block_table || !seq_lens || !sel) return PA_EINVAL;
+    if (!aligned16(q) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(q_start) ||
+        !aligned4(q_offset) || !aligned4(sel))
+        return PA_EINVAL;
+    return PA_OK;
+}
+
+}  // namespace
+
+int paged_attn_step_tables(const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages,
+                           int free_cap, const int32_t *free_count, int32_t *block_table, int32_t *seq_lens,
+                           int32_t *q_offset, int32_t *q_start, int32_t *slots, int32_t *free_left, int batch,
+                           int total_tokens, int page_size, int64_t num_pages, int bt_stride, void *stream) {
+    if (batch < 0 || total_tokens < 0 || free_cap < 0 || bt_stride < 0 || num_pages < 1) return PA_EINVAL;
+    if (page_size != 16 && page_size != 32 && page_size != 64) return PA_EUNSUPPORTED;
+    if (num_pages >= ((int64_t)1 << 31) / page_size || (int64_t)bt_stride * page_size >= (int64_t)1 << 31 ||
+        batch > PA_STEP_MAX_BATCH)
+        return PA_EUNSUPPORTED;
+    if (batch == 0) return PA_OK;
+    if (!cached_lens || !new_lens || !free_count || !seq_lens || !q_offset || !q_start || !free_left)
+        return PA_EINVAL;
+    if ((free_cap > 0 && !free_pages) || (bt_stride > 0 && !block_table) || (total_tokens > 0 && !slots))
+        return PA_EINVAL;
+    for (const void *ptr : {(const void *)cached_lens, (const void *)new_lens, (const void *)free_pages,
+                            (const void *)free_count, (const void *)block_table, (const void *)seq_lens,
+                            (const void *)q_offset, (const void *)q_start, (const void *)slots,
+                            (const void *)free_left})
+        if (!aligned4(ptr)) return PA_EINVAL;
+    pa::StepTablesParams p{};
+    int rc = error_word_ptr(&p.err);
+    if (rc != PA_OK) return rc;
+    p.cached_lens = cached_lens;
+    p.new_lens = new_lens;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.q_offset = q_offset;
+    p.q_start = q_start;
+    p.slots = slots;
+    p.free_left = free_left;
+    p.num_pages = num_pages;
+    p.free_cap = free_cap;
+    p.B = batch;
+    p.T = total_tokens;
+    p.ps_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+    p.W = bt_stride;
+    return cuda_status(pa::launch_step_tables(p, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_attn_append(const void *k_new, const void *v_new, const int32_t *slots, int64_t k_stride,
+                      int64_t v_stride, void *k_cache, void *v_cache, int8_t *k_env, float *k_env_scale,
+                      const pa_dims *dims, void *stream) {
+    int rc = check_dims(dims);
+    if (rc != PA_OK) return rc;
+    const int64_t row = (int64_t)dims->num_kv_heads * dims->head_dim;
+    for (int64_t s : {k_stride, v_stride})
+        if (s != 0 && (s < row || (s * esize_of(dims->dtype)) % 16 != 0 || s >= (int64_t)1 << 40)) return PA_EINVAL;
+    if (dims->q_len == 0) return PA_OK;
+    if (!k_new || !v_new || !slots || !k_cache || !v_cache || (k_env == nullptr) != (k_env_scale == nullptr))
+        return PA_EINVAL;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_env) ||
+        !aligned4(slots) || !aligned4(k_env_scale))
+        return PA_EINVAL;
+    pa::AppendParams p{};
+    rc = error_word_ptr(&p.err);
+    if (rc != PA_OK) return rc;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.slots = slots;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.env = k_env;
+    p.env_scale = k_env_scale;
+    p.k_stride = k_stride ? k_stride : row;
+    p.v_stride = v_stride ? v_stride : row;
+    p.num_slots = dims->num_pages * dims->page_size;
+    p.T = dims->q_len;
+    p.Hkv = dims->num_kv_heads;
+    p.ps_shift = dims->page_size == 16 ? 4 : dims->page_size == 32 ? 5 : 6;
+    return cuda_status(pa::launch_append(p, dims->dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_env_scale,
+                            const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_start, int causal,
+                            const int32_t *q_offset, int sink_pages, int local_pages, int top_k, int32_t *sel,
+                            const pa_dims *dims, void *stream) {
+    int64_t n_tok = 0;
+    int rc = check_sparse(dims, q, block_table, seq_lens, q_start, q_offset, sel, top_k, &n_tok);
+    if (rc != PA_OK) return rc;
+    if (sink_pages < 0 || local_pages < 0 || (int64_t)sink_pages + local_pages > top_k) return PA_EINVAL;
+    if (dims->bt_stride > PA_SELECT_MAX_PAGES) return PA_EUNSUPPORTED;
+    if (n_tok == 0) return PA_OK;
+    if (!k_env || !k_env_scale || !aligned16(k_env) || !aligned4(k_env_scale)) return PA_EINVAL;
+    unsigned int *err = nullptr;
+    if ((rc = error_word_ptr(&err)) != PA_OK) return rc;
+    pa::SparseParams sp{};
+    sp.f = fill_params(q, nullptr, nullptr, block_table, seq_lens, causal, q_offset, 1, 1.f, nullptr, nullptr, dims,
+                       err);
+    sp.f.q_start = q_start;
+    sp.env = k_env;
+    sp.env_scale = k_env_scale;
+    sp.sel_out = sel;
+    sp.n_tok = n_tok;
+    sp.K = top_k;
+    sp.sink = sink_pages;
+    sp.local = local_pages;
+    return cuda_status(pa::launch_select_pages(sp, dims->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                          const int32_t *seq_lens, const int32_t *q_start, int causal, const int32_t *q_offset,
+                          const int32_t *sel, int top_k, float scale, void *out, float *lse, const pa_dims *dims,
+                          void *stream) {
+    int64_t n_tok = 0;
+    int rc = check_sparse(dims, q, block_table, seq_lens, q_start, q_offset, sel, top_k, &n_tok);
+    if (rc != PA_OK) return rc;
+    if (!isfinite(scale)) return PA_EINVAL;
+    if (n_tok == 0) return PA_OK;
+    rc = check_fwd_pointers(q, k_cache, v_cache, block_table, seq_lens, q_offset, 1, out, lse);
+    if (rc != PA_OK) return rc;
+    unsigned int *err = nullptr;
+    if ((rc = error_word_ptr(&err)) != PA_OK) return rc;
+    pa::SparseParams sp{};
+    sp.f = fill_params(q, k_cache, v_cache, block_table, seq_lens, causal, q_offset, 1, scale, out, lse, dims, err);
+    sp.f.q_start = q_start;
+    sp.sel = sel;
+    sp.n_tok = n_tok;
+    sp.K = top_k;
+    return cuda_status(pa::launch_sparse_simt(sp, dims->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int paged_attn_combine(const float *part_out, const float *part_lse, int split_kv, int64_t rows, int head_dim,

@@ -62,4 +62,41 @@ cudaError_t launch_gather(const void *cache, const int32_t *block_table, const i
                           int ps, int Hkv, int D, int esize, long long num_pages, int out_tokens, void *out,
                           unsigned int *err, cudaStream_t stream);
 
+// ---------------------------------------------------------------- serving step over selected pages
+struct StepTablesParams {
+    const int32_t *cached_lens, *new_lens, *free_pages, *free_count;
+    int32_t *block_table, *seq_lens, *q_offset, *q_start, *slots, *free_left;
+    unsigned int *err;
+    long long num_pages;
+    int free_cap, B, T, ps_shift, W;
+};
+cudaError_t launch_step_tables(const StepTablesParams &p, cudaStream_t stream);
+
+struct AppendParams {
+    const void *k_new, *v_new;
+    const int32_t *slots;
+    void *k_cache, *v_cache;
+    int8_t *env;       // [num_pages, Hkv, 2, D] or null
+    float *env_scale;  // [num_pages, Hkv]
+    unsigned int *err;
+    long long k_stride, v_stride;  // elements between tokens
+    long long num_slots;           // num_pages * ps
+    int T, Hkv, ps_shift;
+};
+cudaError_t launch_append(const AppendParams &p, int dtype, int D, cudaStream_t stream);
+
+// The pages a query token attends to.  f.Sq is the uniform batch's query count; with f.q_start the
+// tokens are packed and n_tok is the row count of q.
+struct SparseParams {
+    FwdParams f;
+    const int8_t *env;  // selection only
+    const float *env_scale;
+    int32_t *sel_out;
+    const int32_t *sel;  // attention only: [n_tok, Hkv, K]
+    long long n_tok;
+    int K, sink, local;
+};
+cudaError_t launch_select_pages(const SparseParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_sparse_simt(const SparseParams &p, int dtype, cudaStream_t stream);
+
 }  // namespace pa

@@ -1,0 +1,600 @@
+"""The serving step over selected pages on the GPU: tables and slots, append with page envelopes, page
+selection and attention over the selected pages, each against the plain implementation
+(tests/_sparse_ref.py), then run together.
+
+What the calls compute in whole numbers or exactly (tables, slots, cache rows, envelopes, selections)
+must match bit for bit.  Attention is held to the library's bars: half a rounding step of the output
+type (bf16 2^-8, f16 2^-11 relative, within rtol 2^-8) on top of the float32 sums, whose error at unit
+normal inputs is at most 2 max|v| D 2^-24 sum|q_d k_d| scale = 2 * 4 * 256 * 2^-24 * 16 < 2e-3.
+"""
+import numpy as np
+import pytest
+
+from paged_kv_cache_201_gb300 import workloads as W
+from tests import _gpu
+from tests import _sparse_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pa():
+    import paged_kv_cache_201_gb300 as pa
+    pa.load_library(build_if_missing=True)
+    pa.paged_attn_last_error_word()
+    return pa
+
+
+def _t(a, dtype=None):
+    import torch
+    x = torch.from_numpy(np.ascontiguousarray(a, dtype=dtype))
+    return x.cuda()
+
+
+def _bits(t, dtype):
+    return _gpu.to_host_elems(t, dtype)
+
+
+def _raw(a):
+    a = np.ascontiguousarray(a)
+    return a.view(np.uint32) if a.dtype == np.float32 else a
+
+
+# ----------------------------------------------------------------------------- tables and slots
+def _run_tables(pa, cached, new, free, count, table, total, ps, num_pages, alias=False):
+    import torch
+    B = len(cached)
+    c, n, f, cnt, bt = _t(cached, np.int32), _t(new, np.int32), _t(free, np.int32), _t([count], np.int32), _t(table)
+    sl = c if alias else torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    left = cnt if alias else torch.full((1,), -7, dtype=torch.int32, device="cuda")
+    qo, qs = torch.full((B,), -7, dtype=torch.int32, device="cuda"), torch.full((B + 1,), -7, dtype=torch.int32,
+                                                                               device="cuda")
+    slots = torch.full((total,), -7, dtype=torch.int32, device="cuda")
+    pa.paged_attn_step_tables(c, n, f, cnt, bt, sl, qo, qs, slots, left, ps, num_pages)
+    bits = pa.paged_attn_last_error_word()
+    return {"table": bt.cpu().numpy(), "seq_lens": sl.cpu().numpy(), "q_offset": qo.cpu().numpy(),
+            "q_start": qs.cpu().numpy(), "slots": slots.cpu().numpy(), "free_left": left.cpu().numpy()}, bits
+
+
+def _check_tables(pa, cached, new, free, count, table, total, ps, num_pages, alias=False):
+    want = R.step_tables(np.asarray(cached), np.asarray(new), free, count, table, total, ps, num_pages)
+    got, bits = _run_tables(pa, cached, new, free, count, table, total, ps, num_pages, alias)
+    for k, v in got.items():
+        np.testing.assert_array_equal(v, want[k], err_msg=k)
+    assert bool(bits & pa.ERRBIT_REFUSED) == want["refused"]
+    assert bool(bits & pa.ERRBIT_PAGE_RANGE) == want["bad_page"]
+    assert not bits & ~(pa.ERRBIT_REFUSED | pa.ERRBIT_PAGE_RANGE)
+    return want
+
+
+def _tables_case(seed, B, width, ps, chunk, count, idle=0.1):
+    rng = np.random.default_rng(seed)
+    new = np.where(rng.uniform(size=B) < 0.6, 1, rng.integers(1, chunk + 1, B))
+    new[rng.uniform(size=B) < idle] = 0
+    cached = np.minimum(rng.integers(0, width * ps, B), np.maximum(width * ps - new, 0))
+    cached[rng.uniform(size=B) < 0.2] = 0
+    exact = rng.uniform(size=B) < 0.2
+    cached[exact] = cached[exact] // ps * ps  # the last page is full
+    need = -(-cached // ps)
+    pages = int(need.sum()) + count
+    ids = rng.permutation(pages).astype(np.int32)
+    table = np.full((B, width), W.SENTINEL_MAX, np.int32)
+    table[np.arange(width)[None] < need[:, None]] = ids[:int(need.sum())]
+    return cached.astype(np.int32), new.astype(np.int32), ids[int(need.sum()):], table, pages
+
+
+@pytest.mark.parametrize("ps", [16, 32, 64])
+@pytest.mark.parametrize("B,width,chunk", [(1, 4, 1), (1, 40, 600), (33, 20, 50), (1024, 24, 40), (1025, 6, 3),
+                                           (5000, 4, 9)])
+@pytest.mark.parametrize("alias", [False, True])
+def test_tables(pa, B, width, chunk, ps, alias):
+    cached, new, free, table, pages = _tables_case(B + ps, B, width, ps, min(chunk, width * ps), B * 3 + 50)
+    total = int(new.sum()) + 13
+    want = _check_tables(pa, cached, new, free, len(free), table, total, ps, pages, alias)
+    assert not want["refused"] and want["q_start"][-1] == new.sum()
+
+
+def test_tables_largest_batch(pa):
+    B = 16384
+    cached, new, free, table, pages = _tables_case(3, B, 3, 16, 5, 3 * B)
+    _check_tables(pa, cached, new, free, len(free), table, int(new.sum()), 16, pages)
+
+
+@pytest.mark.parametrize("count,total", [(7, 4000), (4000, 61), (0, 300), (9, 100)])
+def test_tables_too_few_pages_or_slots(pa, count, total):
+    """Requests past the free pages or the slots are turned down; those that need no page and fit go on."""
+    cached, new, free, table, pages = _tables_case(11, 60, 20, 16, 40, 4000)
+    want = _check_tables(pa, cached, new, free, count, table, total, 16, pages)
+    assert want["refused"]
+
+
+def test_tables_odd_requests(pa):
+    """Negative lengths, rows without room, a free count past the stack, ids outside the pool, idle
+    requests, lengths whose sum passes 31 bits."""
+    ps, width = 16, 4
+    cached = np.array([-1, 5, 64, 63, 0, 10, 2**31 - 1, 16, 3], np.int32)
+    new = np.array([3, -2, 1, 1, 65, 0, 2**31 - 1, 16, 0], np.int32)
+    table = np.arange(9 * width, dtype=np.int32).reshape(9, width)
+    table[3, 3] = -5  # the last token of request 3 lands in a page outside the pool
+    free = np.array([50, 99, 1], np.int32)  # 99 is outside it too
+    _check_tables(pa, cached, new, free, 3, table, 100, ps, 60)
+    _check_tables(pa, cached, new, free, 2, table, 100, ps, 60)
+    _check_tables(pa, cached, new, free, 8, table, 100, ps, 60)
+    _check_tables(pa, cached, new, free, -3, table, 100, ps, 60)
+    _check_tables(pa, np.zeros(4, np.int32), np.zeros(4, np.int32), free, 3, table[:4], 0, ps, 60)
+
+
+# ----------------------------------------------------------------------------- append
+def _append_case(seed, q_lens, seq_lens, Hkv, D, ps, dtype, pads=3):
+    b = R.Batch(seed, q_lens, seq_lens, Hkv, Hkv, D, ps, dtype)
+    rng = np.random.default_rng(seed + 1)
+    slots = []
+    for s, n in enumerate(q_lens):
+        for x in range(int(b.seq_lens[s]) - n, int(b.seq_lens[s])):
+            slots.append(int(b.table[s, x // ps]) * ps + x % ps)
+    slots += [-1] * pads
+    shape = (len(slots), Hkv, D)
+    return b, np.asarray(slots, np.int32), R.random_elems(rng, shape, dtype), R.random_elems(rng, shape, dtype)
+
+
+def _run_append(pa, b, slots, kn, vn, env=True, strided=False):
+    import torch
+    dt = b.dtype
+    d = b.device()
+    kd, vd = W.host_to_torch(kn, dt).cuda(), W.host_to_torch(vn, dt).cuda()
+    if strided:  # slices of one projection's output, other elements NaN
+        T, Hkv, D = kn.shape
+        fused = torch.full((T, 3 * Hkv, D), float("nan"), dtype=kd.dtype, device="cuda")
+        fused[:, Hkv:2 * Hkv], fused[:, 2 * Hkv:] = kd, vd
+        kd, vd = fused[:, Hkv:2 * Hkv], fused[:, 2 * Hkv:]
+    e = s = None
+    if env:
+        e = torch.full((b.P, b.Hkv, 2, b.D), 77, dtype=torch.int8, device="cuda")
+        s = torch.full((b.P, b.Hkv), -1.0, device="cuda")
+    pa.paged_attn_append(kd, vd, _t(slots), d["k"], d["v"], e, s)
+    torch.cuda.synchronize()
+    return (_bits(d["k"], dt), _bits(d["v"], dt), None if e is None else e.cpu().numpy(),
+            None if s is None else s.cpu().numpy())
+
+
+def _check_append(pa, b, slots, kn, vn, env=True, strided=False):
+    k, v = b.k.copy(), b.v.copy()
+    e = np.full((b.P, b.Hkv, 2, b.D), 77, np.int8) if env else None
+    s = np.full((b.P, b.Hkv), -1.0, np.float32) if env else None
+    R.append(kn, vn, slots, k, v, b.dtype, e, s)
+    gk, gv, ge, gs = _run_append(pa, b, slots, kn, vn, env, strided)
+    np.testing.assert_array_equal(_raw(gk), _raw(k))
+    np.testing.assert_array_equal(_raw(gv), _raw(v))
+    if env:
+        np.testing.assert_array_equal(gs, s)
+        np.testing.assert_array_equal(ge, e)
+
+
+APPEND_BATCHES = [([1], [1]), ([1, 1, 1], [16, 17, 64]), ([5, 1, 130, 16, 0], [5, 40, 131, 32, 9]),
+                  ([200], [333])]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Hkv,D,ps", [(1, 64, 16), (3, 128, 32), (8, 128, 16), (2, 256, 64), (5, 64, 64)])
+@pytest.mark.parametrize("q_lens,seq_lens", APPEND_BATCHES)
+def test_append(pa, dtype, Hkv, D, ps, q_lens, seq_lens):
+    b, slots, kn, vn = _append_case(D + ps, q_lens, seq_lens, Hkv, D, ps, dtype)
+    _check_append(pa, b, slots, kn, vn, strided=len(q_lens) > 1)
+
+
+def test_append_without_envelopes_any_order(pa):
+    """Without envelopes the tokens may come in any order."""
+    b, slots, kn, vn = _append_case(4, [9, 40], [50, 40], 2, 128, 16, "bf16")
+    perm = np.random.default_rng(0).permutation(len(slots))
+    _check_append(pa, b, slots[perm], kn[perm], vn[perm], env=False)
+
+
+def test_append_token_by_token_gives_the_same_envelopes(pa):
+    import torch
+    b, slots, kn, vn = _append_case(5, [37], [37], 2, 128, 32, "bf16", pads=0)
+    _, _, e, s = _run_append(pa, b, slots, kn, vn)
+    d = b.device()
+    env, scale = torch.full((b.P, 2, 2, 128), 77, dtype=torch.int8, device="cuda"), torch.full((b.P, 2), -1.0,
+                                                                                            device="cuda")
+    kd, vd, sd = W.host_to_torch(kn, "bf16").cuda(), W.host_to_torch(vn, "bf16").cuda(), _t(slots)
+    for t in range(37):
+        pa.paged_attn_append(kd[t:t + 1], vd[t:t + 1], sd[t:t + 1], d["k"], d["v"], env, scale)
+    np.testing.assert_array_equal(env.cpu().numpy(), e)
+    np.testing.assert_array_equal(scale.cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_special_values(pa, dtype):
+    """NaN and infinite keys mark the page; zero keys, the smallest and the largest numbers quantise."""
+    b, slots, kn, vn = _append_case(6, [16] * 6, [16] * 6, 2, 64, 16, dtype, pads=0)
+    f32 = dtype == "f32"
+    one = lambda x: np.float32(x) if f32 else W.bf16_bits_rne(np.float32([x]))[0]  # noqa: E731
+    kn[3, 0, 7] = one(np.nan)
+    kn[16 + 5, 1, 9] = one(-np.inf)
+    kn[32:48] = one(0.0)
+    kn[48:64] = one(0.0)
+    kn[50, 0, 3] = one(1e-39)  # below the smallest normal number
+    kn[64:80, 0] = one(3e38)
+    kn[66, 0, 1] = one(-3.3e38)
+    _check_append(pa, b, slots, kn, vn)
+
+
+def test_append_bad_slots(pa):
+    """Slots outside the pool are skipped and reported; -1 is skipped in silence."""
+    b, slots, kn, vn = _append_case(7, [6], [20], 2, 128, 16, "f16")
+    pa.paged_attn_last_error_word()
+    _check_append(pa, b, slots, kn, vn)
+    assert pa.paged_attn_last_error_word() == 0
+    slots[1], slots[4] = b.P * 16, -9
+    b2 = R.Batch(7, [6], [20], 2, 2, 128, 16, "f16")
+    _check_append(pa, b2, slots, kn, vn, env=False)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+
+
+# ----------------------------------------------------------------------------- selection
+def _run_select(pa, b, env, scale, sink, local, K, causal=True, q_offset=None, uniform=False, q=None):
+    import torch
+    d = b.device()
+    q = d["q"] if q is None else q
+    qo = None if q_offset is None else _t(q_offset, np.int32)
+    sel = torch.full((q.shape[0], b.Hkv, K), -9, dtype=torch.int32, device="cuda")
+    if uniform:
+        B = len(b.q_lens)
+        pa.paged_attn_select_pages(q.view(B, -1, b.Hq, b.D), _t(env), _t(scale), d["table"], d["lens"], causal, qo,
+                                   sink, local, sel.view(B, -1, b.Hkv, K), b.ps)
+    else:
+        pa.paged_attn_select_pages(q, _t(env), _t(scale), d["table"], d["lens"], causal, qo, sink, local, sel, b.ps,
+                                   q_start=d["q_start"])
+    torch.cuda.synchronize()
+    return sel.cpu().numpy()
+
+
+def _check_select(pa, b, sink, local, K, causal=True, q_offset=None, env=None, uniform=False):
+    env = b.envelopes() if env is None else env
+    want = R.select(b.q64(), *env, b.table, b.rows(causal, q_offset), b.Hkv, b.ps, sink, local, K)
+    got = _run_select(pa, b, *env, sink, local, K, causal, q_offset, uniform)
+    np.testing.assert_array_equal(got[:b.T], want)
+    assert (got[b.T:] == -9).all()  # rows of no sequence are left as they were
+    assert pa.paged_attn_last_error_word() == 0
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(8, 2, 128, 16), (3, 3, 64, 32), (14, 2, 256, 16), (24, 1, 128, 64),
+                                         (40, 1, 64, 16), (130, 1, 64, 16)])
+def test_select(pa, dtype, Hq, Hkv, D, ps):
+    b = R.Batch(Hq + D, [1, 3, 0, 1, 7], [1, 40 * ps, 9, 31 * ps + 5, 23 * ps + 1], Hq, Hkv, D, ps, dtype, q_pad=2)
+    for sink, local, K in [(1, 2, 8), (0, 0, 1), (0, 0, 5), (2, 3, 5), (0, 4, 23), (1, 0, 64)]:
+        _check_select(pa, b, sink, local, K)
+
+
+def test_select_masks(pa):
+    """Non-causal, explicit offsets (one puts every key out of reach), the uniform layout, a view of q."""
+    import torch
+    b = R.Batch(2, [4, 4, 4], [900, 30, 500], 8, 2, 128, 16, "bf16")
+    _check_select(pa, b, 1, 2, 6, causal=False)
+    _check_select(pa, b, 1, 2, 6, q_offset=[300, -9, 496])
+    _check_select(pa, b, 1, 2, 6, uniform=True)
+    env = b.envelopes()
+    fused = torch.full((b.T, 12, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fused[:, 2:10] = b.device()["q"]
+    got = _run_select(pa, b, *env, 1, 2, 6, q=fused[:, 2:10])
+    np.testing.assert_array_equal(got, R.select(b.q64(), *env, b.table, b.rows(), 2, 16, 1, 2, 6))
+
+
+def test_select_ties_and_marks(pa):
+    """Equal scores go to the lowest pages; marked (non-finite) pages come first; a non-finite or zero
+    query scores 0 everywhere."""
+    b = R.Batch(3, [1, 1, 2], [1600, 1000, 700], 4, 2, 64, 16, "f32")
+    env, scale = b.envelopes()
+    same = np.broadcast_to(env[:1, :1], env.shape).copy()
+    _check_select(pa, b, 1, 1, 9, env=(same, np.ones_like(scale)))
+    marked = scale.copy()
+    marked[np.random.default_rng(0).uniform(size=scale.shape) < 0.1] = np.inf
+    _check_select(pa, b, 1, 1, 9, env=(env, marked))
+    _check_select(pa, b, 0, 0, 30, env=(env, np.where(np.isnan(scale), scale, np.float32(3e38))))  # scores overflow
+    b.q[0] = 0
+    b.q[1, 1, 5] = np.nan
+    b.q[2, 3, 0] = np.inf
+    _check_select(pa, b, 0, 1, 9)
+
+
+@pytest.mark.parametrize("B,pages,K,ps", [(2, 4097, 64, 16), (1, 20000, 128, 16), (3, 1025, 100, 64),
+                                          (1, 49151, 700, 16), (5, 2047, 2000, 32)])
+def test_select_long(pa, B, pages, K, ps):
+    """Long sequences: envelopes drawn directly (many equal scores among them)."""
+    rng = np.random.default_rng(pages)
+    b = R.Batch(pages, [1] * B, [1] * B, 4, 1, 64, ps, "bf16")
+    lens = pages * ps - rng.integers(0, ps, B) - ps * rng.integers(0, pages // 3, B)
+    lens[0] = pages * ps
+    b.seq_lens = lens.astype(np.int32)
+    b.width, b.P = pages, 5000
+    b.table = rng.integers(0, b.P, (B, pages)).astype(np.int32)
+    hi = rng.integers(-127, 128, (b.P, 1, 64)).astype(np.int8)
+    lo = np.minimum(hi, rng.integers(-127, 128, (b.P, 1, 64))).astype(np.int8)
+    _check_select(pa, b, 1, 2, K, env=(np.stack([lo, hi], 2), rng.uniform(0.5, 1, (b.P, 1)).astype(np.float32)))
+
+
+def test_select_bad_pages(pa):
+    """Ids outside the pool score 0 and are reported."""
+    b = R.Batch(8, [2, 1], [800, 600], 4, 2, 128, 16, "bf16")
+    env = b.envelopes()
+    b.table[0, 3], b.table[1, 20], b.table[0, 30] = b.P, -1, W.SENTINEL_MAX
+    want = R.select(b.q64(), *env, b.table, b.rows(), 2, 16, 1, 2, 8)
+    np.testing.assert_array_equal(_run_select(pa, b, *env, 1, 2, 8), want)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+
+
+# ----------------------------------------------------------------------------- attention over listed pages
+def _lists(b, K, seed=0, causal=True, q_offset=None):
+    """Random lists: distinct reachable pages in any order, some rows short, one empty."""
+    rng = np.random.default_rng(seed)
+    sel = np.full((b.T, b.Hkv, K), -1, np.int32)
+    for t, (_, reach) in enumerate(b.rows(causal, q_offset)):
+        np_ = -(-reach // b.ps)
+        for h in range(b.Hkv):
+            n = min(np_, K if rng.uniform() < 0.7 else rng.integers(0, K + 1))
+            sel[t, h, :n] = rng.permutation(np_)[:n]
+    return sel
+
+
+def _run_attend(pa, b, sel, causal=True, q_offset=None, uniform=False, q=None, scale=None, stream=None):
+    import torch
+    d = b.device()
+    q = d["q"] if q is None else q
+    qo = None if q_offset is None else _t(q_offset, np.int32)
+    full = np.full((q.shape[0], b.Hkv, sel.shape[-1]), 0, np.int32)
+    full[:b.T] = sel
+    out = torch.full(tuple(q.shape), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(tuple(q.shape[:-1]), 7.0, device="cuda")
+    scale = b.D ** -0.5 if scale is None else scale
+    if uniform:
+        B = len(b.q_lens)
+        u = lambda t: t.view(B, -1, *t.shape[1:])  # noqa: E731
+        pa.paged_attn_fwd_sparse(u(q), d["k"], d["v"], d["table"], d["lens"], causal, qo, u(_t(full)), scale, u(out),
+                                 u(lse))
+    else:
+        pa.paged_attn_fwd_sparse(q, d["k"], d["v"], d["table"], d["lens"], causal, qo, _t(full), scale, out, lse,
+                                 q_start=d["q_start"])
+    torch.cuda.synchronize()
+    assert (out[b.T:] == 7.0).all() and (lse[b.T:] == 7.0).all()  # rows of no sequence are left as they were
+    return _gpu.to_f64(out[:b.T], b.dtype), _gpu.to_f64(lse[:b.T], "f32")
+
+
+def _check_attend(pa, b, sel, causal=True, q_offset=None, scale=None, **kw):
+    out, lse = _run_attend(pa, b, sel, causal, q_offset, scale=scale, **kw)
+    k, v = R.elems_to_f64(b.k, b.dtype), R.elems_to_f64(b.v, b.dtype)
+    want = R.attend(b.q64(), k, v, b.table, b.rows(causal, q_offset), sel, b.ps, b.D ** -0.5 if scale is None else scale)
+    _gpu.assert_close(out, want[0], b.dtype, "out")
+    _gpu.assert_close(lse, want[1], b.dtype, "lse")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(8, 2, 128, 16), (3, 3, 64, 32), (14, 2, 128, 64), (24, 1, 64, 16),
+                                         (33, 1, 128, 32), (6, 2, 256, 16), (16, 1, 256, 64), (2, 2, 256, 32),
+                                         (4, 4, 128, 16), (16, 1, 64, 64)])
+def test_attend(pa, dtype, Hq, Hkv, D, ps):
+    b = R.Batch(Hq * D, [1, 3, 0, 1, 5], [1, 12 * ps, 9, 7 * ps + 5, 9 * ps + 1], Hq, Hkv, D, ps, dtype, q_pad=2)
+    for K in (1, 7, 12):
+        _check_attend(pa, b, _lists(b, K))
+
+
+def test_attend_few_rows_long_lists(pa):
+    """One token over hundreds of pages (the split over the list), in each type."""
+    for dtype, D in (("bf16", 128), ("f16", 64), ("f32", 128), ("bf16", 256)):
+        for n in (1, 2):
+            b = R.Batch(D, [1] * n, [6000, 4000][:n], 8, 2, D, 16, dtype)
+            _check_attend(pa, b, _lists(b, 300))
+
+
+def test_attend_masks(pa):
+    """Non-causal, explicit offsets (one puts every key out of reach), the uniform layout, a view of q,
+    a negative and a zero scale."""
+    import torch
+    for dtype in ("bf16", "f32"):
+        b = R.Batch(2, [4, 4, 4], [190, 30, 150], 8, 2, 128, 16, dtype)
+        _check_attend(pa, b, _lists(b, 6, causal=False), causal=False)
+        qo = [60, -9, 146]
+        _check_attend(pa, b, _lists(b, 6, q_offset=qo), q_offset=qo)
+        sel = _lists(b, 6)
+        _check_attend(pa, b, sel, uniform=True)
+        _check_attend(pa, b, sel, scale=-0.1)
+        _check_attend(pa, b, sel, scale=0.0)
+        fused = torch.full((b.T, 12, 128), float("nan"), dtype=b.device()["q"].dtype, device="cuda")
+        fused[:, 2:10] = b.device()["q"]
+        _check_attend(pa, b, sel, q=fused[:, 2:10])
+
+
+def test_attend_any_list(pa):
+    """Entries out of reach and negative ones list nothing, repeated ones count again; an empty list gives
+    0 and -inf."""
+    for dtype in ("f16", "f32"):
+        b = R.Batch(9, [2, 1], [150, 80], 4, 2, 128, 16, dtype)
+        sel = _lists(b, 9)
+        sel[0, 0] = [-1, 3, W.SENTINEL_MAX, 3, 9, -2**31, 0, 10, 3]
+        sel[1, 1] = -1
+        sel[2, 0] = 99
+        _check_attend(pa, b, sel)
+    assert pa.paged_attn_last_error_word() == 0
+
+
+def test_attend_bad_pages(pa):
+    """A listed page whose id is outside the pool reads as zeros and is reported."""
+    for dtype in ("bf16", "f32"):
+        b = R.Batch(8, [2, 1], [300, 200], 4, 2, 128, 16, dtype)
+        b.table[0, 3], b.table[1, 2] = b.P, -1
+        sel = _lists(b, 8)
+        sel[:, :, 0], sel[:, :, 1] = 3, 2
+        _check_attend(pa, b, sel)
+        assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+
+
+def test_attend_every_page_is_dense_attention(pa):
+    """Listing every page gives what the dense call gives, to its bars."""
+    import torch
+    b = R.Batch(12, [1] * 4, [300, 17, 64, 1], 16, 4, 128, 16, "bf16")
+    d = b.device()
+    K = b.width
+    sel = torch.arange(K, dtype=torch.int32, device="cuda").repeat(4, 1, 4, 1).contiguous()
+    q = d["q"].view(4, 1, 16, 128)
+    out, lse = torch.empty_like(q), torch.empty(4, 1, 16, device="cuda")
+    pa.paged_attn_fwd_sparse(q, d["k"], d["v"], d["table"], d["lens"], True, None, sel, 128 ** -0.5, out, lse)
+    dense, dl = pa.attention(q, d["k"], d["v"], d["table"], d["lens"], causal=True, want_lse=True)
+    _gpu.assert_close(_gpu.to_f64(out, "bf16"), _gpu.to_f64(dense, "bf16"), "bf16", "out")
+    _gpu.assert_close(_gpu.to_f64(lse, "f32"), _gpu.to_f64(dl, "f32"), "bf16", "lse")
+
+
+def test_attend_nan_reaches_its_rows_only(pa):
+    """A NaN in a listed page gives NaN in the rows that list it, and only there."""
+    b = R.Batch(13, [1, 1], [200, 200], 4, 2, 128, 16, "bf16")
+    sel = np.zeros((2, 2, 3), np.int32)
+    sel[:] = [1, 4, 12]
+    b.k[b.table[0, 4], 2, 1, 3] = 0x7FC0
+    out, lse = _run_attend(pa, b, sel)
+    bad = np.isnan(out).all(-1)
+    assert bad[0, 2:].all() and not np.isnan(out[0, :2]).any() and not np.isnan(out[1]).any()
+
+
+# ----------------------------------------------------------------------------- the step as it is used
+def _serve(pa, dtype, Hq, Hkv, D, ps, plan, top_k, graph=False, stream=None):
+    """Run a serving loop: ``plan`` is a list of new-token counts per request and step.  Every step's
+    output is checked against the plain implementation on the host's own copy of the state."""
+    import torch
+    rng = np.random.default_rng(17)
+    B, steps = len(plan[0]), len(plan)
+    total_len = np.asarray(plan).sum(0)
+    width = int(-(-total_len.max() // ps)) + 1
+    P = int((-(-total_len // ps)).sum()) + 5
+    T = int(np.asarray(plan).sum(1).max()) + 3
+    pool = (P, ps, Hkv, D)
+    nan = {"f32": np.float32(np.nan), "f16": np.uint16(0x7E00), "bf16": np.uint16(0x7FC0)}[dtype]
+    zero = np.zeros(pool, np.float32 if dtype == "f32" else np.uint16)
+    hk, hv = zero + nan, zero + nan
+    k, v = W.host_to_torch(hk, dtype).cuda(), W.host_to_torch(hv, dtype).cuda()
+    env, scale = pa.page_envelopes(k)
+    henv, hscale = np.zeros((P, Hkv, 2, D), np.int8), np.zeros((P, Hkv), np.float32)
+    i32 = lambda a: _t(np.asarray(a), np.int32)  # noqa: E731
+    free = rng.permutation(P).astype(np.int32)
+    table = np.full((B, width), -1, np.int32)
+    lens = np.zeros(B, np.int32)
+    count = P
+    d_free, d_count, d_table, d_lens = i32(free), i32([count]), _t(table), i32(lens)
+    d_new, d_qo, d_qs, d_slots = i32([0] * B), i32([0] * B), i32([0] * (B + 1)), i32([0] * T)
+    tdt = W.torch_dtype(dtype)
+    qkv = torch.zeros((T, Hq + 2 * Hkv, D), dtype=tdt, device="cuda")
+    sel = torch.zeros((T, Hkv, top_k), dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros((T, Hq, D), dtype=tdt, device="cuda"), torch.zeros((T, Hq), device="cuda")
+
+    def step():
+        pa.paged_attn_step_tables(d_lens, d_new, d_free, d_count, d_table, d_lens, d_qo, d_qs, d_slots, d_count, ps, P)
+        pa.paged_attn_append(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], d_slots, k, v, env, scale)
+        pa.paged_attn_select_pages(qkv[:, :Hq], env, scale, d_table, d_lens, True, d_qo, 1, 1, sel, ps, q_start=d_qs)
+        pa.paged_attn_fwd_sparse(qkv[:, :Hq], k, v, d_table, d_lens, True, d_qo, sel, D ** -0.5, out, lse,
+                                 q_start=d_qs)
+
+    run = step
+    if graph:
+        d_new.zero_()
+        step()  # first calls outside the capture; an idle step changes nothing
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        run = g.replay
+    for n, new in enumerate(plan):
+        new = np.asarray(new, np.int32)
+        h = R.random_elems(rng, (T, Hq + 2 * Hkv, D), dtype)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        d_new.copy_(_t(new))
+        qkv.copy_(W.host_to_torch(h, dtype))
+        torch.cuda.synchronize()
+        if stream is None:
+            run()
+        else:
+            with torch.cuda.stream(stream):
+                run()
+        torch.cuda.synchronize()
+        want = R.step_tables(lens, new, free, count, table, T, ps, P)
+        assert not want["refused"]
+        np.testing.assert_array_equal(d_slots.cpu().numpy(), want["slots"])
+        np.testing.assert_array_equal(d_table.cpu().numpy(), want["table"])
+        table, lens, count = want["table"], want["seq_lens"], int(want["free_left"][0])
+        R.append(h[:, Hq:Hq + Hkv], h[:, Hq + Hkv:], want["slots"], hk, hv, dtype, henv, hscale)
+        np.testing.assert_array_equal(env.cpu().numpy(), henv)
+        np.testing.assert_array_equal(scale.cpu().numpy(), hscale)
+        rows = R.token_rows(new.tolist(), lens, width, ps, True, None)
+        m = int(new.sum())
+        q64 = R.elems_to_f64(h[:m, :Hq], dtype)
+        ref_sel = R.select(q64, henv, hscale, table, rows, Hkv, ps, 1, 1, top_k)
+        np.testing.assert_array_equal(sel.cpu().numpy()[:m], ref_sel)
+        ref = R.attend(q64, R.elems_to_f64(hk, dtype), R.elems_to_f64(hv, dtype), table, rows, ref_sel, ps, D ** -0.5)
+        _gpu.assert_close(_gpu.to_f64(out, dtype)[:m], ref[0], dtype, f"step {n} out")
+        _gpu.assert_close(_gpu.to_f64(lse, "f32")[:m], ref[1], dtype, f"step {n} lse")
+    assert pa.paged_attn_last_error_word() == 0
+
+
+PLAN = [[130, 0, 7, 64], [1, 90, 1, 1], [1, 1, 0, 1], [3, 1, 1, 1], [1, 1, 33, 1]]
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,ps", [("bf16", 8, 2, 128, 16), ("f16", 3, 3, 64, 32), ("f32", 4, 1, 256, 16),
+                                               ("bf16", 14, 2, 256, 32)])
+def test_serving_loop(pa, dtype, Hq, Hkv, D, ps):
+    _serve(pa, dtype, Hq, Hkv, D, ps, PLAN, top_k=4)
+
+
+def test_serving_loop_as_a_graph(pa):
+    """The four calls captured once; every replay takes the state the last one left."""
+    _serve(pa, "bf16", 8, 2, 128, 16, PLAN, top_k=4, graph=True)
+
+
+def test_serving_loop_on_another_stream(pa):
+    import torch
+    _serve(pa, "bf16", 8, 2, 128, 16, PLAN, top_k=4, stream=torch.cuda.Stream())
+
+
+def test_attention_sparse(pa):
+    """The convenience call: selection and attention, with its allocations on a stream of its own."""
+    import torch
+    b = R.Batch(21, [1, 1], [700, 400], 8, 2, 128, 16, "bf16")
+    env = b.envelopes()
+    d = b.device()
+    e, s = _t(env[0]), _t(env[1])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    out, lse, sel = pa.attention_sparse(d["q"], d["k"], d["v"], e, s, d["table"], d["lens"], top_k=12,
+                                        q_start=d["q_start"], want_lse=True, want_pages=True, stream=st)
+    torch.cuda.synchronize()
+    ref_sel = R.select(b.q64(), *env, b.table, b.rows(), 2, 16, 1, 2, 12)
+    np.testing.assert_array_equal(sel.cpu().numpy(), ref_sel)
+    k, v = R.elems_to_f64(b.k, "bf16"), R.elems_to_f64(b.v, "bf16")
+    ref = R.attend(b.q64(), k, v, b.table, b.rows(), ref_sel, 16, 128 ** -0.5)
+    _gpu.assert_close(_gpu.to_f64(out, "bf16"), ref[0], "bf16", "out")
+    _gpu.assert_close(_gpu.to_f64(lse, "f32"), ref[1], "bf16", "lse")
+
+
+def test_same_bits_on_every_run(pa):
+    b = R.Batch(22, [1, 2, 1], [5000, 900, 3000], 8, 2, 128, 16, "bf16")
+    sel = _lists(b, 100)
+    first = _run_attend(pa, b, sel)
+    for _ in range(3):
+        again = _run_attend(pa, b, sel)
+        assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+def test_malformed_q_start(pa):
+    """A sequence whose q_start entries are out of range is skipped and reported."""
+    import torch
+    b = R.Batch(23, [1, 1, 1], [300, 200, 100], 4, 2, 64, 16, "bf16")
+    d = b.device()
+    env = b.envelopes()
+    for qs in ([0, 1, 2, 9], [0, 1, -5, 3], [0, 9, 2, 3]):
+        sel = torch.full((3, 2, 4), -9, dtype=torch.int32, device="cuda")
+        q_start = _t(qs, np.int32)
+        pa.paged_attn_select_pages(d["q"], _t(env[0]), _t(env[1]), d["table"], d["lens"], True, None, 1, 1, sel, 16,
+                                   q_start=q_start)
+        good = sel.clamp(min=-1)
+        out = torch.empty_like(d["q"])
+        pa.paged_attn_fwd_sparse(d["q"], d["k"], d["v"], d["table"], d["lens"], True, None, good, 0.1, out, None,
+                                 q_start=q_start)
+        assert pa.paged_attn_last_error_word() & ~pa.ERRBIT_QSTART == 0
