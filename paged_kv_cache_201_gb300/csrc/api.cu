@@ -788,7 +788,12 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
     sp.sel = sel;
     sp.n_tok = n_tok;
     sp.K = top_k;
-    return cuda_status(pa::launch_sparse_simt(sp, dims->dtype, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dims->dtype == PA_F32) return cuda_status(pa::launch_sparse_simt(sp, dims->dtype, st));
+    CUtensorMap tmk, tmv;
+    if ((rc = make_pool_map(&tmk, k_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;
+    if ((rc = make_pool_map(&tmv, v_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;
+    return cuda_status(pa::launch_sparse_mma(sp, dims->dtype, device_sm_count(), tmk, tmv, st));
 }
 
 int paged_attn_combine(const float *part_out, const float *part_lse, int split_kv, int64_t rows, int head_dim,
