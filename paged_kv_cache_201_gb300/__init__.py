@@ -189,9 +189,11 @@ def _q_token_stride(q) -> int:
 
 
 def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle, without building a Stream object (3 us on the Grace host)
     torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def dims_of(q, k_cache, block_table) -> PaDims:
@@ -476,28 +478,44 @@ def paged_attn_fwd_varlen_overlap(q, k_cache, v_cache, block_table, seq_lens, q_
 
 
 # ----------------------------------------------------------------------------- serving step over selected pages
-def _check_device(*named) -> None:
-    """The tensors of one call are all on the current CUDA device (the one its stream belongs to)."""
-    dev = _torch().cuda.current_device()
-    for t, name in named:
-        if t is not None and t.get_device() != dev:
+def _need(t, name, dev, dtype, shape) -> None:
+    """t is a dense tensor of this type and shape on the current CUDA device dev, the one its stream
+    belongs to.  (These calls take tens of small tensors and a few microseconds: one test decides, and
+    the message is worked out only after it fails.)"""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _check(t, name, dtype, len(shape))
+        if t.get_device() != dev:
             raise ValueError(f"{name} must be on the current CUDA device {dev}")
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _check_rows(t, name, dtype, heads, head_dim) -> int:
-    """t [T, heads, head_dim] may be a view whose tokens are further apart than its heads; returns the
-    elements between tokens (0: dense)."""
+def _rows_stride(t, name, dev, dtype, shape) -> int:
+    """t [tokens, heads, head_dim] (or [batch, q_len, heads, head_dim]) may be a view whose tokens are
+    further apart than its heads; returns the elements between tokens (0: dense)."""
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return 0
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be [T, {heads}, {head_dim}], got {tuple(t.shape)}")
-    if t.is_contiguous():
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device {dev}")
+    tokens = t.numel() // max(1, shape[-2] * shape[-1])
+    if tokens == 0:
         return 0
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim) or t.stride(0) < heads * head_dim:
-        raise ValueError(f"{name}'s heads must be dense and its tokens apart ([T, H, D] rows)")
-    return int(t.stride(0)) if t.shape[0] > 1 else 0
+    heads, st = shape[-2], t.stride()
+    if st[-1] != 1 or (heads > 1 and st[-2] != shape[-1]):
+        raise ValueError(f"{name}'s heads must be dense ([..., H, D] contiguous)")
+    if tokens == 1:
+        return 0
+    tok = st[-3] if shape[-3] > 1 else st[0]
+    if len(shape) == 4 and shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * tok:
+        raise ValueError(f"{name}'s tokens must be evenly spaced across sequences")
+    if tok < heads * shape[-1]:
+        raise ValueError(f"{name}'s tokens must be apart (no broadcast or overlapping view)")
+    return int(tok)
 
 
 def paged_attn_step_tables(cached_lens, new_lens, free_pages, free_count, block_table, seq_lens, q_offset, q_start,
@@ -507,22 +525,26 @@ def paged_attn_step_tables(cached_lens, new_lens, free_pages, free_count, block_
     new_lens, seq_lens, q_offset [B], free_pages [F] (a stack), free_count, free_left [1], block_table
     [B, W] (in place), q_start [B + 1], slots [T].  seq_lens may be cached_lens, free_left free_count."""
     torch = _torch()
-    i32 = torch.int32
-    B, W = block_table.shape
-    for t, name, n in ((cached_lens, "cached_lens", B), (new_lens, "new_lens", B), (free_pages, "free_pages", None),
-                       (free_count, "free_count", 1), (seq_lens, "seq_lens", B), (q_offset, "q_offset", B),
-                       (q_start, "q_start", B + 1), (slots, "slots", None), (free_left, "free_left", 1)):
-        _check(t, name, i32, 1)
-        if n is not None and t.shape[0] != n:
-            raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    _check(block_table, "block_table", i32, 2)
-    _check_device((cached_lens, "cached_lens"), (new_lens, "new_lens"), (free_pages, "free_pages"),
-                  (free_count, "free_count"), (block_table, "block_table"), (seq_lens, "seq_lens"),
-                  (q_offset, "q_offset"), (q_start, "q_start"), (slots, "slots"), (free_left, "free_left"))
+    i32, dev = torch.int32, torch.cuda.current_device()
+    if block_table.dim() != 2 or free_pages.dim() != 1 or slots.dim() != 1:
+        raise ValueError("block_table must be [B, W], free_pages [F] and slots [T]")
+    B, W = bw = block_table.shape
+    F, T = free_pages.shape[0], slots.shape[0]
+    per_request, one = (B,), (1,)
+    _need(block_table, "block_table", dev, i32, bw)
+    _need(cached_lens, "cached_lens", dev, i32, per_request)
+    _need(new_lens, "new_lens", dev, i32, per_request)
+    _need(free_pages, "free_pages", dev, i32, (F,))
+    _need(free_count, "free_count", dev, i32, one)
+    _need(seq_lens, "seq_lens", dev, i32, per_request)
+    _need(q_offset, "q_offset", dev, i32, per_request)
+    _need(q_start, "q_start", dev, i32, (B + 1,))
+    _need(slots, "slots", dev, i32, (T,))
+    _need(free_left, "free_left", dev, i32, one)
     rc = load_library().paged_attn_step_tables(
-        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
-        free_count.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), q_offset.data_ptr(), q_start.data_ptr(),
-        slots.data_ptr(), free_left.data_ptr(), B, slots.shape[0], int(page_size), int(num_pages), W, _stream(stream))
+        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), F, free_count.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), q_offset.data_ptr(), q_start.data_ptr(), slots.data_ptr(),
+        free_left.data_ptr(), B, T, page_size, num_pages, W, _stream(stream))
     if rc:
         _raise(rc, "paged_attn_step_tables")
 
@@ -533,65 +555,53 @@ def paged_attn_append(k_new, v_new, slots, k_cache, v_cache, k_env=None, k_env_s
     [num_pages, Hkv, 2, D]) and k_env_scale (float32 [num_pages, Hkv]), the envelopes of the pages they
     land in; see ``paged_attn_append`` in include/paged_attn.h."""
     torch = _torch()
-    _check(k_cache, "k_cache", None, 4)
-    _check(v_cache, "v_cache", k_cache.dtype, 4)
-    P, ps, Hkv, D = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache shapes differ")
-    ks = _check_rows(k_new, "k_new", k_cache.dtype, Hkv, D)
-    vs = _check_rows(v_new, "v_new", k_cache.dtype, Hkv, D)
-    _check(slots, "slots", torch.int32, 1)
+    dev, dt = torch.cuda.current_device(), k_cache.dtype
+    if k_cache.dim() != 4 or slots.dim() != 1:
+        raise ValueError("k_cache must be [num_pages, page_size, Hkv, D] and slots [T]")
+    P, ps, Hkv, D = pool = k_cache.shape
     T = slots.shape[0]
-    if k_new.shape[0] != T or v_new.shape[0] != T:
-        raise ValueError("k_new, v_new and slots must have the same number of tokens")
+    _need(k_cache, "k_cache", dev, dt, pool)
+    _need(v_cache, "v_cache", dev, dt, pool)
+    _need(slots, "slots", dev, torch.int32, (T,))
+    rows = (T, Hkv, D)
+    ks, vs = _rows_stride(k_new, "k_new", dev, dt, rows), _rows_stride(v_new, "v_new", dev, dt, rows)
     if (k_env is None) != (k_env_scale is None):
         raise ValueError("k_env and k_env_scale come together")
+    env = scale = None
     if k_env is not None:
-        _check_env(k_env, k_env_scale, P, Hkv, D)
-    _check_device((k_new, "k_new"), (v_new, "v_new"), (slots, "slots"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                  (k_env, "k_env"), (k_env_scale, "k_env_scale"))
+        _need(k_env, "k_env", dev, torch.int8, (P, Hkv, 2, D))
+        _need(k_env_scale, "k_env_scale", dev, torch.float32, (P, Hkv))
+        env, scale = k_env.data_ptr(), k_env_scale.data_ptr()
     dims = PaDims(1, T, Hkv, Hkv, D, ps, P, 0, _dtype_code(k_cache))
-    rc = load_library().paged_attn_append(_ptr(k_new), _ptr(v_new), _ptr(slots), ks, vs, _ptr(k_cache), _ptr(v_cache),
-                                          _ptr(k_env), _ptr(k_env_scale), ctypes.byref(dims), _stream(stream))
+    rc = load_library().paged_attn_append(k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), ks, vs,
+                                          k_cache.data_ptr(), v_cache.data_ptr(), env, scale, dims, _stream(stream))
     if rc:
         _raise(rc, "paged_attn_append")
 
 
-def _check_env(k_env, k_env_scale, P, Hkv, D) -> None:
-    torch = _torch()
-    _check(k_env, "k_env", torch.int8, 4)
-    _check(k_env_scale, "k_env_scale", torch.float32, 2)
-    if tuple(k_env.shape) != (P, Hkv, 2, D) or tuple(k_env_scale.shape) != (P, Hkv):
-        raise ValueError(f"k_env must be {(P, Hkv, 2, D)} and k_env_scale {(P, Hkv)}, got {tuple(k_env.shape)} "
-                         f"and {tuple(k_env_scale.shape)}")
-
-
-def _sparse_dims(q, Hkv, D, ps, P, block_table, seq_lens, q_offset, q_start, sel, sel_name) -> PaDims:
-    """Shapes of a call over selected pages: q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start."""
-    torch = _torch()
-    _check_q(q, 4 if q_start is None else 3)
-    _check(block_table, "block_table", torch.int32, 2)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
-    _check(q_offset, "q_offset", torch.int32, 1)
-    _check(q_start, "q_start", torch.int32, 1)
-    _check(sel, sel_name, torch.int32, q.dim())
-    B, W = block_table.shape
-    Hq = q.shape[-2]
-    if q.shape[-1] != D:
+def _sparse_dims(q, Hkv, D, ps, P, block_table, seq_lens, q_offset, q_start, sel, dev) -> PaDims:
+    """Checks of a call over selected pages: q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start."""
+    i32 = _torch().int32
+    if block_table.dim() != 2 or q.dim() != (4 if q_start is None else 3) or sel.dim() != q.dim():
+        raise ValueError("block_table must be [B, W]; q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start; sel "
+                         "as q with [Hkv, top_k] for [Hq, D]")
+    B, W = bw = block_table.shape
+    shape = q.shape
+    Hq = shape[-2]
+    if shape[-1] != D:
         raise ValueError("q's head dim differs from the cache's")
-    if seq_lens.shape[0] != B or (q_offset is not None and q_offset.shape[0] != B):
-        raise ValueError("seq_lens and q_offset must have one entry per block_table row")
     if q_start is None:
-        if q.shape[0] != B:
+        if shape[0] != B:
             raise ValueError("q must have one batch entry per block_table row")
-    elif q_start.shape[0] != B + 1:
-        raise ValueError("q_start must have one entry more than block_table has rows")
-    if sel.shape[:-2] != q.shape[:-2] or sel.shape[-2] != Hkv:
-        raise ValueError(f"{sel_name} must be {tuple(q.shape[:-2])} + ({Hkv}, top_k), got {tuple(sel.shape)}")
-    stride = _q_token_stride(q)
-    if not stride and not q.is_contiguous() or stride and stride < Hq * D:
-        raise ValueError("q's tokens must be apart (no broadcast or overlapping view)")
-    return PaDims(B, q.shape[-3], Hq, Hkv, D, ps, P, W, _dtype_code(q), stride)
+    else:
+        _need(q_start, "q_start", dev, i32, (B + 1,))
+    _need(block_table, "block_table", dev, i32, bw)
+    _need(seq_lens, "seq_lens", dev, i32, (B,))
+    if q_offset is not None:
+        _need(q_offset, "q_offset", dev, i32, (B,))
+    _need(sel, "sel", dev, i32, (*shape[:-2], Hkv, sel.shape[-1]))
+    stride = _rows_stride(q, "q", dev, q.dtype, shape)
+    return PaDims(B, shape[-3], Hq, Hkv, D, ps, P, W, _dtype_code(q), stride)
 
 
 def paged_attn_select_pages(q, k_env, k_env_scale, block_table, seq_lens, causal, q_offset, sink_pages: int,
@@ -600,17 +610,18 @@ def paged_attn_select_pages(q, k_env, k_env_scale, block_table, seq_lens, causal
     logical pages, then -1): the first sink_pages, the last local_pages and the best of the others by
     the score of their key envelope; see ``paged_attn_select_pages`` in include/paged_attn.h.
     q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start [B + 1]."""
-    if k_env.dim() != 4:
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    if k_env.dim() != 4 or k_env.shape[2] != 2:
         raise ValueError("k_env must be [num_pages, Hkv, 2, D]")
     P, Hkv, _, D = k_env.shape
-    _check_env(k_env, k_env_scale, P, Hkv, D)
-    dims = _sparse_dims(q, Hkv, D, int(page_size), P, block_table, seq_lens, q_offset, q_start, sel, "sel")
-    _check_device((q, "q"), (k_env, "k_env"), (k_env_scale, "k_env_scale"), (block_table, "block_table"),
-                  (seq_lens, "seq_lens"), (q_offset, "q_offset"), (q_start, "q_start"), (sel, "sel"))
+    _need(k_env, "k_env", dev, torch.int8, k_env.shape)
+    _need(k_env_scale, "k_env_scale", dev, torch.float32, (P, Hkv))
+    dims = _sparse_dims(q, Hkv, D, page_size, P, block_table, seq_lens, q_offset, q_start, sel, dev)
     rc = load_library().paged_attn_select_pages(
-        _ptr(q), _ptr(k_env), _ptr(k_env_scale), _ptr(block_table), _ptr(seq_lens), _ptr(q_start), int(bool(causal)),
-        _ptr(q_offset), int(sink_pages), int(local_pages), sel.shape[-1], _ptr(sel), ctypes.byref(dims),
-        _stream(stream))
+        q.data_ptr(), k_env.data_ptr(), k_env_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        _ptr(q_start), 1 if causal else 0, _ptr(q_offset), sink_pages, local_pages, sel.shape[-1], sel.data_ptr(),
+        dims, _stream(stream))
     if rc:
         _raise(rc, "paged_attn_select_pages")
 
@@ -621,23 +632,20 @@ def paged_attn_fwd_sparse(q, k_cache, v_cache, block_table, seq_lens, causal, q_
     ``paged_attn_select_pages`` gives them); see ``paged_attn_fwd_sparse`` in include/paged_attn.h.
     q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start [B + 1]; out as q (dense), lse without D or None."""
     torch = _torch()
-    _check(k_cache, "k_cache", q.dtype, 4)
-    _check(v_cache, "v_cache", q.dtype, 4)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache shapes differ")
-    P, ps, Hkv, D = k_cache.shape
-    dims = _sparse_dims(q, Hkv, D, ps, P, block_table, seq_lens, q_offset, q_start, sel, "sel")
-    _check(out, "out", q.dtype)
-    _check(lse, "lse", torch.float32)
-    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:-1]):
-        raise ValueError("out must be shaped as q, and lse as q without its last dim")
-    _check_device((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (block_table, "block_table"),
-                  (seq_lens, "seq_lens"), (q_offset, "q_offset"), (q_start, "q_start"), (sel, "sel"), (out, "out"),
-                  (lse, "lse"))
+    dev, dt = torch.cuda.current_device(), q.dtype
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, page_size, Hkv, D]")
+    P, ps, Hkv, D = pool = k_cache.shape
+    _need(k_cache, "k_cache", dev, dt, pool)
+    _need(v_cache, "v_cache", dev, dt, pool)
+    dims = _sparse_dims(q, Hkv, D, ps, P, block_table, seq_lens, q_offset, q_start, sel, dev)
+    _need(out, "out", dev, dt, q.shape)
+    if lse is not None:
+        _need(lse, "lse", dev, torch.float32, q.shape[:-1])
     rc = load_library().paged_attn_fwd_sparse(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(q_start), int(bool(causal)),
-        _ptr(q_offset), _ptr(sel), sel.shape[-1], float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims),
-        _stream(stream))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        _ptr(q_start), 1 if causal else 0, _ptr(q_offset), sel.data_ptr(), sel.shape[-1], scale, out.data_ptr(),
+        _ptr(lse), dims, _stream(stream))
     if rc:
         _raise(rc, "paged_attn_fwd_sparse")
 

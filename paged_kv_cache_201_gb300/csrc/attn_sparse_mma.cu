@@ -353,7 +353,8 @@ static cudaError_t launch_sparse_mma_t(const SparseParams &sp, int sms, const CU
     auto kern = paged_attn_sparse_mma_kernel<T, D, NSTAGE>;
     const size_t smem = mma_smem_bytes(D, NSTAGE);
     static_assert(Merge<D>::kBytes <= NSTAGE * 2 * Geo<D>::kStageBytes, "the merge must fit in the ring");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise((const void *)kern, smem);
     if (e != cudaSuccess) return e;
     int ps_shift = 0;
     while ((1 << ps_shift) < p.ps) ++ps_shift;

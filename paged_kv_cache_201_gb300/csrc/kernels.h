@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace pa {
@@ -63,6 +65,23 @@ cudaError_t launch_gather(const void *cache, const int32_t *block_table, const i
                           unsigned int *err, cudaStream_t stream);
 
 // ---------------------------------------------------------------- serving step over selected pages
+// Raise a kernel's dynamic shared memory limit to `bytes` once per device: the attribute is a driver
+// call of its own, and these launches take a few microseconds in all.  `done` belongs to the kernel.
+struct SmemLimit {
+    std::atomic<uint64_t> done[2];
+    cudaError_t raise(const void *kern, size_t bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool known = dev >= 0 && dev < 128;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (known && (done[dev >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && known) done[dev >> 6].fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
+
 struct StepTablesParams {
     const int32_t *cached_lens, *new_lens, *free_pages, *free_count;
     int32_t *block_table, *seq_lens, *q_offset, *q_start, *slots, *free_left;

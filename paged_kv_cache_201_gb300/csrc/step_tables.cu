@@ -158,8 +158,9 @@ __global__ void __launch_bounds__(kStepThreads, 1) paged_attn_step_tables_kernel
 
 cudaError_t launch_step_tables(const StepTablesParams &p, cudaStream_t stream) {
     const size_t smem = ((size_t)3 * p.B + 1) * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise((const void *)paged_attn_step_tables_kernel,
+                                      ((size_t)3 * PA_STEP_MAX_BATCH + 1) * sizeof(int32_t));
     if (e != cudaSuccess) return e;
     paged_attn_step_tables_kernel<<<1, kStepThreads, smem, stream>>>(p);
     return cudaGetLastError();
