@@ -766,7 +766,7 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
     sp.K = top_k;
     sp.sink = sink_pages;
     sp.local = local_pages;
-    return cuda_status(pa::launch_select_pages(sp, dims->dtype, static_cast<cudaStream_t>(stream)));
+    return cuda_status(pa::launch_select_pages(sp, dims->dtype, device_sm_count(), static_cast<cudaStream_t>(stream)));
 }
 
 int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,

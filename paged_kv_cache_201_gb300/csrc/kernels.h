@@ -115,7 +115,7 @@ struct SparseParams {
     long long n_tok;
     int K, sink, local;
 };
-cudaError_t launch_select_pages(const SparseParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_select_pages(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
 // bf16/f16: tensor cores, a list's pages split over a cluster when there are few rows (sms: SM count)
 cudaError_t launch_sparse_mma(const SparseParams &p, int dtype, int sms, const CUtensorMap &tmk,
                               const CUtensorMap &tmv, cudaStream_t stream);

@@ -299,6 +299,32 @@ def test_select_ties_and_marks(pa):
     _check_select(pa, b, 0, 1, 9)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_select_largest_scores(pa, D):
+    """Scores of the largest magnitude that differ by one: every product 127 * 127 or 127 * -127, one
+    corner off by one, in both signs."""
+    b = R.Batch(D, [1, 1], [200 * 16, 150 * 16], 16, 2, D, 16, "bf16")
+    rng = np.random.default_rng(D)
+    sign = rng.choice([-1, 1], D)
+    b.q[:] = W.bf16_bits_rne(np.broadcast_to(3.0 * sign, b.q.shape).astype(np.float32))
+    top = np.where(sign > 0, 127, -127).astype(np.int8)
+    env = np.broadcast_to(top, (b.P, b.Hkv, 2, D)).copy()
+    env[b.P // 2:] *= -1
+    for p in range(b.P):
+        d = rng.integers(0, D)
+        env[p, :, :, d] -= np.sign(env[p, :, :, d]) * np.int8(rng.integers(0, 3))
+    _check_select(pa, b, 1, 1, 30, env=(env, np.ones((b.P, b.Hkv), np.float32)))
+
+
+@pytest.mark.parametrize("chunk", [64, 300, 700])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (6, 2), (8, 2), (8, 1), (32, 8), (12, 1)])
+def test_select_prompt_chunks(pa, chunk, Hq, Hkv):
+    """Prompt chunks beside single tokens: tokens that share a block, blocks that hold several sequences."""
+    b = R.Batch(chunk + Hq, [chunk, 1, 0, 5, 1, 37], [chunk + 600, 900, 3, 5, 700, 200], Hq, Hkv, 64, 16, "bf16",
+                q_pad=3)
+    _check_select(pa, b, 1, 2, 8)
+
+
 @pytest.mark.parametrize("B,pages,K,ps", [(2, 4097, 64, 16), (1, 20000, 128, 16), (3, 1025, 100, 64),
                                           (1, 49151, 700, 16), (5, 2047, 2000, 32)])
 def test_select_long(pa, B, pages, K, ps):
