@@ -63,11 +63,17 @@ __device__ __forceinline__ unsigned threshold_key(unsigned lo, unsigned hi, int 
     return thr;
 }
 
-// Element i of q, whose type is a value here: only the quantisation reads it.
-__device__ __forceinline__ float q_elem(const void *q, int dtype, long long i) {
-    if (dtype == PA_F32) return __ldg(static_cast<const float *>(q) + i);
-    const unsigned short u = __ldg(static_cast<const unsigned short *>(q) + i);
-    return dtype == PA_BF16 ? __uint_as_float((unsigned)u << 16) : __half2float(__ushort_as_half(u));
+// Elements i .. i + 3 of q, whose type is a value here: only the quantisation reads it.
+__device__ __forceinline__ void q_load4(const void *q, int dtype, long long i, float (&v)[4]) {
+    if (dtype == PA_F32) {
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(q) + i));
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        return;
+    }
+    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(q) + i));
+    const float2 x = dtype == PA_BF16 ? MmaOp<__nv_bfloat16>::unpack(u.x) : MmaOp<__half>::unpack(u.x);
+    const float2 y = dtype == PA_BF16 ? MmaOp<__nv_bfloat16>::unpack(u.y) : MmaOp<__half>::unpack(u.y);
+    v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
 }
 
 struct SelectPlan {
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(kSelThreads)
     __shared__ float s_sub[COLS];                  // 128 sum_d q of a column, or kNoHead
     __shared__ int s_seq[kSelMaxTokens], s_reach[kSelMaxTokens];
     __shared__ unsigned s_red[kSelWarps][2];
-    __shared__ float s_amax[kSelMaxTokens];
+    __shared__ unsigned s_amax[kSelMaxTokens];  // bits of the largest |q| of each token's group
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, tq = lane & 3;
     const int S = plan.S, rank = blockIdx.x % S;
@@ -196,59 +202,74 @@ __global__ void __launch_bounds__(kSelThreads)
         load_pages(id, raw, scale);
 
         const int passes = plan.Gp > COLS ? (p.G + COLS - 1) / COLS : 1;
+        constexpr int NQ = (D / 4 + 31) / 32;  // 4-element groups of a head a lane takes
         if (scored) {
-            // the largest |q| of each token's group
-            for (int i = i0 + warp; i < i1; i += kSelWarps) {
-                const long long q0 = q_row_offset(p, (t0 + i) * p.Hq + (long long)h * p.G);
-                float a = 0.f;
-                bool odd = false;
-                for (int e = lane; e < p.G * D; e += 32) {
-                    const float x = fabsf(q_elem(p.q, plan.dtype, q0 + e));
-                    odd |= !(x <= FLT_MAX);
-                    a = fmaxf(a, x);
+            if (tid < kSelMaxTokens) s_amax[tid] = 0u;
+            __syncthreads();
+            // heads to the warps, `per_tok` of them to a token
+            const int per_tok = passes > 1 || plan.TT == 1 ? p.G : plan.Gp, cols = per_tok * (i1 - i0);
+#pragma unroll 2
+            for (int w = warp; w < cols; w += kSelWarps) {
+                const int tok = i0 + w / per_tok, hd = w % per_tok;
+                if (hd >= p.G) continue;
+                const long long q0 = q_row_offset(p, (t0 + tok) * p.Hq + (long long)h * p.G + hd);
+                unsigned a = 0;  // magnitudes order as their bits, infinities and NaNs on top
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    const int d = (i * 32 + lane) * 4;
+                    if (D % 128 == 0 || d < D) {
+                        float x[4];
+                        q_load4(p.q, plan.dtype, q0 + d, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+                    }
                 }
-                // non-negative floats order as their bits
-                a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-                if (__any_sync(0xffffffffu, odd)) a = 0.f;  // a non-finite query: scores 0
-                if (lane == 0) s_amax[i] = a;
+                a = __reduce_max_sync(0xffffffffu, a);
+                if (lane == 0) atomicMax(&s_amax[tok], a);
             }
         }
         for (int pass = 0; scored && pass < passes; ++pass) {
             __syncthreads();  // s_amax is there; s_b of the last pass has been read
-            if (tid < COLS) s_sub[tid] = kNoHead;
-            __syncthreads();
             // Query columns in 8 bits: each group of four elements d .. d + 3 is one lane's slot in the
             // fragments of k step ks (lo corners) and ks + KS / 2 (hi corners).
             const int heads = passes > 1 ? min(COLS, p.G - pass * COLS) : p.G;
+#pragma unroll 2
             for (int w = warp; w < COLS; w += kSelWarps) {
                 const int tok = i0 + (passes > 1 || plan.TT == 1 ? 0 : w / plan.Gp);
                 const int hd = passes > 1 || plan.TT == 1 ? w : w % plan.Gp;
                 const bool there = hd < heads && tok < i1;
-                const float a = there ? s_amax[tok] : 0.f;
+                // a non-finite query scores 0 everywhere
+                const unsigned bits = there ? s_amax[tok] : 0u;
+                const float a = bits < 0x7f800000u ? __uint_as_float(bits) : 0.f;
                 const long long q0 =
                     q_row_offset(p, there ? (t0 + tok) * p.Hq + (long long)h * p.G + pass * COLS + hd : 0);
                 int sum = 0;
-                for (int d4 = lane; d4 < D / 4; d4 += 32) {
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    const int m = (i * 32 + lane) * 4;
+                    if (D % 128 != 0 && m >= D) continue;
+                    float x[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (a > 0.f) q_load4(p.q, plan.dtype, q0 + m, x);
                     __half lo[4], hi[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = a > 0.f ? rintf(__fmul_rn(__fdiv_rn(q_elem(p.q, plan.dtype, q0 + d4 * 4 + e), a), 127.f)) : 0.f;
-                        sum += (int)x;
-                        lo[e] = __float2half_rn(fminf(x, 0.f));
-                        hi[e] = __float2half_rn(fmaxf(x, 0.f));
+                        const float y = a > 0.f ? rintf(__fmul_rn(__fdiv_rn(x[e], a), 127.f)) : 0.f;
+                        sum += (int)y;
+                        lo[e] = __float2half_rn(fminf(y, 0.f));
+                        hi[e] = __float2half_rn(fmaxf(y, 0.f));
                     }
                     // byte m = 64 c + 16 tq + 4 w + e of the envelope is element e of lane tq in k step 4 c + w
-                    const int m = d4 * 4, ks = (m >> 6) * 4 + ((m & 15) >> 2), l = (w & 7) * 4 + ((m & 63) >> 4);
+                    const int ks = (m >> 6) * 4 + ((m & 15) >> 2), l = (w & 7) * 4 + ((m & 63) >> 4);
                     auto put = [&](int k, const __half (&v)[4]) {
-                        const __half2 x = __halves2half2(v[0], v[1]), y = __halves2half2(v[2], v[3]);
-                        s_b[(k * NT + (w >> 3)) * 32 + l] = make_uint2(*reinterpret_cast<const uint32_t *>(&x),
-                                                                      *reinterpret_cast<const uint32_t *>(&y));
+                        const __half2 x2 = __halves2half2(v[0], v[1]), y2 = __halves2half2(v[2], v[3]);
+                        s_b[(k * NT + (w >> 3)) * 32 + l] = make_uint2(*reinterpret_cast<const uint32_t *>(&x2),
+                                                                      *reinterpret_cast<const uint32_t *>(&y2));
                     };
                     put(ks, lo);
                     put(ks + KS / 2, hi);
                 }
                 sum = __reduce_add_sync(0xffffffffu, sum);
-                if (lane == 0 && there) s_sub[w] = 128.f * (float)sum;
+                if (lane == 0) s_sub[w] = there ? 128.f * (float)sum : kNoHead;
             }
             __syncthreads();
             for (int tile = tile0 + warp; tile < tile1; tile += kSelWarps) {
