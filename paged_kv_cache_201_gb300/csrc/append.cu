@@ -7,7 +7,7 @@
 // way), older rows from the cache.
 #include <float.h>
 
-#include "kernels.h"
+#include "sparse_common.cuh"
 
 namespace pa {
 
@@ -107,9 +107,11 @@ __global__ void __launch_bounds__(256) paged_attn_append_kernel(const AppendPara
         if (kQuads % 32 != 0 && g >= kQuads) continue;
         char4 cl = make_char4(0, 0, 0, 0), ch = cl;
         if (!odd && a > 0.f) {
-            auto q8 = [a](float x) { return (signed char)(int)rintf(__fmul_rn(__fdiv_rn(x, a), 127.f)); };
-            cl = make_char4(q8(lo[i][0]), q8(lo[i][1]), q8(lo[i][2]), q8(lo[i][3]));
-            ch = make_char4(q8(hi[i][0]), q8(hi[i][1]), q8(hi[i][2]), q8(hi[i][3]));
+            const float inv = 127.f / a;
+            quantise8<4>(lo[i], a, inv);
+            quantise8<4>(hi[i], a, inv);
+            cl = make_char4((int)lo[i][0], (int)lo[i][1], (int)lo[i][2], (int)lo[i][3]);
+            ch = make_char4((int)hi[i][0], (int)hi[i][1], (int)hi[i][2], (int)hi[i][3]);
         }
         env[g] = cl;
         env[kQuads + g] = ch;

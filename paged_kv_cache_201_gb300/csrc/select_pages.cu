@@ -15,8 +15,11 @@
 //
 // One cluster of S CTAs = one kv head and TT consecutive query tokens (1 in a decode batch; up to 32 / G
 // in prompt chunks, whose tokens read the same envelopes).  Its pages are shared out to the CTAs; their
-// scores, as ordered 32-bit keys, meet in the first CTA's shared memory, which finds each token's
-// threshold key by bisection over the key bits and writes the pages above it in order.
+// scores meet in the first CTA's shared memory, which finds each token's threshold by bisection and
+// writes the pages above it in order.  Where there are
+// enough rows to fill the GPU with single warps, a warp takes a row by itself (WPU = 1): its latencies
+// (lengths, table, envelopes, bisection) then overlap with other rows' instead of holding three idle
+// warps at barriers.
 #include <float.h>
 
 #include "sparse_common.cuh"
@@ -27,15 +30,18 @@ namespace {
 
 constexpr int kSelWarps = 4;
 constexpr int kSelThreads = kSelWarps * 32;
+constexpr int kRowWarps = 1;           // of a row, where rows fill the GPU
 constexpr int kSelMaxTokens = 32;      // of one CTA
+constexpr int kWarpSelectPages = 1024;  // longest row a warp of its own selects from
 constexpr float kTwo24 = 16777216.f;
-constexpr float kNoHead = 1e30f;       // subtracted from the column of a head that is not there
+constexpr float kNoHead = -1e30f;      // score of a column without a head
 
-// Order-preserving map of a float to an unsigned key (no NaN comes here).
+// Order-preserving map of a float to an unsigned number, and back (no NaN comes here).
 __device__ __forceinline__ unsigned ordered(float x) {
-    const unsigned u = __float_as_uint(x + 0.f);  // -0 becomes +0
+    const unsigned u = __float_as_uint(x);
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
+__device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -44,111 +50,236 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 
-// The want-th largest of n keys (0 < want < n) as (threshold, pages at the threshold to take): keys
-// above the threshold are taken whole.  count(c): how many keys are >= c, in every thread.  lo / hi: the
-// smallest and largest key.  Ends as soon as exactly `want` keys reach a candidate.
+// Which of a row's scores are taken: those above `cut`, and of those at it the first `ties` pages; or,
+// if `whole`, all that are at least `cut`.
+struct Threshold {
+    float cut;
+    bool whole;
+    __device__ __forceinline__ bool above(float x) const { return whole ? x >= cut : x > cut; }
+    __device__ __forceinline__ bool at(float x) const { return !whole && x == cut; }
+};
+
+// The want-th largest of a row's scores, by bisection from a bracket: at least `want` scores reach lo,
+// fewer exceed hi, and both are scores of the row.  count(c): how many are >= c, in every thread.  The
+// values are bisected first; what is not found in 14 steps is found by bisection of the numbers between
+// (infinite scores).  It ends as soon as exactly `want` scores reach a candidate.
 template <typename Count>
-__device__ __forceinline__ unsigned threshold_key(unsigned lo, unsigned hi, int want, Count count) {
-    // bits above the first one in which lo and hi differ are common to all keys
-    const int top = lo == hi ? -1 : 31 - __clz((int)(lo ^ hi));
-    unsigned thr = top == 31 ? 0u : top < 0 ? lo : (lo >> (top + 1)) << (top + 1);
-    for (int bit = top; bit >= 0; --bit) {
-        const unsigned cand = thr | (1u << bit);
-        const int c = count(cand);
-        if (c >= want) {
-            thr = cand;
-            if (c == want) break;
+__device__ __forceinline__ Threshold find_threshold(float lo, float hi, int want, Count count) {
+    unsigned kl = ordered(lo), kh = ordered(hi) + 1;  // want or more reach kl, fewer reach kh
+    for (int step = 0; kh - kl > 1; ++step) {
+        unsigned k = kl + (kh - kl) / 2;
+        if (step < 14) {
+            const float mid = 0.5f * value_of(kl) + 0.5f * value_of(kh - 1);
+            if (fabsf(mid) <= FLT_MAX) k = min(max(ordered(mid), kl + 1), kh - 1);
         }
+        const float c = value_of(k);
+        const int n = count(c);
+        if (n == want) return {c, true};
+        if (n > want)
+            kl = k;
+        else
+            kh = k;
     }
-    return thr;
+    return {value_of(kl), false};
 }
 
-// Elements i .. i + 3 of q, whose type is a value here: only the quantisation reads it.
-__device__ __forceinline__ void q_load4(const void *q, int dtype, long long i, float (&v)[4]) {
+// Elements i .. i + 15 of q (16-byte aligned), whose type is a value here: only the quantisation reads it.
+__device__ __forceinline__ void q_load16(const void *q, int dtype, long long i, float (&v)[16]) {
     if (dtype == PA_F32) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(q) + i));
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = __ldg(src + k);
+            v[4 * k] = x.x, v[4 * k + 1] = x.y, v[4 * k + 2] = x.z, v[4 * k + 3] = x.w;
+        }
         return;
     }
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(q) + i));
-    const float2 x = dtype == PA_BF16 ? MmaOp<__nv_bfloat16>::unpack(u.x) : MmaOp<__half>::unpack(u.x);
-    const float2 y = dtype == PA_BF16 ? MmaOp<__nv_bfloat16>::unpack(u.y) : MmaOp<__half>::unpack(u.y);
-    v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(q) + i);
+    const uint4 x = __ldg(src), y = __ldg(src + 1);
+    const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 f = dtype == PA_BF16 ? MmaOp<__nv_bfloat16>::unpack(u[k]) : MmaOp<__half>::unpack(u[k]);
+        v[2 * k] = f.x, v[2 * k + 1] = f.y;
+    }
 }
 
 struct SelectPlan {
     int TT;    // query tokens of a CTA
     int Gp;    // columns of a token: G rounded up to a power of two (G <= 8), or all of them
     int S;     // CTAs of a cluster
-    int Wk;    // key stride of a token in shared memory
+    int Wk;    // score stride of a token in shared memory
     int dtype; // of q
 };
 
-// One warp writes a token's pages: `thr` as threshold_key gives it.
-__device__ __forceinline__ void write_selected(const unsigned *keys, int n, int want, unsigned thr, int base,
-                                               int32_t *out, int lane) {
-    int above = 0;
-    for (int j = lane; j < n; j += 32) above += keys[j] > thr;
-    above = __reduce_add_sync(0xffffffffu, above);
-    int ties = want - above, done = 0;  // the first `ties` pages at the threshold are taken
+// Score j of a row of n; past the row a NaN, which no comparison takes.
+__device__ __forceinline__ float score_at(const float *row, int n, int j) {
+    return j < n ? row[j] : __uint_as_float(0x7fffffffu);
+}
+
+__device__ __forceinline__ float warp_min(float x) { return value_of(__reduce_min_sync(0xffffffffu, ordered(x))); }
+__device__ __forceinline__ float warp_max(float x) { return value_of(__reduce_max_sync(0xffffffffu, ordered(x))); }
+
+// A row's scores sorted into equal parts of [lo, hi]; not decreasing in x, so the parts above the one that
+// holds the threshold are taken whole and only that part is searched further.
+struct Bins {
+    float lo, per;
+    int last;
+    __device__ __forceinline__ Bins(float lo_, float hi, int n) : lo(lo_), per((float)n / (hi - lo_)), last(n - 1) {}
+    __device__ __forceinline__ bool usable() const { return per > 0.f && per <= FLT_MAX; }  // a finite, wide range
+    __device__ __forceinline__ int of(float x) const { return min((int)((x - lo) * per), last); }
+};
+
+// The part that holds the want-th largest score, counted from the top by one warp: lane l holds the counts
+// of parts PL l .. PL l + PL - 1.  Returns its index, and how many scores lie in higher parts and in it.
+template <int PL>
+__device__ __forceinline__ int find_bin(const int (&c)[PL], int want, int lane, int &above, int &in) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) mine += c[i];
+    int from = mine;  // scores in this lane's parts and all higher lanes'
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_down_sync(0xffffffffu, from, o);
+        if (lane + o < 32) from += x;
+    }
+    const int owner = 31 - __clz((int)__ballot_sync(0xffffffffu, from >= want));  // the highest such lane
+    int up = from - mine, bin = 0, n = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = PL - 1; i >= 0; --i) {
+        if (!found) {
+            bin = i;
+            n = c[i];
+            if (up + n >= want)
+                found = true;
+            else
+                up += n;
+        }
+    }
+    above = __shfl_sync(0xffffffffu, up, owner);
+    in = __shfl_sync(0xffffffffu, n, owner);
+    return owner * PL + __shfl_sync(0xffffffffu, bin, owner);
+}
+
+constexpr int kBinsPerLane = 4, kBins = 32 * kBinsPerLane;  // of one warp; a CTA's warps have four times as many
+
+// Writes the pages of 32 NK scores k (score i * 32 + lane of a run) that are taken: those above the
+// threshold and, while there are `ties` of them left in the row, those at it.  gt / eq: scores above / at it
+// before the run, moved on.
+template <int NK>
+__device__ __forceinline__ void write_pages(const float (&k)[NK], Threshold thr, int ties, int &gt, int &eq, int base,
+                                            int32_t *out, int lane) {
     const unsigned below = (1u << lane) - 1;
-    for (int j0 = 0; j0 < n && done < want; j0 += 32) {
-        const int j = j0 + lane;
-        const unsigned key = j < n ? keys[j] : 0u;
-        const bool eq = j < n && key == thr;
-        const unsigned eqs = __ballot_sync(0xffffffffu, eq);
-        const bool take = (j < n && key > thr) || (eq && __popc(eqs & below) < ties);
-        const unsigned taken = __ballot_sync(0xffffffffu, take);
-        if (take) out[done + __popc(taken & below)] = base + j;
-        done += __popc(taken);
-        ties -= min(ties, __popc(eqs));
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        const bool up = thr.above(k[i]), at = thr.at(k[i]);
+        const unsigned ups = __ballot_sync(0xffffffffu, up);
+        const unsigned ats = thr.whole ? 0u : __ballot_sync(0xffffffffu, at);
+        const int e = eq + __popc(ats & below);
+        if (up || (at && e < ties)) out[gt + __popc(ups & below) + min(e, ties)] = base + i * 32 + lane;
+        gt += __popc(ups);
+        eq += __popc(ats);
     }
 }
 
-// A token's selection by one warp, its keys in registers (n <= 32 NK).
+// A token's selection by one warp, its scores in registers (n <= 32 NK); hist: kBins counters of the warp.
 template <int NK>
-__device__ __forceinline__ void warp_select(const unsigned *keys, int n, int want, int base, int32_t *out, int lane) {
-    unsigned k[NK], lo = 0xffffffffu, hi = 0;
+__device__ __forceinline__ void warp_select(const float *row, int n, int want, int base, int32_t *out, int *hist,
+                                            int lane) {
+    float k[NK], lo = INFINITY, hi = -INFINITY;
+    *reinterpret_cast<int4 *>(hist + lane * 4) = make_int4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-        const int j = i * 32 + lane;
-        k[i] = j < n ? keys[j] : 0u;  // 0 is below every key
-        if (j < n) lo = min(lo, k[i]);
-        hi = max(hi, k[i]);
+        k[i] = score_at(row, n, i * 32 + lane);
+        lo = fminf(lo, k[i]);  // fminf and fmaxf return the number where one of the two is NaN
+        hi = fmaxf(hi, k[i]);
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    const unsigned thr = threshold_key(lo, hi, want, [&](unsigned c) {
-        int s = 0;
+    lo = warp_min(lo);
+    hi = warp_max(hi);
+    const Bins bins(lo, hi, kBins);
+    bool done = false;
+    Threshold thr{lo, false};
+    if (bins.usable()) {
 #pragma unroll
-        for (int i = 0; i < NK; ++i) s += k[i] >= c;
-        return (int)__reduce_add_sync(0xffffffffu, s);
-    });
-    write_selected(keys, n, want, thr, base, out, lane);
+        for (int i = 0; i < NK; ++i)
+            if (i * 32 + lane < n) atomicAdd(hist + bins.of(k[i]), 1);
+        __syncwarp();
+        const int4 h = *reinterpret_cast<const int4 *>(hist + lane * 4);
+        const int c[4] = {h.x, h.y, h.z, h.w};
+        int above, in;
+        const int bin = find_bin<4>(c, want, lane, above, in);
+        lo = INFINITY;
+        hi = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+            if (i * 32 + lane < n && bins.of(k[i]) == bin) {
+                lo = fminf(lo, k[i]);
+                hi = fmaxf(hi, k[i]);
+            }
+        lo = warp_min(lo);
+        hi = warp_max(hi);
+        done = above + in == want;
+        if (done) thr = {lo, true};
+        __syncwarp();  // before the counters are cleared for another row
+    }
+    if (!done)
+        thr = find_threshold(lo, hi, want, [&](float c) {
+            int s = 0;
+#pragma unroll
+            for (int i = 0; i < NK; ++i) s += k[i] >= c;
+            return (int)__reduce_add_sync(0xffffffffu, s);
+        });
+    int up = 0;
+    if (!thr.whole) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) up += thr.above(k[i]);
+        up = __reduce_add_sync(0xffffffffu, up);
+    }
+    int gt = 0, eq = 0;
+    write_pages<NK>(k, thr, want - up, gt, eq, base, out, lane);
 }
 
 }  // namespace
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kSelThreads)
+template <int D, int NT, int WPU>
+__global__ void __launch_bounds__(kSelThreads, 4)
     paged_attn_select_kernel(const SparseParams sp, const SelectPlan plan) {
     constexpr int KS = 2 * D / 16;  // k steps of a page's envelope
     constexpr int NC = 2 * D / 64;  // 16-byte loads of a lane and page
     constexpr int COLS = 8 * NT;
     const FwdParams &p = sp.f;
+    constexpr int UNITS = kSelWarps / WPU;  // of a CTA
     extern __shared__ __align__(16) uint8_t sm_raw[];
-    uint2 *s_b = reinterpret_cast<uint2 *>(sm_raw);                         // [KS][NT][32] query fragments
-    unsigned *s_key = reinterpret_cast<unsigned *>(s_b + KS * NT * 32);     // [TT][Wk]
-    __shared__ float s_sub[COLS];                  // 128 sum_d q of a column, or kNoHead
-    __shared__ int s_seq[kSelMaxTokens], s_reach[kSelMaxTokens];
-    __shared__ unsigned s_red[kSelWarps][2];
-    __shared__ unsigned s_amax[kSelMaxTokens];  // bits of the largest |q| of each token's group
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ __align__(8) float s_sub_[UNITS][COLS];  // -128 2^-24 sum_d q of a column, or kNoHead
+    __shared__ int s_seq_[UNITS][kSelMaxTokens], s_reach_[UNITS][kSelMaxTokens];
+    __shared__ unsigned s_amax_[UNITS][kSelMaxTokens];  // bits of the largest |q| of each token's group
+    __shared__ int s_red[2][kSelWarps][2];
+    __shared__ __align__(16) int s_hist[kSelWarps][kBins];
+    const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
+    const int warp = wi % WPU, tid = warp * 32 + lane;  // within the unit
+    constexpr int kThreads = WPU * 32;
+    const int me = wi / WPU;
     const int g = lane >> 2, tq = lane & 3;
+    auto sync = [me] {
+        if (WPU == 1)
+            __syncwarp();
+        else if (WPU < kSelWarps)
+            named_bar_sync(1 + me, kThreads);
+        else
+            __syncthreads();
+    };
+    const size_t unit_bytes = (size_t)KS * NT * 32 * sizeof(uint2) + (size_t)plan.TT * plan.Wk * 4;
+    uint2 *s_b = reinterpret_cast<uint2 *>(sm_raw + me * unit_bytes);    // [KS][NT][32] query fragments
+    float *s_key = reinterpret_cast<float *>(s_b + KS * NT * 32);  // [TT][Wk]
+    float *s_sub = s_sub_[me];
+    int *s_seq = s_seq_[me], *s_reach = s_reach_[me];
+    unsigned *s_amax = s_amax_[me];
     const int S = plan.S, rank = blockIdx.x % S;
-    const int unit = blockIdx.x / S;
-    const int h = unit % p.Hkv;
-    const long long t0 = (long long)(unit / p.Hkv) * plan.TT;
+    const long long unit = (long long)(blockIdx.x / S) * UNITS + me;
+    const int h = (int)(unit % p.Hkv);
+    const long long t0 = unit / p.Hkv * plan.TT;
+    if (t0 >= sp.n_tok) return;  // a warp of its own without a row (WPU = 1)
     const int nt_tok = (int)min((long long)plan.TT, sp.n_tok - t0);
     // a peer's shared memory may be written only once it runs
     if (S > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -158,7 +289,7 @@ __global__ void __launch_bounds__(kSelThreads)
         s_reach[tid] = tr.reach;
     }
     if (S > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-    __syncthreads();
+    sync();
 
     for (int i0 = 0, i1 = 0; i0 < nt_tok; i0 = i1) {  // tokens [i0, i1) of one sequence
         const int b = s_seq[i0];
@@ -173,164 +304,180 @@ __global__ void __launch_bounds__(kSelThreads)
         const int tiles = scored ? (m1 - m0 + 15) / 16 : 0, per = (tiles + S - 1) / S;
         const int tile0 = min(rank * per, tiles), tile1 = min(tile0 + per, tiles);
 
-        // A lane's two pages of a tile: id (-1: outside the pool, -2: none), envelope bytes and scale.
-        int id[2];
+        // A lane's two pages of a tile.  A page that is not there (past the row, or an id outside the
+        // pool) reads page 0; its score is dropped or set to 0 below.
+        const uint4 *src[2];  // envelope bytes, from this lane's first 16 on
+        const float *src_scale[2];
+        bool in_pool[2];
+        int id_next[2];
         uint4 raw[2][NC];
-        float scale[2];
-        auto load_ids = [&](int tile, int (&x)[2]) {
+        auto load_ids = [&](int tile) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int j = m0 + tile * 16 + g + r * 8;
-                x[r] = tile < tile1 && j < m1 ? max(__ldg(bt + j), -1) : -2;
+                id_next[r] = tile < tile1 && j < m1 ? __ldg(bt + j) : 0;
             }
         };
-        auto load_pages = [&](const int (&x)[2], uint4 (&v)[2][NC], float (&sc)[2]) {
+        auto point = [&] {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const bool ok = x[r] >= 0 && x[r] < p.num_pages;
-                if (!ok && x[r] != -2) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
-                const long long at = (long long)(ok ? x[r] : 0) * p.Hkv + h;
-                const uint4 *src = reinterpret_cast<const uint4 *>(sp.env + at * 2 * D) + tq;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) v[r][c] = ok ? __ldg(src + c * 4) : make_uint4(0u, 0u, 0u, 0u);
-                sc[r] = ok ? __ldg(sp.env_scale + at) : 0.f;
+                in_pool[r] = id_next[r] >= 0 && id_next[r] < p.num_pages;
+                if (!in_pool[r]) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+                const long long at = (long long)(in_pool[r] ? id_next[r] : 0) * p.Hkv + h;
+                src[r] = reinterpret_cast<const uint4 *>(sp.env + at * 2 * D) + tq;
+                src_scale[r] = sp.env_scale + at;
             }
         };
-        int id_next[2];
-        load_ids(tile0 + warp, id);
-        load_ids(tile0 + warp + kSelWarps, id_next);
-        load_pages(id, raw, scale);
+        float scale[2];
+        if (tile0 + warp < tile1) {
+            load_ids(tile0 + warp);
+            point();
+            load_ids(tile0 + warp + WPU);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                scale[r] = __ldg(src_scale[r]);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) raw[r][c] = __ldg(src[r] + c * 4);
+            }
+        }
 
         const int passes = plan.Gp > COLS ? (p.G + COLS - 1) / COLS : 1;
-        constexpr int NQ = (D / 4 + 31) / 32;  // 4-element groups of a head a lane takes
+        // Queries to 8 bits.  Lane (g, tq) holds column g's elements 64 c + 16 tq .. + 15, which are its
+        // slots in the fragments of k steps 4 c .. 4 c + 3 (lo corners) and KS / 2 further (hi corners).
+        const bool one_token = plan.TT == 1 || passes > 1;
         if (scored) {
-            if (tid < kSelMaxTokens) s_amax[tid] = 0u;
-            __syncthreads();
-            // heads to the warps, `per_tok` of them to a token
-            const int per_tok = passes > 1 || plan.TT == 1 ? p.G : plan.Gp, cols = per_tok * (i1 - i0);
-#pragma unroll 2
-            for (int w = warp; w < cols; w += kSelWarps) {
-                const int tok = i0 + w / per_tok, hd = w % per_tok;
-                if (hd >= p.G) continue;
-                const long long q0 = q_row_offset(p, (t0 + tok) * p.Hq + (long long)h * p.G + hd);
+            for (int i = tid; i < plan.TT; i += kThreads) s_amax[i] = 0u;
+            sync();
+            const int groups = one_token ? (p.G + 7) / 8 : NT;
+            for (int n = warp; n < groups; n += WPU) {
+                const int col = n * 8 + g;
+                const int tok = i0 + (one_token ? 0 : col / plan.Gp), hd = one_token ? col : col % plan.Gp;
                 unsigned a = 0;  // magnitudes order as their bits, infinities and NaNs on top
+                if (hd < p.G && tok < i1) {
+                    const long long q0 = q_row_offset(p, (t0 + tok) * p.Hq + (long long)h * p.G + hd) + tq * 16;
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    const int d = (i * 32 + lane) * 4;
-                    if (D % 128 == 0 || d < D) {
-                        float x[4];
-                        q_load4(p.q, plan.dtype, q0 + d, x);
+                    for (int c = 0; c < D / 64; ++c) {
+                        float x[16];
+                        q_load16(p.q, plan.dtype, q0 + c * 64, x);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+                        for (int e = 0; e < 16; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
                     }
                 }
-                a = __reduce_max_sync(0xffffffffu, a);
-                if (lane == 0) atomicMax(&s_amax[tok], a);
+                a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                if (tq == 0 && a != 0) atomicMax(&s_amax[tok], a);
             }
         }
         for (int pass = 0; scored && pass < passes; ++pass) {
-            __syncthreads();  // s_amax is there; s_b of the last pass has been read
-            // Query columns in 8 bits: each group of four elements d .. d + 3 is one lane's slot in the
-            // fragments of k step ks (lo corners) and ks + KS / 2 (hi corners).
+            sync();  // s_amax is there; s_b of the last pass has been read
             const int heads = passes > 1 ? min(COLS, p.G - pass * COLS) : p.G;
-#pragma unroll 2
-            for (int w = warp; w < COLS; w += kSelWarps) {
-                const int tok = i0 + (passes > 1 || plan.TT == 1 ? 0 : w / plan.Gp);
-                const int hd = passes > 1 || plan.TT == 1 ? w : w % plan.Gp;
+#pragma unroll
+            for (int n = warp; n < NT; n += WPU) {
+                const int col = n * 8 + g;
+                const int tok = i0 + (one_token ? 0 : col / plan.Gp), hd = one_token ? col : col % plan.Gp;
                 const bool there = hd < heads && tok < i1;
                 // a non-finite query scores 0 everywhere
                 const unsigned bits = there ? s_amax[tok] : 0u;
-                const float a = bits < 0x7f800000u ? __uint_as_float(bits) : 0.f;
+                const float a = bits < 0x7f800000u ? __uint_as_float(bits) : 0.f, inv = 127.f / a;
                 const long long q0 =
-                    q_row_offset(p, there ? (t0 + tok) * p.Hq + (long long)h * p.G + pass * COLS + hd : 0);
-                int sum = 0;
+                    q_row_offset(p, there ? (t0 + tok) * p.Hq + (long long)h * p.G + pass * COLS + hd : 0) + tq * 16;
+                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    const int m = (i * 32 + lane) * 4;
-                    if (D % 128 != 0 && m >= D) continue;
-                    float x[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (a > 0.f) q_load4(p.q, plan.dtype, q0 + m, x);
-                    __half lo[4], hi[4];
+                for (int c = 0; c < D / 64; ++c) {
+                    float x[16] = {};
+                    if (a > 0.f) {
+                        q_load16(p.q, plan.dtype, q0 + c * 64, x);
+                        quantise8<16>(x, a, inv);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = a > 0.f ? rintf(__fmul_rn(__fdiv_rn(x[e], a), 127.f)) : 0.f;
-                        sum += (int)y;
-                        lo[e] = __float2half_rn(fminf(y, 0.f));
-                        hi[e] = __float2half_rn(fmaxf(y, 0.f));
+                        for (int e = 0; e < 16; ++e) sum += x[e];
                     }
-                    // byte m = 64 c + 16 tq + 4 w + e of the envelope is element e of lane tq in k step 4 c + w
-                    const int ks = (m >> 6) * 4 + ((m & 15) >> 2), l = (w & 7) * 4 + ((m & 63) >> 4);
-                    auto put = [&](int k, const __half (&v)[4]) {
-                        const __half2 x2 = __halves2half2(v[0], v[1]), y2 = __halves2half2(v[2], v[3]);
-                        s_b[(k * NT + (w >> 3)) * 32 + l] = make_uint2(*reinterpret_cast<const uint32_t *>(&x2),
-                                                                      *reinterpret_cast<const uint32_t *>(&y2));
-                    };
-                    put(ks, lo);
-                    put(ks + KS / 2, hi);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const __half2 zero = __float2half2_rn(0.f);
+                        const __half2 u = __floats2half2_rn(x[4 * w], x[4 * w + 1]);
+                        const __half2 v = __floats2half2_rn(x[4 * w + 2], x[4 * w + 3]);
+                        auto put = [&](int k, const __half2 &y, const __half2 &z) {
+                            s_b[(k * NT + n) * 32 + lane] = make_uint2(*reinterpret_cast<const uint32_t *>(&y),
+                                                                      *reinterpret_cast<const uint32_t *>(&z));
+                        };
+                        put(c * 4 + w, __hmin2(u, zero), __hmin2(v, zero));
+                        put(c * 4 + w + KS / 2, __hmax2(u, zero), __hmax2(v, zero));
+                    }
                 }
-                sum = __reduce_add_sync(0xffffffffu, sum);
-                if (lane == 0) s_sub[w] = there ? 128.f * (float)sum : kNoHead;
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);  // whole numbers: exact
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (tq == 0) s_sub[col] = there ? -128.f / kTwo24 * sum : kNoHead;
             }
-            __syncthreads();
-            for (int tile = tile0 + warp; tile < tile1; tile += kSelWarps) {
-                // the next tile's pages are on their way while this one is scored
-                uint4 cur[2][NC];
-                float cur_scale[2];
+            sync();
+            for (int tile = tile0 + warp; tile < tile1; tile += WPU) {
                 const int j0 = m0 + tile * 16 + g;
+                float cur_scale[2];
+                bool marked[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    cur_scale[r] = scale[r];
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) cur[r][c] = raw[r][c];
+                    cur_scale[r] = in_pool[r] ? scale[r] : 0.f;
+                    marked[r] = cur_scale[r] == INFINITY;
                 }
-                const bool last = tile + kSelWarps >= tile1;
-                if (!last || pass + 1 < passes) {
-                    if (last) {  // the next pass begins again
-                        load_ids(tile0 + warp, id);
-                        load_ids(tile0 + warp + kSelWarps, id_next);
-                    } else {
-                        id[0] = id_next[0], id[1] = id_next[1];
-                        load_ids(tile + 2 * kSelWarps, id_next);
-                    }
-                    load_pages(id, raw, scale);
-                }
-                float acc[NT][4];
+                // Each 16 bytes make room for the next tile's once they are converted, so those are on
+                // their way while this tile is scored.  After the last tile the first is read again,
+                // for the next pass.
+                const bool last = tile + WPU >= tile1, more = !last || pass + 1 < passes;
+                if (last && more) load_ids(tile0 + warp);
+                if (more) {
+                    point();
+                    load_ids((last ? tile0 + warp : tile + WPU) + WPU);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                    for (int r = 0; r < 2; ++r) scale[r] = __ldg(src_scale[r]);
+                }
+                // with one column tile, two sets of sums halve the chain of dependent products
+                constexpr int SETS = NT == 1 ? 2 : 1;
+                float acc[NT][4], odd[4] = {};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float2 init = *reinterpret_cast<const float2 *>(s_sub + n * 8 + 2 * tq);
+                    acc[n][0] = acc[n][2] = init.x;
+                    acc[n][1] = acc[n][3] = init.y;
+                }
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const uint32_t wa[4] = {cur[0][c].x, cur[0][c].y, cur[0][c].z, cur[0][c].w};
-                    const uint32_t wb[4] = {cur[1][c].x, cur[1][c].y, cur[1][c].z, cur[1][c].w};
+                    const uint32_t wa[4] = {raw[0][c].x, raw[0][c].y, raw[0][c].z, raw[0][c].w};
+                    const uint32_t wb[4] = {raw[1][c].x, raw[1][c].y, raw[1][c].z, raw[1][c].w};
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const uint32_t xa = wa[w] ^ 0x80808080u, xb = wb[w] ^ 0x80808080u;
                         const uint32_t a[4] = {__byte_perm(xa, 0, 0x4140), __byte_perm(xb, 0, 0x4140),
                                                __byte_perm(xa, 0, 0x4342), __byte_perm(xb, 0, 0x4342)};
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(acc[n], a, s_b[((c * 4 + w) * NT + n) * 32 + lane]);
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(SETS == 2 && (w & 1) ? odd : acc[n], a, s_b[((c * 4 + w) * NT + n) * 32 + lane]);
+                    }
+                    if (more) {
+                        raw[0][c] = __ldg(src[0] + c * 4);
+                        raw[1][c] = __ldg(src[1] + c * 4);
                     }
                 }
-                // whole scores of (page g / g + 8, columns 2 tq, 2 tq + 1), largest over a token's heads
-                auto key_of = [&](float s, int r) {
-                    return ordered(cur_scale[r] == INFINITY ? INFINITY : __fmul_rn(s, cur_scale[r]));
+                if (SETS == 2)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[0][e] += odd[e];  // whole numbers: exact
+                // scores of (page g / g + 8, columns 2 tq, 2 tq + 1) in units of 2^24, largest over a
+                // token's heads
+                auto score_of = [&](float s, int r) {
+                    return marked[r] ? INFINITY : __fmul_rn(s * kTwo24, cur_scale[r]);
                 };
-                if (plan.TT == 1 || passes > 1) {
-                    float best[2] = {-2e30f, -2e30f};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            best[e >> 1] = fmaxf(best[e >> 1], acc[n][e] * kTwo24 - s_sub[n * 8 + 2 * tq + (e & 1)]);
+                if (one_token) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
-                        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+                        float best = fmaxf(acc[0][2 * r], acc[0][2 * r + 1]);
+#pragma unroll
+                        for (int n = 1; n < NT; ++n) best = fmaxf(best, fmaxf(acc[n][2 * r], acc[n][2 * r + 1]));
+                        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+                        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
                         const int j = j0 + r * 8;
                         if (tq == 0 && j < m1) {
-                            // the scale is not negative: the largest key is the key of the largest score
-                            unsigned key = key_of(best[r], r);
-                            if (pass > 0) key = max(key, s_key[j - m0]);
-                            s_key[j - m0] = key;
+                            // the scale is not negative: the largest score is that of the largest sum
+                            float x = score_of(best, r);
+                            if (pass > 0) x = fmaxf(x, s_key[j - m0]);
+                            s_key[j - m0] = x;
                         }
                     }
                 } else {
@@ -338,14 +485,14 @@ __global__ void __launch_bounds__(kSelThreads)
                     for (int n = 0; n < NT; ++n) {
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            float x = acc[n][2 * r] * kTwo24 - s_sub[n * 8 + 2 * tq];
-                            float y = acc[n][2 * r + 1] * kTwo24 - s_sub[n * 8 + 2 * tq + 1];
+                            float x = acc[n][2 * r];
+                            const float y = acc[n][2 * r + 1];
                             const int j = j0 + r * 8;
                             if (plan.Gp == 1) {
                                 const int tok = n * 8 + 2 * tq;
                                 if (j < m1) {
-                                    if (i0 + tok < i1) s_key[tok * plan.Wk + j - m0] = key_of(x, r);
-                                    if (i0 + tok + 1 < i1) s_key[(tok + 1) * plan.Wk + j - m0] = key_of(y, r);
+                                    if (i0 + tok < i1) s_key[tok * plan.Wk + j - m0] = score_of(x, r);
+                                    if (i0 + tok + 1 < i1) s_key[(tok + 1) * plan.Wk + j - m0] = score_of(y, r);
                                 }
                                 continue;
                             }
@@ -353,7 +500,7 @@ __global__ void __launch_bounds__(kSelThreads)
                             if (plan.Gp >= 4) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                             if (plan.Gp >= 8) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                             const int col = n * 8 + 2 * tq, tok = col / plan.Gp;
-                            if (col % plan.Gp == 0 && i0 + tok < i1 && j < m1) s_key[tok * plan.Wk + j - m0] = key_of(x, r);
+                            if (col % plan.Gp == 0 && i0 + tok < i1 && j < m1) s_key[tok * plan.Wk + j - m0] = score_of(x, r);
                         }
                     }
                 }
@@ -361,26 +508,26 @@ __global__ void __launch_bounds__(kSelThreads)
         }
 
         if (S > 1) {
-            // this CTA's keys into the first one's shared memory
+            // this CTA's scores into the first one's shared memory
             if (scored && rank != 0) {
-                __syncthreads();
+                sync();
                 const int a = tile0 * 16, e = min(tile1 * 16, m1 - m0);
                 for (int i = 0; i < i1 - i0; ++i)
-                    for (int j = a + tid; j < e; j += kSelThreads) {
+                    for (int j = a + tid; j < e; j += kThreads) {
                         uint32_t dst;
                         asm("mapa.shared::cluster.u32 %0, %1, %2;"
                             : "=r"(dst)
                             : "r"(smem_u32(s_key + i * plan.Wk + j)), "r"(0));
-                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(s_key[i * plan.Wk + j]) : "memory");
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(__float_as_uint(s_key[i * plan.Wk + j])) : "memory");
                     }
             }
             asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
         } else {
-            __syncthreads();
+            sync();
         }
         if (rank == 0) {
             // token i's scored pages are the first n_i: np_i - local - sink
-            for (int i = i0 + warp; i < i1; i += kSelWarps) {
+            for (int i = i0 + warp; i < i1; i += WPU) {
                 const int np = (s_reach[i] + p.ps - 1) / p.ps;
                 int32_t *out = sp.sel_out + ((t0 + i) * p.Hkv + h) * sp.K;
                 if (np <= sp.K) {
@@ -390,73 +537,134 @@ __global__ void __launch_bounds__(kSelThreads)
                 for (int j = lane; j < sp.sink; j += 32) out[j] = j;
                 for (int j = lane; j < sp.local; j += 32) out[sp.K - sp.local + j] = np - sp.local + j;
                 const int n = np - sp.local - sp.sink;
-                const unsigned *keys = s_key + (i - i0) * plan.Wk;
-                if (want == 0 || n > 1024) continue;
+                const float *row = s_key + (i - i0) * plan.Wk;
+                if (want == 0 || n > kWarpSelectPages) continue;
                 if (n <= 256)
-                    warp_select<8>(keys, n, want, sp.sink, out + sp.sink, lane);
+                    warp_select<8>(row, n, want, sp.sink, out + sp.sink, s_hist[wi], lane);
                 else if (n <= 512)
-                    warp_select<16>(keys, n, want, sp.sink, out + sp.sink, lane);
+                    warp_select<16>(row, n, want, sp.sink, out + sp.sink, s_hist[wi], lane);
                 else
-                    warp_select<32>(keys, n, want, sp.sink, out + sp.sink, lane);
+                    warp_select<kWarpSelectPages / 32>(row, n, want, sp.sink, out + sp.sink, s_hist[wi], lane);
             }
-            // longer rows: the whole CTA counts, one warp writes
-            for (int i = i0; i < i1 && want > 0; ++i) {
+            // longer rows: the CTA counts and writes them together
+            for (int i = i0; WPU == kSelWarps && i < i1 && want > 0; ++i) {
                 const int np = (s_reach[i] + p.ps - 1) / p.ps, n = np - sp.local - sp.sink;
-                if (np <= sp.K || n <= 1024) continue;
-                const unsigned *keys = s_key + (i - i0) * plan.Wk;
-                unsigned lo = 0xffffffffu, hi = 0;
-                for (int j = tid; j < n; j += kSelThreads) {
-                    lo = min(lo, keys[j]);
-                    hi = max(hi, keys[j]);
-                }
-                lo = __reduce_min_sync(0xffffffffu, lo);
-                hi = __reduce_max_sync(0xffffffffu, hi);
-                if (lane == 0) s_red[warp][0] = lo, s_red[warp][1] = hi;
-                __syncthreads();
+                if (np <= sp.K || n <= kWarpSelectPages) continue;
+                const float *row = s_key + (i - i0) * plan.Wk;
+                int *hist = s_hist[0];  // all the warps' counters as one
+                constexpr int BINS = kBins * kSelWarps;
+                for (int j = tid; j < BINS; j += kThreads) hist[j] = 0;
+                int turn = 0;  // two sets of partial results: one barrier an exchange
+                auto exchange = [&](int x, int y) {
+                    if (lane == 0) s_red[turn][warp][0] = x, s_red[turn][warp][1] = y;
+                    sync();
+                    turn ^= 1;
+                };
+                auto range = [&](float &lo, float &hi) {
+                    exchange(__float_as_int(warp_min(lo)), __float_as_int(warp_max(hi)));
 #pragma unroll
-                for (int w = 0; w < kSelWarps; ++w) {
-                    lo = min(lo, s_red[w][0]);
-                    hi = max(hi, s_red[w][1]);
-                }
-                __syncthreads();
-                const unsigned thr = threshold_key(lo, hi, want, [&](unsigned c) {
-                    int s = 0;
-                    for (int j = tid; j < n; j += kSelThreads) s += keys[j] >= c;
-                    s = __reduce_add_sync(0xffffffffu, s);
-                    if (lane == 0) s_red[warp][0] = s;
-                    __syncthreads();
+                    for (int w = 0; w < WPU; ++w) {
+                        lo = fminf(lo, __int_as_float(s_red[turn ^ 1][w][0]));
+                        hi = fmaxf(hi, __int_as_float(s_red[turn ^ 1][w][1]));
+                    }
+                };
+                auto total = [&](int s) {
+                    exchange(__reduce_add_sync(0xffffffffu, s), 0);
                     s = 0;
 #pragma unroll
-                    for (int w = 0; w < kSelWarps; ++w) s += s_red[w][0];
-                    __syncthreads();
+                    for (int w = 0; w < WPU; ++w) s += s_red[turn ^ 1][w][0];
                     return s;
-                });
-                int32_t *out = sp.sel_out + ((t0 + i) * p.Hkv + h) * sp.K;
-                if (warp == 0) write_selected(keys, n, want, thr, sp.sink, out + sp.sink, lane);
+                };
+                float lo = INFINITY, hi = -INFINITY;
+#pragma unroll 4
+                for (int j = tid; j < n; j += kThreads) {
+                    lo = fminf(lo, row[j]);
+                    hi = fmaxf(hi, row[j]);
+                }
+                range(lo, hi);
+                const Bins bins(lo, hi, BINS);
+                bool done = false;
+                Threshold thr{lo, false};
+                if (bins.usable()) {
+#pragma unroll 4
+                    for (int j = tid; j < n; j += kThreads) atomicAdd(hist + bins.of(row[j]), 1);
+                    sync();
+                    int c[BINS / 32], above, in;
+#pragma unroll
+                    for (int k = 0; k < BINS / 32; k += 4) {
+                        const int4 x = *reinterpret_cast<const int4 *>(hist + lane * (BINS / 32) + k);
+                        c[k] = x.x, c[k + 1] = x.y, c[k + 2] = x.z, c[k + 3] = x.w;
+                    }
+                    const int bin = find_bin<BINS / 32>(c, want, lane, above, in);
+                    lo = INFINITY;
+                    hi = -INFINITY;
+#pragma unroll 4
+                    for (int j = tid; j < n; j += kThreads)
+                        if (bins.of(row[j]) == bin) {
+                            lo = fminf(lo, row[j]);
+                            hi = fmaxf(hi, row[j]);
+                        }
+                    range(lo, hi);
+                    done = above + in == want;
+                    if (done) thr = {lo, true};
+                }
+                if (!done)
+                    thr = find_threshold(lo, hi, want, [&](float c) {
+                        int s = 0;
+#pragma unroll 4
+                        for (int j = tid; j < n; j += kThreads) s += row[j] >= c;
+                        return total(s);
+                    });
+                // each warp a run of scores, after counting the runs before it
+                const int run = (n + WPU * 128 - 1) / (WPU * 128) * 128, a = min(warp * run, n), e = min(a + run, n);
+                int gt = 0, eq = 0;
+#pragma unroll 4
+                for (int j = a + lane; j < e; j += 32) {
+                    gt += thr.above(row[j]);
+                    eq += thr.at(row[j]);
+                }
+                exchange(__reduce_add_sync(0xffffffffu, gt), __reduce_add_sync(0xffffffffu, eq));
+                int all = 0;
+                gt = eq = 0;
+#pragma unroll
+                for (int w = 0; w < WPU; ++w) {
+                    if (w < warp) gt += s_red[turn ^ 1][w][0], eq += s_red[turn ^ 1][w][1];
+                    all += s_red[turn ^ 1][w][0];
+                }
+                int32_t *out = sp.sel_out + ((t0 + i) * p.Hkv + h) * sp.K + sp.sink;
+                for (int j = a; j < e; j += 128) {
+                    float k[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) k[x] = score_at(row, e, j + x * 32 + lane);
+                    write_pages<4>(k, thr, want - all, gt, eq, sp.sink + j, out, lane);
+                }
+                sync();  // the counters are used again by the next row
             }
         }
-        if (i1 < nt_tok) {  // the next sequence's keys go to the same place
+        if (i1 < nt_tok) {  // the next sequence's scores go to the same place
             if (S > 1)
                 asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
             else
-                __syncthreads();
+                sync();
         }
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, int WPU>
 static cudaError_t launch_select_t(const SparseParams &sp, const SelectPlan &plan, cudaStream_t stream) {
-    auto kern = paged_attn_select_kernel<D, NT>;
+    auto kern = paged_attn_select_kernel<D, NT, WPU>;
     const size_t frag = (size_t)(2 * D / 16) * NT * 32 * sizeof(uint2);
     static SmemLimit limit;
-    const cudaError_t e = limit.raise((const void *)kern, frag + (size_t)PA_SELECT_MAX_PAGES * 4);
+    const size_t most = WPU < kSelWarps ? kSelWarps / WPU * (frag + kWarpSelectPages * 4) : frag + (size_t)PA_SELECT_MAX_PAGES * 4;
+    const cudaError_t e = limit.raise((const void *)kern, most);
     if (e != cudaSuccess) return e;
-    const long long units = (sp.n_tok + plan.TT - 1) / plan.TT * sp.f.Hkv;
+    const long long rows = (sp.n_tok + plan.TT - 1) / plan.TT * sp.f.Hkv;
+    const long long units = (rows + kSelWarps / WPU - 1) / (kSelWarps / WPU);  // clusters
     if (units * plan.S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * plan.S));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = frag + (size_t)plan.TT * plan.Wk * 4;
+    cfg.dynamicSmemBytes = kSelWarps / WPU * (frag + (size_t)plan.TT * plan.Wk * 4);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -481,7 +689,7 @@ static cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, c
     } else {
         plan.Gp = 1;
         while (plan.Gp < p.G) plan.Gp *= 2;
-        // Prompt chunks: as many tokens a CTA as fill 32, 16 or 8 columns while their keys take at most
+        // Prompt chunks: as many tokens a CTA as fill 32, 16 or 8 columns while their scores take at most
         // 64 KB and there is a CTA for every multiprocessor; a batch of mostly single tokens takes one.
         NT = 4;
         plan.TT = 32 / plan.Gp;
@@ -497,13 +705,16 @@ static cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, c
             plan.TT = 1;
         }
     }
-    // Few rows: a cluster shares their pages, each CTA at least two tiles for each of its warps.
-    const long long units = (sp.n_tok + plan.TT - 1) / plan.TT * p.Hkv;
+    const long long rows = (sp.n_tok + plan.TT - 1) / plan.TT * p.Hkv;
     plan.S = 1;
-    while (plan.S < 8 && units * plan.S * 2 <= 2ll * sms && p.W >= plan.S * 2 * 2 * kSelWarps * 16) plan.S *= 2;
-    if (NT == 1) return launch_select_t<D, 1>(sp, plan, stream);
-    if (NT == 2) return launch_select_t<D, 2>(sp, plan, stream);
-    return launch_select_t<D, 4>(sp, plan, stream);
+    // A warp to a row once that gives every multiprocessor eight warps.
+    if (plan.TT == 1 && NT <= 2 && p.W <= kWarpSelectPages && rows >= 8ll * sms)
+        return NT == 1 ? launch_select_t<D, 1, kRowWarps>(sp, plan, stream) : launch_select_t<D, 2, kRowWarps>(sp, plan, stream);
+    // Few rows: a cluster shares their pages, each CTA at least two tiles for each of its warps.
+    while (plan.S < 8 && rows * plan.S * 2 <= 2ll * sms && p.W >= plan.S * 2 * 2 * kSelWarps * 16) plan.S *= 2;
+    if (NT == 1) return launch_select_t<D, 1, kSelWarps>(sp, plan, stream);
+    if (NT == 2) return launch_select_t<D, 2, kSelWarps>(sp, plan, stream);
+    return launch_select_t<D, 4, kSelWarps>(sp, plan, stream);
 }
 
 cudaError_t launch_select_pages(const SparseParams &sp, int dtype, int sms, cudaStream_t stream) {

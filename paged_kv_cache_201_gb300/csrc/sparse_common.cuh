@@ -6,6 +6,28 @@
 
 namespace pa {
 
+// x[i] = rint((x[i] / a) * 127) for |x[i]| <= a, 0 < a < inf, in float32 steps rounded to nearest even;
+// inv = 127 / a.  x inv and the two-step value are each within 127 * 2^-23 < 2e-5 of the exact quotient,
+// so they round to the same integer unless x inv lies within 1e-3 of a border: only then (one value in
+// 500; and where inv overflows) are the divisions carried out.
+template <int N>
+__device__ __forceinline__ void quantise8(float (&x)[N], float a, float inv) {
+    float r[N];
+    bool clear = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float y = x[i] * inv;
+        r[i] = rintf(y);
+        clear = clear && fabsf(y - r[i]) <= 0.499f;
+    }
+    if (!clear) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = rintf(__fmul_rn(__fdiv_rn(x[i], a), 127.f));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = r[i];
+}
+
 struct TokenRow {
     int b;      // sequence; -1: the row belongs to none (padding, or a malformed q_start)
     int reach;  // keys the token may see
@@ -15,25 +37,41 @@ struct TokenRow {
 // batch has one token a sequence, so b = t is tried before the binary search.  One thread's view:
 // every caller of a block gets the same answer.
 __device__ __forceinline__ TokenRow token_row(const FwdParams &p, long long t, long long n_tok, bool report) {
-    int b, n, i;
+    int b, n, i, L;
     if (!p.q_start) {
         b = (int)(t / p.Sq);
         n = p.Sq;
         i = (int)(t - (long long)b * p.Sq);
+        L = __ldg(p.seq_lens + b);
     } else {
         int lo = 0, hi = p.B;  // q_start[lo] <= t < q_start[hi] for a well-formed batch
-        if (t < p.B && __ldg(p.q_start + t) <= t) {
-            lo = (int)t;
-            if (__ldg(p.q_start + t + 1) > t) hi = lo + 1;
+        int q0 = 0, q1 = 0;
+        L = 0;
+        if (t < p.B) {  // one trip to memory for a decode batch
+            q0 = __ldg(p.q_start + t);
+            q1 = __ldg(p.q_start + t + 1);
+            L = __ldg(p.seq_lens + t);
+            if (q0 <= t) {
+                lo = (int)t;
+                if (q1 > t) hi = lo + 1;
+            }
         }
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldg(p.q_start + mid) <= t)
-                lo = mid;
-            else
-                hi = mid;
+        if (hi - lo > 1) {
+            do {
+                const int mid = (lo + hi) >> 1;
+                if (__ldg(p.q_start + mid) <= t)
+                    lo = mid;
+                else
+                    hi = mid;
+            } while (hi - lo > 1);
+            q0 = __ldg(p.q_start + lo);
+            q1 = __ldg(p.q_start + lo + 1);
+            L = __ldg(p.seq_lens + lo);
+        } else if (lo != t) {
+            q0 = __ldg(p.q_start);  // one sequence, and t past it
+            q1 = __ldg(p.q_start + 1);
+            L = __ldg(p.seq_lens);
         }
-        const int q0 = __ldg(p.q_start + lo), q1 = __ldg(p.q_start + lo + 1);
         if (q0 < 0 || q1 < q0 || q1 > n_tok) {
             if (report) atomicOr(p.err, (unsigned int)PA_ERRBIT_QSTART);
             return {-1, 0};
@@ -43,7 +81,7 @@ __device__ __forceinline__ TokenRow token_row(const FwdParams &p, long long t, l
         n = q1 - q0;
         i = (int)(t - q0);
     }
-    int L = max(__ldg(p.seq_lens + b), 0);
+    L = max(L, 0);
     if (L > p.W * p.ps) {  // never read past the sequence's block-table row
         if (report) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
         L = p.W * p.ps;
