@@ -182,6 +182,16 @@ def test_append(pa, dtype, Hkv, D, ps, q_lens, seq_lens):
     _check_append(pa, b, slots, kn, vn, strided=len(q_lens) > 1)
 
 
+@pytest.mark.parametrize("dtype,D,ps", [("bf16", 64, 16), ("f16", 128, 64), ("f32", 64, 32), ("bf16", 256, 16)])
+def test_append_many_tokens(pa, dtype, D, ps):
+    """Enough tokens for several to a warp; the last warp holds fewer."""
+    b, slots, kn, vn = _append_case(D + ps, [1900, 1, 0, 3, 149], [1913, 77, 5, 3, 160], 8, D, ps, dtype, pads=1)
+    assert len(slots) * 8 >= 16384 and len(slots) % 4
+    slots[700:703] = -1  # a hole: its page ends before it and goes on behind it
+    slots[703:720] = -1
+    _check_append(pa, b, slots, kn, vn, strided=True)
+
+
 def test_append_without_envelopes_any_order(pa):
     """Without envelopes the tokens may come in any order."""
     b, slots, kn, vn = _append_case(4, [9, 40], [50, 40], 2, 128, 16, "bf16")
