@@ -1,11 +1,16 @@
 // New tokens' K and V rows into their slots, and the envelopes of the pages they land in.
 //
-// One warp per kv head and TPW consecutive tokens copies their rows.  The warp that holds the last new
-// token of a page also takes the page's smallest and largest key elements over rows 0 .. r: minima and
-// maxima are exact whatever their order, so an envelope is the same bits whether a page is filled at
-// once or token by token.  Rows of this call's run come from k_new (their stores by other warps may still
-// be under way), older rows from the cache; for a prompt they are in L2, just read by the neighbours.
-// A decode step is a chain of three trips to memory (slots, rows, stores).
+// One launch of two kinds of CTAs.  The copying ones move rows, a warp for one kv head of TPW tokens.  The
+// others, placed first in the grid, take the envelopes: a warp finds the tokens that close a page (none of
+// the next 64 tokens lies in it) and takes the smallest and largest key elements of the page's rows
+// 0 .. r, from k_new where this call writes them (told by the slots of the 63 tokens before) and from the
+// cache where an earlier one did; it waits for no copy.  Minima and maxima are exact whatever their
+// order, so an envelope is the same bits whether a page is filled at once or token by token.
+// Kept apart, the long chain of an envelope (slots, rows, reduction, division) overlaps the copies; where
+// few pages close, as in a prompt, the CTA's warps share a page's rows.  6656 prompt tokens of 8 heads of
+// 128 (f16, 64-token pages) take 14.2 us, 57 % of the copy rate; with the closing warps among the copying
+// ones they took 21, and the copies alone take 10.7.  A decode step of 256 tokens takes 5.3 us, a chain
+// of three trips to memory.
 #include <float.h>
 
 #include "sparse_common.cuh"
@@ -30,129 +35,277 @@ __device__ __forceinline__ void unpack16(uint4 u, float (&v)[16 / sizeof(T)]) {
     }
 }
 
-// The envelope of the page that token t (slot `slot`) closes, by one warp; run: tokens t - run + 1 .. t
-// lie in the page's rows up to slot's.
+constexpr int kOld = 255;  // a row that an earlier call wrote
+
+// How a warp reads rows of one kv head, 16 bytes a lane.
 template <typename T, int D>
-__device__ __forceinline__ void page_envelope(const AppendParams &p, int t, int h, int slot, int run, int lane) {
-    constexpr int E = 16 / (int)sizeof(T);       // elements of a chunk
-    constexpr int CH = D / E;                    // chunks of a row
-    constexpr int LPR = CH < 32 ? CH : 32;       // lanes of a row
-    constexpr int CPL = CH / LPR;                // chunks of a lane
-    constexpr int RPI = 32 / LPR;                // rows a warp reads at once
-    constexpr int U = 8 / CPL;                   // such reads on their way together
-    const int ps = 1 << p.ps_shift, row = slot & (ps - 1);
-    const int c0 = lane % LPR, r0 = lane / LPR;
+struct Rows {
+    static constexpr int E = 16 / (int)sizeof(T);  // elements of a chunk
+    static constexpr int CH = D / E;               // chunks of a row
+    static constexpr int LPR = CH < 32 ? CH : 32;  // lanes of a row
+    static constexpr int CPL = CH / LPR;           // chunks of a lane
+    static constexpr int RPI = 32 / LPR;           // rows a warp reads at once
+    static constexpr int U = 8 / CPL;              // such reads on their way together
+};
+
+// A page that gets its last new token of the call: rows 0 .. row; row r is token t - from[r]'s, or the
+// cache's where from[r] is kOld.
+struct Closing {
+    int t, page, row;  // row < 0: none
+    uint8_t from[64];
+};
+
+// The smallest and largest elements of rows [r1, r2) of a closing page, by one warp: lane l of each group
+// of LPR lanes ends up with chunks l, l + LPR of both.  Returns whether an element is not finite.
+template <typename T, int D>
+__device__ __forceinline__ bool row_bounds(const AppendParams &p, const Closing &cl, int h, int r1, int r2,
+                                           float (&lo)[Rows<T, D>::CPL][Rows<T, D>::E],
+                                           float (&hi)[Rows<T, D>::CPL][Rows<T, D>::E], int lane) {
+    using R = Rows<T, D>;
+    const int c0 = lane % R::LPR, r0 = lane / R::LPR;
     const long long row_elems = (long long)p.Hkv * D;
-    const T *fresh = static_cast<const T *>(p.k_new) + h * D + t * p.k_stride;
-    const T *page = static_cast<const T *>(p.k_cache) + (slot - row) * row_elems + h * D;
-    float lo[CPL][E], hi[CPL][E];
+    const T *fresh = static_cast<const T *>(p.k_new) + h * D + cl.t * p.k_stride;
+    const T *page = static_cast<const T *>(p.k_cache) + ((long long)cl.page << p.ps_shift) * row_elems + h * D;
 #pragma unroll
-    for (int i = 0; i < CPL; ++i)
+    for (int i = 0; i < R::CPL; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) lo[i][e] = INFINITY, hi[i][e] = -INFINITY;
-    bool odd = false;  // an infinity or a NaN among the keys
-    for (int r1 = 0; r1 <= row; r1 += RPI * U) {
-        uint4 u[U][CPL];
+        for (int e = 0; e < R::E; ++e) lo[i][e] = INFINITY, hi[i][e] = -INFINITY;
+    bool odd = false;
+    for (int r3 = r1; r3 < r2; r3 += R::RPI * R::U) {
+        uint4 u[R::U][R::CPL];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int r = min(r1 + k * RPI + r0, row);  // past the last row, that row again
-            const T *src = row - r < run ? fresh - (row - r) * p.k_stride : page + r * row_elems;
+        for (int k = 0; k < R::U; ++k) {
+            const int r = min(r3 + k * R::RPI + r0, r2 - 1);  // past the last row, that row again
+            const int back = cl.from[r];
+            const T *src = back != kOld ? fresh - back * p.k_stride : page + r * row_elems;
 #pragma unroll
-            for (int i = 0; i < CPL; ++i) u[k][i] = reinterpret_cast<const uint4 *>(src)[c0 + i * LPR];
+            for (int i = 0; i < R::CPL; ++i) u[k][i] = reinterpret_cast<const uint4 *>(src)[c0 + i * R::LPR];
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+        for (int k = 0; k < R::U; ++k)
 #pragma unroll
-            for (int i = 0; i < CPL; ++i) {
-                float x[E];
+            for (int i = 0; i < R::CPL; ++i) {
+                float x[R::E];
                 unpack16<T>(u[k][i], x);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
+                for (int e = 0; e < R::E; ++e) {
                     odd |= !(fabsf(x[e]) <= FLT_MAX);
                     lo[i][e] = fminf(lo[i][e], x[e]);
                     hi[i][e] = fmaxf(hi[i][e], x[e]);
                 }
             }
     }
-    float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < CPL; ++i)
+    for (int i = 0; i < R::CPL; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+        for (int e = 0; e < R::E; ++e)
 #pragma unroll
-            for (int o = LPR; o < 32; o <<= 1) {
+            for (int o = R::LPR; o < 32; o <<= 1) {
                 lo[i][e] = fminf(lo[i][e], __shfl_xor_sync(0xffffffffu, lo[i][e], o));
                 hi[i][e] = fmaxf(hi[i][e], __shfl_xor_sync(0xffffffffu, hi[i][e], o));
             }
-            a = fmaxf(a, fmaxf(fabsf(lo[i][e]), fabsf(hi[i][e])));
-        }
+    return __any_sync(0xffffffffu, odd);
+}
+
+// A closing page's envelope by one warp.
+template <typename T, int D>
+__device__ __forceinline__ void warp_envelope(const AppendParams &p, const Closing &cl, int h, int lane) {
+    using R = Rows<T, D>;
+    float lo[R::CPL][R::E], hi[R::CPL][R::E];
+    const bool odd = row_bounds<T, D>(p, cl, h, 0, cl.row + 1, lo, hi, lane);
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < R::CPL; ++i)
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) a = fmaxf(a, fmaxf(fabsf(lo[i][e]), fabsf(hi[i][e])));
     a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));  // not negative: ordered as bits
-    odd = __any_sync(0xffffffffu, odd);
-    const long long unit = (long long)(slot >> p.ps_shift) * p.Hkv + h;
+    const long long unit = (long long)cl.page * p.Hkv + h;
     if (lane == 0) p.env_scale[unit] = odd ? INFINITY : __fdiv_rn(a, 127.f);
-    if (r0 != 0) return;
+    if (lane >= R::LPR) return;
     const float inv = 127.f / a;
 #pragma unroll
-    for (int i = 0; i < CPL; ++i)
+    for (int i = 0; i < R::CPL; ++i)
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            float(&x)[E] = side ? hi[i] : lo[i];
+            float(&x)[R::E] = side ? hi[i] : lo[i];
             if (!odd && a > 0.f)
-                quantise8<E>(x, a, inv);
+                quantise8<R::E>(x, a, inv);
             else
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = 0.f;
-            uint32_t w[E / 4];
+                for (int e = 0; e < R::E; ++e) x[e] = 0.f;
+            uint32_t w[R::E / 4];
 #pragma unroll
-            for (int e = 0; e < E; e += 4)
+            for (int e = 0; e < R::E; e += 4)
                 w[e / 4] = ((int)x[e] & 0xff) | ((int)x[e + 1] & 0xff) << 8 | ((int)x[e + 2] & 0xff) << 16 |
                            (unsigned)(int)x[e + 3] << 24;
-            int8_t *dst = p.env + (unit * 2 + side) * D + (c0 + i * LPR) * E;
-            if constexpr (E == 8)
+            int8_t *dst = p.env + (unit * 2 + side) * D + (lane + i * R::LPR) * R::E;
+            if constexpr (R::E == 8)
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
             else
                 *reinterpret_cast<uint32_t *>(dst) = w[0];
         }
 }
 
+constexpr int kAppendThreads = 128, kAppendWarps = 4;
+
+// The envelopes of one or two closing pages by a CTA: SPLIT warps share a page's rows.  s_part:
+// [kAppendWarps][2][D] partial bounds, s_max: [kAppendWarps / SPLIT] zeros.
+template <typename T, int D, int SPLIT>
+__device__ __forceinline__ void cta_envelope(const AppendParams &p, const Closing &cl, int h, float *s_part,
+                                             unsigned *s_max, int warp, int lane) {
+    using R = Rows<T, D>;
+    constexpr int EPT = D / (SPLIT * 32) > 0 ? D / (SPLIT * 32) : 1;  // elements of a thread in the second half
+    const int part = warp % SPLIT, n = cl.row + 1, share = (n + SPLIT - 1) / SPLIT;
+    const int r1 = min(part * share, n), r2 = min(r1 + share, n);
+    float lo[R::CPL][R::E], hi[R::CPL][R::E];
+    const bool odd = row_bounds<T, D>(p, cl, h, r1, r2, lo, hi, lane);
+    if (lane < R::LPR) {
+#pragma unroll
+        for (int i = 0; i < R::CPL; ++i)
+#pragma unroll
+            for (int e = 0; e < R::E; ++e) {
+                s_part[2 * warp * D + (lane + i * R::LPR) * R::E + e] = lo[i][e];
+                s_part[(2 * warp + 1) * D + (lane + i * R::LPR) * R::E + e] = hi[i][e];
+            }
+    }
+    unsigned *top = s_max + warp / SPLIT;  // bits of the largest |element|; a NaN where one is not finite
+    if (odd && lane == 0) atomicMax(top, 0x7fffffffu);
+    __syncthreads();
+    const float *first = s_part + 2 * (warp - part) * D;
+    const int d0 = part * 32 + lane;
+    float x[2][EPT];
+    unsigned a = 0;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        const int d = d0 + i * SPLIT * 32;
+        x[0][i] = INFINITY, x[1][i] = -INFINITY;
+        if (d >= D) continue;
+#pragma unroll
+        for (int w = 0; w < SPLIT; ++w) {
+            x[0][i] = fminf(x[0][i], first[2 * w * D + d]);
+            x[1][i] = fmaxf(x[1][i], first[(2 * w + 1) * D + d]);
+        }
+        a = max(a, __float_as_uint(fmaxf(fabsf(x[0][i]), fabsf(x[1][i]))));
+    }
+    a = __reduce_max_sync(0xffffffffu, a);
+    if (lane == 0) atomicMax(top, a);
+    __syncthreads();
+    a = *top;
+    const float big = __uint_as_float(a);
+    const long long unit = (long long)cl.page * p.Hkv + h;
+    if (part == 0 && lane == 0) p.env_scale[unit] = a >= 0x7f800000u ? INFINITY : __fdiv_rn(big, 127.f);
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        if (a < 0x7f800000u && a > 0)
+            quantise8<EPT>(x[side], big, 127.f / big);
+        else
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) x[side][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int d = d0 + i * SPLIT * 32;
+            if (d < D) p.env[(unit * 2 + side) * D + d] = (int8_t)(int)x[side][i];
+        }
+    }
+}
+
 }  // namespace
 
-template <typename T, int D, int TPW>
-__global__ void __launch_bounds__(256) paged_attn_append_kernel(const AppendParams p) {
+// TPW: tokens of a copying warp; ET: tokens of an envelope CTA.
+template <typename T, int D, int TPW, int ET>
+__global__ void __launch_bounds__(kAppendThreads) paged_attn_append_kernel(const AppendParams p, int env_ctas) {
     constexpr int CH = D * (int)sizeof(T) / 16;  // 16-byte chunks of a row
-    constexpr int N = (2 * CH + 31) / 32;        // of a token's two rows, per lane
-    const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    if ((int)blockIdx.x < env_ctas) {
+        const int t0 = (int)(blockIdx.x / p.Hkv) * ET, h = blockIdx.x % p.Hkv;
+        __shared__ int s_slot[ET + 128];  // of tokens t0 - 64 ..
+        for (int i = threadIdx.x; i < ET + 128; i += kAppendThreads) {
+            const int t = t0 - 64 + i;
+            s_slot[i] = t >= 0 && t < p.T ? p.slots[t] : -1;
+        }
+        __shared__ Closing s_close[kAppendWarps];
+        __shared__ unsigned s_max[2];
+        __shared__ bool s_closes[ET];
+        __shared__ __align__(16) float s_part[kAppendWarps * 2 * D];
+        Closing &cl = s_close[warp];
+        if (threadIdx.x < 2) s_max[threadIdx.x] = 0u;
+        __syncthreads();
+        auto here = [&](int slot, int page) { return slot >= 0 && slot >> p.ps_shift == page; };
+#pragma unroll
+        for (int k = warp; k < ET; k += kAppendWarps) {
+            const int mine = s_slot[64 + k], page = mine >> p.ps_shift;
+            const bool later = here(s_slot[65 + k + lane], page) || (k + 97 + lane < ET + 128 && here(s_slot[k + 97 + lane], page));
+            const bool any = __any_sync(0xffffffffu, later);
+            if (lane == 0) s_closes[k] = mine >= 0 && mine < p.num_slots && !any;
+        }
+        __syncthreads();
+        const unsigned closes = __ballot_sync(0xffffffffu, lane < ET && s_closes[lane < ET ? lane : 0]);
+        const int n = __popc(closes);
+        // the c-th closing token's page: its rows' sources
+        auto look_up = [&](int c) {
+            const int k = (int)__fns(closes, 0, c + 1), page = s_slot[64 + k] >> p.ps_shift;
+            cl.from[lane] = cl.from[lane + 32] = kOld;
+            __syncwarp();
+            int row = 0;
+#pragma unroll
+            for (int back = lane; back < 64; back += 32) {
+                const int x = s_slot[64 + k - back];
+                if (here(x, page)) {
+                    const int r = x & ((1 << p.ps_shift) - 1);
+                    cl.from[r] = (uint8_t)back;
+                    row = max(row, r);
+                }
+            }
+            row = __reduce_max_sync(0xffffffffu, row);
+            if (lane == 0) {
+                cl.t = t0 + k;
+                cl.page = page;
+                cl.row = row;
+            }
+            __syncwarp();
+        };
+        if (n == 1) {  // as in a prompt
+            look_up(0);
+            cta_envelope<T, D, 4>(p, cl, h, s_part, s_max, warp, lane);
+        } else if (n == 2) {
+            look_up(warp / 2);
+            cta_envelope<T, D, 2>(p, cl, h, s_part, s_max, warp, lane);
+        } else {
+#pragma unroll 1
+            for (int c = warp; c < n; c += kAppendWarps) {
+                look_up(c);
+                warp_envelope<T, D>(p, cl, h, lane);
+                __syncwarp();  // before cl is written for another page
+            }
+        }
+        return;
+    }
+
+    constexpr int N = (2 * CH + 31) / 32;  // chunks of a token's two rows, per lane
+    const long long unit = (long long)(blockIdx.x - env_ctas) * kAppendWarps + warp;
     const long long group = unit / p.Hkv;
     const int h = (int)(unit - group * p.Hkv);
     if (group * TPW >= p.T) return;
     const int t0 = (int)group * TPW;
-    // slots t0 - 64 .. t0 + TPW, one trip: lane l holds t0 + TPW - 1 - l, t0 + TPW - 33 - l, ...
-    const int tl = min(t0 + TPW, p.T) - 1;  // the warp's last token
-    const int s_next = tl + 1 < p.T ? p.slots[tl + 1] : -1;
-    int s[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-        s[i] = tl - i * 32 - lane >= 0 && (i == 0 || p.env) ? p.slots[tl - i * 32 - lane] : -1;
-
+    const int mine = lane < TPW && t0 + lane < p.T ? p.slots[t0 + lane] : -1;
+    if (mine != -1 && (mine < 0 || mine >= p.num_slots)) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+    const long long row_elems = (long long)p.Hkv * D;
     int slot[TPW];
     uint4 v[TPW][N];
-    const long long row_elems = (long long)p.Hkv * D;
 #pragma unroll
-    for (int k = 0; k < TPW; ++k) {  // token tl - k
-        slot[k] = __shfl_sync(0xffffffffu, s[0], k);
-        const bool on = tl - k >= t0 && slot[k] >= 0 && slot[k] < p.num_slots;
-        if (!on) {
-            if (tl - k >= t0 && slot[k] != -1 && lane == 0) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+    for (int k = 0; k < TPW; ++k) {
+        slot[k] = __shfl_sync(0xffffffffu, mine, k);
+        if (slot[k] < 0 || slot[k] >= p.num_slots) {
             slot[k] = -1;
             continue;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = i * 32 + lane;
-            const T *src = c < CH ? static_cast<const T *>(p.k_new) + (tl - k) * p.k_stride
-                                  : static_cast<const T *>(p.v_new) + (tl - k) * p.v_stride;
-            if (c < 2 * CH) v[k][i] = reinterpret_cast<const uint4 *>(src + h * D)[c < CH ? c : c - CH];
+            const T *src = c < CH ? static_cast<const T *>(p.k_new) + (t0 + k) * p.k_stride
+                                  : static_cast<const T *>(p.v_new) + (t0 + k) * p.v_stride;
+            if (c < 2 * CH) v[k][i] = __ldg(reinterpret_cast<const uint4 *>(src + h * D) + (c < CH ? c : c - CH));
         }
     }
 #pragma unroll
@@ -165,40 +318,26 @@ __global__ void __launch_bounds__(256) paged_attn_append_kernel(const AppendPara
             if (c < 2 * CH) reinterpret_cast<uint4 *>(dst)[c < CH ? c : c - CH] = v[k][i];
         }
     }
-    if (!p.env) return;
-    const int ps = 1 << p.ps_shift;
-#pragma unroll 1
-    for (int k = 0; k < TPW; ++k) {
-        const int t = tl - k;
-        const int mine = __shfl_sync(0xffffffffu, s[0], k), next = k == 0 ? s_next : __shfl_sync(0xffffffffu, s[0], k - 1);
-        if (t < t0 || mine < 0 || mine >= p.num_slots) continue;
-        const int row = mine & (ps - 1);
-        if (row != ps - 1 && next == mine + 1) continue;  // a later token closes the page
-        // token tl - l lies in the page's run if its slot is l - k rows before token t's
-        unsigned long long in = 0;  // bit j: token t - j
-#pragma unroll
-        for (int i = 2; i >= 0; --i) {
-            const int j = i * 32 + lane - k;
-            const unsigned b = __ballot_sync(0xffffffffu, j >= 0 && j <= row && s[i] == mine - j);
-            in |= i * 32 - k >= 0 ? (i * 32 - k < 64 ? (unsigned long long)b << (i * 32 - k) : 0ull) : (unsigned long long)(b >> k);
-        }
-        const int run = ~in ? __ffsll((long long)~in) - 1 : 64;
-        page_envelope<T, D>(p, t, h, mine, run, lane);
-    }
+}
+
+template <typename T, int D, int TPW, int ET>
+static cudaError_t launch_append_k(const AppendParams &p, cudaStream_t stream) {
+    const long long env = p.env ? ((long long)p.T + ET - 1) / ET * p.Hkv : 0;
+    const long long units = ((long long)p.T + TPW - 1) / TPW * p.Hkv;
+    const long long blocks = env + (units + kAppendWarps - 1) / kAppendWarps;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    paged_attn_append_kernel<T, D, TPW, ET><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p, (int)env);
+    return cudaGetLastError();
 }
 
 template <typename T, int D>
 static cudaError_t launch_append_d(const AppendParams &p, cudaStream_t stream) {
-    // Several tokens a warp once there are warps for every multiprocessor many times over.
-    const bool many = (long long)p.T * p.Hkv >= 16384;
-    const long long blocks = ((long long)(many ? (p.T + 3) / 4 : p.T) * p.Hkv + 7) / 8;
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (many)
-        paged_attn_append_kernel<T, D, 4><<<(unsigned)blocks, 256, 0, stream>>>(p);
-    else
-        paged_attn_append_kernel<T, D, 1><<<(unsigned)blocks, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    // Prompts (warps for every multiprocessor many times over): several tokens a warp and few closing
+    // pages among them (14.2 us as above; 27.7 with one token a warp); single tokens: a warp each, most of
+    // them closing a page.
+    if ((long long)p.T * p.Hkv >= 16384) return launch_append_k<T, D, 4, 32>(p, stream);
+    return launch_append_k<T, D, 1, 4>(p, stream);
 }
 
 template <typename T>
