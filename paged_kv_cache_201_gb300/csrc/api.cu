@@ -789,10 +789,24 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
     sp.n_tok = n_tok;
     sp.K = top_k;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dims->dtype == PA_F32) return cuda_status(pa::launch_sparse_simt(sp, dims->dtype, st));
+    if (dims->dtype == PA_F32) return cuda_status(pa::launch_sparse_simt(sp, st));
     CUtensorMap tmk, tmv;
     if ((rc = make_pool_map(&tmk, k_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;
     if ((rc = make_pool_map(&tmv, v_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;
+    // Sequences with enough query tokens go to the kernel whose CTAs share page loads between tokens; in a
+    // packed batch both kernels find their sequences from q_start, and the second launch is left out
+    // where no sequence can be that long.
+    const int tile = pa::sparse_group_tokens(dims->num_q_heads / dims->num_kv_heads);
+    if (tile > 0 && dims->head_dim != 256 && dims->bt_stride <= pa::kSparseGroupMaxPages) {
+        // a batch of mostly single tokens: one launch takes them all
+        const bool runs = q_start ? n_tok >= 2 * (int64_t)dims->batch : true;
+        const int64_t longest = q_start ? n_tok : dims->q_len;
+        if (runs && longest >= tile / 2) {
+            sp.group_min = tile / 2;
+            rc = cuda_status(pa::launch_sparse_group(sp, dims->dtype, tmk, tmv, st));
+            if (rc != PA_OK || !q_start) return rc;
+        }
+    }
     return cuda_status(pa::launch_sparse_mma(sp, dims->dtype, device_sm_count(), tmk, tmv, st));
 }
 

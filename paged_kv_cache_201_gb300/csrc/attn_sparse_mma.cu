@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
     const int rt = unit % row_tiles;
     const long long t_row = unit / row_tiles;
     const TokenRow tr = token_row(p, t_row, sp.n_tok, threadIdx.x == 0);
-    if (tr.b < 0) return;  // the whole cluster: it has one token
+    // the whole cluster returns: it has one token
+    if (tr.b < 0) return;
+    if (sp.group_min && __ldg(p.q_start + tr.b + 1) - __ldg(p.q_start + tr.b) >= sp.group_min) return;
 
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;

@@ -423,6 +423,80 @@ def test_attend_few_rows_long_lists(pa):
             _check_attend(pa, b, _lists(b, 300))
 
 
+CHUNKS = [1, 70, 0, 16, 15, 1, 33]
+CHUNK_LENS = [90, 300, 5, 16, 700, 64, 33]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(8, 2, 128, 16), (4, 4, 64, 32), (14, 2, 64, 64), (16, 1, 128, 16),
+                                         (3, 1, 128, 64), (10, 2, 128, 32), (18, 1, 64, 16)])
+def test_attend_prompt_chunks(pa, dtype, Hq, Hkv, D, ps):
+    """Runs of tokens whose lists are read together, beside short sequences in the same call."""
+    b = R.Batch(Hq * D + ps, CHUNKS, CHUNK_LENS, Hq, Hkv, D, ps, dtype, q_pad=3)
+    for K in (1, 5, 14):
+        _check_attend(pa, b, _lists(b, K))
+    qo = [max(0, L - n - 7) for n, L in zip(CHUNKS, CHUNK_LENS)]
+    qo[4] = -6  # a chunk whose first tokens see nothing
+    _check_attend(pa, b, _lists(b, 5, q_offset=qo), q_offset=qo)
+    _check_attend(pa, b, _lists(b, 5, causal=False), causal=False)
+
+
+def test_attend_prompt_chunks_uniform(pa):
+    for n in (8, 16, 50):
+        b = R.Batch(n, [n] * 3, [n, 200, 130], 8, 2, 128, 16, "bf16")
+        _check_attend(pa, b, _lists(b, 6), uniform=True)
+        _check_attend(pa, b, _lists(b, 6), uniform=True, scale=-0.2)
+
+
+def test_attend_prompt_chunks_any_list(pa):
+    """Repeated entries count again, in one tile of a chunk or in all; ids outside the pool read as zeros."""
+    for dtype in ("bf16", "f16"):
+        b = R.Batch(31, CHUNKS, CHUNK_LENS, 8, 2, 128, 16, dtype)
+        sel = _lists(b, 9)
+        sel[40, 1, :4] = [2, 0, 2, 2]
+        sel[45, 0] = [-1, W.SENTINEL_MAX, -2**31, 1, 1, 99, 1, 0, -7]
+        _check_attend(pa, b, sel)
+        assert pa.paged_attn_last_error_word() == 0
+        sel[:, :, 1] = sel[:, :, 0]
+        _check_attend(pa, b, sel)
+        b.table[1, 2], b.table[4, 7] = b.P, -1
+        sel = _lists(b, 9, seed=3)
+        sel[:, :, 0] = 2
+        sel[:, :, 1:][sel[:, :, 1:] == 2] = -1
+        _check_attend(pa, b, sel)
+        assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+
+
+def test_attend_prompt_chunks_non_finite(pa):
+    """An infinity or a NaN in a key or a value reaches the rows that list its page and see its key, and
+    no other row of the tile."""
+    for dtype, inf, nan in (("bf16", 0x7F80, 0x7FC0), ("f16", 0x7C00, 0x7E00)):
+        b = R.Batch(32, [64], [200], 8, 2, 128, 16, dtype)
+        sel = np.zeros((64, 2, 3), np.int32)
+        sel[:] = [1, 4, 8]
+        sel[20:23, :, 1] = 6
+        sel[30, 1, 1] = 5
+        clean = _run_attend(pa, b, sel)[0]
+        b.v[b.table[0, 6], 2, 0, 3] = nan
+        b.k[b.table[0, 5], 7, 1, 9] = nan
+        b.v[b.table[0, 9], 10, 1, 64] = inf  # position 154: no token lists page 9
+        b.v[b.table[0, 8], 15, 0, 11] = inf  # position 143, below every token's 144 keys in page 8
+        sel[5, 0] = [1, 4, 9]                # token 5 sees positions up to 141: not page 9's
+        out = _run_attend(pa, b, sel)[0]
+        bad = ~np.isfinite(out)
+        want = np.zeros_like(bad)
+        want[20:23, :4, 3] = True             # page 6, kv head 0, one column
+        want[30, 4:, :] = True                # a NaN score: every column
+        want[7:, :4, 11] = True               # tokens that see position 143 (136 + 7)
+        np.testing.assert_array_equal(bad, want)
+        same = ~want.any(-1)
+        same[5, :4] = False
+        k, v = R.elems_to_f64(b.k, dtype), R.elems_to_f64(b.v, dtype)
+        rows = np.isfinite(out).all(-1)
+        _gpu.assert_close(out[same], clean[same], dtype, "rows without them")
+        assert rows[~want.any(-1)].all()
+
+
 def test_attend_masks(pa):
     """Non-causal, explicit offsets (one puts every key out of reach), the uniform layout, a view of q,
     a negative and a zero scale."""
