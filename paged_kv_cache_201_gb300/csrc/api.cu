@@ -803,7 +803,16 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
         const int64_t longest = q_start ? n_tok : dims->q_len;
         if (runs && longest >= tile / 2) {
             sp.group_min = tile / 2;
-            rc = cuda_status(pa::launch_sparse_group(sp, dims->dtype, tmk, tmv, st));
+            const int G = dims->num_q_heads / dims->num_kv_heads;
+            if (dims->head_dim == 128 && (G == 4 || G == 8) && scale > 0.f && dims->bt_stride <= pa::kSparseTc05MaxPages) {
+                CUtensorMap tmq, tmk5, tmv5;
+                if ((rc = make_q_map(&tmq, q, dims, q_start != nullptr)) != PA_OK) return rc;
+                if ((rc = make_pool_map(&tmk5, k_cache, dims, 1)) != PA_OK) return rc;
+                if ((rc = make_pool_map(&tmv5, v_cache, dims, 1)) != PA_OK) return rc;
+                rc = cuda_status(pa::launch_sparse_tc05(sp, dims->dtype, tmq, tmk5, tmv5, st));
+            } else {
+                rc = cuda_status(pa::launch_sparse_group(sp, dims->dtype, tmk, tmv, st));
+            }
             if (rc != PA_OK || !q_start) return rc;
         }
     }

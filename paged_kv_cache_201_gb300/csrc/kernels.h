@@ -126,6 +126,11 @@ constexpr int kSparseGroupMaxPages = 8192;
 int sparse_group_tokens(int G);
 cudaError_t launch_sparse_group(const SparseParams &p, int dtype, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                 cudaStream_t stream);
+// The same on tcgen05: head_dim 128, G = 4 or 8 (tiles of 128 / G tokens), scale > 0, at most
+// kSparseTc05MaxPages pages a sequence.
+constexpr int kSparseTc05MaxPages = 4608;
+cudaError_t launch_sparse_tc05(const SparseParams &p, int dtype, const CUtensorMap &tmq, const CUtensorMap &tmk,
+                               const CUtensorMap &tmv, cudaStream_t stream);
 cudaError_t launch_sparse_simt(const SparseParams &p, cudaStream_t stream);  // f32
 
 }  // namespace pa

@@ -429,7 +429,8 @@ CHUNK_LENS = [90, 300, 5, 16, 700, 64, 33]
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("Hq,Hkv,D,ps", [(8, 2, 128, 16), (4, 4, 64, 32), (14, 2, 64, 64), (16, 1, 128, 16),
-                                         (3, 1, 128, 64), (10, 2, 128, 32), (18, 1, 64, 16)])
+                                         (3, 1, 128, 64), (10, 2, 128, 32), (18, 1, 64, 16),
+                                         (8, 1, 128, 32), (16, 2, 128, 64), (4, 1, 128, 64)])
 def test_attend_prompt_chunks(pa, dtype, Hq, Hkv, D, ps):
     """Runs of tokens whose lists are read together, beside short sequences in the same call."""
     b = R.Batch(Hq * D + ps, CHUNKS, CHUNK_LENS, Hq, Hkv, D, ps, dtype, q_pad=3)
