@@ -440,6 +440,15 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
                           void *stream);
 
 /*
+ * paged_attn_sparse_shares_pages — whether paged_attn_fwd_sparse, for this shape on a GPU of num_sms SMs,
+ * takes its tcgen05 kernel for sequences with runs of query tokens (1: a CTA reads the pages that any of up
+ * to 32 consecutive tokens lists, each once) or reads every token's list by itself (0).  packed: q is
+ * [T, Hq, D] with T = dims->q_len.  Both give the same results within the rounding of the sums.  Host-only.
+ * Negative status for bad dims, top_k < 1 or num_sms < 1.
+ */
+int paged_attn_sparse_shares_pages(const pa_dims *dims, int packed, int top_k, float scale, int num_sms);
+
+/*
  * paged_attn_plan — the split plan as data: plan [batch, split_kv, 2] int32 =
  * {first page, one past the last page} of each run (see paged_attn_fwd).
  * seq_lens is a device pointer [batch]; negative lengths count as 0.

@@ -25,7 +25,7 @@ __all__ = [
     "paged_attn_fwd_kvq_splitkv", "attention_kvq", "paged_attn_fwd_varlen", "attention_varlen",
     "paged_attn_fwd_varlen_overlap", "paged_attn_varlen_hint", "paged_attn_varlen_overlap_share", "PaVarlenHint",
     "paged_attn_step_tables", "paged_attn_append", "paged_attn_select_pages", "paged_attn_fwd_sparse",
-    "step_tables", "page_envelopes", "attention_sparse", "PA_F32", "PA_F16", "PA_BF16", "PA_FP8_E4M3",
+    "paged_attn_sparse_shares_pages", "step_tables", "page_envelopes", "attention_sparse", "PA_F32", "PA_F16", "PA_BF16", "PA_FP8_E4M3",
     "PA_INT8",
     "VARIANT_AUTO", "VARIANT_SIMT", "VARIANT_MMA_DECODE", "VARIANT_MMA_PREFILL", "VARIANT_TC05_PREFILL",
     "VARIANT_MMA_T", "VARIANT_MMA_SPLIT_GROUP",
@@ -113,6 +113,8 @@ def load_library(build_if_missing: bool = False):
     lib.paged_attn_select_pages.restype = ctypes.c_int
     lib.paged_attn_fwd_sparse.argtypes = [P, P, P, P, P, P, I32, P, P, I32, F, P, P, D, P]
     lib.paged_attn_fwd_sparse.restype = ctypes.c_int
+    lib.paged_attn_sparse_shares_pages.argtypes = [D, I32, I32, F, I32]
+    lib.paged_attn_sparse_shares_pages.restype = ctypes.c_int
     lib.paged_attn_debug_gather.argtypes = [P, P, P, D, I32, P, P]
     lib.paged_attn_debug_wait_timeout.argtypes = [ctypes.c_uint32, P]
     lib.paged_attn_debug_wait_timeout.restype = ctypes.c_int
@@ -648,6 +650,19 @@ def paged_attn_fwd_sparse(q, k_cache, v_cache, block_table, seq_lens, causal, q_
         _ptr(lse), dims, _stream(stream))
     if rc:
         _raise(rc, "paged_attn_fwd_sparse")
+
+
+def paged_attn_sparse_shares_pages(batch: int, tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                   page_size: int, table_width: int, top_k: int, scale: float, num_sms: int,
+                                   dtype: int = PA_BF16, packed: bool = True) -> bool:
+    """Whether the sparse forward reads the pages of runs of tokens once for up to 32 of them (True) or
+    every token's list by itself; see ``paged_attn_sparse_shares_pages`` in include/paged_attn.h.
+    tokens: all of a packed batch's, or a sequence's of a uniform one."""
+    dims = PaDims(batch, tokens, num_q_heads, num_kv_heads, head_dim, page_size, 1, table_width, dtype)
+    rc = load_library().paged_attn_sparse_shares_pages(dims, 1 if packed else 0, top_k, scale, num_sms)
+    if rc < 0:
+        _raise(rc, "paged_attn_sparse_shares_pages")
+    return bool(rc)
 
 
 def paged_attn_combine(part_out, part_lse, out, lse=None, stream=None) -> None:

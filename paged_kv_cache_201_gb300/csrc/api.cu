@@ -666,6 +666,46 @@ int check_sparse(const pa_dims *d, const void *q, const int32_t *block_table, co
     return PA_OK;
 }
 
+// 4-D view of q for the tcgen05 kernel over listed pages: (d within a half, half, query head, token); one box
+// = one half of a tile: its tokens x the G heads of a kv head.
+int make_sparse_q_map(CUtensorMap *m, const void *q, const pa_dims *d, int64_t n_tok) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return PA_ECUDA;
+    const cuuint64_t esz = 2, D = (cuuint64_t)d->head_dim, Hq = (cuuint64_t)d->num_q_heads;
+    const int G = d->num_q_heads / d->num_kv_heads;
+    const cuuint64_t dims[4] = {64, D / 64, Hq, (cuuint64_t)n_tok};
+    const cuuint64_t strides[3] = {64 * esz, D * esz, (cuuint64_t)q_token_stride(d) * esz};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)G, (cuuint32_t)pa::sparse_tile_tokens(G)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(m, tma_dtype(d->dtype), 4, const_cast<void *>(q), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ECUDA;
+}
+
+// Whether paged_attn_fwd_sparse takes the kernel whose CTAs read the union of a run of tokens' lists
+// (tcgen05) next to the one that reads each token's own.  Both are estimated, in microseconds, from their
+// measured rates: the first takes c a 128-key tile of the union and some 6 to set up, in waves of one CTA
+// an SM; the second reads its lists at 8.9 TB/s from L2.  The union is taken as half of the tile's lists'
+// total, at most the whole table: neighbouring tokens' lists overlap.  Measured with random lists of 64 of
+// 512 16-token pages, 8 kv heads, G = 4, bf16: 128 tokens 103 against 71 us, 256 tokens 106 against 128,
+// 1024 tokens 212 against 485.
+bool sparse_shares_pages(const pa_dims *d, int64_t n_tok, bool packed, int top_k, float scale, int sms) {
+    const int G = d->num_q_heads / d->num_kv_heads, tile = pa::sparse_tile_tokens(G);
+    if (d->dtype == PA_F32 || d->head_dim == 256 || tile == 0 || !(scale > 0.f) ||
+        d->bt_stride > pa::kSparseTc05MaxPages || n_tok >= (int64_t)1 << 31)
+        return false;
+    // a batch of mostly single tokens, or of too few for half a tile
+    if (packed ? n_tok < 2 * (int64_t)d->batch : d->q_len < (tile + 1) / 2) return false;
+    const double W = d->bt_stride, K = top_k < W ? top_k : W;
+    const double c = (d->dtype == PA_BF16 ? 1.53 : 1.05) * (d->head_dim == 64 ? 0.9 : 1.0);
+    const double whole = tile * K / 2, pages = whole < W ? whole : W;
+    const double tiles = packed ? ceil((double)n_tok / tile) : (double)d->batch * ((d->q_len + tile - 1) / tile);
+    const double shared = ceil(tiles * d->num_kv_heads / sms) * (pages * d->page_size / 128 * c + 6);
+    const double own = 8 + (double)n_tok * d->num_kv_heads * ((G + 15) / 16) * K * d->page_size * d->head_dim * 4 / 8.9e6;
+    return shared < own;
+}
+
 }  // namespace
 
 int paged_attn_step_tables(const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages,
@@ -793,30 +833,26 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
     CUtensorMap tmk, tmv;
     if ((rc = make_pool_map(&tmk, k_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;
     if ((rc = make_pool_map(&tmv, v_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;
-    // Sequences with enough query tokens go to the kernel whose CTAs share page loads between tokens; in a
-    // packed batch both kernels find their sequences from q_start, and the second launch is left out
-    // where no sequence can be that long.
-    const int tile = pa::sparse_group_tokens(dims->num_q_heads / dims->num_kv_heads);
-    if (tile > 0 && dims->head_dim != 256 && dims->bt_stride <= pa::kSparseGroupMaxPages) {
-        // a batch of mostly single tokens: one launch takes them all
-        const bool runs = q_start ? n_tok >= 2 * (int64_t)dims->batch : true;
-        const int64_t longest = q_start ? n_tok : dims->q_len;
-        if (runs && longest >= tile / 2) {
-            sp.group_min = tile / 2;
-            const int G = dims->num_q_heads / dims->num_kv_heads;
-            if (dims->head_dim == 128 && (G == 4 || G == 8) && scale > 0.f && dims->bt_stride <= pa::kSparseTc05MaxPages) {
-                CUtensorMap tmq, tmk5, tmv5;
-                if ((rc = make_q_map(&tmq, q, dims, q_start != nullptr)) != PA_OK) return rc;
-                if ((rc = make_pool_map(&tmk5, k_cache, dims, 1)) != PA_OK) return rc;
-                if ((rc = make_pool_map(&tmv5, v_cache, dims, 1)) != PA_OK) return rc;
-                rc = cuda_status(pa::launch_sparse_tc05(sp, dims->dtype, tmq, tmk5, tmv5, st));
-            } else {
-                rc = cuda_status(pa::launch_sparse_group(sp, dims->dtype, tmk, tmv, st));
-            }
-            if (rc != PA_OK || !q_start) return rc;
-        }
+    // Sequences with half a tile of query tokens or more go to the kernel whose CTAs read the union of
+    // their tokens' lists; in a packed batch both kernels find their sequences from q_start.
+    if (sparse_shares_pages(dims, n_tok, q_start != nullptr, top_k, scale, device_sm_count())) {
+        sp.group_min = (pa::sparse_tile_tokens(dims->num_q_heads / dims->num_kv_heads) + 1) / 2;
+        CUtensorMap tmq, tmk5, tmv5;
+        if ((rc = make_sparse_q_map(&tmq, q, dims, n_tok)) != PA_OK) return rc;
+        if ((rc = make_pool_map(&tmk5, k_cache, dims, 1)) != PA_OK) return rc;
+        if ((rc = make_pool_map(&tmv5, v_cache, dims, 1)) != PA_OK) return rc;
+        rc = cuda_status(pa::launch_sparse_tc05(sp, dims->dtype, tmq, tmk5, tmv5, st));
+        if (rc != PA_OK || !q_start) return rc;
     }
     return cuda_status(pa::launch_sparse_mma(sp, dims->dtype, device_sm_count(), tmk, tmv, st));
+}
+
+int paged_attn_sparse_shares_pages(const pa_dims *dims, int packed, int top_k, float scale, int num_sms) {
+    int rc = check_dims(dims);
+    if (rc != PA_OK) return rc;
+    if (top_k < 1 || num_sms < 1) return PA_EINVAL;
+    const int64_t n_tok = packed ? (int64_t)dims->q_len : (int64_t)dims->batch * dims->q_len;
+    return sparse_shares_pages(dims, n_tok, packed != 0, top_k, scale, num_sms) ? 1 : 0;
 }
 
 int paged_attn_combine(const float *part_out, const float *part_lse, int split_kv, int64_t rows, int head_dim,

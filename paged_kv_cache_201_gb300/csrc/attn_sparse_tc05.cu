@@ -1,8 +1,8 @@
 // Attention over listed pages for runs of query tokens of one sequence, on the 5th-generation tensor cores
-// (bf16 / f16, head_dim 128, 4 or 8 query heads to a kv head, scale > 0).
+// (bf16 / f16, head_dim 64 or 128, up to 128 query heads to a kv head, scale > 0).
 //
-// A CTA takes 128 rows (128 / G consecutive tokens x the G heads of a kv head) and walks the union of the
-// tokens' page lists, each page once, in 128-key tiles of 128 / page_size listed pages:
+// A CTA takes up to 128 rows (TPC = min(32, 128 / G) consecutive tokens x the G heads of a kv head) and walks
+// the union of the tokens' page lists, each page once, in 128-key tiles of 128 / page_size listed pages:
 //   warp 0      loads the Q tile, then K pages by TMA into a two-slot ring; warp 2 the V pages
 //   warp 1      one thread issues tcgen05.mma: S = Q K^T into one of two S buffers of tensor memory (128
 //               float32 columns), then O += P V with P read from tensor memory; P V of a tile is issued
@@ -17,9 +17,10 @@
 // A masked key's weight is 0, but 0 times an infinity or a NaN in V is a NaN.  Such values are rare, so no
 // product is guarded: a CTA whose result is not finite, and one whose lists name a page twice (it counts
 // twice), does its tokens again on CUDA cores, where a key that is not seen is not multiplied.
-// The products run over all 128 rows of every listed page, whoever lists it: at random lists (64 of some 400
-// pages a token, 32 tokens) six times what the lists ask for, and still faster than reading the lists token
-// by token, which moves 3.9 GB through L2.
+// The products run over all rows of every listed page, whoever lists it: at random lists (64 of some 400
+// pages a token, 32 tokens, G = 4) six times what the lists ask for, at 1.05 us a tile in f16 and 1.53 in
+// bf16 (head_dim 128).  936 such tokens of 8 kv heads take 145 us (f16); read token by token their lists
+// move 3.9 GB through L2, 451 us.  Lists that overlap more cost less here.
 #include <float.h>
 
 #include <type_traits>
@@ -36,7 +37,6 @@ constexpr int kSt5Threads = 384, kSt5Warps = kSt5Threads / 32;
 // Registers once the roles part: 128 x 64 + 256 x 208 are fewer than the launch's 384 x 168.
 constexpr uint32_t kSt5LoadRegs = 64, kSt5SoftmaxRegs = 208;
 constexpr int kSt5Half = 128 * 128;    // bytes of one 64-column half of a 128-row tile
-constexpr int kSt5Tile = 2 * kSt5Half;
 constexpr uint32_t kSt5ColO = 256;
 constexpr float kSt5Rescale = 8.f;     // rescale O only when the maximum grows by more than 2^8
 enum { S_QF = 0, S_KF = 1, S_KE = 3, S_VF = 5, S_VE = 7, S_PF = 9, S_COUNT = 11 };
@@ -80,12 +80,13 @@ __device__ __forceinline__ void block_exp(const uint32_t (&u)[32], float c, floa
 
 }  // namespace
 
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(kSt5Threads, 1)
     paged_attn_sparse_tc05_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                                   const __grid_constant__ CUtensorMap tmV, const SparseParams sp, int ps_shift,
-                                  int g_shift, uint32_t idesc_qk, uint32_t idesc_pv) {
+                                  int TPC, uint32_t idesc_qk, uint32_t idesc_pv) {
     constexpr bool kSplit = !std::is_same<T, __half>::value;
+    constexpr int NH = D / 64, kTile = NH * kSt5Half;  // a tile of Q, K or V: NH 64-column halves
     const FwdParams &p = sp.f;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[S_COUNT];
@@ -97,18 +98,18 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
     const int ps = 1 << ps_shift;
     const int kvh = blockIdx.x % p.Hkv;
     TokenTile x;
-    if (!token_tile(sp, blockIdx.x / p.Hkv, 128 >> g_shift, x)) return;
+    if (!token_tile(sp, blockIdx.x / p.Hkv, TPC, x)) return;
     if (tid < x.nt) s_reach[tid] = row_key_limit(p, x.b, x.L, x.i0 + tid, x.n_seq);
     const int reach_max = row_key_limit(p, x.b, x.L, x.i0 + x.nt - 1, x.n_seq);  // grows with the token
     const int reach_min = row_key_limit(p, x.b, x.L, x.i0, x.n_seq);
     const int np = (reach_max + ps - 1) >> ps_shift;
 
-    // shared memory: Q | K x2 | V x2 (128 x 128 tiles, two 64-column swizzled halves each), masks, list
+    // shared memory: Q | K x2 | V x2 (128-row tiles of swizzled 64-column halves), list, masks
     const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
     const uint32_t sQ = sbase;
-    auto sK = [&](int s) { return sbase + (uint32_t)kSt5Tile * (1u + (uint32_t)s); };
-    auto sV = [&](int s) { return sbase + (uint32_t)kSt5Tile * (3u + (uint32_t)s); };
-    Listed *s_list = reinterpret_cast<Listed *>(smem_raw + (sbase - raw) + 5 * kSt5Tile);  // [W]
+    auto sK = [&](int s) { return sbase + (uint32_t)kTile * (1u + (uint32_t)s); };
+    auto sV = [&](int s) { return sbase + (uint32_t)kTile * (3u + (uint32_t)s); };
+    Listed *s_list = reinterpret_cast<Listed *>(smem_raw + (sbase - raw) + 5 * kTile);  // [W]
     uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_list + p.W);                         // [W]
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     if (tid == 0) {
@@ -151,9 +152,10 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                 tma_prefetch_desc(tm);
                 if (kq && n_tiles > 0) {
                     tma_prefetch_desc(&tmQ);
-                    mbar_arrive_expect_tx(bar(S_QF), (uint32_t)kSt5Tile);
-                    tma_load_4d(sQ, &tmQ, bar(S_QF), 0, 0, kvh << g_shift, (int)x.tok0);
-                    tma_load_4d(sQ + kSt5Half, &tmQ, bar(S_QF), 0, 1, kvh << g_shift, (int)x.tok0);
+                    mbar_arrive_expect_tx(bar(S_QF), (uint32_t)(NH * TPC * p.G * 128));
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+                        tma_load_4d(sQ + (uint32_t)h * kSt5Half, &tmQ, bar(S_QF), 0, h, kvh * p.G, (int)x.tok0);
                 }
             }
             const uint32_t box = (uint32_t)ps * 128u;
@@ -181,12 +183,12 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                     bad = __any_sync(0xffffffffu, !ok);
                     if (bad) break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(bar(b_full + slot), (uint32_t)nvalid * 2u * box);
+                if (lane == 0) mbar_arrive_expect_tx(bar(b_full + slot), (uint32_t)nvalid * (uint32_t)NH * box);
                 __syncwarp();
                 if (lane < nvalid) {
                     const uint32_t dst = (kq ? sK(slot) : sV(slot)) + (uint32_t)lane * box;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < NH; ++h)
                         tma_load_4d(dst + (uint32_t)h * kSt5Half, tm, bar(b_full + slot), 0, tok, h, kvh);
                 }
                 issued = t + 1;
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                     tc05::fence_after_sync();
                     const uint32_t d = tmem + (slot ? 128u : 0u), dk = slot ? dk1 : dk0;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
+                    for (int kk = 0; kk < D / 16; ++kk) {
                         // columns 16 kk .. + 15: 64-column half kk / 4, 32-byte slice kk % 4 of its rows
                         const uint32_t off = ((uint32_t)(kk >> 2) * kSt5Half + (uint32_t)(kk & 3) * 32u) >> 4;
                         tc05::mma_ss_lh(d, dq + off, dhi, dk + off, dhi, idesc_qk, kk > 0 ? 1u : 0u);
@@ -248,8 +250,9 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                     // only the list's last page can reach past the last token's keys
                     const int in_tile = n_list - 1 - t * ppt;
                     const int z0 = in_tile * ps + min(ps, reach_max - (s_list[n_list - 1].j << ps_shift));
-                    for (int i = lane; i < (128 - z0) * 16; i += 32) {
-                        const uint32_t a = sV(slot) + (uint32_t)((i >> 3) & 1) * kSt5Half + (uint32_t)(z0 + (i >> 4)) * 128u +
+                    for (int i = lane; i < (128 - z0) * 8 * NH; i += 32) {
+                        const int c = i >> 3;  // 128-byte row half
+                        const uint32_t a = sV(slot) + (uint32_t)(c % NH) * kSt5Half + (uint32_t)(z0 + c / NH) * 128u +
                                            16u * (uint32_t)(i & 7);
                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
                     }
@@ -264,8 +267,8 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
         const int hh = (warp >> 2) - 1;  // keys 64 hh .. + 63 of a tile
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-        const int tk = r >> g_shift;
-        const bool row_valid = tk < x.nt;
+        const int tk = r / p.G;
+        const bool row_valid = tk < x.nt;  // at most TPC tokens, TPC G <= 128
         const int lim = row_valid ? s_reach[tk] : 0;
         const uint32_t bit = row_valid ? 1u << tk : 0u;
         const float c2 = p.scale_log2;
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                     if (!bad) {
                         tc05::fence_after_sync();
 #pragma unroll 1
-                        for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
+                        for (int c = NH * hh; c < NH * hh + NH; ++c) {
                             uint32_t o[32];
                             tc05::ld_32cols(tmem + lane_addr + kSt5ColO + 32u * c, o);
                             tc05::wait_ld();
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
             tc05::fence_before_sync();
             mbar_arrive(bar(S_PF + st));
         }
-        // the row's sum, then its columns 64 hh .. + 63
+        // the row's sum, then its half of the columns
         s_lsum[hh][r] = l;
         named_bar_sync(1, 256);
         l = s_lsum[0][r] + s_lsum[1][r];
@@ -362,11 +365,11 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
             bad = __any_sync(0xffffffffu, !mbar_wait(bar(S_VE + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.err));
         tc05::fence_after_sync();
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const long long row = (x.tok0 + tk) * p.Hq + ((long long)kvh << g_shift) + (r & ((1 << g_shift) - 1));
+        const long long row = (x.tok0 + tk) * p.Hq + (long long)kvh * p.G + (r - tk * p.G);
         bool finite = l <= FLT_MAX;
         if (!bad) {
 #pragma unroll 1
-            for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
+            for (int c = NH * hh; c < NH * hh + NH; ++c) {
                 uint32_t o[32];
                 if (n_tiles > 0) {
                     tc05::ld_32cols(tmem + lane_addr + kSt5ColO + 32u * c, o);
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) finite = finite && fabsf(__uint_as_float(o[j])) <= FLT_MAX;
                 if (row_valid) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * 128 + 32 * c);
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * D + 32 * c);
                     auto pk = [&](int i) {
                         return MmaOp<T>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
                     };
@@ -395,11 +398,11 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
         if (*(volatile int *)&s_redo == 1) {
             // ---------------------------------------------------------------- again, on CUDA cores
             float *scratch = reinterpret_cast<float *>(smem_raw + (sbase - raw));
-            static_assert(simt_scratch<128, 4, 8>() * 4 <= 5 * kSt5Tile, "the scratch must fit in the tiles");
+            static_assert(simt_scratch<D, 4, 8>() * 4 <= 5 * kTile, "the scratch must fit in the tiles");
             for (int tok = 0; tok < x.nt; ++tok) {
                 const TokenRow tr{x.b, s_reach[tok]};
                 for (int hc = 0; hc * 4 < p.G; ++hc) {
-                    simt_token<T, 128, 4, 8>(sp, tr, x.tok0 + tok, kvh, hc, scratch, tid - 128,
+                    simt_token<T, D, 4, 8>(sp, tr, x.tok0 + tok, kvh, hc, scratch, tid - 128,
                                              [] { named_bar_sync(1, 256); });
                     named_bar_sync(1, 256);  // before the scratch is used again
                 }
@@ -414,12 +417,12 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
     }
 }
 
-template <typename T>
+template <typename T, int D>
 static cudaError_t launch_st5(const SparseParams &sp, const CUtensorMap &tmq, const CUtensorMap &tmk,
                               const CUtensorMap &tmv, cudaStream_t stream) {
     const FwdParams &p = sp.f;
-    auto kern = paged_attn_sparse_tc05_kernel<T>;
-    const size_t tiles_bytes = 5 * kSt5Tile + 1024;
+    auto kern = paged_attn_sparse_tc05_kernel<T, D>;
+    const size_t tiles_bytes = 5 * (D / 64) * kSt5Half + 1024;
     static SmemLimit limit;
     cudaError_t e = limit.raise((const void *)kern, tiles_bytes + (size_t)kSparseTc05MaxPages * 12);
     if (e != cudaSuccess) return e;
@@ -434,21 +437,26 @@ static cudaError_t launch_st5(const SparseParams &sp, const CUtensorMap &tmq, co
         launch_regs.store(regs, std::memory_order_relaxed);
     }
     if (regs * kSt5Threads < 128 * (int)kSt5LoadRegs + 256 * (int)kSt5SoftmaxRegs) return cudaErrorInvalidConfiguration;
-    int ps_shift = 0, g_shift = 0;
+    int ps_shift = 0;
     while ((1 << ps_shift) < p.ps) ++ps_shift;
-    while ((1 << g_shift) < p.G) ++g_shift;
-    const long long units = count_tiles(sp, 128 >> g_shift) * p.Hkv;
+    const int TPC = sparse_tile_tokens(p.G);
+    const long long units = count_tiles(sp, TPC) * p.Hkv;
     if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
     kern<<<(unsigned)units, kSt5Threads, tiles_bytes + (size_t)p.W * 12, stream>>>(
-        tmq, tmk, tmv, sp, ps_shift, g_shift, tc05::idesc_f16(bf, false, 128, 128), tc05::idesc_f16(bf, true, 128, 128));
+        tmq, tmk, tmv, sp, ps_shift, TPC, tc05::idesc_f16(bf, false, 128, 128), tc05::idesc_f16(bf, true, 128, D));
     return cudaGetLastError();
 }
 
+int sparse_tile_tokens(int G) { return G > 128 ? 0 : 128 / G < kTileMaxTokens ? 128 / G : kTileMaxTokens; }
+
 cudaError_t launch_sparse_tc05(const SparseParams &sp, int dtype, const CUtensorMap &tmq, const CUtensorMap &tmk,
                                const CUtensorMap &tmv, cudaStream_t stream) {
-    return dtype == PA_BF16 ? launch_st5<__nv_bfloat16>(sp, tmq, tmk, tmv, stream)
-                            : launch_st5<__half>(sp, tmq, tmk, tmv, stream);
+    if (dtype == PA_BF16)
+        return sp.f.D == 64 ? launch_st5<__nv_bfloat16, 64>(sp, tmq, tmk, tmv, stream)
+                            : launch_st5<__nv_bfloat16, 128>(sp, tmq, tmk, tmv, stream);
+    return sp.f.D == 64 ? launch_st5<__half, 64>(sp, tmq, tmk, tmv, stream)
+                        : launch_st5<__half, 128>(sp, tmq, tmk, tmv, stream);
 }
 
 }  // namespace pa

@@ -114,21 +114,17 @@ struct SparseParams {
     const int32_t *sel;  // attention only: [n_tok, Hkv, K]
     long long n_tok;
     int K, sink, local;
-    int group_min;  // tokens of a sequence from which on the group kernel takes it (attention, packed batches)
+    int group_min;  // packed batches: sequences of so many tokens are the tcgen05 kernel's (0: none)
 };
 cudaError_t launch_select_pages(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
 // bf16/f16: tensor cores, a list's pages split over a cluster when there are few rows (sms: SM count)
 cudaError_t launch_sparse_mma(const SparseParams &p, int dtype, int sms, const CUtensorMap &tmk,
                               const CUtensorMap &tmv, cudaStream_t stream);
-// bf16/f16, head_dim 64/128, G <= 16: runs of a sequence's tokens that share page loads; at most
-// kSparseGroupMaxPages pages a sequence.  sparse_group_tokens: tokens of one CTA (0: not for this G).
-constexpr int kSparseGroupMaxPages = 8192;
-int sparse_group_tokens(int G);
-cudaError_t launch_sparse_group(const SparseParams &p, int dtype, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                                cudaStream_t stream);
-// The same on tcgen05: head_dim 128, G = 4 or 8 (tiles of 128 / G tokens), scale > 0, at most
-// kSparseTc05MaxPages pages a sequence.
+// bf16/f16, head_dim 64/128, G <= 128, scale > 0: runs of a sequence's tokens that share page loads, on
+// tcgen05; at most kSparseTc05MaxPages pages a sequence.  sparse_tile_tokens: tokens of one CTA (0: not for
+// this G).
 constexpr int kSparseTc05MaxPages = 4608;
+int sparse_tile_tokens(int G);
 cudaError_t launch_sparse_tc05(const SparseParams &p, int dtype, const CUtensorMap &tmq, const CUtensorMap &tmk,
                                const CUtensorMap &tmv, cudaStream_t stream);
 cudaError_t launch_sparse_simt(const SparseParams &p, cudaStream_t stream);  // f32

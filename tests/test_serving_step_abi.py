@@ -93,6 +93,20 @@ def test_sparse_refusals(lib, dims, kw, code):
                                      a["K"], a["factor"], a["out"], a["lse"], _ref(d), None) == code
 
 
+def test_sparse_kernel_choice(lib):
+    """Runs of many tokens share page loads; single tokens, short runs, f32, head_dim 256, scale <= 0, wide
+    tables and over 128 query heads to a kv head do not."""
+    f = lambda scale=0.1, K=64, sms=152, packed=1, **kw: lib.paged_attn_sparse_shares_pages(  # noqa: E731
+        _ref(_dims(**{**dict(batch=2, q_len=1024, num_q_heads=32, num_kv_heads=8, bt_stride=512), **kw})), packed, K,
+        scale, sms)
+    assert f() == 1 and f(dtype=pa.PA_F16) == 1 and f(packed=0) == 1
+    assert f(q_len=64) == 0 and f(batch=600) == 0 and f(packed=0, q_len=15, batch=300) == 0
+    assert f(dtype=pa.PA_F32) == 0 and f(head_dim=256) == 0 and f(scale=0.0) == 0 and f(scale=-1.0) == 0
+    assert f(bt_stride=4609, q_len=100000) == 0 and f(num_q_heads=129, num_kv_heads=1) == 0
+    assert f(K=0) == EINVAL and f(sms=0) == EINVAL and f(head_dim=96) == EUNSUP
+    assert lib.paged_attn_sparse_shares_pages(None, 1, 4, 0.1, 152) == EINVAL
+
+
 # ----------------------------------------------------------------------------- the binding's checks
 class FakeCuda:
     """Enough of a CUDA tensor for the binding's checks; its pointer is never read."""

@@ -423,47 +423,63 @@ def test_attend_few_rows_long_lists(pa):
             _check_attend(pa, b, _lists(b, 300))
 
 
-CHUNKS = [1, 70, 0, 16, 15, 1, 33]
-CHUNK_LENS = [90, 300, 5, 16, 700, 64, 33]
+# Runs of tokens long enough, with the lists below, for the kernel that reads the union of their lists.
+CHUNKS = [1, 230, 0, 16, 15, 1, 129]
+CHUNK_LENS = [90, 500, 5, 16, 700, 64, 129]
+
+
+def _shares(pa, b, K, uniform=False, scale=0.1):
+    import torch
+    code = {"bf16": pa.PA_BF16, "f16": pa.PA_F16, "f32": pa.PA_F32}[b.dtype]
+    B = len(b.q_lens)
+    return pa.paged_attn_sparse_shares_pages(B, b.T // B if uniform else b.T, b.Hq, b.Hkv, b.D, b.ps, b.width, K, scale,
+                                             torch.cuda.get_device_properties(0).multi_processor_count, code,
+                                             not uniform)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("Hq,Hkv,D,ps", [(8, 2, 128, 16), (4, 4, 64, 32), (14, 2, 64, 64), (16, 1, 128, 16),
-                                         (3, 1, 128, 64), (10, 2, 128, 32), (18, 1, 64, 16),
-                                         (8, 1, 128, 32), (16, 2, 128, 64), (4, 1, 128, 64)])
+                                         (3, 1, 128, 64), (10, 2, 128, 32), (18, 1, 64, 16), (8, 1, 128, 32),
+                                         (16, 2, 128, 64), (4, 1, 128, 64), (64, 1, 128, 16), (2, 2, 64, 16)])
 def test_attend_prompt_chunks(pa, dtype, Hq, Hkv, D, ps):
     """Runs of tokens whose lists are read together, beside short sequences in the same call."""
     b = R.Batch(Hq * D + ps, CHUNKS, CHUNK_LENS, Hq, Hkv, D, ps, dtype, q_pad=3)
-    for K in (1, 5, 14):
+    assert _shares(pa, b, 40)
+    for K in (1, 5, 40):
         _check_attend(pa, b, _lists(b, K))
     qo = [max(0, L - n - 7) for n, L in zip(CHUNKS, CHUNK_LENS)]
-    qo[4] = -6  # a chunk whose first tokens see nothing
-    _check_attend(pa, b, _lists(b, 5, q_offset=qo), q_offset=qo)
-    _check_attend(pa, b, _lists(b, 5, causal=False), causal=False)
+    qo[1] = -6  # a chunk whose first tokens see nothing
+    _check_attend(pa, b, _lists(b, 40, q_offset=qo), q_offset=qo)
+    _check_attend(pa, b, _lists(b, 40, causal=False), causal=False)
 
 
 def test_attend_prompt_chunks_uniform(pa):
-    for n in (8, 16, 50):
-        b = R.Batch(n, [n] * 3, [n, 200, 130], 8, 2, 128, 16, "bf16")
-        _check_attend(pa, b, _lists(b, 6), uniform=True)
-        _check_attend(pa, b, _lists(b, 6), uniform=True, scale=-0.2)
+    for n in (15, 16, 50, 64):
+        b = R.Batch(n, [n] * 8, [n, 200, 130, 180, 199, 64, 65, 66], 8, 2, 128, 16, "bf16")
+        assert _shares(pa, b, 13, True) == (n >= 16) and not _shares(pa, b, 13, True, -0.2)
+        _check_attend(pa, b, _lists(b, 13), uniform=True)
+        _check_attend(pa, b, _lists(b, 13), uniform=True, scale=-0.2)
+        _check_attend(pa, b, _lists(b, 13), uniform=True, scale=3.0)  # the row maximum moves far
 
 
 def test_attend_prompt_chunks_any_list(pa):
     """Repeated entries count again, in one tile of a chunk or in all; ids outside the pool read as zeros."""
     for dtype in ("bf16", "f16"):
         b = R.Batch(31, CHUNKS, CHUNK_LENS, 8, 2, 128, 16, dtype)
-        sel = _lists(b, 9)
+        assert _shares(pa, b, 40)
+        sel = _lists(b, 40)
         sel[40, 1, :4] = [2, 0, 2, 2]
-        sel[45, 0] = [-1, W.SENTINEL_MAX, -2**31, 1, 1, 99, 1, 0, -7]
+        sel[45, 0] = -7
+        sel[45, 0, :9] = [-1, W.SENTINEL_MAX, -2**31, 1, 1, 99, 1, 0, -7]
+        sel[300, 0] = -1
         _check_attend(pa, b, sel)
         assert pa.paged_attn_last_error_word() == 0
         sel[:, :, 1] = sel[:, :, 0]
         _check_attend(pa, b, sel)
         b.table[1, 2], b.table[4, 7] = b.P, -1
-        sel = _lists(b, 9, seed=3)
-        sel[:, :, 0] = 2
+        sel = _lists(b, 40, seed=3)
         sel[:, :, 1:][sel[:, :, 1:] == 2] = -1
+        sel[:, :, 0] = 2
         _check_attend(pa, b, sel)
         assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
 
@@ -472,30 +488,28 @@ def test_attend_prompt_chunks_non_finite(pa):
     """An infinity or a NaN in a key or a value reaches the rows that list its page and see its key, and
     no other row of the tile."""
     for dtype, inf, nan in (("bf16", 0x7F80, 0x7FC0), ("f16", 0x7C00, 0x7E00)):
-        b = R.Batch(32, [64], [200], 8, 2, 128, 16, dtype)
-        sel = np.zeros((64, 2, 3), np.int32)
-        sel[:] = [1, 4, 8]
+        b = R.Batch(32, [64] * 8, [200] * 8, 8, 2, 128, 16, dtype)
+        assert _shares(pa, b, 13, True)
+        sel = np.zeros((512, 2, 13), np.int32) - 1
+        sel[:, :, :3] = [1, 4, 8]
         sel[20:23, :, 1] = 6
         sel[30, 1, 1] = 5
-        clean = _run_attend(pa, b, sel)[0]
+        clean = _run_attend(pa, b, sel, uniform=True)[0]
         b.v[b.table[0, 6], 2, 0, 3] = nan
         b.k[b.table[0, 5], 7, 1, 9] = nan
-        b.v[b.table[0, 9], 10, 1, 64] = inf  # position 154: no token lists page 9
-        b.v[b.table[0, 8], 15, 0, 11] = inf  # position 143, below every token's 144 keys in page 8
-        sel[5, 0] = [1, 4, 9]                # token 5 sees positions up to 141: not page 9's
-        out = _run_attend(pa, b, sel)[0]
+        b.v[b.table[0, 9], 10, 1, 64] = inf  # position 154: no token of head 1 lists page 9
+        b.v[b.table[0, 8], 15, 0, 11] = inf  # position 143
+        sel[5, 0, :3] = [1, 4, 9]            # token 5 sees positions up to 141: no key of page 9
+        out = _run_attend(pa, b, sel, uniform=True)[0]
         bad = ~np.isfinite(out)
         want = np.zeros_like(bad)
         want[20:23, :4, 3] = True             # page 6, kv head 0, one column
         want[30, 4:, :] = True                # a NaN score: every column
-        want[7:, :4, 11] = True               # tokens that see position 143 (136 + 7)
+        want[7:64, :4, 11] = True             # tokens that see position 143 (136 + 7)
         np.testing.assert_array_equal(bad, want)
         same = ~want.any(-1)
         same[5, :4] = False
-        k, v = R.elems_to_f64(b.k, dtype), R.elems_to_f64(b.v, dtype)
-        rows = np.isfinite(out).all(-1)
         _gpu.assert_close(out[same], clean[same], dtype, "rows without them")
-        assert rows[~want.any(-1)].all()
 
 
 def test_attend_masks(pa):
