@@ -107,6 +107,7 @@ __device__ __forceinline__ void q_load16(const void *q, int dtype, long long i, 
 struct SelectPlan {
     int TT;    // query tokens of a CTA
     int Gp;    // columns of a token: G rounded up to a power of two (G <= 8), or all of them
+    int gs;    // its logarithm (TT > 1)
     int S;     // CTAs of a cluster
     int Wk;    // score stride of a token in shared memory
     int dtype; // of q
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kSelThreads, 4)
             const int groups = one_token ? (p.G + 7) / 8 : NT;
             for (int n = warp; n < groups; n += WPU) {
                 const int col = n * 8 + g;
-                const int tok = i0 + (one_token ? 0 : col / plan.Gp), hd = one_token ? col : col % plan.Gp;
+                const int tok = i0 + (one_token ? 0 : col >> plan.gs), hd = one_token ? col : col & (plan.Gp - 1);
                 unsigned a = 0;  // magnitudes order as their bits, infinities and NaNs on top
                 if (hd < p.G && tok < i1) {
                     const long long q0 = q_row_offset(p, (t0 + tok) * p.Hq + (long long)h * p.G + hd) + tq * 16;
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kSelThreads, 4)
 #pragma unroll
             for (int n = warp; n < NT; n += WPU) {
                 const int col = n * 8 + g;
-                const int tok = i0 + (one_token ? 0 : col / plan.Gp), hd = one_token ? col : col % plan.Gp;
+                const int tok = i0 + (one_token ? 0 : col >> plan.gs), hd = one_token ? col : col & (plan.Gp - 1);
                 const bool there = hd < heads && tok < i1;
                 // a non-finite query scores 0 everywhere
                 const unsigned bits = there ? s_amax[tok] : 0u;
@@ -409,6 +410,12 @@ __global__ void __launch_bounds__(kSelThreads, 4)
                 if (tq == 0) s_sub[col] = there ? -128.f / kTwo24 * sum : kNoHead;
             }
             sync();
+            // In a block of tokens a lane writes the scores of columns 8 n + 2 tq (the first of a token's,
+            // else none): token i0 + tok0 + n tok_step, while n tok_step < tok_left.
+            const int tok0 = one_token ? 0 : (2 * tq) >> plan.gs, tok_step = one_token ? 0 : 8 >> plan.gs;
+            const int tok_left = one_token || ((2 * tq) & (plan.Gp - 1)) ? 0 : i1 - i0 - tok0;
+            const int row_step = tok_step * plan.Wk;
+            float *s_mine = s_key + tok0 * plan.Wk + g;
             for (int tile = tile0 + warp; tile < tile1; tile += WPU) {
                 const int j0 = m0 + tile * 16 + g;
                 float cur_scale[2];
@@ -487,20 +494,19 @@ __global__ void __launch_bounds__(kSelThreads, 4)
                         for (int r = 0; r < 2; ++r) {
                             float x = acc[n][2 * r];
                             const float y = acc[n][2 * r + 1];
-                            const int j = j0 + r * 8;
-                            if (plan.Gp == 1) {
-                                const int tok = n * 8 + 2 * tq;
-                                if (j < m1) {
-                                    if (i0 + tok < i1) s_key[tok * plan.Wk + j - m0] = score_of(x, r);
-                                    if (i0 + tok + 1 < i1) s_key[(tok + 1) * plan.Wk + j - m0] = score_of(y, r);
+                            const bool store = j0 + r * 8 < m1 && n * tok_step < tok_left;
+                            float *dst = s_mine + n * row_step + tile * 16 + r * 8;
+                            if (plan.gs == 0) {
+                                if (store) {
+                                    dst[0] = score_of(x, r);
+                                    if (n * tok_step + 1 < tok_left) dst[plan.Wk] = score_of(y, r);
                                 }
                                 continue;
                             }
                             x = fmaxf(x, y);
-                            if (plan.Gp >= 4) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                            if (plan.Gp >= 8) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                            const int col = n * 8 + 2 * tq, tok = col / plan.Gp;
-                            if (col % plan.Gp == 0 && i0 + tok < i1 && j < m1) s_key[tok * plan.Wk + j - m0] = score_of(x, r);
+                            if (plan.gs >= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                            if (plan.gs >= 3) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                            if (store) dst[0] = score_of(x, r);
                         }
                     }
                 }
@@ -688,7 +694,7 @@ static cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, c
         plan.TT = 1;
     } else {
         plan.Gp = 1;
-        while (plan.Gp < p.G) plan.Gp *= 2;
+        while (plan.Gp < p.G) plan.Gp *= 2, ++plan.gs;
         // Prompt chunks: as many tokens a CTA as fill 32, 16 or 8 columns while their scores take at most
         // 64 KB and there is a CTA for every multiprocessor; a batch of mostly single tokens takes one.
         NT = 4;
