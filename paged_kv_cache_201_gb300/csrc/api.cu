@@ -806,7 +806,17 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
     sp.K = top_k;
     sp.sink = sink_pages;
     sp.local = local_pages;
-    return cuda_status(pa::launch_select_pages(sp, dims->dtype, device_sm_count(), static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Sequences with half a tile of query tokens or more go to the tcgen05 kernel; in a packed batch both
+    // kernels find theirs from q_start.
+    const int tile = pa::select_tile_tokens(dims->head_dim, sp.f.G, dims->bt_stride);
+    const bool runs = q_start ? n_tok >= 2 * (int64_t)dims->batch : dims->q_len >= (tile + 1) / 2;
+    if (tile > 0 && runs && n_tok >= (tile + 1) / 2) {
+        sp.group_min = (tile + 1) / 2;
+        rc = cuda_status(pa::launch_select_tc05(sp, dims->dtype, st));
+        if (rc != PA_OK || !q_start) return rc;
+    }
+    return cuda_status(pa::launch_select_pages(sp, dims->dtype, device_sm_count(), st));
 }
 
 int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,

@@ -327,12 +327,72 @@ def test_select_largest_scores(pa, D):
 
 
 @pytest.mark.parametrize("chunk", [64, 300, 700])
-@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (6, 2), (8, 2), (8, 1), (32, 8), (12, 1)])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (6, 2), (8, 2), (8, 1), (32, 8), (12, 1), (32, 1), (40, 1)])
 def test_select_prompt_chunks(pa, chunk, Hq, Hkv):
     """Prompt chunks beside single tokens: tokens that share a block, blocks that hold several sequences."""
     b = R.Batch(chunk + Hq, [chunk, 1, 0, 5, 1, 37], [chunk + 600, 900, 3, 5, 700, 200], Hq, Hkv, 64, 16, "bf16",
                 q_pad=3)
     _check_select(pa, b, 1, 2, 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(8, 2, 128, 16), (3, 1, 128, 32), (2, 2, 64, 64), (14, 2, 128, 16),
+                                         (16, 1, 64, 16), (8, 2, 256, 16)])
+def test_select_prompt_chunks_types(pa, dtype, Hq, Hkv, D, ps):
+    b = R.Batch(Hq + D, [130, 1, 40, 64], [40 * ps + 130, 900, 25 * ps, 64], Hq, Hkv, D, ps, dtype, q_pad=1)
+    for sink, local, K in [(1, 2, 8), (0, 0, 1), (2, 3, 5), (0, 0, 23)]:
+        _check_select(pa, b, sink, local, K)
+    _check_select(pa, b, 1, 2, 6, causal=False)
+    _check_select(pa, b, 1, 2, 6, q_offset=[-5, 100, 20 * ps, 3])
+
+
+def test_select_prompt_chunks_special(pa):
+    """Ties, marked pages, overflowing scores, zero and non-finite queries, ids outside the pool, the uniform
+    layout, for runs of tokens."""
+    b = R.Batch(3, [60] * 3, [1600, 1000, 700], 4, 2, 64, 16, "f32")
+    env, scale = b.envelopes()
+    same = np.broadcast_to(env[:1, :1], env.shape).copy()
+    _check_select(pa, b, 1, 1, 9, env=(same, np.ones_like(scale)))
+    marked = scale.copy()
+    marked[np.random.default_rng(0).uniform(size=scale.shape) < 0.1] = np.inf
+    _check_select(pa, b, 1, 1, 9, env=(env, marked), uniform=True)
+    _check_select(pa, b, 0, 0, 30, env=(env, np.where(np.isnan(scale), scale, np.float32(3e38))))
+    b.q[0] = 0
+    b.q[61, 1, 5] = np.nan
+    b.q[122, 3, 0] = np.inf
+    _check_select(pa, b, 0, 1, 9)
+    b.table[0, 3], b.table[1, 20], b.table[0, 30] = b.P, -1, W.SENTINEL_MAX
+    want = R.select(b.q64(), env, scale, b.table, b.rows(), 2, 16, 1, 2, 8)
+    np.testing.assert_array_equal(_run_select(pa, b, env, scale, 1, 2, 8), want)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_prompt_chunks_largest_scores(pa, D):
+    """The largest scores, that differ by one, for a run of tokens."""
+    b = R.Batch(D, [64], [200 * 16], 8, 2, D, 16, "bf16")
+    rng = np.random.default_rng(D)
+    sign = rng.choice([-1, 1], D)
+    b.q[:] = W.bf16_bits_rne(np.broadcast_to(3.0 * sign, b.q.shape).astype(np.float32))
+    env = np.broadcast_to(np.where(sign > 0, 127, -127).astype(np.int8), (b.P, b.Hkv, 2, D)).copy()
+    env[b.P // 2:] *= -1
+    for p in range(b.P):
+        d = rng.integers(0, D)
+        env[p, :, :, d] -= np.sign(env[p, :, :, d]) * np.int8(rng.integers(0, 3))
+    _check_select(pa, b, 1, 1, 30, env=(env, np.ones((b.P, b.Hkv), np.float32)))
+
+
+@pytest.mark.parametrize("pages,Hq", [(700, 8), (1500, 4), (3000, 16), (8000, 4)])
+def test_select_prompt_chunks_long(pa, pages, Hq):
+    """Runs of tokens behind long prefixes, many equal scores among them."""
+    rng = np.random.default_rng(pages)
+    b = R.Batch(pages, [70], [70], Hq, 2, 64, 16, "bf16")
+    b.seq_lens = np.array([pages * 16 - 3], np.int32)
+    b.width, b.P = pages, 2000
+    b.table = rng.integers(0, b.P, (1, pages)).astype(np.int32)
+    hi = rng.integers(-127, 128, (b.P, 2, 64)).astype(np.int8)
+    lo = np.minimum(hi, rng.integers(-127, 128, (b.P, 2, 64))).astype(np.int8)
+    _check_select(pa, b, 1, 2, 50, env=(np.stack([lo, hi], 2), rng.uniform(0.5, 1, (b.P, 2)).astype(np.float32)))
 
 
 @pytest.mark.parametrize("B,pages,K,ps", [(2, 4097, 64, 16), (1, 20000, 128, 16), (3, 1025, 100, 64),
