@@ -118,11 +118,17 @@ struct SparseParams {
 };
 // Runs of tokens of a sequence, scored with tcgen05: head_dim 64 / 128, G <= 32.  select_tile_tokens: tokens of
 // one CTA (0: not for this shape or table width).
-constexpr size_t kSelectTc05MaxSmem = 216 * 1024;  // next to 8.3 KB of static shared memory
+constexpr size_t kSelectTc05MaxSmem = 224 * 1024;
 size_t select_tc05_smem(int D, int N, int TT, int W);
 int select_tile_tokens(int D, int G, int W);
-cudaError_t launch_select_tc05(const SparseParams &p, int dtype, cudaStream_t stream);
-cudaError_t launch_select_pages(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_select_tc05(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_select_pages_64(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_select_pages_128(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_select_pages_256(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+inline cudaError_t launch_select_pages(const SparseParams &p, int dtype, int sms, cudaStream_t stream) {
+    return (p.f.D == 64 ? launch_select_pages_64 : p.f.D == 128 ? launch_select_pages_128 : launch_select_pages_256)(
+        p, dtype, sms, stream);
+}
 // bf16/f16: tensor cores, a list's pages split over a cluster when there are few rows (sms: SM count)
 cudaError_t launch_sparse_mma(const SparseParams &p, int dtype, int sms, const CUtensorMap &tmk,
                               const CUtensorMap &tmv, cudaStream_t stream);

@@ -24,26 +24,37 @@ struct Threshold {
     __device__ __forceinline__ bool at(float x) const { return !whole && x == cut; }
 };
 
-// The want-th largest of a row's scores, by bisection from a bracket: at least `want` scores reach lo,
-// fewer exceed hi, and both are scores of the row.  count(c): how many are >= c, in every thread.  The
-// values are bisected first; what is not found in 14 steps is found by bisection of the numbers between
-// (infinite scores).  It ends as soon as exactly `want` scores reach a candidate.
+// The want-th largest of a row's scores, by narrowing a bracket: `reach_lo` >= want scores reach lo,
+// `reach_hi` reach hi, fewer than want exceed it, and both are scores of the row.  count(c): how many are
+// >= c, in every thread.  Two of three steps interpolate between the counts, which takes some five steps
+// where the scores are spread smoothly; the third halves the values, and after 24 steps the numbers between
+// are halved (infinite scores, or a few very large ones).  It ends as soon as exactly `want` scores reach a
+// candidate.
 template <typename Count>
-__device__ __forceinline__ Threshold find_threshold(float lo, float hi, int want, Count count) {
-    unsigned kl = ordered(lo), kh = ordered(hi) + 1;  // want or more reach kl, fewer reach kh
+__device__ __forceinline__ Threshold find_threshold(float lo, float hi, int reach_lo, int reach_hi, int want,
+                                                    Count count) {
+    if (reach_hi >= want) return {hi, reach_hi == want};  // ties at the top, or exactly so many
+    unsigned kl = ordered(lo), kh = ordered(hi);  // want or more reach kl, fewer reach kh
+    float cl = (float)reach_lo, ch = (float)reach_hi;
+#pragma unroll 1
     for (int step = 0; kh - kl > 1; ++step) {
         unsigned k = kl + (kh - kl) / 2;
-        if (step < 14) {
-            const float mid = 0.5f * value_of(kl) + 0.5f * value_of(kh - 1);
+        if (step < 24) {
+            const float vl = value_of(kl), vh = value_of(kh);
+            const float part = step % 3 == 2 ? 0.5f : __fdividef(cl - (float)want, cl - ch);
+            const float mid = vl + part * (vh - vl);
             if (fabsf(mid) <= FLT_MAX) k = min(max(ordered(mid), kl + 1), kh - 1);
         }
         const float c = value_of(k);
         const int n = count(c);
         if (n == want) return {c, true};
-        if (n > want)
+        if (n > want) {
             kl = k;
-        else
+            cl = (float)n;
+        } else {
             kh = k;
+            ch = (float)n;
+        }
     }
     return {value_of(kl), false};
 }
@@ -77,50 +88,6 @@ __device__ __forceinline__ float score_at(const float *row, int n, int j) {
 __device__ __forceinline__ float warp_min(float x) { return value_of(__reduce_min_sync(0xffffffffu, ordered(x))); }
 __device__ __forceinline__ float warp_max(float x) { return value_of(__reduce_max_sync(0xffffffffu, ordered(x))); }
 
-// A row's scores sorted into equal parts of [lo, hi]; not decreasing in x, so the parts above the one that
-// holds the threshold are taken whole and only that part is searched further.
-struct Bins {
-    float lo, per;
-    int last;
-    __device__ __forceinline__ Bins(float lo_, float hi, int n) : lo(lo_), per((float)n / (hi - lo_)), last(n - 1) {}
-    __device__ __forceinline__ bool usable() const { return per > 0.f && per <= FLT_MAX; }  // a finite, wide range
-    __device__ __forceinline__ int of(float x) const { return min((int)((x - lo) * per), last); }
-};
-
-// The part that holds the want-th largest score, counted from the top by one warp: lane l holds the counts
-// of parts PL l .. PL l + PL - 1.  Returns its index, and how many scores lie in higher parts and in it.
-template <int PL>
-__device__ __forceinline__ int find_bin(const int (&c)[PL], int want, int lane, int &above, int &in) {
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) mine += c[i];
-    int from = mine;  // scores in this lane's parts and all higher lanes'
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_down_sync(0xffffffffu, from, o);
-        if (lane + o < 32) from += x;
-    }
-    const int owner = 31 - __clz((int)__ballot_sync(0xffffffffu, from >= want));  // the highest such lane
-    int up = from - mine, bin = 0, n = 0;
-    bool found = false;
-#pragma unroll
-    for (int i = PL - 1; i >= 0; --i) {
-        if (!found) {
-            bin = i;
-            n = c[i];
-            if (up + n >= want)
-                found = true;
-            else
-                up += n;
-        }
-    }
-    above = __shfl_sync(0xffffffffu, up, owner);
-    in = __shfl_sync(0xffffffffu, n, owner);
-    return owner * PL + __shfl_sync(0xffffffffu, bin, owner);
-}
-
-constexpr int kBinsPerLane = 4, kBins = 32 * kBinsPerLane;  // of one warp; a CTA's warps have four times as many
-
 // Writes the pages of 32 NK scores k (score i * 32 + lane of a run) that are taken: those above the
 // threshold and, while there are `ties` of them left in the row, those at it.  gt / eq: scores above / at it
 // before the run, moved on.
@@ -128,11 +95,20 @@ template <int NK>
 __device__ __forceinline__ void write_pages(const float (&k)[NK], Threshold thr, int ties, int &gt, int &eq, int base,
                                             int32_t *out, int lane) {
     const unsigned below = (1u << lane) - 1;
+    if (thr.whole) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const bool up = k[i] >= thr.cut;
+            const unsigned ups = __ballot_sync(0xffffffffu, up);
+            if (up) out[gt + __popc(ups & below)] = base + i * 32 + lane;
+            gt += __popc(ups);
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-        const bool up = thr.above(k[i]), at = thr.at(k[i]);
-        const unsigned ups = __ballot_sync(0xffffffffu, up);
-        const unsigned ats = thr.whole ? 0u : __ballot_sync(0xffffffffu, at);
+        const bool up = k[i] > thr.cut, at = k[i] == thr.cut;
+        const unsigned ups = __ballot_sync(0xffffffffu, up), ats = __ballot_sync(0xffffffffu, at);
         const int e = eq + __popc(ats & below);
         if (up || (at && e < ties)) out[gt + __popc(ups & below) + min(e, ties)] = base + i * 32 + lane;
         gt += __popc(ups);
@@ -140,12 +116,10 @@ __device__ __forceinline__ void write_pages(const float (&k)[NK], Threshold thr,
     }
 }
 
-// A token's selection by one warp, its scores in registers (n <= 32 NK); hist: kBins counters of the warp.
+// A token's selection by one warp, its scores in registers (n <= 32 NK).
 template <int NK>
-__device__ __forceinline__ void warp_select(const float *row, int n, int want, int base, int32_t *out, int *hist,
-                                            int lane) {
+__device__ __forceinline__ void warp_select(const float *row, int n, int want, int base, int32_t *out, int lane) {
     float k[NK], lo = INFINITY, hi = -INFINITY;
-    *reinterpret_cast<int4 *>(hist + lane * 4) = make_int4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
         k[i] = score_at(row, n, i * 32 + lane);
@@ -154,43 +128,17 @@ __device__ __forceinline__ void warp_select(const float *row, int n, int want, i
     }
     lo = warp_min(lo);
     hi = warp_max(hi);
-    const Bins bins(lo, hi, kBins);
-    bool done = false;
-    Threshold thr{lo, false};
-    if (bins.usable()) {
+    auto count = [&](float c) {
+        int s = 0;
 #pragma unroll
-        for (int i = 0; i < NK; ++i)
-            if (i * 32 + lane < n) atomicAdd(hist + bins.of(k[i]), 1);
-        __syncwarp();
-        const int4 h = *reinterpret_cast<const int4 *>(hist + lane * 4);
-        const int c[4] = {h.x, h.y, h.z, h.w};
-        int above, in;
-        const int bin = find_bin<4>(c, want, lane, above, in);
-        lo = INFINITY;
-        hi = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NK; ++i)
-            if (i * 32 + lane < n && bins.of(k[i]) == bin) {
-                lo = fminf(lo, k[i]);
-                hi = fmaxf(hi, k[i]);
-            }
-        lo = warp_min(lo);
-        hi = warp_max(hi);
-        done = above + in == want;
-        if (done) thr = {lo, true};
-        __syncwarp();  // before the counters are cleared for another row
-    }
-    if (!done)
-        thr = find_threshold(lo, hi, want, [&](float c) {
-            int s = 0;
-#pragma unroll
-            for (int i = 0; i < NK; ++i) s += k[i] >= c;
-            return (int)__reduce_add_sync(0xffffffffu, s);
-        });
+        for (int i = 0; i < NK; ++i) s += k[i] >= c;
+        return (int)__reduce_add_sync(0xffffffffu, s);
+    };
+    const Threshold thr = find_threshold(lo, hi, n, count(hi), want, count);
     int up = 0;
     if (!thr.whole) {
 #pragma unroll
-        for (int i = 0; i < NK; ++i) up += thr.above(k[i]);
+        for (int i = 0; i < NK; ++i) up += k[i] > thr.cut;
         up = __reduce_add_sync(0xffffffffu, up);
     }
     int gt = 0, eq = 0;
@@ -198,10 +146,8 @@ __device__ __forceinline__ void warp_select(const float *row, int n, int want, i
 }
 
 // The same for a row of any length, its scores read from shared memory in every pass.
-__device__ __forceinline__ void warp_select_long(const float *row, int n, int want, int base, int32_t *out, int *hist,
-                                                 int lane) {
+__device__ __forceinline__ void warp_select_long(const float *row, int n, int want, int base, int32_t *out, int lane) {
     float lo = INFINITY, hi = -INFINITY;
-    *reinterpret_cast<int4 *>(hist + lane * 4) = make_int4(0, 0, 0, 0);
 #pragma unroll 8
     for (int j = lane; j < n; j += 32) {
         lo = fminf(lo, row[j]);
@@ -209,42 +155,17 @@ __device__ __forceinline__ void warp_select_long(const float *row, int n, int wa
     }
     lo = warp_min(lo);
     hi = warp_max(hi);
-    const Bins bins(lo, hi, kBins);
-    bool done = false;
-    Threshold thr{lo, false};
-    if (bins.usable()) {
+    auto count = [&](float c) {
+        int s = 0;
 #pragma unroll 8
-        for (int j = lane; j < n; j += 32) atomicAdd(hist + bins.of(row[j]), 1);
-        __syncwarp();
-        const int4 h = *reinterpret_cast<const int4 *>(hist + lane * 4);
-        const int c[4] = {h.x, h.y, h.z, h.w};
-        int above, in;
-        const int bin = find_bin<4>(c, want, lane, above, in);
-        lo = INFINITY;
-        hi = -INFINITY;
-#pragma unroll 8
-        for (int j = lane; j < n; j += 32)
-            if (bins.of(row[j]) == bin) {
-                lo = fminf(lo, row[j]);
-                hi = fmaxf(hi, row[j]);
-            }
-        lo = warp_min(lo);
-        hi = warp_max(hi);
-        done = above + in == want;
-        if (done) thr = {lo, true};
-        __syncwarp();  // before the counters are cleared for another row
-    }
-    if (!done)
-        thr = find_threshold(lo, hi, want, [&](float c) {
-            int s = 0;
-#pragma unroll 8
-            for (int j = lane; j < n; j += 32) s += row[j] >= c;
-            return (int)__reduce_add_sync(0xffffffffu, s);
-        });
+        for (int j = lane; j < n; j += 32) s += row[j] >= c;
+        return (int)__reduce_add_sync(0xffffffffu, s);
+    };
+    const Threshold thr = find_threshold(lo, hi, n, count(hi), want, count);
     int up = 0;
     if (!thr.whole) {
 #pragma unroll 8
-        for (int j = lane; j < n; j += 32) up += thr.above(row[j]);
+        for (int j = lane; j < n; j += 32) up += row[j] > thr.cut;
         up = __reduce_add_sync(0xffffffffu, up);
     }
     int gt = 0, eq = 0;

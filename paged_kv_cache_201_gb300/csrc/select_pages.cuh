@@ -15,11 +15,13 @@
 //
 // One cluster of S CTAs = one kv head and TT consecutive query tokens (1 in a decode batch; up to 32 / G
 // in prompt chunks, whose tokens read the same envelopes).  Its pages are shared out to the CTAs; their
-// scores meet in the first CTA's shared memory, which finds each token's threshold by bisection and
+// scores meet in the first CTA's shared memory, which finds each token's threshold by narrowing a bracket and
 // writes the pages above it in order.  Where there are
 // enough rows to fill the GPU with single warps, a warp takes a row by itself (WPU = 1): its latencies
 // (lengths, table, envelopes, bisection) then overlap with other rows' instead of holding three idle
 // warps at barriers.
+#pragma once
+
 #include "select_common.cuh"
 
 namespace pa {
@@ -27,7 +29,8 @@ namespace pa {
 namespace {
 
 constexpr int kSelWarps = 4;
-constexpr int kSelThreads = kSelWarps * 32;
+template <int WPU>
+constexpr int kSelCtaWarps = WPU > kSelWarps ? WPU : kSelWarps;  // of a CTA whose rows take WPU warps each
 constexpr int kRowWarps = 1;           // of a row, where rows fill the GPU
 constexpr int kSelMaxTokens = 32;      // of one CTA
 constexpr int kWarpSelectPages = 1024;  // longest row a warp of its own selects from
@@ -41,6 +44,50 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 
+// A row's scores sorted into equal parts of [lo, hi]; not decreasing in x, so the parts above the one that
+// holds the threshold are taken whole and only that part is searched further.
+struct Bins {
+    float lo, per;
+    int last;
+    __device__ __forceinline__ Bins(float lo_, float hi, int n) : lo(lo_), per((float)n / (hi - lo_)), last(n - 1) {}
+    __device__ __forceinline__ bool usable() const { return per > 0.f && per <= FLT_MAX; }  // a finite, wide range
+    __device__ __forceinline__ int of(float x) const { return min((int)((x - lo) * per), last); }
+};
+
+// The part that holds the want-th largest score, counted from the top by one warp: lane l holds the counts
+// of parts PL l .. PL l + PL - 1.  Returns its index, and how many scores lie in higher parts and in it.
+template <int PL>
+__device__ __forceinline__ int find_bin(const int (&c)[PL], int want, int lane, int &above, int &in) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) mine += c[i];
+    int from = mine;  // scores in this lane's parts and all higher lanes'
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_down_sync(0xffffffffu, from, o);
+        if (lane + o < 32) from += x;
+    }
+    const int owner = 31 - __clz((int)__ballot_sync(0xffffffffu, from >= want));  // the highest such lane
+    int up = from - mine, bin = 0, n = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = PL - 1; i >= 0; --i) {
+        if (!found) {
+            bin = i;
+            n = c[i];
+            if (up + n >= want)
+                found = true;
+            else
+                up += n;
+        }
+    }
+    above = __shfl_sync(0xffffffffu, up, owner);
+    in = __shfl_sync(0xffffffffu, n, owner);
+    return owner * PL + __shfl_sync(0xffffffffu, bin, owner);
+}
+
+constexpr int kBins = 512;
+
 struct SelectPlan {
     int TT;    // query tokens of a CTA
     int Gp;    // columns of a token: G rounded up to a power of two (G <= 8), or all of them
@@ -53,19 +100,19 @@ struct SelectPlan {
 }  // namespace
 
 template <int D, int NT, int WPU>
-__global__ void __launch_bounds__(kSelThreads, 4)
+__global__ void __launch_bounds__(kSelCtaWarps<WPU> * 32, 16 / kSelCtaWarps<WPU>)
     paged_attn_select_kernel(const SparseParams sp, const SelectPlan plan) {
     constexpr int KS = 2 * D / 16;  // k steps of a page's envelope
     constexpr int NC = 2 * D / 64;  // 16-byte loads of a lane and page
     constexpr int COLS = 8 * NT;
     const FwdParams &p = sp.f;
-    constexpr int UNITS = kSelWarps / WPU;  // of a CTA
+    constexpr int UNITS = kSelCtaWarps<WPU> / WPU;  // of a CTA
     extern __shared__ __align__(16) uint8_t sm_raw[];
     __shared__ __align__(8) float s_sub_[UNITS][COLS];  // -128 2^-24 sum_d q of a column, or kNoHead
     __shared__ int s_seq_[UNITS][kSelMaxTokens], s_reach_[UNITS][kSelMaxTokens];
     __shared__ unsigned s_amax_[UNITS][kSelMaxTokens];  // bits of the largest |q| of each token's group
-    __shared__ int s_red[2][kSelWarps][2];
-    __shared__ __align__(16) int s_hist[kSelWarps][kBins];
+    __shared__ int s_red[2][WPU][2];
+    __shared__ __align__(16) int s_hist[kBins];
     const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
     const int warp = wi % WPU, tid = warp * 32 + lane;  // within the unit
     constexpr int kThreads = WPU * 32;
@@ -74,7 +121,7 @@ __global__ void __launch_bounds__(kSelThreads, 4)
     auto sync = [me] {
         if (WPU == 1)
             __syncwarp();
-        else if (WPU < kSelWarps)
+        else if (UNITS > 1)
             named_bar_sync(1 + me, kThreads);
         else
             __syncthreads();
@@ -357,20 +404,18 @@ __global__ void __launch_bounds__(kSelThreads, 4)
                 const float *row = s_key + (i - i0) * plan.Wk;
                 if (want == 0 || n > kWarpSelectPages) continue;
                 if (n <= 256)
-                    warp_select<8>(row, n, want, sp.sink, out + sp.sink, s_hist[wi], lane);
+                    warp_select<8>(row, n, want, sp.sink, out + sp.sink, lane);
                 else if (n <= 512)
-                    warp_select<16>(row, n, want, sp.sink, out + sp.sink, s_hist[wi], lane);
+                    warp_select<16>(row, n, want, sp.sink, out + sp.sink, lane);
                 else
-                    warp_select<kWarpSelectPages / 32>(row, n, want, sp.sink, out + sp.sink, s_hist[wi], lane);
+                    warp_select<kWarpSelectPages / 32>(row, n, want, sp.sink, out + sp.sink, lane);
             }
             // longer rows: the CTA counts and writes them together
-            for (int i = i0; WPU == kSelWarps && i < i1 && want > 0; ++i) {
+            for (int i = i0; UNITS == 1 && i < i1 && want > 0; ++i) {
                 const int np = (s_reach[i] + p.ps - 1) / p.ps, n = np - sp.local - sp.sink;
                 if (np <= sp.K || n <= kWarpSelectPages) continue;
                 const float *row = s_key + (i - i0) * plan.Wk;
-                int *hist = s_hist[0];  // all the warps' counters as one
-                constexpr int BINS = kBins * kSelWarps;
-                for (int j = tid; j < BINS; j += kThreads) hist[j] = 0;
+                for (int j = tid; j < kBins; j += kThreads) s_hist[j] = 0;
                 int turn = 0;  // two sets of partial results: one barrier an exchange
                 auto exchange = [&](int x, int y) {
                     if (lane == 0) s_red[turn][warp][0] = x, s_red[turn][warp][1] = y;
@@ -399,20 +444,21 @@ __global__ void __launch_bounds__(kSelThreads, 4)
                     hi = fmaxf(hi, row[j]);
                 }
                 range(lo, hi);
-                const Bins bins(lo, hi, BINS);
+                const Bins bins(lo, hi, kBins);
                 bool done = false;
+                int reach_lo = n;  // scores that reach lo
                 Threshold thr{lo, false};
                 if (bins.usable()) {
 #pragma unroll 4
-                    for (int j = tid; j < n; j += kThreads) atomicAdd(hist + bins.of(row[j]), 1);
+                    for (int j = tid; j < n; j += kThreads) atomicAdd(s_hist + bins.of(row[j]), 1);
                     sync();
-                    int c[BINS / 32], above, in;
+                    int c[kBins / 32], above, in;
 #pragma unroll
-                    for (int k = 0; k < BINS / 32; k += 4) {
-                        const int4 x = *reinterpret_cast<const int4 *>(hist + lane * (BINS / 32) + k);
+                    for (int k = 0; k < kBins / 32; k += 4) {
+                        const int4 x = *reinterpret_cast<const int4 *>(s_hist + lane * (kBins / 32) + k);
                         c[k] = x.x, c[k + 1] = x.y, c[k + 2] = x.z, c[k + 3] = x.w;
                     }
-                    const int bin = find_bin<BINS / 32>(c, want, lane, above, in);
+                    const int bin = find_bin<kBins / 32>(c, want, lane, above, in);
                     lo = INFINITY;
                     hi = -INFINITY;
 #pragma unroll 4
@@ -422,16 +468,19 @@ __global__ void __launch_bounds__(kSelThreads, 4)
                             hi = fmaxf(hi, row[j]);
                         }
                     range(lo, hi);
-                    done = above + in == want;
+                    reach_lo = above + in;
+                    done = reach_lo == want;
                     if (done) thr = {lo, true};
                 }
-                if (!done)
-                    thr = find_threshold(lo, hi, want, [&](float c) {
+                if (!done) {
+                    auto count = [&](float c) {
                         int s = 0;
 #pragma unroll 4
                         for (int j = tid; j < n; j += kThreads) s += row[j] >= c;
                         return total(s);
-                    });
+                    };
+                    thr = find_threshold(lo, hi, reach_lo, count(hi), want, count);
+                }
                 // each warp a run of scores, after counting the runs before it
                 const int run = (n + WPU * 128 - 1) / (WPU * 128) * 128, a = min(warp * run, n), e = min(a + run, n);
                 int gt = 0, eq = 0;
@@ -472,16 +521,17 @@ static cudaError_t launch_select_t(const SparseParams &sp, const SelectPlan &pla
     auto kern = paged_attn_select_kernel<D, NT, WPU>;
     const size_t frag = (size_t)(2 * D / 16) * NT * 32 * sizeof(uint2);
     static SmemLimit limit;
-    const size_t most = WPU < kSelWarps ? kSelWarps / WPU * (frag + kWarpSelectPages * 4) : frag + (size_t)PA_SELECT_MAX_PAGES * 4;
+    constexpr int UNITS = kSelCtaWarps<WPU> / WPU;
+    const size_t most = UNITS > 1 ? UNITS * (frag + kWarpSelectPages * 4) : frag + (size_t)PA_SELECT_MAX_PAGES * 4;
     const cudaError_t e = limit.raise((const void *)kern, most);
     if (e != cudaSuccess) return e;
     const long long rows = (sp.n_tok + plan.TT - 1) / plan.TT * sp.f.Hkv;
-    const long long units = (rows + kSelWarps / WPU - 1) / (kSelWarps / WPU);  // clusters
+    const long long units = (rows + UNITS - 1) / UNITS;  // clusters
     if (units * plan.S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * plan.S));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = kSelWarps / WPU * (frag + (size_t)plan.TT * plan.Wk * 4);
+    cfg.blockDim = dim3(kSelCtaWarps<WPU> * 32);
+    cfg.dynamicSmemBytes = UNITS * (frag + (size_t)plan.TT * plan.Wk * 4);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -493,7 +543,7 @@ static cudaError_t launch_select_t(const SparseParams &sp, const SelectPlan &pla
 }
 
 template <int D>
-static cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, cudaStream_t stream) {
+cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, cudaStream_t stream) {
     const FwdParams &p = sp.f;
     SelectPlan plan{};
     plan.dtype = dtype;
@@ -529,15 +579,15 @@ static cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, c
         return NT == 1 ? launch_select_t<D, 1, kRowWarps>(sp, plan, stream) : launch_select_t<D, 2, kRowWarps>(sp, plan, stream);
     // Few rows: a cluster shares their pages, each CTA at least two tiles for each of its warps.
     while (plan.S < 8 && rows * plan.S * 2 <= 2ll * sms && p.W >= plan.S * 2 * 2 * kSelWarps * 16) plan.S *= 2;
+    // Long rows on few CTAs: twice the warps.
+    if (rows * plan.S <= sms && p.W > 1024) {
+        if (NT == 1) return launch_select_t<D, 1, 8>(sp, plan, stream);
+        if (NT == 2) return launch_select_t<D, 2, 8>(sp, plan, stream);
+        return launch_select_t<D, 4, 8>(sp, plan, stream);
+    }
     if (NT == 1) return launch_select_t<D, 1, kSelWarps>(sp, plan, stream);
     if (NT == 2) return launch_select_t<D, 2, kSelWarps>(sp, plan, stream);
     return launch_select_t<D, 4, kSelWarps>(sp, plan, stream);
-}
-
-cudaError_t launch_select_pages(const SparseParams &sp, int dtype, int sms, cudaStream_t stream) {
-    if (sp.f.D == 64) return launch_select_d<64>(sp, dtype, sms, stream);
-    if (sp.f.D == 128) return launch_select_d<128>(sp, dtype, sms, stream);
-    return launch_select_d<256>(sp, dtype, sms, stream);
 }
 
 }  // namespace pa

@@ -56,12 +56,11 @@ __global__ void __launch_bounds__(kSelTcThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_reach[kTileMaxTokens];
     __shared__ unsigned s_amax[kTileMaxTokens];
-    __shared__ __align__(16) int s_hist[kSelTcWarps][kBins];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.Hkv;
     TokenTile x;
     if (!token_tile(sp, blockIdx.x / p.Hkv, TT, x)) return;
-    const int N = TT * Gp;
+    const int N = (TT * Gp + 15) / 16 * 16;  // columns; those past the tokens' are never read out
     if (tid < x.nt) s_reach[tid] = row_key_limit(p, x.b, x.L, x.i0 + tid, x.n_seq);
     if (tid < kTileMaxTokens) s_amax[tid] = 0u;
     const int reach_max = row_key_limit(p, x.b, x.L, x.i0 + x.nt - 1, x.n_seq);  // grows with the token
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(kSelTcThreads, 1)
     const int group = warp >> 2;  // of 32 columns
     // Read tile t out of tensor memory: this thread's page, 32 columns.
     auto read_out = [&](int t) {
-        if (group * 32 >= N || bad) return;
+        if (group * 32 >= TT * Gp || bad) return;
         uint32_t u[32];
         tc05::ld_32cols(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((t & 1) * 128 + group * 32), u);
         tc05::wait_ld();
@@ -267,11 +266,11 @@ __global__ void __launch_bounds__(kSelTcThreads, 1)
         if (want == 0) continue;
         const float *row = s_score + i * Wk;
         if (n <= 256)
-            warp_select<8>(row, n, want, sp.sink, out + sp.sink, s_hist[warp], lane);
+            warp_select<8>(row, n, want, sp.sink, out + sp.sink, lane);
         else if (n <= 512)
-            warp_select<16>(row, n, want, sp.sink, out + sp.sink, s_hist[warp], lane);
+            warp_select<16>(row, n, want, sp.sink, out + sp.sink, lane);
         else
-            warp_select_long(row, n, want, sp.sink, out + sp.sink, s_hist[warp], lane);
+            warp_select_long(row, n, want, sp.sink, out + sp.sink, lane);
     }
 }
 
@@ -284,7 +283,7 @@ static cudaError_t launch_select_tc05_t(const SparseParams &sp, int dtype, int T
     const int Wk = (sp.f.W + 3) / 4 * 4;
     const long long units = count_tiles(sp, TT) * sp.f.Hkv;
     if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kern<<<(unsigned)units, kSelTcThreads, select_tc05_smem(D, TT << GS, TT, sp.f.W), stream>>>(sp, dtype, TT, Wk);
+    kern<<<(unsigned)units, kSelTcThreads, select_tc05_smem(D, ((TT << GS) + 15) / 16 * 16, TT, sp.f.W), stream>>>(sp, dtype, TT, Wk);
     return cudaGetLastError();
 }
 
@@ -305,10 +304,19 @@ int select_tile_tokens(int D, int G, int W) {
     return 0;
 }
 
-cudaError_t launch_select_tc05(const SparseParams &sp, int dtype, cudaStream_t stream) {
+cudaError_t launch_select_tc05(const SparseParams &sp, int dtype, int sms, cudaStream_t stream) {
     int GS = 0;
     while ((1 << GS) < sp.f.G) ++GS;
-    const int TT = select_tile_tokens(sp.f.D, sp.f.G, sp.f.W);
+    // One CTA an SM, and its time grows with its tokens: the tile that makes whole waves of them (936 tokens
+    // of 8 kv heads: 25 tokens in two waves instead of 32 in 1.6).
+    const int most = select_tile_tokens(sp.f.D, sp.f.G, sp.f.W);
+    int TT = most;
+    long long best = 0;
+    for (int t = most; 2 * t > most; --t) {
+        const long long tiles = sp.f.q_start ? (sp.n_tok + t - 1) / t : (long long)sp.f.B * ((sp.f.Sq + t - 1) / t);
+        const long long cost = (tiles * sp.f.Hkv + sms - 1) / sms * (t + 8);  // the set-up weighs as 8 tokens
+        if (!best || cost < best) best = cost, TT = t;
+    }
     auto pick = [&](auto d) {
         constexpr int D = decltype(d)::value;
         switch (GS) {

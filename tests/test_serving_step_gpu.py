@@ -367,6 +367,71 @@ def test_select_prompt_chunks_special(pa):
     assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
 
 
+def _long_runs(seed, q_lens, pages, Hq, Hkv, D, dtype, q_pad=2):
+    """Runs of tokens behind long prefixes over a small pool (many equal scores): at least 2^23 (token, query
+    head, page) scores, which is where the tcgen05 kernel takes them."""
+    assert sum(q_lens) * Hq * pages >= 1 << 23
+    rng = np.random.default_rng(seed)
+    b = R.Batch(seed, q_lens, q_lens, Hq, Hkv, D, 16, dtype, q_pad=q_pad)
+    short = rng.integers(0, 3, len(q_lens))
+    b.seq_lens = np.asarray([pages * 16 - int(x) * 37 - int(rng.integers(0, 16)) for x in short], np.int32)
+    b.width, b.P = pages, 600
+    b.table = rng.integers(0, b.P, (len(q_lens), pages)).astype(np.int32)
+    hi = rng.integers(-127, 128, (b.P, Hkv, D)).astype(np.int8)
+    lo = np.minimum(hi, rng.integers(-127, 128, (b.P, Hkv, D))).astype(np.int8)
+    return b, (np.stack([lo, hi], 2), rng.uniform(0.5, 1, (b.P, Hkv)).astype(np.float32))
+
+
+@pytest.mark.parametrize("q_lens,pages,Hq,Hkv,D,dtype", [
+    ([2000, 1, 900, 700], 600, 4, 1, 128, "bf16"), ([500, 0, 460, 1], 1100, 8, 2, 64, "f16"),
+    ([130, 1, 130], 2100, 16, 1, 128, "f32"), ([2000, 1, 1150], 900, 3, 1, 64, "bf16"),
+    ([290], 1500, 20, 1, 128, "f16"), ([3300], 1300, 2, 2, 64, "bf16"), ([380], 700, 32, 1, 64, "bf16"),
+    ([90, 15, 16, 2], 4300, 16, 2, 64, "bf16"), ([1000, 30], 600, 14, 2, 128, "bf16")])
+def test_select_long_runs(pa, q_lens, pages, Hq, Hkv, D, dtype):
+    b, env = _long_runs(pages, q_lens, pages, Hq, Hkv, D, dtype)
+    _check_select(pa, b, 1, 2, 40, env=env)
+    _check_select(pa, b, 0, 0, 3, env=env)
+
+
+def test_select_long_runs_special(pa):
+    """Ties, marked pages, overflowing scores, zero and non-finite queries, no scored page, non-causal, the
+    uniform layout, ids outside the pool."""
+    b, (env, scale) = _long_runs(1, [700, 700], 800, 8, 2, 64, "f32", q_pad=0)
+    b.q[0] = 0
+    b.q[61, 1, 5] = np.nan
+    b.q[722, 3, 0] = np.inf
+    _check_select(pa, b, 0, 1, 9, env=(env, scale))
+    _check_select(pa, b, 3, 6, 9, env=(env, scale))
+    _check_select(pa, b, 1, 1, 9, env=(env, scale), causal=False)
+    _check_select(pa, b, 1, 1, 9, env=(env, scale), uniform=True)
+    _check_select(pa, b, 1, 1, 9, env=(env, scale), q_offset=[-300, 90])
+    same = np.broadcast_to(env[:1, :1], env.shape).copy()
+    _check_select(pa, b, 1, 1, 9, env=(same, np.ones_like(scale)))
+    marked = scale.copy()
+    marked[np.random.default_rng(0).uniform(size=scale.shape) < 0.1] = np.inf
+    _check_select(pa, b, 1, 1, 9, env=(env, marked))
+    _check_select(pa, b, 0, 0, 30, env=(env, np.full_like(scale, 3e38)))
+    b.table[0, 3], b.table[1, 20], b.table[0, 130] = b.P, -1, W.SENTINEL_MAX
+    want = R.select(b.q64(), env, scale, b.table, b.rows(), 2, 16, 1, 2, 8)
+    np.testing.assert_array_equal(_run_select(pa, b, env, scale, 1, 2, 8)[:b.T], want)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_long_runs_largest_scores(pa, D):
+    """The largest scores, that differ by one, for a run of tokens."""
+    b, (env, _) = _long_runs(D, [1400], 800, 8, 2, D, "bf16")
+    rng = np.random.default_rng(D)
+    sign = rng.choice([-1, 1], D)
+    b.q[:] = W.bf16_bits_rne(np.broadcast_to(3.0 * sign, b.q.shape).astype(np.float32))
+    env[:] = np.where(sign > 0, 127, -127).astype(np.int8)
+    env[b.P // 2:] *= -1
+    for p in range(b.P):
+        d = rng.integers(0, D)
+        env[p, :, :, d] -= np.sign(env[p, :, :, d]) * np.int8(rng.integers(0, 3))
+    _check_select(pa, b, 1, 1, 30, env=(env, np.ones((b.P, b.Hkv), np.float32)))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_select_prompt_chunks_largest_scores(pa, D):
     """The largest scores, that differ by one, for a run of tokens."""
