@@ -817,8 +817,9 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
     if (tile > 0 && runs && n_tok >= (tile + 1) / 2 &&
         (double)n_tok * dims->num_q_heads * dims->bt_stride >= (double)(1 << 23)) {
         sp.group_min = (tile + 1) / 2;
+        sp.by_seq = q_start && (int64_t)dims->batch * (sp.group_min - 1) < n_tok;
         rc = cuda_status(pa::launch_select_tc05(sp, dims->dtype, device_sm_count(), st));
-        if (rc != PA_OK || !q_start) return rc;
+        if (rc != PA_OK || !q_start || sp.group_min <= 1) return rc;  // no shorter run
     }
     return cuda_status(pa::launch_select_pages(sp, dims->dtype, device_sm_count(), st));
 }
@@ -851,12 +852,13 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
     // their tokens' lists; in a packed batch both kernels find their sequences from q_start.
     if (sparse_shares_pages(dims, n_tok, q_start != nullptr, top_k, scale, device_sm_count())) {
         sp.group_min = (pa::sparse_tile_tokens(dims->num_q_heads / dims->num_kv_heads) + 1) / 2;
+        sp.by_seq = q_start && (int64_t)dims->batch * (sp.group_min - 1) < n_tok;
         CUtensorMap tmq, tmk5, tmv5;
         if ((rc = make_sparse_q_map(&tmq, q, dims, n_tok)) != PA_OK) return rc;
         if ((rc = make_pool_map(&tmk5, k_cache, dims, 1)) != PA_OK) return rc;
         if ((rc = make_pool_map(&tmv5, v_cache, dims, 1)) != PA_OK) return rc;
         rc = cuda_status(pa::launch_sparse_tc05(sp, dims->dtype, tmq, tmk5, tmv5, st));
-        if (rc != PA_OK || !q_start) return rc;
+        if (rc != PA_OK || !q_start || sp.group_min <= 1) return rc;  // no shorter run
     }
     return cuda_status(pa::launch_sparse_mma(sp, dims->dtype, device_sm_count(), tmk, tmv, st));
 }

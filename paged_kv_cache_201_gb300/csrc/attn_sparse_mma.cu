@@ -76,9 +76,9 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
     const int kvh = unit % p.Hkv;
     unit /= p.Hkv;
     const int rt = unit % row_tiles;
-    const long long t_row = unit / row_tiles;
+    long long t_row = unit / row_tiles;
+    if (sp.by_seq && short_rows(sp, t_row, 1, t_row) == 0) return;  // the whole cluster: it has one token
     const TokenRow tr = token_row(p, t_row, sp.n_tok, threadIdx.x == 0);
-    // the whole cluster returns: it has one token
     if (tr.b < 0) return;
     if (sp.group_min && __ldg(p.q_start + tr.b + 1) - __ldg(p.q_start + tr.b) >= sp.group_min) return;
 
@@ -361,7 +361,7 @@ static cudaError_t launch_sparse_mma_t(const SparseParams &sp, int sms, const CU
     int ps_shift = 0;
     while ((1 << ps_shift) < p.ps) ++ps_shift;
     const int row_tiles = (p.G + 15) / 16;
-    const long long units = sp.n_tok * p.Hkv * row_tiles;
+    const long long units = (sp.by_seq ? short_blocks(sp, 1) : sp.n_tok) * p.Hkv * row_tiles;
     // Split a list over a cluster while its CTAs do not yet fill two per multiprocessor and each keeps
     // two stages of its own.
     const long long stages = ((long long)sp.K * p.ps + kMmaTileKeys - 1) / kMmaTileKeys;

@@ -115,6 +115,7 @@ struct SparseParams {
     long long n_tok;
     int K, sink, local;
     int group_min;  // packed batches: sequences of so many tokens are the tcgen05 kernel's (0: none)
+    int by_seq;     // the other kernel's units are group_min - 1 tokens of every sequence, not the rows of q
 };
 // Runs of tokens of a sequence, scored with tcgen05: head_dim 64 / 128, G <= 32.  select_tile_tokens: tokens of
 // one CTA (0: not for this shape or table width).

@@ -135,9 +135,15 @@ __global__ void __launch_bounds__(kSelCtaWarps<WPU> * 32, 16 / kSelCtaWarps<WPU>
     const int S = plan.S, rank = blockIdx.x % S;
     const long long unit = (long long)(blockIdx.x / S) * UNITS + me;
     const int h = (int)(unit % p.Hkv);
-    const long long t0 = unit / p.Hkv * plan.TT;
-    if (t0 >= sp.n_tok) return;  // a warp of its own without a row (WPU = 1)
-    const int nt_tok = (int)min((long long)plan.TT, sp.n_tok - t0);
+    long long t0 = unit / p.Hkv * plan.TT;
+    if (!sp.by_seq && t0 >= sp.n_tok) return;  // a warp of its own without a row
+    int nt_tok = 0;
+    if (sp.by_seq) {
+        nt_tok = short_rows(sp, unit / p.Hkv, plan.TT, t0);
+        if (nt_tok == 0) return;  // the whole cluster: it has these tokens
+    } else {
+        nt_tok = (int)min((long long)plan.TT, sp.n_tok - t0);
+    }
     // a peer's shared memory may be written only once it runs
     if (S > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     if (tid < nt_tok) {
@@ -525,7 +531,7 @@ static cudaError_t launch_select_t(const SparseParams &sp, const SelectPlan &pla
     const size_t most = UNITS > 1 ? UNITS * (frag + kWarpSelectPages * 4) : frag + (size_t)PA_SELECT_MAX_PAGES * 4;
     const cudaError_t e = limit.raise((const void *)kern, most);
     if (e != cudaSuccess) return e;
-    const long long rows = (sp.n_tok + plan.TT - 1) / plan.TT * sp.f.Hkv;
+    const long long rows = (sp.by_seq ? short_blocks(sp, plan.TT) : (sp.n_tok + plan.TT - 1) / plan.TT) * sp.f.Hkv;
     const long long units = (rows + UNITS - 1) / UNITS;  // clusters
     if (units * plan.S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
@@ -572,7 +578,7 @@ cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, cudaStre
             plan.TT = 1;
         }
     }
-    const long long rows = (sp.n_tok + plan.TT - 1) / plan.TT * p.Hkv;
+    const long long rows = (sp.by_seq ? short_blocks(sp, plan.TT) : (sp.n_tok + plan.TT - 1) / plan.TT) * p.Hkv;
     plan.S = 1;
     // A warp to a row once that gives every multiprocessor eight warps.
     if (plan.TT == 1 && NT <= 2 && p.W <= kWarpSelectPages && rows >= 8ll * sms)

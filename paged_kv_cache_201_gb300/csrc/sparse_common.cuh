@@ -89,4 +89,22 @@ __device__ __forceinline__ TokenRow token_row(const FwdParams &p, long long t, l
     return {b, row_key_limit(p, b, L, i, n)};
 }
 
+// Where a call has launched the tcgen05 kernel for the long runs of a packed batch, the other kernel's units may
+// be the tokens that a short sequence can have, `most` = group_min - 1 of each of the B sequences in blocks of
+// TT (by_seq; fewer than the rows of q where the batch is mostly long runs).  The rows of block `unit`: first
+// and count, 0 where the sequence is another's or shorter.
+__device__ __forceinline__ int short_rows(const SparseParams &sp, long long unit, int TT, long long &first) {
+    const FwdParams &p = sp.f;
+    const int most = sp.group_min - 1, blocks = (most + TT - 1) / TT;
+    const int b = (int)(unit / blocks), i = (int)(unit - (long long)b * blocks) * TT;
+    if (b >= p.B) return 0;
+    const int q0 = __ldg(p.q_start + b), n = __ldg(p.q_start + b + 1) - q0;
+    first = (long long)q0 + i;
+    if (q0 < 0 || n < 0 || (long long)q0 + n > sp.n_tok) return 0;  // reported by the tcgen05 kernel
+    return n > most ? 0 : max(0, min(TT, n - i));
+}
+inline long long short_blocks(const SparseParams &sp, int TT) {
+    return (long long)sp.f.B * ((sp.group_min - 1 + TT - 1) / TT);
+}
+
 }  // namespace pa
