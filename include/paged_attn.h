@@ -419,9 +419,10 @@ int paged_attn_append(const void *k_new, const void *v_new, const int32_t *slots
  * the selection does not depend on the order of any sum.
  *   sel [tokens, Hkv, top_k] int32: the selected logical pages in ascending order, then -1.
  * q has dims->dtype.  A page id outside [0, num_pages) counts as score 0 and sets PA_ERRBIT_PAGE_RANGE.
- * Limit: bt_stride <= PA_SELECT_MAX_PAGES (PA_EUNSUPPORTED).
+ * Limits (PA_EUNSUPPORTED): bt_stride <= PA_SELECT_MAX_PAGES, top_k <= PA_SPARSE_MAX_TOP_K.
  */
 #define PA_SELECT_MAX_PAGES 49152
+#define PA_SPARSE_MAX_TOP_K (1 << 24)
 int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_env_scale,
                             const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_start, int causal,
                             const int32_t *q_offset, int sink_pages, int local_pages, int top_k, int32_t *sel,
@@ -433,6 +434,7 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
  * 0, or at or past ceil(reach / page_size), list nothing; the order is free and an index listed twice
  * counts twice.  out [tokens, Hq, D] in dims->dtype (rounded once, to nearest even), lse [tokens, Hq]
  * float32 or NULL; a row without a key gets 0 and -inf.  q may be a view (dims->q_stride).
+ * top_k <= PA_SPARSE_MAX_TOP_K (PA_EUNSUPPORTED).
  */
 int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
                           const int32_t *seq_lens, const int32_t *q_start, int causal, const int32_t *q_offset,

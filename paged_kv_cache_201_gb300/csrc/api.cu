@@ -657,6 +657,7 @@ int check_sparse(const pa_dims *d, const void *q, const int32_t *block_table, co
     int rc = check_dims(d);
     if (rc != PA_OK) return rc;
     if (top_k < 1) return PA_EINVAL;
+    if (top_k > PA_SPARSE_MAX_TOP_K) return PA_EUNSUPPORTED;
     *n_tok = d->batch == 0 ? 0 : q_start ? (int64_t)d->q_len : (int64_t)d->batch * d->q_len;
     if (*n_tok == 0) return PA_OK;
     if (!q || !block_table || !seq_lens || !sel) return PA_EINVAL;

@@ -68,7 +68,7 @@ def test_append_refusals(lib, dims, kw, code):
     (dict(num_q_heads=7), {}, EINVAL), ({}, dict(env=None), EINVAL), ({}, dict(env=FAKE + 8), EINVAL),
     ({}, dict(scale=None), EINVAL), ({}, dict(q=FAKE + 8), EINVAL), ({}, dict(sel=None), EINVAL),
     ({}, dict(sel=FAKE + 2), EINVAL), ({}, dict(q_start=FAKE + 2), EINVAL), (dict(batch=0), {}, OK),
-    (dict(q_len=0), {}, OK), (dict(q_stride=8 * 128 - 8), {}, EINVAL),
+    ({}, dict(K=(1 << 24) + 1), EUNSUP), (dict(q_len=0), {}, OK), (dict(q_stride=8 * 128 - 8), {}, EINVAL),
 ])
 def test_select_refusals(lib, dims, kw, code):
     a = dict(q=FAKE, env=FAKE, scale=FAKE, table=FAKE, lens=FAKE, q_start=None, sink=1, local=1, K=4, sel=FAKE)
@@ -83,6 +83,7 @@ def test_select_refusals(lib, dims, kw, code):
     ({}, dict(factor=math.nan), EINVAL), ({}, dict(factor=math.inf), EINVAL), ({}, dict(k=None), EINVAL),
     ({}, dict(out=FAKE + 8), EINVAL), ({}, dict(lse=FAKE + 2), EINVAL), ({}, dict(sel=FAKE + 2), EINVAL),
     ({}, dict(table=None), EINVAL), (dict(batch=0), {}, OK), (dict(q_len=0), dict(lse=None), OK),
+    ({}, dict(K=(1 << 24) + 1), EUNSUP),
 ])
 def test_sparse_refusals(lib, dims, kw, code):
     a = dict(q=FAKE, k=FAKE, v=FAKE, table=FAKE, lens=FAKE, q_start=None, sel=FAKE, K=4, factor=0.1, out=FAKE,

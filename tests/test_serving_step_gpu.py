@@ -848,3 +848,95 @@ def test_malformed_q_start(pa):
         pa.paged_attn_fwd_sparse(d["q"], d["k"], d["v"], d["table"], d["lens"], True, None, good, 0.1, out, None,
                                  q_start=q_start)
         assert pa.paged_attn_last_error_word() & ~pa.ERRBIT_QSTART == 0
+
+
+def test_pools_past_2_31_bytes(pa):
+    """The whole step over the last pages of pools of 4.7 GB: byte and element offsets pass 31 bits."""
+    import torch
+    Hq, Hkv, D, ps, P = 8, 8, 128, 16, 144000
+    b = R.Batch(41, [40, 1], [300, 200], Hq, Hkv, D, ps, "bf16", spare=0)
+    low = P - b.P
+    k = torch.zeros((P, ps, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    assert low * ps * Hkv * D > 1 << 31
+    env, scale = pa.page_envelopes(k)
+    table = np.where(b.table < b.P, b.table + low, b.table).astype(np.int32)
+    # every token through append, the first ones as an earlier call
+    k_host, v_host = b.k.copy(), b.v.copy()
+    nan = np.isnan(R.elems_to_f64(k_host, "bf16"))
+    k_host[nan], v_host[nan] = 0, 0
+    d = {n: _t(x) for n, x in (("table", table), ("lens", b.seq_lens), ("q_start", b.q_start))}
+    for part in (0, 1):
+        slots, rows = [], []
+        for s, n in enumerate(b.q_lens):
+            L = int(b.seq_lens[s])
+            for x in (range(L - n) if part == 0 else range(L - n, L)):
+                slots.append(int(table[s, x // ps]) * ps + x % ps)
+                rows.append((int(b.table[s, x // ps]), x % ps))
+        pick = tuple(np.array(rows).T)
+        pa.paged_attn_append(W.host_to_torch(k_host[pick], "bf16").cuda(), W.host_to_torch(v_host[pick], "bf16").cuda(),
+                             _t(slots, np.int32), k, v, env, scale)
+    want_env, want_scale = b.envelopes()
+    live = b.live.any(-1)
+    np.testing.assert_array_equal(env[low:].cpu().numpy()[live], want_env[live])
+    np.testing.assert_array_equal(scale[low:].cpu().numpy()[live], want_scale[live])
+    assert not env[:low].any() and not k[:low].any()
+    q = W.host_to_torch(b.q, "bf16").cuda()
+    out, lse, sel = pa.attention_sparse(q, k, v, env, scale, d["table"], d["lens"], top_k=6, q_start=d["q_start"],
+                                        want_lse=True, want_pages=True)
+    want = R.select(b.q64(), want_env, want_scale, b.table, b.rows(), Hkv, ps, 1, 2, 6)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+    ref = R.attend(b.q64(), R.elems_to_f64(b.k, "bf16"), R.elems_to_f64(b.v, "bf16"), b.table, b.rows(), want, ps,
+                   D ** -0.5)
+    _gpu.assert_close(_gpu.to_f64(out, "bf16"), ref[0], "bf16", "out")
+    _gpu.assert_close(_gpu.to_f64(lse, "f32"), ref[1], "bf16", "lse")
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_sequences_longer_than_their_table(pa, n):
+    """seq_lens past the table row are clipped to it and reported, for single tokens and for runs."""
+    b = R.Batch(42, [n] * 3, [300, 260, 290], 8, 2, 128, 16, "bf16")
+    env = b.envelopes()
+    full = b.table
+    b.width = 16
+    b.table = np.ascontiguousarray(full[:, :16])
+    sel = _lists(b, 12)
+    _check_attend(pa, b, sel)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_SEQ_CLIPPED
+    want = R.select(b.q64(), *env, b.table, b.rows(), 2, 16, 1, 2, 6)
+    np.testing.assert_array_equal(_run_select(pa, b, *env, 1, 2, 6)[:b.T], want)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_SEQ_CLIPPED
+
+
+def test_two_streams_at_once(pa):
+    """Calls on two streams share nothing: each gives what it gives alone."""
+    import torch
+    b = R.Batch(43, [1, 60, 1], [3000, 900, 700], 8, 2, 128, 16, "bf16")
+    d = b.device()
+    env, scale = (_t(x) for x in b.envelopes())
+    sets = []
+    for i in range(2):
+        q = W.host_to_torch(R.random_elems(np.random.default_rng(i), b.q.shape, "bf16"), "bf16").cuda()
+        sets.append([q, torch.empty(b.T, 2, 20, dtype=torch.int32, device="cuda"), torch.empty_like(q)])
+
+    def call(q, sel, out):
+        pa.paged_attn_select_pages(q, env, scale, d["table"], d["lens"], True, None, 1, 2, sel, 16, q_start=d["q_start"])
+        pa.paged_attn_fwd_sparse(q, d["k"], d["v"], d["table"], d["lens"], True, None, sel, 0.1, out, None,
+                                 q_start=d["q_start"])
+    alone = []
+    for s in sets:
+        call(*s)
+        torch.cuda.synchronize()
+        alone.append((s[1].clone(), s[2].clone()))
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in sets:
+        s[1].zero_()
+        s[2].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                call(*s)
+    torch.cuda.synchronize()
+    for s, (sel, out) in zip(sets, alone):
+        assert torch.equal(s[1], sel) and torch.equal(s[2], out)
