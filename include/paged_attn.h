@@ -341,10 +341,11 @@ int paged_attn_fwd_kvq_splitkv(const void *q, const void *k_cache, const void *v
  * The four calls below make one serving step over the paged cache: paged_attn_step_tables turns the
  * requests' lengths into block tables and slots, paged_attn_append writes the new tokens' K and V
  * rows (and the envelopes of the pages they land in), paged_attn_select_pages picks the pages each
- * query token attends to, and paged_attn_fwd_sparse attends over them.  Each is one launch on
- * `stream`, needs no workspace, synchronises nothing and can be captured into a CUDA graph (make the
- * first call on a device outside a capture: it looks up the device error word).
- * These calls are this library's own; the pages have no counterpart.
+ * query token attends to, and paged_attn_fwd_sparse attends over them.  Each is one launch on `stream`
+ * (the last two: two, where a packed batch holds long runs of tokens and short ones), needs no workspace,
+ * synchronises nothing and can be captured into a CUDA graph (make the first call on a device outside a
+ * capture: it looks up the device error word).  The pools hold dims->dtype; 8-bit pools are not taken.
+ * These calls are this library's own; the reference has no counterpart.
  *
  * Query layout of the last two: q_start NULL = q [batch, q_len, Hq, D]; q_start [batch + 1] (device) =
  * q [T, Hq, D] packed as for paged_attn_fwd_varlen, with T = dims->q_len the rows of q.  Rows at or
@@ -414,11 +415,12 @@ int paged_attn_append(const void *k_new, const void *v_new, const int32_t *slots
  *   qi    = rint((q / a) * 127) over the G heads of the kv head, a their largest |element| (float32
  *           steps as for the envelope; a = 0 or not finite: qi = 0)
  *   s     = max over the G heads of  sum_d  qi_d > 0 ? qi_d * k_env[1][d] : qi_d * k_env[0][d]
- *   score = float(s) * k_env_scale, rounded once; +inf where k_env_scale is +inf
+ *   score = float(s) * k_env_scale, rounded once; +inf where k_env_scale is +inf (or a NaN)
  * s bounds q.k over the page's keys up to the rounding to 8 bits; it is an exact integer below 2^24, so
  * the selection does not depend on the order of any sum.
  *   sel [tokens, Hkv, top_k] int32: the selected logical pages in ascending order, then -1.
- * q has dims->dtype.  A page id outside [0, num_pages) counts as score 0 and sets PA_ERRBIT_PAGE_RANGE.
+ * q has dims->dtype; k_env_scale is not negative, as paged_attn_append writes it.  sel may not overlap an
+ * input.  A page id outside [0, num_pages) counts as score 0 and sets PA_ERRBIT_PAGE_RANGE.
  * Limits (PA_EUNSUPPORTED): bt_stride <= PA_SELECT_MAX_PAGES, top_k <= PA_SPARSE_MAX_TOP_K.
  */
 #define PA_SELECT_MAX_PAGES 49152

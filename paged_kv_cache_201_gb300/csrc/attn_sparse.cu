@@ -16,7 +16,9 @@ __global__ void __launch_bounds__(kSparseWarps * 32) paged_attn_sparse_simt_kern
     unit /= chunks;
     const int kvh = unit % p.Hkv;
     const long long t = unit / p.Hkv;
+    RangeCheck ranges(sp);
     const TokenRow tr = token_row(p, t, sp.n_tok, threadIdx.x == 0);
+    ranges.report(p);
     if (tr.b < 0) return;
     simt_token<T, D, HG, kSparseWarps>(sp, tr, t, kvh, hc, scratch, threadIdx.x, [] { __syncthreads(); });
 }

@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
     const int rt = unit % row_tiles;
     long long t_row = unit / row_tiles;
     if (sp.by_seq && short_rows(sp, t_row, 1, t_row) == 0) return;  // the whole cluster: it has one token
+    RangeCheck ranges(sp);
     const TokenRow tr = token_row(p, t_row, sp.n_tok, threadIdx.x == 0);
+    if (!sp.group_min) ranges.report(p);  // else the tcgen05 kernel has
     if (tr.b < 0) return;
     if (sp.group_min && __ldg(p.q_start + tr.b + 1) - __ldg(p.q_start + tr.b) >= sp.group_min) return;
 

@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
     const int ps = 1 << ps_shift;
     const int kvh = blockIdx.x % p.Hkv;
     TokenTile x;
-    if (!token_tile(sp, blockIdx.x / p.Hkv, TPC, x)) return;
+    RangeCheck ranges(sp);
+    const bool here = token_tile(sp, blockIdx.x / p.Hkv, TPC, x);
+    ranges.report(p);
+    if (!here) return;
     if (tid < x.nt) s_reach[tid] = row_key_limit(p, x.b, x.L, x.i0 + tid, x.n_seq);
     const int reach_max = row_key_limit(p, x.b, x.L, x.i0 + x.nt - 1, x.n_seq);  // grows with the token
     const int reach_min = row_key_limit(p, x.b, x.L, x.i0, x.n_seq);

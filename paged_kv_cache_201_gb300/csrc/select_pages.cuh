@@ -136,7 +136,11 @@ __global__ void __launch_bounds__(kSelCtaWarps<WPU> * 32, 16 / kSelCtaWarps<WPU>
     const long long unit = (long long)(blockIdx.x / S) * UNITS + me;
     const int h = (int)(unit % p.Hkv);
     long long t0 = unit / p.Hkv * plan.TT;
-    if (!sp.by_seq && t0 >= sp.n_tok) return;  // a warp of its own without a row
+    RangeCheck ranges(sp);
+    if (!sp.by_seq && t0 >= sp.n_tok) {  // a warp of its own without a row
+        if (!sp.group_min) ranges.report(p);
+        return;
+    }
     int nt_tok = 0;
     if (sp.by_seq) {
         nt_tok = short_rows(sp, unit / p.Hkv, plan.TT, t0);
@@ -153,6 +157,7 @@ __global__ void __launch_bounds__(kSelCtaWarps<WPU> * 32, 16 / kSelCtaWarps<WPU>
         s_seq[tid] = other ? -1 : tr.b;
         s_reach[tid] = tr.reach;
     }
+    if (!sp.group_min) ranges.report(p);  // else the tcgen05 kernel has
     if (S > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     sync();
 
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kSelCtaWarps<WPU> * 32, 16 / kSelCtaWarps<WPU>
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     cur_scale[r] = in_pool[r] ? scale[r] : 0.f;
-                    marked[r] = cur_scale[r] == INFINITY;
+                    marked[r] = !(cur_scale[r] < INFINITY);  // a NaN is no bound either
                 }
                 // Each 16 bytes make room for the next tile's once they are converted, so those are on
                 // their way while this tile is scored.  After the last tile the first is read again,

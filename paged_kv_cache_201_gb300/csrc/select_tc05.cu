@@ -59,7 +59,10 @@ __global__ void __launch_bounds__(kSelTcThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.Hkv;
     TokenTile x;
-    if (!token_tile(sp, blockIdx.x / p.Hkv, TT, x)) return;
+    RangeCheck ranges(sp);
+    const bool here = token_tile(sp, blockIdx.x / p.Hkv, TT, x);
+    ranges.report(p);
+    if (!here) return;
     const int N = (TT * Gp + 15) / 16 * 16;  // columns; those past the tokens' are never read out
     if (tid < x.nt) s_reach[tid] = row_key_limit(p, x.b, x.L, x.i0 + tid, x.n_seq);
     if (tid < kTileMaxTokens) s_amax[tid] = 0u;
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kSelTcThreads, 1)
             float s = __uint_as_float(u[tok << GS]);
 #pragma unroll
             for (int e = 1; e < Gp; ++e) s = fmaxf(s, __uint_as_float(u[(tok << GS) + e]));
-            if (group * (32 >> GS) + tok < x.nt) dst[tok * Wk] = scale == INFINITY ? INFINITY : __fmul_rn(s, scale);
+            if (group * (32 >> GS) + tok < x.nt) dst[tok * Wk] = scale < INFINITY ? __fmul_rn(s, scale) : INFINITY;
         }
     };
     for (int t = 0; t < tiles; ++t) {

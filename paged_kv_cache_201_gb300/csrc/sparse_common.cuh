@@ -28,6 +28,30 @@ __device__ __forceinline__ void quantise8(float (&x)[N], float a, float inv) {
     for (int i = 0; i < N; ++i) x[i] = r[i];
 }
 
+// Each entry of a packed batch's q_start is looked at by one thread of the grid, whoever's rows it holds: a
+// search from a row may pass a malformed sequence by.  The loads are on their way while the kernel finds its
+// own sequence; report() follows.
+struct RangeCheck {
+    long long b, n_tok;
+    int q0 = 0, q1 = 0;
+    __device__ __forceinline__ RangeCheck(const SparseParams &sp)
+        : b((long long)blockIdx.x * blockDim.x + threadIdx.x), n_tok(sp.n_tok) {
+        load(sp.f);
+    }
+    __device__ __forceinline__ void load(const FwdParams &p) {
+        if (!p.q_start || b >= p.B) return;
+        q0 = __ldg(p.q_start + b);
+        q1 = __ldg(p.q_start + b + 1);
+    }
+    __device__ __forceinline__ void report(const FwdParams &p) {
+        while (p.q_start && b < p.B) {
+            if (q0 < 0 || q1 < q0 || q1 > n_tok) atomicOr(p.err, (unsigned int)PA_ERRBIT_QSTART);
+            b += (long long)gridDim.x * blockDim.x;
+            load(p);
+        }
+    }
+};
+
 struct TokenRow {
     int b;      // sequence; -1: the row belongs to none (padding, or a malformed q_start)
     int reach;  // keys the token may see
@@ -72,11 +96,7 @@ __device__ __forceinline__ TokenRow token_row(const FwdParams &p, long long t, l
             q1 = __ldg(p.q_start + 1);
             L = __ldg(p.seq_lens);
         }
-        if (q0 < 0 || q1 < q0 || q1 > n_tok) {
-            if (report) atomicOr(p.err, (unsigned int)PA_ERRBIT_QSTART);
-            return {-1, 0};
-        }
-        if (t < q0 || t >= q1) return {-1, 0};
+        if (q0 < 0 || q1 < q0 || q1 > n_tok || t < q0 || t >= q1) return {-1, 0};
         b = lo;
         n = q1 - q0;
         i = (int)(t - q0);
@@ -100,7 +120,7 @@ __device__ __forceinline__ int short_rows(const SparseParams &sp, long long unit
     if (b >= p.B) return 0;
     const int q0 = __ldg(p.q_start + b), n = __ldg(p.q_start + b + 1) - q0;
     first = (long long)q0 + i;
-    if (q0 < 0 || n < 0 || (long long)q0 + n > sp.n_tok) return 0;  // reported by the tcgen05 kernel
+    if (q0 < 0 || n < 0 || (long long)q0 + n > sp.n_tok) return 0;
     return n > most ? 0 : max(0, min(TT, n - i));
 }
 inline long long short_blocks(const SparseParams &sp, int TT) {

@@ -46,10 +46,7 @@ __device__ __forceinline__ bool token_tile(const SparseParams &sp, long long til
         }
         x.b = lo;
         const int q0 = __ldg(p.q_start + lo), q1 = __ldg(p.q_start + lo + 1);
-        if (q0 < 0 || q1 < q0 || q1 > sp.n_tok) {
-            if (threadIdx.x == 0) atomicOr(p.err, (unsigned int)PA_ERRBIT_QSTART);
-            return false;
-        }
+        if (q0 < 0 || q1 < q0 || q1 > sp.n_tok) return false;
         x.n_seq = q1 - q0;
         const long long j = tile - first_tile(p, lo, TPC);
         if (x.n_seq < sp.group_min || j < 0 || j * TPC >= x.n_seq) return false;

@@ -908,6 +908,94 @@ def test_sequences_longer_than_their_table(pa, n):
     assert pa.paged_attn_last_error_word() == pa.ERRBIT_SEQ_CLIPPED
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("qs", [[0, 40, 20, 80], [0, 10, 70, 60], [0, 81, 81, 81], [-1, 80, 80, 80], [0, 0, 90, 80]])
+def test_every_malformed_range_is_reported(pa, dtype, qs):
+    """Rows that a malformed sequence shares with a sound one do not hide it, whichever kernel runs."""
+    import torch
+    K = 8 if dtype == "f32" else 60
+    b = R.Batch(46, [1] * 3, [1600, 1200, 1500], 8, 2, 128, 16, dtype, q_pad=77)
+    d = b.device()
+    env, scale = (_t(x) for x in b.envelopes())
+    q_start = _t(qs, np.int32)
+    sel = torch.full((80, 2, K), -1, dtype=torch.int32, device="cuda")
+    pa.paged_attn_select_pages(d["q"], env, scale, d["table"], d["lens"], True, None, 1, 1, sel, 16, q_start=q_start)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_QSTART
+    out = torch.empty_like(d["q"])
+    pa.paged_attn_fwd_sparse(d["q"], d["k"], d["v"], d["table"], d["lens"], True, None, sel, 0.1, out, None,
+                             q_start=q_start)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_QSTART
+
+
+def test_malformed_ranges_among_long_runs(pa):
+    """The same where the long runs' kernels take the first launch: sound sequences keep their results."""
+    import torch
+    b = R.Batch(47, [700, 3, 697], [1600, 1200, 1500], 64, 2, 128, 16, "bf16")
+    assert b.T * 64 * b.width >= 1 << 23 and _shares(pa, b, 60)
+    env, scale = b.envelopes()
+    args = [_t(x) for x in (env, scale, b.table, b.seq_lens)]
+    q = b.device()["q"]
+    sel = torch.full((b.T, 2, 60), -9, dtype=torch.int32, device="cuda")
+    q_start = _t([0, 700, 699, b.T], np.int32)
+    pa.paged_attn_select_pages(q, *args, True, None, 1, 1, sel, 16, q_start=q_start)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_QSTART
+    want = R.select(b.q64()[:40], env, scale, b.table, b.rows()[:40], 2, 16, 1, 1, 60)
+    np.testing.assert_array_equal(sel[:40].cpu().numpy(), want)
+    d = b.device()
+    pa.paged_attn_fwd_sparse(q, d["k"], d["v"], d["table"], d["lens"], True, None, sel, 0.1, torch.empty_like(q), None,
+                             q_start=q_start)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_QSTART
+
+
+def test_more_sequences_than_threads(pa):
+    """One token among 6000 sequences of none, the last of them malformed."""
+    import torch
+    B = 6000
+    d = dict(dtype=torch.int32, device="cuda")
+    q_start = torch.zeros(B + 1, **d)
+    q_start[17:] = 1
+    lens, table = torch.full((B,), 40, **d), torch.arange(3, **d).repeat(B, 1)
+    k = torch.randn((3, 16, 1, 64), device="cuda")
+    env, scale = torch.zeros((3, 1, 2, 64), dtype=torch.int8, device="cuda"), torch.zeros((3, 1), device="cuda")
+    q, sel, out = torch.randn((1, 1, 64), device="cuda"), torch.empty((1, 1, 3), **d), torch.empty((1, 1, 64), device="cuda")
+    for bad in (False, True):
+        if bad:
+            q_start[B] = 2
+        for call in (lambda: pa.paged_attn_select_pages(q, env, scale, table, lens, True, None, 1, 1, sel, 16, q_start=q_start),
+                     lambda: pa.paged_attn_fwd_sparse(q, k, k, table, lens, True, None, sel, 0.1, out, None, q_start=q_start)):
+            call()
+            assert pa.paged_attn_last_error_word() == (pa.ERRBIT_QSTART if bad else 0)
+        assert sel.flatten().tolist() == [0, 1, 2] and out.isfinite().all()
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_select_nan_scale(pa, n):
+    """A page whose scale is a NaN has no bound: it comes first, as one with +inf does."""
+    b = R.Batch(44, [n] * 2, [6000, 5000], 8, 2, 128, 16, "bf16")
+    env, scale = b.envelopes()
+    marked = scale.copy()
+    for s, j in ((0, 7), (0, 100), (1, 50), (1, 200)):
+        marked[b.table[s, j]] = np.inf
+        scale[b.table[s, j]] = np.nan
+    want = R.select(b.q64(), env, marked, b.table, b.rows(), 2, 16, 1, 2, 9)
+    np.testing.assert_array_equal(_run_select(pa, b, env, scale, 1, 2, 9)[:b.T], want)
+    assert pa.paged_attn_last_error_word() == 0
+
+
+@pytest.mark.parametrize("D,G,n,pages", [(256, 24, 1, 500), (256, 40, 2, 1500), (256, 24, 1, 49152), (128, 17, 1, 49152),
+                                         (256, 4, 70, 900)])
+def test_select_wide_groups(pa, D, G, n, pages):
+    """Many heads of head_dim 256, up to the longest row."""
+    rng = np.random.default_rng(D + G + pages)
+    b = R.Batch(45, [n], [n], G, 1, D, 16, "bf16")
+    b.seq_lens = np.array([pages * 16 - 5], np.int32)
+    b.width, b.P = pages, 3000
+    b.table = rng.integers(0, b.P, (1, pages)).astype(np.int32)
+    hi = rng.integers(-127, 128, (b.P, 1, D)).astype(np.int8)
+    lo = np.minimum(hi, rng.integers(-127, 128, (b.P, 1, D))).astype(np.int8)
+    _check_select(pa, b, 1, 2, 60, env=(np.stack([lo, hi], 2), rng.uniform(0.5, 1, (b.P, 1)).astype(np.float32)))
+
+
 def test_two_streams_at_once(pa):
     """Calls on two streams share nothing: each gives what it gives alone."""
     import torch
