@@ -4,13 +4,14 @@
 // A CTA takes up to 128 rows (TPC = min(32, 128 / G) consecutive tokens x the G heads of a kv head) and walks
 // the union of the tokens' page lists, each page once, in 128-key tiles of 128 / page_size listed pages:
 //   warp 0      loads the Q tile, then K pages by TMA into a two-slot ring; warp 2 the V pages
-//   warp 1      one thread issues tcgen05.mma: S = Q K^T into one of two S buffers of tensor memory (128
-//               float32 columns), then O += P V with P read from tensor memory; P V of a tile is issued
-//               behind Q K^T of the next one
+//   warp 1      issues tcgen05.mma: S = Q K^T into one of two S buffers of tensor memory (128 float32
+//               columns), then O += P V with P read from tensor memory; P V of a tile is issued behind
+//               Q K^T of the next one
 //   warp 3      clears the V rows of the last tile that hold no key of the sequence (any bits)
 //   warps 4-11  softmax, two threads to a row, 64 columns each: a 16-key block counts for a row if the row's
 //               token lists its page (one bit), so its offset in exp2(s c + off) is the negated maximum or
-//               -inf: the mask costs no instruction for a key.  O is rescaled in tensor memory only when the
+//               -inf: the mask costs no instruction for a key.  A block that no token of the warp's rows
+//               lists is passed by, its P 0.  O is rescaled in tensor memory only when the
 //               maximum grows by more than 2^8.  P is written over S as 16-bit pairs: high part and
 //               remainder for bf16 (two products), alone for f16 (2^-12 of itself).  At the end they scale
 //               the rows by their sums and store them.
@@ -18,9 +19,12 @@
 // product is guarded: a CTA whose result is not finite, and one whose lists name a page twice (it counts
 // twice), does its tokens again on CUDA cores, where a key that is not seen is not multiplied.
 // The products run over all rows of every listed page, whoever lists it: at random lists (64 of some 400
-// pages a token, 32 tokens, G = 4) six times what the lists ask for, at 1.05 us a tile in f16 and 1.53 in
-// bf16 (head_dim 128).  936 such tokens of 8 kv heads take 145 us (f16); read token by token their lists
+// pages a token, 32 tokens, G = 4) six times what the lists ask for, at 1.0 us a tile in f16 and 1.15 in
+// bf16 (head_dim 128).  936 such tokens of 8 kv heads take 127 us (f16); read token by token their lists
 // move 3.9 GB through L2, 451 us.  Lists that overlap more cost less here.
+// What bounds it: the pages' way from L2 (890 MB; loads alone take 111 us) and the softmax's chain (116 us
+// without loads and products; products alone 86) are about even.  Sixty-four tokens a CTA, two tiles of rows
+// over the same pages, halve the loads, but leave a thread a whole row: 131 us.
 #include <float.h>
 
 #include <type_traits>
@@ -47,33 +51,56 @@ struct Listed {
     uint32_t tokens;
 };
 
-// P for 32 keys of one row, two 16-key blocks with their own offsets: p = exp2(s c + off[block]); the sum of
-// the p goes to l, the 32 columns at taddr receive [16 of high parts | 16 of remainders] (bf16) or the p as
-// f16 pairs in the first 16.
+// Two float32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// P for 32 keys of one row, two 16-key blocks with their own offsets: p = exp2(s c + off[block]); the sums of
+// the p go to l, the 32 columns at taddr receive [16 of high parts | 16 of remainders] (bf16) or the p as
+// f16 pairs in the first 16.  any: whether a row of the warp has the block listed; its P is 0 if not.
 template <typename T>
-__device__ __forceinline__ void block_exp(const uint32_t (&u)[32], float c, float off0, float off1, float &l,
-                                          uint32_t taddr) {
+__device__ __forceinline__ void block_exp(const uint32_t (&u)[32], float c, const float (&off)[2], const bool (&any)[2],
+                                          float2 &l, uint32_t taddr) {
     constexpr bool kSplit = !std::is_same<T, __half>::value;
     uint32_t hi[16], lo[16];
-    float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float off = i < 8 ? off0 : off1;
-        const float p0 = fast_exp2(fmaf(__uint_as_float(u[2 * i]), c, off));
-        const float p1 = fast_exp2(fmaf(__uint_as_float(u[2 * i + 1]), c, off));
-        l0 += p0;
-        l1 += p1;
-        if (kSplit) {
-            // the high parts truncated to their top 16 bits; p - high is then exact in float32 and below
-            // 2^-7 p, and its bf16 rounding leaves P within 2^-16 of p
-            hi[i] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-            lo[i] = MmaOp<T>::pack(p0 - __uint_as_float(__float_as_uint(p0) & 0xffff0000u),
-                                   p1 - __uint_as_float(__float_as_uint(p1) & 0xffff0000u));
+    for (int b = 0; b < 2; ++b) {
+        if (any[b]) {
+#pragma unroll
+            for (int i = 8 * b; i < 8 * b + 8; ++i) {
+                const float2 x = fma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
+                                      make_float2(c, c), make_float2(off[b], off[b]));
+                const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                l = add2(l, make_float2(p0, p1));
+                if (kSplit) {
+                    // the high parts truncated to their top 16 bits; p - high is then exact in float32 and below
+                    // 2^-7 p, and its bf16 rounding leaves P within 2^-16 of p
+                    hi[i] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                    lo[i] = MmaOp<T>::pack(p0 - __uint_as_float(__float_as_uint(p0) & 0xffff0000u),
+                                           p1 - __uint_as_float(__float_as_uint(p1) & 0xffff0000u));
+                } else {
+                    hi[i] = MmaOp<T>::pack(p0, p1);
+                }
+            }
         } else {
-            hi[i] = MmaOp<T>::pack(p0, p1);
+#pragma unroll
+            for (int i = 8 * b; i < 8 * b + 8; ++i) hi[i] = lo[i] = 0u;
         }
     }
-    l += l0 + l1;
     tc05::st_16cols(taddr, hi);
     if (kSplit) tc05::st_16cols(taddr + 16u, lo);
 }
@@ -122,7 +149,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
             mbar_init(bar(S_KE + i), 1);
             mbar_init(bar(S_VF + i), 1);
             mbar_init(bar(S_VE + i), 1);
-            mbar_init(bar(S_PF + i), 256 + 32);
+            mbar_init(bar(S_PF + i), 8 + 1);
         }
         fence_barrier_init();
     }
@@ -179,7 +206,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                     cur = nxt;
                     nxt = entry(batch + 32 + lane);
                 }
-                const int tok = __shfl_sync(0xffffffffu, cur, (first + lane - batch) & 31);
+                const int tok = __shfl_sync(0xffffffffu, cur, (first + lane / NH - batch) & 31);
                 const int nvalid = min(ppt, n_list - first);
                 if (t >= 2) {
                     const bool ok = mbar_wait(bar(b_empty + slot), ((t >> 1) - 1) & 1, p.err);
@@ -188,12 +215,9 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(bar(b_full + slot), (uint32_t)nvalid * (uint32_t)NH * box);
                 __syncwarp();
-                if (lane < nvalid) {
-                    const uint32_t dst = (kq ? sK(slot) : sV(slot)) + (uint32_t)lane * box;
-#pragma unroll
-                    for (int h = 0; h < NH; ++h)
-                        tma_load_4d(dst + (uint32_t)h * kSt5Half, tm, bar(b_full + slot), 0, tok, h, kvh);
-                }
+                if (lane / NH < nvalid)
+                    tma_load_4d((kq ? sK(slot) : sV(slot)) + (uint32_t)(lane % NH * kSt5Half) + (uint32_t)(lane / NH) * box, tm,
+                                bar(b_full + slot), 0, tok, lane % NH, kvh);
                 issued = t + 1;
             }
             // no copy may outlive the CTA
@@ -201,47 +225,57 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
             if (kq && n_tiles > 0) mbar_wait(bar(S_QF), 0, p.err);
         } else if (warp == 1) {
             // ---------------------------------------------------------------- products
-            if (lane == 0 && n_tiles > 0) {
+            // The whole warp runs this, its values the same in every lane as the compiler can see, and one lane issues:
+            // the operands then live in uniform registers (with one lane's own, an instruction took 60 cycles).
+            auto same = [](auto v) { return __shfl_sync(0xffffffffu, v, 0); };
+            const int nt = same(n_tiles);
+            const uint32_t tm = same(tmem);
+            if (nt > 0) {
+                const bool leader = tc05::elect_one();
                 const uint32_t dhi = tc05::smem_desc_sw128_hi(1024);
                 const uint32_t dq = tc05::smem_desc_sw128_lo(sQ, 16);
                 const uint32_t dk0 = tc05::smem_desc_sw128_lo(sK(0), 16), dk1 = tc05::smem_desc_sw128_lo(sK(1), 16);
                 const uint32_t dv0 = tc05::smem_desc_sw128_lo(sV(0), (uint32_t)kSt5Half);
                 const uint32_t dv1 = tc05::smem_desc_sw128_lo(sV(1), (uint32_t)kSt5Half);
-                auto issue_pv = [&](int t) -> bool {
-                    const int slot = t & 1;
-                    if (!mbar_wait(bar(S_PF + slot), (t >> 1) & 1, p.err)) return false;  // P there, V cleared
-                    tc05::fence_after_sync();
-                    const uint32_t pcol = tmem + (slot ? 128u : 0u), dv = slot ? dv1 : dv0;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        // keys 16 kk .. + 15: half kk & 1 of 32-key chunk kk / 2, high parts at + 0, remainders at + 16
-                        const uint32_t vlo = dv + (uint32_t)kk * (2048u >> 4);
-                        const uint32_t pa = pcol + 32u * (uint32_t)(kk >> 1) + 8u * (uint32_t)(kk & 1);
-                        tc05::mma_ts_lh(tmem + kSt5ColO, pa, vlo, dhi, idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
-                        if (kSplit) tc05::mma_ts_lh(tmem + kSt5ColO, pa + 16u, vlo, dhi, idesc_pv, 1u);
-                    }
-                    tc05::commit(bar(S_VE + slot));  // V slot free, O holds this tile's product
-                    return true;
-                };
                 bad = !mbar_wait(bar(S_QF), 0, p.err);
-                for (int t = 0; t < n_tiles && !bad; ++t) {
-                    const int slot = t & 1;
-                    if (!mbar_wait(bar(S_KF + slot), (t >> 1) & 1, p.err)) {
-                        bad = true;
-                        break;
-                    }
-                    tc05::fence_after_sync();
-                    const uint32_t d = tmem + (slot ? 128u : 0u), dk = slot ? dk1 : dk0;
+                // Q K^T of tile t, then P V of the tile before
+                for (int t = 0; t <= nt; ++t) {
+                    if (t < nt) {
+                        const int slot = t & 1;
+                        bad = bad || !mbar_wait(bar(S_KF + slot), (t >> 1) & 1, p.err);
+                        if (__any_sync(0xffffffffu, bad)) break;
+                        tc05::fence_after_sync();
+                        const uint32_t d = tm + (slot ? 128u : 0u), dk = slot ? dk1 : dk0;
+                        if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        // columns 16 kk .. + 15: 64-column half kk / 4, 32-byte slice kk % 4 of its rows
-                        const uint32_t off = ((uint32_t)(kk >> 2) * kSt5Half + (uint32_t)(kk & 3) * 32u) >> 4;
-                        tc05::mma_ss_lh(d, dq + off, dhi, dk + off, dhi, idesc_qk, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                // columns 16 kk .. + 15: 64-column half kk / 4, 32-byte slice kk % 4 of its rows
+                                const uint32_t off = ((uint32_t)(kk >> 2) * kSt5Half + (uint32_t)(kk & 3) * 32u) >> 4;
+                                tc05::mma_ss_lh(d, dq + off, dhi, dk + off, dhi, idesc_qk, kk > 0 ? 1u : 0u);
+                            }
+                            tc05::commit(bar(S_KE + slot));  // K slot free, S holds the scores
+                        }
                     }
-                    tc05::commit(bar(S_KE + slot));  // K slot free, S holds the scores
-                    if (t > 0 && !issue_pv(t - 1)) bad = true;
+                    if (t > 0) {
+                        const int slot = (t - 1) & 1;
+                        bad = !mbar_wait(bar(S_PF + slot), ((t - 1) >> 1) & 1, p.err);  // P there, V cleared
+                        if (__any_sync(0xffffffffu, bad)) break;
+                        tc05::fence_after_sync();
+                        const uint32_t pcol = tm + (slot ? 128u : 0u), dv = slot ? dv1 : dv0;
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk) {
+                                // keys 16 kk .. + 15: half kk & 1 of 32-key chunk kk / 2, high parts at + 0,
+                                // remainders at + 16
+                                const uint32_t vlo = dv + (uint32_t)kk * (2048u >> 4);
+                                const uint32_t pa = pcol + 32u * (uint32_t)(kk >> 1) + 8u * (uint32_t)(kk & 1);
+                                tc05::mma_ts_lh(tm + kSt5ColO, pa, vlo, dhi, idesc_pv, (t > 1 || kk > 0) ? 1u : 0u);
+                                if (kSplit) tc05::mma_ts_lh(tm + kSt5ColO, pa + 16u, vlo, dhi, idesc_pv, 1u);
+                            }
+                            tc05::commit(bar(S_VE + slot));  // V slot free, O holds this tile's product
+                        }
+                    }
                 }
-                if (!bad) issue_pv(n_tiles - 1);
             }
             __syncwarp();
         } else {
@@ -261,7 +295,8 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                mbar_arrive(bar(S_PF + slot));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S_PF + slot));
             }
         }
     } else {
@@ -274,33 +309,47 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
         const bool row_valid = tk < x.nt;  // at most TPC tokens, TPC G <= 128
         const int lim = row_valid ? s_reach[tk] : 0;
         const uint32_t bit = row_valid ? 1u << tk : 0u;
+        // those of the warp's rows
+        const int w0 = (warp & 3) * 32 / p.G, w1 = min((warp & 3) * 32 + 31, TPC * p.G - 1) / p.G;
+        const uint32_t warp_bits = w1 < w0 ? 0u : (w1 >= 31 ? 0xffffffffu : (2u << w1) - 1u) & ~((1u << w0) - 1u);
         const float c2 = p.scale_log2;
         bool bad = false;
-        float m_used = kNegInf, l = 0.f;
+        float m_used = kNegInf;
+        float2 l2 = make_float2(0.f, 0.f);  // sums of even and odd keys
+        // the pages of a tile's four 16-key blocks, one tile ahead
+        Listed page[4];
+        auto look_up = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = t * ppt + ((64 * hh + 16 * i) >> ps_shift);
+                page[i] = e < n_list ? s_list[e] : Listed{-1, 0u};
+            }
+        };
+        look_up(0);
         for (int t = 0; t < n_tiles; ++t) {
             const int st = t & 1;
-            // this row's four 16-key blocks: listed by its token?
-            bool on[4];
+            // this row's four 16-key blocks: listed by its token, by any of the warp's
+            bool on[4], any[4];
             int nv[4];  // keys of the block that the token sees
             int end = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int k0 = 64 * hh + 16 * i, e = t * ppt + (k0 >> ps_shift);
-                const Listed v = e < n_list ? s_list[e] : Listed{0, 0u};
-                const int pos = (v.j << ps_shift) + (k0 & (ps - 1));
-                on[i] = v.tokens & bit;
+                const int pos = (page[i].j << ps_shift) + ((64 * hh + 16 * i) & (ps - 1));
+                on[i] = page[i].tokens & bit;
+                any[i] = page[i].tokens & warp_bits;
                 nv[i] = on[i] ? lim - pos : 0;
-                end = max(end, e < n_list ? pos + 16 : 0x7fffffff);
+                end = max(end, page[i].j >= 0 ? pos + 16 : 0x7fffffff);
             }
-            if (!bad) bad = __any_sync(0xffffffffu, !mbar_wait(bar(S_KE + st), (t >> 1) & 1, p.err));
+            if (!bad) bad = !mbar_wait(bar(S_KE + st), (t >> 1) & 1, p.err);
+            __syncwarp();
             tc05::fence_after_sync();
             const uint32_t sbuf = tmem + lane_addr + (st ? 128u : 0u) + 64u * (uint32_t)hh;
             uint32_t ua[32], ub[32];
             float mx = kNegInf;
-            if (!bad) {
-                tc05::ld_32cols(sbuf, ua);
-                tc05::ld_32cols(sbuf + 32u, ub);
-                tc05::wait_ld();
+            tc05::ld_32cols(sbuf, ua);
+            tc05::ld_32cols(sbuf + 32u, ub);
+            tc05::wait_ld();
+            {
                 if (end > reach_min) {  // some key is past some token's reach, or was never loaded
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -310,26 +359,30 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                         if (j >= nv[3]) ub[16 + j] = 0xff800000u;
                     }
                 }
-                float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    m4[0] = fmaxf(m4[0], __uint_as_float(ua[j]));
-                    m4[1] = fmaxf(m4[1], __uint_as_float(ua[16 + j]));
-                    m4[2] = fmaxf(m4[2], __uint_as_float(ub[j]));
-                    m4[3] = fmaxf(m4[3], __uint_as_float(ub[16 + j]));
+                for (int i = 0; i < 4; ++i) {
+                    if (!any[i]) continue;
+                    const uint32_t(&u)[32] = i < 2 ? ua : ub;
+                    float a = __uint_as_float(u[(i & 1) * 16]), b = __uint_as_float(u[(i & 1) * 16 + 1]);
+#pragma unroll
+                    for (int j = 2; j < 16; j += 2) {
+                        a = fmaxf(a, __uint_as_float(u[(i & 1) * 16 + j]));
+                        b = fmaxf(b, __uint_as_float(u[(i & 1) * 16 + j + 1]));
+                    }
+                    if (on[i]) mx = fmaxf(mx, fmaxf(a, b));
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, on[i] ? m4[i] : kNegInf);
             }
             s_xmax[st][hh][r] = mx;
+            look_up(t + 1);
             named_bar_sync(1, 256);
             mx = fmaxf(mx, s_xmax[st][hh ^ 1][r]);
             const float m_new = fmaxf(m_used, mx * c2);
             const bool need = m_new > m_used + kSt5Rescale;  // also when m_used is -inf and m_new is not
-            if (__any_sync(0xffffffffu, need) && !bad) {
+            if (__any_sync(0xffffffffu, need || bad) && !(bad = __any_sync(0xffffffffu, bad))) {
                 const float alpha = need ? exp2f(m_used - m_new) : 1.f;
                 if (need) {
-                    l *= alpha;
+                    l2.x *= alpha;
+                    l2.y *= alpha;
                     m_used = m_new;
                 }
                 if (t > 0) {
@@ -350,20 +403,21 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
             }
             if (!bad) {
                 const float nmu = m_used == kNegInf ? 0.f : -m_used;  // -inf - (-inf) guard
-                float off[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) off[i] = on[i] ? nmu : kNegInf;
-                block_exp<T>(ua, c2, off[0], off[1], l, sbuf);
-                block_exp<T>(ub, c2, off[2], off[3], l, sbuf + 32u);
+                const float oa[2] = {on[0] ? nmu : kNegInf, on[1] ? nmu : kNegInf};
+                const float ob[2] = {on[2] ? nmu : kNegInf, on[3] ? nmu : kNegInf};
+                const bool na[2] = {any[0], any[1]}, nb[2] = {any[2], any[3]};
+                block_exp<T>(ua, c2, oa, na, l2, sbuf);
+                block_exp<T>(ub, c2, ob, nb, l2, sbuf + 32u);
                 tc05::wait_st();
             }
             tc05::fence_before_sync();
-            mbar_arrive(bar(S_PF + st));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S_PF + st));
         }
         // the row's sum, then its half of the columns
-        s_lsum[hh][r] = l;
+        s_lsum[hh][r] = l2.x + l2.y;
         named_bar_sync(1, 256);
-        l = s_lsum[0][r] + s_lsum[1][r];
+        const float l = s_lsum[0][r] + s_lsum[1][r];
         if (!bad && n_tiles > 0)
             bad = __any_sync(0xffffffffu, !mbar_wait(bar(S_VE + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.err));
         tc05::fence_after_sync();
