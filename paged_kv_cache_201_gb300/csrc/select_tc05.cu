@@ -227,17 +227,22 @@ __global__ void __launch_bounds__(kSelTcThreads, 1)
         fence_proxy_async_smem();
         tc05::fence_before_sync();
         bad = __syncthreads_or(bad);  // A (and B) written, tile t - 2 read out
-        if (tid == 0 && !bad) {
+        if (warp == 0 && !bad) {
+            // the values the same in every lane as the compiler can see: operands in uniform registers
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + (uint32_t)((t & 1) * 128);
             tc05::fence_after_sync();
             const uint32_t dhi = tc05::smem_desc_sw128_hi(1024);
             const uint32_t da = tc05::smem_desc_sw128_lo(sA, 16), db = tc05::smem_desc_sw128_lo(sB, 16);
+            if (tc05::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < KH * 4; ++kk) {
-                const uint32_t oa = ((uint32_t)(kk >> 2) * kSelTcHalf + (uint32_t)(kk & 3) * 32u) >> 4;
-                const uint32_t ob = ((uint32_t)(kk >> 2) * b_half + (uint32_t)(kk & 3) * 32u) >> 4;
-                tc05::mma_ss_lh(tmem + (uint32_t)((t & 1) * 128), da + oa, dhi, db + ob, dhi, idesc, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < KH * 4; ++kk) {
+                    const uint32_t oa = ((uint32_t)(kk >> 2) * kSelTcHalf + (uint32_t)(kk & 3) * 32u) >> 4;
+                    const uint32_t ob = ((uint32_t)(kk >> 2) * b_half + (uint32_t)(kk & 3) * 32u) >> 4;
+                    tc05::mma_ss_lh(tm, da + oa, dhi, db + ob, dhi, idesc, kk > 0 ? 1u : 0u);
+                }
+                tc05::commit(bar0 + 8 * (t & 1));
             }
-            tc05::commit(bar0 + 8 * (t & 1));
+            __syncwarp();
         }
         tc05::fence_after_sync();
         if (t > 0) read_out(t - 1);
