@@ -8,7 +8,7 @@
 // order, so an envelope is the same bits whether a page is filled at once or token by token.
 // Kept apart, the long chain of an envelope (slots, rows, reduction, division) overlaps the copies; where
 // few pages close, as in a prompt, the CTA's warps share a page's rows.  6656 prompt tokens of 8 heads of
-// 128 (f16, 64-token pages) take 14.2 us, 57 % of the copy rate; with the closing warps among the copying
+// 128 (f16, 64-token pages) take 14.6 us, 56 % of the copy rate; with the closing warps among the copying
 // ones they took 21, and the copies alone take 10.7.  A decode step of 256 tokens takes 5.3 us, a chain
 // of three trips to memory.
 #include <float.h>
@@ -334,7 +334,7 @@ static cudaError_t launch_append_k(const AppendParams &p, cudaStream_t stream) {
 template <typename T, int D>
 static cudaError_t launch_append_d(const AppendParams &p, cudaStream_t stream) {
     // Prompts (warps for every multiprocessor many times over): several tokens a warp and few closing
-    // pages among them (14.2 us as above; 27.7 with one token a warp); single tokens: a warp each, most of
+    // pages among them (14.6 us as above; 27.7 with one token a warp); single tokens: a warp each, most of
     // them closing a page.
     if ((long long)p.T * p.Hkv >= 16384) return launch_append_k<T, D, 4, 32>(p, stream);
     return launch_append_k<T, D, 1, 4>(p, stream);

@@ -10,7 +10,8 @@
 // a request) and then writes its share of the tokens: no workspace and no second launch.  A cluster
 // barrier separates every CTA's reads of the lengths from the first CTA's writes, so that the outputs
 // may be the inputs' own arrays.  The step is a chain of a few trips to memory; what is read and written
-// (0.3 MB for 1024 requests and 65536 tokens) would take 0.04 us at the copy rate.
+// (0.3 MB for 1024 requests and 65536 tokens) would take 0.04 us at the copy rate; measured, that step takes
+// 8.0 us, and one of 16 requests with a token each 2.4.
 #include "kernels.h"
 
 namespace pa {
