@@ -811,12 +811,13 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
     // Sequences with half a tile of query tokens or more go to the tcgen05 kernel once there is work enough for
     // its CTAs (one an SM, with a long set-up); in a packed batch both kernels find theirs from q_start.
     // Measured, in microseconds, tcgen05 and mma.sync: 1024 tokens of 8 kv heads, G = 4, 512 pages (2^24 scores
-    // of a head) 53 and 65, 256 tokens 26 and 27, 64 tokens 24 and 17; 1024 tokens of 2 kv heads, G = 16, 2048
-    // pages (2^26) 114 and 213, 64 tokens (2^22) 56 and 33.
+    // of a head) 48 and 66, 512 tokens 26 and 37, 256 tokens 26 and 27, 64 tokens 24 and 17; 1024 tokens of 2
+    // kv heads, G = 16, 2048 pages (2^26) 108 and 194, 256 tokens 55 and 57 (64 CTAs), 128 tokens 55 and 41.
     const int tile = pa::select_tile_tokens(dims->head_dim, sp.f.G, dims->bt_stride);
     const bool runs = q_start ? n_tok >= 2 * (int64_t)dims->batch : dims->q_len >= (tile + 1) / 2;
     if (tile > 0 && runs && n_tok >= (tile + 1) / 2 &&
-        (double)n_tok * dims->num_q_heads * dims->bt_stride >= (double)(1 << 23)) {
+        (double)n_tok * dims->num_q_heads * dims->bt_stride >= (double)(1 << 23) &&
+        (n_tok + tile - 1) / tile * dims->num_kv_heads * 5 >= 2 * (int64_t)device_sm_count()) {
         sp.group_min = (tile + 1) / 2;
         sp.by_seq = q_start && (int64_t)dims->batch * (sp.group_min - 1) < n_tok;
         rc = cuda_status(pa::launch_select_tc05(sp, dims->dtype, device_sm_count(), st));

@@ -574,11 +574,14 @@ cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, cudaStre
         plan.Gp = 1;
         while (plan.Gp < p.G) plan.Gp *= 2, ++plan.gs;
         // Prompt chunks: as many tokens a CTA as fill 32, 16 or 8 columns while their scores take at most
-        // 64 KB and there is a CTA for every multiprocessor; a batch of mostly single tokens takes one.
+        // 64 KB and there is a CTA for every multiprocessor, for 8 columns every other one (96 tokens of 8
+        // heads, G = 1: 22 us, single tokens 33; 64 tokens, 64 CTAs: no better than single ones, 20); a batch
+        // of mostly single tokens takes one.
         NT = 4;
         plan.TT = 32 / plan.Gp;
         auto fits = [&] {
-            return (long long)plan.TT * plan.Wk * 4 <= 65536 && (sp.n_tok + plan.TT - 1) / plan.TT * p.Hkv >= sms;
+            return (long long)plan.TT * plan.Wk * 4 <= 65536 &&
+                   (sp.n_tok + plan.TT - 1) / plan.TT * p.Hkv * (NT == 1 ? 2 : 1) >= sms;
         };
         while (NT > 1 && !fits()) {
             NT /= 2;
