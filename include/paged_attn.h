@@ -342,7 +342,7 @@ int paged_attn_fwd_kvq_splitkv(const void *q, const void *k_cache, const void *v
  * requests' lengths into block tables and slots, paged_attn_append writes the new tokens' K and V
  * rows (and the envelopes of the pages they land in), paged_attn_select_pages picks the pages each
  * query token attends to, and paged_attn_fwd_sparse attends over them.  Each is one launch on `stream`
- * (the last two: two, where a packed batch holds long runs of tokens and short ones), needs no workspace,
+ * (the last two: two, side by side, where a packed batch may hold long runs of tokens and short ones), needs no workspace,
  * synchronises nothing and can be captured into a CUDA graph (make the first call on a device outside a
  * capture: it looks up the device error word).  The pools hold dims->dtype; 8-bit pools are not taken.
  * These calls are this library's own; the reference has no counterpart.

@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
     unit /= p.Hkv;
     const int rt = unit % row_tiles;
     long long t_row = unit / row_tiles;
+    const BehindFirst order(sp);
     if (sp.by_seq && short_rows(sp, t_row, 1, t_row) == 0) return;  // the whole cluster: it has one token
     RangeCheck ranges(sp);
     const TokenRow tr = token_row(p, t_row, sp.n_tok, threadIdx.x == 0);
@@ -378,12 +379,9 @@ static cudaError_t launch_sparse_mma_t(const SparseParams &sp, int sms, const CU
     cfg.blockDim = dim3(kMmaThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = S;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2]{};
+    cfg.numAttrs = second_launch_attrs(attr, S, sp.group_min > 0);
+    cfg.attrs = attr;
     return cudaLaunchKernelEx(&cfg, kern, tmk, tmv, sp, ps_shift, S, row_tiles);
 }
 

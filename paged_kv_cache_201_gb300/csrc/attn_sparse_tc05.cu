@@ -20,7 +20,7 @@
 // twice), does its tokens again on CUDA cores, where a key that is not seen is not multiplied.
 // The products run over all rows of every listed page, whoever lists it: at random lists (64 of some 400
 // pages a token, 32 tokens, G = 4) six times what the lists ask for, at 1.0 us a tile in f16 and 1.15 in
-// bf16 (head_dim 128).  936 such tokens of 8 kv heads take 127 us (f16); read token by token their lists
+// bf16 (head_dim 128).  936 such tokens of 8 kv heads take 126 us (f16); read token by token their lists
 // move 3.9 GB through L2, 451 us.  Lists that overlap more cost less here.
 // What bounds it: the pages' way from L2 (890 MB; loads alone take 111 us) and the softmax's chain (116 us
 // without loads and products; products alone 86) are about even.  Sixty-four tokens a CTA, two tiles of rows
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
     const int ps = 1 << ps_shift;
     const int kvh = blockIdx.x % p.Hkv;
     TokenTile x;
+    let_second_start();
     RangeCheck ranges(sp);
     const bool here = token_tile(sp, blockIdx.x / p.Hkv, TPC, x);
     ranges.report(p);

@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kSelCtaWarps<WPU> * 32, 16 / kSelCtaWarps<WPU>
     const long long unit = (long long)(blockIdx.x / S) * UNITS + me;
     const int h = (int)(unit % p.Hkv);
     long long t0 = unit / p.Hkv * plan.TT;
+    const BehindFirst order(sp);
     RangeCheck ranges(sp);
     if (!sp.by_seq && t0 >= sp.n_tok) {  // a warp of its own without a row
         if (!sp.group_min) ranges.report(p);
@@ -550,12 +551,9 @@ static cudaError_t launch_select_t(const SparseParams &sp, const SelectPlan &pla
     cfg.blockDim = dim3(kSelCtaWarps<WPU> * 32);
     cfg.dynamicSmemBytes = UNITS * (frag + (size_t)plan.TT * plan.Wk * 4);
     cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = plan.S;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2]{};
+    cfg.numAttrs = second_launch_attrs(attr, plan.S, sp.group_min > 0);
+    cfg.attrs = attr;
     return cudaLaunchKernelEx(&cfg, kern, sp, plan);
 }
 

@@ -11,7 +11,7 @@
 // thread holds one page and 32 columns, takes each token's maximum and stores the score.  Then each warp
 // takes the pages of two tokens.
 //
-// 936 tokens of 8 kv heads over some 400 pages take 45.7 us in two waves of CTAs, the kernel of
+// 936 tokens of 8 kv heads over some 400 pages take 44.9 us in two waves of CTAs, the kernel of
 // select_pages.cuh 58; 3.3 us is the products' floor.  Half of a CTA's time is the selection, bound by
 // instructions (a warp counts a row's 400 scores six times), a quarter the set-up (queries to 8 bits).
 #include <type_traits>
@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kSelTcThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.Hkv;
     TokenTile x;
+    let_second_start();
     RangeCheck ranges(sp);
     const bool here = token_tile(sp, blockIdx.x / p.Hkv, TT, x);
     ranges.report(p);

@@ -28,6 +28,28 @@ __device__ __forceinline__ void quantise8(float (&x)[N], float a, float inv) {
     for (int i = 0; i < N; ++i) x[i] = r[i];
 }
 
+// Two launches of a call: the second, over the short sequences, may start beside the first's last CTAs (its
+// inputs are older than both launches, its rows are others) and ends behind it, its last CTA waiting for the
+// first launch; what follows on the stream follows both.
+__device__ __forceinline__ void let_second_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+struct BehindFirst {
+    const bool waits;
+    __device__ __forceinline__ explicit BehindFirst(const SparseParams &sp)
+        : waits(sp.group_min && blockIdx.x == gridDim.x - 1) {}
+    __device__ __forceinline__ ~BehindFirst() {
+        if (waits) asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+};
+// The launch attributes of such kernels: a cluster of S CTAs, and for a second launch the early start.
+inline int second_launch_attrs(cudaLaunchAttribute (&attr)[2], int S, bool second) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    return second ? 2 : 1;
+}
+
 // Each entry of a packed batch's q_start is looked at by one thread of the grid, whoever's rows it holds: a
 // search from a row may pass a malformed sequence by.  The loads are on their way while the kernel finds its
 // own sequence; report() follows.

@@ -1028,3 +1028,45 @@ def test_two_streams_at_once(pa):
     torch.cuda.synchronize()
     for s, (sel, out) in zip(sets, alone):
         assert torch.equal(s[1], sel) and torch.equal(s[2], out)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_what_follows_follows_both_launches(pa, graph):
+    """Where a call is two launches side by side, the next work on the stream sees all its rows and may
+    overwrite them."""
+    import torch
+    b = R.Batch(48, [700, 3, 1, 697], [1600, 1200, 900, 1500], 64, 2, 128, 16, "bf16")
+    assert b.T * 64 * b.width >= 1 << 23 and _shares(pa, b, 40)
+    env, scale = (_t(x) for x in b.envelopes())
+    d = b.device()
+    sel = torch.full((b.T, 2, 40), -9, dtype=torch.int32, device="cuda")
+    out, lists, outs = torch.empty_like(d["q"]), [], []
+
+    def step():
+        pa.paged_attn_select_pages(d["q"], env, scale, d["table"], d["lens"], True, None, 1, 2, sel, 16,
+                                   q_start=d["q_start"])
+        lists.append(sel.clone())
+        pa.paged_attn_fwd_sparse(d["q"], d["k"], d["v"], d["table"], d["lens"], True, None, lists[-1], 0.1, out, None,
+                                 q_start=d["q_start"])
+        outs.append(out.clone())
+        sel.fill_(-9)
+        out.fill_(7)
+    step()
+    torch.cuda.synchronize()
+    want = R.select(b.q64(), env.cpu().numpy(), scale.cpu().numpy(), b.table, b.rows(), 2, 16, 1, 2, 40)
+    np.testing.assert_array_equal(lists[0].cpu().numpy(), want)
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                step()
+        for _ in range(3):
+            g.replay()
+    else:
+        for _ in range(30):
+            step()
+    torch.cuda.synchronize()
+    for x, y in zip(lists, outs):
+        assert torch.equal(x, lists[0]) and torch.equal(y, outs[0])
+    assert (sel == -9).all() and (out == 7).all()
+    assert pa.paged_attn_last_error_word() == 0
