@@ -137,12 +137,17 @@ def _torch():
     return torch
 
 
+_codes: dict = {}  # torch dtype -> PA_*, filled at the first call
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
-    if t.dtype not in m:
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16})
+    code = _codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _ptr(t) -> Optional[int]:
@@ -194,8 +199,8 @@ def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
     # the current stream's handle, without building a Stream object (3 us on the Grace host)
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def dims_of(q, k_cache, block_table) -> PaDims:
