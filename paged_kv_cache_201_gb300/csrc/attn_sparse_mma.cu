@@ -10,8 +10,8 @@
 //     mma.m16n8k16 with float32 accumulators; P enters as a 16-bit high part plus its remainder, which
 //     keeps the weights to 2^-17.  Online softmax in the log2 domain, one pass over K and V.
 //   * the 4 S warp states are merged once at the end: each CTA leaves its four in shared memory and the
-//     cluster's CTAs share out the output columns, reading one another's states over distributed shared
-//     memory.  No workspace, no second launch, and a fixed order of sums.
+//     cluster's CTAs share out the output columns, S lanes to four of them, each lane reading one CTA's
+//     states over distributed shared memory.  No workspace, no second launch, and a fixed order of sums.
 // A decode step is bound by HBM: its lists differ between kv heads, so nothing is read twice.  256
 // sequences, 8 kv heads of 128, 64 pages of 16 tokens each (1.08 GB): 175 to 178 us, 6.1 TB/s, 90 % of the
 // copy rate.  One sequence of 131072 tokens, 128 of its 32-token pages: 12.7 us (2.5 at the copy rate), latency:
@@ -322,27 +322,42 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
     const int rows = min(16, p.G - rt * 16);
     const long long row0 = t_row * p.Hq + (long long)kvh * p.G + rt * 16;
     const uint32_t m_addr = sbase + Merge<D>::kAcc * 4, l_addr = m_addr + kNW * 16 * 4;
-    for (int idx = s * kMmaThreads + threadIdx.x; idx < rows * (D / 4); idx += S * kMmaThreads) {
-        const int r = idx / (D / 4), c = idx % (D / 4) * 4;
-        float M = kNegInf;
-        for (int cta = 0; cta < S; ++cta)
+    // Four columns of a row to S lanes, each the states of one CTA: every load of a lane is on its way before
+    // the first is needed, and the lanes' sums are added in a fixed order.
+    const int items = rows * (D / 4);
+    for (int i0 = (s * kMmaThreads + warp * 32) / S; i0 < items; i0 += kMmaThreads) {
+        const int idx = i0 + lane / S, cta = lane % S;
+        const int r = idx < items ? idx / (D / 4) : 0, c = idx % (D / 4) * 4;
+        float m[kNW], l[kNW];
+        float4 v[kNW];
 #pragma unroll
-            for (int w = 0; w < kNW; ++w) M = fmaxf(M, peer_load(peer_addr(m_addr + (w * 16 + r) * 4, cta)));
+        for (int w = 0; w < kNW; ++w) {
+            m[w] = peer_load(peer_addr(m_addr + (w * 16 + r) * 4, cta));
+            l[w] = peer_load(peer_addr(l_addr + (w * 16 + r) * 4, cta));
+            v[w] = peer_load4(peer_addr(sbase + ((w * 16 + r) * kRow + c) * 4, cta));
+        }
+        float M = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        for (int o = 1; o < S; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         const float mu = M == kNegInf ? 0.f : M;
         float L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int cta = 0; cta < S; ++cta) {
 #pragma unroll
-            for (int w = 0; w < kNW; ++w) {
-                const float x = exp2f(peer_load(peer_addr(m_addr + (w * 16 + r) * 4, cta)) - mu);
-                L = fmaf(x, peer_load(peer_addr(l_addr + (w * 16 + r) * 4, cta)), L);
-                const float4 v = peer_load4(peer_addr(sbase + ((w * 16 + r) * kRow + c) * 4, cta));
-                o.x = fmaf(x, v.x, o.x);
-                o.y = fmaf(x, v.y, o.y);
-                o.z = fmaf(x, v.z, o.z);
-                o.w = fmaf(x, v.w, o.w);
-            }
+        for (int w = 0; w < kNW; ++w) {
+            const float x = exp2f(m[w] - mu);
+            L = fmaf(x, l[w], L);
+            o.x = fmaf(x, v[w].x, o.x);
+            o.y = fmaf(x, v[w].y, o.y);
+            o.z = fmaf(x, v[w].z, o.z);
+            o.w = fmaf(x, v[w].w, o.w);
         }
+        for (int k = 1; k < S; k <<= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, k);
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, k);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, k);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, k);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
+        }
+        if (cta != 0 || idx >= items) continue;
         // a row without a key: 0 and -inf (a NaN sum stays a NaN)
         const float inv = L == 0.f ? 0.f : 1.f / L;
         uint2 packed;
