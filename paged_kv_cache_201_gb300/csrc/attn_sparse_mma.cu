@@ -82,6 +82,23 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
     long long t_row = unit / row_tiles;
     const BehindFirst order(sp);
     if (sp.by_seq && short_rows(sp, t_row, 1, t_row) == 0) return;  // the whole cluster: it has one token
+    const int pps = kMmaTileKeys >> ps_shift;  // list entries of a stage
+    // this CTA's entries [e0, e1): whole stages
+    const int per = ((sp.K + S - 1) / S + pps - 1) / pps * pps;
+    const int e0 = min((long long)s * per, (long long)sp.K), e1 = min(e0 + per, sp.K);
+    const int n_tiles = (e1 - e0 + pps - 1) / pps;
+    const int32_t *list = sp.sel + (t_row * p.Hkv + kvh) * sp.K;
+    // the producer's first entries are on their way while the row's sequence is looked up
+    auto listed = [&](int e) { return e < e1 ? __ldg(list + e) : -1; };
+    int j_cur = -1, j_nxt = -1;
+    if (warp == kNW) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        j_cur = listed(e0 + lane);
+        j_nxt = listed(e0 + 32 + lane);
+    }
     RangeCheck ranges(sp);
     const TokenRow tr = token_row(p, t_row, sp.n_tok, threadIdx.x == 0);
     if (!sp.group_min) ranges.report(p);  // else the tcgen05 kernel has
@@ -101,12 +118,6 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
     }
     __syncthreads();
 
-    const int pps = kMmaTileKeys >> ps_shift;  // list entries of a stage
-    // this CTA's entries [e0, e1): whole stages
-    const int per = ((sp.K + S - 1) / S + pps - 1) / pps * pps;
-    const int e0 = min((long long)s * per, (long long)sp.K), e1 = min(e0 + per, sp.K);
-    const int n_tiles = (e1 - e0 + pps - 1) / pps;
-    const int32_t *list = sp.sel + (t_row * p.Hkv + kvh) * sp.K;
     const int np = (tr.reach + ps - 1) >> ps_shift;
 
     const int g = lane >> 2, tq = lane & 3;
@@ -119,15 +130,10 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
 
     if (warp == kNW) {
         // ---------------------------------------------------------------- producer
-        if (lane == 0) {
-            tma_prefetch_desc(&tmK);
-            tma_prefetch_desc(&tmV);
-        }
         const uint32_t box_bytes = (uint32_t)(Geo<D>::NH * ps * 128);
         const int32_t *bt = p.block_table + (long long)tr.b * p.W;
-        // first token of the entry's page, -ps for an id outside the pool, -1 for an entry that lists nothing
-        auto entry = [&](int e) {
-            const int j = e < e1 ? __ldg(list + e) : -1;
+        // first token of a listed page, -ps for an id outside the pool, -1 for an entry that lists nothing
+        auto entry = [&](int j) {
             if (j < 0 || j >= np) return -1;
             const int id = __ldg(bt + j);
             if (id < 0 || id >= p.num_pages) {
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
             return id << ps_shift;
         };
         int batch = e0;
-        int cur = entry(batch + lane), nxt = n_tiles * pps > 32 ? entry(batch + 32 + lane) : -1;
+        int cur = entry(j_cur), nxt = entry(j_nxt);
         int issued = 0;
         for (int t = 0; t < n_tiles; ++t) {
             const int st = t % NSTAGE;
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
             if (first >= batch + 32) {
                 batch += 32;
                 cur = nxt;
-                nxt = entry(batch + 32 + lane);
+                nxt = entry(listed(batch + 32 + lane));
             }
             const int tok = __shfl_sync(0xffffffffu, cur, (first - batch + lane) & 31);
             const bool on = lane < pps && tok != -1;
