@@ -1,6 +1,9 @@
 // Attention over listed pages on CUDA cores: the kernel for f32.  One CTA per (query token, kv head, chunk
 // of HG query heads); see sparse_simt.cuh.  Five sequences of three tokens, lists of nine 16-token pages,
-// head_dim 64: 9.0 us, the latency of one list's pages after another.
+// head_dim 64: 6.7 us, the latency of one list's pages after another.  256 sequences, 8 kv heads of 128, G = 4,
+// lists of 64 16-token pages (2.15 GB): 494 us, 64 % of the copy rate, bound by the products' instructions
+// and by 255 registers (two CTAs an SM; three, 168 registers, take 602).  Two pages loaded together, entries
+// looked up 32 at a time: 560 us with one after the other (head_dim 256: 343 -> 262).
 #include "sparse_simt.cuh"
 
 namespace pa {
@@ -21,7 +24,7 @@ __global__ void __launch_bounds__(kSparseWarps * 32) paged_attn_sparse_simt_kern
     const TokenRow tr = token_row(p, t, sp.n_tok, threadIdx.x == 0);
     ranges.report(p);
     if (tr.b < 0) return;
-    simt_token<T, D, HG, kSparseWarps>(sp, tr, t, kvh, hc, scratch, threadIdx.x, [] { __syncthreads(); });
+    simt_token<T, D, HG, kSparseWarps, 2>(sp, tr, t, kvh, hc, scratch, threadIdx.x, [] { __syncthreads(); });
 }
 
 template <typename T>

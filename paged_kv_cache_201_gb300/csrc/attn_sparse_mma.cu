@@ -13,8 +13,8 @@
 //     cluster's CTAs share out the output columns, S lanes to four of them, each lane reading one CTA's
 //     states over distributed shared memory.  No workspace, no second launch, and a fixed order of sums.
 // A decode step is bound by HBM: its lists differ between kv heads, so nothing is read twice.  256
-// sequences, 8 kv heads of 128, 64 pages of 16 tokens each (1.08 GB): 175 to 178 us, 6.1 TB/s, 90 % of the
-// copy rate.  One sequence of 131072 tokens, 128 of its 32-token pages: 12.7 us (2.5 at the copy rate), latency:
+// sequences, 8 kv heads of 128, 64 pages of 16 tokens each (1.08 GB): 174 us, 6.2 TB/s, 91 % of the
+// copy rate.  One sequence of 131072 tokens, 128 of its 32-token pages: 11.6 us (2.5 at the copy rate), latency:
 // list, table, pages, products and the cluster's merge follow one another.
 #include "mma_common.cuh"
 #include "sparse_common.cuh"

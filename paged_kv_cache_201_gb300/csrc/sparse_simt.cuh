@@ -31,8 +31,9 @@ template <int D, int HG, int NW>
 constexpr int simt_scratch() { return NW * HG * (D + 2); }
 
 // Token t (reach and sequence in tr), kv head kvh, query heads hc HG .. + HG - 1 of the group; called by NW
-// warps of a CTA, tid 0 .. 32 NW - 1 among them, with `sync` a barrier over them.
-template <typename T, int D, int HG, int NW, typename Sync>
+// warps of a CTA, tid 0 .. 32 NW - 1 among them, with `sync` a barrier over them.  PAGES: listed pages whose
+// keys are loaded together.
+template <typename T, int D, int HG, int NW, int PAGES, typename Sync>
 __device__ __forceinline__ void simt_token(const SparseParams &sp, const TokenRow tr, long long t, int kvh, int hc,
                                            float *scratch, int tid, Sync sync) {
     constexpr int N = D / 8;
@@ -55,41 +56,62 @@ __device__ __forceinline__ void simt_token(const SparseParams &sp, const TokenRo
     const int32_t *bt = p.block_table + (long long)tr.b * p.W;
     const int np = (tr.reach + p.ps - 1) / p.ps;
     const long long row_elems = (long long)p.Hkv * D;
-    for (int e = 0; e < sp.K; ++e) {
-        const int j = __ldg(list + e);
-        if (j < 0 || j >= np) continue;
-        const int nv = min(p.ps, tr.reach - j * p.ps);
-        const int id = __ldg(bt + j);
-        const bool on = id >= 0 && id < p.num_pages;
-        if (!on && tid == 0) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
-        for (int k0 = 0; k0 < nv; k0 += NW * 4) {
-            const int key = k0 + stream;
-            const bool valid = key < nv;
-            float kk[N], vv[N];
-            const long long off = ((long long)id * p.ps + key) * row_elems + (long long)kvh * D + l8 * 4;
-            if (valid && on) {
-                load_row(static_cast<const T *>(p.k_cache) + off, kk);
-                load_row(static_cast<const T *>(p.v_cache) + off, vv);
-            } else {
+    for (int e0 = 0; e0 < sp.K; e0 += 32) {
+        // 32 entries' pages in two trips, a lane each
+        int my_j = e0 + lane < sp.K ? __ldg(list + e0 + lane) : -1, my_id = 0;
+        if (my_j >= np) my_j = -1;
+        if (my_j >= 0) my_id = __ldg(bt + my_j);
+        const bool out_of_pool = my_j >= 0 && (my_id < 0 || my_id >= p.num_pages);
+        if (out_of_pool && warp == 0) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+        unsigned live = __ballot_sync(0xffffffffu, my_j >= 0);
+        while (live) {
+            int nv[PAGES], id[PAGES];  // keys of a page that the token sees
+            bool on[PAGES];
 #pragma unroll
-                for (int i = 0; i < N; ++i) kk[i] = vv[i] = 0.f;
+            for (int u = 0; u < PAGES; ++u) {
+                const int src = live ? __ffs((int)live) - 1 : 0;
+                const int j = __shfl_sync(0xffffffffu, my_j, src);
+                id[u] = __shfl_sync(0xffffffffu, my_id, src);
+                on[u] = id[u] >= 0 && id[u] < p.num_pages;
+                nv[u] = live ? min(p.ps, tr.reach - j * p.ps) : 0;
+                live &= live - 1;
             }
+            int most = nv[0];
 #pragma unroll
-            for (int g = 0; g < HG; ++g) {
-                float s = 0.f;
+            for (int u = 1; u < PAGES; ++u) most = max(most, nv[u]);
+            for (int k0 = 0; k0 < most; k0 += NW * 4) {
+                const int key = k0 + stream;
+                float kk[PAGES][N], vv[PAGES][N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) s = fmaf(q[g][i], kk[i], s);
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                s += __shfl_xor_sync(0xffffffffu, s, 4);
-                s = valid ? s * p.scale_log2 : kNegInf;
-                const float mn = fmaxf(m[g], s);
-                const float mu = mn == kNegInf ? 0.f : mn;
-                const float al = exp2f(m[g] - mu), w = exp2f(s - mu);
-                m[g] = mn;
-                l[g] = l[g] * al + w;
+                for (int u = 0; u < PAGES; ++u) {
+                    const long long off = ((long long)id[u] * p.ps + key) * row_elems + (long long)kvh * D + l8 * 4;
+                    if (key < nv[u] && on[u]) {
+                        load_row(static_cast<const T *>(p.k_cache) + off, kk[u]);
+                        load_row(static_cast<const T *>(p.v_cache) + off, vv[u]);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[g][i] = fmaf(w, vv[i], acc[g][i] * al);
+                        for (int i = 0; i < N; ++i) kk[u][i] = vv[u][i] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < PAGES; ++u)
+#pragma unroll
+                    for (int g = 0; g < HG; ++g) {
+                        float s = 0.f;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) s = fmaf(q[g][i], kk[u][i], s);
+                        s += __shfl_xor_sync(0xffffffffu, s, 1);
+                        s += __shfl_xor_sync(0xffffffffu, s, 2);
+                        s += __shfl_xor_sync(0xffffffffu, s, 4);
+                        s = key < nv[u] ? s * p.scale_log2 : kNegInf;
+                        const float mn = fmaxf(m[g], s);
+                        const float mu = mn == kNegInf ? 0.f : mn;
+                        const float al = exp2f(m[g] - mu), w = exp2f(s - mu);
+                        m[g] = mn;
+                        l[g] = l[g] * al + w;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) acc[g][i] = fmaf(w, vv[u][i], acc[g][i] * al);
+                    }
             }
         }
     }
