@@ -846,7 +846,7 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
     sp.n_tok = n_tok;
     sp.K = top_k;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dims->dtype == PA_F32) return cuda_status(pa::launch_sparse_simt(sp, st));
+    if (dims->dtype == PA_F32) return cuda_status(pa::launch_sparse_simt(sp, device_sm_count(), st));
     CUtensorMap tmk, tmv;
     if ((rc = make_pool_map(&tmk, k_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;
     if ((rc = make_pool_map(&tmv, v_cache, dims, dims->head_dim / 64)) != PA_OK) return rc;

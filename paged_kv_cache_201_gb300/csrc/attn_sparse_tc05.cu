@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
             for (int tok = 0; tok < x.nt; ++tok) {
                 const TokenRow tr{x.b, s_reach[tok]};
                 for (int hc = 0; hc * 4 < p.G; ++hc) {
-                    simt_token<T, D, 4, 8, 1>(sp, tr, x.tok0 + tok, kvh, hc, scratch, tid - 128,
+                    simt_token<T, D, 4, 8, 1, false>(sp, tr, x.tok0 + tok, kvh, hc, scratch, tid - 128, 0, 1,
                                              [] { named_bar_sync(1, 256); });
                     named_bar_sync(1, 256);  // before the scratch is used again
                 }

@@ -140,6 +140,7 @@ constexpr int kSparseTc05MaxPages = 4608;
 int sparse_tile_tokens(int G);
 cudaError_t launch_sparse_tc05(const SparseParams &p, int dtype, const CUtensorMap &tmq, const CUtensorMap &tmk,
                                const CUtensorMap &tmv, cudaStream_t stream);
-cudaError_t launch_sparse_simt(const SparseParams &p, cudaStream_t stream);  // f32
+// f32: CUDA cores, a list split over a cluster when there are few rows
+cudaError_t launch_sparse_simt(const SparseParams &p, int sms, cudaStream_t stream);
 
 }  // namespace pa

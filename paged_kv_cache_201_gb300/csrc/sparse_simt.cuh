@@ -32,10 +32,11 @@ constexpr int simt_scratch() { return NW * HG * (D + 2); }
 
 // Token t (reach and sequence in tr), kv head kvh, query heads hc HG .. + HG - 1 of the group; called by NW
 // warps of a CTA, tid 0 .. 32 NW - 1 among them, with `sync` a barrier over them.  PAGES: listed pages whose
-// keys are loaded together.
-template <typename T, int D, int HG, int NW, int PAGES, typename Sync>
+// keys are loaded together.  CLUSTER: CTA s of a cluster of S takes the s-th part of the list, and they
+// share out the merge; `sync` is a barrier over the cluster, passed once more by the caller at the end.
+template <typename T, int D, int HG, int NW, int PAGES, bool CLUSTER, typename Sync>
 __device__ __forceinline__ void simt_token(const SparseParams &sp, const TokenRow tr, long long t, int kvh, int hc,
-                                           float *scratch, int tid, Sync sync) {
+                                           float *scratch, int tid, int s, int S, Sync sync) {
     constexpr int N = D / 8;
     const FwdParams &p = sp.f;
     const int lane = tid & 31, warp = tid >> 5;
@@ -56,9 +57,11 @@ __device__ __forceinline__ void simt_token(const SparseParams &sp, const TokenRo
     const int32_t *bt = p.block_table + (long long)tr.b * p.W;
     const int np = (tr.reach + p.ps - 1) / p.ps;
     const long long row_elems = (long long)p.Hkv * D;
-    for (int e0 = 0; e0 < sp.K; e0 += 32) {
+    const int part = CLUSTER ? (sp.K + S - 1) / S : sp.K;
+    const int e_first = CLUSTER ? min(s * part, sp.K) : 0, e_last = CLUSTER ? min(e_first + part, sp.K) : sp.K;
+    for (int e0 = e_first; e0 < e_last; e0 += 32) {
         // 32 entries' pages in two trips, a lane each
-        int my_j = e0 + lane < sp.K ? __ldg(list + e0 + lane) : -1, my_id = 0;
+        int my_j = e0 + lane < e_last ? __ldg(list + e0 + lane) : -1, my_id = 0;
         if (my_j >= np) my_j = -1;
         if (my_j >= 0) my_id = __ldg(bt + my_j);
         const bool out_of_pool = my_j >= 0 && (my_id < 0 || my_id >= p.num_pages);
@@ -139,19 +142,24 @@ __device__ __forceinline__ void simt_token(const SparseParams &sp, const TokenRo
         }
     }
     sync();
-    for (int idx = tid; idx < gn * D; idx += NW * 32) {
+    auto state = [&](const float *x, int cta) { return CLUSTER ? peer_load(peer_addr(smem_u32(x), cta)) : *x; };
+    const int ctas = CLUSTER ? S : 1;
+    for (int idx = (CLUSTER ? s * NW * 32 : 0) + tid; idx < gn * D; idx += ctas * NW * 32) {
         const int g = idx / D, d = idx % D;
-        float M = kNegInf;
+        float M = kNegInf, L = 0.f, o = 0.f;
+#pragma unroll 4
+        for (int cta = 0; cta < ctas; ++cta)
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * HG + g]);
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, state(s_m + w * HG + g, cta));
         const float mu = M == kNegInf ? 0.f : M;
-        float L = 0.f, o = 0.f;
+#pragma unroll 4
+        for (int cta = 0; cta < ctas; ++cta)
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float x = exp2f(s_m[w * HG + g] - mu);
-            L = fmaf(x, s_l[w * HG + g], L);
-            o = fmaf(x, s_acc[(w * HG + g) * D + d], o);
-        }
+            for (int w = 0; w < NW; ++w) {
+                const float x = exp2f(state(s_m + w * HG + g, cta) - mu);
+                L = fmaf(x, state(s_l + w * HG + g, cta), L);
+                o = fmaf(x, state(s_acc + (w * HG + g) * D + d, cta), o);
+            }
         // a row without a key: 0 and -inf (a NaN sum stays a NaN)
         static_cast<T *>(p.out)[(row0 + g) * D + d] = from_float<T>(L == 0.f ? 0.f : o / L);
         if (d == 0 && p.lse) p.lse[row0 + g] = L == 0.f ? kNegInf : M * kLn2 + logf(L);

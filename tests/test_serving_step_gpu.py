@@ -548,6 +548,19 @@ def test_attend_few_rows_long_lists(pa):
             _check_attend(pa, b, _lists(b, 300))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(7, 1, 64), (8, 2, 128), (3, 1, 256)])
+def test_attend_few_rows_split_lists(pa, dtype, Hq, Hkv, D):
+    """Lists split over clusters of every size, parts of them empty or cut short, entries repeated."""
+    b = R.Batch(D + 1, [1, 0, 2], [5000, 90, 700], Hq, Hkv, D, 16, dtype, q_pad=1)
+    for K in (15, 16, 33, 65, 129, 300):
+        sel = _lists(b, K, seed=K)
+        sel[1, 0, :K // 2] = -1
+        sel[2, 0, -3:] = sel[2, 0, 0]
+        _check_attend(pa, b, sel)
+    assert pa.paged_attn_last_error_word() == 0
+
+
 # Runs of tokens long enough, with the lists below, for the kernel that reads the union of their lists.
 CHUNKS = [1, 230, 0, 16, 15, 1, 129]
 CHUNK_LENS = [90, 500, 5, 16, 700, 64, 129]
