@@ -597,8 +597,9 @@ cudaError_t launch_select_d(const SparseParams &sp, int dtype, int sms, cudaStre
         return NT == 1 ? launch_select_t<D, 1, kRowWarps>(sp, plan, stream) : launch_select_t<D, 2, kRowWarps>(sp, plan, stream);
     // Few rows: a cluster shares their pages, each CTA at least two tiles for each of its warps.
     while (plan.S < 8 && rows * plan.S * 2 <= 2ll * sms && p.W >= plan.S * 2 * 2 * kSelWarps * 16) plan.S *= 2;
-    // Long rows on few CTAs: twice the warps.
-    if (rows * plan.S <= sms && p.W > 1024) {
+    // Long rows, up to four CTAs a multiprocessor: twice the warps (152 rows of up to 3900 pages, head_dim 128: 42
+    // -> 31 us, 320 rows of 2500: 51 -> 49; 800 rows of 1500: 64 -> 67).
+    if (rows * plan.S <= 4ll * sms && p.W > 1024) {
         if (NT == 1) return launch_select_t<D, 1, 8>(sp, plan, stream);
         if (NT == 2) return launch_select_t<D, 2, 8>(sp, plan, stream);
         return launch_select_t<D, 4, 8>(sp, plan, stream);
