@@ -808,6 +808,7 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
     sp.sink = sink_pages;
     sp.local = local_pages;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dims->bt_stride <= top_k) return cuda_status(pa::launch_select_all(sp, device_sm_count(), st));
     // Sequences with half a tile of query tokens or more go to the tcgen05 kernel once there is work enough for
     // its CTAs (one an SM, with a long set-up); in a packed batch both kernels find theirs from q_start.
     // Measured, in microseconds, tcgen05 and mma.sync: 1024 tokens of 8 kv heads, G = 4, 512 pages (2^24 scores

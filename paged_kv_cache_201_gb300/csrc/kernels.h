@@ -122,6 +122,7 @@ struct SparseParams {
 constexpr size_t kSelectTc05MaxSmem = 224 * 1024;
 size_t select_tc05_smem(int D, int N, int TT, int W);
 int select_tile_tokens(int D, int G, int W);
+cudaError_t launch_select_all(const SparseParams &p, int sms, cudaStream_t stream);  // rows of at most top_k pages
 cudaError_t launch_select_tc05(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_select_pages_64(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_select_pages_128(const SparseParams &p, int dtype, int sms, cudaStream_t stream);

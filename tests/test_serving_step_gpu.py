@@ -476,6 +476,28 @@ def test_select_long(pa, B, pages, K, ps):
     _check_select(pa, b, 1, 2, K, env=(np.stack([lo, hi], 2), rng.uniform(0.5, 1, (b.P, 1)).astype(np.float32)))
 
 
+@pytest.mark.parametrize("Hkv,ps", [(1, 16), (3, 64), (8, 32)])
+def test_select_rows_shorter_than_the_list(pa, Hkv, ps):
+    """Tables no wider than top_k: every reachable page, for few tokens and for many; rows of no sequence stay."""
+    for q_lens, seq_lens in (([1], [1]), ([3, 0, 1, 70], [200, 5, 90, 130]), ([600] * 9 + [1], [640, 600] * 5)):
+        b = R.Batch(50, q_lens, seq_lens, 2 * Hkv, Hkv, 64, ps, "bf16", q_pad=5)
+        W_ = b.width
+        for K in (W_, W_ + 1, W_ + 37, 200):
+            _check_select(pa, b, 0, 1, K)
+        _check_select(pa, b, 0, 0, W_, causal=False)
+        qo = [int(L) - 2 * n - 9 for n, L in zip(q_lens, b.seq_lens)]  # the first tokens see nothing
+        _check_select(pa, b, 1, 0, W_, q_offset=qo)
+    b = R.Batch(51, [4] * 3, [60, 4, 33], 2 * Hkv, Hkv, 64, ps, "f32")
+    _check_select(pa, b, 0, 0, b.width, uniform=True)
+    b = R.Batch(52, [1, 40], [300, 290], 2, 1, 64, 16, "bf16")
+    b.table = np.ascontiguousarray(b.table[:, :3])
+    b.width = 3
+    env = b.envelopes()
+    want = R.select(b.q64(), *env, b.table, b.rows(), 1, 16, 0, 0, 4)
+    np.testing.assert_array_equal(_run_select(pa, b, *env, 0, 0, 4), want)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_SEQ_CLIPPED
+
+
 def test_select_bad_pages(pa):
     """Ids outside the pool score 0 and are reported."""
     b = R.Batch(8, [2, 1], [800, 600], 4, 2, 128, 16, "bf16")
