@@ -689,8 +689,8 @@ int make_sparse_q_map(CUtensorMap *m, const void *q, const pa_dims *d, int64_t n
 // measured rates: the first takes c a 128-key tile of the union and some 8 to set up, in waves of one CTA
 // an SM; the second reads its lists at 8.9 TB/s from L2.  The union is taken as half of the tile's lists'
 // total, at most the whole table: neighbouring tokens' lists overlap.  Measured with random lists of 64 of
-// 512 16-token pages, 8 kv heads, G = 4, bf16: 128 tokens 82 against 71 us, 256 tokens 82 against 128,
-// 1024 tokens 156 against 485.
+// 512 16-token pages, 8 kv heads, G = 4, bf16 and f16: 128 tokens 82 against 71 us, 256 tokens 82 against
+// 128, 1024 tokens 156 against 485.
 bool sparse_shares_pages(const pa_dims *d, int64_t n_tok, bool packed, int top_k, float scale, int sms) {
     const int G = d->num_q_heads / d->num_kv_heads, tile = pa::sparse_tile_tokens(G);
     if (d->dtype == PA_F32 || d->head_dim == 256 || tile == 0 || !(scale > 0.f) ||
@@ -699,7 +699,7 @@ bool sparse_shares_pages(const pa_dims *d, int64_t n_tok, bool packed, int top_k
     // a batch of mostly single tokens, or of too few for half a tile
     if (packed ? n_tok < 2 * (int64_t)d->batch : d->q_len < (tile + 1) / 2) return false;
     const double W = d->bt_stride, K = top_k < W ? top_k : W;
-    const double c = (d->dtype == PA_BF16 ? 1.14 : 0.97) * (d->head_dim == 64 ? 0.95 : 1.0);
+    const double c = d->head_dim == 64 ? 1.08 : 1.14;
     const double whole = tile * K / 2, pages = whole < W ? whole : W;
     const double tiles = packed ? ceil((double)n_tok / tile) : (double)d->batch * ((d->q_len + tile - 1) / tile);
     const double shared = ceil(tiles * d->num_kv_heads / sms) * (pages * d->page_size / 128 * c + 8);

@@ -12,19 +12,20 @@
 //               token lists its page (one bit), so its offset in exp2(s c + off) is the negated maximum or
 //               -inf: the mask costs no instruction for a key.  A block that no token of the warp's rows
 //               lists is passed by, its P 0.  O is rescaled in tensor memory only when the
-//               maximum grows by more than 2^8.  P is written over S as 16-bit pairs: high part and
-//               remainder for bf16 (two products), alone for f16 (2^-12 of itself).  At the end they scale
-//               the rows by their sums and store them.
+//               maximum has grown by a few powers of two (struct Scaling).  P is written over S as 16-bit
+//               pairs, high part and remainder (two products): 2^-16 of itself for bf16, 2^-22 for f16 down to
+//               its quantum.  At the end they scale the rows by their sums and store them.
 // A masked key's weight is 0, but 0 times an infinity or a NaN in V is a NaN.  Such values are rare, so no
 // product is guarded: a CTA whose result is not finite, and one whose lists name a page twice (it counts
 // twice), does its tokens again on CUDA cores, where a key that is not seen is not multiplied.
 // The products run over all rows of every listed page, whoever lists it: at random lists (64 of some 400
-// pages a token, 32 tokens, G = 4) six times what the lists ask for, at 1.0 us a tile in f16 and 1.15 in
-// bf16 (head_dim 128).  936 such tokens of 8 kv heads take 126 us (f16); read token by token their lists
-// move 3.9 GB through L2, 451 us.  Lists that overlap more cost less here.
-// What bounds it: the pages' way from L2 (890 MB; loads alone take 111 us) and the softmax's chain (116 us
-// without loads and products; products alone 86) are about even.  Sixty-four tokens a CTA, two tiles of rows
-// over the same pages, halve the loads, but leave a thread a whole row: 131 us.
+// pages a token, 32 tokens, G = 4) six times what the lists ask for, at 1.15 us a tile (head_dim 128).  936
+// such tokens of 8 kv heads take 145 us in either type; read token by token their lists move 3.9 GB through L2,
+// 451 us.  Lists that overlap more cost less here.
+// What bounds it: the softmax's chain (131 us in f16, 124 in bf16, without loads and products), before the
+// products (110 alone) and the pages' way from L2 (890 MB, 99 alone).  With f16 weights of one part, 11 bits,
+// f16 took 127 us, 5 % further from the exact result.  Sixty-four tokens a CTA, two tiles of rows over the
+// same pages, halve the loads, but leave a thread a whole row: 131 us then.
 #include <float.h>
 
 #include <type_traits>
@@ -42,7 +43,21 @@ constexpr int kSt5Threads = 384, kSt5Warps = kSt5Threads / 32;
 constexpr uint32_t kSt5LoadRegs = 64, kSt5SoftmaxRegs = 208;
 constexpr int kSt5Half = 128 * 128;    // bytes of one 64-column half of a 128-row tile
 constexpr uint32_t kSt5ColO = 256;
-constexpr float kSt5Rescale = 8.f;     // rescale O only when the maximum grows by more than 2^8
+
+// A row's weights are p = exp2(s c - m), m its maximum less kTop, and O is rescaled only when the maximum has
+// grown by more than kGrow powers of two: the largest p lies in [2^kTop, 2^(kTop + kGrow)].  bf16 has float32's
+// exponents.  f16 has a quantum of 2^-24 and ends at 2^16, so there the weights are moved up: those down to
+// 2^-24 of a row's largest keep 11 bits in the pair, and none loses more than 2^-35 of the largest.  A smaller
+// kGrow would move them further up, but 936 tokens that take 145 us with 5 (and with 8) take 155 with 3.
+template <typename T>
+struct Scaling {
+    static constexpr float kTop = 0.f, kGrow = 8.f;
+};
+template <>
+struct Scaling<__half> {
+    static constexpr float kTop = 10.f, kGrow = 5.f;
+};
+
 enum { S_QF = 0, S_KF = 1, S_KE = 3, S_VF = 5, S_VE = 7, S_PF = 9, S_COUNT = 11 };
 
 // One listed page of the union: its logical index and the tokens that list it.
@@ -70,12 +85,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // P for 32 keys of one row, two 16-key blocks with their own offsets: p = exp2(s c + off[block]); the sums of
-// the p go to l, the 32 columns at taddr receive [16 of high parts | 16 of remainders] (bf16) or the p as
-// f16 pairs in the first 16.  any: whether a row of the warp has the block listed; its P is 0 if not.
+// the p go to l, the 32 columns at taddr receive [16 of high parts | 16 of remainders], 16-bit pairs.  any:
+// whether a row of the warp has the block listed; its P is 0 if not.
 template <typename T>
 __device__ __forceinline__ void block_exp(const uint32_t (&u)[32], float c, const float (&off)[2], const bool (&any)[2],
                                           float2 &l, uint32_t taddr) {
-    constexpr bool kSplit = !std::is_same<T, __half>::value;
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -86,14 +100,17 @@ __device__ __forceinline__ void block_exp(const uint32_t (&u)[32], float c, cons
                                       make_float2(c, c), make_float2(off[b], off[b]));
                 const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
                 l = add2(l, make_float2(p0, p1));
-                if (kSplit) {
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                     // the high parts truncated to their top 16 bits; p - high is then exact in float32 and below
                     // 2^-7 p, and its bf16 rounding leaves P within 2^-16 of p
                     hi[i] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
                     lo[i] = MmaOp<T>::pack(p0 - __uint_as_float(__float_as_uint(p0) & 0xffff0000u),
                                            p1 - __uint_as_float(__float_as_uint(p1) & 0xffff0000u));
                 } else {
+                    // rounded to nearest, the remainder exact before its own rounding: within 2^-22 of p, or 2^-25
                     hi[i] = MmaOp<T>::pack(p0, p1);
+                    const float2 h = MmaOp<T>::unpack(hi[i]);
+                    lo[i] = MmaOp<T>::pack(p0 - h.x, p1 - h.y);
                 }
             }
         } else {
@@ -102,7 +119,7 @@ __device__ __forceinline__ void block_exp(const uint32_t (&u)[32], float c, cons
         }
     }
     tc05::st_16cols(taddr, hi);
-    if (kSplit) tc05::st_16cols(taddr + 16u, lo);
+    tc05::st_16cols(taddr + 16u, lo);
 }
 
 }  // namespace
@@ -112,7 +129,6 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
     paged_attn_sparse_tc05_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                                   const __grid_constant__ CUtensorMap tmV, const SparseParams sp, int ps_shift,
                                   int TPC, uint32_t idesc_qk, uint32_t idesc_pv) {
-    constexpr bool kSplit = !std::is_same<T, __half>::value;
     constexpr int NH = D / 64, kTile = NH * kSt5Half;  // a tile of Q, K or V: NH 64-column halves
     const FwdParams &p = sp.f;
     extern __shared__ uint8_t smem_raw[];
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
                                 const uint32_t vlo = dv + (uint32_t)kk * (2048u >> 4);
                                 const uint32_t pa = pcol + 32u * (uint32_t)(kk >> 1) + 8u * (uint32_t)(kk & 1);
                                 tc05::mma_ts_lh(tm + kSt5ColO, pa, vlo, dhi, idesc_pv, (t > 1 || kk > 0) ? 1u : 0u);
-                                if (kSplit) tc05::mma_ts_lh(tm + kSt5ColO, pa + 16u, vlo, dhi, idesc_pv, 1u);
+                                tc05::mma_ts_lh(tm + kSt5ColO, pa + 16u, vlo, dhi, idesc_pv, 1u);
                             }
                             tc05::commit(bar(S_VE + slot));  // V slot free, O holds this tile's product
                         }
@@ -377,8 +393,8 @@ __global__ void __launch_bounds__(kSt5Threads, 1)
             look_up(t + 1);
             named_bar_sync(1, 256);
             mx = fmaxf(mx, s_xmax[st][hh ^ 1][r]);
-            const float m_new = fmaxf(m_used, mx * c2);
-            const bool need = m_new > m_used + kSt5Rescale;  // also when m_used is -inf and m_new is not
+            const float m_new = fmaxf(m_used, mx * c2 - Scaling<T>::kTop);
+            const bool need = m_new > m_used + Scaling<T>::kGrow;  // also when m_used is -inf and m_new is not
             if (__any_sync(0xffffffffu, need || bad) && !(bad = __any_sync(0xffffffffu, bad))) {
                 const float alpha = need ? exp2f(m_used - m_new) : 1.f;
                 if (need) {
