@@ -435,7 +435,9 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
  * attend to the keys below the token's reach of the logical pages sel[t][h][0 .. top_k).  Entries below
  * 0, or at or past ceil(reach / page_size), list nothing; the order is free and an index listed twice
  * counts twice.  out [tokens, Hq, D] in dims->dtype (rounded once, to nearest even), lse [tokens, Hq]
- * float32 or NULL; a row without a key gets 0 and -inf.  q may be a view (dims->q_stride).
+ * float32 or NULL; a row without a key gets 0 and -inf.  q may be a view (dims->q_stride).  The 16-bit types'
+ * weights meet V as a high part and a remainder of the type: bf16 within 2^-16 of a weight, f16 within 2^-20
+ * of it or 2^-35 of the row's largest.
  * top_k <= PA_SPARSE_MAX_TOP_K (PA_EUNSUPPORTED).
  */
 int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,

@@ -8,7 +8,9 @@
 //   * warps 0-3 each own 16 keys of a stage, all in one page since page_size >= 16, so a key's mask is one
 //     count for each warp and stage: min(16, reach - first key).  S = Q K^T and O += P V are
 //     mma.m16n8k16 with float32 accumulators; P enters as a 16-bit high part plus its remainder, which
-//     keeps the weights to 2^-17.  Online softmax in the log2 domain, one pass over K and V.
+//     keeps the weights to 2^-17 in bf16, to 2^-22 in f16.  f16 has a quantum of 2^-24, so there P is moved up
+//     by 2^15 (the largest weight is 1, the largest f16 below 2^16): none loses more than 2^-40 of the largest.
+//     Online softmax in the log2 domain, one pass over K and V.
 //   * the 4 S warp states are merged once at the end: each CTA leaves its four in shared memory and the
 //     cluster's CTAs share out the output columns, S lanes to four of them, each lane reading one CTA's
 //     states over distributed shared memory.  No workspace, no second launch, and a fixed order of sums.
@@ -16,6 +18,8 @@
 // sequences, 8 kv heads of 128, 64 pages of 16 tokens each (1.08 GB): 174 us, 6.2 TB/s, 91 % of the
 // copy rate.  One sequence of 131072 tokens, 128 of its 32-token pages: 11.6 us (2.5 at the copy rate), latency:
 // list, table, pages, products and the cluster's merge follow one another.
+#include <type_traits>
+
 #include "mma_common.cuh"
 #include "sparse_common.cuh"
 
@@ -26,6 +30,9 @@ using namespace mmac;
 namespace {
 
 constexpr int kNW = kMmaConsumerWarps;
+
+template <typename T>
+constexpr float kWeightUp = std::is_same<T, __half>::value ? 32768.f : 1.f;
 
 template <int D>
 struct Merge {  // a CTA's states: acc [4][16][D + 4], m [4][16], l [4][16]
@@ -218,15 +225,16 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
                 float rs_a = 0.f, rs_b = 0.f;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float p0 = exp2f(sc[n][0] - mu_a), p1 = exp2f(sc[n][1] - mu_a);
-                    const float p2 = exp2f(sc[n][2] - mu_b), p3 = exp2f(sc[n][3] - mu_b);
+                    float p0 = exp2f(sc[n][0] - mu_a), p1 = exp2f(sc[n][1] - mu_a);
+                    float p2 = exp2f(sc[n][2] - mu_b), p3 = exp2f(sc[n][3] - mu_b);
+                    rs_a += p0 + p1;
+                    rs_b += p2 + p3;
+                    p0 *= kWeightUp<T>, p1 *= kWeightUp<T>, p2 *= kWeightUp<T>, p3 *= kWeightUp<T>;
                     ph[n][0] = Op::pack(p0, p1);
                     ph[n][1] = Op::pack(p2, p3);
                     const float2 ha = Op::unpack(ph[n][0]), hb = Op::unpack(ph[n][1]);
                     pl[n][0] = Op::pack(p0 - ha.x, p1 - ha.y);
                     pl[n][1] = Op::pack(p2 - hb.x, p3 - hb.y);
-                    rs_a += p0 + p1;
-                    rs_b += p2 + p3;
                 }
                 l_a = l_a * al_a + rs_a;
                 l_b = l_b * al_b + rs_b;
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(kMmaThreads, D == 256 ? 1 : 2)
         }
         if (cta != 0 || idx >= items) continue;
         // a row without a key: 0 and -inf (a NaN sum stays a NaN)
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = L == 0.f ? 0.f : 1.f / (L * kWeightUp<T>);
         uint2 packed;
         packed.x = Op::pack(o.x * inv, o.y * inv);
         packed.y = Op::pack(o.z * inv, o.w * inv);

@@ -62,3 +62,24 @@ def test_small_weights_runs_of_tokens(pa, D, Hq, Hkv, x, sink):  # noqa: F811
     sel = np.broadcast_to(np.arange(n // 16, dtype=np.int32), (b.T, Hkv, n // 16)).copy()
     assert _shares(pa, b, n // 16, scale=LN2)
     _check_sink(pa, b, n, sel)
+
+
+@pytest.mark.parametrize("x", [14, 17, 20, 24, 25])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 3, 3), (256, 6, 2)])
+@pytest.mark.parametrize("q_lens", [[1], [1] * 40])
+def test_small_weights_single_tokens(pa, D, Hq, Hkv, x, q_lens):  # noqa: F811
+    """The kernel that reads a token's own list, split over a cluster or not."""
+    n = 1024
+    b = _sink_batch(q_lens, n, D, Hq, Hkv, x, 37, x)
+    sel = np.broadcast_to(np.arange(n // 16, dtype=np.int32), (b.T, Hkv, n // 16)).copy()
+    assert not _shares(pa, b, n // 16, scale=LN2)
+    _check_sink(pa, b, n, sel)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [200, 200]])
+def test_large_scores(pa, q_lens):  # noqa: F811
+    """Scores up to 2^13 apart, the largest met late: the weights' scaling follows the maximum."""
+    b = R.Batch(5, q_lens, [700, 650], 8, 2, 128, 16, "f16")
+    sel = _lists(b, 44)
+    for scale in (1.0, 30.0):
+        _check_attend(pa, b, sel, scale=scale)
