@@ -416,8 +416,9 @@ int paged_attn_append(const void *k_new, const void *v_new, const int32_t *slots
  *           steps as for the envelope; a = 0 or not finite: qi = 0)
  *   s     = max over the G heads of  sum_d  qi_d > 0 ? qi_d * k_env[1][d] : qi_d * k_env[0][d]
  *   score = float(s) * k_env_scale, rounded once; +inf where k_env_scale is +inf (or a NaN)
- * s bounds q.k over the page's keys up to the rounding to 8 bits; it is an exact integer below 2^24, so
- * the selection does not depend on the order of any sum.
+ * s bounds q.k over the page's keys from above, up to the rounding to 8 bits; it is an exact integer below
+ * 2^24, so the selection does not depend on the order of any sum.  The pages of largest weight are meant for
+ * attention with a scale that is not negative (for a negative one pass -q).
  *   sel [tokens, Hkv, top_k] int32: the selected logical pages in ascending order, then -1.
  * q has dims->dtype; k_env_scale is not negative, as paged_attn_append writes it.  sel may not overlap an
  * input.  A page id outside [0, num_pages) counts as score 0 and sets PA_ERRBIT_PAGE_RANGE.

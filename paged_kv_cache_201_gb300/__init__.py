@@ -857,10 +857,13 @@ def attention_sparse(q, k_cache, v_cache, k_env, k_env_scale, block_table, seq_l
     """Select top_k pages per query token and kv head by their key envelopes and attend over them: q
     [B, Sq, Hq, D], or packed [T, Hq, D] with q_start [B + 1].  Rows of a packed q that belong to no
     sequence are not written.  Returns ``out``, or a tuple with ``lse`` (want_lse) and the selected
-    pages (want_pages) after it."""
+    pages (want_pages) after it.  scale must not be negative: the envelopes bound q.k from above, and a
+    negative one would keep the pages of least weight."""
     torch = _torch()
     if scale is None:
         scale = q.shape[-1] ** -0.5
+    if not scale >= 0:
+        raise ValueError(f"scale must not be negative, got {scale} (pages are selected by an upper bound of q.k)")
     sel = torch.empty((*q.shape[:-2], k_cache.shape[2], int(top_k)), dtype=torch.int32, device=q.device)
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
