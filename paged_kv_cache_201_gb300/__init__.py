@@ -828,7 +828,8 @@ def attention_varlen(q, k_cache, v_cache, block_table, seq_lens, q_start, *, cau
 def step_tables(cached_lens, new_lens, free_pages, free_count, block_table, total_tokens: int, page_size: int,
                 num_pages: int, stream=None):
     """``paged_attn_step_tables`` with its outputs allocated: updates block_table in place and returns
-    ``(seq_lens, q_offset, q_start, slots, free_left)``."""
+    ``(seq_lens, q_offset, q_start, slots, free_left)``.  An empty batch gives no slots (all -1) and
+    leaves free_count (clamped to the stack, as otherwise)."""
     torch = _torch()
     B = block_table.shape[0]
     def i32(n):
@@ -839,6 +840,11 @@ def step_tables(cached_lens, new_lens, free_pages, free_count, block_table, tota
             t.record_stream(stream)
     paged_attn_step_tables(cached_lens, new_lens, free_pages, free_count, block_table, seq_lens, q_offset, q_start,
                            slots, free_left, page_size, num_pages, stream)
+    if B == 0:  # the call writes nothing then
+        with torch.cuda.stream(stream):
+            q_start.zero_()
+            slots.fill_(-1)
+            free_left.copy_(free_count.clamp(0, free_pages.shape[0]))
     return seq_lens, q_offset, q_start, slots, free_left
 
 
