@@ -399,7 +399,8 @@ int paged_attn_step_tables(const int32_t *cached_lens, const int32_t *new_lens, 
  * in float32, each operation rounded to nearest even (a = 0: all 0).  Keys with a non-finite element
  * give k_env 0 and k_env_scale +inf.  Rows 0 .. r must all hold tokens by then, and the new tokens of
  * one page must lie within 64 consecutive ones, as paged_attn_step_tables gives them (without envelopes
- * the tokens may come in any order).  A slot named twice holds either token's elements.
+ * the tokens may come in any order); an envelope can miss keys otherwise, and nothing reports it.  A slot named
+ * twice holds either token's elements, and its page has no bound: k_env 0 and k_env_scale +inf.
  * dims->batch, num_q_heads, bt_stride and q_stride are not used (num_q_heads a multiple of
  * num_kv_heads all the same).
  */

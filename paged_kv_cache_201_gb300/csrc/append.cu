@@ -8,8 +8,8 @@
 // order, so an envelope is the same bits whether a page is filled at once or token by token.
 // Kept apart, the long chain of an envelope (slots, rows, reduction, division) overlaps the copies; where
 // few pages close, as in a prompt, the CTA's warps share a page's rows.  6656 prompt tokens of 8 heads of
-// 128 (f16, 64-token pages) take 14.6 us, 56 % of the copy rate; with the closing warps among the copying
-// ones they took 21, and the copies alone take 10.7.  A decode step of 256 tokens takes 5.3 us, a chain
+// 128 (f16, 64-token pages) take 13.7 us, 59 % of the copy rate; with the closing warps among the copying
+// ones they took 21, and the copies alone take 10.7.  A decode step of 256 tokens takes 5.4 us, a chain
 // of three trips to memory.
 #include <float.h>
 
@@ -109,10 +109,10 @@ __device__ __forceinline__ bool row_bounds(const AppendParams &p, const Closing 
 
 // A closing page's envelope by one warp.
 template <typename T, int D>
-__device__ __forceinline__ void warp_envelope(const AppendParams &p, const Closing &cl, int h, int lane) {
+__device__ __forceinline__ void warp_envelope(const AppendParams &p, const Closing &cl, bool twice, int h, int lane) {
     using R = Rows<T, D>;
     float lo[R::CPL][R::E], hi[R::CPL][R::E];
-    const bool odd = row_bounds<T, D>(p, cl, h, 0, cl.row + 1, lo, hi, lane);
+    const bool odd = row_bounds<T, D>(p, cl, h, 0, cl.row + 1, lo, hi, lane) || twice;
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < R::CPL; ++i)
@@ -151,14 +151,14 @@ constexpr int kAppendThreads = 128, kAppendWarps = 4;
 // The envelopes of one or two closing pages by a CTA: SPLIT warps share a page's rows.  s_part:
 // [kAppendWarps][2][D] partial bounds, s_max: [kAppendWarps / SPLIT] zeros.
 template <typename T, int D, int SPLIT>
-__device__ __forceinline__ void cta_envelope(const AppendParams &p, const Closing &cl, int h, float *s_part,
-                                             unsigned *s_max, int warp, int lane) {
+__device__ __forceinline__ void cta_envelope(const AppendParams &p, const Closing &cl, bool twice, int h,
+                                             float *s_part, unsigned *s_max, int warp, int lane) {
     using R = Rows<T, D>;
     constexpr int EPT = D / (SPLIT * 32) > 0 ? D / (SPLIT * 32) : 1;  // elements of a thread in the second half
     const int part = warp % SPLIT, n = cl.row + 1, share = (n + SPLIT - 1) / SPLIT;
     const int r1 = min(part * share, n), r2 = min(r1 + share, n);
     float lo[R::CPL][R::E], hi[R::CPL][R::E];
-    const bool odd = row_bounds<T, D>(p, cl, h, r1, r2, lo, hi, lane);
+    const bool odd = row_bounds<T, D>(p, cl, h, r1, r2, lo, hi, lane) || twice;
     if (lane < R::LPR) {
 #pragma unroll
         for (int i = 0; i < R::CPL; ++i)
@@ -242,40 +242,48 @@ __global__ void __launch_bounds__(kAppendThreads) paged_attn_append_kernel(const
         __syncthreads();
         const unsigned closes = __ballot_sync(0xffffffffu, lane < ET && s_closes[lane < ET ? lane : 0]);
         const int n = __popc(closes);
-        // the c-th closing token's page: its rows' sources
+        // the c-th closing token's page: its rows' sources.  Returns whether two tokens name a row: either may end up
+        // in the cache, so the page has no bound, as one with a non-finite key.
         auto look_up = [&](int c) {
             const int k = (int)__fns(closes, 0, c + 1), page = s_slot[64 + k] >> p.ps_shift;
             cl.from[lane] = cl.from[lane + 32] = kOld;
             __syncwarp();
-            int row = 0;
+            int row = 0, tokens = 0;
+            unsigned long long rows = 0;
 #pragma unroll
             for (int back = lane; back < 64; back += 32) {
                 const int x = s_slot[64 + k - back];
-                if (here(x, page)) {
+                const bool on = here(x, page);
+                tokens += __popc(__ballot_sync(0xffffffffu, on));
+                if (on) {
                     const int r = x & ((1 << p.ps_shift) - 1);
                     cl.from[r] = (uint8_t)back;
+                    rows |= 1ull << r;
                     row = max(row, r);
                 }
             }
             row = __reduce_max_sync(0xffffffffu, row);
+            const int named = __popc(__reduce_or_sync(0xffffffffu, (unsigned)rows)) +
+                              __popc(__reduce_or_sync(0xffffffffu, (unsigned)(rows >> 32)));
             if (lane == 0) {
                 cl.t = t0 + k;
                 cl.page = page;
                 cl.row = row;
             }
             __syncwarp();
+            return named != tokens;
         };
         if (n == 1) {  // as in a prompt
-            look_up(0);
-            cta_envelope<T, D, 4>(p, cl, h, s_part, s_max, warp, lane);
+            const bool twice = look_up(0);
+            cta_envelope<T, D, 4>(p, cl, twice, h, s_part, s_max, warp, lane);
         } else if (n == 2) {
-            look_up(warp / 2);
-            cta_envelope<T, D, 2>(p, cl, h, s_part, s_max, warp, lane);
+            const bool twice = look_up(warp / 2);
+            cta_envelope<T, D, 2>(p, cl, twice, h, s_part, s_max, warp, lane);
         } else {
 #pragma unroll 1
             for (int c = warp; c < n; c += kAppendWarps) {
-                look_up(c);
-                warp_envelope<T, D>(p, cl, h, lane);
+                const bool twice = look_up(c);
+                warp_envelope<T, D>(p, cl, twice, h, lane);
                 __syncwarp();  // before cl is written for another page
             }
         }
@@ -334,7 +342,7 @@ static cudaError_t launch_append_k(const AppendParams &p, cudaStream_t stream) {
 template <typename T, int D>
 static cudaError_t launch_append_d(const AppendParams &p, cudaStream_t stream) {
     // Prompts (warps for every multiprocessor many times over): several tokens a warp and few closing
-    // pages among them (14.6 us as above; 27.7 with one token a warp); single tokens: a warp each, most of
+    // pages among them (13.7 us as above; 27.7 with one token a warp); single tokens: a warp each, most of
     // them closing a page.
     if ((long long)p.T * p.Hkv >= 16384) return launch_append_k<T, D, 4, 32>(p, stream);
     return launch_append_k<T, D, 1, 4>(p, stream);
