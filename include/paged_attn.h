@@ -350,8 +350,10 @@ int paged_attn_fwd_kvq_splitkv(const void *q, const void *k_cache, const void *v
  * Query layout of the last two: q_start NULL = q [batch, q_len, Hq, D]; q_start [batch + 1] (device) =
  * q [T, Hq, D] packed as for paged_attn_fwd_varlen, with T = dims->q_len the rows of q.  Rows at or
  * past q_start[batch] (padding) belong to no sequence: nothing of theirs is written.  A sequence whose
- * q_start entries are out of [0, T] or decrease is skipped and sets PA_ERRBIT_QSTART.  `causal` and
- * q_offset are paged_attn_fwd's; a query token's reach is the number of keys it may see.
+ * q_start entries are out of [0, T] or decrease is skipped and sets PA_ERRBIT_QSTART; in such a batch a row
+ * of another sequence gets its result or is left as it was, and one that two sequences claim gets either's,
+ * or parts of both.  `causal` and q_offset are paged_attn_fwd's; a query token's reach is the number of keys
+ * it may see.
  */
 
 /*

@@ -6,7 +6,7 @@ import pytest
 from paged_kv_cache_201_gb300 import workloads as W
 from tests import _gpu
 from tests import _sparse_ref as R
-from tests.test_serving_step_gpu import _append_case, _check_append, _lists, _raw, _run_append, _shares, _t, pa  # noqa: F401
+from tests.test_serving_step_gpu import _append_case, _lists, _raw, _run_append, _shares, _t, pa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,116 @@ def test_step_tables_of_an_empty_batch(pa, other_stream):  # noqa: F811
                          stream=torch.cuda.Stream() if other_stream else None)
     torch.cuda.synchronize()
     assert [x.tolist() for x in got] == [[], [], [0], [-1] * 6, [5]]
+
+
+# ----------------------------------------------------------------------------- malformed query ranges
+def _claims(qs, T):
+    """Sound sequences that claim each row."""
+    claims = [[] for _ in range(T)]
+    for b, (a, e) in enumerate(zip(qs, qs[1:])):
+        if 0 <= a <= e <= T:
+            for t in range(a, e):
+                claims[t].append(b)
+    return claims
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,qs,found", [
+    (3, [0, 1, 2, 9], {0, 1}), (3, [0, 1, -5, 3], {0}), (3, [0, 9, 2, 3], {2}), (80, [0, 10, 70, 60], set(range(70))),
+    (80, [0, 20, 90, 80], set(range(20))), (80, [-1, 80, 80, 80], set()), (80, [0, 40, 20, 80], set(range(20))),
+    (80, [0, 0, 500, 4], set()), (80, [0, 500, 40, 80], set())])
+def test_rows_beside_malformed_ranges(pa, dtype, T, qs, found):  # noqa: F811
+    """A malformed sequence's rows stay as they were.  Another sequence's rows are its own or stay, too (`found`:
+    those that are certainly there, ahead of the first malformed entry); a row that two claim is either's."""
+    import torch
+    b = R.Batch(T, [1] * 3, [1600, 1200, 1500], 8, 2, 128, 16, dtype, q_pad=T - 3)
+    q64, (env, scale), K = R.elems_to_f64(b.q, dtype), b.envelopes(), 9
+    k, v = R.elems_to_f64(b.k, dtype), R.elems_to_f64(b.v, dtype)
+    d = b.device()
+    q_start = _t(qs, np.int32)
+    sel = torch.full((T, 2, K), -9, dtype=torch.int32, device="cuda")
+    pa.paged_attn_select_pages(d["q"], _t(env), _t(scale), d["table"], d["lens"], True, None, 1, 1, sel, 16,
+                               q_start=q_start)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_QSTART
+    lists = np.broadcast_to(np.arange(K, dtype=np.int32), (T, 2, K)).copy()
+    out, lse = torch.full_like(d["q"], 7.0), torch.full((T, 8), 7.0, device="cuda")
+    pa.paged_attn_fwd_sparse(d["q"], d["k"], d["v"], d["table"], d["lens"], True, None, _t(lists), 0.1, out, lse,
+                             q_start=q_start)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_QSTART
+    sel, out, lse = sel.cpu().numpy(), _gpu.to_f64(out, dtype), _gpu.to_f64(lse, "f32")
+    for t, claim in enumerate(_claims(qs, T)):
+        if t in found or not (sel[t] == -9).all():
+            wants = []
+            for s in claim:
+                n = qs[s + 1] - qs[s]
+                row = [(s, min(int(b.seq_lens[s]), int(b.seq_lens[s]) - n + t - qs[s] + 1))]
+                wants.append(R.select(q64[t:t + 1], env, scale, b.table, row, 2, 16, 1, 1, K)[0])
+            assert any(np.array_equal(sel[t], w) for w in wants), (t, claim)
+        if t not in found and (out[t] == 7.0).all() and (lse[t] == 7.0).all():
+            continue
+        assert claim
+        fits = []
+        for s in claim:
+            n = qs[s + 1] - qs[s]
+            row = [(s, int(b.seq_lens[s]) - n + t - qs[s] + 1)]
+            want = R.attend(q64[t:t + 1], k, v, b.table, row, lists[t:t + 1], 16, 0.1)
+            atol, rtol = _gpu.TOL[dtype]
+            fits.append((np.abs(out[t] - want[0][0]) <= atol + rtol * np.abs(want[0][0])).all()
+                        and (np.abs(lse[t] - want[1][0]) <= atol + rtol * np.abs(want[1][0])).all())
+        assert any(fits), (t, claim)
+
+
+# ----------------------------------------------------------------------------- the kernels for runs of tokens
+def _two_launches(dtype="bf16", seed=48):
+    """A batch that both of a call's launches work on, in selection (2^23 scores) and attention."""
+    return R.Batch(seed, [700, 3, 1, 697], [1600, 1200, 900, 1500], 64, 2, 128, 16, dtype)
+
+
+def test_runs_of_tokens_on_two_streams_at_once(pa):  # noqa: F811
+    """Each call gives what it gives alone, its tensor memory and its second launch its own."""
+    import torch
+    b = _two_launches()
+    assert b.T * 64 * b.width >= 1 << 23 and _shares(pa, b, 40)
+    d = b.device()
+    env, scale = (_t(x) for x in b.envelopes())
+    sets = []
+    for i in range(2):
+        q = W.host_to_torch(R.random_elems(np.random.default_rng(i), b.q.shape, "bf16"), "bf16").cuda()
+        sets.append([q, torch.empty(b.T, 2, 40, dtype=torch.int32, device="cuda"), torch.empty_like(q)])
+
+    def call(q, sel, out):
+        pa.paged_attn_select_pages(q, env, scale, d["table"], d["lens"], True, None, 1, 2, sel, 16, q_start=d["q_start"])
+        pa.paged_attn_fwd_sparse(q, d["k"], d["v"], d["table"], d["lens"], True, None, sel, 0.1, out, None,
+                                 q_start=d["q_start"])
+    alone = []
+    for s in sets:
+        call(*s)
+        torch.cuda.synchronize()
+        alone.append((s[1].clone(), s[2].clone()))
+        s[1].zero_()
+        s[2].zero_()
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                call(*s)
+    torch.cuda.synchronize()
+    for s, (sel, out) in zip(sets, alone):
+        assert torch.equal(s[1], sel) and torch.equal(s[2], out)
+    assert pa.paged_attn_last_error_word() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_runs_of_tokens_give_the_same_bits_on_every_run(pa, dtype):  # noqa: F811
+    import torch
+    b = _two_launches(dtype, 49)
+    assert _shares(pa, b, 40)
+    d, sel = b.device(), _t(_lists(b, 40))
+    first = None
+    for _ in range(4):
+        out, lse = torch.full_like(d["q"], 7.0), torch.full((b.T, 64), 7.0, device="cuda")
+        pa.paged_attn_fwd_sparse(d["q"], d["k"], d["v"], d["table"], d["lens"], True, None, sel, 0.1, out, lse,
+                                 q_start=d["q_start"])
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
