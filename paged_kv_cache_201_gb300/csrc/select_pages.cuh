@@ -124,11 +124,10 @@ __global__ void __launch_bounds__(kSelCtaWarps<WPU> * 32, 16 / kSelCtaWarps<WPU>
     constexpr int kThreads = WPU * 32;
     const int me = wi / WPU;
     const int g = lane >> 2, tq = lane & 3;
-    auto sync = [me] {
+    static_assert(WPU == 1 || UNITS == 1, "a unit is a warp or the CTA");
+    auto sync = [] {
         if (WPU == 1)
             __syncwarp();
-        else if (UNITS > 1)
-            named_bar_sync(1 + me, kThreads);
         else
             __syncthreads();
     };

@@ -1,7 +1,7 @@
 // The pages that runs of query tokens attend to, scored on the 5th-generation tensor cores (head_dim 64 or
 // 128, up to 32 query heads to a kv head).
 //
-// The score is select_pages.cu's: s = max_h (min(qi, 0) . lo + max(qi, 0) . hi) over integers of 8 bits, here
+// The score is that of select_pages.cuh: s = max_h (min(qi, 0) . lo + max(qi, 0) . hi) over integers of 8 bits, here
 // f16 numbers (exact), summed in float32 (exact, below 2^23), then one product with the page's scale.
 // A CTA takes TT consecutive tokens of a sequence and one kv head.  Its queries are quantised once into the B
 // operand (TT x Gp columns, Gp the heads rounded up to a power of two, head 0 repeated in the gap; 2 D deep);

@@ -118,7 +118,8 @@ __device__ __forceinline__ void simt_token(const SparseParams &sp, const TokenRo
             }
         }
     }
-    // merge the 16 states: across the warp's groups by shuffles, across the warps in shared memory
+    // merge the 4 NW states (of each CTA of a cluster): across the warp's groups by shuffles, across the warps in
+    // shared memory
     float *s_acc = scratch, *s_m = s_acc + NW * HG * D, *s_l = s_m + NW * HG;  // [NW][HG][D], [NW][HG] twice
 #pragma unroll
     for (int g = 0; g < HG; ++g) {
