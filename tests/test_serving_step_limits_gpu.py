@@ -6,7 +6,8 @@ import pytest
 from paged_kv_cache_201_gb300 import workloads as W
 from tests import _gpu
 from tests import _sparse_ref as R
-from tests.test_serving_step_gpu import _append_case, _lists, _raw, _run_append, _shares, _t, pa  # noqa: F401
+from tests.test_serving_step_gpu import (_append_case, _check_attend, _check_select, _lists, _raw, _run_append,  # noqa: F401
+                                         _run_attend, _shares, _t, pa)
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +162,61 @@ def test_runs_of_tokens_give_the_same_bits_on_every_run(pa, dtype):  # noqa: F81
                                  q_start=d["q_start"])
         first = first or (out, lse)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+# ----------------------------------------------------------------------------- tables and batches of a serving loop
+@pytest.mark.parametrize("columns", [300, 1100, 5000])
+@pytest.mark.parametrize("q_lens,seq_lens", [
+    ([1] * 9, [500, 3, 900, 64, 1, 700, 17, 333, 1200]),       # single tokens, lengths spread widely
+    ([260, 1, 1, 40], [900, 500, 7, 300]),                     # chunks beside single tokens
+    ([90] + [1] * 130, [400] + [37 + 11 * i for i in range(130)])])  # single tokens outnumber a chunk's
+def test_tables_wider_than_their_sequences(pa, q_lens, seq_lens, columns):  # noqa: F811
+    """A loop's table is as wide as its longest request may become: the columns past a sequence's pages are not read."""
+    b = R.Batch(columns, q_lens, seq_lens, 8, 2, 128, 16, "f16", q_pad=2)
+    b.table = np.concatenate([b.table, np.full((len(q_lens), columns), W.SENTINEL_MAX, np.int32)], 1)
+    b.width += columns
+    for K in (7, 20):
+        _check_select(pa, b, 1, 2, K)
+        _check_attend(pa, b, _lists(b, K))
+    assert pa.paged_attn_last_error_word() == 0
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [300, 300]])
+@pytest.mark.parametrize("exponent", [5, 15, 23, 25, 27])
+@pytest.mark.parametrize("dtype,D", [("f16", 128), ("f16", 64), ("bf16", 128)])
+def test_largest_scores(pa, q_lens, exponent, dtype, D):  # noqa: F811
+    """Scores up to 2^27, the largest shared by every fifth key, a smaller one met before it: the output is the mean
+    of those keys' values.  The weights are then equal (the others below 2^-22 of them), so the bar is the rounding of the output and of
+    float32 sums: half a step and 2 n 2^-24 of the largest value."""
+    n = 600
+    b = R.Batch(D, q_lens, [n] * 2, 8, 2, D, 16, dtype)
+    el = (lambda x: x.astype(np.float16).view(np.uint16)) if dtype == "f16" else \
+        (lambda x: W.bf16_bits_rne(x.astype(np.float32).ravel()).reshape(x.shape))
+    key = np.zeros(b.k.shape)
+    peak = np.zeros(n, bool)
+    peak[100::5] = True
+    for s in range(2):
+        at = np.arange(n)
+        key[b.table[s, at // 16], at % 16, :, 0] = np.where(peak, 1.0, np.where(at == 3, 0.5, 0.0))[:, None] * 2.0 ** 12
+    b.k[:] = el(key)
+    q = np.zeros(b.q.shape)
+    q[..., 0] = 2.0 ** (exponent - 12)
+    b.q[:] = el(q)
+    b.v[~b.live] = 0
+    K = -(-n // 16)
+    sel = np.broadcast_to(np.arange(K, dtype=np.int32), (b.T, 2, K)).copy()
+    if q_lens[0] > 1:
+        assert _shares(pa, b, K, scale=1.0)
+    out, lse = _run_attend(pa, b, sel, causal=False, scale=1.0)
+    v = R.elems_to_f64(b.v, dtype)
+    eps = 2.0 ** (-11 if dtype == "f16" else -8)
+    for s in range(2):
+        at = np.flatnonzero(peak)
+        want = v[b.table[s, at // 16], at % 16].mean(0)  # [Hkv, D]
+        rows = slice(int(b.q_start[s]), int(b.q_start[s + 1]))
+        got = out[rows].reshape(-1, 2, 4, D)
+        err = np.abs(got - want[None, :, None])
+        assert (err <= eps * np.abs(want[None, :, None]) + 2 * n * 2.0 ** -24 * np.abs(v).max()).all(), err.max()
+        top = 2.0 ** exponent + np.log(peak.sum())
+        assert np.abs(lse[rows] - top).max() <= 2.0 ** -21 * top
+    assert pa.paged_attn_last_error_word() == 0
