@@ -696,7 +696,8 @@ bool sparse_shares_pages(const pa_dims *d, int64_t n_tok, bool packed, int top_k
     if (d->dtype == PA_F32 || d->head_dim == 256 || tile == 0 || !(scale > 0.f) ||
         d->bt_stride > pa::kSparseTc05MaxPages || n_tok >= (int64_t)1 << 31)
         return false;
-    // a batch of mostly single tokens, or of too few for half a tile
+    // a batch of mostly single tokens, or of too few for half a tile; by the average, so 600 single tokens beside a
+    // chunk of 500 take 619 us, the two called apart 384 and 80
     if (packed ? n_tok < 2 * (int64_t)d->batch : d->q_len < (tile + 1) / 2) return false;
     const double W = d->bt_stride, K = top_k < W ? top_k : W;
     const double c = d->head_dim == 64 ? 1.08 : 1.14;
@@ -813,7 +814,9 @@ int paged_attn_select_pages(const void *q, const int8_t *k_env, const float *k_e
     // its CTAs (one an SM, with a long set-up); in a packed batch both kernels find theirs from q_start.
     // Measured, in microseconds, tcgen05 and mma.sync: 1024 tokens of 8 kv heads, G = 4, 512 pages (2^24 scores
     // of a head) 48 and 66, 512 tokens 26 and 37, 256 tokens 26 and 27, 64 tokens 24 and 17; 1024 tokens of 2
-    // kv heads, G = 16, 2048 pages (2^26) 108 and 194, 256 tokens 55 and 57 (64 CTAs), 128 tokens 55 and 41.
+    // kv heads, G = 16, 2048 pages (2^26) 108 and 194, 256 tokens 55 and 57 (64 CTAs), 128 tokens 55 and 41.  Width
+    // and average stand for lengths, which the host does not know: 936 tokens of 400 pages take 45 us in a table
+    // of 512 columns, 104 in one of 2048, and a chunk of 500 beside 600 single tokens 126 (36 and 56 apart).
     const int tile = pa::select_tile_tokens(dims->head_dim, sp.f.G, dims->bt_stride);
     const bool runs = q_start ? n_tok >= 2 * (int64_t)dims->batch : dims->q_len >= (tile + 1) / 2;
     if (tile > 0 && runs && n_tok >= (tile + 1) / 2 &&

@@ -8,7 +8,7 @@
 // order, so an envelope is the same bits whether a page is filled at once or token by token.
 // Kept apart, the long chain of an envelope (slots, rows, reduction, division) overlaps the copies; where
 // few pages close, as in a prompt, the CTA's warps share a page's rows.  6656 prompt tokens of 8 heads of
-// 128 (f16, 64-token pages) take 13.7 us, 59 % of the copy rate; with the closing warps among the copying
+// 128 (f16, 64-token pages) take 14.1 us, 58 % of the copy rate; with the closing warps among the copying
 // ones they took 21, and the copies alone take 10.7.  A decode step of 256 tokens takes 5.4 us, a chain
 // of three trips to memory.
 #include <float.h>
@@ -342,8 +342,9 @@ static cudaError_t launch_append_k(const AppendParams &p, cudaStream_t stream) {
 template <typename T, int D>
 static cudaError_t launch_append_d(const AppendParams &p, cudaStream_t stream) {
     // Prompts (warps for every multiprocessor many times over): several tokens a warp and few closing
-    // pages among them (13.7 us as above; 27.7 with one token a warp); single tokens: a warp each, most of
-    // them closing a page.
+    // pages among them (14.1 us as above; 27.7 with one token a warp); single tokens: a warp each, most of
+    // them closing a page (1024 of 8 heads 11.3 us, 20.9 the other way).  The rule cannot tell a very large batch of
+    // single tokens from a prompt: 2048 take 28.9 us with the first plan, 21.1 with the second, 4096 take 47 and 46.
     if ((long long)p.T * p.Hkv >= 16384) return launch_append_k<T, D, 4, 32>(p, stream);
     return launch_append_k<T, D, 1, 4>(p, stream);
 }
