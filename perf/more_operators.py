@@ -18,7 +18,7 @@ own = False
 
 DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 ESIZE = {"f32": 4, "f16": 2, "bf16": 2}
-MAX_SCALE = 7680.0
+MAX_SCALE = 7168.0
 
 
 # ----------------------------------------------------------------------------- cases
@@ -316,7 +316,7 @@ def _scale_byte(s):
 
 def _scale_value(b):
     f = (b.to(torch.int16) << 7).view(torch.float16).float()
-    return torch.where(b >= 0xDF, MAX_SCALE, f)
+    return torch.where(b >= 0xDE, MAX_SCALE, f)
 
 
 def _packed(c):
@@ -549,7 +549,7 @@ def work(case):
 # ----------------------------------------------------------------------------- the definitions in 64 bits
 def _held64(x):
     """The values that 4 bits hold of rows x [..., D], from the tables of all scales and all codes."""
-    byte = np.arange(0xE0)
+    byte = np.arange(0xDF)
     scales = np.where(byte < 8, byte * 2.0 ** -17, (8 + byte % 8) * 2.0 ** (byte // 8 - 18.0))
     g = x.reshape(*x.shape[:-1], -1, 16)
     t = np.abs(g).max(-1) / 7
@@ -572,7 +572,7 @@ def _exact_attend(st):
     ps, d, hkv = case["page_size"], case["head_dim"], case["kv_heads"]
     G = case["q_heads"] // hkv
     half, few = ps * d // 2, ps * d // 16
-    byte = np.arange(256).clip(max=0xDF)
+    byte = np.arange(256).clip(max=0xDE)
     scale_of = _gpu(np.where(byte < 8, byte * 2.0 ** -17, (8 + byte % 8) * 2.0 ** (byte // 8 - 18.0)))
     out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
     lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device=q.device)
