@@ -64,7 +64,8 @@ enum {
     PA_ERRBIT_TIMEOUT = 2u,      /* a pipeline wait gave up after its time limit (results invalid) */
     PA_ERRBIT_SEQ_CLIPPED = 4u,  /* seq_lens[b] needed more pages than bt_stride holds; clipped to bt_stride pages */
     PA_ERRBIT_QSTART = 8u,       /* a packed batch's q_start entry out of [0, total tokens] or decreasing */
-    PA_ERRBIT_REFUSED = 16u      /* paged_attn_step_tables: a request could not be served (see there) */
+    PA_ERRBIT_REFUSED = 16u,     /* paged_attn_step_tables, _fork, _free: a request could not be served (see there) */
+    PA_ERRBIT_NONFINITE = 32u    /* paged_attn_append_kv4: a new element was infinite or a NaN */
 };
 
 /* kernel variants (paged_attn_fwd_variant) */
@@ -459,6 +460,130 @@ int paged_attn_fwd_sparse(const void *q, const void *k_cache, const void *v_cach
 int paged_attn_sparse_shares_pages(const pa_dims *dims, int packed, int top_k, float scale, int num_sms);
 
 /*
+ * ------------------------------------------------------------------ a cache in 4 bits
+ * paged_attn_append_kv4 writes tokens into a 4-bit pool, paged_attn_fwd_kv4 attends over it and
+ * paged_attn_gather_kv4 reads rows back.  One pool holds both K and V:
+ *   kv [num_pages, num_kv_heads, 9 * page_size * head_dim / 8] bytes
+ * The block of a (page, kv head) holds, one after the other, the K codes of its page_size rows
+ * (head_dim / 2 bytes a row; element 2i in the low half of byte i, 2i + 1 in the high half), the V codes,
+ * the K scales (head_dim / 16 bytes a row, one for 16 consecutive elements) and the V scales.  A code
+ * u in 0 .. 15 with the scale byte c stands for
+ *   (u - 8) * s(c),   s(c) = c * 2^-17 for c < 8,  else (8 + c % 8) * 2^(c / 8 - 18),  at most s(0xDE) = 7168
+ * (bytes above 0xDE count as 0xDE), so any bytes are finite numbers, all of them exact in f16, bf16 and
+ * float32; a pool of zeros holds zeros.  Tables, slots, lengths and pages are those of the other pools, and
+ * these calls follow the rules of the serving step above: a launch or two on `stream`, no workspace,
+ * graph capture after a first call on the device.  They are this library's own.
+ *
+ * paged_attn_append_kv4 — new tokens' K and V rows into their slots.
+ *   k_new, v_new [T, Hkv, D] in dims->dtype (any), k_stride, v_stride and slots [T] as for paged_attn_append
+ * For 16 consecutive elements x of a row, a the largest |x|:
+ *   s = the s(c) nearest to a / 7 (on a tie the even c; at most 7168),   u = 8 + min(max(rint(x / s), -7), 7)
+ * (u = 8 where s = 0): the exact quotients' roundings, to nearest even.  A NaN counts as 0 and an infinity as the largest
+ * value, and either sets PA_ERRBIT_NONFINITE.  A slot named twice holds unspecified (finite) rows.
+ * dims->batch, num_q_heads, bt_stride and q_stride are not used.
+ */
+int paged_attn_append_kv4(const void *k_new, const void *v_new, const int32_t *slots, int64_t k_stride,
+                          int64_t v_stride, void *kv, const pa_dims *dims, void *stream);
+
+/*
+ * paged_attn_gather_kv4 — the values of the rows in slots [T], T = dims->q_len, into k_out and v_out
+ * [T, Hkv, D] in dims->dtype (any; exact).  Slot -1 gives zeros; so does any other value outside the pool,
+ * which sets PA_ERRBIT_PAGE_RANGE.
+ */
+int paged_attn_gather_kv4(const void *kv, const int32_t *slots, void *k_out, void *v_out, const pa_dims *dims,
+                          void *stream);
+
+/*
+ * paged_attn_fwd_kv4 — paged_attn_fwd over a 4-bit pool: q [batch, q_len, Hq, D], or packed [T, Hq, D] with
+ * q_start [batch + 1], laid out, masked and skipped as for the calls over selected pages (rows at or past
+ * q_start[batch] are not written).  q and out are PA_BF16 or PA_F16 (PA_F32: PA_EDTYPE); out is rounded once,
+ * lse [tokens, Hq] float32 or NULL; a row without a key gets 0 and -inf.  bf16 queries enter the products as f16
+ * numbers, each row moved by a power of two, which is exact but for elements below 2^-28 of the row's largest; weights
+ * meet V as f16 pairs, within 2^-22 of the weight or 2^-31 of the row's largest.  A page id outside
+ * [0, num_pages) reads as zeros and sets PA_ERRBIT_PAGE_RANGE.
+ */
+int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table, const int32_t *seq_lens,
+                       const int32_t *q_start, int causal, const int32_t *q_offset, float scale, void *out, float *lse,
+                       const pa_dims *dims, void *stream);
+
+/*
+ * ------------------------------------------------------------------ sharing, freeing and moving pages
+ * Block-table rows may share pages: page_shares [num_pages] int32 counts, for every page, the listings of it
+ * beyond the first (0: one owner, or none).  paged_attn_step_tables takes pages with count 0 from the stack
+ * of free pages and needs no change; only full pages are shared, and those are never written again.  All
+ * arrays are int32 on the device; free_pages [free_cap] is paged_attn_step_tables' stack, its top at
+ * free_count[0] - 1.  Each call is one launch on `stream` without a workspace, can be captured, and gives the same
+ * bits every time.  lens_out may be seq_lens itself and free_left free_count; other arrays must not
+ * overlap.  Lists, tables and counts of another origin may hold anything: no access leaves the arrays, ids outside
+ * [0, num_pages) are not followed (PA_ERRBIT_PAGE_RANGE), lengths are cut to the row's width
+ * (PA_ERRBIT_SEQ_CLIPPED), negative ones count as 0.
+ * Limits (PA_EUNSUPPORTED): batch and n at most PA_STEP_MAX_BATCH, n * bt_stride < 2^30, page_size in {16, 32, 64},
+ * num_pages * page_size < 2^31.
+ *
+ * paged_attn_fork — n sequences that begin as copies of others, for parallel sampling, beams and common prefixes.
+ *   parents, children [n]   rows of the block table; parents[i] = -1: nothing is asked
+ *   prefix_lens [n] or NULL tokens to share, at most the parent's length (NULL: all of them)
+ * Child i's row lists its parent's full pages (their counts go up by one) and, if the shared length is
+ * no multiple of page_size, a page from the stack for the rest: copies [n, 2] holds (the parent's page, that page) for
+ * paged_attn_copy_pages, or (-1, -1).  lens_out [batch] = seq_lens, the child's length set to the shared one.
+ * A request is usable if its rows are two different ones of the table, the child's length is 0, no earlier request names
+ * the child, and prefix_lens[i] is not negative; it is served if it is usable and needs no page, or no more pages are
+ * needed by it and the usable requests before it than free_count.  Pages are taken in the order of the
+ * requests; every length is read as it was before the call.  A request that is asked and not
+ * served sets PA_ERRBIT_REFUSED and changes nothing (copies (-1, -1)), and so does a free_count outside
+ * [0, free_cap], which is clamped.  free_left = free_count - pages taken.
+ */
+int paged_attn_fork(const int32_t *parents, const int32_t *children, const int32_t *prefix_lens, int n,
+                    int32_t *block_table, const int32_t *seq_lens, int32_t *lens_out, int32_t *page_shares,
+                    const int32_t *free_pages, int free_cap, const int32_t *free_count, int32_t *free_left,
+                    int32_t *copies, int batch, int page_size, int64_t num_pages, int bt_stride, void *stream);
+
+/*
+ * paged_attn_free — sequences end: every page of the table rows rows [n] loses an owner, and one without owners
+ * goes back to the stack.  rows[i] = -1: nothing is asked; a row named again counts once; one outside the
+ * table sets PA_ERRBIT_REFUSED.  lens_out [batch] = seq_lens, 0 for the rows.  The pages are pushed in the reverse
+ * order of (request, page in the row), the page that several rows list in the place of its first listing, so that
+ * freeing what paged_attn_step_tables or paged_attn_fork took, listed as it was taken, restores the
+ * stack.  free_left = free_count + pages pushed; pages past free_cap are lost and set PA_ERRBIT_REFUSED (a stack of
+ * num_pages entries never overflows), as a free_count outside [0, free_cap] does, which is clamped.
+ * Table entries are left as they are.
+ */
+int paged_attn_free(const int32_t *rows, int n, const int32_t *block_table, const int32_t *seq_lens, int32_t *lens_out,
+                    int32_t *page_shares, int32_t *free_pages, int free_cap, const int32_t *free_count,
+                    int32_t *free_left, int batch, int page_size, int64_t num_pages, int bt_stride, void *stream);
+
+/*
+ * paged_attn_compact — the used pages move together: as long as a free page's id is below a used one's, the
+ * used pages with the highest ids take the free pages with the lowest.
+ *   moves [num_pages / 2, 2]  (page, new page) in ascending order of both, for paged_attn_copy_pages; entries from
+ *                             n_moves[0] on are left as they were
+ *   page_map [num_pages]      every page's new id (its own, if it does not move)
+ * block_table's listed entries and page_shares follow; the stack holds its free_count[0] pages in descending order, so
+ * that the lowest are taken first.  Pages that are neither listed nor free stay where they are; one that is both counts
+ * as used and leaves the stack (PA_ERRBIT_REFUSED; free_count is written then), as one that the stack holds twice counts
+ * once.  The contents are the caller's to move: nothing may write pages between this call and
+ * paged_attn_copy_pages.
+ */
+int paged_attn_compact(int32_t *block_table, const int32_t *seq_lens, int32_t *page_shares, int32_t *free_pages,
+                       int free_cap, int32_t *free_count, int32_t *moves, int32_t *n_moves, int32_t *page_map, int batch,
+                       int page_size, int64_t num_pages, int bt_stride, void *stream);
+
+/*
+ * paged_attn_copy_pages — page contents from page to page, in up to PA_COPY_MAX_POOLS pools at once (the pools of
+ * every layer, scales and envelopes).
+ *   pools [n_pools]       HOST array of device pointers, each a pool of num_pages pages of page_bytes[i] bytes (HOST;
+ *                         a multiple of 4, pointers 4-byte aligned; 16-byte pages and pointers are copied faster)
+ *   pairs [max_pairs, 2]  device: (from, to); a pair with a -1 is passed over, one with another id outside the
+ *                         pool too and sets PA_ERRBIT_PAGE_RANGE
+ *   n_pairs [1]           device: how many of them count, or NULL (all)
+ * A page that two pairs write, or that one writes and another reads, holds unspecified bytes of theirs
+ * afterwards.  paged_attn_fork and paged_attn_compact give no such pairs.
+ */
+#define PA_COPY_MAX_POOLS 192
+int paged_attn_copy_pages(void *const *pools, const int64_t *page_bytes, int n_pools, const int32_t *pairs, int max_pairs,
+                          const int32_t *n_pairs, int64_t num_pages, void *stream);
+
+/*
  * paged_attn_plan — the split plan as data: plan [batch, split_kv, 2] int32 =
  * {first page, one past the last page} of each run (see paged_attn_fwd).
  * seq_lens is a device pointer [batch]; negative lengths count as 0.
@@ -497,7 +622,7 @@ int paged_attn_debug_wait_timeout(uint32_t limit_us, void *stream);
  *                rocm-libraries PR #14349 kernel leaves this unchecked, "Not in
  *                this PR"), every other sequence's results are exact;
  *   PA_EINVAL    otherwise, PA_ERRBIT_QSTART is set (a packed batch's q_start);
- *   PA_OK        no bit other than PA_ERRBIT_SEQ_CLIPPED and PA_ERRBIT_REFUSED is set.
+ *   PA_OK        no bit other than PA_ERRBIT_SEQ_CLIPPED, PA_ERRBIT_REFUSED and PA_ERRBIT_NONFINITE is set.
  * *flags holds the bits in every case but PA_ECUDA (the read failed) and
  * PA_EINVAL for a NULL flags.  The forward calls are asynchronous and cannot
  * return these themselves: a caller that must not consume invalid outputs

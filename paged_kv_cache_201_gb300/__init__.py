@@ -25,7 +25,10 @@ __all__ = [
     "paged_attn_fwd_kvq_splitkv", "attention_kvq", "paged_attn_fwd_varlen", "attention_varlen",
     "paged_attn_fwd_varlen_overlap", "paged_attn_varlen_hint", "paged_attn_varlen_overlap_share", "PaVarlenHint",
     "paged_attn_step_tables", "paged_attn_append", "paged_attn_select_pages", "paged_attn_fwd_sparse",
-    "paged_attn_sparse_shares_pages", "step_tables", "page_envelopes", "attention_sparse", "PA_F32", "PA_F16", "PA_BF16", "PA_FP8_E4M3",
+    "paged_attn_sparse_shares_pages", "step_tables", "page_envelopes", "attention_sparse",
+    "paged_attn_append_kv4", "paged_attn_gather_kv4", "paged_attn_fwd_kv4", "kv4_pool", "attention_kv4",
+    "paged_attn_fork", "paged_attn_free", "paged_attn_compact", "paged_attn_copy_pages", "fork_sequences",
+    "free_sequences", "compact_pages", "PA_F32", "PA_F16", "PA_BF16", "PA_FP8_E4M3",
     "PA_INT8",
     "VARIANT_AUTO", "VARIANT_SIMT", "VARIANT_MMA_DECODE", "VARIANT_MMA_PREFILL", "VARIANT_TC05_PREFILL",
     "VARIANT_MMA_T", "VARIANT_MMA_SPLIT_GROUP",
@@ -35,6 +38,7 @@ PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT8 = 0, 1, 2, 3, 4
 VARIANT_AUTO, VARIANT_SIMT, VARIANT_MMA_DECODE, VARIANT_MMA_PREFILL, VARIANT_TC05_PREFILL, VARIANT_MMA_T = 0, 1, 2, 3, 4, 5
 VARIANT_MMA_SPLIT_GROUP = 6
 ERRBIT_PAGE_RANGE, ERRBIT_TIMEOUT, ERRBIT_SEQ_CLIPPED, ERRBIT_QSTART, ERRBIT_REFUSED = 1, 2, 4, 8, 16
+ERRBIT_NONFINITE = 32
 PA_OK, PA_EINVAL, PA_EDTYPE, PA_EUNSUPPORTED, PA_ECUDA, PA_EBOUNDS, PA_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6
 
 
@@ -115,6 +119,20 @@ def load_library(build_if_missing: bool = False):
     lib.paged_attn_fwd_sparse.restype = ctypes.c_int
     lib.paged_attn_sparse_shares_pages.argtypes = [D, I32, I32, F, I32]
     lib.paged_attn_sparse_shares_pages.restype = ctypes.c_int
+    lib.paged_attn_append_kv4.argtypes = [P, P, P, I64, I64, P, D, P]
+    lib.paged_attn_append_kv4.restype = ctypes.c_int
+    lib.paged_attn_gather_kv4.argtypes = [P, P, P, P, D, P]
+    lib.paged_attn_gather_kv4.restype = ctypes.c_int
+    lib.paged_attn_fwd_kv4.argtypes = [P, P, P, P, P, I32, P, F, P, P, D, P]
+    lib.paged_attn_fwd_kv4.restype = ctypes.c_int
+    lib.paged_attn_fork.argtypes = [P, P, P, I32, P, P, P, P, P, I32, P, P, P, I32, I32, I64, I32, P]
+    lib.paged_attn_fork.restype = ctypes.c_int
+    lib.paged_attn_free.argtypes = [P, I32, P, P, P, P, P, I32, P, P, I32, I32, I64, I32, P]
+    lib.paged_attn_free.restype = ctypes.c_int
+    lib.paged_attn_compact.argtypes = [P, P, P, P, I32, P, P, P, P, I32, I32, I64, I32, P]
+    lib.paged_attn_compact.restype = ctypes.c_int
+    lib.paged_attn_copy_pages.argtypes = [P, P, I32, P, I32, P, I64, P]
+    lib.paged_attn_copy_pages.restype = ctypes.c_int
     lib.paged_attn_debug_gather.argtypes = [P, P, P, D, I32, P, P]
     lib.paged_attn_debug_wait_timeout.argtypes = [ctypes.c_uint32, P]
     lib.paged_attn_debug_wait_timeout.restype = ctypes.c_int
@@ -670,6 +688,201 @@ def paged_attn_sparse_shares_pages(batch: int, tokens: int, num_q_heads: int, nu
     return bool(rc)
 
 
+# ----------------------------------------------------------------------------- a cache in 4 bits
+def _kv4_page_size(kv, D: int) -> int:
+    """Page size of a 4-bit pool [num_pages, Hkv, 9 page_size D / 8]."""
+    if kv.dim() != 3:
+        raise ValueError("kv must be [num_pages, Hkv, 9 * page_size * head_dim / 8] (see kv4_pool)")
+    ps, rest = divmod(kv.shape[2] * 8, 9 * D) if D > 0 else (0, 1)
+    if rest or ps not in (16, 32, 64):
+        raise ValueError(f"kv's blocks of {kv.shape[2]} bytes do not hold 16, 32 or 64 rows of head_dim {D}")
+    return ps
+
+
+def paged_attn_append_kv4(k_new, v_new, slots, kv, stream=None) -> None:
+    """Write the new tokens' K and V rows ([T, Hkv, D], possibly slices of a fused projection; any float
+    type) in 4 bits into their slots (int32 [T], page * page_size + row, -1 to skip) of kv (``kv4_pool``);
+    see ``paged_attn_append_kv4`` in include/paged_attn.h."""
+    torch = _torch()
+    dev, dt = torch.cuda.current_device(), k_new.dtype
+    if k_new.dim() != 3 or slots.dim() != 1:
+        raise ValueError("k_new must be [T, Hkv, D] and slots [T]")
+    T, Hkv, D = rows = k_new.shape
+    ps = _kv4_page_size(kv, D)
+    _need(kv, "kv", dev, torch.uint8, (kv.shape[0], Hkv, kv.shape[2]))
+    _need(slots, "slots", dev, torch.int32, (T,))
+    ks, vs = _rows_stride(k_new, "k_new", dev, dt, rows), _rows_stride(v_new, "v_new", dev, dt, rows)
+    dims = PaDims(1, T, Hkv, Hkv, D, ps, kv.shape[0], 0, _dtype_code(k_new))
+    rc = load_library().paged_attn_append_kv4(k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), ks, vs,
+                                              kv.data_ptr(), dims, _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_append_kv4")
+
+
+def paged_attn_gather_kv4(kv, slots, k_out, v_out, stream=None) -> None:
+    """The values of the rows in slots (int32 [T]; -1: zeros) of a 4-bit pool into k_out and v_out
+    [T, Hkv, D], any float type; see ``paged_attn_gather_kv4`` in include/paged_attn.h."""
+    torch = _torch()
+    dev, dt = torch.cuda.current_device(), k_out.dtype
+    if k_out.dim() != 3 or slots.dim() != 1:
+        raise ValueError("k_out must be [T, Hkv, D] and slots [T]")
+    T, Hkv, D = rows = k_out.shape
+    ps = _kv4_page_size(kv, D)
+    _need(kv, "kv", dev, torch.uint8, (kv.shape[0], Hkv, kv.shape[2]))
+    _need(slots, "slots", dev, torch.int32, (T,))
+    _need(k_out, "k_out", dev, dt, rows)
+    _need(v_out, "v_out", dev, dt, rows)
+    dims = PaDims(1, T, Hkv, Hkv, D, ps, kv.shape[0], 0, _dtype_code(k_out))
+    rc = load_library().paged_attn_gather_kv4(kv.data_ptr(), slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), dims,
+                                              _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_gather_kv4")
+
+
+def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, out, lse, q_start=None,
+                       stream=None) -> None:
+    """Forward over a 4-bit pool (``kv4_pool``, filled by ``paged_attn_append_kv4``); see
+    ``paged_attn_fwd_kv4`` in include/paged_attn.h.  q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start
+    [B + 1], in f16 or bf16; out as q (dense), lse without D or None."""
+    torch = _torch()
+    i32, dev, dt = torch.int32, torch.cuda.current_device(), q.dtype
+    if block_table.dim() != 2 or q.dim() != (4 if q_start is None else 3):
+        raise ValueError("block_table must be [B, W]; q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start")
+    B, W = bw = block_table.shape
+    shape = q.shape
+    Hq, D = shape[-2], shape[-1]
+    ps = _kv4_page_size(kv, D)
+    _need(kv, "kv", dev, torch.uint8, kv.shape)
+    if q_start is None:
+        if shape[0] != B:
+            raise ValueError("q must have one batch entry per block_table row")
+    else:
+        _need(q_start, "q_start", dev, i32, (B + 1,))
+    _need(block_table, "block_table", dev, i32, bw)
+    _need(seq_lens, "seq_lens", dev, i32, (B,))
+    if q_offset is not None:
+        _need(q_offset, "q_offset", dev, i32, (B,))
+    stride = _rows_stride(q, "q", dev, dt, shape)
+    _need(out, "out", dev, dt, shape)
+    if lse is not None:
+        _need(lse, "lse", dev, torch.float32, shape[:-1])
+    dims = PaDims(B, shape[-3], Hq, kv.shape[1], D, ps, kv.shape[0], W, _dtype_code(q), stride)
+    rc = load_library().paged_attn_fwd_kv4(q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                                           _ptr(q_start), 1 if causal else 0, _ptr(q_offset), scale, out.data_ptr(),
+                                           _ptr(lse), dims, _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_fwd_kv4")
+
+
+# ----------------------------------------------------------------------------- pages shared, freed and moved
+def _pages_args(block_table, seq_lens, page_shares, free_pages, free_count, dev):
+    """Checks that the page calls share; returns (batch, table width, stack capacity, pages)."""
+    i32 = _torch().int32
+    if block_table.dim() != 2 or free_pages.dim() != 1 or page_shares.dim() != 1:
+        raise ValueError("block_table must be [B, W], free_pages [F] and page_shares [num_pages]")
+    B, W = bw = block_table.shape
+    _need(block_table, "block_table", dev, i32, bw)
+    _need(seq_lens, "seq_lens", dev, i32, (B,))
+    _need(page_shares, "page_shares", dev, i32, page_shares.shape)
+    _need(free_pages, "free_pages", dev, i32, free_pages.shape)
+    _need(free_count, "free_count", dev, i32, (1,))
+    return B, W, free_pages.shape[0], page_shares.shape[0]
+
+
+def paged_attn_fork(parents, children, block_table, seq_lens, lens_out, page_shares, free_pages, free_count, free_left,
+                    copies, page_size: int, prefix_lens=None, stream=None) -> None:
+    """Rows children (int32 [n]) of the block table become copies of rows parents (-1: nothing), sharing
+    their full pages; the last part of a page goes to a page of its own, listed in copies [n, 2] for
+    ``paged_attn_copy_pages``.  See ``paged_attn_fork`` in include/paged_attn.h; every tensor int32 on the device,
+    lens_out may be seq_lens and free_left free_count."""
+    torch = _torch()
+    i32, dev = torch.int32, torch.cuda.current_device()
+    if parents.dim() != 1:
+        raise ValueError("parents must be [n]")
+    n = parents.shape[0]
+    B, W, F, P = _pages_args(block_table, seq_lens, page_shares, free_pages, free_count, dev)
+    _need(parents, "parents", dev, i32, (n,))
+    _need(children, "children", dev, i32, (n,))
+    if prefix_lens is not None:
+        _need(prefix_lens, "prefix_lens", dev, i32, (n,))
+    _need(lens_out, "lens_out", dev, i32, (B,))
+    _need(free_left, "free_left", dev, i32, (1,))
+    _need(copies, "copies", dev, i32, (n, 2))
+    rc = load_library().paged_attn_fork(
+        parents.data_ptr(), children.data_ptr(), _ptr(prefix_lens), n, block_table.data_ptr(), seq_lens.data_ptr(),
+        lens_out.data_ptr(), page_shares.data_ptr(), free_pages.data_ptr(), F, free_count.data_ptr(), free_left.data_ptr(),
+        copies.data_ptr(), B, page_size, P, W, _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_fork")
+
+
+def paged_attn_free(rows, block_table, seq_lens, lens_out, page_shares, free_pages, free_count, free_left,
+                    page_size: int, stream=None) -> None:
+    """Give back the pages of block-table rows (int32 [n], -1: nothing): those without an owner left go onto the stack
+    free_pages.  See ``paged_attn_free`` in include/paged_attn.h; every tensor int32 on the device, lens_out
+    may be seq_lens and free_left free_count."""
+    torch = _torch()
+    i32, dev = torch.int32, torch.cuda.current_device()
+    if rows.dim() != 1:
+        raise ValueError("rows must be [n]")
+    B, W, F, P = _pages_args(block_table, seq_lens, page_shares, free_pages, free_count, dev)
+    _need(rows, "rows", dev, i32, rows.shape)
+    _need(lens_out, "lens_out", dev, i32, (B,))
+    _need(free_left, "free_left", dev, i32, (1,))
+    rc = load_library().paged_attn_free(
+        rows.data_ptr(), rows.shape[0], block_table.data_ptr(), seq_lens.data_ptr(), lens_out.data_ptr(),
+        page_shares.data_ptr(), free_pages.data_ptr(), F, free_count.data_ptr(), free_left.data_ptr(), B, page_size, P, W,
+        _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_free")
+
+
+def paged_attn_compact(block_table, seq_lens, page_shares, free_pages, free_count, moves, n_moves, page_map,
+                       page_size: int, stream=None) -> None:
+    """Move the used pages with the highest ids to the free ones with the lowest: rewrites the tables, the counts
+    and the stack, and lists (from, to) in moves [num_pages // 2, 2], n_moves [1] of them, for
+    ``paged_attn_copy_pages``; page_map [num_pages] holds every page's new id.  See ``paged_attn_compact`` in
+    include/paged_attn.h; every tensor int32 on the device."""
+    torch = _torch()
+    i32, dev = torch.int32, torch.cuda.current_device()
+    B, W, F, P = _pages_args(block_table, seq_lens, page_shares, free_pages, free_count, dev)
+    _need(moves, "moves", dev, i32, (P // 2, 2))
+    _need(n_moves, "n_moves", dev, i32, (1,))
+    _need(page_map, "page_map", dev, i32, (P,))
+    rc = load_library().paged_attn_compact(
+        block_table.data_ptr(), seq_lens.data_ptr(), page_shares.data_ptr(), free_pages.data_ptr(), F,
+        free_count.data_ptr(), moves.data_ptr(), n_moves.data_ptr(), page_map.data_ptr(), B, page_size, P, W,
+        _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_compact")
+
+
+def paged_attn_copy_pages(pools, pairs, n_pairs=None, stream=None) -> None:
+    """Copy pages within every pool of a list (dense tensors [num_pages, ...] of any type, all of one
+    num_pages): pairs (int32 [n, 2], (from, to); a pair with a -1 is passed over), the first n_pairs [1] of
+    them if given.  See ``paged_attn_copy_pages`` in include/paged_attn.h."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    if pairs.dim() != 2:
+        raise ValueError("pairs must be [n, 2]")
+    n = len(pools)
+    if n == 0:
+        raise ValueError("pools is empty")
+    P = pools[0].shape[0] if pools[0].dim() else 0
+    where, size = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+    for i, t in enumerate(pools):
+        if t.get_device() != dev or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != P or P == 0:
+            raise ValueError(f"pools[{i}] must be a dense tensor [{P}, ...] on the current CUDA device {dev}")
+        where[i], size[i] = t.data_ptr(), t.numel() // P * t.element_size()
+    _need(pairs, "pairs", dev, torch.int32, (pairs.shape[0], 2))
+    if n_pairs is not None:
+        _need(n_pairs, "n_pairs", dev, torch.int32, (1,))
+    rc = load_library().paged_attn_copy_pages(where, size, n, pairs.data_ptr(), pairs.shape[0], _ptr(n_pairs), P,
+                                              _stream(stream))
+    if rc:
+        _raise(rc, "paged_attn_copy_pages")
+
+
 def paged_attn_combine(part_out, part_lse, out, lse=None, stream=None) -> None:
     """Merge split partials: part_out [S, ..., D] f32, part_lse [S, ...] f32 -> out [..., D], lse [...]."""
     torch = _torch()
@@ -883,3 +1096,63 @@ def attention_sparse(q, k_cache, v_cache, k_env, k_env_scale, block_table, seq_l
                           stream)
     extra = ([lse] if want_lse else []) + ([sel] if want_pages else [])
     return (out, *extra) if extra else out
+
+
+def kv4_pool(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """A zeroed 4-bit pool for K and V, uint8 [num_pages, num_kv_heads, 9 * page_size * head_dim / 8]: 4.5 bits an
+    element; see ``paged_attn_append_kv4`` in include/paged_attn.h."""
+    return _torch().zeros((num_pages, num_kv_heads, 9 * page_size * head_dim // 8), dtype=_torch().uint8, device=device)
+
+
+def attention_kv4(q, kv, block_table, seq_lens, *, causal: bool = True, q_offset=None, q_start=None,
+                  scale: Optional[float] = None, want_lse: bool = False, stream=None):
+    """``paged_attn_fwd_kv4`` with its outputs allocated: returns ``out``, or ``(out, lse)``.  Rows of a packed q
+    that belong to no sequence are not written."""
+    torch = _torch()
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
+    _record(stream, out, lse)
+    paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, out, lse, q_start, stream)
+    return (out, lse) if want_lse else out
+
+
+def _record(stream, *tensors) -> None:
+    """Tensors allocated on the current stream and used on another."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def fork_sequences(parents, children, block_table, seq_lens, page_shares, free_pages, free_count, pools, page_size: int,
+                   prefix_lens=None, stream=None):
+    """``paged_attn_fork`` and the copies of the last pages in every pool of the list; seq_lens and free_count are
+    updated in place.  Returns the pairs that were copied, [n, 2]."""
+    torch = _torch()
+    copies = torch.empty((parents.shape[0], 2), dtype=torch.int32, device=block_table.device)
+    _record(stream, copies)
+    paged_attn_fork(parents, children, block_table, seq_lens, seq_lens, page_shares, free_pages, free_count, free_count,
+                    copies, page_size, prefix_lens, stream)
+    paged_attn_copy_pages(pools, copies, None, stream)
+    return copies
+
+
+def free_sequences(rows, block_table, seq_lens, page_shares, free_pages, free_count, page_size: int, stream=None) -> None:
+    """``paged_attn_free`` with seq_lens and free_count updated in place."""
+    paged_attn_free(rows, block_table, seq_lens, seq_lens, page_shares, free_pages, free_count, free_count, page_size,
+                    stream)
+
+
+def compact_pages(block_table, seq_lens, page_shares, free_pages, free_count, pools, page_size: int, stream=None):
+    """``paged_attn_compact`` and the moves of the contents in every pool of the list.  Returns (page_map, n_moves):
+    every page's new id, and how many pages moved (a tensor)."""
+    torch = _torch()
+    P = page_shares.shape[0]
+    moves, n_moves, page_map = (torch.empty(s, dtype=torch.int32, device=block_table.device) for s in ((P // 2, 2), 1, P))
+    _record(stream, moves, n_moves, page_map)
+    paged_attn_compact(block_table, seq_lens, page_shares, free_pages, free_count, moves, n_moves, page_map, page_size,
+                       stream)
+    paged_attn_copy_pages(pools, moves, n_moves, stream)
+    return page_map, n_moves

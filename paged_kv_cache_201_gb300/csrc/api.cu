@@ -877,6 +877,205 @@ int paged_attn_sparse_shares_pages(const pa_dims *dims, int packed, int top_k, f
     return sparse_shares_pages(dims, n_tok, packed != 0, top_k, scale, num_sms) ? 1 : 0;
 }
 
+// ---------------------------------------------------------------- 4-bit cache, pages of a cache
+namespace {
+
+int kv4_rows_call(const void *k, const void *v, void *k_out, void *v_out, const int32_t *slots, int64_t k_stride,
+                  int64_t v_stride, void *kv, const pa_dims *dims, void *stream) {
+    int rc = check_dims(dims);
+    if (rc != PA_OK) return rc;
+    const int64_t row = (int64_t)dims->num_kv_heads * dims->head_dim;
+    for (int64_t s : {k_stride, v_stride})
+        if (s != 0 && (s < row || (s * esize_of(dims->dtype)) % 16 != 0 || s >= (int64_t)1 << 40)) return PA_EINVAL;
+    if (dims->q_len == 0) return PA_OK;
+    const void *a = k_out ? k_out : k, *b = v_out ? v_out : v;
+    if (!a || !b || !slots || !kv || (k_out == nullptr) != (v_out == nullptr)) return PA_EINVAL;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(kv) || !aligned4(slots)) return PA_EINVAL;
+    pa::Kv4RowsParams p{};
+    if ((rc = error_word_ptr(&p.err)) != PA_OK) return rc;
+    p.k = k;
+    p.v = v;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.slots = slots;
+    p.pool = static_cast<uint8_t *>(kv);
+    p.k_stride = k_stride ? k_stride : row;
+    p.v_stride = v_stride ? v_stride : row;
+    p.num_slots = dims->num_pages * dims->page_size;
+    p.T = dims->q_len;
+    p.Hkv = dims->num_kv_heads;
+    p.ps_shift = dims->page_size == 16 ? 4 : dims->page_size == 32 ? 5 : 6;
+    return cuda_status(pa::launch_kv4_rows(p, dims->dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks that paged_attn_fork, _free and _compact share.
+int check_pages(int n, int free_cap, int batch, int page_size, int64_t num_pages, int bt_stride) {
+    if (n < 0 || batch < 0 || free_cap < 0 || bt_stride < 0 || num_pages < 1) return PA_EINVAL;
+    if (page_size != 16 && page_size != 32 && page_size != 64) return PA_EUNSUPPORTED;
+    if (num_pages >= ((int64_t)1 << 31) / page_size || (int64_t)bt_stride * page_size >= (int64_t)1 << 31 ||
+        batch > PA_STEP_MAX_BATCH || n > PA_STEP_MAX_BATCH || (int64_t)n * bt_stride >= (int64_t)1 << 30)
+        return PA_EUNSUPPORTED;
+    return PA_OK;
+}
+
+}  // namespace
+
+int paged_attn_append_kv4(const void *k_new, const void *v_new, const int32_t *slots, int64_t k_stride,
+                          int64_t v_stride, void *kv, const pa_dims *dims, void *stream) {
+    return kv4_rows_call(k_new, v_new, nullptr, nullptr, slots, k_stride, v_stride, kv, dims, stream);
+}
+
+int paged_attn_gather_kv4(const void *kv, const int32_t *slots, void *k_out, void *v_out, const pa_dims *dims,
+                          void *stream) {
+    if (dims && dims->q_len > 0 && (!k_out || !v_out)) return PA_EINVAL;
+    return kv4_rows_call(nullptr, nullptr, k_out, v_out, slots, 0, 0, const_cast<void *>(kv), dims, stream);
+}
+
+int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table, const int32_t *seq_lens,
+                       const int32_t *q_start, int causal, const int32_t *q_offset, float scale, void *out, float *lse,
+                       const pa_dims *dims, void *stream) {
+    int rc = check_dims(dims);
+    if (rc != PA_OK) return rc;
+    if (dims->dtype == PA_F32) return PA_EDTYPE;
+    if (!isfinite(scale)) return PA_EINVAL;
+    const int64_t n_tok = dims->batch == 0 ? 0 : q_start ? (int64_t)dims->q_len : (int64_t)dims->batch * dims->q_len;
+    if (n_tok == 0) return PA_OK;
+    rc = check_fwd_pointers(q, kv, kv, block_table, seq_lens, q_offset, 1, out, lse);
+    if (rc != PA_OK) return rc;
+    if (!aligned4(q_start)) return PA_EINVAL;
+    unsigned int *err = nullptr;
+    if ((rc = error_word_ptr(&err)) != PA_OK) return rc;
+    pa::SparseParams sp{};
+    sp.f = fill_params(q, kv, nullptr, block_table, seq_lens, causal, q_offset, 1, scale, out, lse, dims, err);
+    sp.f.q_start = q_start;
+    sp.n_tok = n_tok;
+    return cuda_status(pa::launch_kv4_mma(sp, dims->dtype, device_sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+int paged_attn_fork(const int32_t *parents, const int32_t *children, const int32_t *prefix_lens, int n,
+                    int32_t *block_table, const int32_t *seq_lens, int32_t *lens_out, int32_t *page_shares,
+                    const int32_t *free_pages, int free_cap, const int32_t *free_count, int32_t *free_left,
+                    int32_t *copies, int batch, int page_size, int64_t num_pages, int bt_stride, void *stream) {
+    int rc = check_pages(n, free_cap, batch, page_size, num_pages, bt_stride);
+    if (rc != PA_OK) return rc;
+    if (!free_count || !free_left || !page_shares) return PA_EINVAL;
+    if ((n > 0 && (!parents || !children || !copies)) || (batch > 0 && (!seq_lens || !lens_out)) ||
+        (free_cap > 0 && !free_pages) || ((int64_t)batch * bt_stride > 0 && !block_table))
+        return PA_EINVAL;
+    for (const void *ptr : {(const void *)parents, (const void *)children, (const void *)prefix_lens,
+                            (const void *)block_table, (const void *)seq_lens, (const void *)lens_out,
+                            (const void *)page_shares, (const void *)free_pages, (const void *)free_count,
+                            (const void *)free_left, (const void *)copies})
+        if (!aligned4(ptr)) return PA_EINVAL;
+    pa::PagesParams p{};
+    if ((rc = error_word_ptr(&p.err)) != PA_OK) return rc;
+    p.rows = parents;
+    p.children = children;
+    p.prefix_lens = prefix_lens;
+    p.n = n;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.lens_out = lens_out;
+    p.shares = page_shares;
+    p.free_pages = const_cast<int32_t *>(free_pages);
+    p.free_cap = free_cap;
+    p.free_count = free_count;
+    p.free_left = free_left;
+    p.copies = copies;
+    p.B = batch;
+    p.ps_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+    p.num_pages = num_pages;
+    p.W = bt_stride;
+    return cuda_status(pa::launch_fork(p, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_attn_free(const int32_t *rows, int n, const int32_t *block_table, const int32_t *seq_lens, int32_t *lens_out,
+                    int32_t *page_shares, int32_t *free_pages, int free_cap, const int32_t *free_count,
+                    int32_t *free_left, int batch, int page_size, int64_t num_pages, int bt_stride, void *stream) {
+    int rc = check_pages(n, free_cap, batch, page_size, num_pages, bt_stride);
+    if (rc != PA_OK) return rc;
+    if (!free_count || !free_left || !page_shares) return PA_EINVAL;
+    if ((n > 0 && !rows) || (batch > 0 && (!seq_lens || !lens_out)) || (free_cap > 0 && !free_pages) ||
+        ((int64_t)batch * bt_stride > 0 && !block_table))
+        return PA_EINVAL;
+    for (const void *ptr : {(const void *)rows, (const void *)block_table, (const void *)seq_lens,
+                            (const void *)lens_out, (const void *)page_shares, (const void *)free_pages,
+                            (const void *)free_count, (const void *)free_left})
+        if (!aligned4(ptr)) return PA_EINVAL;
+    pa::PagesParams p{};
+    if ((rc = error_word_ptr(&p.err)) != PA_OK) return rc;
+    p.rows = rows;
+    p.n = n;
+    p.block_table = const_cast<int32_t *>(block_table);
+    p.seq_lens = seq_lens;
+    p.lens_out = lens_out;
+    p.shares = page_shares;
+    p.free_pages = free_pages;
+    p.free_cap = free_cap;
+    p.free_count = free_count;
+    p.free_left = free_left;
+    p.B = batch;
+    p.ps_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+    p.num_pages = num_pages;
+    p.W = bt_stride;
+    return cuda_status(pa::launch_free(p, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_attn_compact(int32_t *block_table, const int32_t *seq_lens, int32_t *page_shares, int32_t *free_pages,
+                       int free_cap, int32_t *free_count, int32_t *moves, int32_t *n_moves, int32_t *page_map, int batch,
+                       int page_size, int64_t num_pages, int bt_stride, void *stream) {
+    int rc = check_pages(batch, free_cap, batch, page_size, num_pages, bt_stride);
+    if (rc != PA_OK) return rc;
+    if (!free_count || !page_shares || !n_moves || !page_map || (num_pages > 1 && !moves)) return PA_EINVAL;
+    if ((batch > 0 && !seq_lens) || (free_cap > 0 && !free_pages) || ((int64_t)batch * bt_stride > 0 && !block_table))
+        return PA_EINVAL;
+    for (const void *ptr : {(const void *)block_table, (const void *)seq_lens, (const void *)page_shares,
+                            (const void *)free_pages, (const void *)free_count, (const void *)moves,
+                            (const void *)n_moves, (const void *)page_map})
+        if (!aligned4(ptr)) return PA_EINVAL;
+    pa::PagesParams p{};
+    if ((rc = error_word_ptr(&p.err)) != PA_OK) return rc;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.shares = page_shares;
+    p.free_pages = free_pages;
+    p.free_cap = free_cap;
+    p.free_count = free_count;
+    p.free_left = free_count;
+    p.moves = moves;
+    p.n_moves = n_moves;
+    p.page_map = page_map;
+    p.B = batch;
+    p.ps_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+    p.num_pages = num_pages;
+    p.W = bt_stride;
+    return cuda_status(pa::launch_compact(p, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_attn_copy_pages(void *const *pools, const int64_t *page_bytes, int n_pools, const int32_t *pairs, int max_pairs,
+                          const int32_t *n_pairs, int64_t num_pages, void *stream) {
+    if (n_pools < 0 || max_pairs < 0 || num_pages < 1) return PA_EINVAL;
+    if (n_pools > PA_COPY_MAX_POOLS || num_pages >= (int64_t)1 << 31) return PA_EUNSUPPORTED;
+    if (n_pools > 0 && (!pools || !page_bytes)) return PA_EINVAL;
+    pa::CopyPagesParams p{};
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i] || !aligned4(pools[i]) || page_bytes[i] < 4 || page_bytes[i] % 4 != 0) return PA_EINVAL;
+        if (page_bytes[i] >= (int64_t)1 << 31) return PA_EUNSUPPORTED;
+        p.pool[i] = static_cast<uint8_t *>(pools[i]);
+        p.bytes[i] = page_bytes[i];
+    }
+    if (n_pools == 0 || max_pairs == 0) return PA_OK;
+    if (!pairs || !aligned4(pairs) || !aligned4(n_pairs)) return PA_EINVAL;
+    int rc = error_word_ptr(&p.err);
+    if (rc != PA_OK) return rc;
+    p.pairs = pairs;
+    p.n_pairs = n_pairs;
+    p.num_pages = num_pages;
+    p.n_pools = n_pools;
+    p.max_pairs = max_pairs;
+    return cuda_status(pa::launch_copy_pages(p, device_sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
 int paged_attn_combine(const float *part_out, const float *part_lse, int split_kv, int64_t rows, int head_dim,
                        int out_dtype, void *out, float *lse, void *stream) {
     if (out_dtype != PA_F32 && out_dtype != PA_F16 && out_dtype != PA_BF16) return PA_EDTYPE;

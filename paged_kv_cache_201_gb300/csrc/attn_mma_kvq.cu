@@ -100,13 +100,6 @@ __device__ __forceinline__ uint32_t ring_chunk_addr(uint32_t stage, int k, int c
     return stage + (uint32_t)(k * D + (pc << 4));
 }
 
-__device__ __forceinline__ void lds_v4(uint32_t addr, uint32_t (&w)[4]) {
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
 template <int FMT, int D>
 __device__ __forceinline__ void widen_keys(uint32_t ring, uint32_t wide, int kw0, int key_end, int lane) {
     constexpr int C8 = D / 16;  // 16-byte chunks of 8-bit elements per row
@@ -135,24 +128,6 @@ __device__ __forceinline__ void widen_keys(uint32_t ring, uint32_t wide, int kw0
                      "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                      : "memory");
     }
-}
-
-// Power of two that brings a row whose largest magnitude is amax into f16 with amax x scale in
-// [2^14, 2^15) (clamped to 2^[-113, 100], so both it and its inverse are normal floats); the inverse
-// goes to inv.  Elements below 2^-28 amax become f16 subnormals: their terms of a dot product are
-// below 2^-28 of its largest term.
-__device__ __forceinline__ float f16_row_scale(float amax, float &inv) {
-    const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // amax in [2^e, 2^(e+1))
-    const int s = max(-113, min(14 - e, 100));
-    inv = __uint_as_float((uint32_t)(127 - s) << 23);
-    return __uint_as_float((uint32_t)(127 + s) << 23);
-}
-
-// bf16 pair x (power of two) -> f16 pair, round to nearest even (exact for normal f16 results:
-// a bf16 number has 8 significant bits).
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2_scaled(uint32_t w, float sc) {
-    const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * sc, __uint_as_float(w & 0xffff0000u) * sc);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // K operand of one n-tile (8 keys) for every MMA step: this lane's key row `k`, bytes
@@ -199,14 +174,6 @@ __device__ __forceinline__ void load_q_row(const T *row, bool valid, int tq, uin
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) w[i] = bf16x2_to_f16x2_scaled(w[i], sc);
     }
-}
-
-// Transpose of an 8 x 8 matrix of 16-bit elements held one row pair per lane (lane 4 r + c holds
-// elements (r, 2c) and (r, 2c + 1)); returns the same lane's pair of the transpose.
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
 }
 
 // The producer warp of one unit.  Page ids come 32 at a time, one per lane, never past the unit's

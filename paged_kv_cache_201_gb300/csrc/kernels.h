@@ -144,4 +144,45 @@ cudaError_t launch_sparse_tc05(const SparseParams &p, int dtype, const CUtensorM
 // f32: CUDA cores, a list split over a cluster when there are few rows
 cudaError_t launch_sparse_simt(const SparseParams &p, int sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- 4-bit cache
+struct Kv4RowsParams {
+    const void *k, *v;    // append: new rows
+    void *k_out, *v_out;  // gather: values (null for append)
+    const int32_t *slots;
+    uint8_t *pool;
+    unsigned int *err;
+    long long k_stride, v_stride;  // elements between tokens
+    long long num_slots;           // num_pages * ps
+    int T, Hkv, ps_shift;
+};
+cudaError_t launch_kv4_rows(const Kv4RowsParams &p, int dtype, int D, cudaStream_t stream);
+// Attention over a 4-bit pool (p.f.k_cache), bf16/f16 queries: mma.sync, a sequence's keys split over a cluster when
+// there are few rows.
+cudaError_t launch_kv4_mma(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- pages of a cache
+constexpr int kCopyMaxPools = PA_COPY_MAX_POOLS;
+struct CopyPagesParams {
+    uint8_t *pool[kCopyMaxPools];
+    long long bytes[kCopyMaxPools];  // of a page
+    const int32_t *pairs, *n_pairs;
+    unsigned int *err;
+    long long num_pages;
+    int n_pools, max_pairs;
+};
+cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t stream);
+
+struct PagesParams {
+    const int32_t *rows, *children, *prefix_lens;  // fork: parents, children, prefixes or null; free: rows
+    const int32_t *seq_lens, *free_count;
+    int32_t *block_table, *lens_out, *shares, *free_pages, *free_left, *copies;
+    int32_t *moves, *n_moves, *page_map;  // compact
+    unsigned int *err;
+    long long num_pages;
+    int n, B, W, ps_shift, free_cap;
+};
+cudaError_t launch_fork(const PagesParams &p, cudaStream_t stream);
+cudaError_t launch_free(const PagesParams &p, cudaStream_t stream);
+cudaError_t launch_compact(const PagesParams &p, cudaStream_t stream);
+
 }  // namespace pa

@@ -1,0 +1,72 @@
+// The 4-bit cache: how a pool's bytes stand for K and V elements.
+//
+// The block of a (page, kv head) is contiguous: the K codes of its page_size rows (D / 2 bytes a row: element 2i
+// in the low half of byte i, 2i + 1 in the high one), the V codes, the K scales (D / 16 bytes a row) and the V
+// scales.  A code u in 0 .. 15 stands for u - 8, a scale byte for a number of five exponent and three mantissa
+// bits without a sign: shifted left by 7 its bits are the f16 number's; bytes past kMaxScaleByte count as it, so
+// that any byte is finite.  The element is (u - 8) x scale: at most four significant bits by four, an exact f16
+// and bf16 number.
+#pragma once
+
+#include "common.cuh"
+
+namespace pa {
+namespace kv4 {
+
+constexpr int kGroup = 16;                 // elements that share a scale
+constexpr uint32_t kMaxScaleByte = 0xDE;   // 7168: nine times the largest scale is still an f16 number (see unpack8)
+constexpr float kMaxScale = 7168.f;
+
+__host__ __device__ constexpr int block_bytes(int ps, int D) { return ps * D / 8 * 9; }
+
+// Where a row's parts stand in a block.
+struct Layout {
+    int ps, D;
+    __device__ __forceinline__ int codes(int side, int row) const { return (side * ps + row) * (D / 2); }
+    __device__ __forceinline__ int scales(int side, int row) const { return ps * D + (side * ps + row) * (D / kGroup); }
+};
+
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return __half2float(__ushort_as_half((unsigned short)(min(byte, kMaxScaleByte) << 7)));
+}
+
+// The scale byte of 16 elements whose largest magnitude is a: a / 7 rounded to nearest even.  The division is
+// rounded too, but never onto a border: a border has five significant bits, and where a / 7 lies beside one,
+// a is at least a unit in its last place off seven times it, which is more than half a unit of the quotient.
+__device__ __forceinline__ uint32_t scale_byte(float a) {
+    const float t = fminf(__fdiv_rn(a, 7.f), kMaxScale);
+    if (t < 0x1p-14f) return (uint32_t)__float2int_rn(t * 0x1p17f);  // multiples of 2^-17
+    const uint32_t u = __float_as_uint(t);
+    return min(((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3), kMaxScaleByte);
+}
+
+// Eight codes of a word -> four f16 pairs, pair k = codes k and k + 4, as (u - 8) x scale / 8.  s = scale / 128,
+// c = -9 scale: the code, put below the leading bits of an f16 number, reads 1024 + 16 u, and
+// (1024 + 16 u) s + c = (u - 8) scale / 8 in one rounding, which has nothing to round (an f16 number's last bit is
+// 2^-24 at least, the smallest scale's 2^-17).
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t s, uint32_t c, uint32_t (&h)[4]) {
+    h[0] = fma2(((w << 4) & 0x00F000F0u) | 0x64006400u, s, c);
+    h[1] = fma2((w & 0x00F000F0u) | 0x64006400u, s, c);
+    h[2] = fma2(((w >> 4) & 0x00F000F0u) | 0x64006400u, s, c);
+    h[3] = fma2(((w >> 8) & 0x00F000F0u) | 0x64006400u, s, c);
+}
+// Two scale bytes, one in the low byte of each half of x -> the operands s and c of unpack8.
+__device__ __forceinline__ void scale_pair(uint32_t x, uint32_t &s, uint32_t &c) {
+    uint32_t f;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(f) : "r"(x << 7), "r"(0x6F006F00u));  // 7168; a NaN's bits give it too
+    s = mul2(f, 0x20002000u);  // 2^-7
+    c = mul2(f, 0xC880C880u);  // -9
+}
+
+}  // namespace kv4
+}  // namespace pa

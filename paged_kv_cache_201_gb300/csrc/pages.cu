@@ -1,0 +1,519 @@
+// Pages shared, given back and moved together: the bookkeeping of a paged cache on the device.
+//
+// Each call is one launch of one cluster of CTAs, which takes its steps between cluster barriers; what a step
+// needs from another CTA's shared memory (counts of a scan) it reads there, so no call needs a workspace or a second
+// launch.  What the requests come to (prefix sums of at most PA_STEP_MAX_BATCH small numbers) every CTA works out for
+// itself; the listed pages, one after the other over the rows, are shared out in runs, one a warp.
+//
+// Sums of page counts do not depend on the order of their atomics.  Where an order shows (the stack of free pages), it is
+// fixed: a page that several rows give back belongs to the smallest place that lists it, found with an atomic
+// minimum in page_shares itself.  A page's count runs from its owners - 1 down; below 0 the page is free, and
+// the places' numbers, INT_MIN + e with e < 2^30, lie below every count that is reached.
+#include <limits.h>
+
+#include "sparse_common.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kMaxCtas = 8;
+constexpr int kPer = PA_STEP_MAX_BATCH / kThreads;  // requests of a thread at most
+
+struct Pair {
+    int a, b;
+};
+
+// Exclusive prefix sums over the block, one pair a thread; the totals in every thread.
+__device__ __forceinline__ Pair block_scan(Pair v, Pair *warp_sums, Pair &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Pair inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int xa = __shfl_up_sync(0xffffffffu, inc.a, o), xb = __shfl_up_sync(0xffffffffu, inc.b, o);
+        if (lane >= o) inc.a += xa, inc.b += xb;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    Pair w = warp_sums[lane], run = w;  // every warp sums the warps before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int xa = __shfl_up_sync(0xffffffffu, run.a, o), xb = __shfl_up_sync(0xffffffffu, run.b, o);
+        if (lane >= o) run.a += xa, run.b += xb;
+    }
+    total.a = __shfl_sync(0xffffffffu, run.a, 31);
+    total.b = __shfl_sync(0xffffffffu, run.b, 31);
+    const int before_a = __shfl_sync(0xffffffffu, run.a - w.a, warp);
+    const int before_b = __shfl_sync(0xffffffffu, run.b - w.b, warp);
+    __syncthreads();  // warp_sums may be written again
+    return {before_a + inc.a - v.a, before_b + inc.b - v.b};
+}
+
+// The sums of the cluster's warps before this one, from one pair a warp in every CTA's shared memory.
+__device__ __forceinline__ Pair cluster_scan(Pair mine, Pair *s_warp, int ctas, int rank, Pair &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) s_warp[warp] = mine;
+    cluster_barrier();
+    Pair before{0, 0}, all{0, 0};
+    for (int c = 0; c < ctas; ++c) {
+        const uint32_t at = peer_addr(smem_u32(s_warp + lane), c);
+        Pair v;
+        asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.a), "=r"(v.b) : "r"(at) : "memory");
+        all.a += v.a, all.b += v.b;
+        if (c < rank || (c == rank && lane < warp)) before.a += v.a, before.b += v.b;
+    }
+    total = {__reduce_add_sync(0xffffffffu, all.a), __reduce_add_sync(0xffffffffu, all.b)};
+    return {__reduce_add_sync(0xffffffffu, before.a), __reduce_add_sync(0xffffffffu, before.b)};
+}
+
+// Pages of a row of this length; lengths past the row's width are cut.
+__device__ __forceinline__ int pages_of(const PagesParams &p, int len, bool &clipped) {
+    const long long most = (long long)p.W << p.ps_shift;
+    if (len > most) {
+        clipped = true;
+        len = (int)most;
+    }
+    return (max(len, 0) + (1 << p.ps_shift) - 1) >> p.ps_shift;
+}
+
+// Places e = 0 .. total - 1 of the lists, place e the (e - s_start[i])-th of list i with s_start[i] <= e < s_start[i + 1].
+// This warp's run of them, 32 at a time: f(e, i, j, live) with every lane of the warp.
+template <typename F>
+__device__ __forceinline__ void for_places(const int *s_start, int n, int total, int warp_all, int warps_all, F f) {
+    const int run = ((total + warps_all - 1) / warps_all + 31) & ~31;
+    const int e0 = (int)min((long long)warp_all * run, (long long)total), e1 = (int)min((long long)e0 + run, (long long)total);
+    int lo = 0;
+    for (int first = e0; first < e1; first += 32) {
+        const int e = first + (threadIdx.x & 31);
+        const bool live = e < e1;
+        int hi = n;
+        if (live)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_start[mid] <= e)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+        f(e, lo, live ? e - s_start[lo] : 0, live);
+    }
+}
+
+}  // namespace
+
+// PER: requests of a thread at most.
+template <int PER>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_fork_kernel(const PagesParams p) {
+    extern __shared__ int sm[];
+    int *s_start = sm, *s_row = sm + p.n + 1;  // [n + 1] first places, [n] parent's row
+    int *s_named = s_row + p.n;                // [B] the first request that names a child
+    int *s_child = s_named;                    // [n] the child's row, once that is known
+    __shared__ Pair warp_sums[kWarps];
+    const int tid = threadIdx.x, ctas = gridDim.x, rank = blockIdx.x;
+    const int per = (p.n + kThreads - 1) / kThreads;
+    const int i0 = min(tid * per, p.n), mine = min(per, p.n - i0);
+    const int ps_mask = (1 << p.ps_shift) - 1;
+    bool refused = false, clipped = false, bad_page = false;
+    const int count_in = *p.free_count;
+    const int F = min(max(count_in, 0), p.free_cap);
+    refused |= F != count_in;
+
+    for (int b = tid; b < p.B; b += kThreads) s_named[b] = INT_MAX;
+    __syncthreads();
+    int par[PER], chi[PER], len[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        par[k] = k < mine ? __ldg(p.rows + i0 + k) : -1;
+        chi[k] = k < mine ? __ldg(p.children + i0 + k) : -1;
+        len[k] = k < mine && p.prefix_lens ? __ldg(p.prefix_lens + i0 + k) : INT_MAX;
+        if (par[k] != -1 && chi[k] >= 0 && chi[k] < p.B) atomicMin(s_named + chi[k], i0 + k);
+    }
+    __syncthreads();
+    // usable requests: len the shared length; others: -1
+    Pair sum{0, 0}, total;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const bool asked = par[k] != -1;
+        bool ok = asked && par[k] >= 0 && par[k] < p.B && chi[k] >= 0 && chi[k] < p.B && par[k] != chi[k] && len[k] >= 0;
+        ok = ok && s_named[chi[k]] == i0 + k && __ldcg(p.seq_lens + chi[k]) == 0;
+        if (ok) {
+            const int have = max(__ldcg(p.seq_lens + par[k]), 0);
+            const long long most = (long long)p.W << p.ps_shift;
+            clipped |= have > most;
+            len[k] = (int)min((long long)min(len[k], have), most);
+        } else {
+            refused |= asked;
+            len[k] = -1;
+        }
+        sum.a += ok && (len[k] & ps_mask) != 0;
+    }
+    Pair run = block_scan(sum, warp_sums, total);  // pages that the usable requests before need
+    sum = {0, 0};
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (len[k] < 0) continue;
+        const int need = (len[k] & ps_mask) != 0;
+        run.a += need;
+        if (need && run.a > F) {
+            refused = true;
+            len[k] = -1;
+            continue;
+        }
+        sum.a += need;
+        sum.b += len[k] >> p.ps_shift;
+    }
+    run = block_scan(sum, warp_sums, total);  // of the served ones: pages taken, full pages
+    cluster_barrier();                        // every CTA has read the lengths and the count
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (k >= mine) continue;
+        const int i = i0 + k;
+        const bool served = len[k] >= 0, need = served && (len[k] & ps_mask) != 0;
+        s_start[i] = run.b;
+        s_row[i] = par[k];
+        s_child[i] = chi[k];
+        if (rank == 0) {
+            int from = -1, to = -1;
+            if (need) {
+                const int j = len[k] >> p.ps_shift;
+                from = __ldg(p.block_table + (long long)par[k] * p.W + j);
+                to = __ldg(p.free_pages + (F - 1 - run.a));
+                p.block_table[(long long)chi[k] * p.W + j] = to;
+                if (from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages) {
+                    bad_page = true;
+                    from = to = -1;
+                }
+            }
+            p.copies[2 * i] = from;
+            p.copies[2 * i + 1] = to;
+        }
+        if (served) {
+            run.a += need;
+            run.b += len[k] >> p.ps_shift;
+        }
+    }
+    if (tid == 0) s_start[p.n] = total.b;
+    if (rank == 0) {
+        if (tid == 0) *p.free_left = F - total.a;
+        if (p.lens_out != p.seq_lens)
+            for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = p.seq_lens[b];
+    }
+    __syncthreads();
+    if (rank == 0) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (k < mine && len[k] >= 0) p.lens_out[chi[k]] = len[k];
+    }
+    // the full pages' entries; no row that is read here is written (a child's length was 0)
+    for_places(s_start, p.n, total.b, rank * kWarps + (tid >> 5), ctas * kWarps, [&](int, int i, int j, bool live) {
+        if (!live) return;
+        const int id = __ldg(p.block_table + (long long)s_row[i] * p.W + j);
+        p.block_table[(long long)s_child[i] * p.W + j] = id;
+        if (id >= 0 && id < p.num_pages)
+            atomicAdd(p.shares + id, 1);
+        else
+            bad_page = true;
+    });
+    if (refused) atomicOr(p.err, (unsigned int)PA_ERRBIT_REFUSED);
+    if (clipped) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
+    if (bad_page) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+}
+
+template <int PER>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const PagesParams p) {
+    extern __shared__ int sm[];
+    int *s_start = sm, *s_row = sm + p.n + 1;  // [n + 1] first places, [n] rows
+    int *s_named = s_row + p.n;                // [B] the first request that names a row
+    __shared__ Pair warp_sums[kWarps];
+    __shared__ __align__(8) Pair s_warp[kWarps];
+    const int tid = threadIdx.x, ctas = gridDim.x, rank = blockIdx.x;
+    const int warp_all = rank * kWarps + (tid >> 5), warps_all = ctas * kWarps;
+    const int per = (p.n + kThreads - 1) / kThreads;
+    const int i0 = min(tid * per, p.n), mine = min(per, p.n - i0);
+    bool refused = false, clipped = false, bad_page = false;
+    const int count_in = *p.free_count;
+    const int F = min(max(count_in, 0), p.free_cap);
+    refused |= F != count_in;
+
+    for (int b = tid; b < p.B; b += kThreads) s_named[b] = INT_MAX;
+    __syncthreads();
+    int row[PER], pages[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        row[k] = k < mine ? __ldg(p.rows + i0 + k) : -1;
+        if (row[k] != -1 && (row[k] < 0 || row[k] >= p.B)) {
+            refused = true;
+            row[k] = -1;
+        }
+        if (row[k] >= 0) atomicMin(s_named + row[k], i0 + k);
+    }
+    __syncthreads();
+    Pair sum{0, 0}, total;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (row[k] >= 0 && s_named[row[k]] != i0 + k) row[k] = -1;  // named before
+        pages[k] = row[k] >= 0 ? pages_of(p, __ldcg(p.seq_lens + row[k]), clipped) : 0;
+        sum.a += pages[k];
+    }
+    Pair run = block_scan(sum, warp_sums, total);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (k >= mine) continue;
+        s_start[i0 + k] = run.a;
+        s_row[i0 + k] = row[k];
+        run.a += pages[k];
+    }
+    if (tid == 0) s_start[p.n] = total.a;
+    cluster_barrier();  // every CTA has read the lengths and the count
+    if (rank == 0 && p.lens_out != p.seq_lens)
+        for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = p.seq_lens[b];
+    __syncthreads();
+    if (rank == 0) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (row[k] >= 0) p.lens_out[row[k]] = 0;
+    }
+    auto page_at = [&](int i, int j) { return __ldg(p.block_table + (long long)s_row[i] * p.W + j); };
+    auto in_pool = [&](int id) { return id >= 0 && id < p.num_pages; };
+    // an owner less for every place
+    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int, int i, int j, bool live) {
+        const int id = live ? page_at(i, j) : -1;
+        if (in_pool(id)) atomicSub(p.shares + id, 1);
+        bad_page |= live && !in_pool(id);
+    });
+    cluster_barrier();
+    // the first place of every page that is free now
+    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int e, int i, int j, bool live) {
+        const int id = live ? page_at(i, j) : -1;
+        if (in_pool(id) && __ldcg(p.shares + id) < 0) atomicMin(p.shares + id, INT_MIN + e);
+    });
+    cluster_barrier();
+    Pair n_mine{0, 0}, pushed;
+    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int e, int i, int j, bool live) {
+        const int id = live ? page_at(i, j) : -1;
+        n_mine.a += __popc(__ballot_sync(0xffffffffu, in_pool(id) && __ldcg(p.shares + id) == INT_MIN + e));
+    });
+    int at = cluster_scan(n_mine, s_warp, ctas, rank, pushed).a;
+    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int e, int i, int j, bool live) {
+        const int id = live ? page_at(i, j) : -1;
+        const bool push = in_pool(id) && __ldcg(p.shares + id) == INT_MIN + e;
+        const unsigned all = __ballot_sync(0xffffffffu, push);
+        if (push) {
+            const long long to = (long long)F + pushed.a - 1 - (at + __popc(all & ((1u << (tid & 31)) - 1)));
+            p.shares[id] = 0;
+            if (to < p.free_cap)
+                p.free_pages[to] = id;
+            else
+                refused = true;
+        }
+        at += __popc(all);
+    });
+    if (rank == 0 && tid == 0) *p.free_left = (int)min((long long)F + pushed.a, (long long)p.free_cap);
+    if (refused) atomicOr(p.err, (unsigned int)PA_ERRBIT_REFUSED);
+    if (clipped) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
+    if (bad_page) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+    cluster_barrier();  // the peers have read this CTA's counts
+}
+
+// The used pages to the pool's start.  With U(x) the used pages at or above x and F(x) the free ones below, the first x
+// with F(x) >= U(x) has F(x) = U(x) (one of the two moves by one from page to page): below it every free page takes one
+// of the used pages above, and what lies at or above it and was used or free is free.  Marks (1 used, 2 free) stand in
+// page_map until its values do.
+template <int PER>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const PagesParams p) {
+    extern __shared__ int sm[];
+    int *s_start = sm;  // [B + 1]
+    __shared__ Pair warp_sums[kWarps];
+    __shared__ __align__(8) Pair s_warp[kWarps];
+    __shared__ int s_border[2];
+    const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x, rank = blockIdx.x;
+    const int warp_all = rank * kWarps + (tid >> 5), warps_all = ctas * kWarps;
+    const long long all = (long long)ctas * kThreads, tid_all = (long long)rank * kThreads + tid;
+    const int P = (int)p.num_pages;
+    bool refused = false, clipped = false, bad_page = false;
+    const int count_in = *p.free_count;
+    const int F = min(max(count_in, 0), p.free_cap);
+    refused |= F != count_in;
+    auto in_pool = [&](int id) { return id >= 0 && id < P; };
+
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, p.B), mine = min(per, p.B - b0);
+    int pages[PER];
+    Pair sum{0, 0}, total;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        pages[k] = k < mine ? pages_of(p, __ldg(p.seq_lens + b0 + k), clipped) : 0;
+        sum.a += pages[k];
+    }
+    Pair run = block_scan(sum, warp_sums, total);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (k >= mine) continue;
+        s_start[b0 + k] = run.a;
+        run.a += pages[k];
+    }
+    if (tid == 0) {
+        s_start[p.B] = total.a;
+        s_border[0] = s_border[1] = 0;
+    }
+    for (long long x = tid_all; x < P; x += all) __stcg(p.page_map + x, 0);
+    cluster_barrier();
+    for (long long x = tid_all; x < F; x += all) {
+        const int id = __ldg(p.free_pages + x);
+        if (in_pool(id))
+            refused |= atomicOr(p.page_map + id, 2) != 0;
+        else
+            bad_page = true;
+    }
+    cluster_barrier();
+    for_places(s_start, p.B, total.a, warp_all, warps_all, [&](int, int i, int j, bool live) {
+        const int id = live ? __ldcg(p.block_table + (long long)i * p.W + j) : -1;
+        if (in_pool(id)) {
+            refused |= __ldcg(p.page_map + id) == 2;
+            __stcg(p.page_map + id, 1);
+        }
+        bad_page |= live && !in_pool(id);
+    });
+    cluster_barrier();
+    // every warp's run of pages: its used (a) and free (b) ones, and those of the runs before
+    const int seg = (int)(((long long)P + warps_all - 1) / warps_all + 31) & ~31;
+    const int x0 = (int)min((long long)warp_all * seg, (long long)P), x1 = (int)min((long long)x0 + seg, (long long)P);
+    auto marks = [&](int x, unsigned &used, unsigned &idle) {
+        const int m = x + lane < x1 ? __ldcg(p.page_map + x + lane) : 0;
+        used = __ballot_sync(0xffffffffu, m == 1);
+        idle = __ballot_sync(0xffffffffu, m == 2);
+    };
+    Pair n_mine{0, 0};
+    for (int x = x0; x < x1; x += 32) {
+        unsigned used, idle;
+        marks(x, used, idle);
+        n_mine.a += __popc(used);
+        n_mine.b += __popc(idle);
+    }
+    const Pair before = cluster_scan(n_mine, s_warp, ctas, rank, total);
+    // the border: in the run where F(x) reaches U(x), which one warp of the cluster finds out for all
+    if (before.b < total.a - before.a && before.b + n_mine.b >= total.a - before.a - n_mine.a) {
+        int u = total.a - before.a, f = before.b, border = x0;
+        for (int x = x0; x < x1 && f < u; x += 32) {
+            unsigned used, idle;
+            marks(x, used, idle);
+            const unsigned upto = 2u << lane;  // 0 for lane 31: all
+            const bool there = f + __popc(idle & (upto - 1)) >= u - __popc(used & (upto - 1));
+            const unsigned first = __ballot_sync(0xffffffffu, there);
+            if (first) {
+                border = x + __ffs(first);
+                f += __popc(idle & ((2u << (__ffs(first) - 1)) - 1));
+                break;
+            }
+            f += __popc(idle);
+            u -= __popc(used);
+        }
+        if (lane < ctas) {
+            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(smem_u32(s_border), lane)), "r"(border) : "memory");
+            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(smem_u32(s_border + 1), lane)), "r"(f) : "memory");
+        }
+    }
+    cluster_barrier();
+    const int border = s_border[0], n_moves = s_border[1];
+    // below the border U(0) - n_moves pages are used; at and above it as many are left free as there were
+    int u = before.a, f = before.b;
+    for (int x = x0; x < x1; x += 32) {
+        unsigned used, idle;
+        marks(x, used, idle);
+        const unsigned below = (1u << lane) - 1;
+        const int id = x + lane, ku = u + __popc(used & below), kf = f + __popc(idle & below);
+        const bool is_used = used >> lane & 1, is_idle = idle >> lane & 1;
+        if (id < border) {
+            if (is_idle) p.moves[2 * kf + 1] = id;
+        } else if (is_used || is_idle) {
+            if (is_used) p.moves[2 * (ku - (total.a - n_moves))] = id;
+            p.free_pages[total.b - 1 - (ku - (total.a - n_moves) + kf - n_moves)] = id;
+        }
+        if (id < x1) __stcg(p.page_map + id, id);
+        u += __popc(used);
+        f += __popc(idle);
+    }
+    if (rank == 0 && tid == 0) {
+        *p.n_moves = n_moves;
+        *p.free_left = total.b;
+    }
+    cluster_barrier();
+    for (long long k = tid_all; k < n_moves; k += all) {
+        const int from = __ldcg(p.moves + 2 * k), to = __ldcg(p.moves + 2 * k + 1);
+        __stcg(p.page_map + from, to);
+        p.shares[to] = p.shares[from];
+        p.shares[from] = 0;
+    }
+    cluster_barrier();
+    for_places(s_start, p.B, s_start[p.B], warp_all, warps_all, [&](int, int i, int j, bool live) {
+        int32_t *entry = p.block_table + (long long)i * p.W + j;
+        const int id = live ? __ldcg(entry) : -1;
+        if (!in_pool(id)) return;
+        const int now = __ldcg(p.page_map + id);
+        if (now != id) *entry = now;
+    });
+    if (refused) atomicOr(p.err, (unsigned int)PA_ERRBIT_REFUSED);
+    if (clipped) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
+    if (bad_page) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+}
+
+namespace {
+
+template <typename K>
+cudaError_t launch_cluster(K kern, SmemLimit &limit, size_t smem, size_t smem_max, long long work, const PagesParams &p,
+                           cudaStream_t stream) {
+    const cudaError_t e = limit.raise((const void *)kern, smem_max);
+    if (e != cudaSuccess) return e;
+    int ctas = 1;
+    while (ctas < kMaxCtas && ctas * 2048ll < work) ctas *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+size_t lists_smem(long long n, long long B) { return (size_t)(2 * n + 1 + (n > B ? n : B)) * sizeof(int); }
+
+}  // namespace
+
+template <int PER>
+static cudaError_t launch_fork_n(const PagesParams &p, cudaStream_t stream) {
+    static SmemLimit limit;
+    return launch_cluster(paged_attn_fork_kernel<PER>, limit, lists_smem(p.n, p.B),
+                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, p, stream);
+}
+cudaError_t launch_fork(const PagesParams &p, cudaStream_t stream) {
+    return p.n <= kThreads ? launch_fork_n<1>(p, stream) : launch_fork_n<kPer>(p, stream);
+}
+
+template <int PER>
+static cudaError_t launch_free_n(const PagesParams &p, cudaStream_t stream) {
+    static SmemLimit limit;
+    return launch_cluster(paged_attn_free_kernel<PER>, limit, lists_smem(p.n, p.B),
+                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, p, stream);
+}
+cudaError_t launch_free(const PagesParams &p, cudaStream_t stream) {
+    return p.n <= kThreads ? launch_free_n<1>(p, stream) : launch_free_n<kPer>(p, stream);
+}
+
+template <int PER>
+static cudaError_t launch_compact_n(const PagesParams &p, cudaStream_t stream) {
+    static SmemLimit limit;
+    const long long entries = (long long)p.B * p.W;
+    return launch_cluster(paged_attn_compact_kernel<PER>, limit, (size_t)(p.B + 1) * sizeof(int),
+                          ((size_t)kThreads * PER + 1) * sizeof(int), entries > p.num_pages ? entries : p.num_pages, p, stream);
+}
+cudaError_t launch_compact(const PagesParams &p, cudaStream_t stream) {
+    return p.B <= kThreads ? launch_compact_n<1>(p, stream) : launch_compact_n<kPer>(p, stream);
+}
+
+}  // namespace pa

@@ -1,0 +1,285 @@
+"""The 4-bit cache on the GPU: rows quantised into a pool and read back (bit for bit), and attention over
+the pool against 64-bit arithmetic on the values its bytes stand for.
+
+Attention's bars are derived, not fitted: half a rounding step of the output type (bf16 2^-8, f16 2^-11,
+relative) on top of what float32 sums may lose in the scores, which tests/_kv4_ref.py works out row by row from the
+inputs, and 2^-20 of the largest value for the weights (held to 2^-22) and their sum.
+"""
+import numpy as np
+import pytest
+
+from tests import _kv4_ref as R
+
+pytestmark = pytest.mark.gpu
+
+STEP = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+
+
+@pytest.fixture(scope="module")
+def pa():
+    import paged_kv_cache_201_gb300 as pa
+    pa.load_library(build_if_missing=True)
+    pa.paged_attn_last_error_word()
+    return pa
+
+
+def _dt(name):
+    import torch
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[name]
+
+
+def _t(a, dtype=None):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=dtype)).cuda()
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _rows(rng, shape, dtype):
+    """Rows with groups of very different sizes, zeros among them, and values on the borders between codes."""
+    import torch
+    x = rng.standard_normal(shape) * np.exp(rng.uniform(-12, 6, (*shape[:-1], 1)))
+    x[rng.uniform(size=shape) < 0.1] = 0
+    g = x.reshape(*shape[:-1], -1, 16)
+    g[rng.uniform(size=g.shape[:-1]) < 0.1] = 0
+    tie = rng.uniform(size=g.shape[:-1]) < 0.3  # a group of halves of a power of two: a scale of 1 or 9/8 ...
+    g[tie] = (rng.integers(-15, 16, g[tie].shape) / 2.0) * 2.0 ** rng.integers(-16, 9, (tie.sum(), 1))
+    return torch.from_numpy(x).to(_dt(dtype)).cuda()
+
+
+# ----------------------------------------------------------------------------- rows
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,Hkv,ps", [(1, 1, 16), (37, 3, 32), (130, 8, 64), (300, 2, 16)])
+def test_rows(pa, T, Hkv, D, ps, dtype):
+    import torch
+    rng = np.random.default_rng(T * D + ps)
+    P = -(-T // ps) + 3
+    slots = rng.permutation(P * ps)[:T].astype(np.int32)
+    slots[rng.uniform(size=T) < 0.1] = -1
+    wide = _rows(rng, (T, 3 * Hkv, D), dtype)
+    k, v = wide[:, Hkv:2 * Hkv], wide[:, 2 * Hkv:]  # slices of a projection
+    kv = torch.randint(0, 256, (P, Hkv, 9 * ps * D // 8), dtype=torch.uint8, device="cuda")
+    want = kv.cpu().numpy().copy()
+    pa.paged_attn_append_kv4(k, v, _t(slots), kv)
+    R.write(want, slots, _np(k), _np(v), ps)
+    np.testing.assert_array_equal(kv.cpu().numpy(), want)
+    got_k, got_v = (torch.full((T, Hkv, D), 7.0, dtype=_dt(dtype), device="cuda") for _ in "kv")
+    pa.paged_attn_gather_kv4(kv, _t(slots), got_k, got_v)
+    for got, x in zip((got_k, got_v), R.values(want, ps, D)):
+        held = x.transpose(0, 2, 1, 3).reshape(P * ps, Hkv, D)[np.maximum(slots, 0)]
+        np.testing.assert_array_equal(_np(got), np.where(slots[:, None, None] >= 0, held, 0.0))
+    assert pa.paged_attn_last_error_word() == 0
+
+
+def test_rows_all_scales(pa):
+    """Every scale, and on either side of every border between two of them."""
+    import torch
+    mid = 7 * (R.SCALES[:-1] + R.SCALES[1:]) / 2
+    tops = np.concatenate([7 * R.SCALES, mid, np.nextafter(np.float32(mid), 0), np.nextafter(np.float32(mid), 9e9),
+                           [7 * 7200, 1e30, 3.4e38, 1e-38, 1e-45]]).astype(np.float32)
+    T = len(tops)
+    x = np.zeros((T, 1, 64), np.float32)
+    x[:, 0] = np.random.default_rng(5).uniform(-1, 1, (T, 64)).astype(np.float32) * tops[:, None]
+    x[:, 0, ::16] = tops[:, None]
+    for side in (1, -1):
+        kv = pa.kv4_pool(-(-T // 16), 16, 1, 64)
+        want = kv.cpu().numpy()
+        slots = np.arange(T, dtype=np.int32)
+        pa.paged_attn_append_kv4(_t(side * x), _t(-side * x), _t(slots), kv)
+        R.write(want, slots, side * x.astype(np.float64), -side * x.astype(np.float64), 16)
+        np.testing.assert_array_equal(kv.cpu().numpy(), want)
+    assert pa.paged_attn_last_error_word() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_not_finite(pa, dtype):
+    """NaN counts as 0, infinities as the largest value; both are reported, and nothing else changes."""
+    import torch
+    rng = np.random.default_rng(3)
+    for bad in (np.nan, np.inf, -np.inf):
+        k, v = _rows(rng, (20, 2, 64), dtype), _rows(rng, (20, 2, 64), dtype)
+        k[7, 1, 30], v[9, 0, 2] = bad, bad
+        kv = pa.kv4_pool(2, 16, 2, 64)
+        want = kv.cpu().numpy()
+        slots = np.arange(20, dtype=np.int32)
+        pa.paged_attn_append_kv4(k, v, _t(slots), kv)
+        R.write(want, slots, _np(k), _np(v), 16)
+        np.testing.assert_array_equal(kv.cpu().numpy(), want)
+        assert pa.paged_attn_last_error_status() == (pa.PA_OK, pa.ERRBIT_NONFINITE)
+    # in a row that is not written nothing is reported
+    slots[:] = -1
+    pa.paged_attn_append_kv4(k, v, _t(slots), kv)
+    assert pa.paged_attn_last_error_word() == 0
+
+
+def test_rows_bad_slots(pa):
+    import torch
+    rng = np.random.default_rng(4)
+    k, v = _rows(rng, (6, 2, 128), "bf16"), _rows(rng, (6, 2, 128), "bf16")
+    kv = torch.randint(0, 256, (3, 2, 9 * 16 * 16), dtype=torch.uint8, device="cuda")
+    want = kv.cpu().numpy().copy()
+    slots = np.array([48, -2, 5, 2**31 - 1, -2**31, -1], np.int32)
+    pa.paged_attn_append_kv4(k, v, _t(slots), kv)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+    R.write(want, slots, _np(k), _np(v), 16)
+    np.testing.assert_array_equal(kv.cpu().numpy(), want)
+    a, b = torch.ones_like(k), torch.ones_like(v)
+    pa.paged_attn_gather_kv4(kv, _t(slots), a, b)
+    assert pa.paged_attn_last_error_word() == pa.ERRBIT_PAGE_RANGE
+    assert not _np(a)[[0, 1, 3, 4, 5]].any() and _np(a)[2].any() and not _np(b)[[0, 1, 3, 4, 5]].any()
+
+
+# ----------------------------------------------------------------------------- attention
+def _case(seed, lens, new, Hkv, G, D, ps, dtype, pads=0, spare=2, width=None):
+    """A pool of random rows with garbage behind the last keys, shuffled pages, ragged packed queries."""
+    import torch
+    rng = np.random.default_rng(seed)
+    lens, new = np.asarray(lens), np.asarray(new)
+    need = -(-lens // ps)
+    P = int(need.sum()) + spare
+    pool = rng.integers(0, 256, (P, Hkv, 9 * ps * D // 8)).astype(np.uint8)
+    ids = rng.permutation(P).astype(np.int32)
+    W = width or int(need.max()) + 1
+    table = np.full((len(lens), W), 0x7FFFFFFF, np.int32)
+    table[np.arange(W)[None] < need[:, None]] = ids[:int(need.sum())]
+    slots = np.concatenate([table[b, np.arange(n) // ps] * ps + np.arange(n) % ps for b, n in enumerate(lens)] + [[]])
+    rows = rng.standard_normal((2, len(slots), Hkv, D)) * (1 + 2 * (np.arange(D) % 37 == 5))
+    R.write(pool, slots, rows[0], rows[1], ps)
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((starts[-1] + pads, Hkv * G, D))).to(_dt(dtype)).cuda()
+    return dict(q=q, kv=_t(pool), pool=pool, ps=ps, table=table, lens=lens.astype(np.int32), starts=starts, dtype=dtype)
+
+
+def _check(pa, c, causal=True, q_offset=None, scale=None, packed=True, q=None, err=0):
+    import torch
+    q = c["q"] if q is None else q
+    T, Hq, D = q.shape
+    scale = D ** -0.5 if scale is None else scale
+    out = torch.full((T, Hq, D), 5.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((T, Hq), 5.0, device="cuda")
+    qo = None if q_offset is None else _t(q_offset, np.int32)
+    if packed:
+        pa.paged_attn_fwd_kv4(q, c["kv"], _t(c["table"]), _t(c["lens"]), causal, qo, scale, out, lse,
+                              q_start=_t(c["starts"]))
+    else:
+        B = len(c["lens"])
+        pa.paged_attn_fwd_kv4(q.view(B, -1, Hq, D), c["kv"], _t(c["table"]), _t(c["lens"]), causal, qo, scale,
+                              out.view(B, -1, Hq, D), lse.view(B, -1, Hq))
+    assert pa.paged_attn_last_error_word() == err
+    want, want_lse, off, room = R.attention(_np(q), c["pool"], c["ps"], c["table"], c["lens"], c["starts"], causal,
+                                            q_offset, scale)
+    got, got_lse = _np(out), _np(lse)
+    own = ~np.isnan(want_lse)
+    assert (got[~own] == 5.0).all() and (got_lse[~own] == 5.0).all()  # rows of no sequence
+    empty = own & np.isneginf(want_lse)
+    assert (got[empty] == 0).all() and np.isneginf(got_lse[empty]).all()
+    own &= ~empty
+    bar = STEP[c["dtype"]] * np.abs(want) + room + 2.0 ** -24
+    worst = (np.abs(got - want) / bar)[own]
+    assert worst.size == 0 or worst.max() <= 1, f"output off by {worst.max():.3g} of its bar"
+    worst = (np.abs(got_lse - want_lse) / (off + 2.0 ** -22 * np.abs(want_lse)))[own]
+    assert worst.size == 0 or worst.max() <= 1, f"lse off by {worst.max():.3g} of its bar"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("ps", [16, 32, 64])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 3, 4, 8, 12, 16, 24, 40])
+def test_decode(pa, G, D, ps, dtype):
+    c = _case(G * D + ps, [1, 15, 16, 17, 63, 64, 65, 200, 129], [1] * 9, 2, G, D, ps, dtype)
+    _check(pa, c)
+
+
+@pytest.mark.parametrize("D,G,dtype", [(64, 3, "f16"), (128, 4, "bf16"), (128, 16, "f16"), (256, 2, "bf16")])
+@pytest.mark.parametrize("causal", [False, True])
+def test_ragged_runs(pa, D, G, dtype, causal):
+    """Runs of 0 to 40 tokens beside single ones, sequences without keys, rows behind the last one."""
+    c = _case(D + G, [0, 70, 33, 5, 300, 64, 0, 18], [3, 40, 1, 5, 2, 17, 0, 18], 3, G, D, 16, dtype, pads=6)
+    _check(pa, c, causal)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_uniform_and_offsets(pa, causal):
+    c = _case(8, [40, 90, 7, 64], [6] * 4, 2, 4, 128, 32, "bf16")
+    _check(pa, c, causal, packed=False)
+    # the first tokens see nothing, some only a part, some past the end
+    _check(pa, c, causal, q_offset=[-9, 3, 100, -3], packed=False)
+    _check(pa, c, causal, q_offset=[-9, 3, 100, -3])
+
+
+def test_long_split(pa):
+    """Few rows over many pages: the keys go to the CTAs of a cluster."""
+    _check(pa, _case(1, [9000], [1], 1, 4, 128, 16, "bf16"))
+    _check(pa, _case(2, [5000, 33], [2, 1], 2, 8, 64, 64, "f16"))
+    _check(pa, _case(3, [3000], [1], 1, 2, 256, 32, "bf16"))
+    _check(pa, _case(4, [100], [1], 1, 4, 128, 16, "bf16", width=900))  # a wide table, CTAs without keys
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.5, 40.0])
+def test_scales(pa, scale):
+    """Also scores up to thousands: one key takes everything, references move far."""
+    _check(pa, _case(12, [150, 31], [3, 1], 2, 4, 128, 16, "bf16"), scale=scale)
+
+
+def test_strided_queries(pa):
+    import torch
+    c = _case(13, [80, 40], [5, 2], 2, 4, 128, 16, "bf16")
+    T, Hq, D = c["q"].shape
+    wide = torch.randn((T, Hq + 4, D), device="cuda").bfloat16()
+    wide[:, :Hq] = c["q"]
+    _check(pa, c, q=wide[:, :Hq])
+
+
+def test_bad_pages(pa):
+    """Ids outside the pool read as zeros; other sequences do not notice."""
+    c = _case(14, [100, 70, 200], [2, 1, 1], 2, 4, 128, 16, "bf16")
+    c["table"][0, 2], c["table"][1, 0], c["table"][2, 12] = -1, c["pool"].shape[0], -2**31
+    _check(pa, c, err=pa.ERRBIT_PAGE_RANGE)
+
+
+def test_clipped_lengths(pa):
+    c = _case(15, [64, 40], [1, 1], 1, 2, 64, 16, "f16", width=4)
+    c["lens"][0] = 1000  # more than the row's four pages
+    _check(pa, c, err=pa.ERRBIT_SEQ_CLIPPED)
+
+
+def test_malformed_ranges(pa):
+    """Entries of q_start outside the rows or decreasing: their sequences are skipped and reported."""
+    import torch
+    c = _case(16, [64, 40, 50], [2, 3, 2], 1, 2, 64, 16, "f16")
+    for starts in ([0, 2, 9, 7], [-1, 2, 5, 7], [0, 5, 2, 7], [3, 2, 5, 100]):
+        out = torch.full_like(c["q"], 5.0)
+        pa.paged_attn_fwd_kv4(c["q"], c["kv"], _t(c["table"]), _t(c["lens"]), True, None, 0.1, out, None,
+                              q_start=_t(starts, np.int32))
+        assert pa.paged_attn_last_error_status() == (pa.PA_EINVAL, pa.ERRBIT_QSTART)
+
+
+def test_convenience_and_graph(pa):
+    """Captured append and attention, replayed on new contents; another stream."""
+    import torch
+    c = _case(17, [48, 20], [1, 1], 2, 4, 128, 16, "bf16")
+    kv, table, lens, starts = c["kv"], _t(c["table"]), _t(c["lens"]), _t(c["starts"])
+    ref, ref_lse = pa.attention_kv4(c["q"], kv, table, lens, q_start=starts, want_lse=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = pa.attention_kv4(c["q"], kv, table, lens, q_start=starts, stream=side)
+    side.synchronize()
+    assert torch.equal(got, ref)
+    k = torch.randn((2, 2, 128), device="cuda").bfloat16()
+    slots = _t([c["table"][0, 2] * 16 + 15, c["table"][1, 1] * 16 + 3], np.int32)
+    out = torch.empty_like(c["q"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.paged_attn_append_kv4(k, k, slots, kv)
+        pa.paged_attn_fwd_kv4(c["q"], kv, table, lens, True, None, 128 ** -0.5, out, None, q_start=starts)
+    for seed in range(2):
+        k.copy_(torch.randn((2, 2, 128), generator=torch.Generator().manual_seed(seed)).bfloat16())
+        graph.replay()
+        got = out.clone()
+        pa.paged_attn_append_kv4(k, k, slots, kv)
+        assert torch.equal(got, pa.attention_kv4(c["q"], kv, table, lens, q_start=starts))
+    assert pa.paged_attn_last_error_word() == 0
