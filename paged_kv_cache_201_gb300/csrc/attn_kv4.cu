@@ -1,12 +1,13 @@
 // Attention over a 4-bit cache for bf16 / f16 queries: single tokens and short runs, and whatever the tcgen05 kernel
 // does not take.
 //
-// A unit is up to 8 NR query rows (tokens x the heads of a kv head) of one sequence; a cluster of CTAs shares its
-// keys, and each CTA's four consumer warps share the CTA's: warp w takes keys [16 w, 16 w + 16) of every 64-key
-// stage.  Products are transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and head dimension fill the MMA's
-// 16-row side and a group of up to eight heads its 8-wide side.
+// A unit is up to 8 NR query rows (tokens x the heads of a kv head) of one sequence.  A cluster of CTAs shares its
+// keys in blocks of 16, every warp of it a run of them, with a ring of its own: nothing is shared and nobody waits for
+// another warp until the states are merged.  Products are transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and
+// head dimension fill the MMA's 16-row side and a group of up to eight heads its 8-wide side.
 //
-//   * A (page, kv head) block, codes and scales of K and V, is contiguous: one untiled bulk copy a page.
+//   * A step is two blocks.  The block of a (page, kv head), codes and scales of K and V, is contiguous: a page of 16 rows
+//     is one untiled bulk copy, 16 rows of a larger one are four.
 //   * Codes become f16 operands in registers, (u - 8) x scale / 8, without rounding (kv4.cuh): a shift, a logic
 //     operation and a fused multiply-add for two elements.  The eighth comes back in the score's factor and in
 //     the final division.
@@ -15,12 +16,13 @@
 //     words pairs their halves before the codes are taken apart, so V needs no transposition.
 //   * Softmax statistics are float32.  A weight is 2^(score - ref), ref at least 11 below the largest score so far
 //     when it was last moved and never more than 15 below any: weights stay below 2^15, ref (and with it every sum)
-//     moves rarely, and as an f16 high part and remainder a weight is held to 2^-24, 2^-31 of the row's largest or
-//     less.
-//   * The rows of S^T are physical keys r ^ (r >> 1 & 1): with the four keys of a V load in different rows modulo
+//     moves rarely, and as an f16 high part and remainder a weight is held to 2^-22, or 2^-31 of the row's largest.
+//   * The rows of S^T are keys r ^ (r >> 1 & 1): with the four keys of a V load in different rows modulo
 //     two, their shared-memory loads have half the bank conflicts, and K's none.
 //
 // Any byte stands for a finite number, so what lies behind a sequence's last key needs no cleaning: its weight is 0.
+#include <limits.h>
+
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -33,8 +35,9 @@ using namespace mmac;
 
 namespace {
 
-constexpr int kStageKeys = 64;
+constexpr int kBlockKeys = 16, kStepKeys = 32, kMaxCluster = 16;
 constexpr float kRefBelow = 11.f, kRefMost = 15.f;
+constexpr float kNoRef = -3e38f;  // before the first key; finite, so that kNegInf - ref is no NaN
 
 struct Kv4Params {
     SparseParams s;
@@ -100,55 +103,65 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// Pages [pg0, pg_end) of row bt_row, kStageKeys keys a stage.  An id outside the pool is not followed: its block
-// becomes zeros.
-template <int NSTAGE>
-__device__ __forceinline__ void produce(const FwdParams &p, const int32_t *bt_row, int kvh, int pg0, int pg_end,
-                                        int n_tiles, int ps_shift, int block, uint32_t sbase, uint32_t bar_full,
-                                        uint32_t bar_empty, int lane) {
-    const int pps = kStageKeys >> ps_shift;
-    const uint32_t stage_bytes = (uint32_t)(pps * block);
-    const uint8_t *pool = static_cast<const uint8_t *>(p.k_cache);
-    int batch = pg0;
-    int id_cur = batch + lane < pg_end ? __ldg(bt_row + batch + lane) : 0;
-    int id_next = batch + 32 + lane < pg_end ? __ldg(bt_row + batch + 32 + lane) : 0;
-    bool bad = false;
-    int issued = 0;
-    for (int t = 0; t < n_tiles; ++t) {
-        const int st = t % NSTAGE;
-        if (t >= NSTAGE) {
-            const bool ok = mbar_wait(bar_empty + 8 * st, ((t / NSTAGE) - 1) & 1, p.err);
-            bad = __any_sync(0xffffffffu, !ok);
-            if (bad) break;
+// A warp's ring: blocks [b0, b1) of 16 keys, two a step, into NST slots of its own.
+template <int D, int NST>
+struct Ring {
+    static constexpr int kBlock = kBlockKeys * D / 8 * 9;  // bytes of a block: as a page of 16 rows
+    static constexpr int kStep = 2 * kBlock;
+    const FwdParams &p;
+    const int32_t *bt_row;
+    const uint8_t *pool;  // of this kv head
+    uint32_t smem, bars;
+    int b0, b1, ps_shift, lane;
+    int part, half, lanes;  // which copy of a step this lane issues
+    int id;                 // its page, of the next step to come
+
+    __device__ __forceinline__ Ring(const FwdParams &f, int b, int kvh, int ps_shift_, int block0, int block1, uint32_t smem_,
+                                    uint32_t bars_, int lane_)
+        : p(f), bt_row(f.block_table + (long long)b * f.W),
+          pool(static_cast<const uint8_t *>(f.k_cache) + (long long)kvh * kv4::block_bytes(1 << ps_shift_, D)), smem(smem_),
+          bars(bars_), b0(block0), b1(block1), ps_shift(ps_shift_), lane(lane_) {
+        lanes = ps_shift == 4 ? 2 : 8;
+        half = ps_shift == 4 ? lane : lane >> 2;
+        part = ps_shift == 4 ? 0 : lane & 3;
+        id = look_up(0);
+    }
+    __device__ __forceinline__ int look_up(int step) const {
+        const int blk = b0 + 2 * step + half;
+        return lane < lanes && blk < b1 ? __ldg(bt_row + (blk >> (ps_shift - 4))) : 0;
+    }
+    // Copies step `step` into its slot, which nobody reads any more.  A page outside the pool is not followed: its
+    // rows become zeros.
+    __device__ __forceinline__ void fill(int step) {
+        const int slot = step % NST, blk = b0 + 2 * step + half;
+        const bool mine = lane < lanes && blk < b1, good = mine && id >= 0 && (long long)id < p.num_pages;
+        const uint32_t bar = bars + 8 * slot;
+        const int ps = 1 << ps_shift, r0 = (blk << 4) & (ps - 1);
+        // part of a block: K codes, V codes, K scales, V scales
+        constexpr int kCodes = kBlockKeys * D / 2, kScales = kBlockKeys * D / kv4::kGroup;
+        uint32_t to = smem + slot * kStep + half * kBlock, bytes = kBlock;
+        int from = 0;
+        if (ps_shift != 4) {
+            bytes = part < 2 ? kCodes : kScales;
+            to += part < 2 ? part * kCodes : 2 * kCodes + (part - 2) * kScales;
+            from = part < 2 ? (part * ps + r0) * (D / 2) : ps * D + ((part - 2) * ps + r0) * (D / kv4::kGroup);
         }
-        const int first = pg0 + t * pps;
-        if (first >= batch + 32) {
-            batch += 32;
-            id_cur = id_next;
-            const int nx = batch + 32 + lane;
-            id_next = nx < pg_end ? __ldg(bt_row + nx) : 0;
-        }
-        const int id = __shfl_sync(0xffffffffu, id_cur, (first + lane - batch) & 31);
-        const bool mine = lane < min(pps, pg_end - first);
-        const bool in_pool = id >= 0 && (long long)id < p.num_pages;
-        const uint32_t dst = sbase + (uint32_t)st * stage_bytes + (uint32_t)(lane * block);
-        const unsigned good = __ballot_sync(0xffffffffu, mine && in_pool);
-        if (mine && !in_pool) {
+        const unsigned all = __ballot_sync(0xffffffffu, good);
+        if (mine && !good) {
             atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
-            for (int i = 0; i < block; i += 16)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i), "r"(0) : "memory");
+            for (uint32_t i = 0; i < bytes; i += 16)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + i), "r"(0) : "memory");
             fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(bar_full + 8 * st, (uint32_t)(__popc(good) * block));
+        // a good page's lanes copy a block between them
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(ps_shift == 4 ? all : all & 0x11u) * kBlock));
         __syncwarp();
-        if (mine && in_pool)
-            bulk_load(dst, pool + ((long long)id * p.Hkv + kvh) * block, (uint32_t)block, bar_full + 8 * st);
-        issued = t + 1;
+        if (good)
+            bulk_load(to, pool + (long long)id * p.Hkv * kv4::block_bytes(ps, D) + from, bytes, bar);
+        id = look_up(step + 1);
     }
-    // every copy must have landed before the CTA may exit
-    for (int t = max(0, issued - NSTAGE); t < issued; ++t) mbar_wait(bar_full + 8 * (t % NSTAGE), (t / NSTAGE) & 1, p.err);
-}
+};
 
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
@@ -211,22 +224,26 @@ __device__ __forceinline__ void store4(T *o, float4 v) {
     *reinterpret_cast<uint2 *>(o) = w;
 }
 
-// Shared memory of the merge: rows [4 warps][R][D + 4], maxima and sums [4][R], then the CTA's own [R] each.
-__host__ __device__ constexpr size_t merge_bytes(int D, int R) { return ((size_t)4 * R * (D + 4) + 10 * R) * 4; }
+// Shared memory of the merge: rows [warps][R][D + 4], references and sums [warps][R], then the CTA's own [R] each.
+__host__ __device__ constexpr size_t merge_bytes(int D, int R, int warps) {
+    return ((size_t)warps * R * (D + 4) + (2 * warps + 2) * R) * 4;
+}
+__host__ __device__ constexpr int ring_slots(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 
 }  // namespace
 
-template <typename T, int D, int NR, int NSTAGE, int MINB>
-__global__ void __launch_bounds__(kMmaThreads, MINB) paged_attn_kv4_kernel(const Kv4Params p, int ps_shift) {
+template <typename T, int D, int NR, int NW, int MINB>
+__global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4Params p, int ps_shift) {
     using Op = MmaOp<__half>;
-    constexpr int R = 8 * NR;
-    constexpr int MT = D / 16;    // 16-wide head-dim tiles of O^T
-    constexpr int KW = D / 32;    // words of a lane's part of a K row: D / 4 elements
-    constexpr int VW = D / 64;    // words of a lane's part of a V row: D / 8 elements
-    constexpr int KS = D / 64;    // K scales of a lane's part
+    constexpr int R = 8 * NR, NST = ring_slots(D), kThreads = NW * 32;
+    constexpr int MT = D / 16;  // 16-wide head-dim tiles of O^T
+    constexpr int KW = D / 32;  // words of a lane's part of a K row: D / 4 elements
+    constexpr int VW = D / 64;  // words of a lane's part of a V row: D / 8 elements
+    constexpr int KS = D / 64;  // K scales of a lane's part
     constexpr int VS = D == 256 ? 2 : 1;
+    using RingT = Ring<D, NST>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[2 * NSTAGE];
+    __shared__ __align__(8) uint64_t bars[NW * NST];
     const FwdParams &f = p.s.f;
     RangeCheck ranges(p.s);
     BehindFirst behind(p.s);
@@ -241,12 +258,10 @@ __global__ void __launch_bounds__(kMmaThreads, MINB) paged_attn_kv4_kernel(const
     ranges.report(f);
     if (u.cnt <= 0) return;
 
-    const int ps = 1 << ps_shift;
-    const int block = kv4::block_bytes(ps, D);
     int L = max(__ldg(f.seq_lens + u.b), 0);
-    if (L > f.W * ps) {  // never read past the sequence's block-table row
+    if (L > f.W << ps_shift) {  // never read past the sequence's block-table row
         if (threadIdx.x == 0) atomicOr(f.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
-        L = f.W * ps;
+        L = f.W << ps_shift;
     }
     // unit rows r = token x heads + head; the last token reaches furthest
     const int h0 = ht * R, heads = min(R, f.G - h0);
@@ -255,112 +270,93 @@ __global__ void __launch_bounds__(kMmaThreads, MINB) paged_attn_kv4_kernel(const
     const int k_hi = row_key_limit(f, u.b, L, u.i + u.cnt - 1, u.n);
     if (k_hi <= 0) {
         if (rank == 0) {
-            for (int i = threadIdx.x; i < rows * (D / 4); i += kMmaThreads)
+            for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads)
                 store4<T>(static_cast<T *>(f.out) + row_index(i / (D / 4)) * D + i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
             if (f.lse && threadIdx.x < rows) f.lse[row_index(threadIdx.x)] = kNegInf;
         }
         return;
     }
-    // this CTA's share of the stages
-    const int stages = (k_hi + kStageKeys - 1) / kStageKeys;
-    const int share = (stages + p.S - 1) / p.S;
-    const int s0 = min(rank * share, stages);
-    const int n_tiles = min(share, stages - s0);
-    const int k_lo = s0 * kStageKeys;
+    // this warp's run of the blocks
+    const int blocks = (k_hi + kBlockKeys - 1) / kBlockKeys;
+    const int share = (blocks + p.S * NW - 1) / (p.S * NW);
+    const int b0 = min((rank * NW + warp) * share, blocks), b1 = min(b0 + share, blocks);
+    const int steps = (b1 - b0 + 1) / 2;
 
-    const uint32_t sbase = smem_u32(smem);
-    const uint32_t stage_bytes = (uint32_t)((kStageKeys >> ps_shift) * block);
-    const uint32_t bar_full = smem_u32(&bars[0]), bar_empty = smem_u32(&bars[NSTAGE]);
-    if (threadIdx.x == 0) {
-        for (int st = 0; st < NSTAGE; ++st) {
-            mbar_init(bar_full + 8 * st, 1);
-            mbar_init(bar_empty + 8 * st, kMmaConsumerWarps);
-        }
+    const uint32_t ring_smem = smem_u32(smem) + warp * NST * RingT::kStep;
+    const uint32_t ring_bars = smem_u32(&bars[warp * NST]);
+    if (lane == 0) {
+        for (int st = 0; st < NST; ++st) mbar_init(ring_bars + 8 * st, 1);
         fence_barrier_init();
     }
-    __syncthreads();
+    __syncwarp();
+    RingT ring(f, u.b, kvh, ps_shift, b0, b1, ring_smem, ring_bars, lane);
+#pragma unroll 1
+    for (int st = 0; st < min(NST, steps); ++st) ring.fill(st);
 
+    const int g = lane >> 2, tq = lane & 3;
+    const int kg = g ^ ((g >> 1) & 1);  // this lane's K rows of a block: keys kg and kg + 8
+    const int va = (2 * tq) ^ (tq & 1), vb = (2 * tq + 1) ^ (tq & 1);  // V keys va, vb, va + 8, vb + 8
+    uint32_t qb[NR][D / 8];
+    float srow[NR][2];
+    int lim[NR][2];  // keys of the rows of this lane's score columns; rows past the unit's: all
+    int all_below = b1 * kBlockKeys;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+        const int r = nr * 8 + g;
+        const bool valid = r < rows;
+        const T *q = static_cast<const T *>(f.q) + (valid ? q_row_offset(f, row_index(r)) : 0);
+        float inv;
+        load_q<T, D>(q, valid, tq, qb[nr], inv);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int rc = nr * 8 + 2 * tq + e;
+            srow[nr][e] = 8.f * f.scale_log2 * __shfl_sync(0xffffffffu, inv, 4 * (2 * tq + e));
+            lim[nr][e] = min(rc < rows ? row_key_limit(f, u.b, L, u.i + rc / heads, u.n) : INT_MAX, b1 * kBlockKeys);
+            all_below = min(all_below, lim[nr][e]);
+        }
+    }
+    all_below = __reduce_min_sync(0xffffffffu, all_below);  // keys that every row sees
+    float ref[NR][2], l[NR][2], acc[NR][MT][4];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+        ref[nr][0] = ref[nr][1] = kNoRef;
+        l[nr][0] = l[nr][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) acc[nr][mt][0] = acc[nr][mt][1] = acc[nr][mt][2] = acc[nr][mt][3] = 0.f;
+    }
+    // offsets of this lane's parts within a block
+    constexpr kv4::Layout at{kBlockKeys, D};
+    const uint32_t k_off = at.codes(0, kg) + tq * (D / 8), ks_off = at.scales(0, kg) + tq * KS;
+    const uint32_t va_off = at.codes(1, va) + g * (D / 16), vb_off = at.codes(1, vb) + g * (D / 16);
+    const uint32_t vs_col = at.scales(1, 0) + (D == 64 ? g >> 1 : g * VS);
     bool bad = false;
-    float *sm = reinterpret_cast<float *>(smem);
-    constexpr int STRIDE = D + 4;
-    float *s_m = sm + 4 * R * STRIDE, *s_l = s_m + 4 * R, *s_cta = s_l + 4 * R;  // s_cta: [R] references, [R] sums
-    if (warp == kMmaConsumerWarps) {
-        const int pg_end = (min(k_hi, k_lo + n_tiles * kStageKeys) + ps - 1) >> ps_shift;
-        produce<NSTAGE>(f, f.block_table + (long long)u.b * f.W, kvh, k_lo >> ps_shift, pg_end, n_tiles, ps_shift, block,
-                        sbase, bar_full, bar_empty, lane);
-    } else {
-        const int g = lane >> 2, tq = lane & 3;
-        const int kw0 = warp * 16;
-        const int kg = g ^ ((g >> 1) & 1);  // this lane's K rows: keys kg and kg + 8
-        const int va = (2 * tq) ^ (tq & 1), vb = (2 * tq + 1) ^ (tq & 1);  // V keys va, vb, va + 8, vb + 8
-        uint32_t qb[NR][D / 8];
-        float srow[NR][2];
-        int lim[NR][2];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            const int r = nr * 8 + g;
-            const bool valid = r < rows;
-            const T *q = static_cast<const T *>(f.q) + (valid ? q_row_offset(f, row_index(r)) : 0);
-            float inv;
-            load_q<T, D>(q, valid, tq, qb[nr], inv);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int rc = nr * 8 + 2 * tq + e;
-                srow[nr][e] = 8.f * f.scale_log2 * __shfl_sync(0xffffffffu, inv, 4 * (2 * tq + e));
-                lim[nr][e] = rc < rows ? row_key_limit(f, u.b, L, u.i + rc / heads, u.n) : 0;
+
+    int t = 0;
+#pragma unroll 1
+    for (; t < steps; ++t) {
+        const int slot = t % NST;
+        const uint32_t base = ring_smem + slot * RingT::kStep;
+        const int j0 = (b0 + 2 * t) * kBlockKeys;
+        {
+            const bool ok = mbar_wait(ring_bars + 8 * slot, (t / NST) & 1, f.err);
+            if (__any_sync(0xffffffffu, !ok)) {
+                bad = true;
+                break;
             }
         }
-        float ref[NR][2], l[NR][2], acc[NR][MT][4];
+        // ---- S^T = K Q^T
+        float sc[2][NR][4];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            ref[nr][0] = ref[nr][1] = kNegInf;
-            l[nr][0] = l[nr][1] = 0.f;
+        for (int hb = 0; hb < 2; ++hb) {
+            const uint32_t blk = base + hb * RingT::kBlock;
+            uint32_t kw[2][KW], ksb[2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) acc[nr][mt][0] = acc[nr][mt][1] = acc[nr][mt][2] = acc[nr][mt][3] = 0.f;
-        }
-        // offsets of this lane's parts within a stage
-        const uint32_t blk = (uint32_t)((kw0 >> ps_shift) * block);
-        const int r0 = kw0 & (ps - 1);
-        const kv4::Layout at{ps, D};
-        const uint32_t k_off = blk + at.codes(0, r0 + kg) + tq * (D / 8);
-        const uint32_t ks_off = blk + at.scales(0, r0 + kg) + tq * KS;
-        const uint32_t v_off = blk + at.codes(1, r0) + g * (D / 16);
-        const uint32_t vs_off = blk + at.scales(1, r0) + (D == 64 ? g >> 1 : g * VS);
-
-        for (int t = 0; t < n_tiles; ++t) {
-            const int st = t % NSTAGE;
-            const uint32_t base = sbase + (uint32_t)st * stage_bytes;
-            const int j0 = k_lo + t * kStageKeys + kw0 + kg;  // the position of this lane's first K row
-            const bool active = k_lo + t * kStageKeys + kw0 < k_hi;  // warp-uniform
-            {
-                const bool ok = mbar_wait(bar_full + 8 * st, (t / NSTAGE) & 1, f.err);
-                if (__any_sync(0xffffffffu, !ok)) {
-                    bad = true;
-                    break;
-                }
+            for (int i = 0; i < 2; ++i) {
+                lds_words<KW>(blk + k_off + i * 8 * (D / 2), kw[i]);
+                ksb[i] = lds_bytes<KS>(blk + ks_off + i * 8 * (D / 16));
             }
-            uint32_t kw[2][KW], vw[4][VW], ksb[2], vsb[4];
-            if (active) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    lds_words<KW>(base + k_off + i * 8 * (D / 2), kw[i]);
-                    ksb[i] = lds_bytes<KS>(base + ks_off + i * 8 * (D / 16));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
-                    lds_words<VW>(base + v_off + key * (D / 2), vw[i]);
-                    vsb[i] = lds_bytes<VS>(base + vs_off + key * (D / 16));
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_empty + 8 * st);  // the stage is in registers
-            if (!active) continue;
-
-            // ---- S^T = K Q^T
-            float sc[NR][4];
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) sc[nr][0] = sc[nr][1] = sc[nr][2] = sc[nr][3] = 0.f;
+            for (int nr = 0; nr < NR; ++nr) sc[hb][nr][0] = sc[hb][nr][1] = sc[hb][nr][2] = sc[hb][nr][3] = 0.f;
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 uint32_t h[2][4];
@@ -375,66 +371,99 @@ __global__ void __launch_bounds__(kMmaThreads, MINB) paged_attn_kv4_kernel(const
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t a[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) Op::run(sc[nr], a, qb[nr][4 * w + 2 * k], qb[nr][4 * w + 2 * k + 1]);
+                    for (int nr = 0; nr < NR; ++nr)
+                        Op::run(sc[hb][nr], a, qb[nr][4 * w + 2 * k], qb[nr][4 * w + 2 * k + 1]);
                 }
             }
-            // ---- weights; a score more than kRefMost above its reference moves it
-            uint32_t pb[NR][2][2];  // [row tile][high part / remainder][keys 0-7 / 8-15]
-            bool over = false;
+        }
+        // ---- weights; a score more than kRefMost above its reference moves it
+        float mx[NR][2];
+        bool over = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int kh = 0; kh < 2; ++kh) sc[hb][nr][2 * kh + e] *= srow[nr][e];
+            }
+        if (j0 + kStepKeys > all_below) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sc[nr][e] = j0 < lim[nr][e] ? sc[nr][e] * srow[nr][e] : kNegInf;
-                    sc[nr][2 + e] = j0 + 8 < lim[nr][e] ? sc[nr][2 + e] * srow[nr][e] : kNegInf;
-                    over |= fmaxf(sc[nr][e], sc[nr][2 + e]) > ref[nr][e] + kRefMost;
-                }
-            if (__any_sync(0xffffffffu, over)) {
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    float al[2];
+                    for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(sc[nr][e], sc[nr][2 + e]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float next = fmaxf(ref[nr][e], mx - kRefBelow);
-                        al[e] = next == kNegInf ? 1.f : fast_exp2(ref[nr][e] - next);  // a row without a key so far
-                        ref[nr][e] = next;
-                        l[nr][e] *= al[e];
-                    }
+                        for (int kh = 0; kh < 2; ++kh)
+                            if (j0 + hb * kBlockKeys + kg + 8 * kh >= lim[nr][e]) sc[hb][nr][2 * kh + e] = kNegInf;
+        }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[nr][mt][i] *= al[i & 1];
-                }
+            for (int e = 0; e < 2; ++e) {
+                mx[nr][e] = fmaxf(fmaxf(sc[0][nr][e], sc[0][nr][2 + e]), fmaxf(sc[1][nr][e], sc[1][nr][2 + e]));
+                over |= mx[nr][e] > ref[nr][e] + kRefMost;
             }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                float al[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float m = mx[nr][e];
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    const float next = fmaxf(ref[nr][e], m - kRefBelow);
+                    al[e] = fast_exp2(ref[nr][e] - next);
+                    ref[nr][e] = next;
+                    l[nr][e] *= al[e];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[nr][mt][i] *= al[i & 1];
+            }
+        }
+        uint32_t pb[2][NR][2][2];  // [block][row tile][high part / remainder][keys 0-7 / 8-15]
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
                 float w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float r = ref[nr][i & 1];
-                    w[i] = fast_exp2(sc[nr][i] - (r == kNegInf ? 0.f : r));
-                }
+                for (int i = 0; i < 4; ++i) w[i] = fast_exp2(sc[hb][nr][i] - ref[nr][i & 1]);
                 l[nr][0] += w[0] + w[2];
                 l[nr][1] += w[1] + w[3];
 #pragma unroll
                 for (int kh = 0; kh < 2; ++kh) {
                     const uint32_t hi = Op::pack(w[2 * kh], w[2 * kh + 1]);
                     const float2 x = Op::unpack(hi);
-                    pb[nr][0][kh] = movmatrix_trans(hi);
-                    pb[nr][1][kh] = movmatrix_trans(Op::pack(w[2 * kh] - x.x, w[2 * kh + 1] - x.y));
+                    pb[hb][nr][0][kh] = movmatrix_trans(hi);
+                    pb[hb][nr][1][kh] = movmatrix_trans(Op::pack(w[2 * kh] - x.x, w[2 * kh + 1] - x.y));
                 }
             }
-            // ---- O^T += V^T P^T
-            uint32_t vs[2][VS], vc[2][VS];  // of the keys (va, vb) and (va + 8, vb + 8)
+        // ---- O^T += V^T P^T
 #pragma unroll
-            for (int kh = 0; kh < 2; ++kh)
+        for (int hb = 0; hb < 2; ++hb) {
+            const uint32_t blk = base + hb * RingT::kBlock;
+            uint32_t vw[4][VW], vs[2][VS], vc[2][VS];  // of the keys (va, vb) and (va + 8, vb + 8)
+#pragma unroll
+            for (int kh = 0; kh < 2; ++kh) {
+                lds_words<VW>(blk + va_off + kh * 8 * (D / 2), vw[2 * kh]);
+                lds_words<VW>(blk + vb_off + kh * 8 * (D / 2), vw[2 * kh + 1]);
+                const uint32_t a = lds_bytes<VS>(blk + vs_col + (va + 8 * kh) * (D / 16));
+                const uint32_t b = lds_bytes<VS>(blk + vs_col + (vb + 8 * kh) * (D / 16));
 #pragma unroll
                 for (int i = 0; i < VS; ++i)
-                    kv4::scale_pair(__byte_perm(vsb[2 * kh], vsb[2 * kh + 1], 0x3430 + i * 0x0101), vs[kh][i], vc[kh][i]);
+                    kv4::scale_pair(__byte_perm(a, b, 0x3430 + i * 0x0101), vs[kh][i], vc[kh][i]);
+            }
+            if (hb == 1) {  // the step is in registers
+                __syncwarp();
+                if (t + NST < steps) ring.fill(t + NST);
+            }
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
@@ -450,99 +479,100 @@ __global__ void __launch_bounds__(kMmaThreads, MINB) paged_attn_kv4_kernel(const
                         const uint32_t a[4] = {h[0][2 * k], h[0][2 * k + 1], h[1][2 * k], h[1][2 * k + 1]};
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr) {
-                            Op::run(acc[nr][mt], a, pb[nr][0][0], pb[nr][0][1]);
-                            Op::run(acc[nr][mt], a, pb[nr][1][0], pb[nr][1][1]);
+                            Op::run(acc[nr][mt], a, pb[hb][nr][0][0], pb[hb][nr][0][1]);
+                            Op::run(acc[nr][mt], a, pb[hb][nr][1][0], pb[hb][nr][1][1]);
                         }
                     }
                 }
         }
+    }
+    if (bad)  // every copy must have landed before the ring is written over
+        for (const int filled = min(steps, t + NST); t < filled; ++t) mbar_wait(ring_bars + 8 * (t % NST), (t / NST) & 1, f.err);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 4);
+            l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
+            l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
+        }
+    // ---- the warps' states: tile mt's rows g and g + 8 are elements g D / 8 + 2 mt and the next
+    float *sm = reinterpret_cast<float *>(smem);
+    constexpr int STRIDE = D + 4;
+    float *s_m = sm + NW * R * STRIDE, *s_l = s_m + NW * R, *s_cta = s_l + NW * R;  // s_cta: [R] references, [R] sums
+    __syncthreads();  // no warp reads its ring any more
+    float *wa = sm + warp * R * STRIDE;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float2 *>(wa + (nr * 8 + 2 * tq + e) * STRIDE + g * (D / 8) + 2 * mt) =
+                    make_float2(acc[nr][mt][e], acc[nr][mt][2 + e]);
+        if (g == 0) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 4);
-                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
-                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
-            }
-        // ---- the warps' states: tile mt's rows g and g + 8 are elements g D / 8 + 2 mt and the next
-        named_bar_sync(1, kMmaConsumerWarps * 32);  // no warp reads the ring any more
-        float *wa = sm + warp * R * STRIDE;
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<float2 *>(wa + (nr * 8 + 2 * tq + e) * STRIDE + g * (D / 8) + 2 * mt) =
-                        make_float2(acc[nr][mt][e], acc[nr][mt][2 + e]);
-            if (g == 0) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    s_m[warp * R + nr * 8 + 2 * tq + e] = ref[nr][e];
-                    s_l[warp * R + nr * 8 + 2 * tq + e] = bad ? __uint_as_float(0x7fc00000u) : l[nr][e];
-                }
+                s_m[warp * R + nr * 8 + 2 * tq + e] = ref[nr][e];
+                s_l[warp * R + nr * 8 + 2 * tq + e] = bad ? __uint_as_float(0x7fc00000u) : l[nr][e];
             }
         }
-        named_bar_sync(1, kMmaConsumerWarps * 32);
-        for (int i = threadIdx.x; i < rows * (D / 4); i += kMmaConsumerWarps * 32) {
-            const int r = i / (D / 4), c = i % (D / 4) * 4;
-            float M = kNegInf;
+    }
+    __syncthreads();
+    auto store = [&](int r, int c, float4 o, float M, float sum) {
+        const float inv = sum != 0.f ? 8.f / sum : 0.f;  // a NaN stays one
+        const long long ri = row_index(r);
+        store4<T>(static_cast<T *>(f.out) + ri * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (c == 0 && f.lse) f.lse[ri] = sum != 0.f ? M * kLn2 + logf(sum) : kNegInf;
+    };
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        float M = kNoRef, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w * R + r]);
-            float sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * R + r]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float k = M == kNegInf ? 0.f : exp2f(s_m[w * R + r] - M);
-                const float4 v = *reinterpret_cast<const float4 *>(sm + (w * R + r) * STRIDE + c);
-                sum += k * s_l[w * R + r];
-                o.x += k * v.x, o.y += k * v.y, o.z += k * v.z, o.w += k * v.w;
-            }
-            if (p.S == 1) {
-                const float inv = sum != 0.f ? 8.f / sum : 0.f;  // a NaN stays one
-                const long long ri = row_index(r);
-                store4<T>(static_cast<T *>(f.out) + ri * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-                if (c == 0 && f.lse) f.lse[ri] = sum != 0.f ? M * kLn2 + logf(sum) : kNegInf;
-            } else {  // the row's slot of warp 0 is this thread's alone
-                *reinterpret_cast<float4 *>(sm + r * STRIDE + c) = o;
-                if (c == 0) {
-                    s_cta[r] = M;
-                    s_cta[R + r] = sum;
-                }
+        for (int w = 0; w < NW; ++w) {
+            const float k = fast_exp2(s_m[w * R + r] - M);
+            const float4 v = *reinterpret_cast<const float4 *>(sm + (w * R + r) * STRIDE + c);
+            sum += k * s_l[w * R + r];
+            o.x += k * v.x, o.y += k * v.y, o.z += k * v.z, o.w += k * v.w;
+        }
+        if (p.S == 1) {
+            store(r, c, o, M, sum);
+        } else {  // the row's slot of warp 0 is this thread's alone
+            *reinterpret_cast<float4 *>(sm + r * STRIDE + c) = o;
+            if (c == 0) {
+                s_cta[r] = M;
+                s_cta[R + r] = sum;
             }
         }
     }
     if (p.S == 1) return;
     // ---- the CTAs' states: each stores its share of the rows' elements
     cluster_barrier();
-    for (int i = rank * kMmaThreads + threadIdx.x; i < rows * (D / 4); i += p.S * kMmaThreads) {
+    for (int i = rank * kThreads + threadIdx.x; i < rows * (D / 4); i += p.S * kThreads) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
         const uint32_t at_m = smem_u32(s_cta + r), at_l = smem_u32(s_cta + R + r), at_o = smem_u32(sm + r * STRIDE + c);
-        float M = kNegInf;
+        float M = kNoRef, sum = 0.f;
         for (int x = 0; x < p.S; ++x) M = fmaxf(M, peer_load(peer_addr(at_m, x)));
-        float sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int x = 0; x < p.S; ++x) {
-            const float k = M == kNegInf ? 0.f : exp2f(peer_load(peer_addr(at_m, x)) - M);
+            const float k = fast_exp2(peer_load(peer_addr(at_m, x)) - M);
             const float4 v = peer_load4(peer_addr(at_o, x));
             sum += k * peer_load(peer_addr(at_l, x));
             o.x += k * v.x, o.y += k * v.y, o.z += k * v.z, o.w += k * v.w;
         }
-        const float inv = sum != 0.f ? 8.f / sum : 0.f;  // a NaN stays one
-        const long long ri = row_index(r);
-        store4<T>(static_cast<T *>(f.out) + ri * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (c == 0 && f.lse) f.lse[ri] = sum != 0.f ? M * kLn2 + logf(sum) : kNegInf;
+        store(r, c, o, M, sum);
     }
     cluster_barrier();  // the peers have read this CTA's memory
 }
 
-template <typename T, int D, int NR>
+template <typename T, int D, int NR, int NW, int MINB>
 static cudaError_t launch_kv4(Kv4Params p, int sms, cudaStream_t stream) {
     constexpr int R = 8 * NR;
-    constexpr int NSTAGE = D == 64 ? 8 : 4;
-    constexpr int MINB = D == 256 ? 1 : NR == 1 ? 3 : 2;
-    constexpr size_t ring = (size_t)NSTAGE * kStageKeys * D / 8 * 9;
-    constexpr size_t smem = ring > merge_bytes(D, R) ? ring : merge_bytes(D, R);
+    constexpr size_t ring = (size_t)NW * ring_slots(D) * Ring<D, 1>::kStep;
+    constexpr size_t smem = ring > merge_bytes(D, R, NW) ? ring : merge_bytes(D, R, NW);
     const FwdParams &f = p.s.f;
     p.HT = (f.G + R - 1) / R;
     p.TT = f.q_start && p.s.n_tok <= f.B ? 1 : f.G < R ? R / f.G : 1;
@@ -559,17 +589,18 @@ static cudaError_t launch_kv4(Kv4Params p, int sms, cudaStream_t stream) {
     }
     const long long units = tiles * f.Hkv * p.HT;
     int S = 1;
-    while (S < 8 && units * S * 2 <= (long long)sms * MINB && (long long)f.W * f.ps >= 256ll * S) S *= 2;
+    while (S < kMaxCluster && units * S <= (long long)sms * MINB && (long long)f.W * f.ps >= 2ll * kStepKeys * NW * S) S *= 2;
     p.S = S;
     if (units == 0) return cudaSuccess;
     if (units * S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    auto kern = paged_attn_kv4_kernel<T, D, NR, NSTAGE, MINB>;
-    static SmemLimit limit;
-    const cudaError_t e = limit.raise((const void *)kern, smem);
+    auto kern = paged_attn_kv4_kernel<T, D, NR, NW, MINB>;
+    static SmemLimit limit, wide;
+    cudaError_t e = limit.raise((const void *)kern, smem);
+    if (e == cudaSuccess && S > 8) e = wide.allow_wide_clusters((const void *)kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * S));
-    cfg.blockDim = dim3(kMmaThreads);
+    cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -585,10 +616,12 @@ static cudaError_t launch_kv4_d(const Kv4Params &p, int sms, cudaStream_t stream
     const FwdParams &f = p.s.f;
     // rows of an average sequence (a uniform batch: of every one)
     const double rows = (f.q_start ? (double)p.s.n_tok / f.B : (double)f.Sq) * f.G;
-    if constexpr (D != 256) {
-        if (rows > 8 && !(f.G > 16 && f.G <= 24)) return launch_kv4<T, D, 2>(p, sms, stream);
+    if constexpr (D == 256) {
+        return launch_kv4<T, D, 1, 4, 2>(p, sms, stream);
+    } else {
+        if (rows > 8 && !(f.G > 16 && f.G <= 24)) return launch_kv4<T, D, 2, 4, 3>(p, sms, stream);
+        return launch_kv4<T, D, 1, 8, 2>(p, sms, stream);
     }
-    return launch_kv4<T, D, 1>(p, sms, stream);
 }
 
 template <typename T>

@@ -22,8 +22,8 @@ __host__ __device__ constexpr int block_bytes(int ps, int D) { return ps * D / 8
 // Where a row's parts stand in a block.
 struct Layout {
     int ps, D;
-    __device__ __forceinline__ int codes(int side, int row) const { return (side * ps + row) * (D / 2); }
-    __device__ __forceinline__ int scales(int side, int row) const { return ps * D + (side * ps + row) * (D / kGroup); }
+    __host__ __device__ constexpr int codes(int side, int row) const { return (side * ps + row) * (D / 2); }
+    __host__ __device__ constexpr int scales(int side, int row) const { return ps * D + (side * ps + row) * (D / kGroup); }
 };
 
 __device__ __forceinline__ float scale_value(uint32_t byte) {
