@@ -498,9 +498,10 @@ int paged_attn_gather_kv4(const void *kv, const int32_t *slots, void *k_out, voi
  * q_start [batch + 1], laid out, masked and skipped as for the calls over selected pages (rows at or past
  * q_start[batch] are not written).  q and out are PA_BF16 or PA_F16 (PA_F32: PA_EDTYPE); out is rounded once,
  * lse [tokens, Hq] float32 or NULL; a row without a key gets 0 and -inf.  bf16 queries enter the products as f16
- * numbers, each row moved by a power of two, which is exact but for elements below 2^-28 of the row's largest; weights
- * meet V as f16 pairs, within 2^-22 of the weight or 2^-31 of the row's largest.  A page id outside
- * [0, num_pages) reads as zeros and sets PA_ERRBIT_PAGE_RANGE.
+ * numbers, each row moved by a power of two, which is exact but for elements below 2^-28 of the row's largest.  A
+ * weight meets V as one f16 number for bf16 (within 2^-11 of it, an eighth of the output's own rounding) and as two for
+ * f16 (2^-22), or within 2^-35 of the row's largest.  A page id outside [0, num_pages) reads as zeros and sets
+ * PA_ERRBIT_PAGE_RANGE.
  */
 int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table, const int32_t *seq_lens,
                        const int32_t *q_start, int causal, const int32_t *q_offset, float scale, void *out, float *lse,

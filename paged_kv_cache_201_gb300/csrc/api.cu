@@ -938,6 +938,7 @@ int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table
     if (rc != PA_OK) return rc;
     if (dims->dtype == PA_F32) return PA_EDTYPE;
     if (!isfinite(scale)) return PA_EINVAL;
+    if ((int64_t)dims->num_kv_heads * dims->page_size * dims->head_dim / 8 * 9 >= (int64_t)1 << 31) return PA_EUNSUPPORTED;
     const int64_t n_tok = dims->batch == 0 ? 0 : q_start ? (int64_t)dims->q_len : (int64_t)dims->batch * dims->q_len;
     if (n_tok == 0) return PA_OK;
     rc = check_fwd_pointers(q, kv, kv, block_table, seq_lens, q_offset, 1, out, lse);

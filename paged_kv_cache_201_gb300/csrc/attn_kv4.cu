@@ -6,8 +6,8 @@
 // another warp until the states are merged.  Products are transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and
 // head dimension fill the MMA's 16-row side and a group of up to eight heads its 8-wide side.
 //
-//   * A step is two blocks.  The block of a (page, kv head), codes and scales of K and V, is contiguous: a page of 16 rows
-//     is one untiled bulk copy, 16 rows of a larger one are four.
+//   * A step is two blocks.  The block of a (page, kv head), codes and scales of K and V, is contiguous; 16 rows of a larger
+//     page land as a page of 16 rows does.
 //   * Codes become f16 operands in registers, (u - 8) x scale / 8, without rounding (kv4.cuh): a shift, a logic
 //     operation and a fused multiply-add for two elements.  The eighth comes back in the score's factor and in
 //     the final division.
@@ -16,7 +16,7 @@
 //     words pairs their halves before the codes are taken apart, so V needs no transposition.
 //   * Softmax statistics are float32.  A weight is 2^(score - ref), ref at least 11 below the largest score so far
 //     when it was last moved and never more than 15 below any: weights stay below 2^15, ref (and with it every sum)
-//     moves rarely, and as an f16 high part and remainder a weight is held to 2^-22, or 2^-31 of the row's largest.
+//     moves rarely, and in f16 nothing above 2^-36 of the row's largest weight is lost.
 //   * The rows of S^T are keys r ^ (r >> 1 & 1): with the four keys of a V load in different rows modulo
 //     two, their shared-memory loads have half the bank conflicts, and K's none.
 //
@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kBlockKeys = 16, kStepKeys = 32, kMaxCluster = 16;
 constexpr float kRefBelow = 11.f, kRefMost = 15.f;
+constexpr float kLeastFactor = 0x1p-100f;  // a scale of 0 leaves this: kNegInf times it is still no NaN, and any sum times it 0
 constexpr float kNoRef = -3e38f;  // before the first key; finite, so that kNegInf - ref is no NaN
 
 struct Kv4Params {
@@ -97,69 +98,86 @@ __device__ __forceinline__ Tile find_tile(const Kv4Params &p, int tile, int lane
     return u;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-                 : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
 
-// A warp's ring: blocks [b0, b1) of 16 keys, two a step, into NST slots of its own.
-template <int D, int NST>
+// A warp's ring: blocks [b0, b1) of 16 keys (b0 even), two a step, into NST slots of its own, filled in order.  The copies
+// are 16 bytes a lane and the warp waits for its own by count: a bulk copy's barrier, its byte count and its uniform
+// operands cost 44 instructions a block.  PAGE16: pages of 16 rows, whose blocks are contiguous; a step's rows of a larger
+// page land as two of those.
+template <int D, int NST, bool PAGE16>
 struct Ring {
     static constexpr int kBlock = kBlockKeys * D / 8 * 9;  // bytes of a block: as a page of 16 rows
     static constexpr int kStep = 2 * kBlock;
+    static constexpr int kCodes = kBlockKeys * D / 2, kScales = kBlockKeys * D / kv4::kGroup;
+    static constexpr int kPages = PAGE16 ? 2 : 1;  // of a step
     const FwdParams &p;
-    const int32_t *bt_row;
-    const uint8_t *pool;  // of this kv head
-    uint32_t smem, bars;
-    int b0, b1, ps_shift, lane;
-    int part, half, lanes;  // which copy of a step this lane issues
-    int id;                 // its page, of the next step to come
+    const int32_t *table;        // this sequence's row
+    const uint8_t *from;         // page 0's block of this kv head, at this lane's codes
+    uint32_t stride;             // bytes from page to page
+    uint32_t smem, slot_at;      // this lane's codes in slot 0 and in the next one to fill
+    int v_codes, scales;         // larger pages: from there to the V codes, to this lane's scales
+    int blk, b1, ps_shift, lane;
+    int id[kPages];              // pages of the next step to fill
 
-    __device__ __forceinline__ Ring(const FwdParams &f, int b, int kvh, int ps_shift_, int block0, int block1, uint32_t smem_,
-                                    uint32_t bars_, int lane_)
-        : p(f), bt_row(f.block_table + (long long)b * f.W),
-          pool(static_cast<const uint8_t *>(f.k_cache) + (long long)kvh * kv4::block_bytes(1 << ps_shift_, D)), smem(smem_),
-          bars(bars_), b0(block0), b1(block1), ps_shift(ps_shift_), lane(lane_) {
-        lanes = ps_shift == 4 ? 2 : 8;
-        half = ps_shift == 4 ? lane : lane >> 2;
-        part = ps_shift == 4 ? 0 : lane & 3;
-        id = look_up(0);
+    __device__ __forceinline__ Ring(const FwdParams &f, int b, int kvh, int shift, int block0, int block1, uint32_t smem_,
+                                    int lane_)
+        : p(f), table(f.block_table + (long long)b * f.W), blk(block0), b1(block1), ps_shift(shift), lane(lane_) {
+        const int ps = 1 << shift, size = kv4::block_bytes(ps, D);
+        stride = (uint32_t)f.Hkv * (uint32_t)size;
+        from = static_cast<const uint8_t *>(f.k_cache) + (long long)kvh * size + lane * 16;
+        smem = slot_at = smem_ + lane * 16;
+        v_codes = ps * (D / 2);
+        constexpr int kLanes = kScales / 16;  // of a side's scales
+        scales = ps * D + (lane < kLanes ? 0 : (ps - kBlockKeys) * (D / kv4::kGroup));
+        look_up();
     }
-    __device__ __forceinline__ int look_up(int step) const {
-        const int blk = b0 + 2 * step + half;
-        return lane < lanes && blk < b1 ? __ldg(bt_row + (blk >> (ps_shift - 4))) : 0;
+    __device__ __forceinline__ void look_up() {
+        if (PAGE16) {
+#pragma unroll
+            for (int hb = 0; hb < kPages; ++hb) id[hb] = blk + hb < b1 ? __ldg(table + blk + hb) : 0;
+        } else {
+            id[0] = blk < b1 ? __ldg(table + (blk >> (ps_shift - 4))) : 0;
+        }
     }
-    // Copies step `step` into its slot, which nobody reads any more.  A page outside the pool is not followed: its
-    // rows become zeros.
-    __device__ __forceinline__ void fill(int step) {
-        const int slot = step % NST, blk = b0 + 2 * step + half;
-        const bool mine = lane < lanes && blk < b1, good = mine && id >= 0 && (long long)id < p.num_pages;
-        const uint32_t bar = bars + 8 * slot;
-        const int ps = 1 << ps_shift, r0 = (blk << 4) & (ps - 1);
-        // part of a block: K codes, V codes, K scales, V scales
-        constexpr int kCodes = kBlockKeys * D / 2, kScales = kBlockKeys * D / kv4::kGroup;
-        uint32_t to = smem + slot * kStep + half * kBlock, bytes = kBlock;
-        int from = 0;
-        if (ps_shift != 4) {
-            bytes = part < 2 ? kCodes : kScales;
-            to += part < 2 ? part * kCodes : 2 * kCodes + (part - 2) * kScales;
-            from = part < 2 ? (part * ps + r0) * (D / 2) : ps * D + ((part - 2) * ps + r0) * (D / kv4::kGroup);
+    // A page outside the pool is not followed: its rows become zeros.
+    __device__ __forceinline__ void no_page(uint32_t to) {
+        if (lane == 0) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
+        for (int i = lane * 16; i < kBlock; i += 512)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to - lane * 16 + i), "r"(0) : "memory");
+    }
+    // Starts the copies of the next step into its slot, which nobody reads any more.
+    __device__ __forceinline__ void fill() {
+        const bool my_scales = lane < 2 * kScales / 16;
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+            const uint32_t to = slot_at + hb * kBlock;
+            if (hb == 1 && blk + 1 >= b1) break;
+            const int at = id[PAGE16 ? hb : 0];
+            if ((uint32_t)at >= (uint32_t)p.num_pages) {
+                no_page(to);
+                continue;
+            }
+            const uint8_t *page = from + (unsigned long long)(uint32_t)at * stride;
+            if (PAGE16) {
+#pragma unroll
+                for (int i = 0; i < 2 * kCodes; i += 512) copy16(to + i, page + i);
+                if (my_scales) copy16(to + 2 * kCodes, page + 2 * kCodes);
+            } else {
+                const int row = (blk << 4) & ((1 << ps_shift) - 1);
+                const uint8_t *k = page + row * (D / 2) + hb * kCodes, *v = k + v_codes;
+#pragma unroll
+                for (int i = 0; i < kCodes; i += 512) {
+                    copy16(to + i, k + i);
+                    copy16(to + kCodes + i, v + i);
+                }
+                if (my_scales) copy16(to + 2 * kCodes, page + scales + row * (D / kv4::kGroup) + hb * kScales);
+            }
         }
-        const unsigned all = __ballot_sync(0xffffffffu, good);
-        if (mine && !good) {
-            atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
-            for (uint32_t i = 0; i < bytes; i += 16)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + i), "r"(0) : "memory");
-            fence_proxy_async_smem();
-        }
-        __syncwarp();
-        // a good page's lanes copy a block between them
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(ps_shift == 4 ? all : all & 0x11u) * kBlock));
-        __syncwarp();
-        if (good)
-            bulk_load(to, pool + (long long)id * p.Hkv * kv4::block_bytes(ps, D) + from, bytes, bar);
-        id = look_up(step + 1);
+        blk += 2;
+        look_up();
+        slot_at = slot_at == smem + (NST - 1) * kStep ? smem : slot_at + kStep;
     }
 };
 
@@ -192,9 +210,9 @@ __device__ __forceinline__ uint32_t lds_bytes(uint32_t addr) {
 }
 
 // A query row's D / 4 elements of this lane as f16 operand pairs, pair 4 w + k = elements 8 w + k and 8 w + k + 4.
-// bf16 rows are multiplied by a power of two that brings them into f16; inv is its inverse.
+// bf16 rows are multiplied by a power of two that brings them into f16; inv is its inverse.  negate: as -q.
 template <typename T, int D>
-__device__ __forceinline__ void load_q(const T *row, bool valid, int tq, uint32_t (&w)[D / 8], float &inv) {
+__device__ __forceinline__ void load_q(const T *row, bool valid, bool negate, int tq, uint32_t (&w)[D / 8], float &inv) {
     const uint4 *src = reinterpret_cast<const uint4 *>(row + tq * (D / 4));
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -204,6 +222,9 @@ __device__ __forceinline__ void load_q(const T *row, bool valid, int tq, uint32_
         w[4 * i + 2] = __byte_perm(x.y, x.w, 0x5410);
         w[4 * i + 3] = __byte_perm(x.y, x.w, 0x7632);
     }
+    if (negate)
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] ^= 0x80008000u;
     inv = 1.f;
     if (std::is_same<T, __nv_bfloat16>::value) {
         float am = 0.f;
@@ -232,7 +253,7 @@ __host__ __device__ constexpr int ring_slots(int D) { return D == 64 ? 4 : D == 
 
 }  // namespace
 
-template <typename T, int D, int NR, int NW, int MINB>
+template <typename T, int D, int NR, int NW, int MINB, bool PAGE16>
 __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4Params p, int ps_shift) {
     using Op = MmaOp<__half>;
     constexpr int R = 8 * NR, NST = ring_slots(D), kThreads = NW * 32;
@@ -241,9 +262,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     constexpr int VW = D / 64;  // words of a lane's part of a V row: D / 8 elements
     constexpr int KS = D / 64;  // K scales of a lane's part
     constexpr int VS = D == 256 ? 2 : 1;
-    using RingT = Ring<D, NST>;
+    using RingT = Ring<D, NST, PAGE16>;
+    // Weights of an f16 output as a high part and a remainder, of a bf16 one as the high part alone: its 2^-12 is an
+    // eighth of the output's own rounding (256 sequences 228 -> 205 us).
+    constexpr int kParts = std::is_same<T, __half>::value ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[NW * NST];
     const FwdParams &f = p.s.f;
     RangeCheck ranges(p.s);
     BehindFirst behind(p.s);
@@ -278,20 +301,17 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     }
     // this warp's run of the blocks
     const int blocks = (k_hi + kBlockKeys - 1) / kBlockKeys;
-    const int share = (blocks + p.S * NW - 1) / (p.S * NW);
+    const int share = 2 * ((blocks + 2 * p.S * NW - 1) / (2 * p.S * NW));
     const int b0 = min((rank * NW + warp) * share, blocks), b1 = min(b0 + share, blocks);
     const int steps = (b1 - b0 + 1) / 2;
 
     const uint32_t ring_smem = smem_u32(smem) + warp * NST * RingT::kStep;
-    const uint32_t ring_bars = smem_u32(&bars[warp * NST]);
-    if (lane == 0) {
-        for (int st = 0; st < NST; ++st) mbar_init(ring_bars + 8 * st, 1);
-        fence_barrier_init();
-    }
-    __syncwarp();
-    RingT ring(f, u.b, kvh, ps_shift, b0, b1, ring_smem, ring_bars, lane);
+    RingT ring(f, u.b, kvh, ps_shift, b0, b1, ring_smem, lane);
 #pragma unroll 1
-    for (int st = 0; st < min(NST, steps); ++st) ring.fill(st);
+    for (int st = 0; st < NST; ++st) {
+        if (st < steps) ring.fill();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
 
     const int g = lane >> 2, tq = lane & 3;
     const int kg = g ^ ((g >> 1) & 1);  // this lane's K rows of a block: keys kg and kg + 8
@@ -306,11 +326,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         const bool valid = r < rows;
         const T *q = static_cast<const T *>(f.q) + (valid ? q_row_offset(f, row_index(r)) : 0);
         float inv;
-        load_q<T, D>(q, valid, tq, qb[nr], inv);
+        load_q<T, D>(q, valid, f.scale_log2 < 0.f, tq, qb[nr], inv);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int rc = nr * 8 + 2 * tq + e;
-            srow[nr][e] = 8.f * f.scale_log2 * __shfl_sync(0xffffffffu, inv, 4 * (2 * tq + e));
+            srow[nr][e] = fmaxf(8.f * fabsf(f.scale_log2) * __shfl_sync(0xffffffffu, inv, 4 * (2 * tq + e)), kLeastFactor);
             lim[nr][e] = min(rc < rows ? row_key_limit(f, u.b, L, u.i + rc / heads, u.n) : INT_MAX, b1 * kBlockKeys);
             all_below = min(all_below, lim[nr][e]);
         }
@@ -329,43 +349,37 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     const uint32_t k_off = at.codes(0, kg) + tq * (D / 8), ks_off = at.scales(0, kg) + tq * KS;
     const uint32_t va_off = at.codes(1, va) + g * (D / 16), vb_off = at.codes(1, vb) + g * (D / 16);
     const uint32_t vs_col = at.scales(1, 0) + (D == 64 ? g >> 1 : g * VS);
-    bool bad = false;
-
-    int t = 0;
+    int slot = 0;
 #pragma unroll 1
-    for (; t < steps; ++t) {
-        const int slot = t % NST;
+    for (int t = 0; t < steps; ++t) {
         const uint32_t base = ring_smem + slot * RingT::kStep;
         const int j0 = (b0 + 2 * t) * kBlockKeys;
-        {
-            const bool ok = mbar_wait(ring_bars + 8 * slot, (t / NST) & 1, f.err);
-            if (__any_sync(0xffffffffu, !ok)) {
-                bad = true;
-                break;
-            }
-        }
-        // ---- S^T = K Q^T
+        asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");  // a step is a group
+        __syncwarp();
+        // ---- S^T = K Q^T, the two blocks' products in turn
         float sc[2][NR][4];
+        uint32_t kw[2][2][KW], ksb[2][2];
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
-            const uint32_t blk = base + hb * RingT::kBlock;
-            uint32_t kw[2][KW], ksb[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                lds_words<KW>(blk + k_off + i * 8 * (D / 2), kw[i]);
-                ksb[i] = lds_bytes<KS>(blk + ks_off + i * 8 * (D / 16));
+                lds_words<KW>(base + hb * RingT::kBlock + k_off + i * 8 * (D / 2), kw[hb][i]);
+                ksb[hb][i] = lds_bytes<KS>(base + hb * RingT::kBlock + ks_off + i * 8 * (D / 16));
             }
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) sc[hb][nr][0] = sc[hb][nr][1] = sc[hb][nr][2] = sc[hb][nr][3] = 0.f;
+        }
 #pragma unroll
-            for (int w = 0; w < KW; ++w) {
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb) {
                 uint32_t h[2][4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     // the scale of word w: byte w / 2 of the lane's, in both halves
                     uint32_t s, c;
-                    kv4::scale_pair(__byte_perm(ksb[i], 0, 0x4040 + (w / 2) * 0x0101), s, c);
-                    kv4::unpack8(kw[i][w], s, c, h[i]);
+                    kv4::scale_pair(__byte_perm(ksb[hb][i], 0, 0x4040 + (w / 2) * 0x0101), s, c);
+                    kv4::unpack8(kw[hb][i][w], s, c, h[i]);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -375,19 +389,9 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
                         Op::run(sc[hb][nr], a, qb[nr][4 * w + 2 * k], qb[nr][4 * w + 2 * k + 1]);
                 }
             }
-        }
         // ---- weights; a score more than kRefMost above its reference moves it
         float mx[NR][2];
         bool over = false;
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-                    for (int kh = 0; kh < 2; ++kh) sc[hb][nr][2 * kh + e] *= srow[nr][e];
-            }
         if (j0 + kStepKeys > all_below) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mx[nr][e] = fmaxf(fmaxf(sc[0][nr][e], sc[0][nr][2 + e]), fmaxf(sc[1][nr][e], sc[1][nr][2 + e]));
+                mx[nr][e] = fmaxf(fmaxf(sc[0][nr][e], sc[0][nr][2 + e]), fmaxf(sc[1][nr][e], sc[1][nr][2 + e])) * srow[nr][e];
                 over |= mx[nr][e] > ref[nr][e] + kRefMost;
             }
         if (__any_sync(0xffffffffu, over)) {
@@ -427,22 +431,24 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
                     for (int i = 0; i < 4; ++i) acc[nr][mt][i] *= al[i & 1];
             }
         }
-        uint32_t pb[2][NR][2][2];  // [block][row tile][high part / remainder][keys 0-7 / 8-15]
+        uint32_t pb[2][NR][kParts][2];  // [block][row tile][high part / remainder][keys 0-7 / 8-15]
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
                 float w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = fast_exp2(sc[hb][nr][i] - ref[nr][i & 1]);
+                for (int i = 0; i < 4; ++i) w[i] = fast_exp2(fmaf(sc[hb][nr][i], srow[nr][i & 1], -ref[nr][i & 1]));
                 l[nr][0] += w[0] + w[2];
                 l[nr][1] += w[1] + w[3];
 #pragma unroll
                 for (int kh = 0; kh < 2; ++kh) {
                     const uint32_t hi = Op::pack(w[2 * kh], w[2 * kh + 1]);
-                    const float2 x = Op::unpack(hi);
                     pb[hb][nr][0][kh] = movmatrix_trans(hi);
-                    pb[hb][nr][1][kh] = movmatrix_trans(Op::pack(w[2 * kh] - x.x, w[2 * kh + 1] - x.y));
+                    if (kParts == 2) {
+                        const float2 x = Op::unpack(hi);
+                        pb[hb][nr][kParts - 1][kh] = movmatrix_trans(Op::pack(w[2 * kh] - x.x, w[2 * kh + 1] - x.y));
+                    }
                 }
             }
         // ---- O^T += V^T P^T
@@ -462,7 +468,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
             }
             if (hb == 1) {  // the step is in registers
                 __syncwarp();
-                if (t + NST < steps) ring.fill(t + NST);
+                if (t + NST < steps) ring.fill();
+                asm volatile("cp.async.commit_group;" ::: "memory");
             }
 #pragma unroll
             for (int w = 0; w < VW; ++w)
@@ -474,20 +481,18 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
                         kv4::unpack8(__byte_perm(vw[2 * kh][w], vw[2 * kh + 1][w], half ? 0x7632 : 0x5410),
                                      vs[kh][w * VS / VW], vc[kh][w * VS / VW], h[kh]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int mt = 4 * w + 2 * half + k;
-                        const uint32_t a[4] = {h[0][2 * k], h[0][2 * k + 1], h[1][2 * k], h[1][2 * k + 1]};
+                    for (int part = 0; part < kParts; ++part)
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr) {
-                            Op::run(acc[nr][mt], a, pb[hb][nr][0][0], pb[hb][nr][0][1]);
-                            Op::run(acc[nr][mt], a, pb[hb][nr][1][0], pb[hb][nr][1][1]);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t a[4] = {h[0][2 * k], h[0][2 * k + 1], h[1][2 * k], h[1][2 * k + 1]};
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr)
+                                Op::run(acc[nr][4 * w + 2 * half + k], a, pb[hb][nr][part][0], pb[hb][nr][part][1]);
                         }
-                    }
                 }
         }
+        slot = slot + 1 == NST ? 0 : slot + 1;
     }
-    if (bad)  // every copy must have landed before the ring is written over
-        for (const int filled = min(steps, t + NST); t < filled; ++t) mbar_wait(ring_bars + 8 * (t % NST), (t / NST) & 1, f.err);
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 s_m[warp * R + nr * 8 + 2 * tq + e] = ref[nr][e];
-                s_l[warp * R + nr * 8 + 2 * tq + e] = bad ? __uint_as_float(0x7fc00000u) : l[nr][e];
+                s_l[warp * R + nr * 8 + 2 * tq + e] = l[nr][e];
             }
         }
     }
@@ -569,10 +574,33 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 }
 
 template <typename T, int D, int NR, int NW, int MINB>
+static cudaError_t launch_kv4_w(Kv4Params p, long long units, int S, cudaStream_t stream) {
+    constexpr int R = 8 * NR;
+    constexpr size_t ring = (size_t)NW * ring_slots(D) * 2 * kv4::block_bytes(kBlockKeys, D);
+    constexpr size_t smem = ring > merge_bytes(D, R, NW) ? ring : merge_bytes(D, R, NW);
+    const FwdParams &f = p.s.f;
+    p.S = S;
+    if (units * S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const bool page16 = f.ps == kBlockKeys;
+    auto kern = page16 ? paged_attn_kv4_kernel<T, D, NR, NW, MINB, true> : paged_attn_kv4_kernel<T, D, NR, NW, MINB, false>;
+    static SmemLimit limits[2], wides[2];
+    cudaError_t e = limits[page16].raise((const void *)kern, smem);
+    if (e == cudaSuccess && S > 8) e = wides[page16].allow_wide_clusters((const void *)kern);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(units * S));
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    cfg.numAttrs = second_launch_attrs(attr, S, p.s.group_min != 0);
+    return cudaLaunchKernelEx(&cfg, kern, p, f.ps == 16 ? 4 : f.ps == 32 ? 5 : 6);
+}
+
+template <typename T, int D, int NR, int NW, int MINB>
 static cudaError_t launch_kv4(Kv4Params p, int sms, cudaStream_t stream) {
     constexpr int R = 8 * NR;
-    constexpr size_t ring = (size_t)NW * ring_slots(D) * Ring<D, 1>::kStep;
-    constexpr size_t smem = ring > merge_bytes(D, R, NW) ? ring : merge_bytes(D, R, NW);
     const FwdParams &f = p.s.f;
     p.HT = (f.G + R - 1) / R;
     p.TT = f.q_start && p.s.n_tok <= f.B ? 1 : f.G < R ? R / f.G : 1;
@@ -588,27 +616,15 @@ static cudaError_t launch_kv4(Kv4Params p, int sms, cudaStream_t stream) {
         tiles = p.TT == 1 ? p.s.n_tok : p.s.n_tok / p.TT + f.B;
     }
     const long long units = tiles * f.Hkv * p.HT;
-    int S = 1;
-    while (S < kMaxCluster && units * S <= (long long)sms * MINB && (long long)f.W * f.ps >= 2ll * kStepKeys * NW * S) S *= 2;
-    p.S = S;
     if (units == 0) return cudaSuccess;
-    if (units * S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    auto kern = paged_attn_kv4_kernel<T, D, NR, NW, MINB>;
-    static SmemLimit limit, wide;
-    cudaError_t e = limit.raise((const void *)kern, smem);
-    if (e == cudaSuccess && S > 8) e = wide.allow_wide_clusters((const void *)kern);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(units * S));
-    cfg.blockDim = dim3(NW * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    cfg.attrs = attr;
-    cfg.numAttrs = second_launch_attrs(attr, S, p.s.group_min != 0);
-    int sh = 0;
-    while ((1 << sh) < f.ps) ++sh;
-    return cudaLaunchKernelEx(&cfg, kern, p, sh);
+    // Few units: a cluster each, as long as a warp keeps two steps of the longest sequence.  While every CTA can have a
+    // multiprocessor of its own it takes all of it: clusters of half as large CTAs are packed onto half of them.
+    const long long keys = (long long)f.W * f.ps;
+    int S = 1;
+    while (S < kMaxCluster && units * 2 * S <= sms && keys >= 4ll * kStepKeys * NW * MINB * S) S *= 2;
+    if (S > 1 || units * 2 <= sms) return launch_kv4_w<T, D, NR, NW * MINB, 1>(p, units, S, stream);
+    while (S < 8 && units * S * 2 <= (long long)sms * MINB && keys >= 4ll * kStepKeys * NW * S) S *= 2;
+    return launch_kv4_w<T, D, NR, NW, MINB>(p, units, S, stream);
 }
 
 template <typename T, int D>

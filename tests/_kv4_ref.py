@@ -52,14 +52,14 @@ def values(pool, ps, D):
 
 
 def attention(q, pool, ps, table, lens, starts, causal, q_offset, scale):
-    """Rows of packed q [T, Hq, D]: out, lse, and how far float32 sums may be off in the score (nats)
-    and in the output (float64); rows of no sequence hold NaN."""
+    """Rows of packed q [T, Hq, D]: out, lse, how far float32 sums may be off in the score (nats) and in the
+    output, and the weighted mean of |v| (float64); rows of no sequence hold NaN."""
     T, Hq, D = q.shape
     P, Hkv, _ = pool.shape
     k, v = values(pool, ps, D)
     G = Hq // Hkv
     out, lse = np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan)
-    off, room = np.zeros((T, Hq)), np.zeros((T, Hq, 1))
+    off, room, mass = np.zeros((T, Hq)), np.zeros((T, Hq, 1)), np.zeros((T, Hq, D))
     for b in range(len(lens)):
         n = starts[b + 1] - starts[b]
         L = min(max(int(lens[b]), 0), table.shape[1] * ps)
@@ -79,13 +79,14 @@ def attention(q, pool, ps, table, lens, starts, causal, q_offset, scale):
                 top = s.max()
                 w = np.exp(s - top)
                 out[t, h] = w @ vv[h // G, :r] / w.sum()
+                mass[t, h] = w @ np.abs(vv[h // G, :r]) / w.sum()
                 lse[t, h] = top + np.log(w.sum())
                 # products summed in float32 over D terms (a truncating adder: 2^-23 each), the factor's and the
                 # exponential's roundings on the score
                 off[t, h] = (np.abs(kk[h // G, :r]) @ np.abs(q[t, h])).max() * abs(scale) * D * 2.0 ** -23 + \
                     np.abs(s).max() * 2.0 ** -22 + 2.0 ** -20
                 room[t, h] = 2 * off[t, h] * np.abs(vv[h // G, :r]).max()
-    return out, lse, off, room
+    return out, lse, off, room, mass
 
 
 # ----------------------------------------------------------------------------- pages

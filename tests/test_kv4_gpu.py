@@ -3,7 +3,8 @@ the pool against 64-bit arithmetic on the values its bytes stand for.
 
 Attention's bars are derived, not fitted: half a rounding step of the output type (bf16 2^-8, f16 2^-11,
 relative) on top of what float32 sums may lose in the scores, which tests/_kv4_ref.py works out row by row from the
-inputs, and 2^-20 of the largest value for the weights (held to 2^-22) and their sum.
+inputs, and what the weights lose on their way to V: sum w |v| / sum w times half an f16 step, 2^-11, where they
+are one f16 number (bf16 outputs), the square of it where they are two.
 """
 import numpy as np
 import pytest
@@ -13,6 +14,7 @@ from tests import _kv4_ref as R
 pytestmark = pytest.mark.gpu
 
 STEP = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+WEIGHT = {"bf16": 2.0 ** -11, "f16": 2.0 ** -22}
 
 
 @pytest.fixture(scope="module")
@@ -169,18 +171,18 @@ def _check(pa, c, causal=True, q_offset=None, scale=None, packed=True, q=None, e
         pa.paged_attn_fwd_kv4(q.view(B, -1, Hq, D), c["kv"], _t(c["table"]), _t(c["lens"]), causal, qo, scale,
                               out.view(B, -1, Hq, D), lse.view(B, -1, Hq))
     assert pa.paged_attn_last_error_word() == err
-    want, want_lse, off, room = R.attention(_np(q), c["pool"], c["ps"], c["table"], c["lens"], c["starts"], causal,
-                                            q_offset, scale)
+    want, want_lse, off, room, mass = R.attention(_np(q), c["pool"], c["ps"], c["table"], c["lens"], c["starts"],
+                                                  causal, q_offset, scale)
     got, got_lse = _np(out), _np(lse)
     own = ~np.isnan(want_lse)
     assert (got[~own] == 5.0).all() and (got_lse[~own] == 5.0).all()  # rows of no sequence
     empty = own & np.isneginf(want_lse)
     assert (got[empty] == 0).all() and np.isneginf(got_lse[empty]).all()
     own &= ~empty
-    bar = STEP[c["dtype"]] * np.abs(want) + room + 2.0 ** -24
-    worst = (np.abs(got - want) / bar)[own]
+    bar = STEP[c["dtype"]] * np.abs(want) + room + WEIGHT[c["dtype"]] * mass + 2.0 ** -24
+    worst = np.abs(got - want)[own] / bar[own]
     assert worst.size == 0 or worst.max() <= 1, f"output off by {worst.max():.3g} of its bar"
-    worst = (np.abs(got_lse - want_lse) / (off + 2.0 ** -22 * np.abs(want_lse)))[own]
+    worst = np.abs(got_lse - want_lse)[own] / (off + 2.0 ** -22 * np.abs(want_lse))[own]
     assert worst.size == 0 or worst.max() <= 1, f"lse off by {worst.max():.3g} of its bar"
 
 
