@@ -471,8 +471,8 @@ int paged_attn_sparse_shares_pages(const pa_dims *dims, int packed, int top_k, f
  *   (u - 8) * s(c),   s(c) = c * 2^-17 for c < 8,  else (8 + c % 8) * 2^(c / 8 - 18),  at most s(0xDE) = 7168
  * (bytes above 0xDE count as 0xDE), so any bytes are finite numbers, all of them exact in f16, bf16 and
  * float32; a pool of zeros holds zeros.  Tables, slots, lengths and pages are those of the other pools, and
- * these calls follow the rules of the serving step above: a launch or two on `stream`, no workspace,
- * graph capture after a first call on the device.  They are this library's own.
+ * these calls follow the rules of the serving step above: a launch or two on `stream`, graph capture after a
+ * first call on the device.  They are this library's own.
  *
  * paged_attn_append_kv4 — new tokens' K and V rows into their slots.
  *   k_new, v_new [T, Hkv, D] in dims->dtype (any), k_stride, v_stride and slots [T] as for paged_attn_append
@@ -502,10 +502,18 @@ int paged_attn_gather_kv4(const void *kv, const int32_t *slots, void *k_out, voi
  * weight meets V as one f16 number for bf16 (within 2^-11 of it, an eighth of the output's own rounding) and as two for
  * f16 (2^-22), or within 2^-35 of the row's largest.  A page id outside [0, num_pages) reads as zeros and sets
  * PA_ERRBIT_PAGE_RANGE.
+ * workspace (device, 16-byte aligned, workspace_bytes long) lets few rows over long sequences use the whole GPU, their keys
+ * shared by any number of CTAs and joined by a second launch; with NULL, or less than paged_attn_kv4_workspace_bytes,
+ * clusters of up to four share them.  Its contents mean nothing before and after; calls that may overlap need
+ * one each.
+ *
+ * paged_attn_kv4_workspace_bytes — what such a call makes use of on a GPU of num_sms SMs (0: nothing).  packed: q is
+ * [T, Hq, D] with T = dims->q_len.  Host-only.  Negative status for bad dims or num_sms < 1.
  */
+int64_t paged_attn_kv4_workspace_bytes(const pa_dims *dims, int packed, int num_sms);
 int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table, const int32_t *seq_lens,
                        const int32_t *q_start, int causal, const int32_t *q_offset, float scale, void *out, float *lse,
-                       const pa_dims *dims, void *stream);
+                       const pa_dims *dims, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * ------------------------------------------------------------------ sharing, freeing and moving pages

@@ -26,7 +26,8 @@ __all__ = [
     "paged_attn_fwd_varlen_overlap", "paged_attn_varlen_hint", "paged_attn_varlen_overlap_share", "PaVarlenHint",
     "paged_attn_step_tables", "paged_attn_append", "paged_attn_select_pages", "paged_attn_fwd_sparse",
     "paged_attn_sparse_shares_pages", "step_tables", "page_envelopes", "attention_sparse",
-    "paged_attn_append_kv4", "paged_attn_gather_kv4", "paged_attn_fwd_kv4", "kv4_pool", "attention_kv4",
+    "paged_attn_append_kv4", "paged_attn_gather_kv4", "paged_attn_fwd_kv4", "paged_attn_kv4_workspace_bytes",
+    "kv4_pool", "attention_kv4",
     "paged_attn_fork", "paged_attn_free", "paged_attn_compact", "paged_attn_copy_pages", "fork_sequences",
     "free_sequences", "compact_pages", "PA_F32", "PA_F16", "PA_BF16", "PA_FP8_E4M3",
     "PA_INT8",
@@ -123,7 +124,9 @@ def load_library(build_if_missing: bool = False):
     lib.paged_attn_append_kv4.restype = ctypes.c_int
     lib.paged_attn_gather_kv4.argtypes = [P, P, P, P, D, P]
     lib.paged_attn_gather_kv4.restype = ctypes.c_int
-    lib.paged_attn_fwd_kv4.argtypes = [P, P, P, P, P, I32, P, F, P, P, D, P]
+    lib.paged_attn_fwd_kv4.argtypes = [P, P, P, P, P, I32, P, F, P, P, D, P, I64, P]
+    lib.paged_attn_kv4_workspace_bytes.argtypes = [D, I32, I32]
+    lib.paged_attn_kv4_workspace_bytes.restype = ctypes.c_int64
     lib.paged_attn_fwd_kv4.restype = ctypes.c_int
     lib.paged_attn_fork.argtypes = [P, P, P, I32, P, P, P, P, P, I32, P, P, P, I32, I32, I64, I32, P]
     lib.paged_attn_fork.restype = ctypes.c_int
@@ -739,11 +742,35 @@ def paged_attn_gather_kv4(kv, slots, k_out, v_out, stream=None) -> None:
         _raise(rc, "paged_attn_gather_kv4")
 
 
+_sms: dict = {}  # device -> multiprocessors
+
+
+def _sm_count(dev: int) -> int:
+    n = _sms.get(dev)
+    if n is None:
+        n = _sms[dev] = _device_info(dev)[0]
+    return n
+
+
+def paged_attn_kv4_workspace_bytes(batch: int, tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                   page_size: int, table_width: int, num_sms: int, dtype: int = PA_BF16,
+                                   packed: bool = True) -> int:
+    """Workspace that ``paged_attn_fwd_kv4`` makes use of for this shape (0: none); see
+    ``paged_attn_kv4_workspace_bytes`` in include/paged_attn.h.  tokens: all of a packed batch's, or a sequence's of a
+    uniform one."""
+    dims = PaDims(batch, tokens, num_q_heads, num_kv_heads, head_dim, page_size, 1, table_width, dtype)
+    n = load_library().paged_attn_kv4_workspace_bytes(dims, 1 if packed else 0, num_sms)
+    if n < 0:
+        _raise(int(n), "paged_attn_kv4_workspace_bytes")
+    return int(n)
+
+
 def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, out, lse, q_start=None,
-                       stream=None) -> None:
+                       stream=None, workspace=None) -> None:
     """Forward over a 4-bit pool (``kv4_pool``, filled by ``paged_attn_append_kv4``); see
     ``paged_attn_fwd_kv4`` in include/paged_attn.h.  q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start
-    [B + 1], in f16 or bf16; out as q (dense), lse without D or None."""
+    [B + 1], in f16 or bf16; out as q (dense), lse without D or None.  workspace: a uint8 tensor; without one, what the
+    shape makes use of is taken from torch's caching allocator for the call."""
     torch = _torch()
     i32, dev, dt = torch.int32, torch.cuda.current_device(), q.dtype
     if block_table.dim() != 2 or q.dim() != (4 if q_start is None else 3):
@@ -767,9 +794,18 @@ def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, ou
     if lse is not None:
         _need(lse, "lse", dev, torch.float32, shape[:-1])
     dims = PaDims(B, shape[-3], Hq, kv.shape[1], D, ps, kv.shape[0], W, _dtype_code(q), stride)
-    rc = load_library().paged_attn_fwd_kv4(q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-                                           _ptr(q_start), 1 if causal else 0, _ptr(q_offset), scale, out.data_ptr(),
-                                           _ptr(lse), dims, _stream(stream))
+    lib = load_library()
+    if workspace is None:
+        size = lib.paged_attn_kv4_workspace_bytes(dims, 0 if q_start is None else 1, _sm_count(dev))
+        if size > 0:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            _record(stream, workspace)
+    else:
+        _need(workspace, "workspace", dev, torch.uint8, workspace.shape)
+        size = workspace.numel()
+    rc = lib.paged_attn_fwd_kv4(q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                                _ptr(q_start), 1 if causal else 0, _ptr(q_offset), scale, out.data_ptr(), _ptr(lse), dims,
+                                _ptr(workspace), max(size, 0), _stream(stream))
     if rc:
         _raise(rc, "paged_attn_fwd_kv4")
 

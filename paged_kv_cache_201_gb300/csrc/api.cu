@@ -931,15 +931,41 @@ int paged_attn_gather_kv4(const void *kv, const int32_t *slots, void *k_out, voi
     return kv4_rows_call(nullptr, nullptr, k_out, v_out, slots, 0, 0, const_cast<void *>(kv), dims, stream);
 }
 
-int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table, const int32_t *seq_lens,
-                       const int32_t *q_start, int causal, const int32_t *q_offset, float scale, void *out, float *lse,
-                       const pa_dims *dims, void *stream) {
+namespace {
+
+// Checks of the shape of paged_attn_fwd_kv4; *n_tok: query tokens.
+int check_kv4(const pa_dims *dims, bool packed, int64_t *n_tok) {
     int rc = check_dims(dims);
     if (rc != PA_OK) return rc;
     if (dims->dtype == PA_F32) return PA_EDTYPE;
-    if (!isfinite(scale)) return PA_EINVAL;
     if ((int64_t)dims->num_kv_heads * dims->page_size * dims->head_dim / 8 * 9 >= (int64_t)1 << 31) return PA_EUNSUPPORTED;
-    const int64_t n_tok = dims->batch == 0 ? 0 : q_start ? (int64_t)dims->q_len : (int64_t)dims->batch * dims->q_len;
+    *n_tok = dims->batch == 0 ? 0 : packed ? (int64_t)dims->q_len : (int64_t)dims->batch * dims->q_len;
+    return PA_OK;
+}
+
+}  // namespace
+
+int64_t paged_attn_kv4_workspace_bytes(const pa_dims *dims, int packed, int num_sms) {
+    int64_t n_tok = 0;
+    const int rc = check_kv4(dims, packed != 0, &n_tok);
+    if (rc != PA_OK) return rc;
+    if (num_sms < 1) return PA_EINVAL;
+    if (n_tok == 0) return 0;
+    pa::SparseParams sp{};
+    sp.f = fill_params(nullptr, nullptr, nullptr, nullptr, nullptr, 1, nullptr, 1, 1.f, nullptr, nullptr, dims, nullptr);
+    static const int32_t some = 0;
+    sp.f.q_start = packed ? &some : nullptr;  // only whether there is one counts
+    sp.n_tok = n_tok;
+    return pa::kv4_workspace_bytes(sp, num_sms);
+}
+
+int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table, const int32_t *seq_lens,
+                       const int32_t *q_start, int causal, const int32_t *q_offset, float scale, void *out, float *lse,
+                       const pa_dims *dims, void *workspace, int64_t workspace_bytes, void *stream) {
+    int64_t n_tok = 0;
+    int rc = check_kv4(dims, q_start != nullptr, &n_tok);
+    if (rc != PA_OK) return rc;
+    if (!isfinite(scale) || workspace_bytes < 0 || !aligned16(workspace)) return PA_EINVAL;
     if (n_tok == 0) return PA_OK;
     rc = check_fwd_pointers(q, kv, kv, block_table, seq_lens, q_offset, 1, out, lse);
     if (rc != PA_OK) return rc;
@@ -950,6 +976,8 @@ int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table
     sp.f = fill_params(q, kv, nullptr, block_table, seq_lens, causal, q_offset, 1, scale, out, lse, dims, err);
     sp.f.q_start = q_start;
     sp.n_tok = n_tok;
+    sp.ws = workspace;
+    sp.ws_bytes = workspace_bytes;
     return cuda_status(pa::launch_kv4_mma(sp, dims->dtype, device_sm_count(), static_cast<cudaStream_t>(stream)));
 }
 

@@ -35,14 +35,15 @@ using namespace mmac;
 
 namespace {
 
-constexpr int kBlockKeys = 16, kStepKeys = 32, kMaxCluster = 16;
+constexpr int kBlockKeys = 16, kStepKeys = 32;
 constexpr float kRefBelow = 11.f, kRefMost = 15.f;
 constexpr float kLeastFactor = 0x1p-100f;  // a scale of 0 leaves this: kNegInf times it is still no NaN, and any sum times it 0
 constexpr float kNoRef = -3e38f;  // before the first key; finite, so that kNegInf - ref is no NaN
 
 struct Kv4Params {
     SparseParams s;
-    int S;         // CTAs of a cluster
+    int S;         // CTAs that share a unit's keys: a cluster, or with part_out a grid's
+    float *part_out, *part_state;  // [S, rows of q x heads, D] and [S, rows, 2] (reference, sum) for the second launch
     int TT, HT;    // tokens of a unit; head tiles of a kv head
     int seq_tiles; // tiles of every sequence: a uniform batch, or the short runs of a packed one (0: by rows of q)
 };
@@ -97,6 +98,36 @@ __device__ __forceinline__ Tile find_tile(const Kv4Params &p, int tile, int lane
     u.cnt = min(p.TT, u.n - u.i);
     return u;
 }
+
+// A unit: up to R rows r = token x heads + head of tile u and kv head kvh.
+struct Unit {
+    Tile u;
+    int kvh, h0, heads, rows;
+    int L, k_hi;  // keys of the sequence; those that the unit's last token, which reaches furthest, sees
+    __device__ __forceinline__ Unit(const Kv4Params &p, int R, int index, int lane, int ps_shift, bool report) {
+        const FwdParams &f = p.s.f;
+        h0 = index % p.HT * R;
+        index /= p.HT;
+        kvh = index % f.Hkv;
+        u = find_tile(p, index / f.Hkv, lane);
+        heads = min(R, f.G - h0);
+        rows = L = k_hi = 0;
+        if (u.cnt <= 0) return;
+        rows = u.cnt * heads;
+        L = max(__ldg(f.seq_lens + u.b), 0);
+        if (L > f.W << ps_shift) {  // never read past the sequence's block-table row
+            if (report) atomicOr(f.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
+            L = f.W << ps_shift;
+        }
+        k_hi = limit(f, u.cnt - 1);
+    }
+    __device__ __forceinline__ int limit(const FwdParams &f, int token) const {
+        return row_key_limit(f, u.b, L, u.i + token, u.n);
+    }
+    __device__ __forceinline__ long long row(const FwdParams &f, int r) const {
+        return (u.q0 + u.i + r / heads) * f.Hq + kvh * f.G + h0 + r % heads;
+    }
+};
 
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
@@ -245,13 +276,19 @@ __device__ __forceinline__ void store4(T *o, float4 v) {
     *reinterpret_cast<uint2 *>(o) = w;
 }
 
+// Elements c .. c + 3 of a row whose sums are o (of values / 8) and sum, with reference M.
+template <typename T, int D>
+__device__ __forceinline__ void store_row(const FwdParams &f, long long row, int c, float4 o, float M, float sum) {
+    const float inv = sum != 0.f ? 8.f / sum : 0.f;  // a NaN stays one
+    store4<T>(static_cast<T *>(f.out) + row * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (c == 0 && f.lse) f.lse[row] = sum != 0.f ? M * kLn2 + logf(sum) : kNegInf;
+}
+
 // Shared memory of the merge: rows [warps][R][D + 4], references and sums [warps][R], then the CTA's own [R] each.
 __host__ __device__ constexpr size_t merge_bytes(int D, int R, int warps) {
     return ((size_t)warps * R * (D + 4) + (2 * warps + 2) * R) * 4;
 }
 __host__ __device__ constexpr int ring_slots(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
-
-}  // namespace
 
 template <typename T, int D, int NR, int NW, int MINB, bool PAGE16>
 __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4Params p, int ps_shift) {
@@ -273,24 +310,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % p.S);
-    int unit = (int)(blockIdx.x / p.S);
-    const int ht = unit % p.HT;
-    unit /= p.HT;
-    const int kvh = unit % f.Hkv;
-    const Tile u = find_tile(p, unit / f.Hkv, lane);
+    const Unit un(p, R, (int)(blockIdx.x / p.S), lane, ps_shift, threadIdx.x == 0);
     ranges.report(f);
-    if (u.cnt <= 0) return;
-
-    int L = max(__ldg(f.seq_lens + u.b), 0);
-    if (L > f.W << ps_shift) {  // never read past the sequence's block-table row
-        if (threadIdx.x == 0) atomicOr(f.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
-        L = f.W << ps_shift;
-    }
-    // unit rows r = token x heads + head; the last token reaches furthest
-    const int h0 = ht * R, heads = min(R, f.G - h0);
-    const int rows = u.cnt * heads;
-    auto row_index = [&](int r) { return (u.q0 + u.i + r / heads) * f.Hq + kvh * f.G + h0 + r % heads; };
-    const int k_hi = row_key_limit(f, u.b, L, u.i + u.cnt - 1, u.n);
+    if (un.rows == 0) return;
+    const int rows = un.rows, k_hi = un.k_hi;
+    auto row_index = [&](int r) { return un.row(f, r); };
     if (k_hi <= 0) {
         if (rank == 0) {
             for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads)
@@ -306,7 +330,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     const int steps = (b1 - b0 + 1) / 2;
 
     const uint32_t ring_smem = smem_u32(smem) + warp * NST * RingT::kStep;
-    RingT ring(f, u.b, kvh, ps_shift, b0, b1, ring_smem, lane);
+    RingT ring(f, un.u.b, un.kvh, ps_shift, b0, b1, ring_smem, lane);
 #pragma unroll 1
     for (int st = 0; st < NST; ++st) {
         if (st < steps) ring.fill();
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         for (int e = 0; e < 2; ++e) {
             const int rc = nr * 8 + 2 * tq + e;
             srow[nr][e] = fmaxf(8.f * fabsf(f.scale_log2) * __shfl_sync(0xffffffffu, inv, 4 * (2 * tq + e)), kLeastFactor);
-            lim[nr][e] = min(rc < rows ? row_key_limit(f, u.b, L, u.i + rc / heads, u.n) : INT_MAX, b1 * kBlockKeys);
+            lim[nr][e] = min(rc < rows ? un.limit(f, rc / un.heads) : INT_MAX, b1 * kBlockKeys);
             all_below = min(all_below, lim[nr][e]);
         }
     }
@@ -524,12 +548,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         }
     }
     __syncthreads();
-    auto store = [&](int r, int c, float4 o, float M, float sum) {
-        const float inv = sum != 0.f ? 8.f / sum : 0.f;  // a NaN stays one
-        const long long ri = row_index(r);
-        store4<T>(static_cast<T *>(f.out) + ri * D + c, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (c == 0 && f.lse) f.lse[ri] = sum != 0.f ? M * kLn2 + logf(sum) : kNegInf;
-    };
+    auto store = [&](int r, int c, float4 o, float M, float sum) { store_row<T, D>(f, row_index(r), c, o, M, sum); };
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
         float M = kNoRef, sum = 0.f;
@@ -543,7 +562,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
             sum += k * s_l[w * R + r];
             o.x += k * v.x, o.y += k * v.y, o.z += k * v.z, o.w += k * v.w;
         }
-        if (p.S == 1) {
+        if (p.part_out) {
+            const long long at_row = rank * p.s.n_tok * f.Hq + row_index(r);
+            *reinterpret_cast<float4 *>(p.part_out + at_row * D + c) = o;
+            if (c == 0) *reinterpret_cast<float2 *>(p.part_state + 2 * at_row) = make_float2(M, sum);
+        } else if (p.S == 1) {
             store(r, c, o, M, sum);
         } else {  // the row's slot of warp 0 is this thread's alone
             *reinterpret_cast<float4 *>(sm + r * STRIDE + c) = o;
@@ -553,7 +576,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
             }
         }
     }
-    if (p.S == 1) return;
+    if (p.S == 1 || p.part_out) return;
     // ---- the CTAs' states: each stores its share of the rows' elements
     cluster_barrier();
     for (int i = rank * kThreads + threadIdx.x; i < rows * (D / 4); i += p.S * kThreads) {
@@ -573,85 +596,163 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     cluster_barrier();  // the peers have read this CTA's memory
 }
 
+// The second launch where a grid's CTAs shared the keys: one row of a unit a CTA, its parts dealt out to the warps.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_attn_kv4_join_kernel(const Kv4Params p, int R, int ps_shift) {
+    const FwdParams &f = p.s.f;
+    constexpr int C = D / 4, TG = 128 / C;  // threads of a row, parts at once
+    __shared__ float4 s_o[TG][C];
+    __shared__ float s_l[TG];
+    const int c = threadIdx.x % C, tg = threadIdx.x / C, r = blockIdx.x % R;
+    const Unit un(p, R, (int)(blockIdx.x / R), threadIdx.x & 31, ps_shift, false);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (r >= un.rows || un.k_hi <= 0) return;
+    const long long row = un.row(f, r), rows = p.s.n_tok * f.Hq;
+    const float2 *state = reinterpret_cast<const float2 *>(p.part_state) + row;
+    float M = kNoRef, sum = 0.f;
+    for (int x = 0; x < p.S; ++x) M = fmaxf(M, __ldcg(state + x * rows).x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = tg; x < p.S; x += TG) {
+        const float2 st = __ldcg(state + x * rows);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_out + (x * rows + row) * D) + c);
+        const float k = fast_exp2(st.x - M);
+        sum += k * st.y;
+        o.x += k * v.x, o.y += k * v.y, o.z += k * v.z, o.w += k * v.w;
+    }
+    s_o[tg][c] = o;
+    if (c == 0) s_l[tg] = sum;
+    __syncthreads();
+    if (tg != 0) return;
+#pragma unroll
+    for (int x = 1; x < TG; ++x) {
+        const float4 v = s_o[x][c];
+        sum += s_l[x];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    store_row<T, D>(f, row, c * 4, o, M, sum);
+}
+
+// How a call is cut: units of 8 NR rows, the keys of each shared by S CTAs of `warps` warps.
+struct Plan {
+    int nr, warps, HT, TT, seq_tiles;
+    long long units;
+    int S;
+    bool grid;  // S of the grid's CTAs, joined by a second launch; else a cluster
+};
+Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
+    const FwdParams &f = sp.f;
+    Plan a{};
+    // rows of an average sequence (a uniform batch: of every one)
+    const double rows = (f.q_start ? (double)sp.n_tok / f.B : (double)f.Sq) * f.G;
+    a.nr = f.D == 256 || rows <= 8 || (f.G > 16 && f.G <= 24) ? 1 : 2;
+    const int R = 8 * a.nr, full = f.D == 256 ? 8 : a.nr == 2 ? 12 : 16;  // warps that fill a multiprocessor
+    const int ctas = f.D == 256 || a.nr == 1 ? 2 : 3;                     // CTAs that do otherwise
+    a.HT = (f.G + R - 1) / R;
+    a.TT = f.q_start && sp.n_tok <= f.B ? 1 : f.G < R ? R / f.G : 1;
+    long long tiles;
+    if (!f.q_start || sp.by_seq) {
+        a.seq_tiles = ((f.q_start ? sp.group_min - 1 : f.Sq) + a.TT - 1) / a.TT;
+        tiles = (long long)f.B * a.seq_tiles;
+    } else {
+        tiles = a.TT == 1 ? sp.n_tok : sp.n_tok / a.TT + f.B;
+    }
+    a.units = tiles * f.Hkv * a.HT;
+    a.S = 1;
+    if (a.units == 0) return a;
+    // Few units: their keys go to several CTAs, as long as a warp keeps two steps of the longest sequence.  While every CTA
+    // can have a multiprocessor of its own it takes all of it (half as large ones of a cluster would be packed onto half
+    // of the multiprocessors).  Clusters of two or four: 15 of eight and 7 of sixteen fit at once, which leaves too many
+    // multiprocessors idle; with a workspace any number of the grid's CTAs, and a second launch.
+    const long long keys = (long long)f.W * f.ps;
+    a.warps = full;
+    while (a.S < 4 && a.units * 2 * a.S <= sms && keys >= 4ll * kStepKeys * full * a.S) a.S *= 2;
+    long long n = sms / a.units;
+    const long long most = keys / (2ll * kStepKeys * full), part = sp.n_tok * f.Hq * (f.D + 2) * 4;
+    n = n < most ? n : most;
+    if (!sp.group_min && n > a.S && ws_bytes / part >= n && a.units * R <= 0x7fffffffLL) {
+        // 1024 keys take a multiprocessor some 4 us at head_dim 128, the second launch takes 3
+        const double one = 4.0 * keys / 1024 * f.D / 128;
+        if (one / n + 3 < one / a.S) {
+            a.S = (int)n;
+            a.grid = true;
+        }
+    }
+    if (a.units * a.S <= sms) return a;
+    a.warps = full / ctas;
+    while (a.S < 4 && a.units * a.S * 2 <= (long long)sms * ctas && keys >= 4ll * kStepKeys * a.warps * a.S) a.S *= 2;
+    return a;
+}
+
 template <typename T, int D, int NR, int NW, int MINB>
-static cudaError_t launch_kv4_w(Kv4Params p, long long units, int S, cudaStream_t stream) {
+cudaError_t launch_kv4(Kv4Params p, const Plan &a, cudaStream_t stream) {
     constexpr int R = 8 * NR;
     constexpr size_t ring = (size_t)NW * ring_slots(D) * 2 * kv4::block_bytes(kBlockKeys, D);
     constexpr size_t smem = ring > merge_bytes(D, R, NW) ? ring : merge_bytes(D, R, NW);
     const FwdParams &f = p.s.f;
-    p.S = S;
-    if (units * S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (a.units * a.S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    p.S = a.S;
+    p.HT = a.HT;
+    p.TT = a.TT;
+    p.seq_tiles = a.seq_tiles;
+    if (a.grid) {
+        p.part_out = static_cast<float *>(p.s.ws);
+        p.part_state = p.part_out + a.S * p.s.n_tok * f.Hq * D;
+    }
     const bool page16 = f.ps == kBlockKeys;
+    const int ps_shift = f.ps == 16 ? 4 : f.ps == 32 ? 5 : 6;
     auto kern = page16 ? paged_attn_kv4_kernel<T, D, NR, NW, MINB, true> : paged_attn_kv4_kernel<T, D, NR, NW, MINB, false>;
-    static SmemLimit limits[2], wides[2];
+    static SmemLimit limits[2];
     cudaError_t e = limits[page16].raise((const void *)kern, smem);
-    if (e == cudaSuccess && S > 8) e = wides[page16].allow_wide_clusters((const void *)kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(units * S));
+    cfg.gridDim = dim3((unsigned)(a.units * a.S));
     cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = second_launch_attrs(attr, S, p.s.group_min != 0);
-    return cudaLaunchKernelEx(&cfg, kern, p, f.ps == 16 ? 4 : f.ps == 32 ? 5 : 6);
-}
-
-template <typename T, int D, int NR, int NW, int MINB>
-static cudaError_t launch_kv4(Kv4Params p, int sms, cudaStream_t stream) {
-    constexpr int R = 8 * NR;
-    const FwdParams &f = p.s.f;
-    p.HT = (f.G + R - 1) / R;
-    p.TT = f.q_start && p.s.n_tok <= f.B ? 1 : f.G < R ? R / f.G : 1;
-    long long tiles;
-    if (!f.q_start) {
-        p.seq_tiles = (f.Sq + p.TT - 1) / p.TT;
-        tiles = (long long)f.B * p.seq_tiles;
-    } else if (p.s.by_seq) {
-        p.seq_tiles = (p.s.group_min - 1 + p.TT - 1) / p.TT;
-        tiles = (long long)f.B * p.seq_tiles;
-    } else {
-        p.seq_tiles = 0;
-        tiles = p.TT == 1 ? p.s.n_tok : p.s.n_tok / p.TT + f.B;
-    }
-    const long long units = tiles * f.Hkv * p.HT;
-    if (units == 0) return cudaSuccess;
-    // Few units: a cluster each, as long as a warp keeps two steps of the longest sequence.  While every CTA can have a
-    // multiprocessor of its own it takes all of it: clusters of half as large CTAs are packed onto half of them.
-    const long long keys = (long long)f.W * f.ps;
-    int S = 1;
-    while (S < kMaxCluster && units * 2 * S <= sms && keys >= 4ll * kStepKeys * NW * MINB * S) S *= 2;
-    if (S > 1 || units * 2 <= sms) return launch_kv4_w<T, D, NR, NW * MINB, 1>(p, units, S, stream);
-    while (S < 8 && units * S * 2 <= (long long)sms * MINB && keys >= 4ll * kStepKeys * NW * S) S *= 2;
-    return launch_kv4_w<T, D, NR, NW, MINB>(p, units, S, stream);
+    cfg.numAttrs = second_launch_attrs(attr, a.grid ? 1 : a.S, p.s.group_min != 0);
+    e = cudaLaunchKernelEx(&cfg, kern, p, ps_shift);
+    if (e != cudaSuccess || !a.grid) return e;
+    cfg.gridDim = dim3((unsigned)(a.units * R));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;  // may start beside the first's last CTAs
+    return cudaLaunchKernelEx(&cfg, paged_attn_kv4_join_kernel<T, D>, p, R, ps_shift);
 }
 
 template <typename T, int D>
-static cudaError_t launch_kv4_d(const Kv4Params &p, int sms, cudaStream_t stream) {
-    const FwdParams &f = p.s.f;
-    // rows of an average sequence (a uniform batch: of every one)
-    const double rows = (f.q_start ? (double)p.s.n_tok / f.B : (double)f.Sq) * f.G;
+cudaError_t launch_kv4_d(const Kv4Params &p, const Plan &a, cudaStream_t stream) {
     if constexpr (D == 256) {
-        return launch_kv4<T, D, 1, 4, 2>(p, sms, stream);
+        return a.warps == 8 ? launch_kv4<T, D, 1, 8, 1>(p, a, stream) : launch_kv4<T, D, 1, 4, 2>(p, a, stream);
     } else {
-        if (rows > 8 && !(f.G > 16 && f.G <= 24)) return launch_kv4<T, D, 2, 4, 3>(p, sms, stream);
-        return launch_kv4<T, D, 1, 8, 2>(p, sms, stream);
+        if (a.nr == 2) return a.warps == 12 ? launch_kv4<T, D, 2, 12, 1>(p, a, stream) : launch_kv4<T, D, 2, 4, 3>(p, a, stream);
+        return a.warps == 16 ? launch_kv4<T, D, 1, 16, 1>(p, a, stream) : launch_kv4<T, D, 1, 8, 2>(p, a, stream);
     }
 }
 
 template <typename T>
-static cudaError_t launch_kv4_t(const Kv4Params &p, int sms, cudaStream_t stream) {
-    if (p.s.f.D == 64) return launch_kv4_d<T, 64>(p, sms, stream);
-    if (p.s.f.D == 128) return launch_kv4_d<T, 128>(p, sms, stream);
-    return launch_kv4_d<T, 256>(p, sms, stream);
+cudaError_t launch_kv4_t(const Kv4Params &p, const Plan &a, cudaStream_t stream) {
+    if (p.s.f.D == 64) return launch_kv4_d<T, 64>(p, a, stream);
+    if (p.s.f.D == 128) return launch_kv4_d<T, 128>(p, a, stream);
+    return launch_kv4_d<T, 256>(p, a, stream);
+}
+
+}  // namespace
+
+long long kv4_workspace_bytes(const SparseParams &sp, int sms) {
+    const Plan a = make_plan(sp, sms, LLONG_MAX);
+    return a.grid ? a.S * sp.n_tok * sp.f.Hq * (sp.f.D + 2) * 4 : 0;
 }
 
 cudaError_t launch_kv4_mma(const SparseParams &sp, int dtype, int sms, cudaStream_t stream) {
     Kv4Params p{};
     p.s = sp;
-    if (dtype == PA_BF16) return launch_kv4_t<__nv_bfloat16>(p, sms, stream);
-    return launch_kv4_t<__half>(p, sms, stream);
+    const Plan a = make_plan(sp, sms, sp.ws ? sp.ws_bytes : 0);
+    if (a.units == 0) return cudaSuccess;
+    if (dtype == PA_BF16) return launch_kv4_t<__nv_bfloat16>(p, a, stream);
+    return launch_kv4_t<__half>(p, a, stream);
 }
 
 }  // namespace pa

@@ -70,18 +70,13 @@ cudaError_t launch_gather(const void *cache, const int32_t *block_table, const i
 struct SmemLimit {
     std::atomic<uint64_t> done[2];
     cudaError_t raise(const void *kern, size_t bytes) {
-        return once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    }
-    // Clusters of more than eight CTAs.
-    cudaError_t allow_wide_clusters(const void *kern) { return once(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); }
-    cudaError_t once(const void *kern, cudaFuncAttribute attr, int value) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
         const bool known = dev >= 0 && dev < 128;
         const uint64_t bit = 1ull << (dev & 63);
         if (known && (done[dev >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
-        e = cudaFuncSetAttribute(kern, attr, value);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e == cudaSuccess && known) done[dev >> 6].fetch_or(bit, std::memory_order_release);
         return e;
     }
@@ -121,6 +116,8 @@ struct SparseParams {
     int K, sink, local;
     int group_min;  // packed batches: sequences of so many tokens are the tcgen05 kernel's (0: none)
     int by_seq;     // the other kernel's units are group_min - 1 tokens of every sequence, not the rows of q
+    void *ws;       // paged_attn_fwd_kv4: workspace of ws_bytes, or null
+    long long ws_bytes;
 };
 // Runs of tokens of a sequence, scored with tcgen05: head_dim 64 / 128, G <= 32.  select_tile_tokens: tokens of
 // one CTA (0: not for this shape or table width).
@@ -161,9 +158,10 @@ struct Kv4RowsParams {
     int T, Hkv, ps_shift;
 };
 cudaError_t launch_kv4_rows(const Kv4RowsParams &p, int dtype, int D, cudaStream_t stream);
-// Attention over a 4-bit pool (p.f.k_cache), bf16/f16 queries: mma.sync, a sequence's keys split over a cluster when
+// Attention over a 4-bit pool (p.f.k_cache), bf16/f16 queries: mma.sync, a sequence's keys shared by several CTAs when
 // there are few rows.
 cudaError_t launch_kv4_mma(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+long long kv4_workspace_bytes(const SparseParams &p, int sms);  // what lets it share few units' keys out further
 
 // ---------------------------------------------------------------- pages of a cache
 constexpr int kCopyMaxPools = PA_COPY_MAX_POOLS;

@@ -155,7 +155,7 @@ def _case(seed, lens, new, Hkv, G, D, ps, dtype, pads=0, spare=2, width=None):
     return dict(q=q, kv=_t(pool), pool=pool, ps=ps, table=table, lens=lens.astype(np.int32), starts=starts, dtype=dtype)
 
 
-def _check(pa, c, causal=True, q_offset=None, scale=None, packed=True, q=None, err=0):
+def _check(pa, c, causal=True, q_offset=None, scale=None, packed=True, q=None, err=0, workspace=None):
     import torch
     q = c["q"] if q is None else q
     T, Hq, D = q.shape
@@ -165,11 +165,11 @@ def _check(pa, c, causal=True, q_offset=None, scale=None, packed=True, q=None, e
     qo = None if q_offset is None else _t(q_offset, np.int32)
     if packed:
         pa.paged_attn_fwd_kv4(q, c["kv"], _t(c["table"]), _t(c["lens"]), causal, qo, scale, out, lse,
-                              q_start=_t(c["starts"]))
+                              q_start=_t(c["starts"]), workspace=workspace)
     else:
         B = len(c["lens"])
         pa.paged_attn_fwd_kv4(q.view(B, -1, Hq, D), c["kv"], _t(c["table"]), _t(c["lens"]), causal, qo, scale,
-                              out.view(B, -1, Hq, D), lse.view(B, -1, Hq))
+                              out.view(B, -1, Hq, D), lse.view(B, -1, Hq), workspace=workspace)
     assert pa.paged_attn_last_error_word() == err
     want, want_lse, off, room, mass = R.attention(_np(q), c["pool"], c["ps"], c["table"], c["lens"], c["starts"],
                                                   causal, q_offset, scale)
@@ -212,12 +212,26 @@ def test_uniform_and_offsets(pa, causal):
     _check(pa, c, causal, q_offset=[-9, 3, 100, -3])
 
 
-def test_long_split(pa):
-    """Few rows over many pages: the keys go to the CTAs of a cluster."""
-    _check(pa, _case(1, [9000], [1], 1, 4, 128, 16, "bf16"))
-    _check(pa, _case(2, [5000, 33], [2, 1], 2, 8, 64, 64, "f16"))
-    _check(pa, _case(3, [3000], [1], 1, 2, 256, 32, "bf16"))
-    _check(pa, _case(4, [100], [1], 1, 4, 128, 16, "bf16", width=900))  # a wide table, CTAs without keys
+LONG = [([9000], [1], 1, 4, 128, 16, "bf16"), ([5000, 33], [2, 1], 2, 8, 64, 64, "f16"), ([3000], [1], 1, 2, 256, 32, "bf16"),
+        ([100], [1], 1, 4, 128, 16, "bf16"), ([20000, 0, 700], [3, 1, 0], 1, 8, 128, 32, "f16")]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_few_rows_many_keys(pa, case):
+    """Few rows over many pages: with a workspace the whole grid shares the keys, without one clusters do; both beside
+    sequences that leave most of their CTAs without keys, and in a table far wider than any sequence."""
+    import torch
+    lens, new, Hkv, G, D, ps, dtype = LONG[case]
+    c = _case(case, lens, new, Hkv, G, D, ps, dtype, pads=2, width=1400)
+    need = pa.paged_attn_kv4_workspace_bytes(len(lens), c["q"].shape[0], Hkv * G, Hkv, D, ps, 1400,
+                                             torch.cuda.get_device_properties(0).multi_processor_count, pa.PA_BF16)
+    assert need > 0
+    _check(pa, c)
+    _check(pa, c, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+    for less in (0, need - 1):
+        _check(pa, c, workspace=torch.empty(less, dtype=torch.uint8, device="cuda"))
+    c["table"][0, 1] = -1
+    _check(pa, c, causal=False, err=pa.ERRBIT_PAGE_RANGE)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.5, 40.0])
