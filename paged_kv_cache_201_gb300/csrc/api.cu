@@ -943,6 +943,25 @@ int check_kv4(const pa_dims *dims, bool packed, int64_t *n_tok) {
     return PA_OK;
 }
 
+// Tokens from which on a sequence's rows fill half a tile of the tcgen05 kernel.
+int kv4_run_tokens(int G) { return (64 + G - 1) / G; }
+
+// Whether paged_attn_fwd_kv4 takes its tcgen05 kernel for sequences with runs of tokens.  Both kernels are estimated, in
+// microseconds, from their measured rates: the first takes 1.4 a 128-key tile of two tiles of rows in waves of one CTA
+// a multiprocessor, the second 0.1 of a multiprocessor's time for 16 rows by 16 keys (head_dim 128).  The table's width stands
+// for lengths, which the host does not know.
+bool kv4_runs(const pa_dims *d, int64_t n_tok, bool packed, int sms) {
+    const int G = d->num_q_heads / d->num_kv_heads, tile = pa::kv4_tile_tokens(d->head_dim, G);
+    if (tile == 0 || n_tok >= (int64_t)1 << 31) return false;
+    // a batch of mostly single tokens
+    if (packed ? n_tok < 2 * (int64_t)d->batch || n_tok < kv4_run_tokens(G) : d->q_len < kv4_run_tokens(G)) return false;
+    const double keys = (double)d->bt_stride * d->page_size, width = d->head_dim / 128.0;
+    const double tiles = packed ? ceil((double)n_tok / tile) : (double)d->batch * ((d->q_len + tile - 1) / tile);
+    const double runs = ceil(tiles * d->num_kv_heads / sms) * (keys / 128 * 1.4 * width + 5);
+    const double rows = (double)n_tok * d->num_q_heads / 16 * (keys / 16) * 0.1 * width / sms + 4;
+    return runs < rows;
+}
+
 }  // namespace
 
 int64_t paged_attn_kv4_workspace_bytes(const pa_dims *dims, int packed, int num_sms) {
@@ -956,6 +975,7 @@ int64_t paged_attn_kv4_workspace_bytes(const pa_dims *dims, int packed, int num_
     static const int32_t some = 0;
     sp.f.q_start = packed ? &some : nullptr;  // only whether there is one counts
     sp.n_tok = n_tok;
+    if (kv4_runs(dims, n_tok, packed != 0, num_sms)) return 0;
     return pa::kv4_workspace_bytes(sp, num_sms);
 }
 
@@ -978,7 +998,16 @@ int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table
     sp.n_tok = n_tok;
     sp.ws = workspace;
     sp.ws_bytes = workspace_bytes;
-    return cuda_status(pa::launch_kv4_mma(sp, dims->dtype, device_sm_count(), static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Sequences with 64 rows or more go to the tcgen05 kernel where that is expected to be faster; in a packed batch both
+    // kernels find theirs from q_start.
+    if (kv4_runs(dims, n_tok, q_start != nullptr, device_sm_count())) {
+        sp.group_min = kv4_run_tokens(sp.f.G);
+        sp.by_seq = q_start && (int64_t)dims->batch * (sp.group_min - 1) < n_tok;
+        rc = cuda_status(pa::launch_kv4_tc05(sp, dims->dtype, st));
+        if (rc != PA_OK || !q_start || sp.group_min <= 1) return rc;  // no shorter run
+    }
+    return cuda_status(pa::launch_kv4_mma(sp, dims->dtype, device_sm_count(), st));
 }
 
 int paged_attn_fork(const int32_t *parents, const int32_t *children, const int32_t *prefix_lens, int n,

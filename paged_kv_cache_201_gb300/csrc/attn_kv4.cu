@@ -26,8 +26,8 @@
 #include <type_traits>
 
 #include "kv4.cuh"
+#include "kv4_tile.cuh"
 #include "mma_common.cuh"
-#include "sparse_common.cuh"
 
 namespace pa {
 
@@ -36,69 +36,6 @@ using namespace mmac;
 namespace {
 
 constexpr int kBlockKeys = 16, kStepKeys = 32;
-constexpr float kRefBelow = 11.f, kRefMost = 15.f;
-constexpr float kLeastFactor = 0x1p-100f;  // a scale of 0 leaves this: kNegInf times it is still no NaN, and any sum times it 0
-constexpr float kNoRef = -3e38f;  // before the first key; finite, so that kNegInf - ref is no NaN
-
-struct Kv4Params {
-    SparseParams s;
-    int S;         // CTAs that share a unit's keys: a cluster, or with part_out a grid's
-    float *part_out, *part_state;  // [S, rows of q x heads, D] and [S, rows, 2] (reference, sum) for the second launch
-    int TT, HT;    // tokens of a unit; head tiles of a kv head
-    int seq_tiles; // tiles of every sequence: a uniform batch, or the short runs of a packed one (0: by rows of q)
-};
-
-// A unit's tokens: cnt of sequence b from its token i on; q0 the sequence's first row of q, n its tokens.
-struct Tile {
-    int b, n, i, cnt;
-    long long q0;
-};
-
-// Packed batches: sequence b's tiles are q_start[b] / TT + b and on, which leaves room for all of them; with one
-// token a tile they are its rows.
-__device__ __forceinline__ Tile find_tile(const Kv4Params &p, int tile, int lane) {
-    const FwdParams &f = p.s.f;
-    Tile u{0, 0, 0, 0, 0};
-    if (p.seq_tiles) {
-        u.b = tile / p.seq_tiles;
-        u.i = (tile - u.b * p.seq_tiles) * p.TT;
-        if (!f.q_start) {
-            u.n = f.Sq;
-            u.q0 = (long long)u.b * f.Sq;
-            u.cnt = min(p.TT, u.n - u.i);
-            return u;
-        }
-    }
-    auto key = [&](int b, int q) { return p.TT == 1 ? q : max(q, 0) / p.TT + b; };
-    if (!p.seq_tiles) {
-        int lo = 0, hi = f.B;  // key(lo) <= tile < key(hi)
-        const int guess = min(p.TT == 1 ? tile : tile - tile / (p.TT + 1), f.B - 1);  // a token a sequence
-        if (key(guess, __ldg(f.q_start + guess)) <= tile) {
-            lo = guess;
-            if (key(guess + 1, __ldg(f.q_start + guess + 1)) > tile) hi = lo + 1;
-        } else {
-            hi = max(guess, 1);
-        }
-        while (hi - lo > 1) {  // 31 borders a trip
-            const int step = (hi - lo + 31) / 32;
-            const int b = lo + (lane + 1) * step;
-            const bool below = b < hi && key(b, __ldg(f.q_start + b)) <= tile;
-            const int k = __popc(__ballot_sync(0xffffffffu, below));
-            hi = min(hi, lo + (k + 1) * step);
-            lo += k * step;
-        }
-        u.b = lo;
-    }
-    const int q0 = __ldg(f.q_start + u.b), q1 = __ldg(f.q_start + u.b + 1);
-    if (q0 < 0 || q1 < q0 || q1 > p.s.n_tok) return u;
-    u.q0 = q0;
-    u.n = q1 - q0;
-    if (!p.seq_tiles) u.i = (tile - key(u.b, q0)) * p.TT;
-    if (u.i < 0 || (p.s.group_min && u.n >= p.s.group_min)) return u;  // malformed, or the other kernel's
-    u.cnt = min(p.TT, u.n - u.i);
-    return u;
-}
-
 // A unit: up to R rows r = token x heads + head of tile u and kv head kvh.
 struct Unit {
     Tile u;

@@ -161,6 +161,10 @@ cudaError_t launch_kv4_rows(const Kv4RowsParams &p, int dtype, int D, cudaStream
 // Attention over a 4-bit pool (p.f.k_cache), bf16/f16 queries: mma.sync, a sequence's keys shared by several CTAs when
 // there are few rows.
 cudaError_t launch_kv4_mma(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
+// Runs of tokens on tcgen05: head_dim 64 / 128, G <= 128; with group_min, the packed batch's sequences of so many tokens.
+// kv4_tile_tokens: tokens of one CTA (0: not for this shape).
+int kv4_tile_tokens(int D, int G);
+cudaError_t launch_kv4_tc05(const SparseParams &p, int dtype, cudaStream_t stream);
 long long kv4_workspace_bytes(const SparseParams &p, int sms);  // what lets it share few units' keys out further
 
 // ---------------------------------------------------------------- pages of a cache

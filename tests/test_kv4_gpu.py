@@ -212,6 +212,40 @@ def test_uniform_and_offsets(pa, causal):
     _check(pa, c, causal, q_offset=[-9, 3, 100, -3])
 
 
+RUNS = [([1500, 900], [300, 200], 2, 8, 128, 16, "bf16"), ([1100, 700, 130], [129, 64, 130], 2, 4, 128, 64, "f16"),
+        ([2000, 64, 9, 800], [500, 64, 1, 33], 3, 3, 64, 32, "bf16"), ([1000], [257], 1, 24, 64, 16, "f16"),
+        ([700, 300], [70, 90], 1, 100, 128, 16, "bf16"), ([2100, 1800, 5, 900], [700, 1, 5, 300], 2, 1, 128, 16, "f16"),
+        ([1300, 0, 640], [400, 10, 0], 2, 16, 128, 32, "bf16")]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", range(len(RUNS)))
+def test_runs(pa, case, causal):
+    """Prompt chunks over longer caches (tcgen05), beside single tokens and short runs; rows behind the last
+    sequence; tiles that end inside a page and inside a token's heads."""
+    lens, new, Hkv, G, D, ps, dtype = RUNS[case]
+    _check(pa, _case(case + 50, lens, new, Hkv, G, D, ps, dtype, pads=5), causal)
+
+
+@pytest.mark.parametrize("case", [(128, 8, "bf16"), (64, 4, "f16")])
+def test_uniform_runs(pa, case):
+    """Also with tokens that see nothing, a part, or past the end; a negative scale, none, and scores in the thousands;
+    pages outside the pool; strided queries."""
+    import torch
+    D, G, dtype = case
+    c = _case(D, [900, 1200], [200, 200], 2, G, D, 16, dtype)
+    _check(pa, c, packed=False)
+    _check(pa, c, q_offset=[-70, 1100], packed=False)
+    for scale in (-0.4, 0.0, 30.0):
+        _check(pa, c, scale=scale, packed=False)
+    T, Hq, _ = c["q"].shape
+    wide = torch.randn((T, Hq + 4, D), device="cuda").to(c["q"].dtype)
+    wide[:, :Hq] = c["q"]
+    _check(pa, c, q=wide[:, :Hq])
+    c["table"][0, 3], c["table"][1, 70] = -1, 10**8
+    _check(pa, c, packed=False, err=pa.ERRBIT_PAGE_RANGE)
+
+
 LONG = [([9000], [1], 1, 4, 128, 16, "bf16"), ([5000, 33], [2, 1], 2, 8, 64, 64, "f16"), ([3000], [1], 1, 2, 256, 32, "bf16"),
         ([100], [1], 1, 4, 128, 16, "bf16"), ([20000, 0, 700], [3, 1, 0], 1, 8, 128, 32, "f16")]
 
