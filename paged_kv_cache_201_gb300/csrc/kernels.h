@@ -70,13 +70,18 @@ cudaError_t launch_gather(const void *cache, const int32_t *block_table, const i
 struct SmemLimit {
     std::atomic<uint64_t> done[2];
     cudaError_t raise(const void *kern, size_t bytes) {
+        return once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    }
+    // The same for clusters of more than eight CTAs.
+    cudaError_t allow_wide_clusters(const void *kern) { return once(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); }
+    cudaError_t once(const void *kern, cudaFuncAttribute attr, int value) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
         const bool known = dev >= 0 && dev < 128;
         const uint64_t bit = 1ull << (dev & 63);
         if (known && (done[dev >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        e = cudaFuncSetAttribute(kern, attr, value);
         if (e == cudaSuccess && known) done[dev >> 6].fetch_or(bit, std::memory_order_release);
         return e;
     }

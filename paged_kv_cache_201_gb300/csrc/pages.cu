@@ -18,7 +18,8 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kMaxCtas = 8;
+constexpr int kMaxCtas = 8, kWideCtas = 16;
+constexpr int kUsed = 1, kFree = 2;  // marks of a page
 constexpr int kPer = PA_STEP_MAX_BATCH / kThreads;  // requests of a thread at most
 
 struct Pair {
@@ -78,25 +79,38 @@ __device__ __forceinline__ int pages_of(const PagesParams &p, int len, bool &cli
 }
 
 // Places e = 0 .. total - 1 of the lists, place e the (e - s_start[i])-th of list i with s_start[i] <= e < s_start[i + 1].
-// This warp's run of them, 32 at a time: f(e, i, j, live) with every lane of the warp.
-template <typename F>
-__device__ __forceinline__ void for_places(const int *s_start, int n, int total, int warp_all, int warps_all, F f) {
+// The list of place e, none before lo: mostly lo or the next.
+__device__ __forceinline__ int list_of(const int *s_start, int n, int e, int lo) {
+    if (lo + 1 >= n || s_start[lo + 1] > e) return lo;
+    if (++lo + 1 >= n || s_start[lo + 1] > e) return lo;
+    int hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= e)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// A warp's run of the places, PT at a time to a lane: load(k, i, j) for all of them, then use(k, live) for all.
+template <int PT, typename L, typename U>
+__device__ __forceinline__ void for_places(const int *s_start, int n, int total, int warp_all, int warps_all, L load, U use) {
     const int run = ((total + warps_all - 1) / warps_all + 31) & ~31;
     const int e0 = (int)min((long long)warp_all * run, (long long)total), e1 = (int)min((long long)e0 + run, (long long)total);
     int lo = 0;
-    for (int first = e0; first < e1; first += 32) {
-        const int e = first + (threadIdx.x & 31);
-        const bool live = e < e1;
-        int hi = n;
-        if (live)
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_start[mid] <= e)
-                    lo = mid;
-                else
-                    hi = mid;
+    for (int first = e0; first < e1; first += 32 * PT) {
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            const int e = first + 32 * k + (threadIdx.x & 31);
+            if (e < e1) {
+                lo = list_of(s_start, n, e, lo);
+                load(k, lo, e - s_start[lo]);
             }
-        f(e, lo, live ? e - s_start[lo] : 0, live);
+        }
+#pragma unroll
+        for (int k = 0; k < PT; ++k) use(k, first + 32 * k + (int)(threadIdx.x & 31) < e1);
     }
 }
 
@@ -206,15 +220,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_fork_kernel(const Page
             if (k < mine && len[k] >= 0) p.lens_out[chi[k]] = len[k];
     }
     // the full pages' entries; no row that is read here is written (a child's length was 0)
-    for_places(s_start, p.n, total.b, rank * kWarps + (tid >> 5), ctas * kWarps, [&](int, int i, int j, bool live) {
-        if (!live) return;
-        const int id = __ldg(p.block_table + (long long)s_row[i] * p.W + j);
-        p.block_table[(long long)s_child[i] * p.W + j] = id;
-        if (id >= 0 && id < p.num_pages)
-            atomicAdd(p.shares + id, 1);
-        else
-            bad_page = true;
-    });
+    constexpr int PT = 8;
+    int id[PT];
+    int32_t *to[PT];
+    for_places<PT>(
+        s_start, p.n, total.b, rank * kWarps + (tid >> 5), ctas * kWarps,
+        [&](int k, int i, int j) {
+            id[k] = __ldg(p.block_table + (long long)s_row[i] * p.W + j);
+            to[k] = p.block_table + (long long)s_child[i] * p.W + j;
+        },
+        [&](int k, bool live) {
+            if (!live) return;
+            *to[k] = id[k];
+            if (id[k] >= 0 && id[k] < p.num_pages)
+                atomicAdd(p.shares + id[k], 1);
+            else
+                bad_page = true;
+        });
     if (refused) atomicOr(p.err, (unsigned int)PA_ERRBIT_REFUSED);
     if (clipped) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
     if (bad_page) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
@@ -227,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
     int *s_named = s_row + p.n;                // [B] the first request that names a row
     __shared__ Pair warp_sums[kWarps];
     __shared__ __align__(8) Pair s_warp[kWarps];
-    const int tid = threadIdx.x, ctas = gridDim.x, rank = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x, rank = blockIdx.x;
     const int warp_all = rank * kWarps + (tid >> 5), warps_all = ctas * kWarps;
     const int per = (p.n + kThreads - 1) / kThreads;
     const int i0 = min(tid * per, p.n), mine = min(per, p.n - i0);
@@ -274,52 +296,86 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
         for (int k = 0; k < PER; ++k)
             if (row[k] >= 0) p.lens_out[row[k]] = 0;
     }
-    auto page_at = [&](int i, int j) { return __ldg(p.block_table + (long long)s_row[i] * p.W + j); };
-    auto in_pool = [&](int id) { return id >= 0 && id < p.num_pages; };
-    // an owner less for every place
-    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int, int i, int j, bool live) {
-        const int id = live ? page_at(i, j) : -1;
-        if (in_pool(id)) atomicSub(p.shares + id, 1);
-        bad_page |= live && !in_pool(id);
-    });
-    cluster_barrier();
-    // the first place of every page that is free now
-    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int e, int i, int j, bool live) {
-        const int id = live ? page_at(i, j) : -1;
-        if (in_pool(id) && __ldcg(p.shares + id) < 0) atomicMin(p.shares + id, INT_MIN + e);
-    });
-    cluster_barrier();
-    Pair n_mine{0, 0}, pushed;
-    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int e, int i, int j, bool live) {
-        const int id = live ? page_at(i, j) : -1;
-        n_mine.a += __popc(__ballot_sync(0xffffffffu, in_pool(id) && __ldcg(p.shares + id) == INT_MIN + e));
-    });
-    int at = cluster_scan(n_mine, s_warp, ctas, rank, pushed).a;
-    for_places(s_start, p.n, total.a, warp_all, warps_all, [&](int e, int i, int j, bool live) {
-        const int id = live ? page_at(i, j) : -1;
-        const bool push = in_pool(id) && __ldcg(p.shares + id) == INT_MIN + e;
-        const unsigned all = __ballot_sync(0xffffffffu, push);
-        if (push) {
-            const long long to = (long long)F + pushed.a - 1 - (at + __popc(all & ((1u << (tid & 31)) - 1)));
-            p.shares[id] = 0;
-            if (to < p.free_cap)
-                p.free_pages[to] = id;
-            else
-                refused = true;
+    // Rounds of at most PT places a lane, the last places first, as the rows end one after the other: a page is pushed in
+    // the round that takes its last owner.  A page that nobody shares needs no count.
+    constexpr int PT = 16;
+    const int round = warps_all * 32 * PT;
+    long long top = F;  // the stack's
+    for (int r = (total.a - 1) / round; r >= 0 && total.a > 0; --r) {
+        const int first = r * round, size = min(round, total.a - first);
+        const int run = ((size + warps_all - 1) / warps_all + 31) & ~31;  // of a warp, at most 32 PT
+        const int e0 = first + min(warp_all * run, size) + lane, e1 = first + min(warp_all * run + run, size);
+        int id[PT], before[PT];
+        int lo = 0;
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            const int e = e0 + 32 * k;
+            id[k] = -1;
+            if (e >= e1) continue;
+            lo = list_of(s_start, p.n, e, lo);
+            id[k] = __ldg(p.block_table + (long long)s_row[lo] * p.W + e - s_start[lo]);
+            if (id[k] < 0 || id[k] >= p.num_pages) {
+                bad_page = true;
+                id[k] = -1;
+            }
         }
-        at += __popc(all);
-    });
-    if (rank == 0 && tid == 0) *p.free_left = (int)min((long long)F + pushed.a, (long long)p.free_cap);
+        unsigned push = 0, shared = 0;  // bits of this lane's places
+#pragma unroll
+        for (int k = 0; k < PT; ++k) before[k] = id[k] >= 0 ? __ldcg(p.shares + id[k]) : 0;
+#pragma unroll
+        for (int k = 0; k < PT; ++k)
+            if (id[k] >= 0) (before[k] == 0 ? push : shared) |= 1u << k;
+        cluster_barrier();  // every count is read as it was
+#pragma unroll
+        for (int k = 0; k < PT; ++k)
+            if (shared >> k & 1) atomicSub(p.shares + id[k], 1);
+        cluster_barrier();
+        // the first place of every page that is free now
+#pragma unroll
+        for (int k = 0; k < PT; ++k)
+            if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            if ((shared >> k & 1) && before[k] >= 0) shared &= ~(1u << k);
+            if (shared >> k & 1) atomicMin(p.shares + id[k], INT_MIN + e0 + 32 * k);
+        }
+        cluster_barrier();
+#pragma unroll
+        for (int k = 0; k < PT; ++k)
+            if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
+        Pair n_mine{0, 0}, pushed;
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            if ((shared >> k & 1) && before[k] == INT_MIN + e0 + 32 * k) push |= 1u << k;
+            n_mine.a += __popc(__ballot_sync(0xffffffffu, push >> k & 1));
+        }
+        int at = cluster_scan(n_mine, s_warp, ctas, rank, pushed).a;
+        top += pushed.a;
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            const unsigned all = __ballot_sync(0xffffffffu, push >> k & 1);
+            if (push >> k & 1) {
+                const long long to = top - 1 - (at + __popc(all & ((1u << lane) - 1)));
+                if (shared >> k & 1) p.shares[id[k]] = 0;
+                if (to < p.free_cap)
+                    p.free_pages[to] = id[k];
+                else
+                    refused = true;
+            }
+            at += __popc(all);
+        }
+        cluster_barrier();  // the counts of the next round are this one's; s_warp has been read
+    }
+    if (rank == 0 && tid == 0) *p.free_left = (int)min(top, (long long)p.free_cap);
     if (refused) atomicOr(p.err, (unsigned int)PA_ERRBIT_REFUSED);
     if (clipped) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
     if (bad_page) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
-    cluster_barrier();  // the peers have read this CTA's counts
 }
 
 // The used pages to the pool's start.  With U(x) the used pages at or above x and F(x) the free ones below, the first x
 // with F(x) >= U(x) has F(x) = U(x) (one of the two moves by one from page to page): below it every free page takes one
-// of the used pages above, and what lies at or above it and was used or free is free.  Marks (1 used, 2 free) stand in
-// page_map until its values do.
+// of the used pages above, and what lies at or above it and was used or free is free.  Marks stand in page_map until its
+// values do.
 template <int PER>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const PagesParams p) {
     extern __shared__ int sm[];
@@ -359,32 +415,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
     }
     for (long long x = tid_all; x < P; x += all) __stcg(p.page_map + x, 0);
     cluster_barrier();
-    for (long long x = tid_all; x < F; x += all) {
-        const int id = __ldg(p.free_pages + x);
-        if (in_pool(id))
-            refused |= atomicOr(p.page_map + id, 2) != 0;
-        else
-            bad_page = true;
-    }
-    cluster_barrier();
-    for_places(s_start, p.B, total.a, warp_all, warps_all, [&](int, int i, int j, bool live) {
-        const int id = live ? __ldcg(p.block_table + (long long)i * p.W + j) : -1;
-        if (in_pool(id)) {
-            refused |= __ldcg(p.page_map + id) == 2;
-            __stcg(p.page_map + id, 1);
+    constexpr int PT = 4;
+    for (long long x0 = tid_all; x0 < F; x0 += all * PT) {
+        int id[PT];
+#pragma unroll
+        for (int k = 0; k < PT; ++k) id[k] = x0 + k * all < F ? __ldg(p.free_pages + x0 + k * all) : 0x7fffffff;
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            if (x0 + k * all >= F) continue;
+            if (in_pool(id[k]))
+                refused |= (atomicOr(p.page_map + id[k], kFree) & kFree) != 0;
+            else
+                bad_page = true;
         }
-        bad_page |= live && !in_pool(id);
-    });
+    }
+    int ids[PT];
+    int32_t *entry[PT];
+    for_places<PT>(
+        s_start, p.B, total.a, warp_all, warps_all,
+        [&](int k, int i, int j) { ids[k] = __ldcg(p.block_table + (long long)i * p.W + j); },
+        [&](int k, bool live) {
+            if (!live) return;
+            if (in_pool(ids[k]))
+                atomicOr(p.page_map + ids[k], kUsed);
+            else
+                bad_page = true;
+        });
     cluster_barrier();
     // every warp's run of pages: its used (a) and free (b) ones, and those of the runs before
     const int seg = (int)(((long long)P + warps_all - 1) / warps_all + 31) & ~31;
     const int x0 = (int)min((long long)warp_all * seg, (long long)P), x1 = (int)min((long long)x0 + seg, (long long)P);
     auto marks = [&](int x, unsigned &used, unsigned &idle) {
         const int m = x + lane < x1 ? __ldcg(p.page_map + x + lane) : 0;
-        used = __ballot_sync(0xffffffffu, m == 1);
-        idle = __ballot_sync(0xffffffffu, m == 2);
+        refused |= m == (kUsed | kFree);
+        used = __ballot_sync(0xffffffffu, m & kUsed);
+        idle = __ballot_sync(0xffffffffu, m == kFree);
     };
     Pair n_mine{0, 0};
+#pragma unroll 4
     for (int x = x0; x < x1; x += 32) {
         unsigned used, idle;
         marks(x, used, idle);
@@ -418,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
     const int border = s_border[0], n_moves = s_border[1];
     // below the border U(0) - n_moves pages are used; at and above it as many are left free as there were
     int u = before.a, f = before.b;
+#pragma unroll 4
     for (int x = x0; x < x1; x += 32) {
         unsigned used, idle;
         marks(x, used, idle);
@@ -430,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
             if (is_used) p.moves[2 * (ku - (total.a - n_moves))] = id;
             p.free_pages[total.b - 1 - (ku - (total.a - n_moves) + kf - n_moves)] = id;
         }
-        if (id < x1) __stcg(p.page_map + id, id);
+        // a page that moves: which move it is, until its new id is known
+        if (id < x1) __stcg(p.page_map + id, is_used && id >= border ? ~(ku - (total.a - n_moves)) : id);
         u += __popc(used);
         f += __popc(idle);
     }
@@ -445,14 +515,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
         p.shares[to] = p.shares[from];
         p.shares[from] = 0;
     }
-    cluster_barrier();
-    for_places(s_start, p.B, s_start[p.B], warp_all, warps_all, [&](int, int i, int j, bool live) {
-        int32_t *entry = p.block_table + (long long)i * p.W + j;
-        const int id = live ? __ldcg(entry) : -1;
-        if (!in_pool(id)) return;
-        const int now = __ldcg(p.page_map + id);
-        if (now != id) *entry = now;
-    });
+    // beside it the tables, which find either the new id or the move
+    for_places<PT>(
+        s_start, p.B, s_start[p.B], warp_all, warps_all,
+        [&](int k, int i, int j) {
+            ids[k] = __ldcg(p.block_table + (long long)i * p.W + j);
+            entry[k] = p.block_table + (long long)i * p.W + j;
+        },
+        [&](int k, bool live) {
+            if (!live || !in_pool(ids[k])) return;
+            int now = __ldcg(p.page_map + ids[k]);
+            if (now < 0) now = __ldcg(p.moves + 2ll * ~now + 1);
+            if (now != ids[k]) *entry[k] = now;
+        });
     if (refused) atomicOr(p.err, (unsigned int)PA_ERRBIT_REFUSED);
     if (clipped) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
     if (bad_page) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
@@ -460,13 +535,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
 
 namespace {
 
+// A cluster for `work` pages at most, which the tables' width makes of rows.
+struct ClusterLimit {
+    SmemLimit smem, wide;
+};
 template <typename K>
-cudaError_t launch_cluster(K kern, SmemLimit &limit, size_t smem, size_t smem_max, long long work, const PagesParams &p,
-                           cudaStream_t stream) {
-    const cudaError_t e = limit.raise((const void *)kern, smem_max);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_cluster(K kern, ClusterLimit &limit, size_t smem, size_t smem_max, long long work, int most,
+                           const PagesParams &p, cudaStream_t stream) {
+    cudaError_t e = limit.smem.raise((const void *)kern, smem_max);
     int ctas = 1;
-    while (ctas < kMaxCtas && ctas * 2048ll < work) ctas *= 2;
+    while (ctas < most && ctas * 2048ll < work) ctas *= 2;
+    if (e == cudaSuccess && ctas > 8) e = limit.wide.allow_wide_clusters((const void *)kern);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
@@ -487,9 +567,9 @@ size_t lists_smem(long long n, long long B) { return (size_t)(2 * n + 1 + (n > B
 
 template <int PER>
 static cudaError_t launch_fork_n(const PagesParams &p, cudaStream_t stream) {
-    static SmemLimit limit;
+    static ClusterLimit limit;
     return launch_cluster(paged_attn_fork_kernel<PER>, limit, lists_smem(p.n, p.B),
-                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, p, stream);
+                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, kWideCtas, p, stream);
 }
 cudaError_t launch_fork(const PagesParams &p, cudaStream_t stream) {
     return p.n <= kThreads ? launch_fork_n<1>(p, stream) : launch_fork_n<kPer>(p, stream);
@@ -497,9 +577,9 @@ cudaError_t launch_fork(const PagesParams &p, cudaStream_t stream) {
 
 template <int PER>
 static cudaError_t launch_free_n(const PagesParams &p, cudaStream_t stream) {
-    static SmemLimit limit;
+    static ClusterLimit limit;
     return launch_cluster(paged_attn_free_kernel<PER>, limit, lists_smem(p.n, p.B),
-                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, p, stream);
+                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, kWideCtas, p, stream);
 }
 cudaError_t launch_free(const PagesParams &p, cudaStream_t stream) {
     return p.n <= kThreads ? launch_free_n<1>(p, stream) : launch_free_n<kPer>(p, stream);
@@ -507,10 +587,11 @@ cudaError_t launch_free(const PagesParams &p, cudaStream_t stream) {
 
 template <int PER>
 static cudaError_t launch_compact_n(const PagesParams &p, cudaStream_t stream) {
-    static SmemLimit limit;
+    static ClusterLimit limit;
     const long long entries = (long long)p.B * p.W;
     return launch_cluster(paged_attn_compact_kernel<PER>, limit, (size_t)(p.B + 1) * sizeof(int),
-                          ((size_t)kThreads * PER + 1) * sizeof(int), entries > p.num_pages ? entries : p.num_pages, p, stream);
+                          ((size_t)kThreads * PER + 1) * sizeof(int), entries > p.num_pages ? entries : p.num_pages, kMaxCtas, p,
+                          stream);
 }
 cudaError_t launch_compact(const PagesParams &p, cudaStream_t stream) {
     return p.B <= kThreads ? launch_compact_n<1>(p, stream) : launch_compact_n<kPer>(p, stream);
