@@ -51,11 +51,19 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair *warp_sums, Pair &total)
     return {before_a + inc.a - v.a, before_b + inc.b - v.b};
 }
 
+// All threads of the cluster; what they wrote before, everybody sees after.  One CTA needs no more than its own barrier.
+__device__ __forceinline__ void sync_all(int ctas) {
+    if (ctas == 1)
+        __syncthreads();
+    else
+        cluster_barrier();
+}
+
 // The sums of the cluster's warps before this one, from one pair a warp in every CTA's shared memory.
 __device__ __forceinline__ Pair cluster_scan(Pair mine, Pair *s_warp, int ctas, int rank, Pair &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0) s_warp[warp] = mine;
-    cluster_barrier();
+    sync_all(ctas);
     Pair before{0, 0}, all{0, 0};
     for (int c = 0; c < ctas; ++c) {
         const uint32_t at = peer_addr(smem_u32(s_warp + lane), c);
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_fork_kernel(const Page
         sum.b += len[k] >> p.ps_shift;
     }
     run = block_scan(sum, warp_sums, total);  // of the served ones: pages taken, full pages
-    cluster_barrier();                        // every CTA has read the lengths and the count
+    sync_all(ctas);                        // every CTA has read the lengths and the count
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         if (k >= mine) continue;
@@ -287,15 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
         run.a += pages[k];
     }
     if (tid == 0) s_start[p.n] = total.a;
-    cluster_barrier();  // every CTA has read the lengths and the count
-    if (rank == 0 && p.lens_out != p.seq_lens)
-        for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = p.seq_lens[b];
     __syncthreads();
-    if (rank == 0) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-            if (row[k] >= 0) p.lens_out[row[k]] = 0;
-    }
     // Rounds of at most PT places a lane, the last places first, as the rows end one after the other: a page is pushed in
     // the round that takes its last owner.  A page that nobody shares needs no count.
     constexpr int PT = 16;
@@ -325,11 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
 #pragma unroll
         for (int k = 0; k < PT; ++k)
             if (id[k] >= 0) (before[k] == 0 ? push : shared) |= 1u << k;
-        cluster_barrier();  // every count is read as it was
+        sync_all(ctas);  // every count is read as it was, and the lengths
 #pragma unroll
         for (int k = 0; k < PT; ++k)
             if (shared >> k & 1) atomicSub(p.shares + id[k], 1);
-        cluster_barrier();
+        sync_all(ctas);
         // the first place of every page that is free now
 #pragma unroll
         for (int k = 0; k < PT; ++k)
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
             if ((shared >> k & 1) && before[k] >= 0) shared &= ~(1u << k);
             if (shared >> k & 1) atomicMin(p.shares + id[k], INT_MIN + e0 + 32 * k);
         }
-        cluster_barrier();
+        sync_all(ctas);
 #pragma unroll
         for (int k = 0; k < PT; ++k)
             if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
@@ -364,9 +364,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
             }
             at += __popc(all);
         }
-        cluster_barrier();  // the counts of the next round are this one's; s_warp has been read
+        if (r > 0 || ctas > 1) sync_all(ctas);  // the counts of the next round are this one's; s_warp has been read
     }
-    if (rank == 0 && tid == 0) *p.free_left = (int)min(top, (long long)p.free_cap);
+    if (total.a == 0) sync_all(ctas);  // every CTA has read the lengths and the count
+    if (rank == 0) {
+        if (p.lens_out != p.seq_lens)
+            for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = p.seq_lens[b];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (row[k] >= 0) p.lens_out[row[k]] = 0;
+        if (tid == 0) *p.free_left = (int)min(top, (long long)p.free_cap);
+    }
     if (refused) atomicOr(p.err, (unsigned int)PA_ERRBIT_REFUSED);
     if (clipped) atomicOr(p.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
     if (bad_page) atomicOr(p.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
         s_border[0] = s_border[1] = 0;
     }
     for (long long x = tid_all; x < P; x += all) __stcg(p.page_map + x, 0);
-    cluster_barrier();
+    sync_all(ctas);
     constexpr int PT = 4;
     for (long long x0 = tid_all; x0 < F; x0 += all * PT) {
         int id[PT];
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
             else
                 bad_page = true;
         });
-    cluster_barrier();
+    sync_all(ctas);
     // every warp's run of pages: its used (a) and free (b) ones, and those of the runs before
     const int seg = (int)(((long long)P + warps_all - 1) / warps_all + 31) & ~31;
     const int x0 = (int)min((long long)warp_all * seg, (long long)P), x1 = (int)min((long long)x0 + seg, (long long)P);
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
             asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(smem_u32(s_border + 1), lane)), "r"(f) : "memory");
         }
     }
-    cluster_barrier();
+    sync_all(ctas);
     const int border = s_border[0], n_moves = s_border[1];
     // below the border U(0) - n_moves pages are used; at and above it as many are left free as there were
     int u = before.a, f = before.b;
@@ -508,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
         *p.n_moves = n_moves;
         *p.free_left = total.b;
     }
-    cluster_barrier();
+    sync_all(ctas);
     for (long long k = tid_all; k < n_moves; k += all) {
         const int from = __ldcg(p.moves + 2 * k), to = __ldcg(p.moves + 2 * k + 1);
         __stcg(p.page_map + from, to);
