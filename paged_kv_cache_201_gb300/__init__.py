@@ -691,6 +691,25 @@ def paged_attn_sparse_shares_pages(batch: int, tokens: int, num_q_heads: int, nu
     return bool(rc)
 
 
+def _device_of(t, name) -> int:
+    """The device of a CUDA tensor, which must be the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _torch()._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current CUDA device {_torch()._C._cuda_getDevice()}")
+    return dev
+
+
+def _token_stride(t, name, dev, dtype, shape) -> int:
+    """``_rows_stride`` of [tokens, heads, head_dim], with one look at what it mostly is."""
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape:
+        tok, head, one = t.stride()
+        if one == 1 and head == shape[2] and tok >= shape[1] * head:
+            return tok
+    return _rows_stride(t, name, dev, dtype, shape)
+
+
 # ----------------------------------------------------------------------------- a cache in 4 bits
 def _kv4_page_size(kv, D: int) -> int:
     """Page size of a 4-bit pool [num_pages, Hkv, 9 page_size D / 8]."""
@@ -707,14 +726,14 @@ def paged_attn_append_kv4(k_new, v_new, slots, kv, stream=None) -> None:
     type) in 4 bits into their slots (int32 [T], page * page_size + row, -1 to skip) of kv (``kv4_pool``);
     see ``paged_attn_append_kv4`` in include/paged_attn.h."""
     torch = _torch()
-    dev, dt = torch.cuda.current_device(), k_new.dtype
     if k_new.dim() != 3 or slots.dim() != 1:
         raise ValueError("k_new must be [T, Hkv, D] and slots [T]")
+    dev, dt = _device_of(k_new, "k_new"), k_new.dtype
     T, Hkv, D = rows = k_new.shape
     ps = _kv4_page_size(kv, D)
     _need(kv, "kv", dev, torch.uint8, (kv.shape[0], Hkv, kv.shape[2]))
     _need(slots, "slots", dev, torch.int32, (T,))
-    ks, vs = _rows_stride(k_new, "k_new", dev, dt, rows), _rows_stride(v_new, "v_new", dev, dt, rows)
+    ks, vs = _token_stride(k_new, "k_new", dev, dt, rows), _token_stride(v_new, "v_new", dev, dt, rows)
     dims = PaDims(1, T, Hkv, Hkv, D, ps, kv.shape[0], 0, _dtype_code(k_new))
     rc = load_library().paged_attn_append_kv4(k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), ks, vs,
                                               kv.data_ptr(), dims, _stream(stream))
@@ -726,9 +745,9 @@ def paged_attn_gather_kv4(kv, slots, k_out, v_out, stream=None) -> None:
     """The values of the rows in slots (int32 [T]; -1: zeros) of a 4-bit pool into k_out and v_out
     [T, Hkv, D], any float type; see ``paged_attn_gather_kv4`` in include/paged_attn.h."""
     torch = _torch()
-    dev, dt = torch.cuda.current_device(), k_out.dtype
     if k_out.dim() != 3 or slots.dim() != 1:
         raise ValueError("k_out must be [T, Hkv, D] and slots [T]")
+    dev, dt = _device_of(k_out, "k_out"), k_out.dtype
     T, Hkv, D = rows = k_out.shape
     ps = _kv4_page_size(kv, D)
     _need(kv, "kv", dev, torch.uint8, (kv.shape[0], Hkv, kv.shape[2]))
@@ -743,6 +762,7 @@ def paged_attn_gather_kv4(kv, slots, k_out, v_out, stream=None) -> None:
 
 
 _sms: dict = {}  # device -> multiprocessors
+_kv4_sizes: dict = {}  # shapes of a call -> workspace bytes
 
 
 def _sm_count(dev: int) -> int:
@@ -772,7 +792,7 @@ def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, ou
     [B + 1], in f16 or bf16; out as q (dense), lse without D or None.  workspace: a uint8 tensor; without one, what the
     shape makes use of is taken from torch's caching allocator for the call."""
     torch = _torch()
-    i32, dev, dt = torch.int32, torch.cuda.current_device(), q.dtype
+    i32, dev, dt = torch.int32, _device_of(q, "q"), q.dtype
     if block_table.dim() != 2 or q.dim() != (4 if q_start is None else 3):
         raise ValueError("block_table must be [B, W]; q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start")
     B, W = bw = block_table.shape
@@ -789,14 +809,20 @@ def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, ou
     _need(seq_lens, "seq_lens", dev, i32, (B,))
     if q_offset is not None:
         _need(q_offset, "q_offset", dev, i32, (B,))
-    stride = _rows_stride(q, "q", dev, dt, shape)
+    stride = 0 if q.is_contiguous() else _rows_stride(q, "q", dev, dt, shape)
     _need(out, "out", dev, dt, shape)
     if lse is not None:
         _need(lse, "lse", dev, torch.float32, shape[:-1])
     dims = PaDims(B, shape[-3], Hq, kv.shape[1], D, ps, kv.shape[0], W, _dtype_code(q), stride)
     lib = load_library()
     if workspace is None:
-        size = lib.paged_attn_kv4_workspace_bytes(dims, 0 if q_start is None else 1, _sm_count(dev))
+        key = (dev, dt, shape, kv.shape, W, q_start is None)
+        size = _kv4_sizes.get(key)
+        if size is None:
+            if len(_kv4_sizes) >= 4096:
+                _kv4_sizes.clear()
+            size = lib.paged_attn_kv4_workspace_bytes(dims, 0 if q_start is None else 1, _sm_count(dev))
+            _kv4_sizes[key] = size
         if size > 0:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
             _record(stream, workspace)
@@ -832,7 +858,7 @@ def paged_attn_fork(parents, children, block_table, seq_lens, lens_out, page_sha
     ``paged_attn_copy_pages``.  See ``paged_attn_fork`` in include/paged_attn.h; every tensor int32 on the device,
     lens_out may be seq_lens and free_left free_count."""
     torch = _torch()
-    i32, dev = torch.int32, torch.cuda.current_device()
+    i32, dev = torch.int32, _device_of(block_table, "block_table")
     if parents.dim() != 1:
         raise ValueError("parents must be [n]")
     n = parents.shape[0]
@@ -858,7 +884,7 @@ def paged_attn_free(rows, block_table, seq_lens, lens_out, page_shares, free_pag
     free_pages.  See ``paged_attn_free`` in include/paged_attn.h; every tensor int32 on the device, lens_out
     may be seq_lens and free_left free_count."""
     torch = _torch()
-    i32, dev = torch.int32, torch.cuda.current_device()
+    i32, dev = torch.int32, _device_of(block_table, "block_table")
     if rows.dim() != 1:
         raise ValueError("rows must be [n]")
     B, W, F, P = _pages_args(block_table, seq_lens, page_shares, free_pages, free_count, dev)
@@ -880,7 +906,7 @@ def paged_attn_compact(block_table, seq_lens, page_shares, free_pages, free_coun
     ``paged_attn_copy_pages``; page_map [num_pages] holds every page's new id.  See ``paged_attn_compact`` in
     include/paged_attn.h; every tensor int32 on the device."""
     torch = _torch()
-    i32, dev = torch.int32, torch.cuda.current_device()
+    i32, dev = torch.int32, _device_of(block_table, "block_table")
     B, W, F, P = _pages_args(block_table, seq_lens, page_shares, free_pages, free_count, dev)
     _need(moves, "moves", dev, i32, (P // 2, 2))
     _need(n_moves, "n_moves", dev, i32, (1,))
@@ -898,7 +924,7 @@ def paged_attn_copy_pages(pools, pairs, n_pairs=None, stream=None) -> None:
     num_pages): pairs (int32 [n, 2], (from, to); a pair with a -1 is passed over), the first n_pairs [1] of
     them if given.  See ``paged_attn_copy_pages`` in include/paged_attn.h."""
     torch = _torch()
-    dev = torch.cuda.current_device()
+    dev = _device_of(pairs, "pairs")
     if pairs.dim() != 2:
         raise ValueError("pairs must be [n, 2]")
     n = len(pools)

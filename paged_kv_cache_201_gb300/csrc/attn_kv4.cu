@@ -649,6 +649,7 @@ cudaError_t launch_kv4(Kv4Params p, const Plan &a, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
     cfg.numAttrs = second_launch_attrs(attr, a.grid ? 1 : a.S, p.s.group_min != 0);
+    if (cfg.numAttrs == 1 && (a.grid || a.S == 1)) cfg.numAttrs = 0;  // no cluster: a plain launch costs the host less
     e = cudaLaunchKernelEx(&cfg, kern, p, ps_shift);
     if (e != cudaSuccess || !a.grid) return e;
     cfg.gridDim = dim3((unsigned)(a.units * R));

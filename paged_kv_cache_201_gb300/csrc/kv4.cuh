@@ -30,11 +30,24 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return __half2float(__ushort_as_half((unsigned short)(min(byte, kMaxScaleByte) << 7)));
 }
 
-// The scale byte of 16 elements whose largest magnitude is a: a / 7 rounded to nearest even.  The division is
-// rounded too, but never onto a border: a border has five significant bits, and where a / 7 lies beside one,
-// a is at least a unit in its last place off seven times it, which is more than half a unit of the quotient.
+// x / d rounded to nearest even, or beside it by less than 2^-45 of the quotient before its one rounding: hi is 1 / d
+// in float32 and lo what that lacks.  Where the exact quotient is a border between two results (a number of at most five
+// significant bits), so is this; where it lies beside one, it is more than half a unit in the last place off it (x
+// is a unit off d times the border, which has at most nine significant bits, and d < 8 in the units of its exponent), and
+// stays on its side.
+struct Reciprocal {
+    float hi, lo;
+};
+__device__ __forceinline__ float divide(float x, Reciprocal d) { return fmaf(x, d.hi, __fmul_rn(x, d.lo)); }
+__device__ __forceinline__ Reciprocal reciprocal(float d) {
+    const float hi = __frcp_rn(d);
+    return {hi, __fmul_rn(fmaf(-hi, d, 1.f), hi)};
+}
+
+// The scale byte of 16 elements whose largest magnitude is a (not a NaN): a / 7 rounded to nearest even.
 __device__ __forceinline__ uint32_t scale_byte(float a) {
-    const float t = fminf(__fdiv_rn(a, 7.f), kMaxScale);
+    constexpr Reciprocal seventh{1.f / 7.f, (float)(1.0 / 7.0 - (double)(1.f / 7.f))};
+    const float t = fminf(divide(fminf(a, 8.f * kMaxScale), seventh), kMaxScale);
     if (t < 0x1p-14f) return (uint32_t)__float2int_rn(t * 0x1p17f);  // multiples of 2^-17
     const uint32_t u = __float_as_uint(t);
     return min(((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3), kMaxScaleByte);

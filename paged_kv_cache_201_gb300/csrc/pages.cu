@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
     int *s_named = s_row + p.n;                // [B] the first request that names a row
     __shared__ Pair warp_sums[kWarps];
     __shared__ __align__(8) Pair s_warp[kWarps];
+    __shared__ int s_any;  // rounds (from 1) whose pages somebody shares
     const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x, rank = blockIdx.x;
     const int warp_all = rank * kWarps + (tid >> 5), warps_all = ctas * kWarps;
     const int per = (p.n + kThreads - 1) / kThreads;
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
         pages[k] = row[k] >= 0 ? pages_of(p, __ldcg(p.seq_lens + row[k]), clipped) : 0;
         sum.a += pages[k];
     }
+    if (tid == 0) s_any = 0;
     Pair run = block_scan(sum, warp_sums, total);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -296,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
     }
     if (tid == 0) s_start[p.n] = total.a;
     __syncthreads();
+    if (rank == 0 && p.lens_out != p.seq_lens)  // the rows' zeros follow behind a barrier
+        for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = p.seq_lens[b];
     // Rounds of at most PT places a lane, the last places first, as the rows end one after the other: a page is pushed in
     // the round that takes its last owner.  A page that nobody shares needs no count.
     constexpr int PT = 16;
@@ -325,24 +329,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
 #pragma unroll
         for (int k = 0; k < PT; ++k)
             if (id[k] >= 0) (before[k] == 0 ? push : shared) |= 1u << k;
+        const int number = r + 1;
+        if (__any_sync(0xffffffffu, shared) && lane < ctas)
+            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(smem_u32(&s_any), lane)), "r"(number) : "memory");
         sync_all(ctas);  // every count is read as it was, and the lengths
+        if (*(volatile int *)&s_any == number) {
 #pragma unroll
-        for (int k = 0; k < PT; ++k)
-            if (shared >> k & 1) atomicSub(p.shares + id[k], 1);
-        sync_all(ctas);
-        // the first place of every page that is free now
+            for (int k = 0; k < PT; ++k)
+                if (shared >> k & 1) atomicSub(p.shares + id[k], 1);
+            sync_all(ctas);
+            // the first place of every page that is free now
 #pragma unroll
-        for (int k = 0; k < PT; ++k)
-            if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
+            for (int k = 0; k < PT; ++k)
+                if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
 #pragma unroll
-        for (int k = 0; k < PT; ++k) {
-            if ((shared >> k & 1) && before[k] >= 0) shared &= ~(1u << k);
-            if (shared >> k & 1) atomicMin(p.shares + id[k], INT_MIN + e0 + 32 * k);
+            for (int k = 0; k < PT; ++k) {
+                if ((shared >> k & 1) && before[k] >= 0) shared &= ~(1u << k);
+                if (shared >> k & 1) atomicMin(p.shares + id[k], INT_MIN + e0 + 32 * k);
+            }
+            sync_all(ctas);
+#pragma unroll
+            for (int k = 0; k < PT; ++k)
+                if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
         }
-        sync_all(ctas);
-#pragma unroll
-        for (int k = 0; k < PT; ++k)
-            if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
         Pair n_mine{0, 0}, pushed;
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
@@ -368,9 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
     }
     if (total.a == 0) sync_all(ctas);  // every CTA has read the lengths and the count
     if (rank == 0) {
-        if (p.lens_out != p.seq_lens)
-            for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = p.seq_lens[b];
-        __syncthreads();
 #pragma unroll
         for (int k = 0; k < PER; ++k)
             if (row[k] >= 0) p.lens_out[row[k]] = 0;
@@ -566,7 +572,7 @@ cudaError_t launch_cluster(K kern, ClusterLimit &limit, size_t smem, size_t smem
     attr.val.clusterDim.x = ctas;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
