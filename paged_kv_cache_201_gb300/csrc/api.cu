@@ -946,20 +946,31 @@ int check_kv4(const pa_dims *dims, bool packed, int64_t *n_tok) {
 // Tokens from which on a sequence's rows fill half a tile of the tcgen05 kernel.
 int kv4_run_tokens(int G) { return (64 + G - 1) / G; }
 
-// Whether paged_attn_fwd_kv4 takes its tcgen05 kernel for sequences with runs of tokens.  Both kernels are estimated, in
-// microseconds, from their measured rates: the first takes 1.4 a 128-key tile of two tiles of rows in waves of one CTA
-// a multiprocessor, the second 0.1 of a multiprocessor's time for 16 rows by 16 keys (head_dim 128).  The table's width stands
-// for lengths, which the host does not know.
-bool kv4_runs(const pa_dims *d, int64_t n_tok, bool packed, int sms) {
+int64_t kv4_part_bytes(const pa_dims *d, int64_t n_tok) { return n_tok * d->num_q_heads * (d->head_dim + 2) * 4; }
+
+// Whether paged_attn_fwd_kv4 takes its tcgen05 kernel for sequences with runs of tokens: 0, or the number of CTAs that
+// share a unit's keys.  Both kernels are estimated, in microseconds, from their measured rates: the first takes 1.75 a
+// 128-key tile of two tiles of rows and 4 to set up, in waves of one CTA a multiprocessor, and where CTAs share keys, 3 and
+// the time of writing and reading their parts; the second 0.08 of a multiprocessor's time for 16 rows by 16 keys (head_dim
+// 128).  The table's width stands for lengths, which the host does not know.
+int kv4_runs(const pa_dims *d, int64_t n_tok, bool packed, int sms, int64_t ws_bytes) {
     const int G = d->num_q_heads / d->num_kv_heads, tile = pa::kv4_tile_tokens(d->head_dim, G);
-    if (tile == 0 || n_tok >= (int64_t)1 << 31) return false;
+    if (tile == 0 || n_tok >= (int64_t)1 << 31) return 0;
     // a batch of mostly single tokens
-    if (packed ? n_tok < 2 * (int64_t)d->batch || n_tok < kv4_run_tokens(G) : d->q_len < kv4_run_tokens(G)) return false;
-    const double keys = (double)d->bt_stride * d->page_size, width = d->head_dim / 128.0;
+    if (packed ? n_tok < 2 * (int64_t)d->batch || n_tok < kv4_run_tokens(G) : d->q_len < kv4_run_tokens(G)) return 0;
+    const double keys = (double)d->bt_stride * d->page_size, width = d->head_dim / 128.0, steps = keys / 128;
     const double tiles = packed ? ceil((double)n_tok / tile) : (double)d->batch * ((d->q_len + tile - 1) / tile);
-    const double runs = ceil(tiles * d->num_kv_heads / sms) * (keys / 128 * 1.4 * width + 5);
-    const double rows = (double)n_tok * d->num_q_heads / 16 * (keys / 16) * 0.1 * width / sms + 4;
-    return runs < rows;
+    const double units = tiles * d->num_kv_heads, part = (double)kv4_part_bytes(d, n_tok);
+    double best = (double)n_tok * d->num_q_heads / 16 * (keys / 16) * 0.08 * width / sms + 4;
+    int S = 0;
+    for (int s = 1; s <= 16 && (s == 1 || (s * part <= (double)ws_bytes && steps >= 4 * s)); ++s) {
+        const double t = ceil(units * s / sms) * (ceil(steps / s) * 1.75 * width + 4) + (s > 1 ? 3 + 2 * s * part / 6e6 : 0);
+        if (t < best) {
+            best = t;
+            S = s;
+        }
+    }
+    return S;
 }
 
 }  // namespace
@@ -975,7 +986,8 @@ int64_t paged_attn_kv4_workspace_bytes(const pa_dims *dims, int packed, int num_
     static const int32_t some = 0;
     sp.f.q_start = packed ? &some : nullptr;  // only whether there is one counts
     sp.n_tok = n_tok;
-    if (kv4_runs(dims, n_tok, packed != 0, num_sms)) return 0;
+    const int S = kv4_runs(dims, n_tok, packed != 0, num_sms, INT64_MAX);
+    if (S > 0) return S > 1 ? S * kv4_part_bytes(dims, n_tok) : 0;
     return pa::kv4_workspace_bytes(sp, num_sms);
 }
 
@@ -1001,11 +1013,14 @@ int paged_attn_fwd_kv4(const void *q, const void *kv, const int32_t *block_table
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Sequences with 64 rows or more go to the tcgen05 kernel where that is expected to be faster; in a packed batch both
     // kernels find theirs from q_start.
-    if (kv4_runs(dims, n_tok, q_start != nullptr, device_sm_count())) {
+    if (const int S = kv4_runs(dims, n_tok, q_start != nullptr, device_sm_count(), workspace ? workspace_bytes : 0)) {
         sp.group_min = kv4_run_tokens(sp.f.G);
         sp.by_seq = q_start && (int64_t)dims->batch * (sp.group_min - 1) < n_tok;
-        rc = cuda_status(pa::launch_kv4_tc05(sp, dims->dtype, st));
-        if (rc != PA_OK || !q_start || sp.group_min <= 1) return rc;  // no shorter run
+        rc = cuda_status(pa::launch_kv4_tc05(sp, dims->dtype, S, st));
+        if (rc == PA_OK && q_start && sp.group_min > 1)  // the shorter runs
+            rc = cuda_status(pa::launch_kv4_mma(sp, dims->dtype, device_sm_count(), st));
+        if (rc == PA_OK && S > 1) rc = cuda_status(pa::launch_kv4_join_runs(sp, dims->dtype, S, st));
+        return rc;
     }
     return cuda_status(pa::launch_kv4_mma(sp, dims->dtype, device_sm_count(), st));
 }

@@ -115,32 +115,39 @@ struct Ring {
         for (int i = lane * 16; i < kBlock; i += 512)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to - lane * 16 + i), "r"(0) : "memory");
     }
+    // A block's copies, from a page's start (of this lane's codes) and, in a larger page, its row.
+    __device__ __forceinline__ void copy_block(uint32_t to, const uint8_t *page, int row) {
+        const bool my_scales = lane < 2 * kScales / 16;
+        if (PAGE16) {
+#pragma unroll
+            for (int i = 0; i < 2 * kCodes; i += 512) copy16(to + i, page + i);
+            if (my_scales) copy16(to + 2 * kCodes, page + 2 * kCodes);
+        } else {
+            const uint8_t *k = page + row * (D / 2), *v = k + v_codes;
+#pragma unroll
+            for (int i = 0; i < kCodes; i += 512) {
+                copy16(to + i, k + i);
+                copy16(to + kCodes + i, v + i);
+            }
+            if (my_scales) copy16(to + 2 * kCodes, page + scales + row * (D / kv4::kGroup));
+        }
+    }
+    __device__ __forceinline__ const uint8_t *page_at(int at) const { return from + (unsigned long long)(uint32_t)at * stride; }
     // Starts the copies of the next step into its slot, which nobody reads any more.
     __device__ __forceinline__ void fill() {
-        const bool my_scales = lane < 2 * kScales / 16;
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-            const uint32_t to = slot_at + hb * kBlock;
-            if (hb == 1 && blk + 1 >= b1) break;
-            const int at = id[PAGE16 ? hb : 0];
-            if ((uint32_t)at >= (uint32_t)p.num_pages) {
-                no_page(to);
-                continue;
-            }
-            const uint8_t *page = from + (unsigned long long)(uint32_t)at * stride;
-            if (PAGE16) {
-#pragma unroll
-                for (int i = 0; i < 2 * kCodes; i += 512) copy16(to + i, page + i);
-                if (my_scales) copy16(to + 2 * kCodes, page + 2 * kCodes);
-            } else {
-                const int row = (blk << 4) & ((1 << ps_shift) - 1);
-                const uint8_t *k = page + row * (D / 2) + hb * kCodes, *v = k + v_codes;
-#pragma unroll
-                for (int i = 0; i < kCodes; i += 512) {
-                    copy16(to + i, k + i);
-                    copy16(to + kCodes + i, v + i);
-                }
-                if (my_scales) copy16(to + 2 * kCodes, page + scales + row * (D / kv4::kGroup) + hb * kScales);
+        const uint32_t last = max((uint32_t)id[0], (uint32_t)id[kPages - 1]);
+        const int row = (blk << 4) & ((1 << ps_shift) - 1);
+        if (blk + 1 < b1 && last < (uint32_t)p.num_pages) {  // two blocks, their pages in the pool
+            copy_block(slot_at, page_at(id[0]), row);
+            copy_block(slot_at + kBlock, page_at(id[kPages - 1]), row + kBlockKeys);
+        } else {
+#pragma unroll 1
+            for (int hb = 0; hb < 2 && blk + hb < b1; ++hb) {
+                const int at = hb ? id[kPages - 1] : id[0];
+                if ((uint32_t)at < (uint32_t)p.num_pages)
+                    copy_block(slot_at + hb * kBlock, page_at(at), row + hb * kBlockKeys);
+                else
+                    no_page(slot_at + hb * kBlock);
             }
         }
         blk += 2;
@@ -319,12 +326,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         __syncwarp();
         // ---- S^T = K Q^T, the two blocks' products in turn
         float sc[2][NR][4];
-        uint32_t kw[2][2][KW], ksb[2][2];
+        uint32_t ksb[2][2];
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                lds_words<KW>(base + hb * RingT::kBlock + k_off + i * 8 * (D / 2), kw[hb][i]);
                 ksb[hb][i] = lds_bytes<KS>(base + hb * RingT::kBlock + ks_off + i * 8 * (D / 16));
             }
 #pragma unroll
@@ -340,7 +346,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
                     // the scale of word w: byte w / 2 of the lane's, in both halves
                     uint32_t s, c;
                     kv4::scale_pair(__byte_perm(ksb[hb][i], 0, 0x4040 + (w / 2) * 0x0101), s, c);
-                    kv4::unpack8(kw[hb][i][w], s, c, h[i]);
+                    // (word by word: a whole row's at once leaves too few registers, 3 us of 192)
+                    uint32_t code[1];
+                    lds_words<1>(base + hb * RingT::kBlock + k_off + i * 8 * (D / 2) + 4 * w, code);
+                    kv4::unpack8(code[0], s, c, h[i]);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -583,7 +592,7 @@ Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
     const double rows = (f.q_start ? (double)sp.n_tok / f.B : (double)f.Sq) * f.G;
     a.nr = f.D == 256 || rows <= 8 || (f.G > 16 && f.G <= 24) ? 1 : 2;
     const int R = 8 * a.nr, full = f.D == 256 ? 8 : a.nr == 2 ? 12 : 16;  // warps that fill a multiprocessor
-    const int ctas = f.D == 256 || a.nr == 1 ? 2 : 3;                     // CTAs that do otherwise
+    const int ctas = f.D == 256 ? 2 : a.nr == 2 ? 3 : 4;                  // CTAs that do otherwise
     a.HT = (f.G + R - 1) / R;
     a.TT = f.q_start && sp.n_tok <= f.B ? 1 : f.G < R ? R / f.G : 1;
     long long tiles;
@@ -666,7 +675,7 @@ cudaError_t launch_kv4_d(const Kv4Params &p, const Plan &a, cudaStream_t stream)
         return a.warps == 8 ? launch_kv4<T, D, 1, 8, 1>(p, a, stream) : launch_kv4<T, D, 1, 4, 2>(p, a, stream);
     } else {
         if (a.nr == 2) return a.warps == 12 ? launch_kv4<T, D, 2, 12, 1>(p, a, stream) : launch_kv4<T, D, 2, 4, 3>(p, a, stream);
-        return a.warps == 16 ? launch_kv4<T, D, 1, 16, 1>(p, a, stream) : launch_kv4<T, D, 1, 8, 2>(p, a, stream);
+        return a.warps == 16 ? launch_kv4<T, D, 1, 16, 1>(p, a, stream) : launch_kv4<T, D, 1, 4, 4>(p, a, stream);
     }
 }
 

@@ -121,10 +121,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float s_factor[256];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ps = 1 << ps_shift;
-    const int kvh = blockIdx.x % f.Hkv;
+    const int part = blockIdx.x % p.S, unit = blockIdx.x / p.S, kvh = unit % f.Hkv;
     let_second_start();
     RangeCheck ranges(p.s);
-    const Tile u = find_tile(p, blockIdx.x / f.Hkv, lane);
+    const Tile u = find_tile(p, unit / f.Hkv, lane);
     ranges.report(f);
     if (u.cnt <= 0) return;
     int L = max(__ldg(f.seq_lens + u.b), 0);
@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         L = f.W << ps_shift;
     }
     const int k_hi = row_key_limit(f, u.b, L, u.i + u.cnt - 1, u.n);  // the last token reaches furthest
-    const int n_tiles = (max(k_hi, 0) + 127) >> 7;
+    // this CTA's share of the 128-key tiles
+    const int all_tiles = (max(k_hi, 0) + 127) >> 7, share = (all_tiles + p.S - 1) / p.S;
+    const int tile0 = min(part * share, all_tiles), n_tiles = min(share, all_tiles - tile0);
     const int half_tokens = p.TT / 2;  // tokens of a tile of rows
 
     // shared memory: Q x2 | K x2 | V x2
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto look_up = [&](int t, int (&id)[C::kTurns]) {
 #pragma unroll
             for (int i = 0; i < C::kTurns; ++i) {
-                const int pg = (t * 128 + C::first_row(i, w)) >> ps_shift;
+                const int pg = ((tile0 + t) * 128 + C::first_row(i, w)) >> ps_shift;
                 id[i] = pg < np ? __ldg(row + pg) : -1;
             }
         };
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < C::kTurns; ++i)
                 if ((uint32_t)id[i] >= (uint32_t)f.num_pages) {
-                    if (lane == 0 && (t * 128 + C::first_row(i, w)) >> ps_shift < np)
+                    if (lane == 0 && ((tile0 + t) * 128 + C::first_row(i, w)) >> ps_shift < np)
                         atomicOr(f.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
                     id[i] = -1;
                 }
@@ -331,19 +333,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) tc05::ld_32cols(sbuf + 32u * i, s[i]);
             tc05::wait_ld();
-            if (t * 128 + 128 > all_below) {
+            const int j0 = (tile0 + t) * 128;
+            if (j0 + 128 > all_below) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (t * 128 + 32 * i + j >= lim) s[i][j] = 0xff800000u;
+                        if (j0 + 32 * i + j >= lim) s[i][j] = 0xff800000u;
             }
             float m[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                m[i] = __uint_as_float(s[i][0]);
+                m[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
-                for (int j = 1; j < 32; ++j) m[i] = fmaxf(m[i], __uint_as_float(s[i][j]));
+                for (int j = 2; j < 32; j += 2) m[i] = fmaxf(fmaxf(m[i], __uint_as_float(s[i][j])), __uint_as_float(s[i][j + 1]));
             }
             const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * factor;
             const bool over = mx > ref + kRefMost;
@@ -408,18 +411,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0u;
                 }
-                if (valid) {
+                // columns 0 1 2 .. 7 hold elements 0 4 1 5 2 6 3 7
+                auto e = [&](int i, int x) { return __uint_as_float(o[8 * i + (x < 4 ? 2 * x : 2 * x - 7)]); };
+                if (valid && p.part_out) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_out + (part * p.s.n_tok * f.Hq + row) * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        dst[2 * i] = make_float4(e(i, 0), e(i, 1), e(i, 2), e(i, 3));
+                        dst[2 * i + 1] = make_float4(e(i, 4), e(i, 5), e(i, 6), e(i, 7));
+                    }
+                } else if (valid) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(f.out) + row * D + 32 * c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // columns 0 1 2 .. 7 hold elements 0 4 1 5 2 6 3 7
-                        auto e = [&](int x) { return __uint_as_float(o[8 * i + (x < 4 ? 2 * x : 2 * x - 7)]) * inv; };
-                        dst[i] = make_uint4(MmaOp<T>::pack(e(0), e(1)), MmaOp<T>::pack(e(2), e(3)), MmaOp<T>::pack(e(4), e(5)),
-                                            MmaOp<T>::pack(e(6), e(7)));
+                        auto pk = [&](int x) { return MmaOp<T>::pack(e(i, x) * inv, e(i, x + 1) * inv); };
+                        dst[i] = make_uint4(pk(0), pk(2), pk(4), pk(6));
                     }
                 }
             }
-            if (valid && f.lse) f.lse[row] = l != 0.f ? ref * kLn2 + logf(l) : kNegInf;
+            if (valid && p.part_out)
+                *reinterpret_cast<float2 *>(p.part_state + 2 * (part * p.s.n_tok * f.Hq + row)) = make_float2(ref, l);
+            else if (valid && f.lse)
+                f.lse[row] = l != 0.f ? ref * kLn2 + logf(l) : kNegInf;
         }
     }
     tc05::fence_before_sync();
@@ -428,6 +441,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc05::fence_after_sync();
         tc05::tmem_dealloc(tmem, 512);
     }
+}
+
+// The parts of rows whose keys several CTAs shared, a warp a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_attn_kv4_join_runs_kernel(const Kv4Params p) {
+    const FwdParams &f = p.s.f;
+    const int lane = threadIdx.x & 31, unit = blockIdx.x / 32, kvh = unit % f.Hkv;
+    const Tile u = find_tile(p, unit / f.Hkv, lane);
+    const int tr = (blockIdx.x % 32) * 8 + (threadIdx.x >> 5), r = tr & 127, half_tokens = p.TT / 2;
+    const int tk = (tr >> 7) * half_tokens + r / f.G;
+    if (r >= half_tokens * f.G || tk >= u.cnt) return;
+    const long long row = (u.q0 + u.i + tk) * f.Hq + kvh * f.G + r % f.G, rows = p.s.n_tok * f.Hq;
+    const float2 *state = reinterpret_cast<const float2 *>(p.part_state) + row;
+    float M = kNoRef, sum = 0.f;
+    for (int x = 0; x < p.S; ++x) M = fmaxf(M, __ldcg(state + x * rows).x);
+    constexpr int C = D / 4;  // lanes with elements
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < p.S; ++x) {
+        const float2 st = __ldcg(state + x * rows);
+        const float k = fast_exp2(st.x - M);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_out + (x * rows + row) * D) + lane % C);
+        sum += k * st.y;
+        o.x += k * v.x, o.y += k * v.y, o.z += k * v.z, o.w += k * v.w;
+    }
+    const float inv = sum != 0.f ? 8.f / sum : 0.f;  // a NaN stays one
+    if (lane < C)
+        *reinterpret_cast<uint2 *>(static_cast<T *>(f.out) + row * D + 4 * lane) =
+            make_uint2(MmaOp<T>::pack(o.x * inv, o.y * inv), MmaOp<T>::pack(o.z * inv, o.w * inv));
+    if (lane == 0 && f.lse) f.lse[row] = sum != 0.f ? M * kLn2 + logf(sum) : kNegInf;
 }
 
 template <typename T, int D>
@@ -449,14 +492,14 @@ static cudaError_t launch_tc(const Kv4Params &p, long long units, cudaStream_t s
     }
     if (regs * kThreads < 128 * (int)(kIssueRegs + kCodeRegs) + 256 * (int)kSoftmaxRegs) return cudaErrorInvalidConfiguration;
     const FwdParams &f = p.s.f;
-    kern<<<(unsigned)units, kThreads, smem, stream>>>(p, f.ps == 16 ? 4 : f.ps == 32 ? 5 : 6, tc05::idesc_f16(false, false, 128, 128),
-                                                       tc05::idesc_f16(false, true, 128, D));
+    kern<<<(unsigned)(units * p.S), kThreads, smem, stream>>>(p, f.ps == 16 ? 4 : f.ps == 32 ? 5 : 6,
+                                                              tc05::idesc_f16(false, false, 128, 128),
+                                                              tc05::idesc_f16(false, true, 128, D));
     return cudaGetLastError();
 }
 
-int kv4_tile_tokens(int D, int G) { return D == 256 || G > 128 ? 0 : 2 * (128 / G); }
-
-cudaError_t launch_kv4_tc05(const SparseParams &sp, int dtype, cudaStream_t stream) {
+// What the launches of a call have in common; units: tiles x kv heads.
+static Kv4Params runs_params(const SparseParams &sp, int S, long long &units) {
     const FwdParams &f = sp.f;
     Kv4Params p{};
     p.s = sp;
@@ -464,12 +507,37 @@ cudaError_t launch_kv4_tc05(const SparseParams &sp, int dtype, cudaStream_t stre
     p.min_tokens = sp.group_min;
     p.TT = kv4_tile_tokens(f.D, f.G);
     p.seq_tiles = f.q_start ? 0 : (f.Sq + p.TT - 1) / p.TT;
-    const long long tiles = f.q_start ? sp.n_tok / p.TT + f.B : (long long)f.B * p.seq_tiles, units = tiles * f.Hkv;
+    p.S = S;
+    if (S > 1) {
+        p.part_out = static_cast<float *>(sp.ws);
+        p.part_state = p.part_out + S * sp.n_tok * f.Hq * f.D;
+    }
+    units = (f.q_start ? sp.n_tok / p.TT + f.B : (long long)f.B * p.seq_tiles) * f.Hkv;
+    return p;
+}
+
+int kv4_tile_tokens(int D, int G) { return D == 256 || G > 128 ? 0 : 2 * (128 / G); }
+
+cudaError_t launch_kv4_tc05(const SparseParams &sp, int dtype, int S, cudaStream_t stream) {
+    long long units;
+    const Kv4Params p = runs_params(sp, S, units);
     if (units == 0) return cudaSuccess;
-    if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (units * S > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if (dtype == PA_BF16)
-        return f.D == 64 ? launch_tc<__nv_bfloat16, 64>(p, units, stream) : launch_tc<__nv_bfloat16, 128>(p, units, stream);
-    return f.D == 64 ? launch_tc<__half, 64>(p, units, stream) : launch_tc<__half, 128>(p, units, stream);
+        return sp.f.D == 64 ? launch_tc<__nv_bfloat16, 64>(p, units, stream) : launch_tc<__nv_bfloat16, 128>(p, units, stream);
+    return sp.f.D == 64 ? launch_tc<__half, 64>(p, units, stream) : launch_tc<__half, 128>(p, units, stream);
+}
+
+cudaError_t launch_kv4_join_runs(const SparseParams &sp, int dtype, int S, cudaStream_t stream) {
+    long long units;
+    const Kv4Params p = runs_params(sp, S, units);
+    if (units == 0) return cudaSuccess;
+    if (units * 32 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    auto kern = dtype == PA_BF16
+                    ? sp.f.D == 64 ? paged_attn_kv4_join_runs_kernel<__nv_bfloat16, 64> : paged_attn_kv4_join_runs_kernel<__nv_bfloat16, 128>
+                    : sp.f.D == 64 ? paged_attn_kv4_join_runs_kernel<__half, 64> : paged_attn_kv4_join_runs_kernel<__half, 128>;
+    kern<<<(unsigned)(units * 32), 256, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace pa

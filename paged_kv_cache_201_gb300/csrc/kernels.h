@@ -168,8 +168,11 @@ cudaError_t launch_kv4_rows(const Kv4RowsParams &p, int dtype, int D, cudaStream
 cudaError_t launch_kv4_mma(const SparseParams &p, int dtype, int sms, cudaStream_t stream);
 // Runs of tokens on tcgen05: head_dim 64 / 128, G <= 128; with group_min, the packed batch's sequences of so many tokens.
 // kv4_tile_tokens: tokens of one CTA (0: not for this shape).
+// Each unit's keys may be shared by S CTAs whose parts the workspace takes (S * n_tok * Hq * (D + 2) floats) and a further
+// launch joins.
 int kv4_tile_tokens(int D, int G);
-cudaError_t launch_kv4_tc05(const SparseParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_kv4_tc05(const SparseParams &p, int dtype, int S, cudaStream_t stream);
+cudaError_t launch_kv4_join_runs(const SparseParams &p, int dtype, int S, cudaStream_t stream);
 long long kv4_workspace_bytes(const SparseParams &p, int sms);  // what lets it share few units' keys out further
 
 // ---------------------------------------------------------------- pages of a cache

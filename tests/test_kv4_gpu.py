@@ -215,7 +215,10 @@ def test_uniform_and_offsets(pa, causal):
 RUNS = [([1500, 900], [300, 200], 2, 8, 128, 16, "bf16"), ([1100, 700, 130], [129, 64, 130], 2, 4, 128, 64, "f16"),
         ([2000, 64, 9, 800], [500, 64, 1, 33], 3, 3, 64, 32, "bf16"), ([1000], [257], 1, 24, 64, 16, "f16"),
         ([700, 300], [70, 90], 1, 100, 128, 16, "bf16"), ([2100, 1800, 5, 900], [700, 1, 5, 300], 2, 1, 128, 16, "f16"),
-        ([1300, 0, 640], [400, 10, 0], 2, 16, 128, 32, "bf16")]
+        ([1300, 0, 640], [400, 10, 0], 2, 16, 128, 32, "bf16"),
+        # few tiles over many keys: several CTAs share them
+        ([7000, 300], [260, 3], 1, 8, 128, 16, "bf16"), ([5000], [200], 1, 12, 128, 32, "f16")]
+SHARED = {0, 2, 6, 7, 8}
 
 
 @pytest.mark.parametrize("causal", [True, False])
@@ -223,8 +226,16 @@ RUNS = [([1500, 900], [300, 200], 2, 8, 128, 16, "bf16"), ([1100, 700, 130], [12
 def test_runs(pa, case, causal):
     """Prompt chunks over longer caches (tcgen05), beside single tokens and short runs; rows behind the last
     sequence; tiles that end inside a page and inside a token's heads."""
+    import torch
     lens, new, Hkv, G, D, ps, dtype = RUNS[case]
-    _check(pa, _case(case + 50, lens, new, Hkv, G, D, ps, dtype, pads=5), causal)
+    c = _case(case + 50, lens, new, Hkv, G, D, ps, dtype, pads=5)
+    _check(pa, c, causal)
+    need = pa.paged_attn_kv4_workspace_bytes(len(lens), c["q"].shape[0], Hkv * G, Hkv, D, ps, c["table"].shape[1],
+                                             torch.cuda.get_device_properties(0).multi_processor_count, pa.PA_BF16)
+    assert (need > 0) == (case in SHARED)
+    if need:
+        _check(pa, c, causal, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+        _check(pa, c, causal, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
 
 
 @pytest.mark.parametrize("case", [(128, 8, "bf16"), (64, 4, "f16")])
