@@ -59,21 +59,30 @@ __device__ __forceinline__ void sync_all(int ctas) {
         cluster_barrier();
 }
 
-// The sums of the cluster's warps before this one, from one pair a warp in every CTA's shared memory.
-__device__ __forceinline__ Pair cluster_scan(Pair mine, Pair *s_warp, int ctas, int rank, Pair &total) {
+// The sums over the cluster's warps before this one, from a pair a warp, and over all of them.  warp_sums: [kWarps]; *s_cta
+// is the CTA's sum, which its peers read until the next barrier of all.
+__device__ __forceinline__ Pair cluster_scan(Pair mine, Pair *warp_sums, Pair *s_cta, int ctas, int rank, Pair &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0) s_warp[warp] = mine;
-    sync_all(ctas);
-    Pair before{0, 0}, all{0, 0};
-    for (int c = 0; c < ctas; ++c) {
-        const uint32_t at = peer_addr(smem_u32(s_warp + lane), c);
-        Pair v;
-        asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.a), "=r"(v.b) : "r"(at) : "memory");
-        all.a += v.a, all.b += v.b;
-        if (c < rank || (c == rank && lane < warp)) before.a += v.a, before.b += v.b;
-    }
-    total = {__reduce_add_sync(0xffffffffu, all.a), __reduce_add_sync(0xffffffffu, all.b)};
-    return {__reduce_add_sync(0xffffffffu, before.a), __reduce_add_sync(0xffffffffu, before.b)};
+    if (lane == 0) warp_sums[warp] = mine;
+    __syncthreads();
+    const Pair w = warp_sums[lane];  // every warp sums the warps before it
+    const bool first = lane < warp;
+    Pair before{__reduce_add_sync(0xffffffffu, first ? w.a : 0), __reduce_add_sync(0xffffffffu, first ? w.b : 0)};
+    total = {__reduce_add_sync(0xffffffffu, w.a), __reduce_add_sync(0xffffffffu, w.b)};
+    if (ctas == 1) return before;
+    if (threadIdx.x == 0) *s_cta = total;
+    cluster_barrier();
+    Pair v{0, 0};  // CTA `lane`'s
+    if (lane < ctas)
+        asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+                     : "=r"(v.a), "=r"(v.b)
+                     : "r"(peer_addr(smem_u32(s_cta), lane))
+                     : "memory");
+    total = {__reduce_add_sync(0xffffffffu, v.a), __reduce_add_sync(0xffffffffu, v.b)};
+    if (lane >= rank) v = {0, 0};
+    before.a += __reduce_add_sync(0xffffffffu, v.a);
+    before.b += __reduce_add_sync(0xffffffffu, v.b);
+    return before;
 }
 
 // Pages of a row of this length; lengths past the row's width are cut.
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
     int *s_start = sm, *s_row = sm + p.n + 1;  // [n + 1] first places, [n] rows
     int *s_named = s_row + p.n;                // [B] the first request that names a row
     __shared__ Pair warp_sums[kWarps];
-    __shared__ __align__(8) Pair s_warp[kWarps];
+    __shared__ __align__(8) Pair s_cta;
     __shared__ int s_any;  // rounds (from 1) whose pages somebody shares
     const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x, rank = blockIdx.x;
     const int warp_all = rank * kWarps + (tid >> 5), warps_all = ctas * kWarps;
@@ -358,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
             if ((shared >> k & 1) && before[k] == INT_MIN + e0 + 32 * k) push |= 1u << k;
             n_mine.a += __popc(__ballot_sync(0xffffffffu, push >> k & 1));
         }
-        int at = cluster_scan(n_mine, s_warp, ctas, rank, pushed).a;
+        int at = cluster_scan(n_mine, warp_sums, &s_cta, ctas, rank, pushed).a;
         top += pushed.a;
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
             }
             at += __popc(all);
         }
-        if (r > 0 || ctas > 1) sync_all(ctas);  // the counts of the next round are this one's; s_warp has been read
+        if (r > 0 || ctas > 1) sync_all(ctas);  // the counts of the next round are this one's; s_cta has been read
     }
     if (total.a == 0) sync_all(ctas);  // every CTA has read the lengths and the count
     if (rank == 0) {
@@ -396,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
     extern __shared__ int sm[];
     int *s_start = sm;  // [B + 1]
     __shared__ Pair warp_sums[kWarps];
-    __shared__ __align__(8) Pair s_warp[kWarps];
+    __shared__ __align__(8) Pair s_cta;
     __shared__ int s_border[2];
     const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x, rank = blockIdx.x;
     const int warp_all = rank * kWarps + (tid >> 5), warps_all = ctas * kWarps;
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
         n_mine.a += __popc(used);
         n_mine.b += __popc(idle);
     }
-    const Pair before = cluster_scan(n_mine, s_warp, ctas, rank, total);
+    const Pair before = cluster_scan(n_mine, warp_sums, &s_cta, ctas, rank, total);
     // the border: in the run where F(x) reaches U(x), which one warp of the cluster finds out for all
     if (before.b < total.a - before.a && before.b + n_mine.b >= total.a - before.a - n_mine.a) {
         int u = total.a - before.a, f = before.b, border = x0;

@@ -182,7 +182,7 @@ def _check(pa, c, causal=True, q_offset=None, scale=None, packed=True, q=None, e
     bar = STEP[c["dtype"]] * np.abs(want) + room + WEIGHT[c["dtype"]] * mass + 2.0 ** -24
     worst = np.abs(got - want)[own] / bar[own]
     assert worst.size == 0 or worst.max() <= 1, f"output off by {worst.max():.3g} of its bar"
-    worst = np.abs(got_lse - want_lse)[own] / (off + 2.0 ** -22 * np.abs(want_lse))[own]
+    worst = np.abs(got_lse[own] - want_lse[own]) / (off + 2.0 ** -22 * np.abs(want_lse))[own]
     assert worst.size == 0 or worst.max() <= 1, f"lse off by {worst.max():.3g} of its bar"
 
 
