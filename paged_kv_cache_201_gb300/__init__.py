@@ -9,6 +9,8 @@ library is an error.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -150,6 +152,27 @@ def load_library(build_if_missing: bool = False):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
+
+
+_binding = None
+
+
+def _short():
+    """The compiled short way into the 4-bit cache's and the page calls (csrc/binding.cpp): its functions check their
+    tensors, make the call and return its status, or None where an argument is not as it should be."""
+    global _binding
+    if _binding is None:
+        import torch  # noqa: F401  (its libraries, which the binding needs)
+        load_library()
+        if not os.path.exists(_build.BINDING_PATH):
+            raise RuntimeError(f"paged-attention binding not built ({_build.BINDING_PATH}); run "
+                               "paged_kv_cache_201_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader(_build.BINDING_NAME, _build.BINDING_PATH)
+        spec = importlib.util.spec_from_file_location(_build.BINDING_NAME, _build.BINDING_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
 # ----------------------------------------------------------------------------- marshalling helpers
@@ -701,15 +724,6 @@ def _device_of(t, name) -> int:
     return dev
 
 
-def _token_stride(t, name, dev, dtype, shape) -> int:
-    """``_rows_stride`` of [tokens, heads, head_dim], with one look at what it mostly is."""
-    if t.get_device() == dev and t.dtype is dtype and t.shape == shape:
-        tok, head, one = t.stride()
-        if one == 1 and head == shape[2] and tok >= shape[1] * head:
-            return tok
-    return _rows_stride(t, name, dev, dtype, shape)
-
-
 # ----------------------------------------------------------------------------- a cache in 4 bits
 def _kv4_page_size(kv, D: int) -> int:
     """Page size of a 4-bit pool [num_pages, Hkv, 9 page_size D / 8]."""
@@ -725,6 +739,9 @@ def paged_attn_append_kv4(k_new, v_new, slots, kv, stream=None) -> None:
     """Write the new tokens' K and V rows ([T, Hkv, D], possibly slices of a fused projection; any float
     type) in 4 bits into their slots (int32 [T], page * page_size + row, -1 to skip) of kv (``kv4_pool``);
     see ``paged_attn_append_kv4`` in include/paged_attn.h."""
+    rc = _short().append_kv4(k_new, v_new, slots, kv, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc, "paged_attn_append_kv4") if rc else None
     torch = _torch()
     if k_new.dim() != 3 or slots.dim() != 1:
         raise ValueError("k_new must be [T, Hkv, D] and slots [T]")
@@ -733,7 +750,7 @@ def paged_attn_append_kv4(k_new, v_new, slots, kv, stream=None) -> None:
     ps = _kv4_page_size(kv, D)
     _need(kv, "kv", dev, torch.uint8, (kv.shape[0], Hkv, kv.shape[2]))
     _need(slots, "slots", dev, torch.int32, (T,))
-    ks, vs = _token_stride(k_new, "k_new", dev, dt, rows), _token_stride(v_new, "v_new", dev, dt, rows)
+    ks, vs = _rows_stride(k_new, "k_new", dev, dt, rows), _rows_stride(v_new, "v_new", dev, dt, rows)
     dims = PaDims(1, T, Hkv, Hkv, D, ps, kv.shape[0], 0, _dtype_code(k_new))
     rc = load_library().paged_attn_append_kv4(k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), ks, vs,
                                               kv.data_ptr(), dims, _stream(stream))
@@ -744,6 +761,9 @@ def paged_attn_append_kv4(k_new, v_new, slots, kv, stream=None) -> None:
 def paged_attn_gather_kv4(kv, slots, k_out, v_out, stream=None) -> None:
     """The values of the rows in slots (int32 [T]; -1: zeros) of a 4-bit pool into k_out and v_out
     [T, Hkv, D], any float type; see ``paged_attn_gather_kv4`` in include/paged_attn.h."""
+    rc = _short().gather_kv4(kv, slots, k_out, v_out, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc, "paged_attn_gather_kv4") if rc else None
     torch = _torch()
     if k_out.dim() != 3 or slots.dim() != 1:
         raise ValueError("k_out must be [T, Hkv, D] and slots [T]")
@@ -762,7 +782,6 @@ def paged_attn_gather_kv4(kv, slots, k_out, v_out, stream=None) -> None:
 
 
 _sms: dict = {}  # device -> multiprocessors
-_kv4_sizes: dict = {}  # shapes of a call -> workspace bytes
 
 
 def _sm_count(dev: int) -> int:
@@ -791,6 +810,10 @@ def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, ou
     ``paged_attn_fwd_kv4`` in include/paged_attn.h.  q [B, Sq, Hq, D], or packed [T, Hq, D] with q_start
     [B + 1], in f16 or bf16; out as q (dense), lse without D or None.  workspace: a uint8 tensor; without one, what the
     shape makes use of is taken from torch's caching allocator for the call."""
+    rc = _short().fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, out, lse, q_start,
+                          None if stream is None else stream.cuda_stream, workspace)
+    if rc is not None:
+        return _raise(rc, "paged_attn_fwd_kv4") if rc else None
     torch = _torch()
     i32, dev, dt = torch.int32, _device_of(q, "q"), q.dtype
     if block_table.dim() != 2 or q.dim() != (4 if q_start is None else 3):
@@ -816,13 +839,7 @@ def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, ou
     dims = PaDims(B, shape[-3], Hq, kv.shape[1], D, ps, kv.shape[0], W, _dtype_code(q), stride)
     lib = load_library()
     if workspace is None:
-        key = (dev, dt, shape, kv.shape, W, q_start is None)
-        size = _kv4_sizes.get(key)
-        if size is None:
-            if len(_kv4_sizes) >= 4096:
-                _kv4_sizes.clear()
-            size = lib.paged_attn_kv4_workspace_bytes(dims, 0 if q_start is None else 1, _sm_count(dev))
-            _kv4_sizes[key] = size
+        size = lib.paged_attn_kv4_workspace_bytes(dims, 0 if q_start is None else 1, _sm_count(dev))
         if size > 0:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
             _record(stream, workspace)
@@ -857,6 +874,10 @@ def paged_attn_fork(parents, children, block_table, seq_lens, lens_out, page_sha
     their full pages; the last part of a page goes to a page of its own, listed in copies [n, 2] for
     ``paged_attn_copy_pages``.  See ``paged_attn_fork`` in include/paged_attn.h; every tensor int32 on the device,
     lens_out may be seq_lens and free_left free_count."""
+    rc = _short().fork(parents, children, block_table, seq_lens, lens_out, page_shares, free_pages, free_count,
+                       free_left, copies, page_size, prefix_lens, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc, "paged_attn_fork") if rc else None
     torch = _torch()
     i32, dev = torch.int32, _device_of(block_table, "block_table")
     if parents.dim() != 1:
@@ -883,6 +904,10 @@ def paged_attn_free(rows, block_table, seq_lens, lens_out, page_shares, free_pag
     """Give back the pages of block-table rows (int32 [n], -1: nothing): those without an owner left go onto the stack
     free_pages.  See ``paged_attn_free`` in include/paged_attn.h; every tensor int32 on the device, lens_out
     may be seq_lens and free_left free_count."""
+    rc = _short().free(rows, block_table, seq_lens, lens_out, page_shares, free_pages, free_count, free_left,
+                       page_size, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc, "paged_attn_free") if rc else None
     torch = _torch()
     i32, dev = torch.int32, _device_of(block_table, "block_table")
     if rows.dim() != 1:
@@ -905,6 +930,10 @@ def paged_attn_compact(block_table, seq_lens, page_shares, free_pages, free_coun
     and the stack, and lists (from, to) in moves [num_pages // 2, 2], n_moves [1] of them, for
     ``paged_attn_copy_pages``; page_map [num_pages] holds every page's new id.  See ``paged_attn_compact`` in
     include/paged_attn.h; every tensor int32 on the device."""
+    rc = _short().compact(block_table, seq_lens, page_shares, free_pages, free_count, moves, n_moves, page_map,
+                          page_size, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc, "paged_attn_compact") if rc else None
     torch = _torch()
     i32, dev = torch.int32, _device_of(block_table, "block_table")
     B, W, F, P = _pages_args(block_table, seq_lens, page_shares, free_pages, free_count, dev)
@@ -923,6 +952,9 @@ def paged_attn_copy_pages(pools, pairs, n_pairs=None, stream=None) -> None:
     """Copy pages within every pool of a list (dense tensors [num_pages, ...] of any type, all of one
     num_pages): pairs (int32 [n, 2], (from, to); a pair with a -1 is passed over), the first n_pairs [1] of
     them if given.  See ``paged_attn_copy_pages`` in include/paged_attn.h."""
+    rc = _short().copy_pages(pools, pairs, n_pairs, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc, "paged_attn_copy_pages") if rc else None
     torch = _torch()
     dev = _device_of(pairs, "pairs")
     if pairs.dim() != 2:

@@ -2,16 +2,19 @@
 
 ``python -m paged_kv_cache_201_gb300.build`` compiles every ``csrc/*.cu`` in
 parallel with nvcc and links ``_build/libpaged_attn_gb300.so`` against the
-shared CUDA runtime.
+shared CUDA runtime; beside them it compiles ``csrc/binding.cpp``, the short
+way from Python into some of the calls, against torch's headers.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libpaged_attn_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_NAME = "_paged_attn_binding"
+BINDING_PATH = os.path.join(BUILD_DIR, BINDING_NAME + ".so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -53,11 +59,43 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _binding_flags():
+    """Include and link flags of torch, CUDA and Python, without importing torch."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    libs = [os.path.join(torch, "lib"), os.path.join(cuda, "lib64")]
+    return [f"-I{d}" for d in inc], [f for d in libs for f in (f"-L{d}", f"-Wl,-rpath,{d}")] + [
+        "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-lcudart"]
+
+
+def _compile_binding() -> str:
+    """The binding's object; it is linked once the library is there."""
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *_binding_flags()[0], "-c",
+           BINDING_SRC, "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compiling {BINDING_SRC} failed:\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{BUILD_DIR}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
+           *_binding_flags()[1]]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(f) <= t for f in sources() + _headers() + [__file__])
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    return all(os.path.getmtime(f) <= t for f in sources() + _headers() + [BINDING_SRC, __file__])
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -66,14 +104,17 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding)
     return LIB_PATH
 
 

@@ -253,3 +253,17 @@ def test_pool_layout():
     assert block[ps * D + 5 * 4 + 1] == 120 and block[ps * D + ps * 4 + 5 * 4 + 1] == 128
     kk, vv = R.values(pool, ps, D)
     assert kk[2, 1, 5, 17] == 7.0 and vv[2, 1, 5, 18] == -14.0 and np.abs(kk).sum() == 7.0 and np.abs(vv).sum() == 14.0
+
+
+def test_short_way_refuses_what_is_no_tensor(lib):
+    """What is not as it should be goes the long way, which says what: the short one says nothing."""
+    import torch
+    short = pa._short()
+    arity = dict(append_kv4=5, gather_kv4=5, fwd_kv4=12, fork=13, free=10, compact=10, copy_pages=4)
+    host = torch.zeros((3, 2, 64))
+    for name, n in arity.items():
+        fn = getattr(short, name)
+        assert fn(*[None] * n) is None and fn(*[host] * n) is None and fn(*[FakeCuda(3, 2)] * n) is None
+        with pytest.raises(TypeError):
+            fn(*[None] * (n + 1))
+    assert short.copy_pages([host] * 3, torch.zeros((2, 2), dtype=torch.int32), None, None) is None
