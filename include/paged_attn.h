@@ -480,7 +480,7 @@ int paged_attn_sparse_shares_pages(const pa_dims *dims, int packed, int top_k, f
  *   s = the s(c) nearest to a / 7 (on a tie the even c; at most 7168),   u = 8 + min(max(rint(x / s), -7), 7)
  * (u = 8 where s = 0): the exact quotients' roundings, to nearest even.  A NaN counts as 0 and an infinity as the largest
  * value, and either sets PA_ERRBIT_NONFINITE.  A slot named twice holds unspecified (finite) rows.
- * dims->batch, num_q_heads, bt_stride and q_stride are not used.
+ * dims->batch, num_q_heads, bt_stride and q_stride are not used.  num_kv_heads <= 32767 (PA_EUNSUPPORTED).
  */
 int paged_attn_append_kv4(const void *k_new, const void *v_new, const int32_t *slots, int64_t k_stride,
                           int64_t v_stride, void *kv, const pa_dims *dims, void *stream);

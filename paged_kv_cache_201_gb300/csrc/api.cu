@@ -884,6 +884,7 @@ int kv4_rows_call(const void *k, const void *v, void *k_out, void *v_out, const 
                   int64_t v_stride, void *kv, const pa_dims *dims, void *stream) {
     int rc = check_dims(dims);
     if (rc != PA_OK) return rc;
+    if (dims->num_kv_heads > 32767) return PA_EUNSUPPORTED;  // two of them a grid's row
     const int64_t row = (int64_t)dims->num_kv_heads * dims->head_dim;
     for (int64_t s : {k_stride, v_stride})
         if (s != 0 && (s < row || (s * esize_of(dims->dtype)) % 16 != 0 || s >= (int64_t)1 << 40)) return PA_EINVAL;

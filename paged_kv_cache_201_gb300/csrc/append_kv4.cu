@@ -193,7 +193,6 @@ static cudaError_t launch_rows_u(const Kv4RowsParams &p, cudaStream_t stream) {
 
 template <typename T, int D>
 static cudaError_t launch_rows(const Kv4RowsParams &p, cudaStream_t stream) {
-    if (p.Hkv > 32767) return cudaErrorInvalidConfiguration;
     // Rows for every multiprocessor many times over: several loads of a thread on their way together.
     if ((long long)p.T * p.Hkv * (D / 8) >= (1 << 19)) return launch_rows_u<T, D, 4>(p, stream);
     return launch_rows_u<T, D, 1>(p, stream);

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         return;
     }
     // this warp's run of the blocks
-    const int blocks = (k_hi + kBlockKeys - 1) / kBlockKeys;
+    const int blocks = (k_hi - 1) / kBlockKeys + 1;
     const int share = 2 * ((blocks + 2 * p.S * NW - 1) / (2 * p.S * NW));
     const int b0 = min((rank * NW + warp) * share, blocks), b1 = min(b0 + share, blocks);
     const int steps = (b1 - b0 + 1) / 2;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         // ---- weights; a score more than kRefMost above its reference moves it
         float mx[NR][2];
         bool over = false;
-        if (j0 + kStepKeys > all_below) {
+        if (j0 > all_below - kStepKeys) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
                     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                         for (int kh = 0; kh < 2; ++kh)
-                            if (j0 + hb * kBlockKeys + kg + 8 * kh >= lim[nr][e]) sc[hb][nr][2 * kh + e] = kNegInf;
+                            if (hb * kBlockKeys + kg + 8 * kh >= lim[nr][e] - j0) sc[hb][nr][2 * kh + e] = kNegInf;
         }
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int k_hi = row_key_limit(f, u.b, L, u.i + u.cnt - 1, u.n);  // the last token reaches furthest
     // this CTA's share of the 128-key tiles
-    const int all_tiles = (max(k_hi, 0) + 127) >> 7, share = (all_tiles + p.S - 1) / p.S;
+    const int all_tiles = k_hi > 0 ? ((k_hi - 1) >> 7) + 1 : 0, share = (all_tiles + p.S - 1) / p.S;
     const int tile0 = min(part * share, all_tiles), n_tiles = min(share, all_tiles - tile0);
     const int half_tokens = p.TT / 2;  // tokens of a tile of rows
 
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t *pool = static_cast<const uint8_t *>(f.k_cache) + (long long)kvh * kv4::block_bytes(ps, D);
         const uint32_t stride = (uint32_t)f.Hkv * (uint32_t)kv4::block_bytes(ps, D);
         const int32_t *row = f.block_table + (long long)u.b * f.W;
-        const int np = (max(k_hi, 0) + ps - 1) >> ps_shift;
+        const int np = k_hi > 0 ? ((k_hi - 1) >> ps_shift) + 1 : 0;
         auto look_up = [&](int t, int (&id)[C::kTurns]) {
 #pragma unroll
             for (int i = 0; i < C::kTurns; ++i) {
@@ -334,12 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) tc05::ld_32cols(sbuf + 32u * i, s[i]);
             tc05::wait_ld();
             const int j0 = (tile0 + t) * 128;
-            if (j0 + 128 > all_below) {
+            if (j0 > all_below - 128) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (j0 + 32 * i + j >= lim) s[i][j] = 0xff800000u;
+                        if (32 * i + j >= lim - j0) s[i][j] = 0xff800000u;
             }
             float m[4];
 #pragma unroll

@@ -36,7 +36,7 @@ def _ref(d):
 @pytest.mark.parametrize("dims,kw,code", [
     (None, {}, EINVAL), (dict(dtype=7), {}, EDTYPE), (dict(head_dim=96), {}, EUNSUP), (dict(page_size=8), {}, EUNSUP),
     (dict(num_pages=1 << 27), {}, EUNSUP), (dict(num_pages=0), {}, EINVAL), (dict(num_kv_heads=3), {}, EINVAL),
-    ({}, dict(ks=255), EINVAL), ({}, dict(vs=2 * 128 + 4), EINVAL), ({}, dict(ks=1 << 40), EINVAL),
+    (dict(num_kv_heads=32768, num_q_heads=32768), {}, EUNSUP), ({}, dict(ks=255), EINVAL), ({}, dict(vs=2 * 128 + 4), EINVAL), ({}, dict(ks=1 << 40), EINVAL),
     ({}, dict(k=None), EINVAL), ({}, dict(v=None), EINVAL), ({}, dict(k=FAKE + 8), EINVAL), ({}, dict(kv=None), EINVAL),
     ({}, dict(kv=FAKE + 4), EINVAL), ({}, dict(slots=FAKE + 2), EINVAL), ({}, dict(slots=None), EINVAL),
     (dict(q_len=0), {}, OK), (dict(q_len=0), dict(k=None, v=None, slots=None), OK), (dict(q_len=0, dtype=pa.PA_F32), {}, OK),

@@ -346,3 +346,74 @@ def test_convenience_and_graph(pa):
         pa.paged_attn_append_kv4(k, k, slots, kv)
         assert torch.equal(got, pa.attention_kv4(c["q"], kv, table, lens, q_start=starts))
     assert pa.paged_attn_last_error_word() == 0
+
+
+def test_pool_past_four_gibibytes(pa):
+    """Pages whose bytes lie past 2^32: written, read back and attended to by both kernels."""
+    import torch
+    ps, Hkv, G, D, P = 64, 8, 4, 128, 64000
+    kv = pa.kv4_pool(P, ps, Hkv, D)
+    assert kv.numel() > 1.08 * 2**32
+    lens, new = np.array([70, 3000]), np.array([1, 300])
+    need = -(-lens // ps)
+    table = np.full((2, int(need.max())), -1, np.int32)
+    ids = np.r_[np.arange(P - 40, P), np.arange(10)][::-1]
+    table[0, :need[0]], table[1, :need[1]] = ids[:need[0]], ids[need[0]:need.sum()]
+    pos = [np.arange(n) for n in lens]
+    slots = np.concatenate([table[b, p // ps] * np.int64(ps) + p % ps for b, p in enumerate(pos)])
+    k, v = (torch.randn((len(slots), Hkv, D), device="cuda").bfloat16() for _ in "kv")
+    pa.paged_attn_append_kv4(k, v, _t(slots, np.int32), kv)
+    a, b = torch.empty_like(k), torch.empty_like(v)
+    pa.paged_attn_gather_kv4(kv, _t(slots, np.int32), a, b)
+    # the same sequences in a small pool
+    used = np.unique(table[table >= 0])
+    pool = kv[torch.from_numpy(used.astype(np.int64)).cuda()].cpu().numpy()
+    small = np.where(table >= 0, np.searchsorted(used, np.maximum(table, 0)), -1).astype(np.int32)
+    for got, want in zip((a, b), R.values(pool, ps, D)):
+        flat = want.transpose(0, 2, 1, 3).reshape(-1, Hkv, D)
+        at = np.concatenate([small[i, p // ps] * ps + p % ps for i, p in enumerate(pos)])
+        np.testing.assert_array_equal(_np(got), flat[at])
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.randn((starts[-1], Hkv * G, D), device="cuda").bfloat16()
+    out = pa.attention_kv4(q, kv, _t(table), _t(lens, np.int32), q_start=_t(starts))
+    near = pa.attention_kv4(q, _t(pool), _t(small), _t(lens, np.int32), q_start=_t(starts))
+    assert torch.equal(out, near)
+    rows = np.r_[0, 1, 150, 300]
+    want, _, _, room, mass = R.attention(_np(q[:1]), pool, ps, small[:1], lens[:1], [0, 1], True, None, D ** -0.5)
+    assert (np.abs(_np(out[:1]) - want) <= STEP["bf16"] * np.abs(want) + room + WEIGHT["bf16"] * mass).all()
+    for t in rows[1:]:
+        n = int(lens[1] - new[1] + t)  # keys of the token
+        want, _, _, room, mass = R.attention(_np(q[t:t + 1]), pool, ps, small[1:], [n], [0, 1], True, None, D ** -0.5)
+        assert (np.abs(_np(out[t:t + 1]) - want) <= STEP["bf16"] * np.abs(want) + room + WEIGHT["bf16"] * mass).all()
+    assert pa.paged_attn_last_error_word() == 0
+
+
+def test_two_streams_at_once(pa):
+    """Calls that share their keys out, side by side on two streams, each with a workspace of its own; one captured
+    and replayed on a stream of its own beside an eager one."""
+    import torch
+    cases = [_case(30 + i, [6000 - 900 * i], [2], 1, 4, 128, 16, "bf16", width=600) for i in range(2)]
+    args = [(c["q"], c["kv"], _t(c["table"]), _t(c["lens"])) for c in cases]
+    starts = [_t(c["starts"]) for c in cases]
+    want = [pa.attention_kv4(*a, q_start=s) for a, s in zip(args, starts)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(pa.attention_kv4(*args[i], q_start=starts[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = pa.attention_kv4(*args[0], q_start=starts[0])
+    for _ in range(5):
+        kept.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        with torch.cuda.stream(streams[1]):
+            other = pa.attention_kv4(*args[1], q_start=starts[1])
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want[0]) and torch.equal(other, want[1])
