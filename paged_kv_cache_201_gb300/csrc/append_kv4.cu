@@ -88,6 +88,7 @@ __device__ __forceinline__ uint32_t quantise(const float *x, kv4::Reciprocal s) 
 // A block: one kv head's K or V rows of U x kThreads / (D / 16) tokens.
 template <typename T, int D, int U>
 __global__ void __launch_bounds__(kThreads) paged_attn_append_kv4_kernel(const Kv4RowsParams p) {
+    wait_for_stream();
     constexpr int C = D / kv4::kGroup, TPB = kThreads / C;  // threads of a row, rows at once
     const int c = threadIdx.x % C, side = blockIdx.y & 1, h = blockIdx.y >> 1;
     const long long t0 = (long long)blockIdx.x * (TPB * U) + threadIdx.x / C;
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_append_kv4_kernel(const K
 
 template <typename T, int D, int U>
 __global__ void __launch_bounds__(kThreads) paged_attn_gather_kv4_kernel(const Kv4RowsParams p) {
+    wait_for_stream();
     constexpr int C = D / 8, TPB = kThreads / C;
     const int c = threadIdx.x % C, side = blockIdx.y & 1, h = blockIdx.y >> 1;
     const long long t0 = (long long)blockIdx.x * (TPB * U) + threadIdx.x / C;
@@ -184,11 +186,8 @@ template <typename T, int D, int U>
 static cudaError_t launch_rows_u(const Kv4RowsParams &p, cudaStream_t stream) {
     const int rows = kThreads / (p.k_out ? D / 8 : D / kv4::kGroup) * U;
     const dim3 grid((unsigned)(((long long)p.T + rows - 1) / rows), (unsigned)(2 * p.Hkv));
-    if (p.k_out)
-        paged_attn_gather_kv4_kernel<T, D, U><<<grid, kThreads, 0, stream>>>(p);
-    else
-        paged_attn_append_kv4_kernel<T, D, U><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_behind(p.k_out ? paged_attn_gather_kv4_kernel<T, D, U> : paged_attn_append_kv4_kernel<T, D, U>, grid, kThreads, 0,
+                         1, stream, p);
 }
 
 template <typename T, int D>

@@ -51,7 +51,7 @@ struct Unit {
         rows = L = k_hi = 0;
         if (u.cnt <= 0) return;
         rows = u.cnt * heads;
-        L = max(__ldg(f.seq_lens + u.b), 0);
+        L = max(u.len, 0);
         if (L > f.W << ps_shift) {  // never read past the sequence's block-table row
             if (report) atomicOr(f.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
             L = f.W << ps_shift;
@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     constexpr int kParts = std::is_same<T, __half>::value ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
     const FwdParams &f = p.s.f;
+    if (!p.s.group_min) wait_for_stream();  // else beside the tcgen05 kernel, which came behind the stream's others
     RangeCheck ranges(p.s);
     BehindFirst behind(p.s);
 
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(128) paged_attn_kv4_join_kernel(const Kv4Param
     __shared__ float s_l[TG];
     const int c = threadIdx.x % C, tg = threadIdx.x / C, r = blockIdx.x % R;
     const Unit un(p, R, (int)(blockIdx.x / R), threadIdx.x & 31, ps_shift, false);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     if (r >= un.rows || un.k_hi <= 0) return;
     const long long row = un.row(f, r), rows = p.s.n_tok * f.Hq;
     const float2 *state = reinterpret_cast<const float2 *>(p.part_state) + row;
@@ -650,23 +651,9 @@ cudaError_t launch_kv4(Kv4Params p, const Plan &a, cudaStream_t stream) {
     static SmemLimit limits[2];
     cudaError_t e = limits[page16].raise((const void *)kern, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.units * a.S));
-    cfg.blockDim = dim3(NW * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    cfg.attrs = attr;
-    cfg.numAttrs = second_launch_attrs(attr, a.grid ? 1 : a.S, p.s.group_min != 0);
-    if (cfg.numAttrs == 1 && (a.grid || a.S == 1)) cfg.numAttrs = 0;  // no cluster: a plain launch costs the host less
-    e = cudaLaunchKernelEx(&cfg, kern, p, ps_shift);
+    e = launch_behind(kern, dim3((unsigned)(a.units * a.S)), NW * 32, smem, a.grid ? 1 : a.S, stream, p, ps_shift);
     if (e != cudaSuccess || !a.grid) return e;
-    cfg.gridDim = dim3((unsigned)(a.units * R));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    cfg.attrs = attr + 1;
-    cfg.numAttrs = 1;  // may start beside the first's last CTAs
-    return cudaLaunchKernelEx(&cfg, paged_attn_kv4_join_kernel<T, D>, p, R, ps_shift);
+    return launch_behind(paged_attn_kv4_join_kernel<T, D>, dim3((unsigned)(a.units * R)), 128, 0, 1, stream, p, R, ps_shift);
 }
 
 template <typename T, int D>

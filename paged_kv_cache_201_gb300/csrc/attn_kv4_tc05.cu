@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t bars[B_COUNT];
     __shared__ uint32_t s_tmem;
     __shared__ float s_factor[256];
+    __shared__ long long s_row[256];  // a thread's row of out, -1: none (kept here, not in the softmax warps' registers)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ps = 1 << ps_shift;
     const int part = blockIdx.x % p.S, unit = blockIdx.x / p.S, kvh = unit % f.Hkv;
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Tile u = find_tile(p, unit / f.Hkv, lane);
     ranges.report(f);
     if (u.cnt <= 0) return;
-    int L = max(__ldg(f.seq_lens + u.b), 0);
+    int L = max(u.len, 0);
     if (L > f.W << ps_shift) {  // never read past the sequence's block-table row
         if (tid == 0) atomicOr(f.err, (unsigned int)PA_ERRBIT_SEQ_CLIPPED);
         L = f.W << ps_shift;
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tk = tile * half_tokens + r / f.G;
         const bool valid = r < half_tokens * f.G && tk < u.cnt;
         const int lim = valid ? row_key_limit(f, u.b, L, u.i + tk, u.n) : INT_MAX;
+        s_row[tile * 128 + r] = valid ? (u.q0 + u.i + tk) * f.Hq + kvh * f.G + r % f.G : -1;
         const int all_below = __reduce_min_sync(0xffffffffu, lim);  // keys that every row of the warp sees
         const float factor = s_factor[tile * 128 + r];
         float ref = kNoRef;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc05::fence_after_sync();
         const float l = l2.x + l2.y, inv = l != 0.f ? 8.f / l : 0.f;  // a NaN stays one
         if (!bad) {
-            const long long row = (u.q0 + u.i + tk) * f.Hq + kvh * f.G + r % f.G;
+            const long long row = *(volatile long long *)&s_row[tile * 128 + r];
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -413,14 +415,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // columns 0 1 2 .. 7 hold elements 0 4 1 5 2 6 3 7
                 auto e = [&](int i, int x) { return __uint_as_float(o[8 * i + (x < 4 ? 2 * x : 2 * x - 7)]); };
-                if (valid && p.part_out) {
+                if (row >= 0 && p.part_out) {
                     float4 *dst = reinterpret_cast<float4 *>(p.part_out + (part * p.s.n_tok * f.Hq + row) * D + 32 * c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         dst[2 * i] = make_float4(e(i, 0), e(i, 1), e(i, 2), e(i, 3));
                         dst[2 * i + 1] = make_float4(e(i, 4), e(i, 5), e(i, 6), e(i, 7));
                     }
-                } else if (valid) {
+                } else if (row >= 0) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(f.out) + row * D + 32 * c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -429,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (valid && p.part_out)
+            if (row >= 0 && p.part_out)
                 *reinterpret_cast<float2 *>(p.part_state + 2 * (part * p.s.n_tok * f.Hq + row)) = make_float2(ref, l);
-            else if (valid && f.lse)
+            else if (row >= 0 && f.lse)
                 f.lse[row] = l != 0.f ? ref * kLn2 + logf(l) : kNegInf;
         }
     }

@@ -3,6 +3,7 @@
 // A CTA moves chunks of kChunk bytes; the chunks of a pair's page in every pool stand in one row, so that a few pairs
 // already occupy every multiprocessor.  The number of pairs may be on the device: the grid is sized for all and walks.
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace pa {
 
@@ -32,6 +33,7 @@ __device__ __forceinline__ void copy_chunk(const uint8_t *src, uint8_t *dst, lon
 
 __global__ void __launch_bounds__(kThreads) paged_attn_copy_pages_kernel(const __grid_constant__ CopyPagesParams p,
                                                                          int chunks) {
+    wait_for_stream();
     const int pairs = p.n_pairs ? min(max(__ldg(p.n_pairs), 0), p.max_pairs) : p.max_pairs;
     const long long units = (long long)pairs * chunks;
     for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
@@ -66,8 +68,8 @@ cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t st
     if (chunks == 0 || p.max_pairs == 0) return cudaSuccess;
     if (chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const long long units = chunks * p.max_pairs, most = 8ll * sms;
-    paged_attn_copy_pages_kernel<<<(unsigned)(units < most ? units : most), kThreads, 0, stream>>>(p, (int)chunks);
-    return cudaGetLastError();
+    return launch_behind(paged_attn_copy_pages_kernel, dim3((unsigned)(units < most ? units : most)), kThreads, 0, 1, stream, p,
+                         (int)chunks);
 }
 
 }  // namespace pa

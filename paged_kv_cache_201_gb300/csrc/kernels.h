@@ -151,6 +151,26 @@ cudaError_t launch_sparse_tc05(const SparseParams &p, int dtype, const CUtensorM
 // f32: CUDA cores, a list split over a cluster when there are few rows
 cudaError_t launch_sparse_simt(const SparseParams &p, int sms, cudaStream_t stream);
 
+// A launch that may be set up while the stream's last kernel still runs: its kernel begins with wait_for_stream().  Worth
+// a microsecond where one call of a few microseconds follows another.  ctas > 1: clusters of so many.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, int threads, size_t smem, int ctas, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // ---------------------------------------------------------------- 4-bit cache
 struct Kv4RowsParams {
     const void *k, *v;    // append: new rows

@@ -11,6 +11,10 @@
 #include "common.cuh"
 
 namespace pa {
+
+// See launch_behind: everything that the stream's earlier kernels wrote is there, and they have read what they read.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 namespace kv4 {
 
 constexpr int kGroup = 16;                 // elements that share a scale

@@ -23,52 +23,68 @@ struct Kv4Params {
     int seq_tiles; // tiles of every sequence: a uniform batch, or the short runs of a packed one (0: by rows of q)
 };
 
-// A unit's tokens: cnt of sequence b from its token i on; q0 the sequence's first row of q, n its tokens.
+// A unit's tokens: cnt of sequence b from its token i on; q0 the sequence's first row of q, n its tokens, len its keys.
 struct Tile {
-    int b, n, i, cnt;
+    int b, n, i, cnt, len;
     long long q0;
 };
 
 // Packed batches: sequence b's tiles are q_start[b] / TT + b and on, which leaves room for all of them; with one
-// token a tile they are its rows.
+// token a tile they are its rows.  One trip to memory for a batch of up to 32 sequences or of single tokens.
 __device__ __forceinline__ Tile find_tile(const Kv4Params &p, int tile, int lane) {
     const FwdParams &f = p.s.f;
-    Tile u{0, 0, 0, 0, 0};
+    Tile u{0, 0, 0, 0, 0, 0};
+    int q0, q1;
     if (p.seq_tiles) {
         u.b = tile / p.seq_tiles;
         u.i = (tile - u.b * p.seq_tiles) * p.TT;
+        u.len = __ldg(f.seq_lens + u.b);
         if (!f.q_start) {
             u.n = f.Sq;
             u.q0 = (long long)u.b * f.Sq;
             u.cnt = min(p.TT, u.n - u.i);
             return u;
         }
-    }
-    auto key = [&](int b, int q) { return p.TT == 1 ? q : max(q, 0) / p.TT + b; };
-    if (!p.seq_tiles) {
-        int lo = 0, hi = f.B;  // key(lo) <= tile < key(hi)
-        const int guess = min(p.TT == 1 ? tile : tile - tile / (p.TT + 1), f.B - 1);  // a token a sequence
-        if (key(guess, __ldg(f.q_start + guess)) <= tile) {
-            lo = guess;
-            if (key(guess + 1, __ldg(f.q_start + guess + 1)) > tile) hi = lo + 1;
+        q0 = __ldg(f.q_start + u.b);
+        q1 = __ldg(f.q_start + u.b + 1);
+    } else {
+        auto key = [&](int b, int q) { return p.TT == 1 ? q : max(q, 0) / p.TT + b; };
+        if (f.B <= 32) {  // a sequence a lane
+            const bool mine = lane < f.B;
+            const int a = mine ? __ldg(f.q_start + lane) : 0, e = mine ? __ldg(f.q_start + lane + 1) : 0;
+            const int len = mine ? __ldg(f.seq_lens + lane) : 0;
+            const unsigned below = __ballot_sync(0xffffffffu, mine && key(lane, a) <= tile);
+            u.b = below ? 31 - __clz(below) : 0;
+            q0 = __shfl_sync(0xffffffffu, a, u.b);
+            q1 = __shfl_sync(0xffffffffu, e, u.b);
+            u.len = __shfl_sync(0xffffffffu, len, u.b);
         } else {
-            hi = max(guess, 1);
+            const int guess = min(p.TT == 1 ? tile : tile - tile / (p.TT + 1), f.B - 1);  // a token a sequence
+            q0 = __ldg(f.q_start + guess);
+            q1 = __ldg(f.q_start + guess + 1);
+            u.b = guess;
+            u.len = __ldg(f.seq_lens + guess);
+            if (key(guess, q0) > tile || key(guess + 1, q1) <= tile) {
+                int lo = 0, hi = f.B;  // key(lo) <= tile < key(hi)
+                while (hi - lo > 1) {  // 31 borders a trip
+                    const int step = (hi - lo + 31) / 32;
+                    const int b = lo + (lane + 1) * step;
+                    const bool below = b < hi && key(b, __ldg(f.q_start + b)) <= tile;
+                    const int k = __popc(__ballot_sync(0xffffffffu, below));
+                    hi = min(hi, lo + (k + 1) * step);
+                    lo += k * step;
+                }
+                u.b = lo;
+                q0 = __ldg(f.q_start + lo);
+                q1 = __ldg(f.q_start + lo + 1);
+                u.len = __ldg(f.seq_lens + lo);
+            }
         }
-        while (hi - lo > 1) {  // 31 borders a trip
-            const int step = (hi - lo + 31) / 32;
-            const int b = lo + (lane + 1) * step;
-            const bool below = b < hi && key(b, __ldg(f.q_start + b)) <= tile;
-            const int k = __popc(__ballot_sync(0xffffffffu, below));
-            hi = min(hi, lo + (k + 1) * step);
-            lo += k * step;
-        }
-        u.b = lo;
+        u.i = (tile - key(u.b, q0)) * p.TT;
     }
-    const int q0 = __ldg(f.q_start + u.b), q1 = __ldg(f.q_start + u.b + 1);
     if (q0 < 0 || q1 < q0 || q1 > p.s.n_tok) return u;
     u.q0 = q0;
     u.n = q1 - q0;
-    if (!p.seq_tiles) u.i = (tile - key(u.b, q0)) * p.TT;
     if (u.i < 0 || u.n < p.min_tokens || (p.s.group_min && u.n >= p.s.group_min)) return u;  // malformed, or the other kernel's
     u.cnt = min(p.TT, u.n - u.i);
     return u;

@@ -11,6 +11,7 @@
 // the places' numbers, INT_MIN + e with e < 2^30, lie below every count that is reached.
 #include <limits.h>
 
+#include "kv4.cuh"
 #include "sparse_common.cuh"
 
 namespace pa {
@@ -136,6 +137,7 @@ __device__ __forceinline__ void for_places(const int *s_start, int n, int total,
 // PER: requests of a thread at most.
 template <int PER>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_fork_kernel(const PagesParams p) {
+    wait_for_stream();
     extern __shared__ int sm[];
     int *s_start = sm, *s_row = sm + p.n + 1;  // [n + 1] first places, [n] parent's row
     int *s_named = s_row + p.n;                // [B] the first request that names a child
@@ -261,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_fork_kernel(const Page
 
 template <int PER>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const PagesParams p) {
+    wait_for_stream();
     extern __shared__ int sm[];
     int *s_start = sm, *s_row = sm + p.n + 1;  // [n + 1] first places, [n] rows
     int *s_named = s_row + p.n;                // [B] the first request that names a row
@@ -402,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
 // values do.
 template <int PER>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const PagesParams p) {
+    wait_for_stream();
     extern __shared__ int sm[];
     int *s_start = sm;  // [B + 1]
     __shared__ Pair warp_sums[kWarps];
@@ -571,18 +575,7 @@ cudaError_t launch_cluster(K kern, ClusterLimit &limit, size_t smem, size_t smem
     while (ctas < most && ctas * 2048ll < work) ctas *= 2;
     if (e == cudaSuccess && ctas > 8) e = limit.wide.allow_wide_clusters((const void *)kern);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ctas;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return launch_behind(kern, dim3(ctas), kThreads, smem, ctas, stream, p);
 }
 
 size_t lists_smem(long long n, long long B) { return (size_t)(2 * n + 1 + (n > B ? n : B)) * sizeof(int); }
