@@ -210,10 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tm = same(tmem);
             const bool leader = tc05::elect_one();
             const uint32_t dhi = tc05::smem_desc_sw128_hi(1024);
-            bool bad = false;
+            const uint32_t dq0 = tc05::smem_desc_sw128_lo(sQ(0), 16), dq1 = tc05::smem_desc_sw128_lo(sQ(1), 16);
+            const uint32_t dk0 = tc05::smem_desc_sw128_lo(sK(0), 16), dk1 = tc05::smem_desc_sw128_lo(sK(1), 16);
+            const uint32_t dv0 = tc05::smem_desc_sw128_lo(sV(0), (uint32_t)kHalf), dv1 = tc05::smem_desc_sw128_lo(sV(1), (uint32_t)kHalf);
             auto qk = [&](int tile, int t) {
-                const uint32_t d = tm + 128u * (uint32_t)tile, dq = tc05::smem_desc_sw128_lo(sQ(tile), 16),
-                               dk = tc05::smem_desc_sw128_lo(sK(t & 1), 16);
+                const uint32_t d = tm + 128u * (uint32_t)tile, dq = tile ? dq1 : dq0, dk = t & 1 ? dk1 : dk0;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
@@ -226,8 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto pv = [&](int tile, int t) {
-                const uint32_t pcol = tm + 128u * (uint32_t)tile, o = tm + kColO + (uint32_t)(D * tile),
-                               dv = tc05::smem_desc_sw128_lo(sV(t & 1), (uint32_t)kHalf);
+                const uint32_t pcol = tm + 128u * (uint32_t)tile, o = tm + kColO + (uint32_t)(D * tile), dv = t & 1 ? dv1 : dv0;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {  // keys 16 kk .. + 15
@@ -240,25 +240,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05::commit(bar(B_PD + tile));  // the last one is waited for before the CTA ends
                 }
             };
-            auto wait = [&](int b, int t) {
-                bad = bad || !mbar_wait(bar(b), (uint32_t)t & 1u, f.err);
-                bad = __any_sync(0xffffffffu, bad);
+            // whether a wait ran out (the same in every lane, as the compiler can see: the loop's counters stay uniform)
+            auto gone = [&](int b, int phase) {
+                const bool ok = mbar_wait(bar(b), (uint32_t)phase & 1u, f.err);
                 tc05::fence_after_sync();
+                return __any_sync(0xffffffffu, !ok);
             };
-            wait(B_KF, 0);
-            if (!bad) qk(0, 0);
-            if (!bad) qk(1, 0);
-            for (int t = 0; t < nt && !bad; ++t) {
-#pragma unroll 1
-                for (int tile = 0; tile < 2 && !bad; ++tile) {
-                    if (tile == 0) wait(B_VF + (t & 1), t >> 1);
-                    wait(B_PF + tile, t);
-                    if (bad) break;
-                    pv(tile, t);
+            if (!gone(B_KF, 0)) {
+                qk(0, 0);
+                qk(1, 0);
+                for (int t = 0; t < nt; ++t) {
+                    if (gone(B_VF + (t & 1), t >> 1)) break;
+                    if (gone(B_PF + 0, t)) break;
+                    pv(0, t);
                     if (t + 1 < nt) {
-                        if (tile == 0) wait(B_KF + ((t + 1) & 1), (t + 1) >> 1);
-                        if (!bad) qk(tile, t + 1);  // over S, and the P that the products before have read by then
+                        if (gone(B_KF + ((t + 1) & 1), (t + 1) >> 1)) break;
+                        qk(0, t + 1);  // over S, and the P that the products before have read by then
                     }
+                    if (gone(B_PF + 1, t)) break;
+                    pv(1, t);
+                    if (t + 1 < nt) qk(1, t + 1);
                 }
             }
         }
