@@ -471,7 +471,7 @@ int paged_attn_sparse_shares_pages(const pa_dims *dims, int packed, int top_k, f
  *   (u - 8) * s(c),   s(c) = c * 2^-17 for c < 8,  else (8 + c % 8) * 2^(c / 8 - 18),  at most s(0xDE) = 7168
  * (bytes above 0xDE count as 0xDE), so any bytes are finite numbers, all of them exact in f16, bf16 and
  * float32; a pool of zeros holds zeros.  Tables, slots, lengths and pages are those of the other pools, and
- * these calls follow the rules of the serving step above: a launch or two on `stream`, graph capture after a
+ * these calls follow the rules of the serving step above: one to three launches on `stream`, graph capture after a
  * first call on the device.  They are this library's own.
  *
  * paged_attn_append_kv4 — new tokens' K and V rows into their slots.

@@ -271,19 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t *pool = static_cast<const uint8_t *>(f.k_cache) + (long long)kvh * kv4::block_bytes(ps, D);
         const uint32_t stride = (uint32_t)f.Hkv * (uint32_t)kv4::block_bytes(ps, D);
         const int32_t *row = f.block_table + (long long)u.b * f.W;
-        const int np = k_hi > 0 ? ((k_hi - 1) >> ps_shift) + 1 : 0;
+        const uint32_t np = k_hi > 0 ? (uint32_t)((k_hi - 1) >> ps_shift) + 1 : 0;
+        // page of a tile's turn; tiles behind the last may begin past 2^31 keys
+        auto page = [&](int t, int i) { return ((uint32_t)(tile0 + t) * 128u + (uint32_t)C::first_row(i, w)) >> ps_shift; };
         auto look_up = [&](int t, int (&id)[C::kTurns]) {
 #pragma unroll
-            for (int i = 0; i < C::kTurns; ++i) {
-                const int pg = ((tile0 + t) * 128 + C::first_row(i, w)) >> ps_shift;
-                id[i] = pg < np ? __ldg(row + pg) : -1;
-            }
+            for (int i = 0; i < C::kTurns; ++i) id[i] = page(t, i) < np ? __ldg(row + page(t, i)) : -1;
         };
         auto check = [&](int t, int (&id)[C::kTurns]) {  // ids outside the pool read as zeros
 #pragma unroll
             for (int i = 0; i < C::kTurns; ++i)
                 if ((uint32_t)id[i] >= (uint32_t)f.num_pages) {
-                    if (lane == 0 && ((tile0 + t) * 128 + C::first_row(i, w)) >> ps_shift < np)
+                    if (lane == 0 && page(t, i) < np)
                         atomicOr(f.err, (unsigned int)PA_ERRBIT_PAGE_RANGE);
                     id[i] = -1;
                 }

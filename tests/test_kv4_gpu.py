@@ -417,3 +417,28 @@ def test_two_streams_at_once(pa):
             other = pa.attention_kv4(*args[1], q_start=starts[1])
         torch.cuda.synchronize()
         assert torch.equal(kept, want[0]) and torch.equal(other, want[1])
+
+
+@pytest.mark.parametrize("tokens,Hkv", [(1, 1), (16, 16)])
+def test_nearly_two_to_the_31_keys(pa, tokens, Hkv):
+    """The longest sequence that there can be.  All but its last five pages are one page whose keys weigh nothing."""
+    import torch
+    ps, G, D = 64, 8, 64
+    rng = np.random.default_rng(70)
+    pool = np.zeros((4, Hkv, 9 * ps * D // 8), np.uint8)
+    rows = rng.standard_normal((2, 4 * ps, Hkv, D))
+    rows[0, :, :, :16] = 0
+    rows[0, :ps, :, :16] = -7.0
+    R.write(pool, np.arange(4 * ps), rows[0], rows[1], ps)
+    q = rng.standard_normal((tokens, Hkv * G, D))
+    q[:, :, :16] = 8.0  # with the weightless page: a score some 100 below the others'
+    q = torch.from_numpy(q).bfloat16().cuda()
+    W = 2**25 - 1
+    table = torch.zeros((1, W), dtype=torch.int32, device="cuda")
+    table[0, -5:] = torch.tensor([1, 2, 3, 1, 2], device="cuda")
+    lens = _t([W * ps], np.int32)
+    out = pa.attention_kv4(q[None], _t(pool), table, lens)[0]
+    assert pa.paged_attn_last_error_word() == 0
+    want, _, _, room, mass = R.attention(_np(q), pool, ps, np.array([[0, 1, 2, 3, 1, 2]], np.int32), np.array([6 * ps], np.int32),
+                                         [0, tokens], True, None, D ** -0.5)
+    assert (np.abs(_np(out) - want) <= STEP["bf16"] * np.abs(want) + room + WEIGHT["bf16"] * mass + 2.0 ** -24).all()
