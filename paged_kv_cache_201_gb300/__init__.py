@@ -841,8 +841,7 @@ def paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, ou
     if workspace is None:
         size = lib.paged_attn_kv4_workspace_bytes(dims, 0 if q_start is None else 1, _sm_count(dev))
         if size > 0:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-            _record(stream, workspace)
+            workspace, = _made(stream, q.device, (size, torch.uint8))
     else:
         _need(workspace, "workspace", dev, torch.uint8, workspace.shape)
         size = workspace.numel()
@@ -1205,19 +1204,24 @@ def attention_kv4(q, kv, block_table, seq_lens, *, causal: bool = True, q_offset
     torch = _torch()
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
-    _record(stream, out, lse)
+    out, lse = _made(stream, q.device, (q.shape, q.dtype), (q.shape[:-1], torch.float32) if want_lse else None)
     paged_attn_fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, out, lse, q_start, stream)
     return (out, lse) if want_lse else out
 
 
-def _record(stream, *tensors) -> None:
-    """Tensors allocated on the current stream and used on another."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _made(stream, device, *wanted):
+    """New tensors of (shape, dtype) each (None: none) for work on stream.  On another stream than the current one they are
+    taken from that stream's memory, which the current one's pending work may not use, and kept until the current one,
+    which goes on with them, has come past their end."""
+    torch = _torch()
+    if stream is None:
+        return [w and torch.empty(w[0], dtype=w[1], device=device) for w in wanted]
+    with torch.cuda.stream(stream):
+        made = [w and torch.empty(w[0], dtype=w[1], device=device) for w in wanted]
+    for t in made:
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream())
+    return made
 
 
 def fork_sequences(parents, children, block_table, seq_lens, page_shares, free_pages, free_count, pools, page_size: int,
@@ -1225,8 +1229,7 @@ def fork_sequences(parents, children, block_table, seq_lens, page_shares, free_p
     """``paged_attn_fork`` and the copies of the last pages in every pool of the list; seq_lens and free_count are
     updated in place.  Returns the pairs that were copied, [n, 2]."""
     torch = _torch()
-    copies = torch.empty((parents.shape[0], 2), dtype=torch.int32, device=block_table.device)
-    _record(stream, copies)
+    copies, = _made(stream, block_table.device, ((parents.shape[0], 2), torch.int32))
     paged_attn_fork(parents, children, block_table, seq_lens, seq_lens, page_shares, free_pages, free_count, free_count,
                     copies, page_size, prefix_lens, stream)
     paged_attn_copy_pages(pools, copies, None, stream)
@@ -1244,8 +1247,7 @@ def compact_pages(block_table, seq_lens, page_shares, free_pages, free_count, po
     every page's new id, and how many pages moved (a tensor)."""
     torch = _torch()
     P = page_shares.shape[0]
-    moves, n_moves, page_map = (torch.empty(s, dtype=torch.int32, device=block_table.device) for s in ((P // 2, 2), 1, P))
-    _record(stream, moves, n_moves, page_map)
+    moves, n_moves, page_map = _made(stream, block_table.device, ((P // 2, 2), torch.int32), (1, torch.int32), (P, torch.int32))
     paged_attn_compact(block_table, seq_lens, page_shares, free_pages, free_count, moves, n_moves, page_map, page_size,
                        stream)
     paged_attn_copy_pages(pools, moves, n_moves, stream)

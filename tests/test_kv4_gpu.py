@@ -419,6 +419,24 @@ def test_two_streams_at_once(pa):
         assert torch.equal(kept, want[0]) and torch.equal(other, want[1])
 
 
+def test_memory_of_another_stream(pa):
+    """What a call on another stream allocates is not memory that the current stream's pending work may still use."""
+    import torch
+    c = _case(60, [6000], [2], 1, 4, 128, 16, "bf16", width=600)
+    args, starts = (c["q"], c["kv"], _t(c["table"]), _t(c["lens"])), _t(c["starts"])
+    want, want_lse = pa.attention_kv4(*args, q_start=starts, want_lse=True)
+    size = pa.paged_attn_kv4_workspace_bytes(1, 2, 4, 1, 128, 16, 600, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert size > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(want), torch.empty_like(want_lse), torch.empty(size, dtype=torch.uint8, device="cuda")]
+    freed = {t.data_ptr() for t in freed}  # and given back
+    out, lse = pa.attention_kv4(*args, q_start=starts, want_lse=True, stream=side)
+    assert out.data_ptr() not in freed and lse.data_ptr() not in freed
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 @pytest.mark.parametrize("tokens,Hkv", [(1, 1), (16, 16)])
 def test_nearly_two_to_the_31_keys(pa, tokens, Hkv):
     """The longest sequence that there can be.  All but its last five pages are one page whose keys weigh nothing."""
