@@ -36,6 +36,53 @@ using namespace mmac;
 namespace {
 
 constexpr int kBlockKeys = 16, kStepKeys = 32;
+// Which sequence (or row of a batch of single tokens) the CTAs of place `place` take, so that the longest start first and
+// the last to start are short: up to 256 of them by eight classes of length.  Every place has one and every one a place.
+__device__ __forceinline__ int longest_first(const FwdParams &f, int place, int lane) {
+    constexpr int N = 8;
+    int len[N], least = INT_MAX, most = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int b = 32 * k + lane;
+        len[k] = b < f.B ? max(__ldg(f.seq_lens + b), 0) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (len[k] >= 0) least = min(least, len[k]), most = max(most, len[k]);
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const float scale = 8.f / ((float)(most - least) + 1.f);
+    int of[N];  // class, the longest's 0
+    uint32_t count = 0;  // of this lane's, four bits a class
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        of[k] = len[k] < 0 ? 8 : min((int)((float)(most - len[k]) * scale), 7);
+        if (len[k] >= 0) count += 1u << (4 * of[k]);
+    }
+    uint32_t all[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) all[i] = __reduce_add_sync(0xffffffffu, count >> (4 * i) & 0x000F000Fu);
+    int c = 0, left = place;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = all[i & 3] >> (i < 4 ? 0 : 16) & 0xffff;
+        if (c == i && left >= n) {
+            left -= n;
+            ++c;
+        }
+    }
+    int found = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const unsigned in = __ballot_sync(0xffffffffu, of[k] == c);
+        const bool me = of[k] == c && __popc(in & ((1u << lane) - 1)) == left;
+        const unsigned who = __ballot_sync(0xffffffffu, me);
+        if (who) found = 32 * k + __ffs(who) - 1;
+        left -= __popc(in);
+    }
+    return found;
+}
+
 // A unit: up to R rows r = token x heads + head of tile u and kv head kvh.
 struct Unit {
     Tile u;
@@ -46,7 +93,12 @@ struct Unit {
         h0 = index % p.HT * R;
         index /= p.HT;
         kvh = index % f.Hkv;
-        u = find_tile(p, index / f.Hkv, lane);
+        index /= f.Hkv;
+        if (p.longest_first) {  // see make_plan
+            const int tiles = max(p.seq_tiles, 1), place = index / tiles;
+            index = longest_first(f, place, lane) * tiles + (index - place * tiles);
+        }
+        u = find_tile(p, index, lane);
         heads = min(R, f.G - h0);
         rows = L = k_hi = 0;
         if (u.cnt <= 0) return;
@@ -585,6 +637,7 @@ struct Plan {
     long long units;
     int S;
     bool grid;  // S of the grid's CTAs, joined by a second launch; else a cluster
+    bool longest_first;
 };
 Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
     const FwdParams &f = sp.f;
@@ -627,6 +680,13 @@ Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
     if (a.units * a.S <= sms) return a;
     a.warps = full / ctas;
     while (a.S < 4 && a.units * a.S * 2 <= (long long)sms * ctas && keys >= 4ll * kStepKeys * a.warps * a.S) a.S *= 2;
+    // More than one wave of CTAs: the longest sequences first, lest one starts when the others end.  Sequences of 0.4 to 1
+    // times the table's 4096 columns, 8 kv heads: 256 of them 178 -> 170 us, 152 114 -> 101, 110 99 -> 89.  Finding the
+    // sequence costs a CTA half a microsecond: with 1024 columns 100 sequences 29.5 -> 27.2, but 256 59.7 -> 61.2 (2048
+    // columns: 96.8 -> 95.1).
+    const long long wave = (long long)sms * ctas, n_ctas = a.units * a.S;
+    a.longest_first = n_ctas > wave && f.B > 1 && f.B <= 256 && (keys >= 2048 || (keys >= 1024 && n_ctas <= 2 * wave)) &&
+                      (a.seq_tiles > 0 || (a.TT == 1 && sp.n_tok == f.B));
     return a;
 }
 
@@ -641,6 +701,7 @@ cudaError_t launch_kv4(Kv4Params p, const Plan &a, cudaStream_t stream) {
     p.HT = a.HT;
     p.TT = a.TT;
     p.seq_tiles = a.seq_tiles;
+    p.longest_first = a.longest_first;
     if (a.grid) {
         p.part_out = static_cast<float *>(p.s.ws);
         p.part_state = p.part_out + a.S * p.s.n_tok * f.Hq * D;

@@ -21,6 +21,7 @@ struct Kv4Params {
     int TT, HT;    // tokens of a unit; head tiles of a kv head
     int min_tokens;  // tcgen05 kernel, packed batches: of sequences of so many tokens or more
     int seq_tiles; // tiles of every sequence: a uniform batch, or the short runs of a packed one (0: by rows of q)
+    int longest_first;  // the mma kernel's sequences by length
 };
 
 // A unit's tokens: cnt of sequence b from its token i on; q0 the sequence's first row of q, n its tokens, len its keys.

@@ -281,6 +281,26 @@ def test_few_rows_many_keys(pa, case):
     _check(pa, c, causal=False, err=pa.ERRBIT_PAGE_RANGE)
 
 
+MANY = [  # sequences, kv heads, G, head_dim, new tokens of each (None: one, but for two that share theirs out), all one length
+    (256, 4, 2, 64, 1, False), (130, 5, 4, 64, 1, True), (200, 4, 1, 128, None, False), (60, 4, 4, 64, 9, False), (33, 19, 3, 256, 1, False)]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_more_sequences_than_fit_at_once(pa, case):
+    """Batches of several waves, whose longest sequences are taken first: lengths of all sizes, none among them, and all
+    alike."""
+    B, Hkv, G, D, new, same = MANY[case]
+    rng = np.random.default_rng(80 + case)
+    lens = np.full(B, 40) if same else np.where(rng.uniform(size=B) < 0.8, rng.integers(0, 120, B), rng.integers(100, 900, B))
+    if not same:
+        lens[rng.integers(0, B)] = 2080
+    count = np.full(B, new or 1)
+    if new is None:
+        count[7], count[B - 1] = 2, 0
+    c = _case(90 + case, lens, count, Hkv, G, D, 16, "bf16", width=130)
+    _check(pa, c, packed=new in (None, 1))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.5, 40.0])
 def test_scales(pa, scale):
     """Also scores up to thousands: one key takes everything, references move far."""
