@@ -497,8 +497,9 @@ int paged_attn_gather_kv4(const void *kv, const int32_t *slots, void *k_out, voi
  * paged_attn_fwd_kv4 — paged_attn_fwd over a 4-bit pool: q [batch, q_len, Hq, D], or packed [T, Hq, D] with
  * q_start [batch + 1], laid out, masked and skipped as for the calls over selected pages (rows at or past
  * q_start[batch] are not written).  q and out are PA_BF16 or PA_F16 (PA_F32: PA_EDTYPE); out is rounded once,
- * lse [tokens, Hq] float32 or NULL; a row without a key gets 0 and -inf.  bf16 queries enter the products as f16
- * numbers, each row moved by a power of two, which is exact but for elements below 2^-28 of the row's largest.  A
+ * lse [tokens, Hq] float32 or NULL; a row without a key gets 0 and -inf.  Queries enter the products as f16
+ * numbers, each row moved by a power of two, which is exact but for elements below 2^-24 of the row's largest (off by at
+ * most 2^-35 of that).  A
  * weight meets V as one f16 number for bf16 (within 2^-11 of it, an eighth of the output's own rounding) and as two for
  * f16 (2^-22), or within 2^-35 of the row's largest.  A page id outside [0, num_pages) reads as zeros and sets
  * PA_ERRBIT_PAGE_RANGE.

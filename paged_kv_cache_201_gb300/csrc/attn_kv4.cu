@@ -8,9 +8,9 @@
 //
 //   * A step is two blocks.  The block of a (page, kv head), codes and scales of K and V, is contiguous; 16 rows of a larger
 //     page land as a page of 16 rows does.
-//   * Codes become f16 operands in registers, (u - 8) x scale / 8, without rounding (kv4.cuh): a shift, a logic
-//     operation and a fused multiply-add for two elements.  The eighth comes back in the score's factor and in
-//     the final division.
+//   * Codes become f16 operands in registers, (u - 8) x scale / 8 or / 128, without rounding (kv4.cuh): a logic
+//     operation and a fused multiply-add for two elements, and a shift for eight.  The shares come back in the queries, in the
+//     score's factor, when the states are written and in the final division.
 //   * K: a lane's 16 (D = 128) bytes are consecutive elements of its key; a register pairs elements d and d + 4, and
 //     so do the query operands.  V: O^T's operand pairs two keys of one element.  A byte permutation of two keys'
 //     words pairs their halves before the codes are taken apart, so V needs no transposition.
@@ -237,9 +237,9 @@ __device__ __forceinline__ uint32_t lds_bytes(uint32_t addr) {
 }
 
 // A query row's D / 4 elements of this lane as f16 operand pairs, pair 4 w + k = elements 8 w + k and 8 w + k + 4.
-// bf16 rows are multiplied by a power of two that brings them into f16; inv is its inverse.  negate: as -q.
+// Returns the factor of their products.  negate: as -q.
 template <typename T, int D>
-__device__ __forceinline__ void load_q(const T *row, bool valid, bool negate, int tq, uint32_t (&w)[D / 8], float &inv) {
+__device__ __forceinline__ float load_q(const T *row, bool valid, bool negate, int tq, uint32_t (&w)[D / 8]) {
     const uint4 *src = reinterpret_cast<const uint4 *>(row + tq * (D / 4));
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -252,18 +252,10 @@ __device__ __forceinline__ void load_q(const T *row, bool valid, bool negate, in
     if (negate)
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) w[i] ^= 0x80008000u;
-    inv = 1.f;
-    if (std::is_same<T, __nv_bfloat16>::value) {
-        float am = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        const float sc = f16_row_scale(am, inv);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) w[i] = bf16x2_to_f16x2_scaled(w[i], sc);
-    }
+    float am = kv4::largest_of<T>(w);
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    return kv4::scale_query<T>(w, am);
 }
 
 template <typename T>
@@ -346,12 +338,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
         const int r = nr * 8 + g;
         const bool valid = r < rows;
         const T *q = static_cast<const T *>(f.q) + (valid ? q_row_offset(f, row_index(r)) : 0);
-        float inv;
-        load_q<T, D>(q, valid, f.scale_log2 < 0.f, tq, qb[nr], inv);
+        const float factor = load_q<T, D>(q, valid, f.scale_log2 < 0.f, tq, qb[nr]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int rc = nr * 8 + 2 * tq + e;
-            srow[nr][e] = fmaxf(8.f * fabsf(f.scale_log2) * __shfl_sync(0xffffffffu, inv, 4 * (2 * tq + e)), kLeastFactor);
+            srow[nr][e] = fmaxf(fabsf(f.scale_log2) * __shfl_sync(0xffffffffu, factor, 4 * (2 * tq + e)), kLeastFactor);
             lim[nr][e] = min(rc < rows ? un.limit(f, rc / un.heads) : INT_MAX, b1 * kBlockKeys);
             all_below = min(all_below, lim[nr][e]);
         }
@@ -397,12 +388,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     // the scale of word w: byte w / 2 of the lane's, in both halves
-                    uint32_t s, c;
-                    kv4::scale_pair(__byte_perm(ksb[hb][i], 0, 0x4040 + (w / 2) * 0x0101), s, c);
+                    const kv4::ScalePair x = kv4::scale_pair(__byte_perm(ksb[hb][i], 0, 0x4040 + (w / 2) * 0x0101));
                     // (word by word: a whole row's at once leaves too few registers, 3 us of 192)
                     uint32_t code[1];
                     lds_words<1>(base + hb * RingT::kBlock + k_off + i * 8 * (D / 2) + 4 * w, code);
-                    kv4::unpack8(code[0], s, c, h[i]);
+                    kv4::unpack8(code[0], x, h[i]);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -478,7 +468,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
             const uint32_t blk = base + hb * RingT::kBlock;
-            uint32_t vw[4][VW], vs[2][VS], vc[2][VS];  // of the keys (va, vb) and (va + 8, vb + 8)
+            uint32_t vw[4][VW];
+            kv4::ScalePair vs[2][VS];  // of the keys (va, vb) and (va + 8, vb + 8)
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) {
                 lds_words<VW>(blk + va_off + kh * 8 * (D / 2), vw[2 * kh]);
@@ -487,7 +478,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
                 const uint32_t b = lds_bytes<VS>(blk + vs_col + (vb + 8 * kh) * (D / 16));
 #pragma unroll
                 for (int i = 0; i < VS; ++i)
-                    kv4::scale_pair(__byte_perm(a, b, 0x3430 + i * 0x0101), vs[kh][i], vc[kh][i]);
+                    vs[kh][i] = kv4::scale_pair(__byte_perm(a, b, 0x3430 + i * 0x0101));
             }
             if (hb == 1) {  // the step is in registers
                 __syncwarp();
@@ -502,7 +493,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 #pragma unroll
                     for (int kh = 0; kh < 2; ++kh)
                         kv4::unpack8(__byte_perm(vw[2 * kh][w], vw[2 * kh + 1][w], half ? 0x7632 : 0x5410),
-                                     vs[kh][w * VS / VW], vc[kh][w * VS / VW], h[kh]);
+                                     vs[kh][w * VS / VW], h[kh]);
 #pragma unroll
                     for (int part = 0; part < kParts; ++part)
 #pragma unroll
@@ -537,7 +528,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 *reinterpret_cast<float2 *>(wa + (nr * 8 + 2 * tq + e) * STRIDE + g * (D / 8) + 2 * mt) =
-                    make_float2(acc[nr][mt][e], acc[nr][mt][2 + e]);
+                    make_float2(kv4::kEvenShare * acc[nr][mt][e], acc[nr][mt][2 + e]);
         if (g == 0) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {

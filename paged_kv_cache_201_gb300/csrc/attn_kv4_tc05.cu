@@ -5,8 +5,8 @@
 // 128-key tiles of its cache, which it turns into f16 once for both:
 //   warp 0       issues tcgen05.mma: S = Q K^T of a tile of rows into 128 columns of tensor memory, then O += P V with P
 //                read from there.  The two tiles of rows take turns, one's products under the other's softmax.
-//   warps 4-7    read codes and scales into registers a tile ahead and write K and V, (u - 8) scale / 8 without rounding
-//                (kv4.cuh), as swizzled f16 tiles, two slots each.  A register pairs elements d and d + 4 of eight, so
+//   warps 4-7    read codes and scales into registers a tile ahead and write K and V, (u - 8) scale / 8 or / 128 without
+//                rounding (kv4.cuh), as swizzled f16 tiles, two slots each.  A register pairs elements d and d + 4 of eight, so
 //                eight elements land in the order 0 4 1 5 2 6 3 7; Q is written in the same one, and the output's
 //                columns are put back when they are stored.
 //   warps 8-15   softmax, a thread a row, warps 8-11 the first tile's: weights as in attn_kv4.cu, P over S as f16 pairs
@@ -22,9 +22,6 @@
 #include "tc05.cuh"
 
 namespace pa {
-
-using mmac::bf16x2_to_f16x2_scaled;
-using mmac::f16_row_scale;
 
 namespace {
 
@@ -97,9 +94,8 @@ struct Codes {
             const uint32_t word[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                uint32_t s, b, h[4];
-                kv4::scale_pair(__byte_perm(scale[i], 0, 0x4040 + (k / 2) * 0x0101), s, b);
-                kv4::unpack8(word[k], s, b, h);
+                uint32_t h[4];
+                kv4::unpack8(word[k], kv4::scale_pair(__byte_perm(scale[i], 0, 0x4040 + (k / 2) * 0x0101)), h);
                 sts16(chunk_at(half, r, (c & 1) * 4 + k), h[0], h[1], h[2], h[3]);
             }
         }
@@ -178,20 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (f.scale_log2 < 0.f)  // as -q: the factor is positive
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] ^= 0x80008000u;
-            float inv = 1.f;
-            if (std::is_same<T, __nv_bfloat16>::value) {
-                float am = 0.f;
+            float am = kv4::largest_of<T>(w);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-#pragma unroll
-                for (int o = 1; o < C; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-                const float sc = f16_row_scale(am, inv);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = bf16x2_to_f16x2_scaled(w[i], sc);
-            }
+            for (int o = 1; o < C; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            const float factor = kv4::scale_query<T>(w, am);
             sts16(chunk_at(sQ(tile) + (uint32_t)(c >> 3) * kHalf, r & 127, c & 7), w[0], w[1], w[2], w[3]);
-            if (c == 0) s_factor[r] = fmaxf(8.f * fabsf(f.scale_log2) * inv, kLeastFactor);
+            if (c == 0) s_factor[r] = fmaxf(fabsf(f.scale_log2) * factor, kLeastFactor);
         }
         fence_proxy_async_smem();
     }
@@ -414,7 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; ++j) o[j] = 0u;
                 }
                 // columns 0 1 2 .. 7 hold elements 0 4 1 5 2 6 3 7
-                auto e = [&](int i, int x) { return __uint_as_float(o[8 * i + (x < 4 ? 2 * x : 2 * x - 7)]); };
+                auto e = [&](int i, int x) {
+                    return (x & 1 ? 1.f : kv4::kEvenShare) * __uint_as_float(o[8 * i + (x < 4 ? 2 * x : 2 * x - 7)]);
+                };
                 if (row >= 0 && p.part_out) {
                     float4 *dst = reinterpret_cast<float4 *>(p.part_out + (part * p.s.n_tok * f.Hq + row) * D + 32 * c);
 #pragma unroll

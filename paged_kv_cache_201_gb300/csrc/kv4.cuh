@@ -8,7 +8,7 @@
 // and bf16 number.
 #pragma once
 
-#include "common.cuh"
+#include "mma_common.cuh"
 
 namespace pa {
 
@@ -57,10 +57,14 @@ __device__ __forceinline__ uint32_t scale_byte(float a) {
     return min(((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3), kMaxScaleByte);
 }
 
-// Eight codes of a word -> four f16 pairs, pair k = codes k and k + 4, as (u - 8) x scale / 8.  s = scale / 128,
-// c = -9 scale: the code, put below the leading bits of an f16 number, reads 1024 + 16 u, and
-// (1024 + 16 u) s + c = (u - 8) scale / 8 in one rounding, which has nothing to round (an f16 number's last bit is
-// 2^-24 at least, the smallest scale's 2^-17).
+// Eight codes of a word -> four f16 pairs, pair k = codes k and k + 4: the odd ones as (u - 8) x scale / 8, the even ones,
+// which lie four bits lower, as (u - 8) x scale / 128.  A code put below the leading bits of an f16 number reads
+// 1024 + 16 u or 1024 + u, and with s = scale / 128, c = -9 scale and d = -8.0625 scale
+//   (1024 + 16 u) s + c = (u - 8) scale / 8,   (1024 + u) s + d = (u - 8) scale / 128
+// in one rounding, which has nothing to round (an f16 number's last bit is 2^-24 at least, the smallest scale's
+// 2^-17; c and d are a scale's four significant bits times 9 and 129).  The missing 16 of the even elements is put into the
+// queries and into the output's columns; bringing the even codes up to the odd ones' place takes two shifts a word
+// (256 sequences 170 us instead of 164).
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -71,26 +75,55 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// (a & 0x00F000F0) | 0x64006400, as the one operation that it is (written in C, nvcc 13.0 makes two of it: 494
+// (a & mask) | 0x64006400, as the one operation that it is (written in C, nvcc 13.0 makes two of it: 494
 // instructions a block of 16 keys instead of 431).
-__device__ __forceinline__ uint32_t code_in_f16(uint32_t a) {
+__device__ __forceinline__ uint32_t code_in_f16(uint32_t a, uint32_t mask) {
     uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(0x00F000F0u), "r"(0x64006400u));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(0x64006400u));
     return d;
 }
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t s, uint32_t c, uint32_t (&h)[4]) {
+constexpr float kEvenShare = 16.f;  // what an even element lacks beside an odd one
+struct ScalePair {  // of two scales, one for each half of a pair
+    uint32_t s, c, d;
+};
+__device__ __forceinline__ void unpack8(uint32_t w, ScalePair x, uint32_t (&h)[4]) {
     const uint32_t v = w >> 8;
-    h[0] = fma2(code_in_f16(w << 4), s, c);
-    h[1] = fma2(code_in_f16(w), s, c);
-    h[2] = fma2(code_in_f16(v << 4), s, c);
-    h[3] = fma2(code_in_f16(v), s, c);
+    h[0] = fma2(code_in_f16(w, 0x000F000Fu), x.s, x.d);
+    h[1] = fma2(code_in_f16(w, 0x00F000F0u), x.s, x.c);
+    h[2] = fma2(code_in_f16(v, 0x000F000Fu), x.s, x.d);
+    h[3] = fma2(code_in_f16(v, 0x00F000F0u), x.s, x.c);
 }
-// Two scale bytes, one in the low byte of each half of x -> the operands s and c of unpack8.
-__device__ __forceinline__ void scale_pair(uint32_t x, uint32_t &s, uint32_t &c) {
+// From two scale bytes, one in the low byte of each half of x.
+__device__ __forceinline__ ScalePair scale_pair(uint32_t x) {
     uint32_t f;
     asm("min.f16x2 %0, %1, %2;" : "=r"(f) : "r"(x << 7), "r"(0x6F006F00u));  // 7168; a NaN's bits give it too
-    s = mul2(f, 0x20002000u);  // 2^-7
-    c = mul2(f, 0xC880C880u);  // -9
+    return {mul2(f, 0x20002000u), mul2(f, 0xC880C880u), mul2(f, 0xC808C808u)};  // 2^-7, -9, -8.0625
+}
+
+// A row of queries in f16: by a power of two into its range, elements that meet odd ones a sixteenth of that.  w: pairs, the
+// even elements' first; largest: the row's largest magnitude.  The result, with the factors of the keys' elements, is
+// to be multiplied by the value returned.
+template <typename T, int N>
+__device__ __forceinline__ float scale_query(uint32_t (&w)[N], float largest) {
+    float inv;
+    const float even = mmac::f16_row_scale(largest, inv), odd = even / kEvenShare;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float2 x = MmaOp<T>::unpack(w[i]);
+        const float f = i & 1 ? odd : even;
+        w[i] = MmaOp<__half>::pack(x.x * f, x.y * f);
+    }
+    return 8.f * kEvenShare * inv;
+}
+template <typename T, int N>
+__device__ __forceinline__ float largest_of(const uint32_t (&w)[N]) {
+    float am = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float2 x = MmaOp<T>::unpack(w[i]);
+        am = fmaxf(am, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    return am;
 }
 
 }  // namespace kv4

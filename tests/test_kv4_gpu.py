@@ -307,6 +307,16 @@ def test_scales(pa, scale):
     _check(pa, _case(12, [150, 31], [3, 1], 2, 4, 128, 16, "bf16"), scale=scale)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16"), (128, "f16"), (256, "bf16")])
+@pytest.mark.parametrize("low,high,scale", [(0, 8, 1000.0), (1, 3, -4000.0), (0xD0, 0x100, 1e-5)])
+def test_smallest_and_largest_scales(pa, low, high, scale, D, dtype):
+    """Scale bytes below the normal numbers and around the largest, single tokens and a run beside them."""
+    c = _case(95 + low, [300, 90, 17, 0], [70, 1, 2, 1], 2, 4, D, 16, dtype)
+    c["pool"][:, :, 16 * D:] = np.random.default_rng(low).integers(low, high, c["pool"][:, :, 16 * D:].shape)
+    c["kv"] = _t(c["pool"])
+    _check(pa, c, scale=scale)
+
+
 def test_strided_queries(pa):
     import torch
     c = _case(13, [80, 40], [5, 2], 2, 4, 128, 16, "bf16")
