@@ -600,14 +600,26 @@ __global__ void __launch_bounds__(128) paged_attn_kv4_join_kernel(const Kv4Param
     const long long row = un.row(f, r), rows = p.s.n_tok * f.Hq;
     const float2 *state = reinterpret_cast<const float2 *>(p.part_state) + row;
     float M = kNoRef, sum = 0.f;
-    for (int x = 0; x < p.S; ++x) M = fmaxf(M, __ldcg(state + x * rows).x);
+    for (int x = threadIdx.x & 31; x < p.S; x += 32) M = fmaxf(M, __ldcg(state + x * rows).x);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x = tg; x < p.S; x += TG) {
-        const float2 st = __ldcg(state + x * rows);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_out + (x * rows + row) * D) + c);
-        const float k = fast_exp2(st.x - M);
-        sum += k * st.y;
-        o.x += k * v.x, o.y += k * v.y, o.z += k * v.z, o.w += k * v.w;
+    constexpr int U = 8;  // parts of a thread on their way together
+    for (int x0 = tg; x0 < p.S; x0 += U * TG) {
+        float2 st[U];
+        float4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int x = min(x0 + i * TG, p.S - 1);
+            st[i] = __ldcg(state + x * rows);
+            v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_out + (x * rows + row) * D) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const float k = x0 + i * TG < p.S ? fast_exp2(st[i].x - M) : 0.f;
+            sum += k * st[i].y;
+            o.x += k * v[i].x, o.y += k * v[i].y, o.z += k * v[i].z, o.w += k * v[i].w;
+        }
     }
     s_o[tg][c] = o;
     if (c == 0) s_l[tg] = sum;
