@@ -21,6 +21,11 @@
 //     two, their shared-memory loads have half the bank conflicts, and K's none.
 //
 // Any byte stands for a finite number, so what lies behind a sequence's last key needs no cleaning: its weight is 0.
+//
+// What bounds it is instructions: 341 a block of 16 keys of 128 and warp, 140 of them on the integer pipe and 135 on the
+// one of multiplications, issued in 67 % of cycles by four warps a scheduler, which wait for those pipes (ncu); memory
+// keeps nobody waiting.  256 sequences of 0.4 to 1 times 4096 tokens (8 kv heads of 128, G = 4, bf16) take 164 us, 5.3 TB/s
+// or 78 % of the copy rate; one of 131072 tokens, as 19 CTAs a kv head, 39 us, 58 %.
 #include <limits.h>
 
 #include <type_traits>
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     constexpr int VS = D == 256 ? 2 : 1;
     using RingT = Ring<D, NST, PAGE16>;
     // Weights of an f16 output as a high part and a remainder, of a bf16 one as the high part alone: its 2^-12 is an
-    // eighth of the output's own rounding (256 sequences 228 -> 205 us).
+    // eighth of the output's own rounding (256 sequences 228 -> 205 us when that was all that changed).
     constexpr int kParts = std::is_same<T, __half>::value ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
     const FwdParams &f = p.s.f;
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
                 for (int i = 0; i < 2; ++i) {
                     // the scale of word w: byte w / 2 of the lane's, in both halves
                     const kv4::ScalePair x = kv4::scale_pair(__byte_perm(ksb[hb][i], 0, 0x4040 + (w / 2) * 0x0101));
-                    // (word by word: a whole row's at once leaves too few registers, 3 us of 192)
+                    // (word by word: a whole row's at once leaves too few registers, 3 us of 192 then)
                     uint32_t code[1];
                     lds_words<1>(base + hb * RingT::kBlock + k_off + i * 8 * (D / 2) + 4 * w, code);
                     kv4::unpack8(code[0], x, h[i]);

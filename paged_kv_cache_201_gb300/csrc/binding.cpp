@@ -2,7 +2,7 @@
 // the current stream and the call, in one step.
 //
 // These calls take a few microseconds on the GPU and up to eleven tensors.  Checked and marshalled in Python, a call costs the
-// host 7 to 10 us, of which its launch is 3; from here 4 to 5.  A function returns the call's status, or None where
+// host 7 to 10 us; from here 2 to 3, most of it the launch.  A function returns the call's status, or None where
 // anything about an argument is not as it should be: the caller then goes the long way, which says what.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -2,6 +2,8 @@
 //
 // A CTA moves chunks of kChunk bytes; the chunks of a pair's page in every pool stand in one row, so that a few pairs
 // already occupy every multiprocessor.  The number of pairs may be on the device: the grid is sized for all and walks.
+// 8192 moves of 64 KB (1.07 GB read and written) take 165 us, 6.5 TB/s or 97 % of the copy rate; four pages of 18 KB in two
+// pools 3.4 us, a launch and two trips to memory.
 #include "kernels.h"
 #include "kv4.cuh"
 

@@ -9,6 +9,12 @@
 // fixed: a page that several rows give back belongs to the smallest place that lists it, found with an atomic
 // minimum in page_shares itself.  A page's count runs from its owners - 1 down; below 0 the page is free, and
 // the places' numbers, INT_MIN + e with e < 2^30, lie below every count that is reached.
+//
+// What bounds them is the chain of dependent trips to memory and of barriers, not bytes.  A fork of 4 rows of 63 pages takes
+// 6.9 us, of 192 rows of some 190 pages 9; 8 rows of some 90 freed 11.5, 1024 rows of some 180 pages 37 (the random reads of
+// page_shares from 16 multiprocessors); a compaction's plan 13 for 2048 pages, 20 for 32768.  The 1024 rows took 122 with
+// places searched for again in every pass and atomics on every page, 45 with a round's places in registers, 16 CTAs instead of
+// 8 and none for pages that nobody shares, 37 with fewer barriers.
 #include <limits.h>
 
 #include "kv4.cuh"
