@@ -65,9 +65,22 @@ __device__ __forceinline__ uint32_t scale_byte(float a) {
 // 2^-17; c and d are a scale's four significant bits times 9 and 129).  The missing 16 of the even elements is put into the
 // queries and into the output's columns; bringing the even codes up to the odd ones' place takes two shifts a word
 // (256 sequences 170 us instead of 164).
+// HALF 0, 1: that half of b and c for both halves of a, which the instruction chooses by itself (as a statement of its own the
+// choice takes a move: 162 us instead of 159).  kPair: each its own.
+constexpr int kPair = -1;
+template <int HALF>
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    if constexpr (HALF == kPair)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    else if constexpr (HALF == 0)
+        asm("{\n\t.reg .b16 p, q, r, t;\n\t.reg .b32 x, y;\n\tmov.b32 {p, q}, %2;\n\tmov.b32 {r, t}, %3;\n\t"
+            "mov.b32 x, {p, p};\n\tmov.b32 y, {r, r};\n\tfma.rn.f16x2 %0, %1, x, y;\n\t}"
+            : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    else
+        asm("{\n\t.reg .b16 p, q, r, t;\n\t.reg .b32 x, y;\n\tmov.b32 {p, q}, %2;\n\tmov.b32 {r, t}, %3;\n\t"
+            "mov.b32 x, {q, q};\n\tmov.b32 y, {t, t};\n\tfma.rn.f16x2 %0, %1, x, y;\n\t}"
+            : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
@@ -86,12 +99,13 @@ constexpr float kEvenShare = 16.f;  // what an even element lacks beside an odd 
 struct ScalePair {  // of two scales, one for each half of a pair
     uint32_t s, c, d;
 };
+template <int HALF = kPair>
 __device__ __forceinline__ void unpack8(uint32_t w, ScalePair x, uint32_t (&h)[4]) {
     const uint32_t v = w >> 8;
-    h[0] = fma2(code_in_f16(w, 0x000F000Fu), x.s, x.d);
-    h[1] = fma2(code_in_f16(w, 0x00F000F0u), x.s, x.c);
-    h[2] = fma2(code_in_f16(v, 0x000F000Fu), x.s, x.d);
-    h[3] = fma2(code_in_f16(v, 0x00F000F0u), x.s, x.c);
+    h[0] = fma2<HALF>(code_in_f16(w, 0x000F000Fu), x.s, x.d);
+    h[1] = fma2<HALF>(code_in_f16(w, 0x00F000F0u), x.s, x.c);
+    h[2] = fma2<HALF>(code_in_f16(v, 0x000F000Fu), x.s, x.d);
+    h[3] = fma2<HALF>(code_in_f16(v, 0x00F000F0u), x.s, x.c);
 }
 // From two scale bytes, one in the low byte of each half of x.
 __device__ __forceinline__ ScalePair scale_pair(uint32_t x) {
