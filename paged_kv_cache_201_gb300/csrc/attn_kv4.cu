@@ -22,10 +22,10 @@
 //
 // Any byte stands for a finite number, so what lies behind a sequence's last key needs no cleaning: its weight is 0.
 //
-// What bounds it is instructions: 341 a block of 16 keys of 128 and warp, 140 of them on the integer pipe and 135 on the
-// one of multiplications, issued in 67 % of cycles by four warps a scheduler, which wait for those pipes (ncu); memory
-// keeps nobody waiting.  256 sequences of 0.4 to 1 times 4096 tokens (8 kv heads of 128, G = 4, bf16) take 164 us, 5.3 TB/s
-// or 78 % of the copy rate; one of 131072 tokens, as 19 CTAs a kv head, 39 us, 58 %.
+// What bounds it is instructions: 322 a block of 16 keys of 128 and warp, 134 of them on the integer pipe and 124 on the
+// one of multiplications, issued in 66 % of cycles by four warps a scheduler, which wait for those pipes (ncu); memory
+// keeps nobody waiting.  256 sequences of 0.4 to 1 times 4096 tokens (8 kv heads of 128, G = 4, bf16) take 159 us, 5.4 TB/s
+// or 81 % of the copy rate; one of 131072 tokens, as 19 CTAs a kv head, 38 us, 59 %.
 #include <limits.h>
 
 #include <type_traits>
