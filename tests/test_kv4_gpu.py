@@ -301,6 +301,17 @@ def test_more_sequences_than_fit_at_once(pa, case):
     _check(pa, c, packed=new in (None, 1))
 
 
+def test_many_single_tokens_beside_runs(pa):
+    """Both kernels at once, the second over the short runs of a batch of several waves."""
+    rng = np.random.default_rng(99)
+    B = 130
+    new = np.where(np.arange(B) % 40 == 7, 200, rng.integers(0, 4, B))
+    lens = np.where(new == 200, 400, rng.integers(0, 200, B))
+    lens[3] = 2080
+    lens = np.maximum(lens, new)
+    _check(pa, _case(99, lens, new, 4, 8, 64, 16, "bf16", pads=3, width=130))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.5, 40.0])
 def test_scales(pa, scale):
     """Also scores up to thousands: one key takes everything, references move far."""
