@@ -127,6 +127,7 @@ __device__ __forceinline__ void for_places(const int *s_start, int n, int total,
     for (int first = e0; first < e1; first += 32 * PT) {
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
+            if (first + 32 * k >= e1) break;
             const int e = first + 32 * k + (threadIdx.x & 31);
             if (e < e1) {
                 lo = list_of(s_start, n, e, lo);
@@ -134,7 +135,10 @@ __device__ __forceinline__ void for_places(const int *s_start, int n, int total,
             }
         }
 #pragma unroll
-        for (int k = 0; k < PT; ++k) use(k, first + 32 * k + (int)(threadIdx.x & 31) < e1);
+        for (int k = 0; k < PT; ++k) {
+            if (first + 32 * k >= e1) break;
+            use(k, first + 32 * k + (int)(threadIdx.x & 31) < e1);
+        }
     }
 }
 
@@ -327,59 +331,79 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
         const int first = r * round, size = min(round, total.a - first);
         const int run = ((size + warps_all - 1) / warps_all + 31) & ~31;  // of a warp, at most 32 PT
         const int e0 = first + min(warp_all * run, size) + lane, e1 = first + min(warp_all * run + run, size);
+        const int turns = run / 32;  // of a lane: all loops end there (few places would pay for sixteen otherwise)
         int id[PT], before[PT];
         int lo = 0;
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
+            if (k >= turns) break;
             const int e = e0 + 32 * k;
             id[k] = -1;
             if (e >= e1) continue;
             lo = list_of(s_start, p.n, e, lo);
             id[k] = __ldg(p.block_table + (long long)s_row[lo] * p.W + e - s_start[lo]);
+        }
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {  // only now: the loads above are on their way together
+            if (k >= turns) break;
             if (id[k] < 0 || id[k] >= p.num_pages) {
-                bad_page = true;
+                bad_page |= e0 + 32 * k < e1;
                 id[k] = -1;
             }
         }
         unsigned push = 0, shared = 0;  // bits of this lane's places
 #pragma unroll
-        for (int k = 0; k < PT; ++k) before[k] = id[k] >= 0 ? __ldcg(p.shares + id[k]) : 0;
+        for (int k = 0; k < PT; ++k) {
+            if (k >= turns) break;
+            before[k] = id[k] >= 0 ? __ldcg(p.shares + id[k]) : 0;
+        }
 #pragma unroll
-        for (int k = 0; k < PT; ++k)
+        for (int k = 0; k < PT; ++k) {
+            if (k >= turns) break;
             if (id[k] >= 0) (before[k] == 0 ? push : shared) |= 1u << k;
+        }
         const int number = r + 1;
         if (__any_sync(0xffffffffu, shared) && lane < ctas)
             asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(smem_u32(&s_any), lane)), "r"(number) : "memory");
         sync_all(ctas);  // every count is read as it was, and the lengths
         if (*(volatile int *)&s_any == number) {
 #pragma unroll
-            for (int k = 0; k < PT; ++k)
+            for (int k = 0; k < PT; ++k) {
+                if (k >= turns) break;
                 if (shared >> k & 1) atomicSub(p.shares + id[k], 1);
+            }
             sync_all(ctas);
             // the first place of every page that is free now
 #pragma unroll
-            for (int k = 0; k < PT; ++k)
+            for (int k = 0; k < PT; ++k) {
+                if (k >= turns) break;
                 if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
+            }
 #pragma unroll
             for (int k = 0; k < PT; ++k) {
+                if (k >= turns) break;
                 if ((shared >> k & 1) && before[k] >= 0) shared &= ~(1u << k);
                 if (shared >> k & 1) atomicMin(p.shares + id[k], INT_MIN + e0 + 32 * k);
             }
             sync_all(ctas);
 #pragma unroll
-            for (int k = 0; k < PT; ++k)
+            for (int k = 0; k < PT; ++k) {
+                if (k >= turns) break;
                 if (shared >> k & 1) before[k] = __ldcg(p.shares + id[k]);
+            }
         }
         Pair n_mine{0, 0}, pushed;
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
+            if (k >= turns) break;
             if ((shared >> k & 1) && before[k] == INT_MIN + e0 + 32 * k) push |= 1u << k;
-            n_mine.a += __popc(__ballot_sync(0xffffffffu, push >> k & 1));
         }
+        n_mine.a = __reduce_add_sync(0xffffffffu, __popc(push));
         int at = cluster_scan(n_mine, warp_sums, &s_cta, ctas, rank, pushed).a;
         top += pushed.a;
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
+            if (k >= turns) break;
             const unsigned all = __ballot_sync(0xffffffffu, push >> k & 1);
             if (push >> k & 1) {
                 const long long to = top - 1 - (at + __popc(all & ((1u << lane) - 1)));
