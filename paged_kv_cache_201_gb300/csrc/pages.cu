@@ -10,11 +10,12 @@
 // minimum in page_shares itself.  A page's count runs from its owners - 1 down; below 0 the page is free, and
 // the places' numbers, INT_MIN + e with e < 2^30, lie below every count that is reached.
 //
-// What bounds them is the chain of dependent trips to memory and of barriers, not bytes.  A fork of 4 rows of 63 pages takes
-// 6.9 us, of 192 rows of some 190 pages 9; 8 rows of some 90 freed 11.5, 1024 rows of some 180 pages 35 (the random reads of
-// page_shares from 16 multiprocessors); a compaction's plan 13 for 2048 pages, 20 for 32768.  The 1024 rows took 122 with
-// places searched for again in every pass and atomics on every page, 45 with a round's places in registers, 16 CTAs instead of
-// 8 and none for pages that nobody shares, 35 with fewer barriers and no wait for the last stores.
+// What bounds them is the chain of dependent trips to memory and of barriers, not bytes.  A prompt of 63 pages forked to
+// 4 rows, copied and freed takes 10.6 us, 192 rows of some 190 pages 25; 8 rows of some 90 freed 7.5, 1024 rows of some 180 pages
+// 35 (the random reads of page_shares from 16 multiprocessors); a compaction's plan 12 for 2048 pages, 20 for 32768.  The 1024
+// rows took 122 with places searched for again in every pass and atomics on every page, 45 with a round's places in registers,
+// 16 CTAs instead of 8 and none for pages that nobody shares, 35 with fewer barriers and no wait for the last stores.  The 8 rows
+// took 4 us more while every warp went through all sixteen turns of a round.
 #include <limits.h>
 
 #include "kv4.cuh"
@@ -596,16 +597,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_compact_kernel(const P
 
 namespace {
 
-// A cluster for `work` pages at most, which the tables' width makes of rows.
+// A cluster for `work` pages at most, which the tables' width makes of rows: one CTA up to `alone` (its barrier is its own), from
+// there four and more, `per` pages each.  Two are never better than one or four: 32 rows of up to 126 pages freed 10.4 us by
+// one, 12.4 by two, 10.5 by four; 64 of up to 251 14.5 by one, 12.4 by sixteen; a compaction of 2048 pages with its copies 25.6
+// by one, 27.6 by two, of 6000 39.0 by one, 37.7 by four.
 struct ClusterLimit {
     SmemLimit smem, wide;
 };
 template <typename K>
-cudaError_t launch_cluster(K kern, ClusterLimit &limit, size_t smem, size_t smem_max, long long work, int most,
-                           const PagesParams &p, cudaStream_t stream) {
+cudaError_t launch_cluster(K kern, ClusterLimit &limit, size_t smem, size_t smem_max, long long work, long long alone, long long per,
+                           int most, const PagesParams &p, cudaStream_t stream) {
     cudaError_t e = limit.smem.raise((const void *)kern, smem_max);
-    int ctas = 1;
-    while (ctas < most && ctas * 2048ll < work) ctas *= 2;
+    int ctas = work <= alone ? 1 : 4;
+    while (ctas > 1 && ctas < most && ctas * per < work) ctas *= 2;
     if (e == cudaSuccess && ctas > 8) e = limit.wide.allow_wide_clusters((const void *)kern);
     if (e != cudaSuccess) return e;
     return launch_behind(kern, dim3(ctas), kThreads, smem, ctas, stream, p);
@@ -619,7 +623,8 @@ template <int PER>
 static cudaError_t launch_fork_n(const PagesParams &p, cudaStream_t stream) {
     static ClusterLimit limit;
     return launch_cluster(paged_attn_fork_kernel<PER>, limit, lists_smem(p.n, p.B),
-                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, kWideCtas, p, stream);
+                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, 2048, 1024, kWideCtas, p,
+                          stream);
 }
 cudaError_t launch_fork(const PagesParams &p, cudaStream_t stream) {
     return p.n <= kThreads ? launch_fork_n<1>(p, stream) : launch_fork_n<kPer>(p, stream);
@@ -629,7 +634,8 @@ template <int PER>
 static cudaError_t launch_free_n(const PagesParams &p, cudaStream_t stream) {
     static ClusterLimit limit;
     return launch_cluster(paged_attn_free_kernel<PER>, limit, lists_smem(p.n, p.B),
-                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, kWideCtas, p, stream);
+                          lists_smem((long long)kThreads * PER, PA_STEP_MAX_BATCH), (long long)p.n * p.W, 2048, 1024, kWideCtas, p,
+                          stream);
 }
 cudaError_t launch_free(const PagesParams &p, cudaStream_t stream) {
     return p.n <= kThreads ? launch_free_n<1>(p, stream) : launch_free_n<kPer>(p, stream);
@@ -640,8 +646,8 @@ static cudaError_t launch_compact_n(const PagesParams &p, cudaStream_t stream) {
     static ClusterLimit limit;
     const long long entries = (long long)p.B * p.W;
     return launch_cluster(paged_attn_compact_kernel<PER>, limit, (size_t)(p.B + 1) * sizeof(int),
-                          ((size_t)kThreads * PER + 1) * sizeof(int), entries > p.num_pages ? entries : p.num_pages, kMaxCtas, p,
-                          stream);
+                          ((size_t)kThreads * PER + 1) * sizeof(int), entries > p.num_pages ? entries : p.num_pages, 4096, 2048,
+                          kMaxCtas, p, stream);
 }
 cudaError_t launch_compact(const PagesParams &p, cudaStream_t stream) {
     return p.B <= kThreads ? launch_compact_n<1>(p, stream) : launch_compact_n<kPer>(p, stream);
