@@ -500,8 +500,7 @@ int paged_attn_gather_kv4(const void *kv, const int32_t *slots, void *k_out, voi
  * lse [tokens, Hq] float32 or NULL; a row without a key gets 0 and -inf.  Queries enter the products as f16
  * numbers, each row moved by a power of two, which is exact but for elements below 2^-24 of the row's largest (off by at
  * most 2^-35 of that).  A
- * weight meets V as one f16 number for bf16 (within 2^-11 of it, an eighth of the output's own rounding) and as two for
- * f16 (2^-22), or within 2^-35 of the row's largest.  A page id outside [0, num_pages) reads as zeros and sets
+ * weight meets V as two f16 numbers (within 2^-22 of it, or 2^-35 of the row's largest).  A page id outside [0, num_pages) reads as zeros and sets
  * PA_ERRBIT_PAGE_RANGE.
  * workspace (device, 16-byte aligned, workspace_bytes long) lets few rows over long sequences use the whole GPU, their keys
  * shared by any number of CTAs and joined by a second launch; with NULL, or less than paged_attn_kv4_workspace_bytes,

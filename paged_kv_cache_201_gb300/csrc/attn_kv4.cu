@@ -17,6 +17,10 @@
 //   * Softmax statistics are float32.  A weight is 2^(score - ref), ref at least 11 below the largest score so far
 //     when it was last moved and never more than 15 below any: weights stay below 2^15, ref (and with it every sum)
 //     moves rarely, and in f16 nothing above 2^-36 of the row's largest weight is lost.
+//   * A weight is an f16 high part plus its remainder, within 2^-22 of it: where the values cancel, a high part alone (2^-12)
+//     leaves outputs up to 40 half steps of bf16 off.  Units of up to four rows (single tokens of G <= 4) have the
+//     remainders' products in columns that nobody else uses: 256 sequences take 164 us, with two products 183, with the
+//     high parts alone 159.
 //   * The rows of S^T are keys r ^ (r >> 1 & 1): with the four keys of a V load in different rows modulo
 //     two, their shared-memory loads have half the bank conflicts, and K's none.
 //
@@ -24,11 +28,9 @@
 //
 // What bounds it is instructions: 322 a block of 16 keys of 128 and warp, 134 of them on the integer pipe and 124 on the
 // one of multiplications, issued in 66 % of cycles by four warps a scheduler, which wait for those pipes (ncu); memory
-// keeps nobody waiting.  256 sequences of 0.4 to 1 times 4096 tokens (8 kv heads of 128, G = 4, bf16) take 159 us, 5.4 TB/s
-// or 81 % of the copy rate; one of 131072 tokens, as 19 CTAs a kv head, 38 us, 59 %.
+// keeps nobody waiting.  256 sequences of 0.4 to 1 times 4096 tokens (8 kv heads of 128, G = 4, bf16) take 164 us, 5.2 TB/s
+// or 78 % of the copy rate; one of 131072 tokens, as 19 CTAs a kv head, 39 us, 58 %.
 #include <limits.h>
-
-#include <type_traits>
 
 #include "kv4.cuh"
 #include "kv4_tile.cuh"
@@ -283,8 +285,12 @@ __host__ __device__ constexpr size_t merge_bytes(int D, int R, int warps) {
 }
 __host__ __device__ constexpr int ring_slots(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 
-template <typename T, int D, int NR, int NW, int MINB, bool PAGE16>
+// HALF: the unit has four rows at most, and columns c and c + 4 of the products are row c: the same scores twice, then the
+// weights' high parts in the first four columns and the remainders in the others, in one product.
+template <typename T, int D, int NR, int NW, int MINB, bool PAGE16, bool HALF>
 __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4Params p, int ps_shift) {
+    static_assert(!HALF || NR == 1, "four rows are one tile of eight columns");
+    constexpr int kParts = HALF ? 1 : 2;  // products of V and the weights
     using Op = MmaOp<__half>;
     constexpr int R = 8 * NR, NST = ring_slots(D), kThreads = NW * 32;
     constexpr int MT = D / 16;  // 16-wide head-dim tiles of O^T
@@ -293,9 +299,6 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     constexpr int KS = D / 64;  // K scales of a lane's part
     constexpr int VS = D == 256 ? 2 : 1;
     using RingT = Ring<D, NST, PAGE16>;
-    // Weights of an f16 output as a high part and a remainder, of a bf16 one as the high part alone: its 2^-12 is an
-    // eighth of the output's own rounding (256 sequences 228 -> 205 us when that was all that changed).
-    constexpr int kParts = std::is_same<T, __half>::value ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
     const FwdParams &f = p.s.f;
     if (!p.s.group_min) wait_for_stream();  // else beside the tcgen05 kernel, which came behind the stream's others
@@ -340,13 +343,13 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     int all_below = b1 * kBlockKeys;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
-        const int r = nr * 8 + g;
+        const int r = HALF ? g & 3 : nr * 8 + g;
         const bool valid = r < rows;
         const T *q = static_cast<const T *>(f.q) + (valid ? q_row_offset(f, row_index(r)) : 0);
         const float factor = load_q<T, D>(q, valid, f.scale_log2 < 0.f, tq, qb[nr]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int rc = nr * 8 + 2 * tq + e;
+            const int rc = HALF ? (2 * tq + e) & 3 : nr * 8 + 2 * tq + e;
             srow[nr][e] = fmaxf(fabsf(f.scale_log2) * __shfl_sync(0xffffffffu, factor, 4 * (2 * tq + e)), kLeastFactor);
             lim[nr][e] = min(rc < rows ? un.limit(f, rc / un.heads) : INT_MAX, b1 * kBlockKeys);
             all_below = min(all_below, lim[nr][e]);
@@ -465,10 +468,13 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 #pragma unroll
                 for (int kh = 0; kh < 2; ++kh) {
                     const uint32_t hi = Op::pack(w[2 * kh], w[2 * kh + 1]);
-                    pb[hb][nr][0][kh] = movmatrix_trans(hi);
-                    if (kParts == 2) {
-                        const float2 x = Op::unpack(hi);
-                        pb[hb][nr][kParts - 1][kh] = movmatrix_trans(Op::pack(w[2 * kh] - x.x, w[2 * kh + 1] - x.y));
+                    const float2 x = Op::unpack(hi);
+                    const uint32_t lo = Op::pack(w[2 * kh] - x.x, w[2 * kh + 1] - x.y);
+                    if constexpr (HALF) {
+                        pb[hb][nr][0][kh] = movmatrix_trans(tq < 2 ? hi : lo);
+                    } else {
+                        pb[hb][nr][0][kh] = movmatrix_trans(hi);
+                        pb[hb][nr][1][kh] = movmatrix_trans(lo);
                     }
                 }
             }
@@ -523,6 +529,12 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
             l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
             l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
         }
+    if constexpr (HALF) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][mt][i] += __shfl_xor_sync(0xffffffffu, acc[0][mt][i], 2);
+    }
     // ---- the warps' states: tile mt's rows g and g + 8 are elements g D / 8 + 2 mt and the next
     float *sm = reinterpret_cast<float *>(smem);
     constexpr int STRIDE = D + 4;
@@ -531,6 +543,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
     float *wa = sm + warp * R * STRIDE;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
+        if (HALF && tq >= 2) break;  // rows 0 .. 3
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -649,6 +662,7 @@ struct Plan {
     int S;
     bool grid;  // S of the grid's CTAs, joined by a second launch; else a cluster
     bool longest_first;
+    bool half;  // units of four rows at most
 };
 Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
     const FwdParams &f = sp.f;
@@ -660,6 +674,7 @@ Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
     const int ctas = f.D == 256 ? 2 : a.nr == 2 ? 3 : 4;                  // CTAs that do otherwise
     a.HT = (f.G + R - 1) / R;
     a.TT = f.q_start && sp.n_tok <= f.B ? 1 : f.G < R ? R / f.G : 1;
+    a.half = a.nr == 1 && f.G * (f.q_start ? a.TT : a.TT < f.Sq ? a.TT : f.Sq) <= 4;
     long long tiles;
     if (!f.q_start || sp.by_seq) {
         a.seq_tiles = ((f.q_start ? sp.group_min - 1 : f.Sq) + a.TT - 1) / a.TT;
@@ -701,7 +716,7 @@ Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
     return a;
 }
 
-template <typename T, int D, int NR, int NW, int MINB>
+template <typename T, int D, int NR, int NW, int MINB, bool HALF>
 cudaError_t launch_kv4(Kv4Params p, const Plan &a, cudaStream_t stream) {
     constexpr int R = 8 * NR;
     constexpr size_t ring = (size_t)NW * ring_slots(D) * 2 * kv4::block_bytes(kBlockKeys, D);
@@ -719,7 +734,7 @@ cudaError_t launch_kv4(Kv4Params p, const Plan &a, cudaStream_t stream) {
     }
     const bool page16 = f.ps == kBlockKeys;
     const int ps_shift = f.ps == 16 ? 4 : f.ps == 32 ? 5 : 6;
-    auto kern = page16 ? paged_attn_kv4_kernel<T, D, NR, NW, MINB, true> : paged_attn_kv4_kernel<T, D, NR, NW, MINB, false>;
+    auto kern = page16 ? paged_attn_kv4_kernel<T, D, NR, NW, MINB, true, HALF> : paged_attn_kv4_kernel<T, D, NR, NW, MINB, false, HALF>;
     static SmemLimit limits[2];
     cudaError_t e = limits[page16].raise((const void *)kern, smem);
     if (e != cudaSuccess) return e;
@@ -728,14 +743,20 @@ cudaError_t launch_kv4(Kv4Params p, const Plan &a, cudaStream_t stream) {
     return launch_behind(paged_attn_kv4_join_kernel<T, D>, dim3((unsigned)(a.units * R)), 128, 0, 1, stream, p, R, ps_shift);
 }
 
+template <typename T, int D, bool HALF>
+cudaError_t launch_kv4_rows8(const Kv4Params &p, const Plan &a, cudaStream_t stream) {
+    if constexpr (D == 256)
+        return a.warps == 8 ? launch_kv4<T, D, 1, 8, 1, HALF>(p, a, stream) : launch_kv4<T, D, 1, 4, 2, HALF>(p, a, stream);
+    else
+        return a.warps == 16 ? launch_kv4<T, D, 1, 16, 1, HALF>(p, a, stream) : launch_kv4<T, D, 1, 4, 4, HALF>(p, a, stream);
+}
+
 template <typename T, int D>
 cudaError_t launch_kv4_d(const Kv4Params &p, const Plan &a, cudaStream_t stream) {
-    if constexpr (D == 256) {
-        return a.warps == 8 ? launch_kv4<T, D, 1, 8, 1>(p, a, stream) : launch_kv4<T, D, 1, 4, 2>(p, a, stream);
-    } else {
-        if (a.nr == 2) return a.warps == 12 ? launch_kv4<T, D, 2, 12, 1>(p, a, stream) : launch_kv4<T, D, 2, 4, 3>(p, a, stream);
-        return a.warps == 16 ? launch_kv4<T, D, 1, 16, 1>(p, a, stream) : launch_kv4<T, D, 1, 4, 4>(p, a, stream);
-    }
+    if constexpr (D != 256)
+        if (a.nr == 2)
+            return a.warps == 12 ? launch_kv4<T, D, 2, 12, 1, false>(p, a, stream) : launch_kv4<T, D, 2, 4, 3, false>(p, a, stream);
+    return a.half ? launch_kv4_rows8<T, D, true>(p, a, stream) : launch_kv4_rows8<T, D, false>(p, a, stream);
 }
 
 template <typename T>

@@ -9,19 +9,19 @@
 //                rounding (kv4.cuh), as swizzled f16 tiles, two slots each.  A register pairs elements d and d + 4 of eight, so
 //                eight elements land in the order 0 4 1 5 2 6 3 7; Q is written in the same one, and the output's
 //                columns are put back when they are stored.
-//   warps 8-15   softmax, a thread a row, warps 8-11 the first tile's: weights as in attn_kv4.cu, P over S as f16 pairs
-//                (with remainders for f16 outputs), O rescaled in tensor memory when a reference moves.
+//   warps 8-15   softmax, a thread a row, warps 8-11 the first tile's: weights as in attn_kv4.cu, P over S as f16 pairs of
+//                high parts and remainders, O rescaled in tensor memory when a reference moves.
 // Q is read, moved into f16's range row by row and written swizzled by all warps at the start.  Any byte of the cache is
 // a finite number, so keys past a row's limit are only left out of its weights.
 //
-// Two tiles of rows over 128 keys are 16.8 MFLOP, 1.35 us of a multiprocessor at the GPU's measured bf16 rate; they take 1.75,
-// the tensor pipe active in 80 % of a busy multiprocessor's cycles.  Two chunks of 512 tokens behind some 8000 (8 kv heads of
-// 128, G = 4, bf16) are 128 CTAs of up to 64 such steps, one wave on 152 multiprocessors: 121 us, against 497 of the
-// mma.sync kernel.  Measured no faster: codes turned by seven warps instead of four (129), S read twice instead of held in
-// registers (139), page ids looked up a tile earlier (147), P handed over in halves (149), K and V in halves of 64 keys (172).
+// Two tiles of rows over 128 keys are 16.8 MFLOP and 8.4 more for the remainders, 2.0 us of a multiprocessor at the GPU's measured
+// bf16 rate; they take 2.5.  Chunks of 512 and 419 tokens over 8192 and 5720 keys (8 kv heads of 128, G = 4, bf16) are 120
+// CTAs of up to 64 such steps, one wave on 152 multiprocessors: 162 us.  Two of 512 over 8192 keys take 178, the mma.sync kernel
+// 714.  With the high parts alone the first take 126, and where the values cancel the outputs are up to 6 half steps of
+// bf16 off.  Measured no faster, then against 121: codes turned by seven warps instead of four (129), S read twice instead of
+// held in registers (139), page ids looked up a tile earlier (147), P handed over in halves (149), K and V in halves of 64
+// keys (172).
 #include <limits.h>
-
-#include <type_traits>
 
 #include "kv4_tile.cuh"
 #include "mma_common.cuh"
@@ -115,7 +115,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kv4_tc05_kernel(const Kv4Params p, int ps_shift, uint32_t idesc_qk, uint32_t idesc_pv) {
     using Op = MmaOp<__half>;
     constexpr int NH = D / 64, kTile = NH * kHalf;  // bytes of a tile of Q, K or V
-    constexpr int kParts = std::is_same<T, __half>::value ? 2 : 1;  // of a weight
     const FwdParams &f = p.s.f;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[B_COUNT];
@@ -226,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {  // keys 16 kk .. + 15
                         const uint32_t vlo = dv + (uint32_t)kk * (2048u >> 4);
-                        const uint32_t pa = pcol + (kParts == 1 ? 8u * (uint32_t)kk : 32u * (uint32_t)(kk >> 1) + 8u * (uint32_t)(kk & 1));
+                        const uint32_t pa = pcol + 32u * (uint32_t)(kk >> 1) + 8u * (uint32_t)(kk & 1);
                         tc05::mma_ts_lh(o, pa, vlo, dhi, idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
-                        if (kParts == 2) tc05::mma_ts_lh(o, pa + 16u, vlo, dhi, idesc_pv, 1u);
+                        tc05::mma_ts_lh(o, pa + 16u, vlo, dhi, idesc_pv, 1u);  // the remainders
                     }
                     if (tile == 1) tc05::commit(bar(B_VE + (t & 1)));
                     tc05::commit(bar(B_PD + tile));  // the last one is waited for before the CTA ends
@@ -377,13 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
                     l2 = add2f(l2, make_float2(w0, w1));
                     hi[j] = Op::pack(w0, w1);
-                    if (kParts == 2) {
-                        const float2 h = Op::unpack(hi[j]);
-                        lo[j] = Op::pack(w0 - h.x, w1 - h.y);
-                    }
+                    const float2 h = Op::unpack(hi[j]);
+                    lo[j] = Op::pack(w0 - h.x, w1 - h.y);
                 }
-                tc05::st_16cols(sbuf + (kParts == 1 ? 16u : 32u) * i, hi);
-                if (kParts == 2) tc05::st_16cols(sbuf + 32u * i + 16u, lo);
+                tc05::st_16cols(sbuf + 32u * i, hi);
+                tc05::st_16cols(sbuf + 32u * i + 16u, lo);
             }
             tc05::wait_st();
             tc05::fence_before_sync();
