@@ -283,6 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
     __shared__ int s_any;  // rounds (from 1) whose pages somebody shares
     const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x, rank = blockIdx.x;
     const int warp_all = rank * kWarps + (tid >> 5), warps_all = ctas * kWarps;
+    // No CTA stores into a peer's s_any before that peer runs and has cleared it: the wait stands before the rounds.
+    if (tid == 0) s_any = 0;
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     const int per = (p.n + kThreads - 1) / kThreads;
     const int i0 = min(tid * per, p.n), mine = min(per, p.n - i0);
     bool refused = false, clipped = false, bad_page = false;
@@ -310,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
         pages[k] = row[k] >= 0 ? pages_of(p, __ldcg(p.seq_lens + row[k]), clipped) : 0;
         sum.a += pages[k];
     }
-    if (tid == 0) s_any = 0;
     Pair run = block_scan(sum, warp_sums, total);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -321,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_free_kernel(const Page
     }
     if (tid == 0) s_start[p.n] = total.a;
     __syncthreads();
+    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     if (rank == 0 && p.lens_out != p.seq_lens)  // the rows' zeros follow behind a barrier
         for (int b = tid; b < p.B; b += kThreads) p.lens_out[b] = p.seq_lens[b];
     // Rounds of at most PT places a lane, the last places first, as the rows end one after the other: a page is pushed in
