@@ -1224,15 +1224,37 @@ def _made(stream, device, *wanted):
     return made
 
 
+COPY_MAX_POOLS = 192  # PA_COPY_MAX_POOLS
+
+
+def _pool_groups(pools, block_table, page_shares):
+    """The pools in lists that a call of ``paged_attn_copy_pages`` takes.  Whatever it would refuse is refused here, before
+    the tables change: a page whose contents stayed behind could not be found again."""
+    pools = list(pools)
+    if _short().check_pools(pools, block_table, page_shares) is None:
+        dev, P = _device_of(block_table, "block_table"), page_shares.numel()
+        for i, t in enumerate(pools):
+            if t.get_device() != dev or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != P or P == 0:
+                raise ValueError(f"pools[{i}] must be a dense tensor [{P}, ...], a page for every count of page_shares, on the "
+                                 f"current CUDA device {dev}")
+            size = t.numel() // P * t.element_size()
+            if size < 4 or size % 4 or size >= 2**31 or t.data_ptr() % 4:
+                raise ValueError(f"pools[{i}] must have pages of a multiple of 4 bytes below 2^31, 4-byte aligned")
+    return [pools[i:i + COPY_MAX_POOLS] for i in range(0, len(pools), COPY_MAX_POOLS)]
+
+
 def fork_sequences(parents, children, block_table, seq_lens, page_shares, free_pages, free_count, pools, page_size: int,
                    prefix_lens=None, stream=None):
-    """``paged_attn_fork`` and the copies of the last pages in every pool of the list; seq_lens and free_count are
-    updated in place.  Returns the pairs that were copied, [n, 2]."""
+    """``paged_attn_fork`` and the copies of the last pages in every pool of the list (of any length, or empty: the caller
+    copies); seq_lens and free_count are updated in place.  Returns the pairs that were copied, [n, 2].  A call that is refused
+    has changed nothing."""
     torch = _torch()
+    groups = _pool_groups(pools, block_table, page_shares)
     copies, = _made(stream, block_table.device, ((parents.shape[0], 2), torch.int32))
     paged_attn_fork(parents, children, block_table, seq_lens, seq_lens, page_shares, free_pages, free_count, free_count,
                     copies, page_size, prefix_lens, stream)
-    paged_attn_copy_pages(pools, copies, None, stream)
+    for group in groups:
+        paged_attn_copy_pages(group, copies, None, stream)
     return copies
 
 
@@ -1243,12 +1265,14 @@ def free_sequences(rows, block_table, seq_lens, page_shares, free_pages, free_co
 
 
 def compact_pages(block_table, seq_lens, page_shares, free_pages, free_count, pools, page_size: int, stream=None):
-    """``paged_attn_compact`` and the moves of the contents in every pool of the list.  Returns (page_map, n_moves):
-    every page's new id, and how many pages moved (a tensor)."""
+    """``paged_attn_compact`` and the moves of the contents in every pool of the list (of any length, or empty).  Returns
+    (page_map, n_moves): every page's new id, and how many pages moved (a tensor).  A call that is refused has changed nothing."""
     torch = _torch()
+    groups = _pool_groups(pools, block_table, page_shares)
     P = page_shares.shape[0]
     moves, n_moves, page_map = _made(stream, block_table.device, ((P // 2, 2), torch.int32), (1, torch.int32), (P, torch.int32))
     paged_attn_compact(block_table, seq_lens, page_shares, free_pages, free_count, moves, n_moves, page_map, page_size,
                        stream)
-    paged_attn_copy_pages(pools, moves, n_moves, stream)
+    for group in groups:
+        paged_attn_copy_pages(group, moves, n_moves, stream)
     return page_map, n_moves

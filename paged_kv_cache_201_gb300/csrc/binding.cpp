@@ -221,6 +221,25 @@ int compact_rows(PyObject *const *a) {
                               stream_of(a[9], p.dev));
 }
 
+// Bytes of a page of pool `t`, dense and of P pages on this device.
+int64_t page_bytes(const at::Tensor &t, int dev, int64_t P) {
+    if (t.dim() < 2 || !t.is_cuda() || t.get_device() != dev || !t.is_contiguous() || P < 1 || t.size(0) != P) throw Refused{};
+    return t.numel() / P * (int64_t)t.element_size();
+}
+
+// check_pools(pools, block_table, page_shares): 0 if paged_attn_copy_pages takes them all, in lists of any length
+int check_pools(PyObject *const *a) {
+    const at::Tensor &shares = tensor(a[2]);
+    if (!PyList_Check(a[0]) || shares.dim() != 1) throw Refused{};
+    const int dev = this_device(tensor(a[1]));
+    for (Py_ssize_t i = 0; i < PyList_GET_SIZE(a[0]); ++i) {
+        const at::Tensor &t = tensor(PyList_GET_ITEM(a[0], i));
+        const int64_t bytes = page_bytes(t, dev, shares.size(0));
+        if (bytes < 4 || bytes % 4 != 0 || bytes > INT32_MAX || reinterpret_cast<uintptr_t>(t.data_ptr()) % 4 != 0) throw Refused{};
+    }
+    return 0;
+}
+
 // copy_pages(pools, pairs, n_pairs, stream)
 int copy_pages(PyObject *const *a) {
     if (!PyList_Check(a[0]) && !PyTuple_Check(a[0])) throw Refused{};
@@ -234,11 +253,9 @@ int copy_pages(PyObject *const *a) {
     int64_t bytes[PA_COPY_MAX_POOLS], P = 0;
     for (Py_ssize_t i = 0; i < n; ++i) {
         const at::Tensor &t = tensor(PySequence_Fast_GET_ITEM(a[0], i));
-        if (t.dim() < 2 || !t.is_cuda() || t.get_device() != dev || !t.is_contiguous()) throw Refused{};
-        if (i == 0) P = t.size(0);
-        if (P < 1 || t.size(0) != P) throw Refused{};
+        if (i == 0) P = t.dim() ? t.size(0) : 0;
+        bytes[i] = page_bytes(t, dev, P);
         pool[i] = t.data_ptr();
-        bytes[i] = t.numel() / P * (int64_t)t.element_size();
     }
     return paged_attn_copy_pages(pool, bytes, (int)n, pp, (int)pairs.size(0), count, P, stream_of(a[3], dev));
 }
@@ -261,7 +278,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     PA_ENTRY("append_kv4", append_kv4, 5), PA_ENTRY("gather_kv4", gather_kv4, 5), PA_ENTRY("fwd_kv4", fwd_kv4, 12),
     PA_ENTRY("fork", fork_rows, 13),            PA_ENTRY("free", free_rows, 10),       PA_ENTRY("compact", compact_rows, 10),
-    PA_ENTRY("copy_pages", copy_pages, 4), {nullptr, nullptr, 0, nullptr}};
+    PA_ENTRY("copy_pages", copy_pages, 4), PA_ENTRY("check_pools", check_pools, 3), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_attn_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
