@@ -12,6 +12,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 from typing import Optional
 
 import numpy as np
@@ -157,16 +158,26 @@ def load_library(build_if_missing: bool = False):
 _binding = None
 
 
+class _LongWay:
+    """What stands for the short way where there is none: nothing is as it should be."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _short():
     """The compiled short way into the 4-bit cache's and the page calls (csrc/binding.cpp): its functions check their
-    tensors, make the call and return its status, or None where an argument is not as it should be."""
+    tensors, make the call and return its status, or None where an argument is not as it should be.  Where it was not
+    built, or for another torch, every call goes the long way, some 5 us longer on the host."""
     global _binding
     if _binding is None:
         import torch  # noqa: F401  (its libraries, which the binding needs)
         load_library()
-        if not os.path.exists(_build.BINDING_PATH):
-            raise RuntimeError(f"paged-attention binding not built ({_build.BINDING_PATH}); run "
-                               "paged_kv_cache_201_gb300.build.build()")
+        if not _build.binding_fits():
+            warnings.warn("the short way into the 4-bit cache's and the page calls is not built for this torch: these calls "
+                          "take some 5 us more on the host (paged_kv_cache_201_gb300.build.build() builds it)", RuntimeWarning)
+            _binding = _LongWay()
+            return _binding
         loader = importlib.machinery.ExtensionFileLoader(_build.BINDING_NAME, _build.BINDING_PATH)
         spec = importlib.util.spec_from_file_location(_build.BINDING_NAME, _build.BINDING_PATH, loader=loader)
         module = importlib.util.module_from_spec(spec)

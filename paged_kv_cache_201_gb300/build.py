@@ -2,13 +2,15 @@
 
 ``python -m paged_kv_cache_201_gb300.build`` compiles every ``csrc/*.cu`` in
 parallel with nvcc and links ``_build/libpaged_attn_gb300.so`` against the
-shared CUDA runtime; beside them it compiles ``csrc/binding.cpp``, the short
-way from Python into some of the calls, against torch's headers.
+shared CUDA runtime.  That is all the C ABI needs.  Where torch, its headers
+and Python's are there too, it also compiles ``csrc/binding.cpp``, the short way
+from Python into some of the calls; without it they go through ctypes.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -26,6 +28,7 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_NAME = "_paged_attn_binding"
 BINDING_PATH = os.path.join(BUILD_DIR, BINDING_NAME + ".so")
+BINDING_FOR = os.path.join(BUILD_DIR, BINDING_NAME + ".for")  # the torch and the Python that it was compiled against
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -59,9 +62,47 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _torch_dir():
+    """torch's folder, found without importing it; None without torch."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def binding_lacks() -> str:
+    """What the binding's compilation would need and is not there; empty if it can be compiled."""
+    torch = _torch_dir()
+    if torch is None:
+        return "torch"
+    if not os.path.exists(os.path.join(torch, "include", "ATen", "core", "Tensor.h")):
+        return "torch's headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    if not shutil.which(os.environ.get("CXX", "g++").split()[0]):
+        return "a C++ compiler"
+    return ""
+
+
+def binding_for() -> str:
+    """The torch and the Python that a binding has to be compiled against."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = ""
+    return f"{version} {_torch_dir()} {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_fits() -> bool:
+    """Whether the binding is there and was compiled against this torch and this Python."""
+    try:
+        with open(BINDING_FOR) as f:
+            return os.path.exists(BINDING_PATH) and f.read() == binding_for()
+    except OSError:
+        return False
+
+
 def _binding_flags():
-    """Include and link flags of torch, CUDA and Python, without importing torch."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """Include and link flags of torch, CUDA and Python."""
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
@@ -73,7 +114,7 @@ def _binding_flags():
 def _compile_binding() -> str:
     """The binding's object; it is linked once the library is there."""
     obj = os.path.join(BUILD_DIR, "binding.o")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *_binding_flags()[0], "-c",
+    cmd = [*os.environ.get("CXX", "g++").split(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *_binding_flags()[0], "-c",
            BINDING_SRC, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
@@ -83,19 +124,23 @@ def _compile_binding() -> str:
 
 def _link_binding(obj: str) -> None:
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{BUILD_DIR}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
+    cmd = [*os.environ.get("CXX", "g++").split(), "-shared", "-o", tmp, obj, f"-L{BUILD_DIR}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
            *_binding_flags()[1]]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"linking the binding failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_FOR, "w") as f:
+        f.write(binding_for())
+
+
+def _newer(path: str, files) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in files)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(f) <= t for f in sources() + _headers() + [BINDING_SRC, __file__])
+    return _newer(LIB_PATH, sources() + _headers() + [__file__]) and (
+        bool(binding_lacks()) or (binding_fits() and _newer(BINDING_PATH, _headers() + [BINDING_SRC, __file__])))
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -104,17 +149,20 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
+    lacks = binding_lacks()
+    if lacks:
+        sys.stderr.write(f"without the short way from Python into some calls: {lacks} not found\n")
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if lacks else ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        binding = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding)
+    if binding:
+        _link_binding(binding.result())
     return LIB_PATH
 
 
