@@ -25,6 +25,13 @@ constexpr auto kInt = at::kInt;
 
 struct Refused {};  // an argument is not as it should be
 
+// The interpreter is others' while a call is made: a launch waits where the stream's queue is full.  Every argument is read
+// before.
+struct WithoutInterpreter {
+    PyThreadState *const state = PyEval_SaveThread();
+    ~WithoutInterpreter() { PyEval_RestoreThread(state); }
+};
+
 const at::Tensor &tensor(PyObject *o) {
     if (!THPVariable_Check(o)) throw Refused{};
     return THPVariable_Unpack(o);
@@ -112,7 +119,10 @@ int append_kv4(PyObject *const *a) {
     const int32_t *slots = ints(a[2], dev, {T});
     const int64_t ks = token_stride(k, dev, k.scalar_type(), {T, Hkv, D}), vs = token_stride(v, dev, k.scalar_type(), {T, Hkv, D});
     const pa_dims d = dims_of(1, T, Hkv, Hkv, D, ps, kv.size(0), 0, type_code(k), 0);
-    return paged_attn_append_kv4(k.data_ptr(), v.data_ptr(), slots, ks, vs, pool, &d, stream_of(a[4], dev));
+    const void *kp = k.data_ptr(), *vp = v.data_ptr();
+    void *stream = stream_of(a[4], dev);
+    const WithoutInterpreter others;
+    return paged_attn_append_kv4(kp, vp, slots, ks, vs, pool, &d, stream);
 }
 
 // gather_kv4(kv, slots, k_out, v_out, stream)
@@ -126,7 +136,9 @@ int gather_kv4(PyObject *const *a) {
     const int32_t *slots = ints(a[1], dev, {T});
     void *ko = dense(k, dev, k.scalar_type(), {T, Hkv, D}), *vo = dense(tensor(a[3]), dev, k.scalar_type(), {T, Hkv, D});
     const pa_dims d = dims_of(1, T, Hkv, Hkv, D, ps, kv.size(0), 0, type_code(k), 0);
-    return paged_attn_gather_kv4(pool, slots, ko, vo, &d, stream_of(a[4], dev));
+    void *stream = stream_of(a[4], dev);
+    const WithoutInterpreter others;
+    return paged_attn_gather_kv4(pool, slots, ko, vo, &d, stream);
 }
 
 // fwd_kv4(q, kv, block_table, seq_lens, causal, q_offset, scale, out, lse, q_start, stream, workspace)
@@ -166,8 +178,10 @@ int fwd_kv4(PyObject *const *a) {
     } else {
         size = 0;  // none, or a shape that the call refuses
     }
-    return paged_attn_fwd_kv4(q.data_ptr(), pool, bt, lens, qs, causal, qo, (float)scale, out, static_cast<float *>(lse), &d, ws,
-                              size, stream_of(a[10], dev));
+    const void *qp = q.data_ptr();
+    void *stream = stream_of(a[10], dev);
+    const WithoutInterpreter others;
+    return paged_attn_fwd_kv4(qp, pool, bt, lens, qs, causal, qo, (float)scale, out, static_cast<float *>(lse), &d, ws, size, stream);
 }
 
 // What the page calls take: block_table, seq_lens, page_shares, free_pages, free_count.
@@ -200,25 +214,37 @@ int64_t length(PyObject *o) {
 int fork_rows(PyObject *const *a) {
     const Pages p(a[2], a[3], a[5], a[6], a[7]);
     const int64_t n = length(a[0]);
-    return paged_attn_fork(ints(a[0], p.dev, {n}), ints(a[1], p.dev, {n}), ints_or_null(a[11], p.dev, {n}), (int)n, p.table,
-                           p.lens, ints(a[4], p.dev, {p.B}), p.shares, p.free, (int)p.F, p.count, ints(a[8], p.dev, {1}),
-                           ints(a[9], p.dev, {n, 2}), (int)p.B, int_of(a[10]), p.P, (int)p.W, stream_of(a[12], p.dev));
+    const int32_t *parents = ints(a[0], p.dev, {n}), *children = ints(a[1], p.dev, {n}), *prefixes = ints_or_null(a[11], p.dev, {n});
+    int32_t *lens_out = ints(a[4], p.dev, {p.B}), *left = ints(a[8], p.dev, {1}), *copies = ints(a[9], p.dev, {n, 2});
+    const int ps = int_of(a[10]);
+    void *stream = stream_of(a[12], p.dev);
+    const WithoutInterpreter others;
+    return paged_attn_fork(parents, children, prefixes, (int)n, p.table, p.lens, lens_out, p.shares, p.free, (int)p.F, p.count, left,
+                           copies, (int)p.B, ps, p.P, (int)p.W, stream);
 }
 
 // free(rows, block_table, seq_lens, lens_out, page_shares, free_pages, free_count, free_left, page_size, stream)
 int free_rows(PyObject *const *a) {
     const Pages p(a[1], a[2], a[4], a[5], a[6]);
     const int64_t n = length(a[0]);
-    return paged_attn_free(ints(a[0], p.dev, {n}), (int)n, p.table, p.lens, ints(a[3], p.dev, {p.B}), p.shares, p.free, (int)p.F,
-                           p.count, ints(a[7], p.dev, {1}), (int)p.B, int_of(a[8]), p.P, (int)p.W, stream_of(a[9], p.dev));
+    const int32_t *rows = ints(a[0], p.dev, {n});
+    int32_t *lens_out = ints(a[3], p.dev, {p.B}), *left = ints(a[7], p.dev, {1});
+    const int ps = int_of(a[8]);
+    void *stream = stream_of(a[9], p.dev);
+    const WithoutInterpreter others;
+    return paged_attn_free(rows, (int)n, p.table, p.lens, lens_out, p.shares, p.free, (int)p.F, p.count, left, (int)p.B, ps, p.P,
+                           (int)p.W, stream);
 }
 
 // compact(block_table, seq_lens, page_shares, free_pages, free_count, moves, n_moves, page_map, page_size, stream)
 int compact_rows(PyObject *const *a) {
     const Pages p(a[0], a[1], a[2], a[3], a[4]);
-    return paged_attn_compact(p.table, p.lens, p.shares, p.free, (int)p.F, p.count, ints(a[5], p.dev, {p.P / 2, 2}),
-                              ints(a[6], p.dev, {1}), ints(a[7], p.dev, {p.P}), (int)p.B, int_of(a[8]), p.P, (int)p.W,
-                              stream_of(a[9], p.dev));
+    int32_t *moves = ints(a[5], p.dev, {p.P / 2, 2}), *n_moves = ints(a[6], p.dev, {1}), *map = ints(a[7], p.dev, {p.P});
+    const int ps = int_of(a[8]);
+    void *stream = stream_of(a[9], p.dev);
+    const WithoutInterpreter others;
+    return paged_attn_compact(p.table, p.lens, p.shares, p.free, (int)p.F, p.count, moves, n_moves, map, (int)p.B, ps, p.P, (int)p.W,
+                              stream);
 }
 
 // Bytes of a page of pool `t`, dense and of P pages on this device.
@@ -257,7 +283,10 @@ int copy_pages(PyObject *const *a) {
         bytes[i] = page_bytes(t, dev, P);
         pool[i] = t.data_ptr();
     }
-    return paged_attn_copy_pages(pool, bytes, (int)n, pp, (int)pairs.size(0), count, P, stream_of(a[3], dev));
+    const int most = (int)pairs.size(0);
+    void *stream = stream_of(a[3], dev);
+    const WithoutInterpreter others;
+    return paged_attn_copy_pages(pool, bytes, (int)n, pp, most, count, P, stream);
 }
 
 template <int (*F)(PyObject *const *), Py_ssize_t N>
