@@ -74,11 +74,12 @@ void *stream_of(PyObject *o, int dev) {
     return s;
 }
 
-// Elements between the tokens of [tokens, heads, head_dim] rows with dense heads.
+// Elements between the tokens of [tokens, heads, head_dim] rows with dense heads; 0: dense, whatever a stride that nothing uses
+// says.
 int64_t token_stride(const at::Tensor &t, int dev, at::ScalarType type, at::IntArrayRef shape) {
-    if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != type || t.sizes() != shape || t.stride(2) != 1 ||
-        t.stride(1) != shape[2] || t.stride(0) < shape[1] * shape[2])
-        throw Refused{};
+    if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != type || t.sizes() != shape) throw Refused{};
+    if (t.is_contiguous()) return 0;
+    if (t.stride(2) != 1 || t.stride(1) != shape[2] || t.stride(0) < shape[1] * shape[2]) throw Refused{};
     return t.stride(0);
 }
 
