@@ -950,10 +950,10 @@ int kv4_run_tokens(int G) { return (64 + G - 1) / G; }
 int64_t kv4_part_bytes(const pa_dims *d, int64_t n_tok) { return n_tok * d->num_q_heads * (d->head_dim + 2) * 4; }
 
 // Whether paged_attn_fwd_kv4 takes its tcgen05 kernel for sequences with runs of tokens: 0, or the number of CTAs that
-// share a unit's keys.  Both kernels are estimated, in microseconds, from their measured rates: the first takes 2.5 (head_dim
-// 128) or 2.05 (64) a 128-key tile of two tiles of rows and 4 to set up, in waves of one CTA a multiprocessor, and where CTAs
+// share a unit's keys.  Both kernels are estimated, in microseconds, from their measured rates: the first takes 2.3 (head_dim
+// 128) or 1.9 (64) a 128-key tile of two tiles of rows and 4 to set up, in waves of one CTA a multiprocessor, and where CTAs
 // share keys, 3 and the time of writing and reading their parts; the second 0.1 of a multiprocessor's time for 16 rows by
-// 16 keys (head_dim 128).  Two chunks of 512 tokens over 8192 keys of 8 heads of 128, G = 4: 178 us against 714, of 64: 148
+// 16 keys (head_dim 128).  Two chunks of 512 tokens over 8192 keys of 8 heads of 128, G = 4: 169 us against 714, of 64: 139
 // against 392.  The table's width stands for lengths, which the host does not know.
 int kv4_runs(const pa_dims *d, int64_t n_tok, bool packed, int sms, int64_t ws_bytes) {
     const int G = d->num_q_heads / d->num_kv_heads, tile = pa::kv4_tile_tokens(d->head_dim, G);
@@ -961,7 +961,7 @@ int kv4_runs(const pa_dims *d, int64_t n_tok, bool packed, int sms, int64_t ws_b
     // a batch of mostly single tokens
     if (packed ? n_tok < 2 * (int64_t)d->batch || n_tok < kv4_run_tokens(G) : d->q_len < kv4_run_tokens(G)) return 0;
     const double keys = (double)d->bt_stride * d->page_size, width = d->head_dim / 128.0, steps = keys / 128;
-    const double step = d->head_dim == 128 ? 2.5 : 2.05;
+    const double step = d->head_dim == 128 ? 2.3 : 1.9;
     const double tiles = packed ? ceil((double)n_tok / tile) : (double)d->batch * ((d->q_len + tile - 1) / tile);
     const double units = tiles * d->num_kv_heads, part = (double)kv4_part_bytes(d, n_tok);
     double best = (double)n_tok * d->num_q_heads / 16 * (keys / 16) * 0.1 * width / sms + 4;

@@ -468,8 +468,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) paged_attn_kv4_kernel(const Kv4
 #pragma unroll
                 for (int kh = 0; kh < 2; ++kh) {
                     const uint32_t hi = Op::pack(w[2 * kh], w[2 * kh + 1]);
-                    const float2 x = Op::unpack(hi);
-                    const uint32_t lo = Op::pack(w[2 * kh] - x.x, w[2 * kh + 1] - x.y);
+                    const uint32_t lo = remainder(hi, w[2 * kh], w[2 * kh + 1]);
                     if constexpr (HALF) {
                         pb[hb][nr][0][kh] = movmatrix_trans(tq < 2 ? hi : lo);
                     } else {

@@ -15,8 +15,8 @@
 // a finite number, so keys past a row's limit are only left out of its weights.
 //
 // Two tiles of rows over 128 keys are 16.8 MFLOP and 8.4 more for the remainders, 2.0 us of a multiprocessor at the GPU's measured
-// bf16 rate; they take 2.5.  Chunks of 512 and 419 tokens over 8192 and 5720 keys (8 kv heads of 128, G = 4, bf16) are 120
-// CTAs of up to 64 such steps, one wave on 152 multiprocessors: 162 us.  Two of 512 over 8192 keys take 178, the mma.sync kernel
+// bf16 rate; they take 2.3.  Chunks of 512 and 419 tokens over 8192 and 5720 keys (8 kv heads of 128, G = 4, bf16) are 120
+// CTAs of up to 64 such steps, one wave on 152 multiprocessors: 154 us.  Two of 512 over 8192 keys take 169, the mma.sync kernel
 // 714.  With the high parts alone the first take 126, and where the values cancel the outputs are up to 6 half steps of
 // bf16 off.  Measured no faster, then against 121: codes turned by seven warps instead of four (129), S read twice instead of
 // held in registers (139), page ids looked up a tile earlier (147), P handed over in halves (149), K and V in halves of 64
@@ -376,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
                     l2 = add2f(l2, make_float2(w0, w1));
                     hi[j] = Op::pack(w0, w1);
-                    const float2 h = Op::unpack(hi[j]);
-                    lo[j] = Op::pack(w0 - h.x, w1 - h.y);
+                    lo[j] = remainder(hi[j], w0, w1);
                 }
                 tc05::st_16cols(sbuf + 32u * i, hi);
                 tc05::st_16cols(sbuf + 32u * i + 16u, lo);

@@ -24,6 +24,16 @@ struct Kv4Params {
     int longest_first;  // the mma kernel's sequences by length
 };
 
+// What the f16 pair hi lacks of the two weights, as an f16 pair: the differences are exact, and taken from the halves as they
+// stand, without a conversion of each.
+__device__ __forceinline__ uint32_t remainder(uint32_t hi, float w0, float w1) {
+    float x, y;
+    asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tsub.f32.f16 %0, p, %3;\n\tsub.f32.f16 %1, q, %4;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "r"(hi), "f"(w0), "f"(w1));
+    return MmaOp<__half>::pack(-x, -y);
+}
+
 // A unit's tokens: cnt of sequence b from its token i on; q0 the sequence's first row of q, n its tokens, len its keys.
 struct Tile {
     int b, n, i, cnt, len;
