@@ -17,8 +17,8 @@
 //   * Softmax statistics are float32.  A weight is 2^(score - ref), ref at least 11 below the largest score so far
 //     when it was last moved and never more than 15 below any: weights stay below 2^15, ref (and with it every sum)
 //     moves rarely, and in f16 nothing above 2^-36 of the row's largest weight is lost.
-//   * A weight is an f16 high part plus its remainder, within 2^-22 of it: where the values cancel, a high part alone (2^-12)
-//     leaves outputs up to 40 half steps of bf16 off.  Units of up to four rows (single tokens of G <= 4) have the
+//   * A weight is an f16 high part plus its remainder, within 2^-22 of it: where the values cancel, a high part alone (2^-11)
+//     left bf16 outputs up to 44 times as far off as their own rounding and the float32 sums do.  Units of up to four rows (single tokens of G <= 4) have the
 //     remainders' products in columns that nobody else uses: 256 sequences take 164 us, with two products 183, with the
 //     high parts alone 159.
 //   * The rows of S^T are keys r ^ (r >> 1 & 1): with the four keys of a V load in different rows modulo
@@ -26,8 +26,8 @@
 //
 // Any byte stands for a finite number, so what lies behind a sequence's last key needs no cleaning: its weight is 0.
 //
-// What bounds it is instructions: 322 a block of 16 keys of 128 and warp, 134 of them on the integer pipe and 124 on the
-// one of multiplications, issued in 66 % of cycles by four warps a scheduler, which wait for those pipes (ncu); memory
+// What bounds it is instructions: 336 a block of 16 keys of 128 and warp, 138 of them on the integer pipe and 132 on the
+// one of multiplications, issued in 67 % of cycles by four warps a scheduler, which wait for those pipes (ncu); memory
 // keeps nobody waiting.  256 sequences of 0.4 to 1 times 4096 tokens (8 kv heads of 128, G = 4, bf16) take 164 us, 5.2 TB/s
 // or 78 % of the copy rate; one of 131072 tokens, as 19 CTAs a kv head, 39 us, 58 %.
 #include <limits.h>
@@ -708,7 +708,8 @@ Plan make_plan(const SparseParams &sp, int sms, long long ws_bytes) {
     // More than one wave of CTAs: the longest sequences first, lest one starts when the others end.  Sequences of 0.4 to 1
     // times the table's 4096 columns, 8 kv heads: 256 of them 178 -> 170 us, 152 114 -> 101, 110 99 -> 89.  Finding the
     // sequence costs a CTA half a microsecond: with 1024 columns 100 sequences 29.5 -> 27.2, but 256 59.7 -> 61.2 (2048
-    // columns: 96.8 -> 95.1).
+    // columns: 96.8 -> 95.1).  Past 256 sequences, more lengths than a warp holds eight to a lane, the order is the caller's: 300
+    // take 194 us mixed and 176 with the longest first in the table, 512 319 and 300.
     const long long wave = (long long)sms * ctas, n_ctas = a.units * a.S;
     a.longest_first = n_ctas > wave && f.B > 1 && f.B <= 256 && (keys >= 2048 || (keys >= 1024 && n_ctas <= 2 * wave)) &&
                       (a.seq_tiles > 0 || (a.TT == 1 && sp.n_tok == f.B));

@@ -16,9 +16,9 @@
 //
 // Two tiles of rows over 128 keys are 16.8 MFLOP and 8.4 more for the remainders, 2.0 us of a multiprocessor at the GPU's measured
 // bf16 rate; they take 2.3.  Chunks of 512 and 419 tokens over 8192 and 5720 keys (8 kv heads of 128, G = 4, bf16) are 120
-// CTAs of up to 64 such steps, one wave on 152 multiprocessors: 154 us.  Two of 512 over 8192 keys take 169, the mma.sync kernel
-// 714.  With the high parts alone the first take 126, and where the values cancel the outputs are up to 6 half steps of
-// bf16 off.  Measured no faster, then against 121: codes turned by seven warps instead of four (129), S read twice instead of
+// CTAs of up to 64 such steps, one wave on 152 multiprocessors: 154 us, the tensor pipe active in two thirds of a working one's cycles.  Two of 512 over 8192 keys take 169, the mma.sync kernel
+// 714.  With the high parts alone the first take 126, and where the values cancel the outputs are up to 6 times as far
+// off as their rounding and the float32 sums leave them.  Measured no faster, then against 121: codes turned by seven warps instead of four (129), S read twice instead of
 // held in registers (139), page ids looked up a tile earlier (147), P handed over in halves (149), K and V in halves of 64
 // keys (172).
 #include <limits.h>

@@ -58,7 +58,8 @@ __device__ __forceinline__ uint32_t scale_byte(float a) {
 }
 
 // Eight codes of a word -> four f16 pairs, pair k = codes k and k + 4: the odd ones as (u - 8) x scale / 8, the even ones,
-// which lie four bits lower, as (u - 8) x scale / 128.  A code put below the leading bits of an f16 number reads
+// which lie four bits lower, as (u - 8) x scale / 128.  To put a few bits below the leading one of 1024 is the usual way to make
+// small integers f16 numbers; the shares and constants are this format's.  A code put below the leading bits of an f16 number reads
 // 1024 + 16 u or 1024 + u, and with s = scale / 128, c = -9 scale and d = -8.0625 scale
 //   (1024 + 16 u) s + c = (u - 8) scale / 8,   (1024 + u) s + d = (u - 8) scale / 128
 // in one rounding, which has nothing to round (an f16 number's last bit is 2^-24 at least, the smallest scale's
@@ -88,8 +89,8 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// (a & mask) | 0x64006400, as the one operation that it is (written in C, nvcc 13.0 makes two of it: 494
-// instructions a block of 16 keys instead of 431).
+// (a & mask) | 0x64006400, as the one operation that it is (written in C the decode kernel executed 494 instructions a block
+// of 16 keys instead of 431).
 __device__ __forceinline__ uint32_t code_in_f16(uint32_t a, uint32_t mask) {
     uint32_t d;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(0x64006400u));
