@@ -149,6 +149,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
+    if os.path.exists(BINDING_FOR):  # an old binding does not meet the new library
+        os.remove(BINDING_FOR)
     lacks = binding_lacks()
     if lacks:
         sys.stderr.write(f"without the short way from Python into some calls: {lacks} not found\n")

@@ -59,6 +59,23 @@ def test_another_torch_builds_again(built, monkeypatch):
     assert _binding_ran(built) and b.binding_fits() and b.up_to_date()
 
 
+def test_an_old_binding_does_not_meet_a_new_library(built, monkeypatch):
+    b.build(force=True)
+    assert b.binding_fits()
+    with monkeypatch.context() as m:  # its headers are gone
+        m.setattr(b.sysconfig, "get_paths", lambda: {"include": "/nowhere"})
+        b.build(force=True)
+        assert not b.binding_fits()
+    b.build()
+    assert b.binding_fits()
+    run = b.subprocess.run  # or it does not compile
+    monkeypatch.setattr(b.subprocess, "run", lambda cmd, **kw: types.SimpleNamespace(returncode=1, stdout="", stderr="no")
+                        if b.BINDING_SRC in cmd else run(cmd, **kw))
+    with pytest.raises(RuntimeError):
+        b.build(force=True)
+    assert not b.binding_fits()
+
+
 def test_a_library_that_fails_says_so(built, monkeypatch):
     """Whatever becomes of the short way, a kernel that does not compile is an error."""
     _without_torch(monkeypatch)
