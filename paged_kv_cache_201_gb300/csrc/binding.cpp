@@ -26,7 +26,7 @@ constexpr auto kInt = at::kInt;
 struct Refused {};  // an argument is not as it should be
 
 // The interpreter is others' while a call is made: a launch waits where the stream's queue is full.  Every argument is read
-// before.
+// before.  It costs a call 0.1 us (two calls over 261 rows 4.5 -> 4.7 us).
 struct WithoutInterpreter {
     PyThreadState *const state = PyEval_SaveThread();
     ~WithoutInterpreter() { PyEval_RestoreThread(state); }
